@@ -77,7 +77,7 @@ typedef enum { M3SSD_F32 = 0, M3SSD_BF16 = 1 } m3ssd_dtype;
 
 /* flags (m3ssd_dims.flags) */
 /* M3SSD_CHECK_FINITE: after its kernels, m3ssd_fwd (and m3ssd_step,
- * m3ssd_mimo_fwd, m3ssd_mimo_step) scans the outputs it wrote -- Y and hT, or
+ * m3ssd_step_q8, m3ssd_mimo_fwd, m3ssd_mimo_step) scans the outputs it wrote -- Y and hT, or
  * y_t -- on the same stream for NaN or infinite values (from an input that was,
  * or from an intermediate that overflowed, e.g. a bf16 input beyond fp16's range
  * on the chunked path); m3ssd_nonfinite_outputs reports what the checks found.
@@ -409,10 +409,139 @@ m3ssd_status m3ssd_block_step(const m3ssd_block_dims* dims, const m3ssd_block_we
                               const void* u_t, void* out_t, const m3ssd_cache* cache,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The residual addition with the root-mean-square norm that stands before the block in a
+ * layer ("VikramLex/mamba3-minimal" README, "Architecture": x + mixer(norm(x))), over
+ * rows of `width` values:
+ *     r = x + residual (rounded once to res_dtype; r = x when residual is NULL),
+ *     rstd = 1 / sqrt(mean r^2 + eps),   y = r rstd w
+ * computed in fp32, y rounded once to x_dtype or quantised to a microscaled format (below).
+ */
+typedef struct {
+  int64_t rows;      /* >= 0 (tokens) */
+  int64_t width;     /* 1 .. 16384 (else M3SSD_ERR_UNSUPPORTED) */
+  int32_t x_dtype;   /* m3ssd_dtype of x and y (and of dy) */
+  int32_t res_dtype; /* m3ssd_dtype of residual and residual_out (and of r) */
+  float eps;         /* >= 0 */
+  uint32_t reserved; /* must be 0 */
+} m3ssd_norm_dims;
+
+/*
+ * Microscaled (MX) tensors: rows of `cols` values in blocks of 32, each block with a
+ * power-of-two scale 2^E, the least with amax <= maxval 2^E, and codes value / 2^E rounded
+ * to nearest even: E2M1 (4 bits, maxval 6) or E4M3 (8 bits, maxval 448).  E is clamped to
+ * [-127, 127] and held as the byte E + 127; a block of zeros takes byte 0; a block with a
+ * NaN or an infinity takes byte 255 (NaN) and reads back as NaN.
+ *   codes:  rows x Kp codes, Kp = cols rounded up to 128, the padding zero; E2M1 two codes
+ *           a byte, the even index in the low half.  m3ssd_mx_codes_size bytes.
+ *   scales: tiles of 128 rows x 4 blocks, 512 bytes each, row-block-major: byte
+ *           (r % 32) 16 + (r / 32) 4 + k of row r and block k of the tile; bytes of missing
+ *           rows 0.  m3ssd_mx_scales_size bytes.
+ * Both 128-byte aligned.  At most 2^31 - 1 groups of 128 columns over the rows rounded up
+ * to 128 (else M3SSD_ERR_UNSUPPORTED).  The functions that write one write the padding too.
+ */
+typedef enum { M3SSD_MXFP4 = 0, M3SSD_MXFP8 = 1 } m3ssd_mx_format;
+typedef struct {
+  int32_t format;    /* m3ssd_mx_format */
+  uint32_t reserved; /* must be 0 */
+  int64_t rows;      /* >= 0 */
+  int64_t cols;      /* >= 1 */
+  void* codes;
+  void* scales;
+} m3ssd_mx;
+
+/* Bytes of the codes and of the scales; 0 for invalid arguments. */
+size_t m3ssd_mx_codes_size(int32_t format, int64_t rows, int64_t cols);
+size_t m3ssd_mx_scales_size(int64_t rows, int64_t cols);
+
+/* x (rows x cols, row stride ldx >= cols elements, x_dtype) to and from an MX tensor.  Read
+ * back, a value is code 2^E, rounded once to x_dtype: exact unless it is subnormal there, or
+ * was rounded up from the type's largest values past its range (then infinite). */
+m3ssd_status m3ssd_mx_quant(const m3ssd_mx* out, int32_t x_dtype, const void* x, int64_t ldx,
+                            void* stream);
+m3ssd_status m3ssd_mx_dequant(const m3ssd_mx* in, int32_t x_dtype, void* x, int64_t ldx,
+                              void* stream);
+
+/*
+ * D (M x N, bf16, row stride ldd >= N) = A W^T of MX operands A (M x K, either format) and
+ * W (N x K, M3SSD_MXFP4; else M3SSD_ERR_UNSUPPORTED), beside m3ssd_gemm_bf16 for the block's
+ * projections with quantised weights.  Products of the held values, fp32 accumulation on
+ * the tensor cores, each output rounded once to bf16.  D 2-byte aligned (tensor stores
+ * when D is 16-byte aligned and N and ldd are multiples of 8).  No allocation, no
+ * synchronisation.
+ */
+m3ssd_status m3ssd_gemm_mx(const m3ssd_mx* A, const m3ssd_mx* W, void* D, int64_t ldd,
+                           void* stream);
+
+/*
+ * Forward of the residual addition and norm.  residual and residual_out are given together
+ * or not at all; residual_out may be residual.  Exactly one of y (rows x width, x_dtype; may
+ * be x) and y_mx (an MX tensor of rows x width, the A operand of m3ssd_gemm_mx) is given.
+ * rstd (rows), for the backward, may be NULL.  x, y, residual: dense rows.
+ */
+m3ssd_status m3ssd_add_rmsnorm(const m3ssd_norm_dims* dims, const void* x, const void* residual,
+                               const float* w, void* y, const m3ssd_mx* y_mx, void* residual_out,
+                               float* rstd, void* stream);
+
+/* Bytes of device workspace m3ssd_add_rmsnorm_bwd needs on the current device (it depends
+ * on the SM count); 0 for invalid dims. */
+size_t m3ssd_add_rmsnorm_bwd_workspace_size(const m3ssd_norm_dims* dims);
+
+/*
+ * Its backward.  dy (rows x width, x_dtype) is the gradient of y, dres (fp32, NULL = 0)
+ * that of residual_out; r (res_dtype) is residual_out (or x without a residual, with
+ * res_dtype = x_dtype) and rstd the forward's.  Writes fp32 dr (rows x width; may be dres),
+ * the gradient of x and of residual alike, and dw (width).  With g = w dy, rhat = r rstd:
+ *     dr = rstd (g - rhat mean(g rhat)) + dres,   dw = sum over rows of dy rhat.
+ * Sums run in a fixed order, so results are deterministic.  workspace: 256-byte aligned,
+ * not read afterwards.
+ */
+m3ssd_status m3ssd_add_rmsnorm_bwd(const m3ssd_norm_dims* dims, const void* dy, const void* r,
+                                   const float* w, const float* rstd, const float* dres, float* dr,
+                                   float* dw, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * A decode cache whose state is held in 8 bits.  A row (b, h, n) of the state, P values, is
+ * E4M3 codes with one fp32 scale: s = amax fp32(1 / 448), code = v (1 / s) rounded to nearest
+ * even, v ~ code s.  Rows with amax < 2^-100 are held as zeros (s = 0); a row with a NaN or an
+ * infinity takes a NaN scale and reads back as NaN.  A held value is within 2^-4 of its
+ * magnitude or 2^-10 s, whichever is larger.
+ */
+typedef struct {
+  float* angle;      /* (b, H, N/2) */
+  void* ssm;         /* (b, H, N, P) E4M3 codes */
+  float* ssm_scale;  /* (b, H, N) */
+  float* x_prev;     /* (b, H, P) */
+  float* b_prev;     /* (b, G, N), unrotated */
+} m3ssd_cache_q8;
+
+/* A whole fp32 state (b, H, N, P), as the forward writes hT, to that form and back
+ * (prefill -> 8-bit decode).  dims: batch, nheads, headdim, dstate (seqlen and chunk are
+ * ignored); limits as m3ssd_step. */
+m3ssd_status m3ssd_quant_state(const m3ssd_dims* dims, const float* ssm, void* codes, float* scale,
+                               void* stream);
+m3ssd_status m3ssd_dequant_state(const m3ssd_dims* dims, const void* codes, const float* scale,
+                                 float* ssm, void* stream);
+
+/*
+ * m3ssd_step on such a cache: the state is read as code s, y_t comes from the updated fp32
+ * state before it is rounded, and the state is rounded once as it is written.  The new
+ * cache goes to cache_out, which may be another cache (the old one stays, for a rollback)
+ * or NULL or the same (in place); its buffers equal the cache's or do not overlap them.
+ * Arguments, limits and flags as m3ssd_step.
+ * Capture-safe (no allocation, no sync).
+ */
+m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float* logdecay_t,
+                           const float* beta_t, const float* gamma_t, const void* B_t,
+                           const void* C_t, const float* theta_t, const float* D,
+                           const m3ssd_cache_q8* cache, const m3ssd_cache_q8* cache_out, void* y_t,
+                           void* stream);
+
 /* Number of bounded device-side waits of the chunked forwards (SISO and
- * MIMO), the tensor-core backward and the projection GEMM that ran out since
+ * MIMO), the tensor-core backward and the GEMMs that ran out since
  * the last call (a forward's CTA then stops and leaves its outputs unwritten;
- * the backward's and the GEMM's CTAs skip their remaining waits and leave their
+ * the backward's and the GEMMs' CTAs skip their remaining waits and leave their
  * outputs undefined); the count is then reset.  This call synchronises the current device
  * and must not be captured in a CUDA graph.  Returns M3SSD_ERR_INVALID_ARG for
  * a NULL pointer and M3SSD_ERR_CUDA if the device cannot be read. */

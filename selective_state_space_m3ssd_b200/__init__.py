@@ -63,6 +63,22 @@ class Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("angle", "ssm", "x_prev", "b_prev")]
 
 
+class NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_uint32)]
+
+
+class Mx(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("reserved", ctypes.c_uint32),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class CacheQ8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("angle", "ssm", "scale", "x_prev", "b_prev")]
+
+
 class BlockDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("batch", "seqlen", "d_model", "nheads", "headdim", "dstate", "ngroups")]
@@ -143,6 +159,27 @@ def load(path: str | None = None):
         i64, i32p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int32)
         lib.m3ssd_test_fwd_split_plan.argtypes = [i64, i64, i64, ctypes.c_int32, i32p, i32p]
         lib.m3ssd_test_fwd_split_plan.restype = ctypes.c_int
+        i32, mxp = ctypes.c_int32, ctypes.POINTER(Mx)
+        lib.m3ssd_mx_codes_size.argtypes = [i32, i64, i64]
+        lib.m3ssd_mx_codes_size.restype = sz
+        lib.m3ssd_mx_scales_size.argtypes = [i64, i64]
+        lib.m3ssd_mx_scales_size.restype = sz
+        for f in (lib.m3ssd_mx_quant, lib.m3ssd_mx_dequant):
+            f.argtypes, f.restype = [mxp, i32, vp, i64, vp], ctypes.c_int
+        lib.m3ssd_gemm_mx.argtypes = [mxp, mxp, vp, i64, vp]
+        lib.m3ssd_gemm_mx.restype = ctypes.c_int
+        ndp = ctypes.POINTER(NormDims)
+        lib.m3ssd_add_rmsnorm.argtypes = [ndp, vp, vp, vp, vp, mxp, vp, vp, vp]
+        lib.m3ssd_add_rmsnorm.restype = ctypes.c_int
+        lib.m3ssd_add_rmsnorm_bwd_workspace_size.argtypes = [ndp]
+        lib.m3ssd_add_rmsnorm_bwd_workspace_size.restype = sz
+        lib.m3ssd_add_rmsnorm_bwd.argtypes = [ndp] + [vp] * 8 + [sz, vp]
+        lib.m3ssd_add_rmsnorm_bwd.restype = ctypes.c_int
+        for f in (lib.m3ssd_quant_state, lib.m3ssd_dequant_state):
+            f.argtypes, f.restype = [ctypes.POINTER(Dims), vp, vp, vp, vp], ctypes.c_int
+        lib.m3ssd_step_q8.argtypes = [ctypes.POINTER(Dims)] + [vp] * 8 + \
+            [ctypes.POINTER(CacheQ8), ctypes.POINTER(CacheQ8), vp, vp]
+        lib.m3ssd_step_q8.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -629,6 +666,294 @@ def block_step(cache: dict, u_t, wts: dict, *, out_t=None, workspace=None):
                                  _stream_handle(dev))
     _check(st, "m3ssd_block_step")
     return out_t
+
+
+def _launch(name: str, dev, *args):
+    """Calls a C entry point whose last argument is the stream, with the tensors'
+    device current (a stream, a workspace size and a launch all go by it)."""
+    import torch
+    f = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, _stream_handle(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream_handle(dev))
+    _check(st, name)
+
+
+# ---- microscaled tensors and their product ------------------------------------------
+
+MXFP4, MXFP8 = 0, 1
+_MX_FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8}
+
+
+def _pad128(n: int) -> int:
+    return (n + 127) // 128 * 128
+
+
+class MXTensor:
+    """A microscaled tensor (``m3ssd_mx``): ``fmt`` "mxfp4" or "mxfp8", ``rows`` x
+    ``cols`` values in blocks of 32; ``codes`` (rows, Kp / 2 or Kp) and ``scales``
+    (flat, tiles of 128 rows x 4 blocks), uint8, as laid out in ``include/m3ssd.h``."""
+
+    __slots__ = ("fmt", "rows", "cols", "codes", "scales")
+
+    def __init__(self, fmt: str, rows: int, cols: int, codes, scales):
+        self.fmt, self.rows, self.cols, self.codes, self.scales = fmt, rows, cols, codes, scales
+
+    @classmethod
+    def empty(cls, fmt: str, rows: int, cols: int, device):
+        """Unwritten storage for a tensor of this size."""
+        import torch
+        kp = _pad128(cols)
+        return cls(fmt, rows, cols,
+                   torch.empty(rows, kp if _mx_format(fmt) == MXFP8 else kp // 2,
+                               dtype=torch.uint8, device=device),
+                   torch.empty(_pad128(rows) * (kp // 32), dtype=torch.uint8, device=device))
+
+
+def _mx_format(fmt) -> int:
+    if fmt not in _MX_FORMATS:
+        raise ValueError(f"format must be one of {sorted(_MX_FORMATS)}, got {fmt!r}")
+    return _MX_FORMATS[fmt]
+
+
+def _mx_struct(t: MXTensor, name: str, device) -> Mx:
+    import torch
+    f, kp = _mx_format(t.fmt), _pad128(t.cols)
+    _need(t.codes, name + ".codes", torch.uint8, (t.rows, kp if f == MXFP8 else kp // 2), device)
+    _need(t.scales, name + ".scales", torch.uint8, (_pad128(t.rows) * (kp // 32),), device)
+    return Mx(f, 0, t.rows, t.cols, t.codes.data_ptr(), t.scales.data_ptr())
+
+
+def _rows_stride(x, name):
+    """A (rows, cols) CUDA tensor with unit column stride; returns its row stride."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, cols = x.shape
+    if (cols > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < cols):
+        raise ValueError(f"{name} must have contiguous rows")
+    return x.stride(0) if rows > 1 else max(cols, 1)
+
+
+def mx_quant(x, fmt: str, *, out: MXTensor | None = None) -> MXTensor:
+    """x (rows, cols), bf16 or fp32, rows contiguous (any row stride), to the
+    microscaled format ``fmt`` through ``m3ssd_mx_quant``."""
+    ldx = _rows_stride(x, "x")
+    rows, cols = x.shape
+    if out is None:
+        out = MXTensor.empty(fmt, rows, cols, x.device)
+    elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
+        raise ValueError(f"out must be {fmt} of {rows} x {cols}")
+    o = _mx_struct(out, "out", x.device)
+    _launch("m3ssd_mx_quant", x.device, ctypes.byref(o), _xdtype(x), _ptr(x), ldx)
+    return out
+
+
+def mx_dequant(t: MXTensor, dtype=None, *, out=None):
+    """The values of a microscaled tensor (rows, cols) through ``m3ssd_mx_dequant``,
+    in ``dtype`` (bf16 unless given) or into ``out`` (rows contiguous)."""
+    import torch
+    dev = t.codes.device
+    if out is None:
+        out = torch.empty(t.rows, t.cols, dtype=dtype or torch.bfloat16, device=dev)
+    _need_shape(out, "out", dtype, (t.rows, t.cols))
+    ldx = _rows_stride(out, "out")
+    m = _mx_struct(t, "t", out.device)
+    _launch("m3ssd_mx_dequant", dev, ctypes.byref(m), _xdtype(out), _ptr(out), ldx)
+    return out
+
+
+def gemm_mx(A: MXTensor, W: MXTensor, *, out=None):
+    """A (M, K) @ W (N, K)^T of microscaled operands through ``m3ssd_gemm_mx`` (W in
+    "mxfp4", A in either format) -> out (M, N) bf16, rows contiguous."""
+    import torch
+    dev = A.codes.device
+    if out is None:
+        out = torch.empty(A.rows, W.rows, dtype=torch.bfloat16, device=dev)
+    _need_shape(out, "out", torch.bfloat16, (A.rows, W.rows))
+    ldd = _rows_stride(out, "out")
+    a, w = _mx_struct(A, "A", out.device), _mx_struct(W, "W", out.device)
+    _launch("m3ssd_gemm_mx", dev, ctypes.byref(a), ctypes.byref(w), _ptr(out), ldd)
+    return out
+
+
+# ---- the residual addition with the RMS norm -------------------------------------------
+
+def add_rmsnorm(x, w, *, residual=None, eps: float = 1e-6, fmt: str | None = None,
+                want_rstd: bool = False, y=None, residual_out=None):
+    """r = x + residual, y = r / sqrt(mean r^2 + eps) * w over the last axis, through
+    ``m3ssd_add_rmsnorm``.  x (..., d) bf16 or fp32; residual (its shape) bf16 or fp32;
+    w (d) fp32.  ``fmt`` ("mxfp8" or "mxfp4") returns y as an :class:`MXTensor` of the
+    flattened rows, the A operand of :func:`gemm_mx`; else y has x's type.  Returns ``(y,
+    residual_out, rstd)``; residual_out (residual's type; pass ``residual`` to write it in
+    place) is None without a residual, rstd (fp32, rows) None unless ``want_rstd``."""
+    import torch
+    dev, f32 = x.device, torch.float32
+    d = x.shape[-1]
+    rows = x.numel() // d if d else 0
+    _need(x, "x", device=dev)
+    _need(w, "w", f32, (d,), dev)
+    xd = rd = _xdtype(x)
+    if residual is not None:
+        rd = _xdtype(residual)
+        _need(residual, "residual", None, x.shape, dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        _need(residual_out, "residual_out", residual.dtype, x.shape, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out is only written with a residual")
+    mx = None
+    if fmt is None:
+        y = torch.empty_like(x) if y is None else y
+        _need(y, "y", x.dtype, x.shape, dev)
+    else:
+        if y is None:
+            y = MXTensor.empty(fmt, rows, d, dev)
+        elif (y.fmt, y.rows, y.cols) != (fmt, rows, d):
+            raise ValueError(f"y must be {fmt} of {rows} x {d}")
+        mx = _mx_struct(y, "y", dev)
+    rstd = torch.empty(rows, dtype=f32, device=dev) if want_rstd else None
+    dims = NormDims(rows, d, xd, rd, eps, 0)
+    _launch("m3ssd_add_rmsnorm", dev, ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(w),
+            None if mx is not None else _ptr(y), None if mx is None else ctypes.byref(mx),
+            _ptr(residual_out), _ptr(rstd))
+    return y, residual_out, rstd
+
+
+def add_rmsnorm_bwd_workspace_size(dims: NormDims) -> int:
+    """Bytes on the current device."""
+    return int(load().m3ssd_add_rmsnorm_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=None):
+    """Backward of :func:`add_rmsnorm` through ``m3ssd_add_rmsnorm_bwd``: dy (..., d) bf16
+    or fp32, r the forward's residual_out (or x without a residual), rstd its rstd, dres
+    the fp32 gradient of residual_out (None = 0).  Returns ``(dr, dw)`` in fp32: dr is the
+    gradient of x and of residual alike."""
+    import torch
+    dev, f32 = dy.device, torch.float32
+    d = dy.shape[-1]
+    rows = dy.numel() // d if d else 0
+    _need(dy, "dy", device=dev)
+    _need(r, "r", None, dy.shape, dev)
+    _need(w, "w", f32, (d,), dev)
+    _need(rstd, "rstd", f32, (rows,), dev)
+    _need(dres, "dres", f32, dy.shape, dev)
+    dr = torch.empty(dy.shape, dtype=f32, device=dev) if dr is None else dr
+    dw = torch.empty(d, dtype=f32, device=dev) if dw is None else dw
+    _need(dr, "dr", f32, dy.shape, dev)
+    _need(dw, "dw", f32, (d,), dev)
+    dims = NormDims(rows, d, _xdtype(dy), _xdtype(r), 0.0, 0)
+    with torch.cuda.device(dev):
+        need = add_rmsnorm_bwd_workspace_size(dims)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch("m3ssd_add_rmsnorm_bwd", dev, ctypes.byref(dims), _ptr(dy), _ptr(r), _ptr(w),
+            _ptr(rstd), _ptr(dres), _ptr(dr), _ptr(dw), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return dr, dw
+
+
+# ---- the decode cache with its state in 8 bits -------------------------------------------
+
+def quant_state(ssm, *, codes=None, scale=None):
+    """An fp32 state (b, H, N, P) as E4M3 codes (uint8, same shape) and scales (b, H, N)
+    fp32, through ``m3ssd_quant_state``; returns ``(codes, scale)``."""
+    import torch
+    _need(ssm, "ssm", torch.float32, device=ssm.device)
+    b, H, N, P = ssm.shape
+    dev = ssm.device
+    codes = torch.empty(b, H, N, P, dtype=torch.uint8, device=dev) if codes is None else codes
+    scale = torch.empty(b, H, N, dtype=torch.float32, device=dev) if scale is None else scale
+    _need(codes, "codes", torch.uint8, (b, H, N, P), dev)
+    _need(scale, "scale", torch.float32, (b, H, N), dev)
+    dims = make_dims(b, 1, H, P, N, 1, F32)
+    _launch("m3ssd_quant_state", dev, ctypes.byref(dims), _ptr(ssm), _ptr(codes), _ptr(scale))
+    return codes, scale
+
+
+def dequant_state(codes, scale, *, ssm=None):
+    """The fp32 state (b, H, N, P) that codes and scales stand for, through
+    ``m3ssd_dequant_state``."""
+    import torch
+    dev = codes.device
+    _need(codes, "codes", torch.uint8, device=dev)
+    b, H, N, P = codes.shape
+    _need(scale, "scale", torch.float32, (b, H, N), dev)
+    ssm = torch.empty(b, H, N, P, dtype=torch.float32, device=dev) if ssm is None else ssm
+    _need(ssm, "ssm", torch.float32, (b, H, N, P), dev)
+    dims = make_dims(b, 1, H, P, N, 1, F32)
+    _launch("m3ssd_dequant_state", dev, ctypes.byref(dims), _ptr(codes), _ptr(scale), _ptr(ssm))
+    return ssm
+
+
+def new_cache_q8(batch, nheads, headdim, dstate, ngroups, device):
+    """A zeroed decode cache with its state in 8 bits: angle, ssm (uint8 E4M3 codes,
+    b,H,N,P), scale (b,H,N), x_prev, b_prev."""
+    import torch
+    c = {k: v for k, v in new_cache(batch, nheads, 1, dstate, ngroups, device).items()}
+    c["x_prev"] = torch.zeros(batch, nheads, headdim, dtype=torch.float32, device=device)
+    c["ssm"] = torch.zeros(batch, nheads, dstate, headdim, dtype=torch.uint8, device=device)
+    c["scale"] = torch.zeros(batch, nheads, dstate, dtype=torch.float32, device=device)
+    return c
+
+
+def quant_cache(cache: dict) -> dict:
+    """An fp32 decode cache (:func:`new_cache`, or prefill's) with its state in 8 bits;
+    the other parts are copied."""
+    codes, scale = quant_state(cache["ssm"])
+    return {"angle": cache["angle"].clone(), "ssm": codes, "scale": scale,
+            "x_prev": cache["x_prev"].clone(), "b_prev": cache["b_prev"].clone()}
+
+
+def dequant_cache(cache: dict) -> dict:
+    """The fp32 decode cache that an 8-bit one stands for."""
+    return {"angle": cache["angle"].clone(), "ssm": dequant_state(cache["ssm"], cache["scale"]),
+            "x_prev": cache["x_prev"].clone(), "b_prev": cache["b_prev"].clone()}
+
+
+def _cache_q8_struct(c, b, H, P, N, G, dev, name):
+    import torch
+    f32 = torch.float32
+    _need(c["angle"], name + ".angle", f32, (b, H, N // 2), dev)
+    _need(c["ssm"], name + ".ssm", torch.uint8, (b, H, N, P), dev)
+    _need(c["scale"], name + ".scale", f32, (b, H, N), dev)
+    _need(c["x_prev"], name + ".x_prev", f32, (b, H, P), dev)
+    _need(c["b_prev"], name + ".b_prev", f32, (b, G, N), dev)
+    return CacheQ8(*(c[k].data_ptr() for k in ("angle", "ssm", "scale", "x_prev", "b_prev")))
+
+
+def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=None, D=None, *,
+            cache_out: dict | None = None, y_t=None, check_finite: bool = False):
+    """:func:`step` on a cache whose state is held in 8 bits (:func:`quant_cache`,
+    :func:`new_cache_q8`), through ``m3ssd_step_q8``.  The new cache is written to
+    ``cache_out`` (the old one stays), or over ``cache``; returns y_t (b, H, P)."""
+    import torch
+    b, H, P = x_t.shape
+    G, N = B_t.shape[1], B_t.shape[2]
+    dev, f32, xd = x_t.device, torch.float32, x_t.dtype
+    _need(x_t, "x_t", device=dev)
+    _need(logdecay_t, "logdecay_t", f32, (b, H), dev)
+    _need(beta_t, "beta_t", f32, (b, H), dev)
+    _need(gamma_t, "gamma_t", f32, (b, H), dev)
+    _need(B_t, "B_t", xd, (b, G, N), dev)
+    _need(C_t, "C_t", xd, (b, G, N), dev)
+    _need(theta_t, "theta_t", f32, (b, H, N // 2), dev)
+    _need(D, "D", f32, (H,), dev)
+    ci = _cache_q8_struct(cache, b, H, P, N, G, dev, "cache")
+    co = None if cache_out is None else \
+        _cache_q8_struct(cache_out, b, H, P, N, G, dev, "cache_out")
+    if y_t is None:
+        y_t = torch.empty_like(x_t)
+    _need(y_t, "y_t", xd, (b, H, P), dev)
+    dims = make_dims(b, 1, H, P, N, G, _xdtype(x_t), 0, CHECK_FINITE if check_finite else 0)
+    _launch("m3ssd_step_q8", dev, ctypes.byref(dims), _ptr(x_t), _ptr(logdecay_t), _ptr(beta_t),
+            _ptr(gamma_t), _ptr(B_t), _ptr(C_t), _ptr(theta_t), _ptr(D), ctypes.byref(ci),
+            None if co is None else ctypes.byref(co), _ptr(y_t))
+    return y_t
 
 
 class PreparedFwd:

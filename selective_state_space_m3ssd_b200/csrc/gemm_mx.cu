@@ -1,0 +1,445 @@
+// Product of microscaled operands on the sm_100a tensor cores:
+//     D (M x N, bf16, row-major, row stride ldd) = A (M x K) W^T,
+// with A in E2M1 or E4M3 codes and W (N x K) in E2M1 codes, blocks of 32 along K with a
+// power-of-two scale each (mx.cuh), and fp32 accumulation in tensor memory.  The tensor
+// cores apply the scales: an operand's codes go from global to shared memory by TMA, its
+// scales by one bulk copy a 512-byte tile and from there into TMEM (tcgen05.cp), and
+// kind::mxf4 (A in 4 bits) or kind::mxf8f6f4 (A in 8 bits; TMA spreads the packed 4-bit
+// codes of W over 8-bit containers as it loads them) multiplies value times scale.
+//
+// The operand with 128 rows a tile ("rows") is A, or W for few tokens (SWAP): then the
+// tokens are the product's narrow side, no more of them than the tile is wide, and W's
+// rows fill the 128 lanes.  One persistent CTA per SM; warp 0 copies, warp 1 issues the
+// scale copies and the products, warps 2-5 are the epilogue on the other of the two
+// accumulators.  Every stage of the ring has its own TMEM columns for its scales: they are
+// free when the stage is (the products that read them have finished), so a copy never
+// overtakes a product.
+//
+// Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
+// others, and the launch is counted in a device word the host query reads.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <cstddef>
+#include <cstring>
+
+#include "internal.h"
+#include "mx.cuh"
+#include "tc5.cuh"
+
+namespace m3ssd {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+__device__ unsigned int g_gemm_mx_wait_timeouts;
+
+namespace {
+
+constexpr int BM = 128;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kTile = 512;  // bytes of a scale tile (128 rows x 4 blocks)
+constexpr uint32_t kStgBytes = 32 * 32 * 2;
+constexpr int kEpiWarps = 4, kThreads = 32 * (2 + kEpiWarps);
+
+// AF: A's format.  A stage is 128 bytes of K a row: 256 values in 4 bits, 128 in 8.
+template <int AF, int BN, bool SWAP>
+struct Cfg {
+  static constexpr int ATOMS = AF == mx::kFp4 ? 2 : 1;       // scale tiles along K a stage
+  static constexpr int NSB = (BN + 127) / 128;               // scale tiles along the columns
+  static constexpr uint32_t R_BYTES = BM * 128, C_BYTES = BN * 128;
+  // bytes the copies of a stage count on its barrier: W's 4-bit codes count as they are in
+  // global memory, whether or not they are spread
+  static constexpr uint32_t R_TX = (AF != mx::kFp4 && SWAP) ? R_BYTES / 2 : R_BYTES;
+  static constexpr uint32_t C_TX = (AF != mx::kFp4 && !SWAP) ? C_BYTES / 2 : C_BYTES;
+  static constexpr uint32_t SR_BYTES = ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
+  static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
+  static constexpr int STAGES = (208 * 1024) / STAGE < 8 ? (208 * 1024) / STAGE : 8;
+  static constexpr int SF_COLS = ATOMS * 4 * (1 + NSB);      // TMEM columns of a stage's scales
+  static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
+  static constexpr int COLS = 2 * ACC_COLS + STAGES * SF_COLS;
+  static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static_assert(COLS <= 512, "tensor memory");
+  // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
+  // E4M3 = 0, E2M1 = 5)
+  static constexpr uint32_t FA = AF == mx::kFp4 ? 1 : 0, FW = AF == mx::kFp4 ? 1 : 5;
+  static constexpr uint32_t IDESC = tc5::idesc_mx(BM, BN, SWAP ? FW : FA, SWAP ? FA : FW);
+};
+
+template <typename C>
+struct Smem {
+  uint8_t r[C::STAGES][C::R_BYTES];
+  uint8_t c[C::STAGES][C::C_BYTES];
+  uint8_t sr[C::STAGES][C::SR_BYTES];
+  uint8_t sc[C::STAGES][C::SC_BYTES];
+  uint8_t stg[kEpiWarps][2][kStgBytes];
+  uint64_t full[C::STAGES];
+  uint64_t empty[C::STAGES];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  uint32_t err;
+};
+
+struct MMaps {
+  CUtensorMap r, c;  // codes of the rows and the columns operand, box 128 bytes x 128 / BN rows
+  CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 32 x 32 (stores; when vec)
+};
+
+struct MArgs {
+  int M, N;  // of D
+  int64_t ldd;
+  __nv_bfloat16* D;
+  const uint8_t* rs;  // scales of the rows and the columns operand
+  const uint8_t* cs;
+  int mt, nt;         // tiles along the rows and the columns operand
+  int nkb;            // 128-column groups of K
+  int crb;            // 128-row blocks of the columns operand
+  bool vec;
+};
+
+template <int AF, int BN, bool SWAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_mx_kernel(MArgs g, const __grid_constant__ MMaps tm) {
+  using C = Cfg<AF, BN, SWAP>;
+  constexpr int STAGES = C::STAGES, ATOMS = C::ATOMS, NSB = C::NSB;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw_addr = tc5::saddr(smem_raw);
+  Smem<C>& sm = *reinterpret_cast<Smem<C>*>(smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int total = g.mt * g.nt, nk = (g.nkb + ATOMS - 1) / ATOMS;
+  volatile uint32_t* err = &sm.err;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc5::mbar_init(&sm.full[s], 1);
+      tc5::mbar_init(&sm.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc5::mbar_init(&sm.tfull[i], 1);
+      tc5::mbar_init(&sm.tempty[i], kEpiWarps);
+    }
+    tc5::mbar_init(&sm.drain, 1);
+    tc5::fence_mbar_init();
+    sm.err = 0;
+  }
+  if (warp == 1) tc5::tmem_alloc(&sm.tmem, C::TMEM_COLS);
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  const uint32_t tmem = sm.tmem, sf0 = tmem + 2 * C::ACC_COLS;
+
+  if (warp == 0) {
+    // ---- producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, last_par = 0;
+      for (int t = blockIdx.x; t < total && !*err; t += gridDim.x) {
+        const int mb = t / g.nt, nb = t % g.nt;
+        const int rb0 = nb * BN / 128;  // the columns operand's first scale tile
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!tc5::mbar_wait(&sm.empty[stage], phase ^ 1u, kWaitLimitNs, err)) {
+            *err = 1;
+            break;
+          }
+          const int a0 = kb * ATOMS, na = min(ATOMS, g.nkb - a0);
+          const int nsb = min(NSB, g.crb - rb0);
+          uint64_t* const full = &sm.full[stage];
+          tc5::mbar_arrive_expect_tx(
+              full, C::R_TX + C::C_TX + (uint32_t)((1 + nsb) * na) * kTile);
+          tc5::tma_load_2d(tc5::saddr(sm.r[stage]), &tm.r, full, kb * 128, mb * BM);
+          tc5::tma_load_2d(tc5::saddr(sm.c[stage]), &tm.c, full, kb * 128, nb * BN);
+          tc5::bulk_load(tc5::saddr(sm.sr[stage]), g.rs + ((int64_t)mb * g.nkb + a0) * kTile,
+                         na * kTile, full);
+          for (int j = 0; j < nsb; ++j)
+            tc5::bulk_load(tc5::saddr(sm.sc[stage]) + j * ATOMS * kTile,
+                           g.cs + ((int64_t)(rb0 + j) * g.nkb + a0) * kTile, na * kTile, full);
+          armed |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // the copies issued last land before the CTA can exit
+      for (int s = 0; s < STAGES; ++s)
+        if (armed & (1u << s)) (void)tc5::mbar_wait(&sm.full[s], (last_par >> s) & 1u, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    // ---- scale copies and products
+    if (lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, aphase = 0;
+      for (int t = blockIdx.x; t < total && !*err; t += gridDim.x) {
+        if (!tc5::mbar_wait(&sm.tempty[acc], aphase ^ 1u, kWaitLimitNs, err)) {
+          *err = 1;
+          break;
+        }
+        tc5::fence_after_sync();
+        const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+        const uint32_t shift = (uint32_t)((t % g.nt) * BN % 128) / 32;  // inside the first tile
+        bool ok = true;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!tc5::mbar_wait(&sm.full[stage], phase, kWaitLimitNs, err)) {
+            *err = 1;
+            ok = false;
+            break;
+          }
+          tc5::fence_after_sync();
+          const int na = min(ATOMS, g.nkb - kb * ATOMS);
+          // columns: rows operand's tiles, then for each tile along K the columns operand's
+          const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * 4;
+#pragma unroll
+          for (int a = 0; a < ATOMS; ++a) {
+            if (a < na) {
+              tc5::cp_scales(sfr + 4 * a, tc5::desc_scales(tc5::saddr(sm.sr[stage]) + a * kTile));
+#pragma unroll
+              for (int j = 0; j < NSB; ++j)
+                tc5::cp_scales(sfc + 4 * (a * NSB + j),
+                               tc5::desc_scales(tc5::saddr(sm.sc[stage]) + (j * ATOMS + a) * kTile));
+            }
+          }
+          const uint64_t dr = tc5::desc_sw128(tc5::saddr(sm.r[stage]), 16, 1024);
+          const uint64_t dc = tc5::desc_sw128(tc5::saddr(sm.c[stage]), 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
+            if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
+              if (k / 2 < na)
+                tc5::mma_mxf4(d, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
+                              tc5::idesc_mx_sf(C::IDESC, 2 * (k & 1)), sfr + 4 * (k / 2),
+                              sfc + 4 * NSB * (k / 2) + shift, kb > 0 || k > 0);
+            } else {  // 32 values, one block
+              tc5::mma_mxf8f6f4(d, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
+                                tc5::idesc_mx_sf(C::IDESC, k), sfr, sfc + shift, kb > 0 || k > 0);
+            }
+          }
+          tc5::commit(&sm.empty[stage]);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        tc5::commit(&sm.tfull[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          aphase ^= 1u;
+        }
+      }
+      // every product issued has finished before TMEM is released
+      tc5::commit(&sm.drain);
+      (void)tc5::mbar_wait(&sm.drain, 0, kWaitLimitNs);
+    }
+  } else {
+    // ---- epilogue: TMEM lane quarter q, one row of the rows operand a thread
+    const int q = warp & 3, ew = warp - 2;
+    int acc = 0;
+    uint32_t nst = 0, aphase = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
+        *err = 1;
+        break;
+      }
+      tc5::fence_after_sync();
+      const int mb = t / g.nt, nb = t % g.nt;
+      const int row0 = mb * BM + 32 * q, row = row0 + lane, col0 = nb * BN;
+      const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS);
+      if constexpr (SWAP) {
+        // a row is a column of D: 32 lanes store 32 consecutive values
+#pragma unroll
+        for (int c = 0; c < BN / 16; ++c) {
+          uint32_t v[16];
+          tc5::ld_32x32b_x16(tbase + (uint32_t)(16 * c), v);
+          tc5::wait_ld();
+          tc5::reg_after_ld(v);
+          if (row < g.N) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int m = col0 + 16 * c + j;
+              if (m < g.M) g.D[m * g.ldd + row] = __float2bfloat16_rn(__uint_as_float(v[j]));
+            }
+          }
+        }
+        tc5::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
+      } else if (g.vec) {
+        // the row into registers as bf16, then TMEM goes back: the stores below drain
+        // while the next tile's products run
+        const int nch = min(BN / 32, (g.N - col0 + 31) / 32);
+        uint32_t pk[BN / 32][16];
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          if (c < nch) {
+#pragma unroll
+            for (int hc = 0; hc < 2; ++hc) {
+              uint32_t v[16];
+              tc5::ld_32x32b_x16(tbase + (uint32_t)(32 * c + 16 * hc), v);
+              tc5::wait_ld();
+              tc5::reg_after_ld(v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]),
+                                                         __uint_as_float(v[2 * j + 1]));
+                pk[c][8 * hc + j] = *reinterpret_cast<uint32_t*>(&h);
+              }
+            }
+          }
+        }
+        tc5::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          if (c < nch) {
+            uint8_t* const blk = sm.stg[ew][nst & 1];
+            if (lane == 0) tc5::bulk_wait_group_read<1>();  // the block's previous store has read it
+            __syncwarp();
+            uint4* dst = reinterpret_cast<uint4*>(blk + lane * 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
+            tc5::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 32 * c, row0);
+              tc5::bulk_commit_group();
+            }
+            ++nst;
+          }
+        }
+      } else {
+        const int nch = min(BN / 32, (g.N - col0 + 31) / 32);
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+          const int col = col0 + 32 * c;
+          uint32_t v[32];
+          tc5::ld_32x32b_x32(tbase + (uint32_t)(32 * c), v);
+          tc5::wait_ld();
+          tc5::reg_after_ld(v);
+          if (row < g.M) {
+            __nv_bfloat16* const drow = g.D + (int64_t)row * g.ldd;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j < g.N) drow[col + j] = __float2bfloat16_rn(__uint_as_float(v[j]));
+          }
+        }
+        tc5::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        aphase ^= 1u;
+      }
+    }
+    if (lane == 0) tc5::bulk_wait_group<0>();  // every store of this warp has landed
+    __syncwarp();
+  }
+  tc5::fence_before_sync();
+  __syncthreads();
+  tc5::fence_after_sync();
+  if (warp == 1) tc5::tmem_dealloc(tmem, C::TMEM_COLS);
+  if (threadIdx.x == 0 && sm.err) atomicAdd(&g_gemm_mx_wait_timeouts, 1u);
+}
+
+// Codes (rows x Kp) as boxes of 128 bytes of shared memory a row.  spread: packed 4-bit
+// codes go to 8-bit containers (16 codes in 8 of 16 bytes).
+bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t Kp, int fmt, bool spread,
+                  uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return false;
+  const cuuint64_t bytes = (cuuint64_t)(fmt == mx::kFp4 ? Kp / 2 : Kp);
+  const cuuint64_t dims[2] = {spread ? (cuuint64_t)Kp : bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {bytes};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Operands {
+  int64_t M, N, K;
+  const void *A, *As, *W, *Ws;
+  void* D;
+  int64_t ldd;
+};
+
+template <int AF, int BN, bool SWAP>
+cudaError_t launch(const Operands& o, cudaStream_t s) {
+  using C = Cfg<AF, BN, SWAP>;
+  const int64_t Kp = mx::pad128(o.K), sms = current_device_sms() > 0 ? current_device_sms() : 148;
+  const int64_t rows = SWAP ? o.N : o.M, cols = SWAP ? o.M : o.N;
+  MMaps tm;
+  memset(&tm, 0, sizeof(tm));
+  const bool spread = AF != mx::kFp4;
+  const bool ok =
+      SWAP ? encode_codes(&tm.r, o.W, o.N, Kp, mx::kFp4, spread, BM) &&
+                 encode_codes(&tm.c, o.A, o.M, Kp, AF, false, BN)
+           : encode_codes(&tm.r, o.A, o.M, Kp, AF, false, BM) &&
+                 encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, spread, BN);
+  if (!ok) return cudaErrorInvalidValue;
+  MArgs g{};
+  g.M = (int)o.M;
+  g.N = (int)o.N;
+  g.ldd = o.ldd;
+  g.D = static_cast<__nv_bfloat16*>(o.D);
+  g.rs = static_cast<const uint8_t*>(SWAP ? o.Ws : o.As);
+  g.cs = static_cast<const uint8_t*>(SWAP ? o.As : o.Ws);
+  const int64_t mt = (rows + BM - 1) / BM, nt = (cols + BN - 1) / BN;
+  if (mt * nt > INT32_MAX) return cudaErrorInvalidValue;
+  g.mt = (int)mt;
+  g.nt = (int)nt;
+  g.nkb = (int)(Kp / 128);
+  g.crb = (int)((cols + 127) / 128);
+  // a TMA store ends a row at a multiple of 16 bytes, so the columns must too
+  g.vec = !SWAP && o.N % 8 == 0 && o.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 15) == 0;
+  if (g.vec) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    const cuuint64_t dims[2] = {(cuuint64_t)o.N, (cuuint64_t)o.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)o.ldd * 2};
+    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t estr[2] = {1, 1};
+    g.vec = fn && fn(&tm.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.D, dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                        CUDA_SUCCESS;
+  }
+  const size_t smem = sizeof(Smem<C>) + 1024;
+  static_assert(sizeof(Smem<C>) + 1024 <= 232448, "one CTA's shared memory");
+  cudaError_t e = cudaFuncSetAttribute(gemm_mx_kernel<AF, BN, SWAP>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = mt * nt;
+  gemm_mx_kernel<AF, BN, SWAP><<<(unsigned)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(g, tm);
+  return cudaGetLastError();
+}
+
+template <int AF>
+cudaError_t launch_af(const Operands& o, cudaStream_t s) {
+  if (o.M <= 16) return launch<AF, 16, true>(o, s);
+  if (o.M <= 64) return launch<AF, 64, true>(o, s);
+  return launch<AF, 128, false>(o, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const void* A,
+                           const void* A_scales, const void* W, const void* W_scales, void* D,
+                           int64_t ldd, cudaStream_t s) {
+  if (M == 0 || N == 0) return cudaSuccess;
+  const Operands o{M, N, K, A, A_scales, W, W_scales, D, ldd};
+  return a_fmt == mx::kFp4 ? launch_af<mx::kFp4>(o, s) : launch_af<mx::kFp8>(o, s);
+}
+
+cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(count, g_gemm_mx_wait_timeouts, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_gemm_mx_wait_timeouts, &zero, sizeof(unsigned int));
+}
+
+}  // namespace m3ssd

@@ -199,6 +199,86 @@ cudaError_t read_and_clear_nonfinite(unsigned int* flag);
 cudaError_t launch_gemm_bf16(int64_t M, int64_t N, int64_t K, const void* A, const void* W,
                              void* D, int64_t ldd, cudaStream_t s);
 cudaError_t read_and_clear_gemm_wait_timeouts(unsigned int* count);
+// The residual addition with the RMS norm (csrc/norm.cu): rows of d values; res and res_out
+// nullable together; y in x's type (fmt < 0) or quantised (fmt a mx.cuh format, Kp codes a
+// row); rstd nullable.
+struct NormArgs {
+  int64_t rows, d;
+  bool bf16, res_bf16;  // types of x and y, and of res and res_out
+  float eps;
+  const void* x;
+  const void* res;
+  const float* w;
+  void* y;
+  void* res_out;
+  float* rstd;
+  int fmt;
+  int64_t Kp;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+// Its backward; `part` holds norm_bwd_workspace_bytes(rows, d) bytes (one partial dw row a
+// CTA, so the size depends on the current device's SM count).
+struct NormBwdArgs {
+  int64_t rows, d;
+  bool bf16, res_bf16;  // types of dy and of r
+  const void* dy;
+  const void* r;
+  const float* w;
+  const float* rstd;
+  const float* dres;  // nullable
+  float* dr;
+  float* dw;
+  float* part;
+};
+bool norm_width_ok(int64_t d);
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t d);
+cudaError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t s);
+
+// Microscaled formats (csrc/mx.cuh, csrc/mx.cu); fmt 0: E2M1, 1: E4M3 codes.
+cudaError_t launch_mx_quant(int fmt, int64_t rows, int64_t cols, bool bf16, const void* x,
+                            int64_t ldx, void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_mx_dequant(int fmt, int64_t rows, int64_t cols, bool bf16, const void* codes,
+                              const void* scales, void* x, int64_t ldx, cudaStream_t s);
+// D (M x N, bf16, row stride ldd) = A W^T of a microscaled A (a_fmt, M x K) and E2M1 W
+// (N x K), fp32 accumulation (csrc/gemm_mx.cu).
+cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const void* A,
+                           const void* A_scales, const void* W, const void* W_scales, void* D,
+                           int64_t ldd, cudaStream_t s);
+cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count);
+
+// Decode step on a cache whose state is held as E4M3 codes with a scale a row
+// (csrc/step_q8.cu); every *_out may be the input it replaces.
+struct StepQ8Args {
+  int64_t b, H, P, N, G;
+  bool bf16;
+  const void* x_t;
+  const float* logdecay_t;
+  const float* beta_t;   // nullable
+  const float* gamma_t;
+  const void* B_t;
+  const void* C_t;
+  const float* theta_t;  // nullable
+  const float* D;        // nullable
+  const float* angle;
+  const uint8_t* ssm;
+  const float* scale;
+  const float* x_prev;
+  const float* b_prev;
+  float* angle_out;
+  uint8_t* ssm_out;
+  float* scale_out;
+  float* x_prev_out;
+  float* b_prev_out;
+  void* y_t;
+};
+cudaError_t launch_step_q8(const StepQ8Args& a, cudaStream_t s);
+// The state (rows of P fp32 values) into that form and back.
+cudaError_t launch_quant_state(int64_t rows, int64_t P, const float* h, void* codes, float* scale,
+                               cudaStream_t s);
+cudaError_t launch_dequant_state(int64_t rows, int64_t P, const void* codes, const float* scale,
+                                 float* h, cudaStream_t s);
 // Decode step (two launches: the state/outputs, then b_prev <- B_t).
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 

@@ -86,7 +86,9 @@ m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count) {
   unsigned int nm32 = 0, ns = 0;
   if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_mimo32_wait_timeouts(&nm32));
   if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_seg_wait_timeouts(&ns));
-  *count = n + nb + nm + ng + n32 + nw + nm32 + ns;
+  unsigned int nx = 0;
+  if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_gemm_mx_wait_timeouts(&nx));
+  *count = n + nb + nm + ng + n32 + nw + nm32 + ns + nx;
   return st;
 }
 
