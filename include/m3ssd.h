@@ -389,8 +389,8 @@ m3ssd_status m3ssd_block_fwd(const m3ssd_block_dims* dims, const m3ssd_block_wei
  * callers that compose the block themselves:
  *     D (M x N, row stride ldd elements) = A (M x K) W^T
  * A (M x K) and W (N x K): bf16, row-major (row stride K), 16-byte aligned,
- * K a multiple of 8; D: bf16, ldd >= N, 2-byte aligned (16-byte stores when D
- * is 16-byte aligned and ldd a multiple of 8).  fp32 accumulation on the
+ * K a multiple of 8; D: bf16, ldd >= N, 2-byte aligned (tensor stores when D
+ * is 16-byte aligned and N and ldd are multiples of 8).  fp32 accumulation on the
  * tensor cores, each output rounded once to bf16 (nearest even).  M, N, K up
  * to 2^31 - 1 with at most 2^31 - 1 output tiles of 128 x 256; M = 0 or N = 0
  * does nothing.  Other shapes or alignments: M3SSD_ERR_INVALID_ARG (or

@@ -109,7 +109,7 @@ struct GArgs {
   int64_t ldd;
   __nv_bfloat16* D;
   int mt, nt, nk;  // tiles along M and N, K slices
-  bool vec;        // TMA stores (ldd % 8 == 0 and D 16-byte aligned)
+  bool vec;        // TMA stores (N % 8 == 0, ldd % 8 == 0 and D 16-byte aligned)
   bool nfast;      // tile t = (row block t / nt, column block t % nt), else (t % mt, t / mt)
 };
 
@@ -385,7 +385,9 @@ cudaError_t launch_gemm_bf16(int64_t M, int64_t N, int64_t K, const void* A, con
   g.mt = (int)((M + H * BM - 1) / (H * BM));
   g.nt = (int)nt;
   g.nk = (int)((K + BK - 1) / BK);
-  g.vec = ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(D) & 15) == 0;
+  // a TMA store ends a row at a multiple of 16 bytes (it fills the rest with zeros), so N
+  // must be a multiple of 8 too
+  g.vec = N % 8 == 0 && ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(D) & 15) == 0;
   // the CTAs in flight share the panels of the smaller operand, which L2 keeps
   // while the larger one streams from DRAM once
   g.nfast = M > N;

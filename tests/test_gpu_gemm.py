@@ -64,6 +64,21 @@ def test_gemm_strided_and_unaligned_outputs():
     assert flat[0].item() == 7.0
 
 
+def test_gemm_row_ends_inside_a_16_byte_unit():
+    """N not a multiple of 8 with an aligned row stride: the columns past N and the bytes
+    behind the last row's end stay as they were."""
+    M, N, ldd = 333, 300, 312
+    A, W = operands(M, N, 96, 6)
+    big = torch.full((M + 1, ldd), 7.0, dtype=torch.bfloat16, device="cuda")
+    st = m3.load().m3ssd_gemm_bf16(M, N, 96, ctypes.c_void_p(A.data_ptr()),
+                                   ctypes.c_void_p(W.data_ptr()),
+                                   ctypes.c_void_p(big.data_ptr()), ldd, None)
+    assert st == m3.OK
+    torch.cuda.synchronize()
+    check(big[:M, :N], A, W)
+    assert torch.all(big[:M, N:] == 7.0) and torch.all(big[M] == 7.0)
+
+
 def test_gemm_two_half_tiles_ragged():
     """A shape whose 256-row tiles fill the SMs evenly (the two-half instance),
     with ragged M and K, on sampled rows."""
