@@ -203,7 +203,7 @@ def _ptr(t):
 
 def _stream_handle(device):
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def _xdtype(t) -> int:
@@ -224,6 +224,10 @@ def _need_shape(t, name, dtype=None, shape=None):
 
 def _need(t, name, dtype=None, shape=None, device=None):
     if t is None:
+        return
+    # one pass over what a valid tensor has; what is wrong is found below
+    if (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape) and \
+            (device is None or t.device == device) and t.is_cuda and t.is_contiguous():
         return
     _need_shape(t, name, dtype, shape)
     if not t.is_cuda:
@@ -672,13 +676,19 @@ def _launch(name: str, dev, *args):
     """Calls a C entry point whose last argument is the stream, with the tensors'
     device current (a stream, a workspace size and a launch all go by it)."""
     import torch
-    f = getattr(load(), name)
+    f = getattr(_lib or load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        st = f(*args, _stream_handle(dev))
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream_handle(dev))
-    _check(st, name)
+            st = f(*args, stream)
+    if st != OK:
+        _check(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ---- microscaled tensors and their product ------------------------------------------
@@ -748,7 +758,7 @@ def mx_quant(x, fmt: str, *, out: MXTensor | None = None) -> MXTensor:
     elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
         raise ValueError(f"out must be {fmt} of {rows} x {cols}")
     o = _mx_struct(out, "out", x.device)
-    _launch("m3ssd_mx_quant", x.device, ctypes.byref(o), _xdtype(x), _ptr(x), ldx)
+    _launch("m3ssd_mx_quant", x.device, ctypes.byref(o), _xdtype(x), _addr(x), ldx)
     return out
 
 
@@ -762,7 +772,7 @@ def mx_dequant(t: MXTensor, dtype=None, *, out=None):
     _need_shape(out, "out", dtype, (t.rows, t.cols))
     ldx = _rows_stride(out, "out")
     m = _mx_struct(t, "t", out.device)
-    _launch("m3ssd_mx_dequant", dev, ctypes.byref(m), _xdtype(out), _ptr(out), ldx)
+    _launch("m3ssd_mx_dequant", dev, ctypes.byref(m), _xdtype(out), _addr(out), ldx)
     return out
 
 
@@ -776,7 +786,7 @@ def gemm_mx(A: MXTensor, W: MXTensor, *, out=None):
     _need_shape(out, "out", torch.bfloat16, (A.rows, W.rows))
     ldd = _rows_stride(out, "out")
     a, w = _mx_struct(A, "A", out.device), _mx_struct(W, "W", out.device)
-    _launch("m3ssd_gemm_mx", dev, ctypes.byref(a), ctypes.byref(w), _ptr(out), ldd)
+    _launch("m3ssd_gemm_mx", dev, ctypes.byref(a), ctypes.byref(w), _addr(out), ldd)
     return out
 
 
@@ -817,9 +827,9 @@ def add_rmsnorm(x, w, *, residual=None, eps: float = 1e-6, fmt: str | None = Non
         mx = _mx_struct(y, "y", dev)
     rstd = torch.empty(rows, dtype=f32, device=dev) if want_rstd else None
     dims = NormDims(rows, d, xd, rd, eps, 0)
-    _launch("m3ssd_add_rmsnorm", dev, ctypes.byref(dims), _ptr(x), _ptr(residual), _ptr(w),
-            None if mx is not None else _ptr(y), None if mx is None else ctypes.byref(mx),
-            _ptr(residual_out), _ptr(rstd))
+    _launch("m3ssd_add_rmsnorm", dev, ctypes.byref(dims), _addr(x), _addr(residual), _addr(w),
+            None if mx is not None else _addr(y), None if mx is None else ctypes.byref(mx),
+            _addr(residual_out), _addr(rstd))
     return y, residual_out, rstd
 
 
@@ -851,8 +861,8 @@ def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=No
         need = add_rmsnorm_bwd_workspace_size(dims)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("m3ssd_add_rmsnorm_bwd", dev, ctypes.byref(dims), _ptr(dy), _ptr(r), _ptr(w),
-            _ptr(rstd), _ptr(dres), _ptr(dr), _ptr(dw), _ptr(workspace),
+    _launch("m3ssd_add_rmsnorm_bwd", dev, ctypes.byref(dims), _addr(dy), _addr(r), _addr(w),
+            _addr(rstd), _addr(dres), _addr(dr), _addr(dw), _addr(workspace),
             0 if workspace is None else workspace.numel() * workspace.element_size())
     return dr, dw
 
@@ -871,7 +881,7 @@ def quant_state(ssm, *, codes=None, scale=None):
     _need(codes, "codes", torch.uint8, (b, H, N, P), dev)
     _need(scale, "scale", torch.float32, (b, H, N), dev)
     dims = make_dims(b, 1, H, P, N, 1, F32)
-    _launch("m3ssd_quant_state", dev, ctypes.byref(dims), _ptr(ssm), _ptr(codes), _ptr(scale))
+    _launch("m3ssd_quant_state", dev, ctypes.byref(dims), _addr(ssm), _addr(codes), _addr(scale))
     return codes, scale
 
 
@@ -886,7 +896,7 @@ def dequant_state(codes, scale, *, ssm=None):
     ssm = torch.empty(b, H, N, P, dtype=torch.float32, device=dev) if ssm is None else ssm
     _need(ssm, "ssm", torch.float32, (b, H, N, P), dev)
     dims = make_dims(b, 1, H, P, N, 1, F32)
-    _launch("m3ssd_dequant_state", dev, ctypes.byref(dims), _ptr(codes), _ptr(scale), _ptr(ssm))
+    _launch("m3ssd_dequant_state", dev, ctypes.byref(dims), _addr(codes), _addr(scale), _addr(ssm))
     return ssm
 
 
@@ -950,9 +960,9 @@ def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=Non
         y_t = torch.empty_like(x_t)
     _need(y_t, "y_t", xd, (b, H, P), dev)
     dims = make_dims(b, 1, H, P, N, G, _xdtype(x_t), 0, CHECK_FINITE if check_finite else 0)
-    _launch("m3ssd_step_q8", dev, ctypes.byref(dims), _ptr(x_t), _ptr(logdecay_t), _ptr(beta_t),
-            _ptr(gamma_t), _ptr(B_t), _ptr(C_t), _ptr(theta_t), _ptr(D), ctypes.byref(ci),
-            None if co is None else ctypes.byref(co), _ptr(y_t))
+    _launch("m3ssd_step_q8", dev, ctypes.byref(dims), _addr(x_t), _addr(logdecay_t), _addr(beta_t),
+            _addr(gamma_t), _addr(B_t), _addr(C_t), _addr(theta_t), _addr(D), ctypes.byref(ci),
+            None if co is None else ctypes.byref(co), _addr(y_t))
     return y_t
 
 

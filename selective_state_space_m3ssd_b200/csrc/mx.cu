@@ -17,78 +17,104 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // groups a half-warp has in flight
 
 struct MxArgs {
-  uint32_t rows, rows_pad, cols, nkb;  // nkb: 128-column groups
-  uint32_t total;                      // rows_pad * nkb (quant) or rows * nkb (dequant)
+  uint32_t rows, cols, nkb;  // nkb: 128-column groups a row
+  uint32_t total;            // groups: rows (quant: rounded up to 128) * nkb
   int64_t ldx;
   void* x;
   uint8_t* codes;
   uint8_t* scales;
 };
 
+// A half-warp's groups: i, i + step, ...; row and group within the row kept beside i (a
+// division a group would cost as much as its conversion).
+struct Walk {
+  uint32_t i, row, kb, nkb, drow, dkb, step;
+  __device__ Walk(uint32_t first, uint32_t step, uint32_t nkb) : i(first), nkb(nkb), step(step) {
+    row = i / nkb;
+    kb = i - row * nkb;
+    drow = step / nkb;
+    dkb = step - drow * nkb;
+  }
+  __device__ void next() {  // i stays below 2^32: at most 2^31 groups and a step below 2^31
+    i += step;
+    row += drow;
+    kb += dkb;
+    if (kb >= nkb) {
+      kb -= nkb;
+      ++row;
+    }
+  }
+};
+
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
-  const uint32_t lane = threadIdx.x & 31, sub = lane & 15;
-  const uint32_t nhalf = gridDim.x * (kThreads / 16);
-  const uint32_t wbase = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 2;
-  const int64_t Kp = (int64_t)a.nkb * 128;
-  const T* const x = static_cast<const T*>(a.x);
-  for (uint64_t i0 = wbase; i0 < a.total; i0 += (uint64_t)kUnroll * nhalf) {
+  const uint32_t sub = threadIdx.x & 15, nhalf = gridDim.x * (kThreads / 16);
+  Walk w((blockIdx.x * kThreads + threadIdx.x) >> 4, nhalf, a.nkb);
+  const T* const x = static_cast<const T*>(a.x) + 8 * sub;
+  // the two halves of a warp go round together (quant8's shuffles): i - its half's place
+  for (uint32_t base = w.i & ~1u; base < a.total; base += kUnroll * nhalf) {
     float v[kUnroll][8];
-    uint32_t row[kUnroll], kb[kUnroll];
+    uint32_t at[kUnroll];  // byte offset of the scale word, in words
+    bool live[kUnroll];
+    const uint32_t i0 = w.i;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint64_t i = i0 + (uint64_t)u * nhalf + (lane >> 4);
-      row[u] = i < a.total ? (uint32_t)i / a.nkb : 0xffffffffu;
-      kb[u] = (uint32_t)i - row[u] * a.nkb;
-      const uint32_t c = kb[u] * 128 + sub * 8;
+      const uint32_t c = w.kb * 128 + sub * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-      if (row[u] < a.rows && c < a.cols) {
-        const T* p = x + (int64_t)row[u] * a.ldx + c;
+      live[u] = w.row < a.rows;
+      if (live[u] && c < a.cols) {
+        const T* p = x + ((int64_t)w.row * a.ldx + w.kb * 128);
         if (VEC && c + 8 <= a.cols)
           mx::load8(p, v[u]);
         else
           mx::load8_tail(p, (int)(a.cols - c), v[u]);
       }
+      at[u] = (((w.row >> 7) * a.nkb + w.kb) << 7) + ((w.row & 31) << 2) + ((w.row >> 5) & 3);
+      w.next();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      mx::quant_store8<FMT>(v[u], row[u], kb[u] * 16 + sub, Kp, a.codes, a.scales,
-                            row[u] < a.rows, 0xffffffffu);
-      if (row[u] >= a.rows && row[u] < a.rows_pad && sub == 0)  // the last tile's missing rows
-        *reinterpret_cast<uint32_t*>(a.scales + mx::scale_word(row[u], kb[u], a.nkb)) = 0;
+      const uint32_t i = i0 + u * nhalf;
+      uint2 c;
+      const uint32_t word = mx::quant8<FMT>(v[u], c);
+      if (live[u]) mx::store_codes<FMT>(a.codes, i, sub, c);
+      // rows missing from the last tile have zeros
+      if (sub == 0 && i < a.total)
+        reinterpret_cast<uint32_t*>(a.scales)[at[u]] = live[u] ? word : 0u;
     }
   }
 }
 
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
-  const uint32_t lane = threadIdx.x & 31, sub = lane & 15;
-  const uint32_t nhalf = gridDim.x * (kThreads / 16);
-  const int64_t Kp = (int64_t)a.nkb * 128;
-  T* const x = static_cast<T*>(a.x);
-  const uint32_t hbase = (blockIdx.x * kThreads + threadIdx.x) >> 4;
-  for (uint64_t i0 = hbase; i0 < a.total; i0 += (uint64_t)kUnroll * nhalf) {
+  const uint32_t sub = threadIdx.x & 15, nhalf = gridDim.x * (kThreads / 16);
+  Walk w((blockIdx.x * kThreads + threadIdx.x) >> 4, nhalf, a.nkb);
+  T* const x = static_cast<T*>(a.x) + 8 * sub;
+  while (w.i < a.total) {
     uint2 q[kUnroll];
-    uint32_t byte[kUnroll], row[kUnroll], kb[kUnroll];
+    uint32_t byte[kUnroll], col[kUnroll];
+    T* out[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint64_t i = i0 + (uint64_t)u * nhalf;
-      row[u] = i < a.total ? (uint32_t)i / a.nkb : 0xffffffffu;
-      kb[u] = (uint32_t)i - row[u] * a.nkb;
-      if (row[u] < a.rows) {
-        const int64_t c = (int64_t)kb[u] * 16 + sub;
+      col[u] = 0xffffffffu;
+      const uint32_t c = w.kb * 128 + sub * 8;
+      if (w.i < a.total && c < a.cols) {
+        col[u] = c;
+        out[u] = x + ((int64_t)w.row * a.ldx + w.kb * 128);
         if (FMT == mx::kFp4)
-          q[u].x = *reinterpret_cast<const uint32_t*>(a.codes + (int64_t)row[u] * (Kp / 2) + c * 4);
+          q[u].x = *reinterpret_cast<const uint32_t*>(a.codes + (int64_t)w.i * 64 + sub * 4);
         else
-          q[u] = *reinterpret_cast<const uint2*>(a.codes + (int64_t)row[u] * Kp + c * 8);
-        byte[u] = a.scales[mx::scale_word(row[u], kb[u], a.nkb) + (sub >> 2)];
+          q[u] = *reinterpret_cast<const uint2*>(a.codes + (int64_t)w.i * 128 + sub * 8);
+        const uint32_t at =
+            (((w.row >> 7) * a.nkb + w.kb) << 7) + ((w.row & 31) << 2) + ((w.row >> 5) & 3);
+        byte[u] = a.scales[(int64_t)at * 4 + (sub >> 2)];
       }
+      w.next();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t c = kb[u] * 128 + sub * 8;
-      if (row[u] >= a.rows || c >= a.cols) continue;
+      if (col[u] == 0xffffffffu) continue;
       const float s = mx::scale_value(byte[u]);
       float v[8];
 #pragma unroll
@@ -98,11 +124,10 @@ __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
         v[2 * j] = f.x * s;
         v[2 * j + 1] = f.y * s;
       }
-      T* p = x + (int64_t)row[u] * a.ldx + c;
-      if (VEC && c + 8 <= a.cols)
-        mx::store8(p, v);
+      if (VEC && col[u] + 8 <= a.cols)
+        mx::store8(out[u], v);
       else
-        mx::store8_tail(p, (int)(a.cols - c), v);
+        mx::store8_tail(out[u], (int)(a.cols - col[u]), v);
     }
   }
 }
@@ -120,9 +145,7 @@ cudaError_t launch(const MxArgs& a, bool quant, cudaStream_t s) {
 }
 
 cudaError_t dispatch(int fmt, bool bf16, const MxArgs& a, bool quant, cudaStream_t s) {
-  // 16-byte accesses need every row to start on a 16-byte boundary
-  const int64_t e = bf16 ? 2 : 4;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) % 16) == 0 && (a.ldx * e) % 16 == 0;
+  const bool vec = bf16 ? mx::aligned8<__nv_bfloat16>(a.x, a.ldx) : mx::aligned8<float>(a.x, a.ldx);
   if (a.total == 0) return cudaSuccess;
   if (fmt == mx::kFp4) {
     if (bf16)
@@ -144,10 +167,9 @@ cudaError_t launch_mx_quant(int fmt, int64_t rows, int64_t cols, bool bf16, cons
                             int64_t ldx, void* codes, void* scales, cudaStream_t s) {
   MxArgs a{};
   a.rows = (uint32_t)rows;
-  a.rows_pad = (uint32_t)mx::pad128(rows);
   a.cols = (uint32_t)cols;
   a.nkb = (uint32_t)(mx::pad128(cols) / 128);
-  a.total = a.rows_pad * a.nkb;
+  a.total = (uint32_t)mx::pad128(rows) * a.nkb;
   a.ldx = ldx;
   a.x = const_cast<void*>(x);
   a.codes = static_cast<uint8_t*>(codes);

@@ -31,19 +31,17 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int64_t kb, int64_t nkb
   return ((r >> 7) * nkb + kb) * 512 + (i & 31u) * 16 + (i >> 5) * 4;
 }
 
-// The scale byte for a block whose largest magnitude has these bits.
+// The scale byte for a block whose largest magnitude has these bits: adding what is missing
+// from maxval's mantissa to 2 carries into the exponent exactly when m exceeds it.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
-  if (amax_bits >= 0x7f800000u) return 255u;  // NaN or infinity
-  const int e = (int)(amax_bits >> 23) - (FMT == kFp4 ? 2 : 8);  // biased E
-  const uint32_t m = amax_bits & 0x007fffffu;
-  return (uint32_t)max(e + (m > (FMT == kFp4 ? 0x400000u : 0x600000u) ? 1 : 0), 0);
+  constexpr uint32_t up = FMT == kFp4 ? 0x3fffffu : 0x1fffffu;
+  const int e = (int)((amax_bits + up) >> 23) - (FMT == kFp4 ? 2 : 8);  // biased E
+  return amax_bits >= 0x7f800000u ? 255u : (uint32_t)max(e, 0);  // 255: NaN or infinity
 }
-// 2^-E as a float, E = byte - 127 (byte 255: 0, which makes every finite code 0).
+// 2^-E as a float, E = byte - 127, for the bytes scale_byte gives a finite block (at most 253).
 __device__ __forceinline__ float inv_scale(uint32_t byte) {
-  // biased exponent of 2^-E: 254 - byte; byte 254 (2^-127) is subnormal
-  return byte < 254u ? __uint_as_float((254u - byte) << 23)
-                     : __uint_as_float(byte == 254u ? 0x00400000u : 0u);
+  return __uint_as_float((254u - byte) << 23);
 }
 // 2^E as a float (byte 0 is the subnormal 2^-127, byte 255 NaN).
 __device__ __forceinline__ float scale_value(uint32_t byte) {
@@ -104,47 +102,51 @@ __device__ __forceinline__ float2 unpack2_e2m1(uint32_t codes) {
   return half2_bits_to_float2(h);
 }
 
-// The largest magnitude's bits of eight values (integer order: NaN > infinity > finite).
-__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  return m;
+// The largest magnitude of a, b and c; NaN when one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  const float m = max3_abs(v[0], v[1], v[2]);
+  return max3_abs(max3_abs(m, v[3], v[4]), max3_abs(v[5], v[6], v[7]), 0.f);
 }
 
-// Quantises a lane's eight values (columns 8 c .. 8 c + 7 of row r, four lanes to a block
-// of 32, sixteen to a scale word; every lane of a 16-lane group is in the same row and
-// takes part) and stores the codes; the group's first lane stores the scale word.
+// A lane's eight of the values of a 128-column group (sixteen lanes; four lanes to a block of
+// 32) to codes; returns the group's scale word, in every lane.  Warps call it together.
 template <int FMT>
-__device__ __forceinline__ void quant_store8(const float (&v)[8], int64_t r, int64_t c, int64_t Kp,
-                                             uint8_t* __restrict__ codes,
-                                             uint8_t* __restrict__ scales, bool active,
-                                             uint32_t mask) {
-  uint32_t m = amax_bits8(v);
-  m = max(m, __shfl_xor_sync(mask, m, 1));
-  m = max(m, __shfl_xor_sync(mask, m, 2));
-  const uint32_t byte = scale_byte<FMT>(m);
+__device__ __forceinline__ uint32_t quant8(const float (&v)[8], uint2& codes) {
+  float m = amax8(v);
+  m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 1), 0.f);
+  m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, 2), 0.f);
+  const uint32_t byte = scale_byte<FMT>(__float_as_uint(m));
   const float inv = inv_scale(byte);
   float q[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j] = byte == 255u ? 0.f : v[j] * inv;
-  // the four blocks' bytes into one word
-  uint32_t w = byte << (8 * ((threadIdx.x >> 2) & 3));
-  w |= __shfl_xor_sync(mask, w, 4);
-  w |= __shfl_xor_sync(mask, w, 8);
-  if (!active) return;
+  for (int j = 0; j < 8; ++j) q[j] = v[j] * inv;
   if (FMT == kFp4) {
-    *reinterpret_cast<uint32_t*>(codes + r * (Kp / 2) + c * 4) = pack_e2m1(q);
+    codes = make_uint2(pack_e2m1(q), 0u);
   } else {
-    *reinterpret_cast<uint2*>(codes + r * Kp + c * 8) = make_uint2(
-        pack4_e4m3(q[0], q[1], q[2], q[3]), pack4_e4m3(q[4], q[5], q[6], q[7]));
+    codes = make_uint2(pack4_e4m3(q[0], q[1], q[2], q[3]), pack4_e4m3(q[4], q[5], q[6], q[7]));
   }
-  if ((threadIdx.x & 15) == 0)
-    *reinterpret_cast<uint32_t*>(scales + scale_word(r, c >> 4, Kp >> 7)) = w;
+  if (byte == 255u) codes = make_uint2(0u, 0u);
+  uint32_t w = byte << (8 * ((threadIdx.x >> 2) & 3));  // the four blocks' bytes
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  w |= __shfl_xor_sync(0xffffffffu, w, 8);
+  return w;
+}
+// Stores a lane's codes of 128-column group i (counted over the rows' groups).
+template <int FMT>
+__device__ __forceinline__ void store_codes(uint8_t* codes, int64_t i, uint32_t sub, uint2 c) {
+  if (FMT == kFp4)
+    *reinterpret_cast<uint32_t*>(codes + i * 64 + sub * 4) = c.x;
+  else
+    *reinterpret_cast<uint2*>(codes + i * 128 + sub * 8) = c;
 }
 
-// Eight elements from global memory as floats: 16-byte loads, or one by one up to `n`
-// valid ones (the rest zero).
+// Eight elements from global memory as floats in one access (16 bytes of bf16, 32 of fp32,
+// aligned to that), or one by one up to `n` valid ones (the rest zero).
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   const uint4 w = *reinterpret_cast<const uint4*>(p);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -155,9 +157,11 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   }
 }
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                 "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
 }
 template <typename T>
 __device__ __forceinline__ void load8_tail(const T* p, int n, float (&v)[8]) {
@@ -174,8 +178,14 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "l"(p)
+               : "memory");
+}
+// Whether rows of `ld` elements starting at p allow those accesses.
+template <typename T>
+__host__ __device__ __forceinline__ bool aligned8(const void* p, int64_t ld) {
+  return reinterpret_cast<uintptr_t>(p) % (8 * sizeof(T)) == 0 && ld % 8 == 0;
 }
 template <typename T>
 __device__ __forceinline__ void store8_tail(T* p, int n, const float (&v)[8]) {

@@ -8,11 +8,13 @@
 //     dr = rstd (g - rhat mean(g rhat)) + dres,   dw = sum over rows of dy rhat.
 //
 // Streams: every tensor is read once and written once, so HBM bounds them.  A thread keeps
-// eight consecutive values (times NV) of a row in registers between the row's sum and its
-// outputs; four lanes share a block of 32 of a microscaled output.  The grid is persistent:
-// a CTA walks rows, holding its columns of w, and in the backward its columns of the dw sum
-// (written once as one partial row a CTA, summed in a fixed order by a second kernel), in
-// registers.
+// eight values (times NV) of a row in registers between the row's sum and its outputs.
+// Where rows are aligned they are consecutive (one access of 16 or 32 bytes; four lanes
+// share a block of 32 of a microscaled output); other rows of plain outputs go by single
+// elements, consecutive across the lanes.  The grid is persistent: a CTA walks rows,
+// fetching the next while it finishes one, with its columns of w, and in the backward its
+// columns of the dw sum, in registers.  The dw sums leave as one partial row a walker, which
+// a second kernel adds in a fixed order.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -23,9 +25,9 @@ namespace {
 
 constexpr int kMaxThreads = 512;
 
-// Sum over the CTA; the result in every thread.  `red` holds one float a warp, twice, so
-// that consecutive calls alternate and one barrier a call is enough.
-__device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
+// Sum over a row's threads (blockDim.x); the result in every thread.  `red` holds one float
+// a warp, twice, so that consecutive calls alternate and one barrier a call is enough.
+__device__ __forceinline__ float row_sum(float v, float* red, int& flip) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int nw = blockDim.x >> 5;
@@ -39,105 +41,201 @@ __device__ __forceinline__ float cta_sum(float v, float* red, int& flip) {
   return t;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void ld(const T* row, int c, int d, float (&v)[8]) {
-  if (VEC && c + 8 <= d) {
-    mx::load8(row + c, v);
-  } else {
-    mx::load8_tail(row + c, d - c, v);
+// How a thread's values lie in a row: eight consecutive ones in one access, eight
+// consecutive ones one by one, or eight that are blockDim.x apart.
+enum Access { kVec, kTail, kStrided };
+
+// Eight values of a row as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float f[8];
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 u;
+};
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = r.f[j];
+}
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t u[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(u[j] << 16);
+    v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
   }
 }
-template <typename T, bool VEC>
-__device__ __forceinline__ void st(T* row, int c, int d, const float (&v)[8]) {
-  if (VEC && c + 8 <= d) {
-    mx::store8(row + c, v);
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<float>& r) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.f[j] = v[j];
+}
+__device__ __forceinline__ void pack(const float (&v)[8], Raw<__nv_bfloat16>& r) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)  // the values are bf16: nothing is rounded
+    u[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xffff0000u);
+  r.u = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void load_vec(const float* p, Raw<float>& r) { mx::load8(p, r.f); }
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Raw<__nv_bfloat16>& r) {
+  r.u = *reinterpret_cast<const uint4*>(p);
+}
+
+// Group k of the thread's values of a row (zeros past its end), and back.
+template <int ACC, typename T>
+__device__ __forceinline__ void load_row(const T* row, int k, int d, Raw<T>& r) {
+  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x);
+  float v[8];
+  if constexpr (ACC == kVec) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    pack(v, r);
+    if (c < d) load_vec(row + c, r);  // d is a multiple of 8
   } else {
-    mx::store8_tail(row + c, d - c, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = ACC == kTail ? c + j : (int)threadIdx.x + (8 * k + j) * (int)blockDim.x;
+      v[j] = i < d ? to_f32(row[i]) : 0.f;
+    }
+    pack(v, r);
   }
 }
-// One eight-value group; loads past the row's end give zeros.
+template <int ACC, typename T>
+__device__ __forceinline__ void store_row(T* row, int k, int d, const float (&v)[8]) {
+  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x);
+  if constexpr (ACC == kVec) {
+    if (c < d) mx::store8(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = ACC == kTail ? c + j : (int)threadIdx.x + (8 * k + j) * (int)blockDim.x;
+      if (i < d) row[i] = from_f32<T>(v[j]);
+    }
+  }
+}
+// Whether a thread holds the next row's values while it finishes one: up to 16 values a
+// tensor; more would spill.
+constexpr bool ahead(int nv) { return nv <= 2; }
 template <typename T>
 __device__ __forceinline__ float round_to(float v) { return to_f32(from_f32<T>(v)); }
 
 // FMT: -1 y in x's type, else the microscaled format.
-template <typename T, typename R, bool RES, int FMT, int NV, bool VEC>
+template <typename T, typename R, bool RES, int FMT, int NV, int ACC>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
   __shared__ float red[32];
-  const int d = (int)a.d, T8 = 8 * blockDim.x, c0 = 8 * threadIdx.x;
+  const int d = (int)a.d;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   int flip = 0;
   float w[NV][8];
+  Raw<T> xr[NV];
+  Raw<R> rr[RES ? NV : 1];
+  auto fetch = [&](int64_t i) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) mx::load8_tail(a.w + c0 + k * T8, d - c0 - k * T8, w[k]);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + row * a.d;
-    float v[NV][8];
-    float ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) ld<T, VEC>(x, c0 + k * T8, d, v[k]);
+    for (int k = 0; k < NV; ++k) load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, xr[k]);
     if (RES) {
-      const R* res = static_cast<const R*>(a.res) + row * a.d;
-      R* out = static_cast<R*>(a.res_out) + row * a.d;
-      float q[NV][8];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) ld<R, VEC>(res, c0 + k * T8, d, q[k]);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = round_to<R>(v[k][j] + q[k][j]);
-        st<R, VEC>(out, c0 + k * T8, d, v[k]);
-      }
+      for (int k = 0; k < NV; ++k)
+        load_row<ACC>(static_cast<const R*>(a.res) + i * d, k, d, rr[RES ? k : 0]);
     }
+  };
+  if (ahead(NV) && row < a.rows) fetch(row);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+  for (int k = 0; k < NV; ++k) {
+    Raw<float> t;
+    load_row<ACC == kVec ? kTail : ACC>(a.w, k, d, t);
+    unpack(t, w[k]);
+  }
+  for (; row < a.rows; row += step) {
+    float v[NV][8], ss = 0.f;
+    if (!ahead(NV)) fetch(row);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      unpack(xr[k], v[k]);
+      if (RES) {
+        float q[8];
+        unpack(rr[RES ? k : 0], q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = round_to<R>(v[k][j] + q[j]);
+        store_row<ACC>(static_cast<R*>(a.res_out) + row * d, k, d, v[k]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
-    const float rstd = 1.f / sqrtf(cta_sum(ss, red, flip) / (float)d + a.eps);
+    }
+    if (ahead(NV) && row + step < a.rows) fetch(row + step);
+    const float rstd = 1.f / sqrtf(row_sum(ss, red, flip) / (float)d + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rstd * w[k][j];
       if (FMT < 0) {
-        st<T, VEC>(static_cast<T*>(a.y) + row * a.d, c0 + k * T8, d, v[k]);
+        store_row<ACC>(static_cast<T*>(a.y) + row * d, k, d, v[k]);
       } else {
         // columns past d (zero) fill the row's padding; past the padding nothing is stored
-        mx::quant_store8<FMT>(v[k], row, (c0 + k * T8) / 8, a.Kp, a.codes, a.scales,
-                              c0 + k * T8 < a.Kp, 0xffffffffu);
+        const uint32_t c8 = threadIdx.x + k * blockDim.x, nkb = (uint32_t)(a.Kp >> 7);
+        uint2 codes;
+        const uint32_t word = mx::quant8<FMT>(v[k], codes);
+        if (c8 < 16 * nkb) {
+          mx::store_codes<FMT>(a.codes, row * nkb + (c8 >> 4), c8 & 15, codes);
+          if ((c8 & 15) == 0)
+            *reinterpret_cast<uint32_t*>(a.scales + mx::scale_word(row, c8 >> 4, nkb)) = word;
+        }
       }
     }
   }
   if (FMT >= 0) {  // scale bytes of the last tile's missing rows
-    const int64_t pad = mx::pad128(a.rows), nkb = a.Kp >> 7;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (pad - a.rows) * nkb;
-         i += (int64_t)gridDim.x * blockDim.x)
+    const int64_t pad = mx::pad128(a.rows), nkb = a.Kp >> 7, per = blockDim.x * blockDim.y;
+    for (int64_t i = blockIdx.x * per + threadIdx.y * blockDim.x + threadIdx.x;
+         i < (pad - a.rows) * nkb; i += gridDim.x * per)
       *reinterpret_cast<uint32_t*>(a.scales + mx::scale_word(a.rows + i / nkb, i % nkb, nkb)) = 0;
   }
 }
 
-template <typename T, typename R, bool DRES, int NV, bool VEC>
+template <typename T, typename R, bool DRES, int NV, int ACC>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[32];
-  const int d = (int)a.d, T8 = 8 * blockDim.x, c0 = 8 * threadIdx.x;
+  const int d = (int)a.d;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   int flip = 0;
   float w[NV][8], dw[NV][8];
+  Raw<T> yr[NV];
+  Raw<R> rr[NV];
+  Raw<float> ur[DRES ? NV : 1];
+  float rs = 0.f;
+  auto fetch = [&](int64_t i) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, yr[k]);
+      load_row<ACC>(static_cast<const R*>(a.r) + i * d, k, d, rr[k]);
+      if (DRES) load_row<ACC>(a.dres + i * d, k, d, ur[DRES ? k : 0]);
+    }
+    rs = a.rstd[i];
+  };
+  if (ahead(NV) && first < a.rows) fetch(first);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    mx::load8_tail(a.w + c0 + k * T8, d - c0 - k * T8, w[k]);
+    Raw<float> t;
+    load_row<ACC == kVec ? kTail : ACC>(a.w, k, d, t);
+    unpack(t, w[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
   }
   const float inv_d = 1.f / (float)d;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float g[NV][8], rh[NV][8];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      ld<T, VEC>(static_cast<const T*>(a.dy) + row * a.d, c0 + k * T8, d, g[k]);
-      ld<R, VEC>(static_cast<const R*>(a.r) + row * a.d, c0 + k * T8, d, rh[k]);
-    }
-    const float rstd = a.rstd[row];
+  for (int64_t row = first; row < a.rows; row += step) {
+    float g[NV][8], rh[NV][8], o[NV][8];
+    if (!ahead(NV)) fetch(row);
+    const float rstd = rs;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+      unpack(yr[k], g[k]);
+      unpack(rr[k], rh[k]);
+      if (DRES) unpack(ur[DRES ? k : 0], o[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         rh[k][j] *= rstd;
@@ -145,80 +243,86 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
         g[k][j] *= w[k][j];
         s = fmaf(g[k][j], rh[k][j], s);
       }
-    const float m = cta_sum(s, red, flip) * inv_d;
+    }
+    if (ahead(NV) && row + step < a.rows) fetch(row + step);
+    const float m = row_sum(s, red, flip) * inv_d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float o[8];
-      if (DRES) ld<float, VEC>(a.dres + row * a.d, c0 + k * T8, d, o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float t = rstd * (g[k][j] - rh[k][j] * m);
-        o[j] = DRES ? o[j] + t : t;
+        o[k][j] = DRES ? o[k][j] + t : t;
       }
-      st<float, VEC>(a.dr + row * a.d, c0 + k * T8, d, o);
+      store_row<ACC>(a.dr + row * d, k, d, o[k]);
     }
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    mx::store8_tail(a.part + (int64_t)blockIdx.x * a.d + c0 + k * T8, d - c0 - k * T8, dw[k]);
+    store_row<ACC == kVec ? kTail : ACC>(a.part + first * d, k, d, dw[k]);
 }
 
-// dw = sum of the partial rows, in a fixed order: 32 columns a CTA, eight warps taking the
-// partial rows in turn, then the eight sums.
+// dw = sum of the partial rows, in a fixed order: a CTA takes eight columns, thread (c, p)
+// every 32nd partial row of column c, then the 32 sums.
 __global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int nparts,
                                                       int64_t d, float* __restrict__ dw) {
-  __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  __shared__ float red[32][8];
+  const int c8 = threadIdx.x & 7, p0 = threadIdx.x >> 3;
+  const int64_t c = (int64_t)blockIdx.x * 8 + c8;
   float s = 0.f;
-  if (c < d)
-    for (int p = warp; p < nparts; p += 8) s += part[(int64_t)p * d + c];
-  red[warp][lane] = s;
+  if (c < d) {
+#pragma unroll 8
+    for (int p = p0; p < nparts; p += 32) s += part[(int64_t)p * d + c];
+  }
+  red[p0][c8] = s;
   __syncthreads();
-  if (warp == 0 && c < d) {
+  if (threadIdx.x < 8 && c < d) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += red[i][lane];
+    for (int i = 0; i < 32; ++i) t += red[i][threadIdx.x];
     dw[c] = t;
   }
 }
 
-// Threads of a CTA and eight-value groups a thread for rows of `width` values.
+// Threads of a row, rows of a CTA and eight-value groups of a thread for rows of `width`.
 struct Shape {
-  int threads, nv;
+  int threads, rows, nv;
 };
 Shape shape_of(int64_t width) {
   int64_t t = ((width + 7) / 8 + 31) / 32 * 32;
   if (t > kMaxThreads) t = kMaxThreads;
   const int64_t nv = (width + 8 * t - 1) / (8 * t);
-  return {(int)t, nv <= 1 ? 1 : nv <= 2 ? 2 : 4};
+  // a row of one warp needs no barrier: four of them make a CTA
+  return {(int)t, t == 32 ? 4 : 1, nv <= 1 ? 1 : nv <= 2 ? 2 : 4};
 }
 
-unsigned grid_of(int64_t rows, int threads) {
+// CTAs: up to 1024 threads an SM (the registers allow that and the fetch ahead keeps enough
+// bytes in flight), but `least` rows each.
+unsigned grid_of(int64_t rows, const Shape& h, int least) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
-  const int64_t most = sms * (2048 / threads < 16 ? 2048 / threads : 16) / 2;
-  return (unsigned)(rows < most ? rows : most);
+  const int64_t most = sms * (1024 / (h.threads * h.rows)), per = (int64_t)h.rows * least;
+  const int64_t want = (rows + per - 1) / per;
+  return (unsigned)(want < most ? want : most);
 }
-
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename T, typename R, bool RES, int FMT, int NV>
-cudaError_t fwd_nv(const NormArgs& a, int threads, bool vec, cudaStream_t s) {
-  const unsigned grid = grid_of(a.rows, threads);
+cudaError_t fwd_nv(const NormArgs& a, const Shape& h, bool vec, cudaStream_t s) {
+  const dim3 block(h.threads, h.rows);
+  const unsigned grid = grid_of(a.rows, h, 1);
   if (vec)
-    add_rmsnorm_kernel<T, R, RES, FMT, NV, true><<<grid, threads, 0, s>>>(a);
-  else
-    add_rmsnorm_kernel<T, R, RES, FMT, NV, false><<<grid, threads, 0, s>>>(a);
+    add_rmsnorm_kernel<T, R, RES, FMT, NV, kVec><<<grid, block, 0, s>>>(a);
+  else  // a microscaled output needs its blocks' values together
+    add_rmsnorm_kernel<T, R, RES, FMT, NV, FMT < 0 ? kStrided : kTail><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, typename R, bool RES, int FMT>
 cudaError_t fwd_fmt(const NormArgs& a, cudaStream_t s) {
   const Shape h = shape_of(FMT < 0 ? a.d : a.Kp);
-  const bool vec = a.d % 8 == 0 && al16(a.x) && (!RES || (al16(a.res) && al16(a.res_out))) &&
-                   (FMT >= 0 || al16(a.y));
-  return h.nv == 1   ? fwd_nv<T, R, RES, FMT, 1>(a, h.threads, vec, s)
-         : h.nv == 2 ? fwd_nv<T, R, RES, FMT, 2>(a, h.threads, vec, s)
-                     : fwd_nv<T, R, RES, FMT, 4>(a, h.threads, vec, s);
+  const bool vec = mx::aligned8<T>(a.x, a.d) &&
+                   (!RES || (mx::aligned8<R>(a.res, a.d) && mx::aligned8<R>(a.res_out, a.d))) &&
+                   (FMT >= 0 || mx::aligned8<T>(a.y, a.d));
+  return h.nv == 1   ? fwd_nv<T, R, RES, FMT, 1>(a, h, vec, s)
+         : h.nv == 2 ? fwd_nv<T, R, RES, FMT, 2>(a, h, vec, s)
+                     : fwd_nv<T, R, RES, FMT, 4>(a, h, vec, s);
 }
 template <typename T, typename R, bool RES>
 cudaError_t fwd_res(const NormArgs& a, cudaStream_t s) {
@@ -232,26 +336,36 @@ cudaError_t fwd_t(const NormArgs& a, cudaStream_t s) {
   return a.res_bf16 ? fwd_res<T, __nv_bfloat16, true>(a, s) : fwd_res<T, float, true>(a, s);
 }
 
+// The backward's CTAs take at least four rows each: every walker costs a partial row.
+constexpr int kLeastRows = 4;
+
 template <typename T, typename R, bool DRES, int NV>
-cudaError_t bwd_nv(const NormBwdArgs& a, int threads, unsigned grid, bool vec, cudaStream_t s) {
+cudaError_t bwd_nv(const NormBwdArgs& a, const Shape& h, bool vec, cudaStream_t s) {
+  const dim3 block(h.threads, h.rows);
+  const unsigned grid = grid_of(a.rows, h, kLeastRows);
   if (vec)
-    add_rmsnorm_bwd_kernel<T, R, DRES, NV, true><<<grid, threads, 0, s>>>(a);
+    add_rmsnorm_bwd_kernel<T, R, DRES, NV, kVec><<<grid, block, 0, s>>>(a);
   else
-    add_rmsnorm_bwd_kernel<T, R, DRES, NV, false><<<grid, threads, 0, s>>>(a);
+    add_rmsnorm_bwd_kernel<T, R, DRES, NV, kStrided><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, typename R>
 cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t s) {
   const Shape h = shape_of(a.d);
-  const unsigned grid = grid_of(a.rows, h.threads);
-  const bool vec = a.d % 8 == 0 && al16(a.dy) && al16(a.r) && al16(a.dr) && al16(a.dres);
+  const bool vec = mx::aligned8<T>(a.dy, a.d) && mx::aligned8<R>(a.r, a.d) &&
+                   mx::aligned8<float>(a.dr, a.d) && mx::aligned8<float>(a.dres, a.d);
   if (a.dres)
-    return h.nv == 1   ? bwd_nv<T, R, true, 1>(a, h.threads, grid, vec, s)
-           : h.nv == 2 ? bwd_nv<T, R, true, 2>(a, h.threads, grid, vec, s)
-                       : bwd_nv<T, R, true, 4>(a, h.threads, grid, vec, s);
-  return h.nv == 1   ? bwd_nv<T, R, false, 1>(a, h.threads, grid, vec, s)
-         : h.nv == 2 ? bwd_nv<T, R, false, 2>(a, h.threads, grid, vec, s)
-                     : bwd_nv<T, R, false, 4>(a, h.threads, grid, vec, s);
+    return h.nv == 1   ? bwd_nv<T, R, true, 1>(a, h, vec, s)
+           : h.nv == 2 ? bwd_nv<T, R, true, 2>(a, h, vec, s)
+                       : bwd_nv<T, R, true, 4>(a, h, vec, s);
+  return h.nv == 1   ? bwd_nv<T, R, false, 1>(a, h, vec, s)
+         : h.nv == 2 ? bwd_nv<T, R, false, 2>(a, h, vec, s)
+                     : bwd_nv<T, R, false, 4>(a, h, vec, s);
+}
+
+int64_t partial_rows(int64_t rows, int64_t d) {
+  const Shape h = shape_of(d);
+  return (int64_t)grid_of(rows, h, kLeastRows) * h.rows;
 }
 
 }  // namespace
@@ -264,8 +378,7 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
 }
 
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t d) {
-  if (rows == 0) return 0;
-  return (size_t)grid_of(rows, shape_of(d).threads) * (size_t)d * sizeof(float);
+  return rows == 0 ? 0 : (size_t)partial_rows(rows, d) * (size_t)d * sizeof(float);
 }
 
 cudaError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t s) {
@@ -275,8 +388,8 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t s) {
                          : (a.res_bf16 ? bwd_t<float, __nv_bfloat16>(a, s)
                                        : bwd_t<float, float>(a, s));
   if (e != cudaSuccess) return e;
-  norm_dw_kernel<<<(unsigned)((a.d + 31) / 32), 256, 0, s>>>(
-      a.part, (int)grid_of(a.rows, shape_of(a.d).threads), a.d, a.dw);
+  norm_dw_kernel<<<(unsigned)((a.d + 7) / 8), 256, 0, s>>>(a.part, (int)partial_rows(a.rows, a.d),
+                                                          a.d, a.dw);
   return cudaGetLastError();
 }
 

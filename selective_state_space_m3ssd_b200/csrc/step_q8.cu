@@ -97,20 +97,27 @@ struct RowCoef {
 
 // N = 128, P = 64: W warps share a (b, h); a lane owns 16 columns (lane % 4) of the rows
 // lane / 4 + 8 k, sixteen codes a load, so a warp's load is 512 contiguous bytes and every
-// row is complete in four lanes.  W = 1 has the fewest instructions a value (the sums of
-// y end in one warp); W = 4 is for launches that would leave SMs without a warp.
+// row is complete in four lanes.
 template <typename T, int W>
-__global__ void __launch_bounds__(128) step_q8_n128p64(StepQ8Args a) {
+__global__ void __launch_bounds__(128, 4) step_q8_n128p64(StepQ8Args a) {
   constexpr int kGroups = 4 / W;       // (b, h) a CTA
   constexpr int kK = 16 / W;           // rows a lane
   __shared__ RowCoef coef[kGroups][kN];
-  __shared__ float ysum[W == 1 ? 1 : W][kP];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = W == 1 ? warp : 0, t = W == 1 ? lane : (int)threadIdx.x;
+  __shared__ float ysum[kGroups][W == 1 ? 1 : W][kP];
+  const int lane = threadIdx.x & 31, grp = threadIdx.x / (32 * W), t = threadIdx.x % (32 * W);
+  const int warp = t >> 5;  // within the group
   const int64_t bh = (int64_t)blockIdx.x * kGroups + grp;
-  if (W == 1 && bh >= a.b * a.H) return;
+  if (kGroups > 1 && bh >= a.b * a.H) return;
+  auto sync = [&]() {
+    if (W == 1)
+      __syncwarp();
+    else if (W == 4)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(32 * W) : "memory");
+  };
   const int64_t b = bh / a.H, h = bh % a.H, rep = a.H / a.G, g = h / rep;
-  const int q = lane & 3, r0 = (W == 1 ? 0 : warp * (kN / W)) + (lane >> 2);
+  const int q = lane & 3, r0 = warp * (kN / W) + (lane >> 2);
 
   const uint4* S = reinterpret_cast<const uint4*>(a.ssm + bh * kN * kP);
   uint4 hv[kK];
@@ -152,9 +159,9 @@ __global__ void __launch_bounds__(128) step_q8_n128p64(StepQ8Args a) {
     coef[grp][2 * i + 1].as = alpha * sc.y;
   };
   float ph = 0.f;  // W = 4: phi' of pair t % 64
-  if (W == 1) {
+  if (W <= 2) {
 #pragma unroll
-    for (int i = lane; i < kN / 2; i += 32) {
+    for (int i = t; i < kN / 2; i += 32 * W) {
       const float ang = a.angle[bh * 64 + i];
       const float p = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * 64 + i] : 0.f));
       turned_new(i, p);
@@ -171,10 +178,7 @@ __global__ void __launch_bounds__(128) step_q8_n128p64(StepQ8Args a) {
       turned_old(i, ang);
     }
   }
-  if (W == 1)
-    __syncwarp();
-  else
-    __syncthreads();
+  sync();
 
   uint64_t x2[8], xp2[8], acc[8];
 #pragma unroll
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(128) step_q8_n128p64(StepQ8Args a) {
       v[j] = fma2(bc, x2[j], fma2(bp, xp2[j], mul2(as, pack2(c.x, c.y))));
       acc[j] = fma2(cc, v[j], acc[j]);
       const float2 u = unpack2(v[j]);
-      amax = max_nan(max_nan(amax, fabsf(u.x)), fabsf(u.y));
+      amax = mx::max3_abs(amax, u.x, u.y);
     }
     amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -236,15 +240,15 @@ __global__ void __launch_bounds__(128) step_q8_n128p64(StepQ8Args a) {
     col += up ? w : 0;
   }
   if (W > 1) {
-    ysum[warp][col] = y8[0];
-    ysum[warp][col + 1] = y8[1];
-    __syncthreads();
-    if (threadIdx.x >= 64) return;
-    a.angle_out[bh * 64 + t] = ph;  // every read of the old angles came before the barriers
-    col = threadIdx.x;
+    ysum[grp][warp][col] = y8[0];
+    ysum[grp][warp][col + 1] = y8[1];
+    sync();
+    if (t >= 64) return;
+    if (W == 4) a.angle_out[bh * 64 + t] = ph;  // every old angle was read before the barriers
+    col = t;
     float y = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) y += ysum[w][col];
+    for (int w = 0; w < W; ++w) y += ysum[grp][w][col];
     const float xv = to_f32(xt[col]);
     if (a.D) y = fmaf(a.D[h], xv, y);
     static_cast<T*>(a.y_t)[bh * kP + col] = from_f32<T>(y);
@@ -370,7 +374,7 @@ cudaError_t launch_step_t(StepQ8Args a, cudaStream_t s) {
     if (nbh <= 2 * (int64_t)sms)
       step_q8_n128p64<T, 4><<<(unsigned)nbh, 128, 0, s>>>(a);
     else
-      step_q8_n128p64<T, 1><<<(unsigned)((nbh + 3) / 4), 128, 0, s>>>(a);
+      step_q8_n128p64<T, 2><<<(unsigned)((nbh + 1) / 2), 128, 0, s>>>(a);
   } else {
     const size_t smem = sizeof(float) * (size_t)(3 * a.N + kGenWarps * a.P);
     step_q8_kernel<T><<<(unsigned)nbh, kGenThreads, smem, s>>>(a);
@@ -418,9 +422,7 @@ __global__ void __launch_bounds__(kStThreads) quant_state_kernel(StateArgs a) {
 #pragma unroll
     for (int u = 0; u < kStUnroll; ++u) {
       const int64_t r = base + u * stride + threadIdx.x / a.lanes;
-      float amax = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(v[u][j]));
+      float amax = mx::amax8(v[u]);
       for (int o = 1; o < a.lanes; o <<= 1)
         amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float s, inv;
@@ -493,8 +495,7 @@ cudaError_t launch_state(bool quant, int64_t rows, int64_t P, float* h, void* co
   if (rows == 0) return cudaSuccess;
   StateArgs a{rows, (int)P, 1, h, static_cast<uint8_t*>(codes), scale};
   while (8 * a.lanes < P) a.lanes *= 2;  // P <= 256: at most 32
-  const bool vec = P % 8 == 0 && reinterpret_cast<uintptr_t>(h) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(codes) % 8 == 0;
+  const bool vec = mx::aligned8<float>(h, P) && reinterpret_cast<uintptr_t>(codes) % 8 == 0;
   const int64_t per = (int64_t)(kStThreads / a.lanes) * kStUnroll;
   const int64_t want = (rows + per - 1) / per, sms = current_device_sms();
   const unsigned grid = (unsigned)(sms > 0 && want > sms * 8 ? sms * 8 : want);

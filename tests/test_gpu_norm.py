@@ -159,8 +159,12 @@ def test_unaligned_tensors_and_in_place():
     rbuf = torch.empty(rows * d + 1, device="cuda")
     ro = rbuf[1:].view(rows, d).copy_(r)
     y, out, rstd = m3.add_rmsnorm(xo, w.cuda(), residual=ro, residual_out=ro, y=xo, want_rstd=True)
-    assert y is xo and out is ro
-    assert torch.equal(y, want[0]) and torch.equal(out, want[1]) and torch.equal(rstd, want[2])
+    assert y is xo and out is ro and torch.equal(out, want[1])
+    # rows that are not aligned are summed in another order: both are within FP (and half a
+    # step of bf16) of the exact value, so within twice that of each other
+    assert np.all(np.abs(np64(rstd) - np64(want[2])) <= 2 * FP * np64(rstd))
+    assert np.all(np.abs(np64(y) - np64(want[0])) <= 2 * (FP + 2.0 ** -8) * np.abs(np64(y)))
+    rstd = want[2]
     up = torch.randn(rows, d, device="cuda")
     a = m3.add_rmsnorm_bwd(x.cuda(), want[1], w.cuda(), rstd, dres=up)
     b = m3.add_rmsnorm_bwd(x.cuda(), want[1], w.cuda(), rstd, dres=up, dr=up)
