@@ -7,13 +7,18 @@
 // kind::mxf4 (A in 4 bits) or kind::mxf8f6f4 (A in 8 bits; TMA spreads the packed 4-bit
 // codes of W over 8-bit containers as it loads them) multiplies value times scale.
 //
-// The operand with 128 rows a tile ("rows") is A, or W for few tokens (SWAP): then the
+// The operand with 128 H rows a tile ("rows") is A, or W for few tokens (SWAP): then the
 // tokens are the product's narrow side, no more of them than the tile is wide, and W's
 // rows fill the 128 lanes.  One persistent CTA per SM; warp 0 copies, warp 1 issues the
-// scale copies and the products, warps 2-5 are the epilogue on the other of the two
-// accumulators.  Every stage of the ring has its own TMEM columns for its scales: they are
-// free when the stage is (the products that read them have finished), so a copy never
-// overtakes a product.
+// scale copies and the products, four warps a half are the epilogue.  The accumulators
+// alternate where two fit beside the scales in TMEM; with one, the epilogue's first step,
+// the whole row into registers as bf16, is all the products wait for.  Every stage of the
+// ring has its own TMEM columns for its scales: they are free when the stage is (the products
+// that read them have finished), so a copy never overtakes a product.  A 192-column tile may
+// start in the middle of a scale tile: its products read the columns from there on.
+// Output blocks of 32 x 64 leave by TMA from a swizzled staging buffer (a thread holds a row:
+// stores straight from the registers touch 32 lines each), or, where the rows of D are not
+// multiples of 16 bytes, row by row from the same buffer.
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
@@ -21,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstring>
 
@@ -38,26 +44,31 @@ namespace {
 
 constexpr int BM = 128;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kTile = 512;  // bytes of a scale tile (128 rows x 4 blocks)
-constexpr uint32_t kStgBytes = 32 * 32 * 2;
-constexpr int kEpiWarps = 4, kThreads = 32 * (2 + kEpiWarps);
+constexpr uint32_t kTile = 512;           // bytes of a scale tile (128 rows x 4 blocks)
+constexpr uint32_t kStgBytes = 32 * 128;  // an output block: 32 rows x 64 bf16 columns
 
-// AF: A's format.  A stage is 128 bytes of K a row: 256 values in 4 bits, 128 in 8.
-template <int AF, int BN, bool SWAP>
+// AF: A's format.  H: 128-row halves of a tile.  A stage is 128 bytes of K a row: 256 values
+// in 4 bits, 128 in 8.
+template <int AF, int H, int BN, bool SWAP>
 struct Cfg {
-  static constexpr int ATOMS = AF == mx::kFp4 ? 2 : 1;       // scale tiles along K a stage
-  static constexpr int NSB = (BN + 127) / 128;               // scale tiles along the columns
-  static constexpr uint32_t R_BYTES = BM * 128, C_BYTES = BN * 128;
+  static constexpr int ATOMS = AF == mx::kFp4 ? 2 : 1;  // scale tiles along K a stage
+  static constexpr int NSB = (BN + 127) / 128;          // scale tiles along the columns
+  static constexpr int EPI_WARPS = 4 * H, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t R_BYTES = H * BM * 128, C_BYTES = BN * 128;
   // bytes the copies of a stage count on its barrier: W's 4-bit codes count as they are in
   // global memory, whether or not they are spread
   static constexpr uint32_t R_TX = (AF != mx::kFp4 && SWAP) ? R_BYTES / 2 : R_BYTES;
   static constexpr uint32_t C_TX = (AF != mx::kFp4 && !SWAP) ? C_BYTES / 2 : C_BYTES;
-  static constexpr uint32_t SR_BYTES = ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
+  static constexpr uint32_t SR_BYTES = H * ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
   static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
-  static constexpr int STAGES = (208 * 1024) / STAGE < 8 ? (208 * 1024) / STAGE : 8;
-  static constexpr int SF_COLS = ATOMS * 4 * (1 + NSB);      // TMEM columns of a stage's scales
-  static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
-  static constexpr int COLS = 2 * ACC_COLS + STAGES * SF_COLS;
+  static constexpr int NSTG = SWAP ? 0 : (H == 1 ? 2 : 1);  // output blocks of an epilogue warp
+  static constexpr int ROOM = 226 * 1024 - EPI_WARPS * NSTG * (int)kStgBytes - 1024;
+  static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
+  static constexpr int SF_COLS = ATOMS * 4 * (H + NSB);     // TMEM columns of a stage's scales
+  static constexpr int ACC_COLS = H * (BN < 32 ? 32 : BN);  // an accumulator, its halves side by side
+  // two accumulators, where they fit, alternate between the products and the epilogue
+  static constexpr int NACC = 2 * ACC_COLS + STAGES * SF_COLS <= 512 ? 2 : 1;
+  static constexpr int COLS = NACC * ACC_COLS + STAGES * SF_COLS;
   static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
   // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
@@ -68,11 +79,12 @@ struct Cfg {
 
 template <typename C>
 struct Smem {
+  // every buffer a TMA copy reads or writes starts on a 1024-byte boundary
   uint8_t r[C::STAGES][C::R_BYTES];
   uint8_t c[C::STAGES][C::C_BYTES];
+  uint8_t stg[C::NSTG ? C::EPI_WARPS * C::NSTG : 1][C::NSTG ? kStgBytes : 1024];
   uint8_t sr[C::STAGES][C::SR_BYTES];
   uint8_t sc[C::STAGES][C::SC_BYTES];
-  uint8_t stg[kEpiWarps][2][kStgBytes];
   uint64_t full[C::STAGES];
   uint64_t empty[C::STAGES];
   uint64_t tfull[2];
@@ -83,8 +95,8 @@ struct Smem {
 };
 
 struct MMaps {
-  CUtensorMap r, c;  // codes of the rows and the columns operand, box 128 bytes x 128 / BN rows
-  CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 32 x 32 (stores; when vec)
+  CUtensorMap r, c;  // codes of the rows and the columns operand, box 128 bytes x 128 H / BN rows
+  CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 64 x 32, 128-byte swizzle (when vec)
 };
 
 struct MArgs {
@@ -95,14 +107,19 @@ struct MArgs {
   const uint8_t* cs;
   int mt, nt;         // tiles along the rows and the columns operand
   int nkb;            // 128-column groups of K
-  int crb;            // 128-row blocks of the columns operand
+  int rrb, crb;       // 128-row blocks of the rows and the columns operand
   bool vec;
 };
 
-template <int AF, int BN, bool SWAP>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+template <int AF, int H, int BN, bool SWAP>
+__global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
     gemm_mx_kernel(MArgs g, const __grid_constant__ MMaps tm) {
-  using C = Cfg<AF, BN, SWAP>;
+  using C = Cfg<AF, H, BN, SWAP>;
   constexpr int STAGES = C::STAGES, ATOMS = C::ATOMS, NSB = C::NSB;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw_addr = tc5::saddr(smem_raw);
@@ -117,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc5::mbar_init(&sm.tfull[i], 1);
-      tc5::mbar_init(&sm.tempty[i], kEpiWarps);
+      tc5::mbar_init(&sm.tempty[i], C::EPI_WARPS);
     }
     tc5::mbar_init(&sm.drain, 1);
     tc5::fence_mbar_init();
@@ -127,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  const uint32_t tmem = sm.tmem, sf0 = tmem + 2 * C::ACC_COLS;
+  const uint32_t tmem = sm.tmem, sf0 = tmem + C::NACC * C::ACC_COLS;
 
   if (warp == 0) {
     // ---- producer
@@ -143,14 +160,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           const int a0 = kb * ATOMS, na = min(ATOMS, g.nkb - a0);
-          const int nsb = min(NSB, g.crb - rb0);
+          const int nsb = min(NSB, g.crb - rb0), nsr = min(H, g.rrb - mb * H);
           uint64_t* const full = &sm.full[stage];
           tc5::mbar_arrive_expect_tx(
-              full, C::R_TX + C::C_TX + (uint32_t)((1 + nsb) * na) * kTile);
-          tc5::tma_load_2d(tc5::saddr(sm.r[stage]), &tm.r, full, kb * 128, mb * BM);
+              full, C::R_TX + C::C_TX + (uint32_t)((nsr + nsb) * na) * kTile);
+          tc5::tma_load_2d(tc5::saddr(sm.r[stage]), &tm.r, full, kb * 128, mb * (H * BM));
           tc5::tma_load_2d(tc5::saddr(sm.c[stage]), &tm.c, full, kb * 128, nb * BN);
-          tc5::bulk_load(tc5::saddr(sm.sr[stage]), g.rs + ((int64_t)mb * g.nkb + a0) * kTile,
-                         na * kTile, full);
+          for (int j = 0; j < nsr; ++j)
+            tc5::bulk_load(tc5::saddr(sm.sr[stage]) + j * ATOMS * kTile,
+                           g.rs + ((int64_t)(mb * H + j) * g.nkb + a0) * kTile, na * kTile, full);
           for (int j = 0; j < nsb; ++j)
             tc5::bulk_load(tc5::saddr(sm.sc[stage]) + j * ATOMS * kTile,
                            g.cs + ((int64_t)(rb0 + j) * g.nkb + a0) * kTile, na * kTile, full);
@@ -188,30 +206,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc5::fence_after_sync();
           const int na = min(ATOMS, g.nkb - kb * ATOMS);
-          // columns: rows operand's tiles, then for each tile along K the columns operand's
-          const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * 4;
+          // the stage's columns: for each tile along K the halves' tiles, then the columns'
+          const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * H * 4;
 #pragma unroll
           for (int a = 0; a < ATOMS; ++a) {
             if (a < na) {
-              tc5::cp_scales(sfr + 4 * a, tc5::desc_scales(tc5::saddr(sm.sr[stage]) + a * kTile));
+#pragma unroll
+              for (int j = 0; j < H; ++j)
+                tc5::cp_scales(sfr + 4 * (a * H + j),
+                               tc5::desc_scales(tc5::saddr(sm.sr[stage]) + (j * ATOMS + a) * kTile));
 #pragma unroll
               for (int j = 0; j < NSB; ++j)
                 tc5::cp_scales(sfc + 4 * (a * NSB + j),
                                tc5::desc_scales(tc5::saddr(sm.sc[stage]) + (j * ATOMS + a) * kTile));
             }
           }
-          const uint64_t dr = tc5::desc_sw128(tc5::saddr(sm.r[stage]), 16, 1024);
           const uint64_t dc = tc5::desc_sw128(tc5::saddr(sm.c[stage]), 16, 1024);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
-            if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
-              if (k / 2 < na)
-                tc5::mma_mxf4(d, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                              tc5::idesc_mx_sf(C::IDESC, 2 * (k & 1)), sfr + 4 * (k / 2),
-                              sfc + 4 * NSB * (k / 2) + shift, kb > 0 || k > 0);
-            } else {  // 32 values, one block
-              tc5::mma_mxf8f6f4(d, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                                tc5::idesc_mx_sf(C::IDESC, k), sfr, sfc + shift, kb > 0 || k > 0);
+          for (int hh = 0; hh < H; ++hh) {
+            const uint64_t dr = tc5::desc_sw128(tc5::saddr(sm.r[stage]) + hh * BM * 128, 16, 1024);
+            const uint32_t dh = d + (uint32_t)(hh * BN);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
+              if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
+                if (k / 2 < na)
+                  tc5::mma_mxf4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
+                                tc5::idesc_mx_sf(C::IDESC, 2 * (k & 1)),
+                                sfr + 4 * (k / 2 * H + hh), sfc + 4 * NSB * (k / 2) + shift,
+                                kb > 0 || k > 0);
+              } else {  // 32 values, one block
+                tc5::mma_mxf8f6f4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
+                                  tc5::idesc_mx_sf(C::IDESC, k), sfr + 4 * hh, sfc + shift,
+                                  kb > 0 || k > 0);
+              }
             }
           }
           tc5::commit(&sm.empty[stage]);
@@ -222,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         tc5::commit(&sm.tfull[acc]);
-        if (++acc == 2) {
+        if (++acc == C::NACC) {
           acc = 0;
           aphase ^= 1u;
         }
@@ -232,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       (void)tc5::mbar_wait(&sm.drain, 0, kWaitLimitNs);
     }
   } else {
-    // ---- epilogue: TMEM lane quarter q, one row of the rows operand a thread
-    const int q = warp & 3, ew = warp - 2;
+    // ---- epilogue: TMEM lane quarter q of half hh, one row of the rows operand a thread
+    const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
     int acc = 0;
     uint32_t nst = 0, aphase = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
@@ -243,8 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc5::fence_after_sync();
       const int mb = t / g.nt, nb = t % g.nt;
-      const int row0 = mb * BM + 32 * q, row = row0 + lane, col0 = nb * BN;
-      const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS);
+      const int row0 = (mb * H + hh) * BM + 32 * q, row = row0 + lane, col0 = nb * BN;
+      const uint32_t tbase =
+          tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS + hh * BN);
       if constexpr (SWAP) {
         // a row is a column of D: 32 lanes store 32 consecutive values
 #pragma unroll
@@ -264,26 +292,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc5::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
-      } else if (g.vec) {
+      } else {
         // the row into registers as bf16, then TMEM goes back: the stores below drain
-        // while the next tile's products run
-        const int nch = min(BN / 32, (g.N - col0 + 31) / 32);
-        uint32_t pk[BN / 32][16];
+        // while the next products run
+        const int nch = min(BN / 64, (g.N - col0 + 63) / 64);
+        uint32_t pk[BN / 64][32];
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < BN / 64; ++c) {
           if (c < nch) {
+            uint32_t v0[32], v1[32];
+            tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c), v0);
+            tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c + 32), v1);
+            tc5::wait_ld();
+            tc5::reg_after_ld(v0);
+            tc5::reg_after_ld(v1);
 #pragma unroll
-            for (int hc = 0; hc < 2; ++hc) {
-              uint32_t v[16];
-              tc5::ld_32x32b_x16(tbase + (uint32_t)(32 * c + 16 * hc), v);
-              tc5::wait_ld();
-              tc5::reg_after_ld(v);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]),
-                                                         __uint_as_float(v[2 * j + 1]));
-                pk[c][8 * hc + j] = *reinterpret_cast<uint32_t*>(&h);
-              }
+            for (int j = 0; j < 16; ++j) {
+              pk[c][j] = pack2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
+              pk[c][16 + j] = pack2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
             }
           }
         }
@@ -291,45 +317,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < BN / 64; ++c) {
           if (c < nch) {
-            uint8_t* const blk = sm.stg[ew][nst & 1];
-            if (lane == 0) tc5::bulk_wait_group_read<1>();  // the block's previous store has read it
+            uint8_t* const blk = sm.stg[ew * C::NSTG + (int)(nst % C::NSTG)];
+            // the block's previous store has read it
+            if (g.vec && lane == 0) tc5::bulk_wait_group_read<C::NSTG ? C::NSTG - 1 : 0>();
             __syncwarp();
-            uint4* dst = reinterpret_cast<uint4*>(blk + lane * 64);
+            uint4* const dst = reinterpret_cast<uint4*>(blk + lane * 128);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[j] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
-            tc5::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 32 * c, row0);
-              tc5::bulk_commit_group();
+            for (int j = 0; j < 8; ++j)  // the 128-byte swizzle: unit j of row r at j ^ (r % 8)
+              dst[j ^ (lane & 7)] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2],
+                                               pk[c][4 * j + 3]);
+            if (g.vec) {
+              tc5::fence_proxy_async();
+              __syncwarp();
+              if (lane == 0) {
+                tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 64 * c, row0);
+                tc5::bulk_commit_group();
+              }
+            } else {  // row by row, consecutive lanes on consecutive columns
+              __syncwarp();
+              const int c0 = col0 + 64 * c + lane, rows = min(32, g.M - row0);
+              for (int r = 0; r < rows; ++r) {
+                const uint8_t* const src = blk + r * 128;
+                __nv_bfloat16* const out = g.D + (int64_t)(row0 + r) * g.ldd + c0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int b = 2 * lane + 64 * i;  // byte of the row
+                  if (c0 + 32 * i < g.N)
+                    out[32 * i] = *reinterpret_cast<const __nv_bfloat16*>(
+                        src + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
+                }
+              }
             }
             ++nst;
           }
         }
-      } else {
-        const int nch = min(BN / 32, (g.N - col0 + 31) / 32);
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-          const int col = col0 + 32 * c;
-          uint32_t v[32];
-          tc5::ld_32x32b_x32(tbase + (uint32_t)(32 * c), v);
-          tc5::wait_ld();
-          tc5::reg_after_ld(v);
-          if (row < g.M) {
-            __nv_bfloat16* const drow = g.D + (int64_t)row * g.ldd;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col + j < g.N) drow[col + j] = __float2bfloat16_rn(__uint_as_float(v[j]));
-          }
-        }
-        tc5::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
       }
-      if (++acc == 2) {
+      if (++acc == C::NACC) {
         acc = 0;
         aphase ^= 1u;
       }
@@ -368,18 +393,33 @@ struct Operands {
   int64_t ldd;
 };
 
-template <int AF, int BN, bool SWAP>
-cudaError_t launch(const Operands& o, cudaStream_t s) {
-  using C = Cfg<AF, BN, SWAP>;
-  const int64_t Kp = mx::pad128(o.K), sms = current_device_sms() > 0 ? current_device_sms() : 148;
+// Lets the kernel have its shared memory: once on each device.
+template <int AF, int H, int BN, bool SWAP>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done;  // a bit a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(gemm_mx_kernel<AF, H, BN, SWAP>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <int AF, int H, int BN, bool SWAP>
+cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
+  using C = Cfg<AF, H, BN, SWAP>;
+  const int64_t Kp = mx::pad128(o.K);
   const int64_t rows = SWAP ? o.N : o.M, cols = SWAP ? o.M : o.N;
   MMaps tm;
   memset(&tm, 0, sizeof(tm));
   const bool spread = AF != mx::kFp4;
   const bool ok =
-      SWAP ? encode_codes(&tm.r, o.W, o.N, Kp, mx::kFp4, spread, BM) &&
+      SWAP ? encode_codes(&tm.r, o.W, o.N, Kp, mx::kFp4, spread, H * BM) &&
                  encode_codes(&tm.c, o.A, o.M, Kp, AF, false, BN)
-           : encode_codes(&tm.r, o.A, o.M, Kp, AF, false, BM) &&
+           : encode_codes(&tm.r, o.A, o.M, Kp, AF, false, H * BM) &&
                  encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, spread, BN);
   if (!ok) return cudaErrorInvalidValue;
   MArgs g{};
@@ -389,11 +429,12 @@ cudaError_t launch(const Operands& o, cudaStream_t s) {
   g.D = static_cast<__nv_bfloat16*>(o.D);
   g.rs = static_cast<const uint8_t*>(SWAP ? o.Ws : o.As);
   g.cs = static_cast<const uint8_t*>(SWAP ? o.As : o.Ws);
-  const int64_t mt = (rows + BM - 1) / BM, nt = (cols + BN - 1) / BN;
+  const int64_t mt = (rows + H * BM - 1) / (H * BM), nt = (cols + BN - 1) / BN;
   if (mt * nt > INT32_MAX) return cudaErrorInvalidValue;
   g.mt = (int)mt;
   g.nt = (int)nt;
   g.nkb = (int)(Kp / 128);
+  g.rrb = (int)((rows + 127) / 128);
   g.crb = (int)((cols + 127) / 128);
   // a TMA store ends a row at a multiple of 16 bytes, so the columns must too
   g.vec = !SWAP && o.N % 8 == 0 && o.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 15) == 0;
@@ -401,28 +442,49 @@ cudaError_t launch(const Operands& o, cudaStream_t s) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     const cuuint64_t dims[2] = {(cuuint64_t)o.N, (cuuint64_t)o.M};
     const cuuint64_t strides[1] = {(cuuint64_t)o.ldd * 2};
-    const cuuint32_t box[2] = {32, 32};
+    const cuuint32_t box[2] = {64, 32};
     const cuuint32_t estr[2] = {1, 1};
     g.vec = fn && fn(&tm.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.D, dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
                         CUDA_SUCCESS;
   }
   const size_t smem = sizeof(Smem<C>) + 1024;
   static_assert(sizeof(Smem<C>) + 1024 <= 232448, "one CTA's shared memory");
-  cudaError_t e = cudaFuncSetAttribute(gemm_mx_kernel<AF, BN, SWAP>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static_assert(offsetof(Smem<C>, c) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&
+                    offsetof(Smem<C>, sr) % 1024 == 0,
+                "TMA buffers on 1024-byte boundaries");
+  const cudaError_t e = allow_smem<AF, H, BN, SWAP>((int)smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = mt * nt;
-  gemm_mx_kernel<AF, BN, SWAP><<<(unsigned)(tiles < sms ? tiles : sms), kThreads, smem, s>>>(g, tm);
+  gemm_mx_kernel<AF, H, BN, SWAP>
+      <<<(unsigned)(tiles < sms ? tiles : sms), C::THREADS, smem, s>>>(g, tm);
   return cudaGetLastError();
 }
 
+// The tile.  Up to 64 tokens fill the narrow side (16 or 64 columns) and W streams once.
+// Otherwise the SMs share L2's bandwidth, so a tile's time goes by the bytes its stages bring
+// in; of four tiles the one with the least bytes over the rounds that the tiles take on the
+// SMs.  On one B200, 4-bit A: 32768 x 6464 x 1024 131 us at 256 x 192, 139 at 128 x 256, 146
+// at 128 x 192, 179 at 128 x 128; 1000 x 2048 x 4096 17.4, 13.8, 13.3 and 11.7 us; 300 x 6464
+// x 1024 9.3, 7.6, 7.1 and 8.0.
 template <int AF>
 cudaError_t launch_af(const Operands& o, cudaStream_t s) {
-  if (o.M <= 16) return launch<AF, 16, true>(o, s);
-  if (o.M <= 64) return launch<AF, 64, true>(o, s);
-  return launch<AF, 128, false>(o, s);
+  const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
+  if (o.M <= 16) return launch<AF, 1, 16, true>(o, sms, s);
+  if (o.M <= 64) return launch<AF, 1, 64, true>(o, sms, s);
+  auto cost = [&](int64_t bm, int64_t bn) {
+    const int64_t tiles = ((o.M + bm - 1) / bm) * ((o.N + bn - 1) / bn);
+    return ((tiles + sms - 1) / sms) * ((AF == mx::kFp4 ? 1 : 2) * bm + bn);
+  };
+  const int64_t c[4] = {cost(256, 192), cost(128, 256), cost(128, 192), cost(128, 128)};
+  int best = 0;
+  for (int i = 1; i < 4; ++i)
+    if (c[i] < c[best]) best = i;
+  return best == 0   ? launch<AF, 2, 192, false>(o, sms, s)
+         : best == 1 ? launch<AF, 1, 256, false>(o, sms, s)
+         : best == 2 ? launch<AF, 1, 192, false>(o, sms, s)
+                     : launch<AF, 1, 128, false>(o, sms, s);
 }
 
 }  // namespace
