@@ -274,6 +274,7 @@ struct StepQ8Args {
   void* y_t;
 };
 cudaError_t launch_step_q8(const StepQ8Args& a, cudaStream_t s);
+cudaError_t read_and_clear_step_q8_wait_timeouts(unsigned int* count);
 // The state (rows of P fp32 values) into that form and back.
 cudaError_t launch_quant_state(int64_t rows, int64_t P, const float* h, void* codes, float* scale,
                                cudaStream_t s);

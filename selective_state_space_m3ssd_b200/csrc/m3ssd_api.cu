@@ -86,9 +86,10 @@ m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count) {
   unsigned int nm32 = 0, ns = 0;
   if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_mimo32_wait_timeouts(&nm32));
   if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_seg_wait_timeouts(&ns));
-  unsigned int nx = 0;
+  unsigned int nx = 0, nq = 0;
   if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_gemm_mx_wait_timeouts(&nx));
-  *count = n + nb + nm + ng + n32 + nw + nm32 + ns + nx;
+  if (st == M3SSD_OK) st = from_cuda(m3ssd::read_and_clear_step_q8_wait_timeouts(&nq));
+  *count = n + nb + nm + ng + n32 + nw + nm32 + ns + nx + nq;
   return st;
 }
 

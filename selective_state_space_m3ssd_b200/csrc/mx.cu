@@ -1,10 +1,12 @@
 // Quantisation to the microscaled formats of mx.cuh, and back.
 //
 // Both are streams: a bf16 element is read once (2 bytes) and leaves as half a byte or a
-// byte plus 1/32 byte of scale, so HBM bounds them.  Sixteen lanes take 128 columns of a
-// row, eight consecutive values a lane: loads and code stores are contiguous across the
-// lanes, a block's largest magnitude is two shuffles, and the four scale bytes of the
-// group leave as one 32-bit word, the tile layout's unit.
+// byte plus 1/32 byte of scale, so HBM bounds them as long as the instructions a value
+// takes stay few.  Eight lanes take 128 columns of a row, sixteen consecutive values a lane:
+// a block's largest magnitude is one shuffle, the four scale bytes of the group leave as one
+// 32-bit word, the tile layout's unit, and what a group costs (its place, scale and word)
+// is shared by sixteen values.  Rows that do not allow 32-byte accesses pass through shared
+// memory, element by element in the lanes' order on the global side.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -13,8 +15,9 @@
 namespace m3ssd {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // groups a half-warp has in flight
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kGroup = 8;   // lanes of a 128-column group
+constexpr int kUnroll = 2;  // groups a lane has in flight
 
 struct MxArgs {
   uint32_t rows, cols, nkb;  // nkb: 128-column groups a row
@@ -25,7 +28,7 @@ struct MxArgs {
   uint8_t* scales;
 };
 
-// A half-warp's groups: i, i + step, ...; row and group within the row kept beside i (a
+// A lane's groups: i, i + step, ...; row and group within the row kept beside i (a
 // division a group would cost as much as its conversion).
 struct Walk {
   uint32_t i, row, kb, nkb, drow, dkb, step;
@@ -46,39 +49,111 @@ struct Walk {
   }
 };
 
+// Sixteen consecutive elements a lane, from and to global memory in 32-byte accesses.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
+  float w[8];
+  mx::load8(reinterpret_cast<const float*>(p), w);  // two bf16 a 32-bit word
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = __float_as_uint(w[j]);
+    v[2 * j] = __uint_as_float(u << 16);
+    v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+  float a[8], b[8];
+  mx::load8(p, a);
+  mx::load8(p + 8, b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = a[j];
+    v[8 + j] = b[j];
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
+  float w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = __uint_as_float(*reinterpret_cast<uint32_t*>(&h));
+  }
+  mx::store8(reinterpret_cast<float*>(p), w);
+}
+__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
+  float a[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    a[j] = v[j];
+    b[j] = v[8 + j];
+  }
+  mx::store8(p, a);
+  mx::store8(p + 8, b);
+}
+// The scale word of a group, counted in words.
+__device__ __forceinline__ uint32_t word_index(uint32_t row, uint32_t kb, uint32_t nkb) {
+  return (((row >> 7) * nkb + kb) << 7) + ((row & 31) << 2) + ((row >> 5) & 3);
+}
+
+// VEC: rows on 32-byte boundaries and columns a multiple of 16, so a lane's sixteen values
+// are all there or all padding.
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
-  const uint32_t sub = threadIdx.x & 15, nhalf = gridDim.x * (kThreads / 16);
-  Walk w((blockIdx.x * kThreads + threadIdx.x) >> 4, nhalf, a.nkb);
-  const T* const x = static_cast<const T*>(a.x) + 8 * sub;
-  // the two halves of a warp go round together (quant8's shuffles): i - its half's place
-  for (uint32_t base = w.i & ~1u; base < a.total; base += kUnroll * nhalf) {
-    float v[kUnroll][8];
-    uint32_t at[kUnroll];  // byte offset of the scale word, in words
+  // a warp's four groups as elements (only where rows are not aligned); a lane reads sixteen
+  // at a stride of 17 words or half-words, which spreads over the banks
+  __shared__ T stage[VEC ? 1 : kWarps][VEC ? 1 : 32 * 17];
+  const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
+  const uint32_t step = gridDim.x * (kThreads / kGroup);
+  Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
+  const T* const x = static_cast<const T*>(a.x);
+  // a warp goes round together (its shuffles): by its first group
+  for (uint32_t base = w.i - lane / kGroup; base < a.total; base += kUnroll * step) {
+    float v[kUnroll][16];
+    uint32_t at[kUnroll];
     bool live[kUnroll];
     const uint32_t i0 = w.i;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t c = w.kb * 128 + sub * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      const uint32_t c = w.kb * 128 + sub * 16;
       live[u] = w.row < a.rows;
-      if (live[u] && c < a.cols) {
-        const T* p = x + ((int64_t)w.row * a.ldx + w.kb * 128);
-        if (VEC && c + 8 <= a.cols)
-          mx::load8(p, v[u]);
-        else
-          mx::load8_tail(p, (int)(a.cols - c), v[u]);
+      if (VEC) {
+        if (live[u] && c < a.cols) {
+          load16(x + ((int64_t)w.row * a.ldx + c), v[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[u][j] = 0.f;
+        }
+      } else {
+        // group e / 128 of the warp's four, column e % 128, lane by lane
+        T* const buf = stage[VEC ? 0 : warp];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t src = 8 * (j / 4);  // a lane of the group, for its row and place
+          const uint32_t row = __shfl_sync(0xffffffffu, w.row, src),
+                         kb = __shfl_sync(0xffffffffu, w.kb, src);
+          const uint32_t e = 32 * j + lane, col = kb * 128 + (e & 127);
+          T val = from_f32<T>(0.f);
+          if (row < a.rows && col < a.cols) val = x[(int64_t)row * a.ldx + col];
+          buf[(e >> 4) * 17 + (e & 15)] = val;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[u][j] = to_f32(buf[lane * 17 + j]);
       }
-      at[u] = (((w.row >> 7) * a.nkb + w.kb) << 7) + ((w.row & 31) << 2) + ((w.row >> 5) & 3);
+      at[u] = word_index(w.row, w.kb, a.nkb);
       w.next();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t i = i0 + u * nhalf;
-      uint2 c;
-      const uint32_t word = mx::quant8<FMT>(v[u], c);
-      if (live[u]) mx::store_codes<FMT>(a.codes, i, sub, c);
+      const uint32_t i = i0 + u * step;
+      uint4 c;
+      const uint32_t word = mx::quant16<FMT>(v[u], c);
+      if (live[u]) {
+        if (FMT == mx::kFp4)
+          *reinterpret_cast<uint2*>(a.codes + (int64_t)i * 64 + sub * 8) = make_uint2(c.x, c.y);
+        else
+          *reinterpret_cast<uint4*>(a.codes + (int64_t)i * 128 + sub * 16) = c;
+      }
       // rows missing from the last tile have zeros
       if (sub == 0 && i < a.total)
         reinterpret_cast<uint32_t*>(a.scales)[at[u]] = live[u] ? word : 0u;
@@ -88,53 +163,70 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
 
 template <int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
-  const uint32_t sub = threadIdx.x & 15, nhalf = gridDim.x * (kThreads / 16);
-  Walk w((blockIdx.x * kThreads + threadIdx.x) >> 4, nhalf, a.nkb);
-  T* const x = static_cast<T*>(a.x) + 8 * sub;
-  while (w.i < a.total) {
-    uint2 q[kUnroll];
-    uint32_t byte[kUnroll], col[kUnroll];
-    T* out[kUnroll];
+  __shared__ T stage[VEC ? 1 : kWarps][VEC ? 1 : 32 * 17];
+  const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
+  const uint32_t step = gridDim.x * (kThreads / kGroup);
+  Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
+  T* const x = static_cast<T*>(a.x);
+  for (uint32_t base = w.i - lane / kGroup; base < a.total; base += kUnroll * step) {
+    uint4 q[kUnroll];
+    uint32_t byte[kUnroll], row[kUnroll], kb[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      col[u] = 0xffffffffu;
-      const uint32_t c = w.kb * 128 + sub * 8;
-      if (w.i < a.total && c < a.cols) {
-        col[u] = c;
-        out[u] = x + ((int64_t)w.row * a.ldx + w.kb * 128);
-        if (FMT == mx::kFp4)
-          q[u].x = *reinterpret_cast<const uint32_t*>(a.codes + (int64_t)w.i * 64 + sub * 4);
-        else
-          q[u] = *reinterpret_cast<const uint2*>(a.codes + (int64_t)w.i * 128 + sub * 8);
-        const uint32_t at =
-            (((w.row >> 7) * a.nkb + w.kb) << 7) + ((w.row & 31) << 2) + ((w.row >> 5) & 3);
-        byte[u] = a.scales[(int64_t)at * 4 + (sub >> 2)];
+      row[u] = w.i < a.total ? w.row : 0xffffffffu;
+      kb[u] = w.kb;
+      q[u] = make_uint4(0u, 0u, 0u, 0u);
+      byte[u] = 0;
+      if (w.i < a.total) {
+        if (FMT == mx::kFp4) {
+          const uint2 c =
+              *reinterpret_cast<const uint2*>(a.codes + (int64_t)w.i * 64 + sub * 8);
+          q[u].x = c.x;
+          q[u].y = c.y;
+        } else {
+          q[u] = *reinterpret_cast<const uint4*>(a.codes + (int64_t)w.i * 128 + sub * 16);
+        }
+        byte[u] = a.scales[(int64_t)word_index(w.row, w.kb, a.nkb) * 4 + (sub >> 1)];
       }
       w.next();
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (col[u] == 0xffffffffu) continue;
       const float s = mx::scale_value(byte[u]);
-      float v[8];
+      const uint32_t c4[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      float v[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = FMT == mx::kFp4 ? mx::unpack2_e2m1((q[u].x >> (8 * j)) & 0xffu)
-                                         : mx::unpack2_e4m3((j < 2 ? q[u].x : q[u].y) >> (16 * (j & 1)));
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = FMT == mx::kFp4 ? mx::unpack2_e2m1((c4[j >> 2] >> (8 * (j & 3))) & 0xffu)
+                                         : mx::unpack2_e4m3(c4[j >> 1] >> (16 * (j & 1)));
         v[2 * j] = f.x * s;
         v[2 * j + 1] = f.y * s;
       }
-      if (VEC && col[u] + 8 <= a.cols)
-        mx::store8(out[u], v);
-      else
-        mx::store8_tail(out[u], (int)(a.cols - col[u]), v);
+      if (VEC) {
+        const uint32_t c = kb[u] * 128 + sub * 16;
+        if (row[u] < a.rows && c < a.cols) store16(x + ((int64_t)row[u] * a.ldx + c), v);
+      } else {
+        T* const buf = stage[VEC ? 0 : warp];
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = from_f32<T>(v[j]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t src = 8 * (j / 4);
+          const uint32_t r = __shfl_sync(0xffffffffu, row[u], src),
+                         k = __shfl_sync(0xffffffffu, kb[u], src);
+          const uint32_t e = 32 * j + lane, col = k * 128 + (e & 127);
+          if (r < a.rows && col < a.cols) x[(int64_t)r * a.ldx + col] = buf[(e >> 4) * 17 + (e & 15)];
+        }
+      }
     }
   }
 }
 
 template <int FMT, typename T, bool VEC>
 cudaError_t launch(const MxArgs& a, bool quant, cudaStream_t s) {
-  const uint64_t per = (uint64_t)(kThreads / 16) * kUnroll;  // groups a CTA takes at a time
+  const uint64_t per = (uint64_t)(kThreads / kGroup) * kUnroll;  // groups a CTA takes at a time
   const uint64_t want = (a.total + per - 1) / per, most = (uint64_t)current_device_sms() * 16;
   const unsigned grid = (unsigned)(want < most || most == 0 ? want : most);
   if (quant)
@@ -145,7 +237,8 @@ cudaError_t launch(const MxArgs& a, bool quant, cudaStream_t s) {
 }
 
 cudaError_t dispatch(int fmt, bool bf16, const MxArgs& a, bool quant, cudaStream_t s) {
-  const bool vec = bf16 ? mx::aligned8<__nv_bfloat16>(a.x, a.ldx) : mx::aligned8<float>(a.x, a.ldx);
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.cols % 16 == 0 &&
+                   a.ldx % (bf16 ? 16 : 8) == 0;
   if (a.total == 0) return cudaSuccess;
   if (fmt == mx::kFp4) {
     if (bf16)

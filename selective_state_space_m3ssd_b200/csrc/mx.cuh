@@ -136,6 +136,32 @@ __device__ __forceinline__ uint32_t quant8(const float (&v)[8], uint2& codes) {
   w |= __shfl_xor_sync(0xffffffffu, w, 8);
   return w;
 }
+// The same with sixteen values a lane: eight lanes to a group, two to a block.
+template <int FMT>
+__device__ __forceinline__ uint32_t quant16(const float (&v)[16], uint4& codes) {
+  float m = max3_abs(v[0], v[1], v[2]);
+#pragma unroll
+  for (int j = 3; j < 15; j += 2) m = max3_abs(m, v[j], v[j + 1]);
+  m = max3_abs(m, v[15], __shfl_xor_sync(0xffffffffu, max3_abs(m, v[15], 0.f), 1));
+  const uint32_t byte = scale_byte<FMT>(__float_as_uint(m));
+  const float inv = inv_scale(byte);
+  float q[2][8];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) q[j >> 3][j & 7] = v[j] * inv;
+  if (FMT == kFp4) {
+    codes = make_uint4(pack_e2m1(q[0]), pack_e2m1(q[1]), 0u, 0u);
+  } else {
+    codes = make_uint4(pack4_e4m3(q[0][0], q[0][1], q[0][2], q[0][3]),
+                       pack4_e4m3(q[0][4], q[0][5], q[0][6], q[0][7]),
+                       pack4_e4m3(q[1][0], q[1][1], q[1][2], q[1][3]),
+                       pack4_e4m3(q[1][4], q[1][5], q[1][6], q[1][7]));
+  }
+  if (byte == 255u) codes = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t w = byte << (8 * ((threadIdx.x >> 1) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 2);
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  return w;
+}
 // Stores a lane's codes of 128-column group i (counted over the rows' groups).
 template <int FMT>
 __device__ __forceinline__ void store_codes(uint8_t* codes, int64_t i, uint32_t sub, uint2 c) {

@@ -19,11 +19,16 @@
 
 #include "internal.h"
 #include "mx.cuh"
+#include "tc5.cuh"
 
 namespace m3ssd {
+
+__device__ unsigned int g_step_q8_wait_timeouts;
+
 namespace {
 
 constexpr int kN = 128, kP = 64;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kTiny = 7.8886090522101181e-31f;  // 2^-100
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -90,179 +95,269 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
   }
 }
 
-// Factors of one state row.
+// Factors of one state row, each twice: a pair for the two-wide operations.
 struct RowCoef {
-  float bp, bc, cc, as;  // beta Bbar_prev, gamma Bbar, Cbar, alpha s
+  float bp[2], bc[2], cc[2], as[2];  // beta Bbar_prev, gamma Bbar, Cbar, alpha s
 };
+__device__ __forceinline__ void set2(float (&d)[2], float v) {
+  *reinterpret_cast<float2*>(d) = make_float2(v, v);
+}
 
-// N = 128, P = 64: W warps share a (b, h); a lane owns 16 columns (lane % 4) of the rows
-// lane / 4 + 8 k, sixteen codes a load, so a warp's load is 512 contiguous bytes and every
-// row is complete in four lanes.
-template <typename T, int W>
-__global__ void __launch_bounds__(128, 4) step_q8_n128p64(StepQ8Args a) {
-  constexpr int kGroups = 4 / W;       // (b, h) a CTA
-  constexpr int kK = 16 / W;           // rows a lane
-  __shared__ RowCoef coef[kGroups][kN];
-  __shared__ float ysum[kGroups][W == 1 ? 1 : W][kP];
-  const int lane = threadIdx.x & 31, grp = threadIdx.x / (32 * W), t = threadIdx.x % (32 * W);
-  const int warp = t >> 5;  // within the group
-  const int64_t bh = (int64_t)blockIdx.x * kGroups + grp;
-  if (kGroups > 1 && bh >= a.b * a.H) return;
-  auto sync = [&]() {
-    if (W == 1)
-      __syncwarp();
-    else if (W == 4)
-      __syncthreads();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "n"(32 * W) : "memory");
-  };
-  const int64_t b = bh / a.H, h = bh % a.H, rep = a.H / a.G, g = h / rep;
-  const int q = lane & 3, r0 = warp * (kN / W) + (lane >> 2);
-
-  const uint4* S = reinterpret_cast<const uint4*>(a.ssm + bh * kN * kP);
-  uint4 hv[kK];
-#pragma unroll
-  for (int k = 0; k < kK; ++k) hv[k] = S[(r0 + 8 * k) * (kP / 16) + q];
-  const T* xt = static_cast<const T*>(a.x_t) + bh * kP;
-  float x[16], xp[16];
-  load16(xt + 16 * q, x);
-  load16(a.x_prev + bh * kP + 16 * q, xp);
-
-  const float alpha = expf(a.logdecay_t[bh]);
-  const float be = a.beta_t ? a.beta_t[bh] : 0.f, ga = a.gamma_t[bh];
-  const T* Bt = static_cast<const T*>(a.B_t) + (b * a.G + g) * kN;
-  const T* Ct = static_cast<const T*>(a.C_t) + (b * a.G + g) * kN;
-  const float* bprev = a.b_prev + (b * a.G + g) * kN;
-  const bool copy_b = a.b_prev_out && h % rep == 0;
-  // the factors of the rows 2 i and 2 i + 1 that turn with the new angle, and with the old
-  auto turned_new = [&](int i, float ph) {
-    float s, c;
-    sincosf(ph, &s, &c);
-    const float b0 = to_f32(Bt[2 * i]), b1 = to_f32(Bt[2 * i + 1]);
-    const float2 rb = rot2(c, s, b0, b1);
-    const float2 rc = rot2(c, s, to_f32(Ct[2 * i]), to_f32(Ct[2 * i + 1]));
-    coef[grp][2 * i].bc = ga * rb.x;
-    coef[grp][2 * i + 1].bc = ga * rb.y;
-    coef[grp][2 * i].cc = rc.x;
-    coef[grp][2 * i + 1].cc = rc.y;
-    if (copy_b)
-      *reinterpret_cast<float2*>(a.b_prev_out + (b * a.G + g) * kN + 2 * i) = make_float2(b0, b1);
-  };
-  auto turned_old = [&](int i, float ang) {
-    float s, c;
-    sincosf(ang, &s, &c);
-    const float2 rp = rot2(c, s, bprev[2 * i], bprev[2 * i + 1]);
-    const float2 sc = *reinterpret_cast<const float2*>(a.scale + bh * kN + 2 * i);
-    coef[grp][2 * i].bp = be * rp.x;
-    coef[grp][2 * i + 1].bp = be * rp.y;
-    coef[grp][2 * i].as = alpha * sc.x;
-    coef[grp][2 * i + 1].as = alpha * sc.y;
-  };
-  float ph = 0.f;  // W = 4: phi' of pair t % 64
-  if (W <= 2) {
-#pragma unroll
-    for (int i = t; i < kN / 2; i += 32 * W) {
-      const float ang = a.angle[bh * 64 + i];
-      const float p = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * 64 + i] : 0.f));
-      turned_new(i, p);
-      turned_old(i, ang);
-      a.angle_out[bh * 64 + i] = p;
-    }
-  } else {  // a thread a pair and angle
-    const int i = t & 63;
-    const float ang = a.angle[bh * 64 + i];
-    if (t < 64) {
-      ph = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * 64 + i] : 0.f));
-      turned_new(i, ph);
-    } else {
-      turned_old(i, ang);
-    }
-  }
-  sync();
-
-  uint64_t x2[8], xp2[8], acc[8];
+// N = 128, P = 64: a lane owns 16 columns (lane % 4) of a row, so a row is complete in four
+// lanes and a warp's access to eight rows is 512 contiguous bytes.
+// One row: the new values' codes and scale from the old codes; adds Cbar h to acc.
+__device__ __forceinline__ uint4 update_row(const uint4& codes, const RowCoef& f,
+                                            const uint64_t (&x2)[8], const uint64_t (&xp2)[8],
+                                            uint64_t (&acc)[8], float& s) {
+  const ulonglong2 f0 = *reinterpret_cast<const ulonglong2*>(f.bp),
+                   f1 = *reinterpret_cast<const ulonglong2*>(f.cc);
+  const uint32_t c4[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint64_t v[8];
+  float amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    x2[j] = pack2(x[2 * j], x[2 * j + 1]);
-    xp2[j] = pack2(xp[2 * j], xp[2 * j + 1]);
-    acc[j] = 0;
+    const float2 c = mx::unpack2_e4m3(c4[j >> 1] >> (16 * (j & 1)));
+    v[j] = fma2(f0.y, x2[j], fma2(f0.x, xp2[j], mul2(f1.y, pack2(c.x, c.y))));
+    acc[j] = fma2(f1.x, v[j], acc[j]);
+    const float2 u = unpack2(v[j]);
+    amax = mx::max3_abs(amax, u.x, u.y);
   }
-  uint4* So = reinterpret_cast<uint4*>(a.ssm_out + bh * kN * kP);
+  amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  float inv;
+  row_scale<false>(amax, s, inv);
+  const uint64_t inv2 = pack2(inv, inv);
+  uint32_t o[4];
 #pragma unroll
-  for (int k = 0; k < kK; ++k) {
-    const int n = r0 + 8 * k;
-    const float4 f = *reinterpret_cast<const float4*>(&coef[grp][n]);
-    const uint64_t bp = pack2(f.x, f.x), bc = pack2(f.y, f.y), cc = pack2(f.z, f.z),
-                   as = pack2(f.w, f.w);
-    const uint32_t c4[4] = {hv[k].x, hv[k].y, hv[k].z, hv[k].w};
-    uint64_t v[8];
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 c = mx::unpack2_e4m3(c4[j >> 1] >> (16 * (j & 1)));
-      v[j] = fma2(bc, x2[j], fma2(bp, xp2[j], mul2(as, pack2(c.x, c.y))));
-      acc[j] = fma2(cc, v[j], acc[j]);
-      const float2 u = unpack2(v[j]);
-      amax = mx::max3_abs(amax, u.x, u.y);
-    }
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    float s, inv;
-    row_scale<false>(amax, s, inv);
-    const uint64_t inv2 = pack2(inv, inv);
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 u = unpack2(mul2(v[2 * j], inv2)), w = unpack2(mul2(v[2 * j + 1], inv2));
-      o[j] = mx::pack4_e4m3(u.x, u.y, w.x, w.y);
-    }
-    So[n * (kP / 16) + q] = make_uint4(o[0], o[1], o[2], o[3]);
-    if (q == 0) a.scale_out[bh * kN + n] = s;
+  for (int j = 0; j < 4; ++j) {
+    const float2 u = unpack2(mul2(v[2 * j], inv2)), w = unpack2(mul2(v[2 * j + 1], inv2));
+    o[j] = mx::pack4_e4m3(u.x, u.y, w.x, w.y);
   }
-  // y: lanes with equal q hold sums of the same 16 columns; each exchange halves what a
-  // lane keeps, until it has two columns of the warp's sum
-  float y8[16];
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Sums acc over the lanes with equal lane % 4 (the same 16 columns): each exchange halves
+// what a lane keeps, until it has columns col and col + 1 of the warp's sum.
+__device__ __forceinline__ float2 sum_columns(const uint64_t (&acc)[8], int lane, int& col) {
+  float y[16];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float2 u = unpack2(acc[j]);
-    y8[2 * j] = u.x;
-    y8[2 * j + 1] = u.y;
+    y[2 * j] = u.x;
+    y[2 * j + 1] = u.y;
   }
-  int col = 16 * q;
+  col = 16 * (lane & 3);
 #pragma unroll
   for (int w = 8, bit = 16; w >= 2; w >>= 1, bit >>= 1) {
     const bool up = lane & bit;
 #pragma unroll
     for (int j = 0; j < w; ++j) {
-      const float send = up ? y8[j] : y8[j + w], keep = up ? y8[j + w] : y8[j];
-      y8[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+      const float send = up ? y[j] : y[j + w], keep = up ? y[j + w] : y[j];
+      y[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
     }
     col += up ? w : 0;
   }
-  if (W > 1) {
-    ysum[grp][warp][col] = y8[0];
-    ysum[grp][warp][col + 1] = y8[1];
-    sync();
-    if (t >= 64) return;
-    if (W == 4) a.angle_out[bh * 64 + t] = ph;  // every old angle was read before the barriers
-    col = t;
-    float y = 0.f;
+  return make_float2(y[0], y[1]);
+}
+
+__device__ __forceinline__ void pairs(const float (&v)[16], uint64_t (&p)[8]) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) y += ysum[grp][w][col];
-    const float xv = to_f32(xt[col]);
-    if (a.D) y = fmaf(a.D[h], xv, y);
-    static_cast<T*>(a.y_t)[bh * kP + col] = from_f32<T>(y);
-    a.x_prev_out[bh * kP + col] = xv;
-    return;
+  for (int j = 0; j < 8; ++j) p[j] = pack2(v[2 * j], v[2 * j + 1]);
+}
+
+// Few (b, h): a CTA of four warps each, everything loaded at once, the rotations a thread a
+// pair and angle.
+template <typename T>
+__global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
+  constexpr int kRows = 4;  // rows a lane
+  __shared__ __align__(16) RowCoef coef[kN];
+  __shared__ float ysum[4][kP];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int64_t bh = blockIdx.x;
+  const int64_t b = bh / a.H, h = bh % a.H, rep = a.H / a.G, g = h / rep;
+  const int q = lane & 3, r0 = warp * 32 + (lane >> 2);
+
+  const uint4* S = reinterpret_cast<const uint4*>(a.ssm + bh * kN * kP);
+  uint4 hv[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) hv[k] = S[(r0 + 8 * k) * (kP / 16) + q];
+  const T* xt = static_cast<const T*>(a.x_t) + bh * kP;
+  float x[16], xp[16];
+  load16(xt + 16 * q, x);
+  load16(a.x_prev + bh * kP + 16 * q, xp);
+
+  const T* Bt = static_cast<const T*>(a.B_t) + (b * a.G + g) * kN;
+  const T* Ct = static_cast<const T*>(a.C_t) + (b * a.G + g) * kN;
+  const int i = t & 63;  // rows 2 i and 2 i + 1
+  const float ang = a.angle[bh * 64 + i];
+  float ph = 0.f, sn, cs;
+  if (t < 64) {  // what turns with the new angle
+    const float ga = a.gamma_t[bh];
+    ph = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * 64 + i] : 0.f));
+    sincosf(ph, &sn, &cs);
+    const float b0 = to_f32(Bt[2 * i]), b1 = to_f32(Bt[2 * i + 1]);
+    const float2 rb = rot2(cs, sn, b0, b1);
+    const float2 rc = rot2(cs, sn, to_f32(Ct[2 * i]), to_f32(Ct[2 * i + 1]));
+    set2(coef[2 * i].bc, ga * rb.x);
+    set2(coef[2 * i + 1].bc, ga * rb.y);
+    set2(coef[2 * i].cc, rc.x);
+    set2(coef[2 * i + 1].cc, rc.y);
+    if (a.b_prev_out && h % rep == 0)
+      *reinterpret_cast<float2*>(a.b_prev_out + (b * a.G + g) * kN + 2 * i) = make_float2(b0, b1);
+  } else {  // and with the old
+    const float alpha = expf(a.logdecay_t[bh]), be = a.beta_t ? a.beta_t[bh] : 0.f;
+    const float2 bp = *reinterpret_cast<const float2*>(a.b_prev + (b * a.G + g) * kN + 2 * i);
+    const float2 sc = *reinterpret_cast<const float2*>(a.scale + bh * kN + 2 * i);
+    sincosf(ang, &sn, &cs);
+    const float2 rp = rot2(cs, sn, bp.x, bp.y);
+    set2(coef[2 * i].bp, be * rp.x);
+    set2(coef[2 * i + 1].bp, be * rp.y);
+    set2(coef[2 * i].as, alpha * sc.x);
+    set2(coef[2 * i + 1].as, alpha * sc.y);
   }
-  __syncwarp();  // every lane has read x_prev
+  __syncthreads();
+
+  uint64_t x2[8], xp2[8], acc[8] = {};
+  pairs(x, x2);
+  pairs(xp, xp2);
+  uint4* So = reinterpret_cast<uint4*>(a.ssm_out + bh * kN * kP);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float xv = to_f32(xt[col + j]);
-    float y = y8[j];
+  for (int k = 0; k < kRows; ++k) {
+    const int n = r0 + 8 * k;
+    float s;
+    So[n * (kP / 16) + q] = update_row(hv[k], coef[n], x2, xp2, acc, s);
+    if (q == 0) a.scale_out[bh * kN + n] = s;
+  }
+  int col;
+  const float2 y2 = sum_columns(acc, lane, col);
+  *reinterpret_cast<float2*>(&ysum[warp][col]) = y2;
+  __syncthreads();
+  if (t >= 64) return;
+  a.angle_out[bh * 64 + t] = ph;  // every old angle and x_prev was read before the barriers
+  float y = (ysum[0][t] + ysum[1][t]) + (ysum[2][t] + ysum[3][t]);
+  const float xv = to_f32(xt[t]);
+  if (a.D) y = fmaf(a.D[h], xv, y);
+  static_cast<T*>(a.y_t)[bh * kP + t] = from_f32<T>(y);
+  a.x_prev_out[bh * kP + t] = xv;
+}
+
+// Many (b, h): CTAs of two warps walk them; bulk copies bring the next one's parts into one
+// of two stages while a CTA works on the other, so the state is never waited for with
+// registers held, and nine CTAs an SM keep 88 KB in flight.
+constexpr int kWalkThreads = 64, kWalkCtas = 9;
+
+template <typename T>
+struct alignas(128) StepStage {
+  uint8_t codes[kN * kP];
+  float scale[kN];
+  float angle[kN / 2];
+  float theta[kN / 2];
+  float xp[kP];
+  T x[kP];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Args a) {
+  constexpr int kRows = 8;  // rows a lane
+  __shared__ StepStage<T> stage[2];
+  __shared__ __align__(16) RowCoef coef[kN];
+  __shared__ float ysum[2][kP];
+  __shared__ uint64_t full[2];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int q = lane & 3, r0 = warp * 64 + (lane >> 2);
+  const int64_t total = a.b * a.H, rep = a.H / a.G;
+  auto fetch = [&](int64_t bh, int st) {
+    StepStage<T>& d = stage[st];
+    const uint32_t bytes = sizeof(d.codes) + sizeof(d.scale) + sizeof(d.angle) + sizeof(d.xp) +
+                           sizeof(d.x) + (a.theta_t ? sizeof(d.theta) : 0);
+    tc5::mbar_arrive_expect_tx(&full[st], bytes);
+    tc5::bulk_load(tc5::saddr(d.codes), a.ssm + bh * kN * kP, sizeof(d.codes), &full[st]);
+    tc5::bulk_load(tc5::saddr(d.scale), a.scale + bh * kN, sizeof(d.scale), &full[st]);
+    tc5::bulk_load(tc5::saddr(d.angle), a.angle + bh * (kN / 2), sizeof(d.angle), &full[st]);
+    tc5::bulk_load(tc5::saddr(d.xp), a.x_prev + bh * kP, sizeof(d.xp), &full[st]);
+    tc5::bulk_load(tc5::saddr(d.x), static_cast<const T*>(a.x_t) + bh * kP, sizeof(d.x), &full[st]);
+    if (a.theta_t)
+      tc5::bulk_load(tc5::saddr(d.theta), a.theta_t + bh * (kN / 2), sizeof(d.theta), &full[st]);
+  };
+  if (t == 0) {
+    tc5::mbar_init(&full[0], 1);
+    tc5::mbar_init(&full[1], 1);
+    tc5::fence_mbar_init();
+  }
+  __syncthreads();
+  int64_t bh = blockIdx.x;
+  if (t == 0) fetch(bh, 0);  // the grid is no larger than the walk
+  for (uint32_t it = 0; bh < total; bh += gridDim.x, ++it) {
+    const int st = it & 1;
+    const int64_t next = bh + gridDim.x;
+    // the other stage was last read before the barrier that ended the round before
+    if (t == 0 && next < total) fetch(next, st ^ 1);
+    const int64_t b = bh / a.H, h = bh - b * a.H, g = h / rep;
+    const int64_t gn = (b * a.G + g) * kN + 2 * t;  // pair t: rows 2 t and 2 t + 1
+    const T* Bt = static_cast<const T*>(a.B_t) + gn;
+    const T* Ct = static_cast<const T*>(a.C_t) + gn;
+    const float b0 = to_f32(Bt[0]), b1 = to_f32(Bt[1]), c0 = to_f32(Ct[0]), c1 = to_f32(Ct[1]);
+    const float2 bp = *reinterpret_cast<const float2*>(a.b_prev + gn);
+    const float alpha = expf(a.logdecay_t[bh]);
+    const float be = a.beta_t ? a.beta_t[bh] : 0.f, ga = a.gamma_t[bh];
+    const StepStage<T>& d = stage[st];
+    const bool late = !tc5::mbar_wait(&full[st], (it >> 1) & 1u, kWaitLimitNs);
+    {
+      float sn, cs;
+      const float ang = d.angle[t];
+      sincosf(ang, &sn, &cs);
+      const float2 rp = rot2(cs, sn, bp.x, bp.y);
+      const float ph = wrap_angle(ang + (a.theta_t ? d.theta[t] : 0.f));
+      sincosf(ph, &sn, &cs);
+      const float2 rb = rot2(cs, sn, b0, b1), rc = rot2(cs, sn, c0, c1);
+      set2(coef[2 * t].bp, be * rp.x);
+      set2(coef[2 * t].bc, ga * rb.x);
+      set2(coef[2 * t].cc, rc.x);
+      set2(coef[2 * t].as, alpha * d.scale[2 * t]);
+      set2(coef[2 * t + 1].bp, be * rp.y);
+      set2(coef[2 * t + 1].bc, ga * rb.y);
+      set2(coef[2 * t + 1].cc, rc.y);
+      set2(coef[2 * t + 1].as, alpha * d.scale[2 * t + 1]);
+      if (!late) {
+        a.angle_out[bh * (kN / 2) + t] = ph;
+        if (a.b_prev_out && h - g * rep == 0)
+          *reinterpret_cast<float2*>(a.b_prev_out + gn) = make_float2(b0, b1);
+      }
+    }
+    if (tc5::bar_or(1, kWalkThreads, late)) {  // the copies in flight land before the CTA ends
+      if (t == 0) {
+        if (next < total)
+          (void)tc5::mbar_wait(&full[st ^ 1], ((it + 1) >> 1) & 1u, kWaitLimitNs);
+        atomicAdd(&g_step_q8_wait_timeouts, 1u);
+      }
+      return;
+    }
+    uint64_t x2[8], xp2[8], acc[8] = {};
+    {
+      float v[16];
+      load16(d.x + 16 * q, v);
+      pairs(v, x2);
+      load16(d.xp + 16 * q, v);
+      pairs(v, xp2);
+    }
+    const float xv = to_f32(d.x[t]);
+    const uint4* S = reinterpret_cast<const uint4*>(d.codes);
+    uint4* So = reinterpret_cast<uint4*>(a.ssm_out + bh * kN * kP);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int n = r0 + 8 * k;
+      float s;
+      So[n * (kP / 16) + q] = update_row(S[n * (kP / 16) + q], coef[n], x2, xp2, acc, s);
+      if (q == 0) a.scale_out[bh * kN + n] = s;
+    }
+    int col;
+    const float2 y2 = sum_columns(acc, lane, col);
+    *reinterpret_cast<float2*>(&ysum[warp][col]) = y2;
+    __syncthreads();
+    float y = ysum[0][t] + ysum[1][t];
     if (a.D) y = fmaf(a.D[h], xv, y);
-    static_cast<T*>(a.y_t)[bh * kP + col + j] = from_f32<T>(y);
-    a.x_prev_out[bh * kP + col + j] = xv;
+    static_cast<T*>(a.y_t)[bh * kP + t] = from_f32<T>(y);
+    a.x_prev_out[bh * kP + t] = xv;
   }
 }
 
@@ -368,13 +463,16 @@ cudaError_t launch_step_t(StepQ8Args a, cudaStream_t s) {
   const int64_t nbh = a.b * a.H;
   const uintptr_t all = reinterpret_cast<uintptr_t>(a.ssm) | reinterpret_cast<uintptr_t>(a.ssm_out) |
                         reinterpret_cast<uintptr_t>(a.x_t) | reinterpret_cast<uintptr_t>(a.x_prev) |
-                        reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(bprev);
+                        reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.angle) |
+                        reinterpret_cast<uintptr_t>(a.theta_t) | reinterpret_cast<uintptr_t>(a.b_prev) |
+                        reinterpret_cast<uintptr_t>(bprev);
   if (a.N == kN && a.P == kP && all % 16 == 0) {
-    const int sms = current_device_sms();
-    if (nbh <= 2 * (int64_t)sms)
-      step_q8_n128p64<T, 4><<<(unsigned)nbh, 128, 0, s>>>(a);
+    const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
+    const int64_t walkers = sms * kWalkCtas;
+    if (nbh <= 2 * sms)
+      step_q8_one<T><<<(unsigned)nbh, 128, 0, s>>>(a);
     else
-      step_q8_n128p64<T, 2><<<(unsigned)((nbh + 1) / 2), 128, 0, s>>>(a);
+      step_q8_walk<T><<<(unsigned)(nbh < walkers ? nbh : walkers), kWalkThreads, 0, s>>>(a);
   } else {
     const size_t smem = sizeof(float) * (size_t)(3 * a.N + kGenWarps * a.P);
     step_q8_kernel<T><<<(unsigned)nbh, kGenThreads, smem, s>>>(a);
@@ -513,6 +611,12 @@ cudaError_t launch_state(bool quant, int64_t rows, int64_t P, float* h, void* co
 cudaError_t launch_step_q8(const StepQ8Args& a, cudaStream_t s) {
   if (a.b * a.H == 0) return cudaSuccess;
   return a.bf16 ? launch_step_t<__nv_bfloat16>(a, s) : launch_step_t<float>(a, s);
+}
+cudaError_t read_and_clear_step_q8_wait_timeouts(unsigned int* count) {
+  const unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(count, g_step_q8_wait_timeouts, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_step_q8_wait_timeouts, &zero, sizeof(unsigned int));
 }
 cudaError_t launch_quant_state(int64_t rows, int64_t P, const float* h, void* codes, float* scale,
                                cudaStream_t s) {
