@@ -21,7 +21,7 @@ constexpr int kUnroll = 2;  // groups a lane has in flight
 
 struct MxArgs {
   uint32_t rows, cols, nkb;  // nkb: 128-column groups a row
-  uint32_t total;            // groups: rows (quant: rounded up to 128) * nkb
+  uint32_t total;            // rows * nkb groups
   int64_t ldx;
   void* x;
   uint8_t* codes;
@@ -49,27 +49,46 @@ struct Walk {
   }
 };
 
-// Sixteen consecutive elements a lane, from and to global memory in 32-byte accesses.
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
-  float w[8];
-  mx::load8(reinterpret_cast<const float*>(p), w);  // two bf16 a 32-bit word
+// Sixteen consecutive elements as loaded in 32-byte accesses (a group in flight holds them so)
+// and as floats.
+template <typename T>
+struct Raw16;
+template <>
+struct Raw16<__nv_bfloat16> {
+  float w[8];  // two bf16 a word
+  __device__ void load(const __nv_bfloat16* p) { mx::load8(reinterpret_cast<const float*>(p), w); }
+  __device__ void clear() {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t u = __float_as_uint(w[j]);
-    v[2 * j] = __uint_as_float(u << 16);
-    v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
   }
-}
-__device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
+  __device__ void get(float (&v)[16]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(w[j]);
+      v[2 * j] = __uint_as_float(u << 16);
+      v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw16<float> {
   float a[8], b[8];
-  mx::load8(p, a);
-  mx::load8(p + 8, b);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = a[j];
-    v[8 + j] = b[j];
+  __device__ void load(const float* p) {
+    mx::load8(p, a);
+    mx::load8(p + 8, b);
   }
-}
+  __device__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.f;
+  }
+  __device__ void get(float (&v)[16]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = a[j];
+      v[8 + j] = b[j];
+    }
+  }
+};
 __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
   float w[8];
 #pragma unroll
@@ -94,37 +113,30 @@ __device__ __forceinline__ uint32_t word_index(uint32_t row, uint32_t kb, uint32
   return (((row >> 7) * nkb + kb) << 7) + ((row & 31) << 2) + ((row >> 5) & 3);
 }
 
-// VEC: rows on 32-byte boundaries and columns a multiple of 16, so a lane's sixteen values
-// are all there or all padding.
-template <int FMT, typename T, bool VEC>
+// How a row is reached: kFull, 32-byte boundaries and columns a multiple of 128; kVec, columns
+// a multiple of 16 (a lane's sixteen values are all there or all padding); kAny.
+enum Access { kFull, kVec, kAny };
+
+template <int FMT, typename T, int ACC>
 __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
-  // a warp's four groups as elements (only where rows are not aligned); a lane reads sixteen
-  // at a stride of 17 words or half-words, which spreads over the banks
-  __shared__ T stage[VEC ? 1 : kWarps][VEC ? 1 : 32 * 17];
+  // kAny: a warp's four groups as elements; a lane reads its sixteen at a stride of 17, which
+  // spreads over the banks
+  __shared__ T stage[ACC == kAny ? kWarps : 1][ACC == kAny ? 32 * 17 : 1];
   const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
   const uint32_t step = gridDim.x * (kThreads / kGroup);
   Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
   const T* const x = static_cast<const T*>(a.x);
   // a warp goes round together (its shuffles): by its first group
   for (uint32_t base = w.i - lane / kGroup; base < a.total; base += kUnroll * step) {
-    float v[kUnroll][16];
+    Raw16<T> raw[kUnroll];
+    float any[ACC == kAny ? kUnroll : 1][16];
     uint32_t at[kUnroll];
-    bool live[kUnroll];
     const uint32_t i0 = w.i;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t c = w.kb * 128 + sub * 16;
-      live[u] = w.row < a.rows;
-      if (VEC) {
-        if (live[u] && c < a.cols) {
-          load16(x + ((int64_t)w.row * a.ldx + c), v[u]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[u][j] = 0.f;
-        }
-      } else {
+      if constexpr (ACC == kAny) {
         // group e / 128 of the warp's four, column e % 128, lane by lane
-        T* const buf = stage[VEC ? 0 : warp];
+        T* const buf = stage[warp];
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -138,7 +150,13 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[u][j] = to_f32(buf[lane * 17 + j]);
+        for (int j = 0; j < 16; ++j) any[u][j] = to_f32(buf[lane * 17 + j]);
+      } else {
+        const uint32_t c = w.kb * 128 + sub * 16;
+        if (w.i < a.total && (ACC == kFull || c < a.cols))
+          raw[u].load(x + ((int64_t)w.row * a.ldx + c));
+        else if (ACC == kVec)
+          raw[u].clear();
       }
       at[u] = word_index(w.row, w.kb, a.nkb);
       w.next();
@@ -146,24 +164,33 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t i = i0 + u * step;
+      float v[16];
+      if constexpr (ACC == kAny) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = any[u][j];
+      } else {
+        raw[u].get(v);
+      }
       uint4 c;
-      const uint32_t word = mx::quant16<FMT>(v[u], c);
-      if (live[u]) {
+      const uint32_t word = mx::quant16<FMT>(v, c);
+      if (i < a.total) {
         if (FMT == mx::kFp4)
           *reinterpret_cast<uint2*>(a.codes + (int64_t)i * 64 + sub * 8) = make_uint2(c.x, c.y);
         else
           *reinterpret_cast<uint4*>(a.codes + (int64_t)i * 128 + sub * 16) = c;
+        if (sub == 0) reinterpret_cast<uint32_t*>(a.scales)[at[u]] = word;
       }
-      // rows missing from the last tile have zeros
-      if (sub == 0 && i < a.total)
-        reinterpret_cast<uint32_t*>(a.scales)[at[u]] = live[u] ? word : 0u;
     }
   }
+  // the words of the rows missing from the last tile are zero
+  const uint32_t missing = (uint32_t)(mx::pad128(a.rows) - a.rows) * a.nkb;
+  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < missing; i += gridDim.x * kThreads)
+    reinterpret_cast<uint32_t*>(a.scales)[word_index(a.rows + i / a.nkb, i % a.nkb, a.nkb)] = 0u;
 }
 
-template <int FMT, typename T, bool VEC>
+template <int FMT, typename T, int ACC>
 __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
-  __shared__ T stage[VEC ? 1 : kWarps][VEC ? 1 : 32 * 17];
+  __shared__ T stage[ACC == kAny ? kWarps : 1][ACC == kAny ? 32 * 17 : 1];
   const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
   const uint32_t step = gridDim.x * (kThreads / kGroup);
   Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
@@ -202,11 +229,8 @@ __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
         v[2 * j] = f.x * s;
         v[2 * j + 1] = f.y * s;
       }
-      if (VEC) {
-        const uint32_t c = kb[u] * 128 + sub * 16;
-        if (row[u] < a.rows && c < a.cols) store16(x + ((int64_t)row[u] * a.ldx + c), v);
-      } else {
-        T* const buf = stage[VEC ? 0 : warp];
+      if constexpr (ACC == kAny) {
+        T* const buf = stage[warp];
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = from_f32<T>(v[j]);
@@ -219,39 +243,43 @@ __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
           const uint32_t e = 32 * j + lane, col = k * 128 + (e & 127);
           if (r < a.rows && col < a.cols) x[(int64_t)r * a.ldx + col] = buf[(e >> 4) * 17 + (e & 15)];
         }
+      } else {
+        const uint32_t c = kb[u] * 128 + sub * 16;
+        if (row[u] < a.rows && (ACC == kFull || c < a.cols))
+          store16(x + ((int64_t)row[u] * a.ldx + c), v);
       }
     }
   }
 }
 
-template <int FMT, typename T, bool VEC>
+template <int FMT, typename T, int ACC>
 cudaError_t launch(const MxArgs& a, bool quant, cudaStream_t s) {
   const uint64_t per = (uint64_t)(kThreads / kGroup) * kUnroll;  // groups a CTA takes at a time
   const uint64_t want = (a.total + per - 1) / per, most = (uint64_t)current_device_sms() * 16;
   const unsigned grid = (unsigned)(want < most || most == 0 ? want : most);
   if (quant)
-    mx_quant_kernel<FMT, T, VEC><<<grid, kThreads, 0, s>>>(a);
+    mx_quant_kernel<FMT, T, ACC><<<grid, kThreads, 0, s>>>(a);
   else
-    mx_dequant_kernel<FMT, T, VEC><<<grid, kThreads, 0, s>>>(a);
+    mx_dequant_kernel<FMT, T, ACC><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t dispatch(int fmt, bool bf16, const MxArgs& a, bool quant, cudaStream_t s) {
+template <int FMT, typename T>
+cudaError_t by_access(const MxArgs& a, bool quant, cudaStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 32 == 0 && a.cols % 16 == 0 &&
-                   a.ldx % (bf16 ? 16 : 8) == 0;
-  if (a.total == 0) return cudaSuccess;
-  if (fmt == mx::kFp4) {
-    if (bf16)
-      return vec ? launch<mx::kFp4, __nv_bfloat16, true>(a, quant, s)
-                 : launch<mx::kFp4, __nv_bfloat16, false>(a, quant, s);
-    return vec ? launch<mx::kFp4, float, true>(a, quant, s)
-               : launch<mx::kFp4, float, false>(a, quant, s);
-  }
-  if (bf16)
-    return vec ? launch<mx::kFp8, __nv_bfloat16, true>(a, quant, s)
-               : launch<mx::kFp8, __nv_bfloat16, false>(a, quant, s);
-  return vec ? launch<mx::kFp8, float, true>(a, quant, s)
-             : launch<mx::kFp8, float, false>(a, quant, s);
+                   a.ldx * (int64_t)sizeof(T) % 32 == 0;
+  return !vec               ? launch<FMT, T, kAny>(a, quant, s)
+         : a.cols % 128 != 0 ? launch<FMT, T, kVec>(a, quant, s)
+                             : launch<FMT, T, kFull>(a, quant, s);
+}
+
+cudaError_t dispatch(int fmt, bool bf16, const MxArgs& a, bool quant, cudaStream_t s) {
+  if (a.rows == 0) return cudaSuccess;
+  if (fmt == mx::kFp4)
+    return bf16 ? by_access<mx::kFp4, __nv_bfloat16>(a, quant, s)
+                : by_access<mx::kFp4, float>(a, quant, s);
+  return bf16 ? by_access<mx::kFp8, __nv_bfloat16>(a, quant, s)
+              : by_access<mx::kFp8, float>(a, quant, s);
 }
 
 }  // namespace
@@ -262,7 +290,7 @@ cudaError_t launch_mx_quant(int fmt, int64_t rows, int64_t cols, bool bf16, cons
   a.rows = (uint32_t)rows;
   a.cols = (uint32_t)cols;
   a.nkb = (uint32_t)(mx::pad128(cols) / 128);
-  a.total = (uint32_t)mx::pad128(rows) * a.nkb;
+  a.total = a.rows * a.nkb;
   a.ldx = ldx;
   a.x = const_cast<void*>(x);
   a.codes = static_cast<uint8_t*>(codes);

@@ -63,19 +63,16 @@ __device__ __forceinline__ float rcp_approx(float v) {
   return r;
 }
 
-// A row's scale and its reciprocal from its largest magnitude (NaN where a value is NaN).
-// EXACT: the correctly rounded reciprocal; else the hardware's, within an ulp, which moves
+// A row's scale from its largest magnitude (NaN where that is not finite: amax 0), and its
+// reciprocal: the correctly rounded one (EXACT), or the hardware's, within an ulp, which moves
 // only values next to a rounding border.
 template <bool EXACT>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
-  if (!(amax <= 3.402823466e38f)) {
-    s = inv = __uint_as_float(0x7fffffffu);
-  } else if (amax < kTiny) {
-    s = inv = 0.f;
-  } else {
-    s = amax * (1.f / 448.f);
-    inv = EXACT ? 1.f / s : rcp_approx(s);
-  }
+  const float t = fmaf(amax, 1.f / 448.f, amax * 0.f);
+  s = amax < kTiny ? 0.f : t;
+  const float u = fmaxf(t, 1.f / 448.f * kTiny);  // a row of zeros: finite, and codes of 0
+  inv = EXACT ? 1.f / u : rcp_approx(u);
+  if (EXACT && amax < kTiny) inv = 0.f;
 }
 
 __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {
@@ -95,24 +92,56 @@ __device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&v)[16]) {
   }
 }
 
-// Factors of one state row, each twice: a pair for the two-wide operations.
-struct RowCoef {
-  float bp[2], bc[2], cc[2], as[2];  // beta Bbar_prev, gamma Bbar, Cbar, alpha s
-};
-__device__ __forceinline__ void set2(float (&d)[2], float v) {
-  *reinterpret_cast<float2*>(d) = make_float2(v, v);
+// sin and cos of x, |x| up to about 1e5, to fp32 precision: x - k pi / 2 with pi / 2 split
+// into its nearest fp32 value and the remainder (Cody-Waite argument reduction), the Taylor
+// series on [-pi/4, pi/4] (the first terms left out are below 2e-9 and 1e-10), and the
+// quadrant's exchange and signs.  About half the instructions of sincosf, which also covers
+// every larger argument.
+__device__ __forceinline__ void sincos_reduced(float x, float* s, float* c) {
+  const float k = rintf(x * 0.636619772367581343f);  // 2 / pi
+  const int quad = (int)k;
+  float r = fmaf(-k, 1.57079637050628662f, x);   // fp32(pi / 2)
+  r = fmaf(-k, -4.37113882867379282e-08f, r);    // pi / 2 - fp32(pi / 2)
+  const float r2 = r * r;
+  float ps = fmaf(r2, 1.f / 362880.f, -1.f / 5040.f);
+  ps = fmaf(r2, ps, 1.f / 120.f);
+  ps = fmaf(r2, ps, -1.f / 6.f);
+  ps = fmaf(r2 * r, ps, r);
+  float pc = fmaf(r2, -1.f / 3628800.f, 1.f / 40320.f);
+  pc = fmaf(r2, pc, -1.f / 720.f);
+  pc = fmaf(r2, pc, 1.f / 24.f);
+  pc = fmaf(r2, pc, -0.5f);
+  pc = fmaf(r2, pc, 1.f);
+  const float a = quad & 1 ? pc : ps, b = quad & 1 ? ps : pc;
+  *s = __uint_as_float(__float_as_uint(a) ^ ((uint32_t)(quad & 2) << 30));
+  *c = __uint_as_float(__float_as_uint(b) ^ ((uint32_t)((quad + 1) & 2) << 30));
 }
+
+// Factors of the state rows, each twice (a pair for the two-wide operations): beta Bbar_prev
+// and gamma Bbar, Cbar and alpha s.  Two arrays of 16 bytes a row: the eight rows a warp
+// works on are read without bank conflicts.
+struct RowCoefs {
+  float4 in[kN], out[kN];
+  __device__ void set_prev(int n, float bp) { *reinterpret_cast<float2*>(&in[n].x) = make_float2(bp, bp); }
+  __device__ void set_new(int n, float bc) { *reinterpret_cast<float2*>(&in[n].z) = make_float2(bc, bc); }
+  __device__ void set_c(int n, float cc) { *reinterpret_cast<float2*>(&out[n].x) = make_float2(cc, cc); }
+  __device__ void set_decay(int n, float as) { *reinterpret_cast<float2*>(&out[n].z) = make_float2(as, as); }
+  __device__ void set_all(int n, float bp, float bc, float cc, float as) {
+    in[n] = make_float4(bp, bp, bc, bc);
+    out[n] = make_float4(cc, cc, as, as);
+  }
+};
 
 // N = 128, P = 64: a lane owns 16 columns (lane % 4) of a row, so a row is complete in four
 // lanes and a warp's access to eight rows is 512 contiguous bytes.
-// One row: the new values' codes and scale from the old codes; adds Cbar h to acc.
-__device__ __forceinline__ uint4 update_row(const uint4& codes, const RowCoef& f,
-                                            const uint64_t (&x2)[8], const uint64_t (&xp2)[8],
-                                            uint64_t (&acc)[8], float& s) {
-  const ulonglong2 f0 = *reinterpret_cast<const ulonglong2*>(f.bp),
-                   f1 = *reinterpret_cast<const ulonglong2*>(f.cc);
+// Sixteen values of a row: the new ones from the old codes, and their part of amax; adds
+// Cbar h to acc.
+__device__ __forceinline__ float advance(const uint4& codes, const RowCoefs& f, int n,
+                                         const uint64_t (&x2)[8], const uint64_t (&xp2)[8],
+                                         uint64_t (&acc)[8], uint64_t (&v)[8]) {
+  const ulonglong2 f0 = *reinterpret_cast<const ulonglong2*>(&f.in[n]),
+                   f1 = *reinterpret_cast<const ulonglong2*>(&f.out[n]);
   const uint32_t c4[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint64_t v[8];
   float amax = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -122,10 +151,9 @@ __device__ __forceinline__ uint4 update_row(const uint4& codes, const RowCoef& f
     const float2 u = unpack2(v[j]);
     amax = mx::max3_abs(amax, u.x, u.y);
   }
-  amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  float inv;
-  row_scale<false>(amax, s, inv);
+  return amax;
+}
+__device__ __forceinline__ uint4 to_codes(const uint64_t (&v)[8], float inv) {
   const uint64_t inv2 = pack2(inv, inv);
   uint32_t o[4];
 #pragma unroll
@@ -134,6 +162,23 @@ __device__ __forceinline__ uint4 update_row(const uint4& codes, const RowCoef& f
     o[j] = mx::pack4_e4m3(u.x, u.y, w.x, w.y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Rows n0 and n1: their new codes and scales.
+__device__ __forceinline__ void update_rows(const uint4& h0, const uint4& h1, const RowCoefs& f,
+                                            int n0, int n1, const uint64_t (&x2)[8],
+                                            const uint64_t (&xp2)[8], uint64_t (&acc)[8],
+                                            uint4& o0, uint4& o1, float& s0, float& s1) {
+  uint64_t v0[8], v1[8];
+  float m0 = advance(h0, f, n0, x2, xp2, acc, v0), m1 = advance(h1, f, n1, x2, xp2, acc, v1);
+  m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+  m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
+  m0 = max_nan(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
+  m1 = max_nan(m1, __shfl_xor_sync(0xffffffffu, m1, 2));
+  float i0, i1;
+  row_scale<false>(m0, s0, i0);
+  row_scale<false>(m1, s1, i1);
+  o0 = to_codes(v0, i0);
+  o1 = to_codes(v1, i1);
 }
 
 // Sums acc over the lanes with equal lane % 4 (the same 16 columns): each exchange halves
@@ -170,11 +215,12 @@ __device__ __forceinline__ void pairs(const float (&v)[16], uint64_t (&p)[8]) {
 template <typename T>
 __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
   constexpr int kRows = 4;  // rows a lane
-  __shared__ __align__(16) RowCoef coef[kN];
+  __shared__ RowCoefs coef;
   __shared__ float ysum[4][kP];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t bh = blockIdx.x;
-  const int64_t b = bh / a.H, h = bh % a.H, rep = a.H / a.G, g = h / rep;
+  const uint32_t H = (uint32_t)a.H, rep = H / (uint32_t)a.G, b = blockIdx.x / H;
+  const uint32_t h = blockIdx.x - b * H, g = h / rep;
   const int q = lane & 3, r0 = warp * 32 + (lane >> 2);
 
   const uint4* S = reinterpret_cast<const uint4*>(a.ssm + bh * kN * kP);
@@ -186,34 +232,34 @@ __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
   load16(xt + 16 * q, x);
   load16(a.x_prev + bh * kP + 16 * q, xp);
 
-  const T* Bt = static_cast<const T*>(a.B_t) + (b * a.G + g) * kN;
-  const T* Ct = static_cast<const T*>(a.C_t) + (b * a.G + g) * kN;
+  const T* Bt = static_cast<const T*>(a.B_t) + ((int64_t)b * a.G + g) * kN;
+  const T* Ct = static_cast<const T*>(a.C_t) + ((int64_t)b * a.G + g) * kN;
   const int i = t & 63;  // rows 2 i and 2 i + 1
   const float ang = a.angle[bh * 64 + i];
   float ph = 0.f, sn, cs;
   if (t < 64) {  // what turns with the new angle
     const float ga = a.gamma_t[bh];
     ph = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * 64 + i] : 0.f));
-    sincosf(ph, &sn, &cs);
+    sincos_reduced(ph, &sn, &cs);
     const float b0 = to_f32(Bt[2 * i]), b1 = to_f32(Bt[2 * i + 1]);
     const float2 rb = rot2(cs, sn, b0, b1);
     const float2 rc = rot2(cs, sn, to_f32(Ct[2 * i]), to_f32(Ct[2 * i + 1]));
-    set2(coef[2 * i].bc, ga * rb.x);
-    set2(coef[2 * i + 1].bc, ga * rb.y);
-    set2(coef[2 * i].cc, rc.x);
-    set2(coef[2 * i + 1].cc, rc.y);
+    coef.set_new(2 * i, ga * rb.x);
+    coef.set_new(2 * i + 1, ga * rb.y);
+    coef.set_c(2 * i, rc.x);
+    coef.set_c(2 * i + 1, rc.y);
     if (a.b_prev_out && h % rep == 0)
-      *reinterpret_cast<float2*>(a.b_prev_out + (b * a.G + g) * kN + 2 * i) = make_float2(b0, b1);
+      *reinterpret_cast<float2*>(a.b_prev_out + ((int64_t)b * a.G + g) * kN + 2 * i) = make_float2(b0, b1);
   } else {  // and with the old
     const float alpha = expf(a.logdecay_t[bh]), be = a.beta_t ? a.beta_t[bh] : 0.f;
-    const float2 bp = *reinterpret_cast<const float2*>(a.b_prev + (b * a.G + g) * kN + 2 * i);
+    const float2 bp = *reinterpret_cast<const float2*>(a.b_prev + ((int64_t)b * a.G + g) * kN + 2 * i);
     const float2 sc = *reinterpret_cast<const float2*>(a.scale + bh * kN + 2 * i);
-    sincosf(ang, &sn, &cs);
+    sincos_reduced(ang, &sn, &cs);
     const float2 rp = rot2(cs, sn, bp.x, bp.y);
-    set2(coef[2 * i].bp, be * rp.x);
-    set2(coef[2 * i + 1].bp, be * rp.y);
-    set2(coef[2 * i].as, alpha * sc.x);
-    set2(coef[2 * i + 1].as, alpha * sc.y);
+    coef.set_prev(2 * i, be * rp.x);
+    coef.set_prev(2 * i + 1, be * rp.y);
+    coef.set_decay(2 * i, alpha * sc.x);
+    coef.set_decay(2 * i + 1, alpha * sc.y);
   }
   __syncthreads();
 
@@ -222,11 +268,17 @@ __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
   pairs(xp, xp2);
   uint4* So = reinterpret_cast<uint4*>(a.ssm_out + bh * kN * kP);
 #pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int n = r0 + 8 * k;
-    float s;
-    So[n * (kP / 16) + q] = update_row(hv[k], coef[n], x2, xp2, acc, s);
-    if (q == 0) a.scale_out[bh * kN + n] = s;
+  for (int k = 0; k < kRows; k += 2) {
+    const int n0 = r0 + 8 * k, n1 = n0 + 8;
+    uint4 o0, o1;
+    float s0, s1;
+    update_rows(hv[k], hv[k + 1], coef, n0, n1, x2, xp2, acc, o0, o1, s0, s1);
+    So[n0 * (kP / 16) + q] = o0;
+    So[n1 * (kP / 16) + q] = o1;
+    if (q == 0) {
+      a.scale_out[bh * kN + n0] = s0;
+      a.scale_out[bh * kN + n1] = s1;
+    }
   }
   int col;
   const float2 y2 = sum_columns(acc, lane, col);
@@ -243,8 +295,8 @@ __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
 
 // Many (b, h): CTAs of two warps walk them; bulk copies bring the next one's parts into one
 // of two stages while a CTA works on the other, so the state is never waited for with
-// registers held, and nine CTAs an SM keep 88 KB in flight.
-constexpr int kWalkThreads = 64, kWalkCtas = 9;
+// registers held, and eight CTAs an SM (128 registers a thread) keep 78 KB in flight.
+constexpr int kWalkThreads = 64, kWalkCtas = 8;
 
 template <typename T>
 struct alignas(128) StepStage {
@@ -260,12 +312,16 @@ template <typename T>
 __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Args a) {
   constexpr int kRows = 8;  // rows a lane
   __shared__ StepStage<T> stage[2];
-  __shared__ __align__(16) RowCoef coef[kN];
+  __shared__ RowCoefs coef;
   __shared__ float ysum[2][kP];
   __shared__ uint64_t full[2];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int q = lane & 3, r0 = warp * 64 + (lane >> 2);
-  const int64_t total = a.b * a.H, rep = a.H / a.G;
+  const int64_t total = a.b * a.H;
+  // the (b, h) and group of a round go along without a division by H
+  const uint32_t H = (uint32_t)a.H, rep = H / (uint32_t)a.G;
+  const uint32_t db = gridDim.x / H, dh = gridDim.x - db * H;
+  uint32_t b = blockIdx.x / H, h = blockIdx.x - b * H;
   auto fetch = [&](int64_t bh, int st) {
     StepStage<T>& d = stage[st];
     const uint32_t bytes = sizeof(d.codes) + sizeof(d.scale) + sizeof(d.angle) + sizeof(d.xp) +
@@ -285,43 +341,65 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     tc5::fence_mbar_init();
   }
   __syncthreads();
+  // what a round reads outside its stage, loaded a round ahead
+  struct Small {
+    T b0, b1, c0, c1;
+    float2 bp;
+    float ld, be, ga;
+    int64_t at;   // of the pair's B, C and b_prev
+    bool first;   // the group's first head
+  } cur, nxt;
+  auto small = [&](int64_t bh) {
+    Small v;
+    const uint32_t g = h / rep;
+    v.at = ((int64_t)b * a.G + g) * kN + 2 * t;  // pair t: rows 2 t and 2 t + 1
+    const T* Bt = static_cast<const T*>(a.B_t) + v.at;
+    const T* Ct = static_cast<const T*>(a.C_t) + v.at;
+    v.b0 = Bt[0];
+    v.b1 = Bt[1];
+    v.c0 = Ct[0];
+    v.c1 = Ct[1];
+    v.bp = *reinterpret_cast<const float2*>(a.b_prev + v.at);
+    v.ld = a.logdecay_t[bh];
+    v.be = a.beta_t ? a.beta_t[bh] : 0.f;
+    v.ga = a.gamma_t[bh];
+    v.first = h == g * rep;
+    b += db;  // to the next round's
+    h += dh;
+    if (h >= H) {
+      h -= H;
+      ++b;
+    }
+    return v;
+  };
   int64_t bh = blockIdx.x;
   if (t == 0) fetch(bh, 0);  // the grid is no larger than the walk
+  cur = small(bh);
   for (uint32_t it = 0; bh < total; bh += gridDim.x, ++it) {
     const int st = it & 1;
     const int64_t next = bh + gridDim.x;
     // the other stage was last read before the barrier that ended the round before
     if (t == 0 && next < total) fetch(next, st ^ 1);
-    const int64_t b = bh / a.H, h = bh - b * a.H, g = h / rep;
-    const int64_t gn = (b * a.G + g) * kN + 2 * t;  // pair t: rows 2 t and 2 t + 1
-    const T* Bt = static_cast<const T*>(a.B_t) + gn;
-    const T* Ct = static_cast<const T*>(a.C_t) + gn;
-    const float b0 = to_f32(Bt[0]), b1 = to_f32(Bt[1]), c0 = to_f32(Ct[0]), c1 = to_f32(Ct[1]);
-    const float2 bp = *reinterpret_cast<const float2*>(a.b_prev + gn);
-    const float alpha = expf(a.logdecay_t[bh]);
-    const float be = a.beta_t ? a.beta_t[bh] : 0.f, ga = a.gamma_t[bh];
+    if (next < total) nxt = small(next);
+    const float b0 = to_f32(cur.b0), b1 = to_f32(cur.b1), c0 = to_f32(cur.c0), c1 = to_f32(cur.c1);
+    const float2 bp = cur.bp;
+    const float alpha = expf(cur.ld), be = cur.be, ga = cur.ga;
     const StepStage<T>& d = stage[st];
     const bool late = !tc5::mbar_wait(&full[st], (it >> 1) & 1u, kWaitLimitNs);
     {
       float sn, cs;
       const float ang = d.angle[t];
-      sincosf(ang, &sn, &cs);
+      sincos_reduced(ang, &sn, &cs);
       const float2 rp = rot2(cs, sn, bp.x, bp.y);
       const float ph = wrap_angle(ang + (a.theta_t ? d.theta[t] : 0.f));
-      sincosf(ph, &sn, &cs);
+      sincos_reduced(ph, &sn, &cs);
       const float2 rb = rot2(cs, sn, b0, b1), rc = rot2(cs, sn, c0, c1);
-      set2(coef[2 * t].bp, be * rp.x);
-      set2(coef[2 * t].bc, ga * rb.x);
-      set2(coef[2 * t].cc, rc.x);
-      set2(coef[2 * t].as, alpha * d.scale[2 * t]);
-      set2(coef[2 * t + 1].bp, be * rp.y);
-      set2(coef[2 * t + 1].bc, ga * rb.y);
-      set2(coef[2 * t + 1].cc, rc.y);
-      set2(coef[2 * t + 1].as, alpha * d.scale[2 * t + 1]);
+      coef.set_all(2 * t, be * rp.x, ga * rb.x, rc.x, alpha * d.scale[2 * t]);
+      coef.set_all(2 * t + 1, be * rp.y, ga * rb.y, rc.y, alpha * d.scale[2 * t + 1]);
       if (!late) {
         a.angle_out[bh * (kN / 2) + t] = ph;
-        if (a.b_prev_out && h - g * rep == 0)
-          *reinterpret_cast<float2*>(a.b_prev_out + gn) = make_float2(b0, b1);
+        if (a.b_prev_out && cur.first)
+          *reinterpret_cast<float2*>(a.b_prev_out + cur.at) = make_float2(b0, b1);
       }
     }
     if (tc5::bar_or(1, kWalkThreads, late)) {  // the copies in flight land before the CTA ends
@@ -343,12 +421,20 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     const float xv = to_f32(d.x[t]);
     const uint4* S = reinterpret_cast<const uint4*>(d.codes);
     uint4* So = reinterpret_cast<uint4*>(a.ssm_out + bh * kN * kP);
+    // two rows at a time: their chains of conversions, maxima and exchanges overlap
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int n = r0 + 8 * k;
-      float s;
-      So[n * (kP / 16) + q] = update_row(S[n * (kP / 16) + q], coef[n], x2, xp2, acc, s);
-      if (q == 0) a.scale_out[bh * kN + n] = s;
+    for (int k = 0; k < kRows; k += 2) {
+      const int n0 = r0 + 8 * k, n1 = n0 + 8;
+      const uint4 h0 = S[n0 * (kP / 16) + q], h1 = S[n1 * (kP / 16) + q];
+      uint4 o0, o1;
+      float s0, s1;
+      update_rows(h0, h1, coef, n0, n1, x2, xp2, acc, o0, o1, s0, s1);
+      So[n0 * (kP / 16) + q] = o0;
+      So[n1 * (kP / 16) + q] = o1;
+      if (q == 0) {
+        a.scale_out[bh * kN + n0] = s0;
+        a.scale_out[bh * kN + n1] = s1;
+      }
     }
     int col;
     const float2 y2 = sum_columns(acc, lane, col);
@@ -358,6 +444,7 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     if (a.D) y = fmaf(a.D[h], xv, y);
     static_cast<T*>(a.y_t)[bh * kP + t] = from_f32<T>(y);
     a.x_prev_out[bh * kP + t] = xv;
+    cur = nxt;
   }
 }
 
