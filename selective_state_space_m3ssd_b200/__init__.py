@@ -728,12 +728,17 @@ def _mx_format(fmt) -> int:
     return _MX_FORMATS[fmt]
 
 
+def _mx_of(t: MXTensor) -> Mx:
+    return Mx(_MX_FORMATS[t.fmt], 0, t.rows, t.cols, t.codes.data_ptr(), t.scales.data_ptr())
+
+
 def _mx_struct(t: MXTensor, name: str, device) -> Mx:
+    """The C descriptor of a caller's tensor, its storage checked."""
     import torch
     f, kp = _mx_format(t.fmt), _pad128(t.cols)
     _need(t.codes, name + ".codes", torch.uint8, (t.rows, kp if f == MXFP8 else kp // 2), device)
     _need(t.scales, name + ".scales", torch.uint8, (_pad128(t.rows) * (kp // 32),), device)
-    return Mx(f, 0, t.rows, t.cols, t.codes.data_ptr(), t.scales.data_ptr())
+    return _mx_of(t)
 
 
 def _rows_stride(x, name):
@@ -755,9 +760,11 @@ def mx_quant(x, fmt: str, *, out: MXTensor | None = None) -> MXTensor:
     rows, cols = x.shape
     if out is None:
         out = MXTensor.empty(fmt, rows, cols, x.device)
+        o = _mx_of(out)
     elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
         raise ValueError(f"out must be {fmt} of {rows} x {cols}")
-    o = _mx_struct(out, "out", x.device)
+    else:
+        o = _mx_struct(out, "out", x.device)
     _launch("m3ssd_mx_quant", x.device, ctypes.byref(o), _xdtype(x), _addr(x), ldx)
     return out
 
@@ -768,9 +775,10 @@ def mx_dequant(t: MXTensor, dtype=None, *, out=None):
     import torch
     dev = t.codes.device
     if out is None:
-        out = torch.empty(t.rows, t.cols, dtype=dtype or torch.bfloat16, device=dev)
-    _need_shape(out, "out", dtype, (t.rows, t.cols))
-    ldx = _rows_stride(out, "out")
+        out, ldx = torch.empty(t.rows, t.cols, dtype=dtype or torch.bfloat16, device=dev), t.cols
+    else:
+        _need_shape(out, "out", dtype, (t.rows, t.cols))
+        ldx = _rows_stride(out, "out")
     m = _mx_struct(t, "t", out.device)
     _launch("m3ssd_mx_dequant", dev, ctypes.byref(m), _xdtype(out), _addr(out), ldx)
     return out
@@ -782,9 +790,10 @@ def gemm_mx(A: MXTensor, W: MXTensor, *, out=None):
     import torch
     dev = A.codes.device
     if out is None:
-        out = torch.empty(A.rows, W.rows, dtype=torch.bfloat16, device=dev)
-    _need_shape(out, "out", torch.bfloat16, (A.rows, W.rows))
-    ldd = _rows_stride(out, "out")
+        out, ldd = torch.empty(A.rows, W.rows, dtype=torch.bfloat16, device=dev), W.rows
+    else:
+        _need_shape(out, "out", torch.bfloat16, (A.rows, W.rows))
+        ldd = _rows_stride(out, "out")
     a, w = _mx_struct(A, "A", out.device), _mx_struct(W, "W", out.device)
     _launch("m3ssd_gemm_mx", dev, ctypes.byref(a), ctypes.byref(w), _addr(out), ldd)
     return out
@@ -812,18 +821,21 @@ def add_rmsnorm(x, w, *, residual=None, eps: float = 1e-6, fmt: str | None = Non
         _need(residual, "residual", None, x.shape, dev)
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        _need(residual_out, "residual_out", residual.dtype, x.shape, dev)
+        else:
+            _need(residual_out, "residual_out", residual.dtype, x.shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out is only written with a residual")
     mx = None
-    if fmt is None:
-        y = torch.empty_like(x) if y is None else y
+    if fmt is None and y is None:
+        y = torch.empty_like(x)
+    elif fmt is None:
         _need(y, "y", x.dtype, x.shape, dev)
+    elif y is None:
+        y = MXTensor.empty(fmt, rows, d, dev)
+        mx = _mx_of(y)
+    elif (y.fmt, y.rows, y.cols) != (fmt, rows, d):
+        raise ValueError(f"y must be {fmt} of {rows} x {d}")
     else:
-        if y is None:
-            y = MXTensor.empty(fmt, rows, d, dev)
-        elif (y.fmt, y.rows, y.cols) != (fmt, rows, d):
-            raise ValueError(f"y must be {fmt} of {rows} x {d}")
         mx = _mx_struct(y, "y", dev)
     rstd = torch.empty(rows, dtype=f32, device=dev) if want_rstd else None
     dims = NormDims(rows, d, xd, rd, eps, 0)
@@ -852,13 +864,20 @@ def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=No
     _need(w, "w", f32, (d,), dev)
     _need(rstd, "rstd", f32, (rows,), dev)
     _need(dres, "dres", f32, dy.shape, dev)
-    dr = torch.empty(dy.shape, dtype=f32, device=dev) if dr is None else dr
-    dw = torch.empty(d, dtype=f32, device=dev) if dw is None else dw
-    _need(dr, "dr", f32, dy.shape, dev)
-    _need(dw, "dw", f32, (d,), dev)
+    if dr is None:
+        dr = torch.empty(dy.shape, dtype=f32, device=dev)
+    else:
+        _need(dr, "dr", f32, dy.shape, dev)
+    if dw is None:
+        dw = torch.empty(d, dtype=f32, device=dev)
+    else:
+        _need(dw, "dw", f32, (d,), dev)
     dims = NormDims(rows, d, _xdtype(dy), _xdtype(r), 0.0, 0)
-    with torch.cuda.device(dev):
+    if torch.cuda.current_device() == dev.index:
         need = add_rmsnorm_bwd_workspace_size(dims)
+    else:
+        with torch.cuda.device(dev):
+            need = add_rmsnorm_bwd_workspace_size(dims)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _launch("m3ssd_add_rmsnorm_bwd", dev, ctypes.byref(dims), _addr(dy), _addr(r), _addr(w),
@@ -958,7 +977,8 @@ def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=Non
         _cache_q8_struct(cache_out, b, H, P, N, G, dev, "cache_out")
     if y_t is None:
         y_t = torch.empty_like(x_t)
-    _need(y_t, "y_t", xd, (b, H, P), dev)
+    else:
+        _need(y_t, "y_t", xd, (b, H, P), dev)
     dims = make_dims(b, 1, H, P, N, G, _xdtype(x_t), 0, CHECK_FINITE if check_finite else 0)
     _launch("m3ssd_step_q8", dev, ctypes.byref(dims), _addr(x_t), _addr(logdecay_t), _addr(beta_t),
             _addr(gamma_t), _addr(B_t), _addr(C_t), _addr(theta_t), _addr(D), ctypes.byref(ci),
