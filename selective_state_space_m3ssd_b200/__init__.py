@@ -687,6 +687,15 @@ def _launch(name: str, dev, *args):
         _check(st, name)
 
 
+def _need_all(dev, *checks):
+    """:func:`_need` for (tensor, name, dtype, shape) on the CUDA device ``dev``, in one
+    loop: a decode step checks some twenty tensors."""
+    for t, name, dtype, shape in checks:
+        if t is not None and (t.dtype != dtype or t.shape != shape or t.device != dev or
+                              not t.is_contiguous()):
+            _need(t, name, dtype, shape, dev)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -860,10 +869,8 @@ def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=No
     d = dy.shape[-1]
     rows = dy.numel() // d if d else 0
     _need(dy, "dy", device=dev)
-    _need(r, "r", None, dy.shape, dev)
-    _need(w, "w", f32, (d,), dev)
-    _need(rstd, "rstd", f32, (rows,), dev)
-    _need(dres, "dres", f32, dy.shape, dev)
+    _need_all(dev, (r, "r", r.dtype, dy.shape), (w, "w", f32, (d,)),
+              (rstd, "rstd", f32, (rows,)), (dres, "dres", f32, dy.shape))
     if dr is None:
         dr = torch.empty(dy.shape, dtype=f32, device=dev)
     else:
@@ -947,12 +954,13 @@ def dequant_cache(cache: dict) -> dict:
 def _cache_q8_struct(c, b, H, P, N, G, dev, name):
     import torch
     f32 = torch.float32
-    _need(c["angle"], name + ".angle", f32, (b, H, N // 2), dev)
-    _need(c["ssm"], name + ".ssm", torch.uint8, (b, H, N, P), dev)
-    _need(c["scale"], name + ".scale", f32, (b, H, N), dev)
-    _need(c["x_prev"], name + ".x_prev", f32, (b, H, P), dev)
-    _need(c["b_prev"], name + ".b_prev", f32, (b, G, N), dev)
-    return CacheQ8(*(c[k].data_ptr() for k in ("angle", "ssm", "scale", "x_prev", "b_prev")))
+    angle, ssm, scale, xp, bp = c["angle"], c["ssm"], c["scale"], c["x_prev"], c["b_prev"]
+    _need_all(dev, (angle, name + ".angle", f32, (b, H, N // 2)),
+              (ssm, name + ".ssm", torch.uint8, (b, H, N, P)),
+              (scale, name + ".scale", f32, (b, H, N)), (xp, name + ".x_prev", f32, (b, H, P)),
+              (bp, name + ".b_prev", f32, (b, G, N)))
+    return CacheQ8(angle.data_ptr(), ssm.data_ptr(), scale.data_ptr(), xp.data_ptr(),
+                   bp.data_ptr())
 
 
 def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=None, D=None, *,
@@ -965,13 +973,10 @@ def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=Non
     G, N = B_t.shape[1], B_t.shape[2]
     dev, f32, xd = x_t.device, torch.float32, x_t.dtype
     _need(x_t, "x_t", device=dev)
-    _need(logdecay_t, "logdecay_t", f32, (b, H), dev)
-    _need(beta_t, "beta_t", f32, (b, H), dev)
-    _need(gamma_t, "gamma_t", f32, (b, H), dev)
-    _need(B_t, "B_t", xd, (b, G, N), dev)
-    _need(C_t, "C_t", xd, (b, G, N), dev)
-    _need(theta_t, "theta_t", f32, (b, H, N // 2), dev)
-    _need(D, "D", f32, (H,), dev)
+    _need_all(dev, (logdecay_t, "logdecay_t", f32, (b, H)), (beta_t, "beta_t", f32, (b, H)),
+              (gamma_t, "gamma_t", f32, (b, H)), (B_t, "B_t", xd, (b, G, N)),
+              (C_t, "C_t", xd, (b, G, N)), (theta_t, "theta_t", f32, (b, H, N // 2)),
+              (D, "D", f32, (H,)))
     ci = _cache_q8_struct(cache, b, H, P, N, G, dev, "cache")
     co = None if cache_out is None else \
         _cache_q8_struct(cache_out, b, H, P, N, G, dev, "cache_out")
