@@ -770,7 +770,7 @@ def mx_quant(x, fmt: str, *, out: MXTensor | None = None) -> MXTensor:
     if out is None:
         out = MXTensor.empty(fmt, rows, cols, x.device)
         o = _mx_of(out)
-    elif (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
+    elif not isinstance(out, MXTensor) or (out.fmt, out.rows, out.cols) != (fmt, rows, cols):
         raise ValueError(f"out must be {fmt} of {rows} x {cols}")
     else:
         o = _mx_struct(out, "out", x.device)
@@ -842,7 +842,7 @@ def add_rmsnorm(x, w, *, residual=None, eps: float = 1e-6, fmt: str | None = Non
     elif y is None:
         y = MXTensor.empty(fmt, rows, d, dev)
         mx = _mx_of(y)
-    elif (y.fmt, y.rows, y.cols) != (fmt, rows, d):
+    elif not isinstance(y, MXTensor) or (y.fmt, y.rows, y.cols) != (fmt, rows, d):
         raise ValueError(f"y must be {fmt} of {rows} x {d}")
     else:
         mx = _mx_struct(y, "y", dev)

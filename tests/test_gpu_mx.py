@@ -116,7 +116,11 @@ def check(D, A, W, rows=None):
 
 SHAPES = [(1, 8, 32), (1, 1, 1), (5, 24, 100), (16, 128, 128), (16, 300, 1024), (17, 129, 257),
           (33, 520, 384), (64, 200, 640), (65, 64, 96), (127, 255, 64), (128, 256, 512),
-          (129, 257, 1032), (300, 520, 200), (1000, 808, 768)]
+          (129, 257, 1032), (300, 520, 200), (1000, 808, 768),
+          # every tile the host chooses from, aligned and ragged: 128 x 192 (two), 128 x 256,
+          # 256 x 192 (128 x 128 above)
+          (300, 6464, 160), (299, 6463, 96), (4096, 1024, 160), (4001, 1001, 224),
+          (3001, 2000, 160), (2000, 3001, 96)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
