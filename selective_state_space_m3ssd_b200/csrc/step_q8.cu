@@ -11,10 +11,14 @@
 // y from the unrounded h, and h rounded once as it is written.
 //
 // Bytes set the pace of the fp32 step; at a quarter of them (2 N P + 8 N a (b, h)) the
-// instructions a value takes come close to the time HBM takes, so the kernel keeps them
-// few: conversions two values at a time, multiply-adds two fp32 values at a time (f32x2),
-// one 16-byte shared-memory load a row for the row's four factors, and a sum of y whose
-// exchanges are a thirtieth of the work.
+// instructions a value takes cost as much as HBM does, so the kernel keeps them few:
+// conversions two values at a time, multiply-adds two fp32 values at a time (f32x2), two
+// 16-byte shared-memory loads for a row's four factors, a sum of y whose exchanges are a
+// thirtieth of the work.  At b256 H32 N128 P64 on one B200: 35 us against 24 for the bytes at
+// the copy rate (the fp32 step takes 87); HBM runs at 47 % and the schedulers issue in 52 % of
+// the cycles (a two-wide operation takes two of them), four warps a scheduler.  Without the
+// decoding, the encoding or the maxima it took 1 to 2 us less, without its stores 4, with
+// 7 or 9 CTAs an SM 39 and 38 us: no one part bounds it.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -211,7 +215,7 @@ __device__ __forceinline__ void pairs(const float (&v)[16], uint64_t (&p)[8]) {
 }
 
 // Few (b, h): a CTA of four warps each, everything loaded at once, the rotations a thread a
-// pair and angle.
+// pair and angle.  2.6 us at 72 (b, h) in a graph, where a launch that does nothing takes 2.
 template <typename T>
 __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
   constexpr int kRows = 4;  // rows a lane
@@ -299,6 +303,10 @@ __global__ void __launch_bounds__(128) step_q8_one(StepQ8Args a) {
 constexpr int kWalkThreads = 64, kWalkCtas = 8;
 
 template <typename T>
+struct alignas(2 * sizeof(T)) Pair {
+  T a, b;
+};
+template <typename T>
 struct alignas(128) StepStage {
   uint8_t codes[kN * kP];
   float scale[kN];
@@ -343,26 +351,23 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
   __syncthreads();
   // what a round reads outside its stage, loaded a round ahead
   struct Small {
-    T b0, b1, c0, c1;
+    Pair<T> B, C;
     float2 bp;
-    float ld, be, ga;
+    float ld, be, ga, D;
     int64_t at;   // of the pair's B, C and b_prev
     bool first;   // the group's first head
   } cur, nxt;
   auto small = [&](int64_t bh) {
     Small v;
-    const uint32_t g = h / rep;
+    const uint32_t g = a.G == 1 ? 0u : h / rep;
     v.at = ((int64_t)b * a.G + g) * kN + 2 * t;  // pair t: rows 2 t and 2 t + 1
-    const T* Bt = static_cast<const T*>(a.B_t) + v.at;
-    const T* Ct = static_cast<const T*>(a.C_t) + v.at;
-    v.b0 = Bt[0];
-    v.b1 = Bt[1];
-    v.c0 = Ct[0];
-    v.c1 = Ct[1];
+    v.B = *reinterpret_cast<const Pair<T>*>(static_cast<const T*>(a.B_t) + v.at);
+    v.C = *reinterpret_cast<const Pair<T>*>(static_cast<const T*>(a.C_t) + v.at);
     v.bp = *reinterpret_cast<const float2*>(a.b_prev + v.at);
     v.ld = a.logdecay_t[bh];
     v.be = a.beta_t ? a.beta_t[bh] : 0.f;
     v.ga = a.gamma_t[bh];
+    v.D = a.D ? a.D[h] : 0.f;
     v.first = h == g * rep;
     b += db;  // to the next round's
     h += dh;
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     // the other stage was last read before the barrier that ended the round before
     if (t == 0 && next < total) fetch(next, st ^ 1);
     if (next < total) nxt = small(next);
-    const float b0 = to_f32(cur.b0), b1 = to_f32(cur.b1), c0 = to_f32(cur.c0), c1 = to_f32(cur.c1);
+    const float b0 = to_f32(cur.B.a), b1 = to_f32(cur.B.b), c0 = to_f32(cur.C.a), c1 = to_f32(cur.C.b);
     const float2 bp = cur.bp;
     const float alpha = expf(cur.ld), be = cur.be, ga = cur.ga;
     const StepStage<T>& d = stage[st];
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     *reinterpret_cast<float2*>(&ysum[warp][col]) = y2;
     __syncthreads();
     float y = ysum[0][t] + ysum[1][t];
-    if (a.D) y = fmaf(a.D[h], xv, y);
+    if (a.D) y = fmaf(cur.D, xv, y);
     static_cast<T*>(a.y_t)[bh * kP + t] = from_f32<T>(y);
     a.x_prev_out[bh * kP + t] = xv;
     cur = nxt;
@@ -552,10 +557,12 @@ cudaError_t launch_step_t(StepQ8Args a, cudaStream_t s) {
                         reinterpret_cast<uintptr_t>(a.x_t) | reinterpret_cast<uintptr_t>(a.x_prev) |
                         reinterpret_cast<uintptr_t>(a.scale) | reinterpret_cast<uintptr_t>(a.angle) |
                         reinterpret_cast<uintptr_t>(a.theta_t) | reinterpret_cast<uintptr_t>(a.b_prev) |
+                        reinterpret_cast<uintptr_t>(a.B_t) | reinterpret_cast<uintptr_t>(a.C_t) |
                         reinterpret_cast<uintptr_t>(bprev);
   if (a.N == kN && a.P == kP && all % 16 == 0) {
     const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
     const int64_t walkers = sms * kWalkCtas;
+    // up to two CTAs of four warps an SM run at once; more (b, h) than that are walked
     if (nbh <= 2 * sms)
       step_q8_one<T><<<(unsigned)nbh, 128, 0, s>>>(a);
     else
