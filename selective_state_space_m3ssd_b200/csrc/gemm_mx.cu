@@ -42,7 +42,7 @@
 
 #include "internal.h"
 #include "mx.cuh"
-#include "tc5.cuh"
+#include "tc5_mx.cuh"
 
 namespace m3ssd {
 

@@ -52,54 +52,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-// ---- block-scaled products (microscaled operands) ------------------------------------
-// Instruction descriptor of kind::mxf4 and kind::mxf8f6f4 with fp32 accumulation, both
-// operands K-major: A / B format (bits 7-9 and 10-12; mxf4: 1 = E2M1; mxf8f6f4: 0 = E4M3,
-// 5 = E2M1), N >> 3 (bits 17-22), scale format (bit 23: 1 = UE8M0), M >> 7 (bits 27-28).
-// The scale-factor ids (which byte of a 32-bit scale column a product reads: bits 4-5 for
-// B, 29-30 for A) are ORed in by idesc_mx_sf.
-__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t a_fmt, uint32_t b_fmt) {
-  return (a_fmt << 7) | (b_fmt << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 7) << 27);
-}
-__host__ __device__ constexpr uint32_t idesc_mx_sf(uint32_t idesc, uint32_t id) {
-  return idesc | (id << 4) | (id << 29);
-}
-
-// D[tmem] (+)= (A . scales) * (B . scales): 64 E2M1 values of K, two UE8M0 scales a row.
-__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
-      "p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u));
-}
-// The same for 8-bit containers: 32 values of K, one UE8M0 scale a row.
-__device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                             bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u));
-}
-
-// Shared-memory descriptor without swizzle of 32 rows of 16 bytes, 8-row groups 128 bytes
-// apart (one 512-byte tile of scales).
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(16 >> 4) << 16) |
-         ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-// One tile of scales (128 rows x 4 blocks) into four TMEM columns, repeated for the four
-// lane quarters.  In order with the products this thread issues afterwards.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
-}
-
 // The mbarrier completes one arrival when every tcgen05 operation this thread
 // issued before has finished.
 __device__ __forceinline__ void commit(uint64_t* mbar) {
