@@ -529,7 +529,8 @@ m3ssd_status m3ssd_dequant_state(const m3ssd_dims* dims, const void* codes, cons
  * state before it is rounded, and the state is rounded once as it is written.  The new
  * cache goes to cache_out, which may be another cache (the old one stays, for a rollback)
  * or NULL or the same (in place); its buffers equal the cache's or do not overlap them.
- * Arguments, limits and flags as m3ssd_step.
+ * Arguments, limits and flags as m3ssd_step; angles and theta up to about 1e5 in magnitude
+ * (the library's own are reduced).  One launch, or two where b_prev is written in place.
  * Capture-safe (no allocation, no sync).
  */
 m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float* logdecay_t,
@@ -539,10 +540,10 @@ m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float*
                            void* stream);
 
 /* Number of bounded device-side waits of the chunked forwards (SISO and
- * MIMO), the tensor-core backward and the GEMMs that ran out since
- * the last call (a forward's CTA then stops and leaves its outputs unwritten;
- * the backward's and the GEMMs' CTAs skip their remaining waits and leave their
- * outputs undefined); the count is then reset.  This call synchronises the current device
+ * MIMO), the tensor-core backward, the GEMMs and the 8-bit step that ran out since
+ * the last call (a forward's and a step's CTA then stops and leaves its
+ * outputs unwritten; the backward's and the GEMMs' CTAs skip their remaining waits and
+ * leave their outputs undefined); the count is then reset.  This call synchronises the current device
  * and must not be captured in a CUDA graph.  Returns M3SSD_ERR_INVALID_ARG for
  * a NULL pointer and M3SSD_ERR_CUDA if the device cannot be read. */
 m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count);

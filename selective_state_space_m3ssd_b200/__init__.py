@@ -6,6 +6,11 @@ runs in the library's CUDA kernels.  Importing this package does not load the
 library; the first call does, and raises ``LibraryMissing`` if it has not been
 built (``python -m selective_state_space_m3ssd_b200.build``).  There is no
 other implementation behind these functions.
+
+Beside the scan, its step and its block: the residual addition and RMS norm
+(:func:`add_rmsnorm`), microscaled tensors and their product (:func:`mx_quant`,
+:func:`gemm_mx`) and the decode step on a cache held in 8 bits (:func:`quant_cache`,
+:func:`step_q8`).
 """
 from __future__ import annotations
 
