@@ -476,7 +476,7 @@ m3ssd_status m3ssd_gemm_mx(const m3ssd_mx* A, const m3ssd_mx* W, void* D, int64_
 /*
  * Forward of the residual addition and norm.  residual and residual_out are given together
  * or not at all; residual_out may be residual.  Exactly one of y (rows x width, x_dtype; may
- * be x) and y_mx (an MX tensor of rows x width, the A operand of m3ssd_gemm_mx) is given.
+ * be x, not residual_out) and y_mx (an MX tensor of rows x width, the A operand of m3ssd_gemm_mx) is given.
  * rstd (rows), for the backward, may be NULL.  x, y, residual: dense rows.
  */
 m3ssd_status m3ssd_add_rmsnorm(const m3ssd_norm_dims* dims, const void* x, const void* residual,

@@ -134,6 +134,7 @@ m3ssd_status m3ssd_add_rmsnorm(const m3ssd_norm_dims* dims, const void* x, const
   if (st != M3SSD_OK) return st;
   if ((y != nullptr) == (y_mx != nullptr) && (dims->rows > 0 || y)) return M3SSD_ERR_INVALID_ARG;
   if ((residual != nullptr) != (residual_out != nullptr)) return M3SSD_ERR_INVALID_ARG;
+  if (y && y == residual_out) return M3SSD_ERR_INVALID_ARG;
   m3ssd::NormArgs a{};
   a.fmt = -1;
   if (y_mx) {

@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     }
     if (tc5::bar_or(1, kWalkThreads, late)) {  // the copies in flight land before the CTA ends
       if (t == 0) {
+        (void)tc5::mbar_wait(&full[st], (it >> 1) & 1u, kWaitLimitNs);
         if (next < total)
           (void)tc5::mbar_wait(&full[st ^ 1], ((it + 1) >> 1) & 1u, kWaitLimitNs);
         atomicAdd(&g_step_q8_wait_timeouts, 1u);

@@ -60,7 +60,8 @@ def test_forward(rows, d, dtype, res):
     assert np.all(np.abs(np64(y) - ref) <= tol * np.abs(ref) + 1e-38)
 
 
-@pytest.mark.parametrize("rows,d", SHAPES)
+# more rows than walkers at the end, unaligned and aligned
+@pytest.mark.parametrize("rows,d", SHAPES + [(9001, 100), (2501, 512)])
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("dtype,res", [(BF16, F32), (F32, None)])
 def test_quantised_output(rows, d, fmt, dtype, res):

@@ -214,3 +214,38 @@ def test_empty_batch():
     y = m3.step_q8(c, z(0, 2, 64), z(0, 2), None, z(0, 2), z(0, 1, 128), z(0, 1, 128))
     assert y.shape == (0, 2, 64)
     assert m3.quant_state(z(0, 2, 128, 64))[0].shape == (0, 2, 128, 64)
+
+
+def test_two_steps_at_once():
+    """Two batches on two streams at the same time, each as it is alone (a walk and a small
+    launch share nothing)."""
+    made = [make(40, 24, 1, 128, 64, "f32", seed=21), make(3, 4, 2, 128, 64, "f32", seed=22)]
+    dev = [(to_cuda(s), to_cuda(c)) for s, c in made]
+    alone = []
+    for s, c in dev:
+        out = {k: torch.empty_like(v) for k, v in c.items()}
+        alone.append((m3.step_q8(c, *[s[k] for k in ORDER], cache_out=out), out))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    both = []
+    for st, (s, c) in zip(streams, dev):
+        with torch.cuda.stream(st):
+            out = {k: torch.empty_like(v) for k, v in c.items()}
+            both.append([(m3.step_q8(c, *[s[k] for k in ORDER], cache_out=out), out)
+                         for _ in range(5)])
+    torch.cuda.synchronize()
+    for (y, out), runs in zip(alone, both):
+        for y2, out2 in runs:
+            assert torch.equal(y, y2) and all(torch.equal(out[k], out2[k]) for k in out)
+
+
+def test_large_batch_of_states():
+    """More (b, h) than the walkers take in a few rounds; sampled against the oracle."""
+    b, H = 300, 32
+    step, cache = make(b, H, 2, 128, 64, "f32", seed=31)
+    sd, cd = to_cuda(step), to_cuda(cache)
+    y = m3.step_q8(cd, *[sd[k] for k in ORDER])
+    rows = [0, 1, 149, 298, 299]
+    cut = lambda v, d: None if v is None else (v if d == "D" else v[rows])  # noqa: E731
+    check({k: cut(v, k) for k, v in step.items()}, {k: v[rows] for k, v in cache.items()}, y[rows],
+          {k: v[rows] for k, v in cd.items()}, False)

@@ -80,6 +80,7 @@ def test_norm_arguments(lib):
     assert f(n, PA, PA, PA, PA, None, None, None, None) == BAD              # residual alone
     assert f(n, PA, None, PA, PA, None, PA, None, None) == BAD              # residual_out alone
     assert f(n, None, None, PA, PA, None, None, None, None) == BAD
+    assert f(n, PA, PA, PA, ctypes.c_void_p(B), None, ctypes.c_void_p(B), None, None) == BAD  # y = r
     assert f(n, PA, None, None, PA, None, None, None, None) == BAD
     assert f(n, PA, None, PA, None, r(mx(rows=5)), None, None, None) == BAD
     assert f(n, PA, None, PA, None, r(mx(cols=65)), None, None, None) == BAD
