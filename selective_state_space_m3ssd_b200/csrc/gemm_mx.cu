@@ -7,59 +7,48 @@
 // kind::mxf4 (A in 4 bits) or kind::mxf8f6f4 (A in 8 bits; TMA spreads the packed 4-bit
 // codes of W over 8-bit containers as it loads them) multiplies value times scale.
 //
-// The operand with 128 H rows a tile ("rows") is A, or W for few tokens (SWAP): then the
-// tokens are the product's narrow side, no more of them than the tile is wide, and W's
-// rows fill the 128 lanes.  One persistent CTA per SM; warp 0 copies, warp 1 issues the
-// scale copies and the products, four warps a half are the epilogue.  The accumulators
-// alternate where two fit beside the scales in TMEM; with one, the epilogue's first step,
-// the whole row into registers as bf16, is all the products wait for.  Every stage of the
-// ring has its own TMEM columns for its scales: they are free when the stage is (the products
-// that read them have finished), so a copy never overtakes a product.  A 192-column tile may
-// start in the middle of a scale tile: its products read the columns from there on.
+// A tile is 128 H rows of A by BN of W.  One persistent CTA per SM; warp 0 copies, warp 1
+// issues the scale copies and the products, four warps a half are the epilogue.  The
+// accumulators alternate where two fit beside the scales in TMEM; with one, the epilogue's
+// first step, the whole row into registers as bf16, is all the products wait for.  Every stage
+// of the ring has its own TMEM columns for its scales: they are free when the stage is (the
+// products that read them have finished), so a copy never overtakes a product.  A 192-column
+// tile may start in the middle of a scale tile: its products read the columns from there on.
+// Few tokens, or few tiles with a long K, go to gemm_mx_split.cu.
 // Output blocks of 32 x 64 leave by TMA from a swizzled staging buffer (a thread holds a row:
 // stores straight from the registers touch 32 lines each), or, where the rows of D are not
 // multiples of 16 bytes, row by row from the same buffer.
 //
+// The two warps stay converged and one elected lane issues: in a branch of one lane the
+// compiler cannot keep descriptors and addresses in uniform registers, and the issue of a
+// stage was what bounded the products (8192^3 in 4 bits 241 us against 191, 32768 x 6464 x
+// 1024 131 against 120).
+//
 // What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
-// writes at HBM's 3.9 TB/s of them, 131 taken); with a long K shared memory, which feeds the
-// products (107 bytes a cycle at 256 x 192) while the stages come in (75), and the scale
-// copies, which hold up the products for about 55 cycles each (eight a stage of 768 cycles of
-// products).  Measured and not kept: the copies of a stage ahead of the products of the one
-// before (5 % slower); the scales written to TMEM by four more warps (8192^3 in 4 bits 226 us
-// against 241, 8-bit A 10 to 20 % slower); row blocks that stay in shared memory (K up to
-// 1024; 133 to 149 us against 136); CTA pairs (256 x 256 a pair: 169 and 279 us against 131
-// and 241, twice the copies a product).
+// writes at HBM's 3.9 TB/s of them, 120 taken); with a long K shared memory, which feeds the
+// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
 #include <cstddef>
 #include <cstring>
 
+#include "gemm_mx.cuh"
 #include "internal.h"
-#include "mx.cuh"
-#include "tc5_mx.cuh"
 
 namespace m3ssd {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 __device__ unsigned int g_gemm_mx_wait_timeouts;
 
 namespace {
 
-constexpr int BM = 128;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint32_t kTile = 512;           // bytes of a scale tile (128 rows x 4 blocks)
+using namespace gemm_mx;
+
 constexpr uint32_t kStgBytes = 32 * 128;  // an output block: 32 rows x 64 bf16 columns
 
 // AF: A's format.  H: 128-row halves of a tile.  A stage is 128 bytes of K a row: 256 values
 // in 4 bits, 128 in 8.
-template <int AF, int H, int BN, bool SWAP>
+template <int AF, int H, int BN>
 struct Cfg {
   static constexpr int ATOMS = AF == mx::kFp4 ? 2 : 1;  // scale tiles along K a stage
   static constexpr int NSB = (BN + 127) / 128;          // scale tiles along the columns
@@ -67,15 +56,15 @@ struct Cfg {
   static constexpr uint32_t R_BYTES = H * BM * 128, C_BYTES = BN * 128;
   // bytes the copies of a stage count on its barrier: W's 4-bit codes count as they are in
   // global memory, whether or not they are spread
-  static constexpr uint32_t R_TX = (AF != mx::kFp4 && SWAP) ? R_BYTES / 2 : R_BYTES;
-  static constexpr uint32_t C_TX = (AF != mx::kFp4 && !SWAP) ? C_BYTES / 2 : C_BYTES;
+  static constexpr uint32_t R_TX = R_BYTES;
+  static constexpr uint32_t C_TX = AF != mx::kFp4 ? C_BYTES / 2 : C_BYTES;
   static constexpr uint32_t SR_BYTES = H * ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
   static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
-  static constexpr int NSTG = SWAP ? 0 : (H == 1 ? 2 : 1);  // output blocks of an epilogue warp
+  static constexpr int NSTG = H == 1 ? 2 : 1;  // output blocks of an epilogue warp
   static constexpr int ROOM = 226 * 1024 - EPI_WARPS * NSTG * (int)kStgBytes - 1024;
   static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
   static constexpr int SF_COLS = ATOMS * 4 * (H + NSB);     // TMEM columns of a stage's scales
-  static constexpr int ACC_COLS = H * (BN < 32 ? 32 : BN);  // an accumulator, its halves side by side
+  static constexpr int ACC_COLS = H * BN;  // an accumulator, its halves side by side
   // two accumulators, where they fit, alternate between the products and the epilogue
   static constexpr int NACC = 2 * ACC_COLS + STAGES * SF_COLS <= 512 ? 2 : 1;
   static constexpr int COLS = NACC * ACC_COLS + STAGES * SF_COLS;
@@ -84,7 +73,7 @@ struct Cfg {
   // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
   // E4M3 = 0, E2M1 = 5)
   static constexpr uint32_t FA = AF == mx::kFp4 ? 1 : 0, FW = AF == mx::kFp4 ? 1 : 5;
-  static constexpr uint32_t IDESC = tc5::idesc_mx(BM, BN, SWAP ? FW : FA, SWAP ? FA : FW);
+  static constexpr uint32_t IDESC = tc5::idesc_mx(BM, BN, FA, FW);
 };
 
 template <typename C>
@@ -92,7 +81,7 @@ struct Smem {
   // every buffer a TMA copy reads or writes starts on a 1024-byte boundary
   uint8_t r[C::STAGES][C::R_BYTES];
   uint8_t c[C::STAGES][C::C_BYTES];
-  uint8_t stg[C::NSTG ? C::EPI_WARPS * C::NSTG : 1][C::NSTG ? kStgBytes : 1024];
+  uint8_t stg[C::EPI_WARPS * C::NSTG][kStgBytes];
   uint8_t sr[C::STAGES][C::SR_BYTES];
   uint8_t sc[C::STAGES][C::SC_BYTES];
   uint64_t full[C::STAGES];
@@ -121,20 +110,15 @@ struct MArgs {
   bool vec;
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-template <int AF, int H, int BN, bool SWAP>
-__global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
+template <int AF, int H, int BN>
+__global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     gemm_mx_kernel(MArgs g, const __grid_constant__ MMaps tm) {
-  using C = Cfg<AF, H, BN, SWAP>;
+  using C = Cfg<AF, H, BN>;
   constexpr int STAGES = C::STAGES, ATOMS = C::ATOMS, NSB = C::NSB;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw_addr = tc5::saddr(smem_raw);
   Smem<C>& sm = *reinterpret_cast<Smem<C>*>(smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int total = g.mt * g.nt, nk = (g.nkb + ATOMS - 1) / ATOMS;
   volatile uint32_t* err = &sm.err;
   if (threadIdx.x == 0) {
@@ -158,17 +142,17 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
 
   if (warp == 0) {
     // ---- producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, last_par = 0;
-      for (int t = blockIdx.x; t < total && !*err; t += gridDim.x) {
-        const int mb = t / g.nt, nb = t % g.nt;
-        const int rb0 = nb * BN / 128;  // the columns operand's first scale tile
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!tc5::mbar_wait(&sm.empty[stage], phase ^ 1u, kWaitLimitNs, err)) {
-            *err = 1;
-            break;
-          }
+    const bool leader = tc5::elect();
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, last_par = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const int mb = t / g.nt, nb = t % g.nt;
+      const int rb0 = nb * BN / 128;  // the columns operand's first scale tile
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = wait_all(&sm.empty[stage], phase ^ 1u, err);
+        if (!ok) break;
+        if (leader) {
           const int a0 = kb * ATOMS, na = min(ATOMS, g.nkb - a0);
           const int nsb = min(NSB, g.crb - rb0), nsr = min(H, g.rrb - mb * H);
           uint64_t* const full = &sm.full[stage];
@@ -182,59 +166,57 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
           for (int j = 0; j < nsb; ++j)
             tc5::bulk_load(tc5::saddr(sm.sc[stage]) + j * ATOMS * kTile,
                            g.cs + ((int64_t)(rb0 + j) * g.nkb + a0) * kTile, na * kTile, full);
-          armed |= 1u << stage;
-          last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        armed |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // the copies issued last land before the CTA can exit
-      for (int s = 0; s < STAGES; ++s)
-        if (armed & (1u << s)) (void)tc5::mbar_wait(&sm.full[s], (last_par >> s) & 1u, kWaitLimitNs);
     }
+    // the copies issued last land before the CTA can exit
+    for (int s = 0; s < STAGES; ++s)
+      if (armed & (1u << s)) (void)tc5::mbar_wait(&sm.full[s], (last_par >> s) & 1u, kWaitLimitNs);
   } else if (warp == 1) {
     // ---- scale copies and products
-    if (lane == 0) {
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, aphase = 0;
-      for (int t = blockIdx.x; t < total && !*err; t += gridDim.x) {
-        if (!tc5::mbar_wait(&sm.tempty[acc], aphase ^ 1u, kWaitLimitNs, err)) {
-          *err = 1;
-          break;
-        }
+    const bool leader = tc5::elect();
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      ok = wait_all(&sm.tempty[acc], aphase ^ 1u, err);
+      if (!ok) break;
+      tc5::fence_after_sync();
+      const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+      const uint32_t shift = (uint32_t)((t % g.nt) * BN % 128) / 32;  // inside the first tile
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = wait_all(&sm.full[stage], phase, err);
+        if (!ok) break;
         tc5::fence_after_sync();
-        const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
-        const uint32_t shift = (uint32_t)((t % g.nt) * BN % 128) / 32;  // inside the first tile
-        bool ok = true;
-        for (int kb = 0; kb < nk; ++kb) {
-          if (!tc5::mbar_wait(&sm.full[stage], phase, kWaitLimitNs, err)) {
-            *err = 1;
-            ok = false;
-            break;
-          }
-          tc5::fence_after_sync();
-          const int na = min(ATOMS, g.nkb - kb * ATOMS);
-          // the stage's columns: for each tile along K the halves' tiles, then the columns'
-          const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * H * 4;
+        const int na = min(ATOMS, g.nkb - kb * ATOMS);
+        // the stage's columns: for each tile along K the halves' tiles, then the columns'
+        const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * H * 4;
+        const uint64_t dc = tc5::desc_sw128(tc5::saddr(sm.c[stage]), 16, 1024);
+        const uint64_t dr0 = tc5::desc_sw128(tc5::saddr(sm.r[stage]), 16, 1024);
+        const uint64_t dsr = tc5::desc_scales(tc5::saddr(sm.sr[stage]));
+        const uint64_t dsc = tc5::desc_scales(tc5::saddr(sm.sc[stage]));
+        if (leader) {
 #pragma unroll
           for (int a = 0; a < ATOMS; ++a) {
             if (a < na) {
 #pragma unroll
               for (int j = 0; j < H; ++j)
-                tc5::cp_scales(sfr + 4 * (a * H + j),
-                               tc5::desc_scales(tc5::saddr(sm.sr[stage]) + (j * ATOMS + a) * kTile));
+                tc5::cp_scales(sfr + 4 * (a * H + j), dsr + (j * ATOMS + a) * (kTile / 16));
 #pragma unroll
               for (int j = 0; j < NSB; ++j)
-                tc5::cp_scales(sfc + 4 * (a * NSB + j),
-                               tc5::desc_scales(tc5::saddr(sm.sc[stage]) + (j * ATOMS + a) * kTile));
+                tc5::cp_scales(sfc + 4 * (a * NSB + j), dsc + (j * ATOMS + a) * (kTile / 16));
             }
           }
-          const uint64_t dc = tc5::desc_sw128(tc5::saddr(sm.c[stage]), 16, 1024);
 #pragma unroll
           for (int hh = 0; hh < H; ++hh) {
-            const uint64_t dr = tc5::desc_sw128(tc5::saddr(sm.r[stage]) + hh * BM * 128, 16, 1024);
+            const uint64_t dr = dr0 + (uint64_t)(hh * BM * 128 / 16);
             const uint32_t dh = d + (uint32_t)(hh * BN);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
@@ -252,22 +234,26 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
             }
           }
           tc5::commit(&sm.empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        tc5::commit(&sm.tfull[acc]);
-        if (++acc == C::NACC) {
-          acc = 0;
-          aphase ^= 1u;
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every product issued has finished before TMEM is released
-      tc5::commit(&sm.drain);
-      (void)tc5::mbar_wait(&sm.drain, 0, kWaitLimitNs);
+      if (!ok) break;
+      if (leader) tc5::commit(&sm.tfull[acc]);
+      __syncwarp();
+      if (++acc == C::NACC) {
+        acc = 0;
+        aphase ^= 1u;
+      }
     }
+    // every product issued has finished before TMEM is released
+    if (leader) tc5::commit(&sm.drain);
+    __syncwarp();
+    (void)tc5::mbar_wait(&sm.drain, 0, kWaitLimitNs);
+    __syncwarp();
   } else {
     // ---- epilogue: TMEM lane quarter q of half hh, one row of the rows operand a thread
     const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
@@ -280,88 +266,67 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
       }
       tc5::fence_after_sync();
       const int mb = t / g.nt, nb = t % g.nt;
-      const int row0 = (mb * H + hh) * BM + 32 * q, row = row0 + lane, col0 = nb * BN;
+      const int row0 = (mb * H + hh) * BM + 32 * q, col0 = nb * BN;
       const uint32_t tbase =
           tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS + hh * BN);
-      if constexpr (SWAP) {
-        // a row is a column of D: 32 lanes store 32 consecutive values
+      // the row into registers as bf16, then TMEM goes back: the stores below drain
+      // while the next products run
+      const int nch = min(BN / 64, (g.N - col0 + 63) / 64);
+      uint32_t pk[BN / 64][32];
 #pragma unroll
-        for (int c = 0; c < BN / 16; ++c) {
-          uint32_t v[16];
-          tc5::ld_32x32b_x16(tbase + (uint32_t)(16 * c), v);
+      for (int c = 0; c < BN / 64; ++c) {
+        if (c < nch) {
+          uint32_t v0[32], v1[32];
+          tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c), v0);
+          tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c + 32), v1);
           tc5::wait_ld();
-          tc5::reg_after_ld(v);
-          if (row < g.N) {
+          tc5::reg_after_ld(v0);
+          tc5::reg_after_ld(v1);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int m = col0 + 16 * c + j;
-              if (m < g.M) g.D[m * g.ldd + row] = __float2bfloat16_rn(__uint_as_float(v[j]));
-            }
+          for (int j = 0; j < 16; ++j) {
+            pk[c][j] = pack2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
+            pk[c][16 + j] = pack2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
           }
         }
-        tc5::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
-      } else {
-        // the row into registers as bf16, then TMEM goes back: the stores below drain
-        // while the next products run
-        const int nch = min(BN / 64, (g.N - col0 + 63) / 64);
-        uint32_t pk[BN / 64][32];
+      }
+      tc5::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
 #pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          if (c < nch) {
-            uint32_t v0[32], v1[32];
-            tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c), v0);
-            tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c + 32), v1);
-            tc5::wait_ld();
-            tc5::reg_after_ld(v0);
-            tc5::reg_after_ld(v1);
+      for (int c = 0; c < BN / 64; ++c) {
+        if (c < nch) {
+          uint8_t* const blk = sm.stg[ew * C::NSTG + (int)(nst % C::NSTG)];
+          // the block's previous store has read it
+          if (g.vec && lane == 0) tc5::bulk_wait_group_read<C::NSTG - 1>();
+          __syncwarp();
+          uint4* const dst = reinterpret_cast<uint4*>(blk + lane * 128);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              pk[c][j] = pack2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
-              pk[c][16 + j] = pack2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
-            }
-          }
-        }
-        tc5::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          if (c < nch) {
-            uint8_t* const blk = sm.stg[ew * C::NSTG + (int)(nst % C::NSTG)];
-            // the block's previous store has read it
-            if (g.vec && lane == 0) tc5::bulk_wait_group_read<C::NSTG ? C::NSTG - 1 : 0>();
+          for (int j = 0; j < 8; ++j)  // the 128-byte swizzle: unit j of row r at j ^ (r % 8)
+            dst[j ^ (lane & 7)] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2],
+                                             pk[c][4 * j + 3]);
+          if (g.vec) {
+            tc5::fence_proxy_async();
             __syncwarp();
-            uint4* const dst = reinterpret_cast<uint4*>(blk + lane * 128);
+            if (lane == 0) {
+              tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 64 * c, row0);
+              tc5::bulk_commit_group();
+            }
+          } else {  // row by row, consecutive lanes on consecutive columns
+            __syncwarp();
+            const int c0 = col0 + 64 * c + lane, rows = min(32, g.M - row0);
+            for (int r = 0; r < rows; ++r) {
+              const uint8_t* const src = blk + r * 128;
+              __nv_bfloat16* const out = g.D + (int64_t)(row0 + r) * g.ldd + c0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)  // the 128-byte swizzle: unit j of row r at j ^ (r % 8)
-              dst[j ^ (lane & 7)] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2],
-                                               pk[c][4 * j + 3]);
-            if (g.vec) {
-              tc5::fence_proxy_async();
-              __syncwarp();
-              if (lane == 0) {
-                tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 64 * c, row0);
-                tc5::bulk_commit_group();
-              }
-            } else {  // row by row, consecutive lanes on consecutive columns
-              __syncwarp();
-              const int c0 = col0 + 64 * c + lane, rows = min(32, g.M - row0);
-              for (int r = 0; r < rows; ++r) {
-                const uint8_t* const src = blk + r * 128;
-                __nv_bfloat16* const out = g.D + (int64_t)(row0 + r) * g.ldd + c0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int b = 2 * lane + 64 * i;  // byte of the row
-                  if (c0 + 32 * i < g.N)
-                    out[32 * i] = *reinterpret_cast<const __nv_bfloat16*>(
-                        src + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
-                }
+              for (int i = 0; i < 2; ++i) {
+                const int b = 2 * lane + 64 * i;  // byte of the row
+                if (c0 + 32 * i < g.N)
+                  out[32 * i] = *reinterpret_cast<const __nv_bfloat16*>(
+                      src + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
               }
             }
-            ++nst;
           }
+          ++nst;
         }
       }
       if (++acc == C::NACC) {
@@ -379,75 +344,31 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN, SWAP>::THREADS, 1)
   if (threadIdx.x == 0 && sm.err) atomicAdd(&g_gemm_mx_wait_timeouts, 1u);
 }
 
-// Codes (rows x Kp) as boxes of 128 bytes of shared memory a row.  spread: packed 4-bit
-// codes go to 8-bit containers (16 codes in 8 of 16 bytes).
-bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t Kp, int fmt, bool spread,
-                  uint32_t box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-  if (!fn) return false;
-  const cuuint64_t bytes = (cuuint64_t)(fmt == mx::kFp4 ? Kp / 2 : Kp);
-  const cuuint64_t dims[2] = {spread ? (cuuint64_t)Kp : bytes, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {bytes};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, spread ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Operands {
-  int64_t M, N, K;
-  const void *A, *As, *W, *Ws;
-  void* D;
-  int64_t ldd;
-};
-
-// Lets the kernel have its shared memory: once on each device.
-template <int AF, int H, int BN, bool SWAP>
-cudaError_t allow_smem(int bytes) {
-  static std::atomic<uint64_t> done;  // a bit a device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(gemm_mx_kernel<AF, H, BN, SWAP>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
-template <int AF, int H, int BN, bool SWAP>
+template <int AF, int H, int BN>
 cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
-  using C = Cfg<AF, H, BN, SWAP>;
+  using C = Cfg<AF, H, BN>;
   const int64_t Kp = mx::pad128(o.K);
-  const int64_t rows = SWAP ? o.N : o.M, cols = SWAP ? o.M : o.N;
   MMaps tm;
   memset(&tm, 0, sizeof(tm));
-  const bool spread = AF != mx::kFp4;
-  const bool ok =
-      SWAP ? encode_codes(&tm.r, o.W, o.N, Kp, mx::kFp4, spread, H * BM) &&
-                 encode_codes(&tm.c, o.A, o.M, Kp, AF, false, BN)
-           : encode_codes(&tm.r, o.A, o.M, Kp, AF, false, H * BM) &&
-                 encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, spread, BN);
+  const bool ok = encode_codes(&tm.r, o.A, o.M, Kp, AF, false, H * BM) &&
+                  encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, BN);
   if (!ok) return cudaErrorInvalidValue;
   MArgs g{};
   g.M = (int)o.M;
   g.N = (int)o.N;
   g.ldd = o.ldd;
   g.D = static_cast<__nv_bfloat16*>(o.D);
-  g.rs = static_cast<const uint8_t*>(SWAP ? o.Ws : o.As);
-  g.cs = static_cast<const uint8_t*>(SWAP ? o.As : o.Ws);
-  const int64_t mt = (rows + H * BM - 1) / (H * BM), nt = (cols + BN - 1) / BN;
+  g.rs = static_cast<const uint8_t*>(o.As);
+  g.cs = static_cast<const uint8_t*>(o.Ws);
+  const int64_t mt = (o.M + H * BM - 1) / (H * BM), nt = (o.N + BN - 1) / BN;
   if (mt * nt > INT32_MAX) return cudaErrorInvalidValue;
   g.mt = (int)mt;
   g.nt = (int)nt;
   g.nkb = (int)(Kp / 128);
-  g.rrb = (int)((rows + 127) / 128);
-  g.crb = (int)((cols + 127) / 128);
+  g.rrb = (int)((o.M + 127) / 128);
+  g.crb = (int)((o.N + 127) / 128);
   // a TMA store ends a row at a multiple of 16 bytes, so the columns must too
-  g.vec = !SWAP && o.N % 8 == 0 && o.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 15) == 0;
+  g.vec = o.N % 8 == 0 && o.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 15) == 0;
   if (g.vec) {
     PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
     const cuuint64_t dims[2] = {(cuuint64_t)o.N, (cuuint64_t)o.M};
@@ -464,25 +385,29 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   static_assert(offsetof(Smem<C>, c) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&
                     offsetof(Smem<C>, sr) % 1024 == 0,
                 "TMA buffers on 1024-byte boundaries");
-  const cudaError_t e = allow_smem<AF, H, BN, SWAP>((int)smem);
+  static std::atomic<uint64_t> done;
+  const cudaError_t e = once_per_device(done, [&]() {
+    return cudaFuncSetAttribute(gemm_mx_kernel<AF, H, BN>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
   if (e != cudaSuccess) return e;
   const int64_t tiles = mt * nt;
-  gemm_mx_kernel<AF, H, BN, SWAP>
+  gemm_mx_kernel<AF, H, BN>
       <<<(unsigned)(tiles < sms ? tiles : sms), C::THREADS, smem, s>>>(g, tm);
   return cudaGetLastError();
 }
 
-// The tile.  Up to 64 tokens fill the narrow side (16 or 64 columns) and W streams once.
-// Otherwise the SMs share L2's bandwidth, so a tile's time goes by the bytes its stages bring
+// The tile.  The SMs share L2's bandwidth and a tile's time goes by the bytes its stages bring
 // in; of four tiles the one with the least bytes over the rounds that the tiles take on the
-// SMs.  On one B200, 4-bit A: 32768 x 6464 x 1024 131 us at 256 x 192, 139 at 128 x 256, 146
-// at 128 x 192, 179 at 128 x 128; 1000 x 2048 x 4096 17.4, 13.8, 13.3 and 11.7 us; 300 x 6464
-// x 1024 9.3, 7.6, 7.1 and 8.0.
+// SMs.  On one B200, us with 4-bit A at 256 x 192, 128 x 256, 128 x 192 and 128 x 128:
+// 32768 x 6464 x 1024 120, 129, 128, 132; 8192 x 8192 x 8192 195, 215, 210, 233; 16384 x 1024
+// x 2048 28.2, 25.4, 28.1, 25.4; 1000 x 2048 x 4096 13.4, 10.3, 9.0, 8.5; 300 x 6464 x 1024
+// 8.2, 6.2, 6.0, 6.2.
 template <int AF>
 cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
-  if (o.M <= 16) return launch<AF, 1, 16, true>(o, sms, s);
-  if (o.M <= 64) return launch<AF, 1, 64, true>(o, sms, s);
+  const int split = split_of(o.M, o.N, o.K, AF, sms);
+  if (split > 0) return launch_split(AF, o, split, s);
   auto cost = [&](int64_t bm, int64_t bn) {
     const int64_t tiles = ((o.M + bm - 1) / bm) * ((o.N + bn - 1) / bn);
     return ((tiles + sms - 1) / sms) * ((AF == mx::kFp4 ? 1 : 2) * bm + bn);
@@ -491,10 +416,10 @@ cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   int best = 0;
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[best]) best = i;
-  return best == 0   ? launch<AF, 2, 192, false>(o, sms, s)
-         : best == 1 ? launch<AF, 1, 256, false>(o, sms, s)
-         : best == 2 ? launch<AF, 1, 192, false>(o, sms, s)
-                     : launch<AF, 1, 128, false>(o, sms, s);
+  return best == 0   ? launch<AF, 2, 192>(o, sms, s)
+         : best == 1 ? launch<AF, 1, 256>(o, sms, s)
+         : best == 2 ? launch<AF, 1, 192>(o, sms, s)
+                     : launch<AF, 1, 128>(o, sms, s);
 }
 
 }  // namespace
@@ -509,9 +434,13 @@ cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const voi
 
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count) {
   const unsigned int zero = 0;
+  unsigned int split = 0;
   cudaError_t e = cudaMemcpyFromSymbol(count, g_gemm_mx_wait_timeouts, sizeof(unsigned int));
-  if (e != cudaSuccess) return e;
-  return cudaMemcpyToSymbol(g_gemm_mx_wait_timeouts, &zero, sizeof(unsigned int));
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbol(g_gemm_mx_wait_timeouts, &zero, sizeof(unsigned int));
+  if (e == cudaSuccess) e = gemm_mx::read_and_clear_split_timeouts(&split);
+  if (e == cudaSuccess) *count += split;
+  return e;
 }
 
 }  // namespace m3ssd

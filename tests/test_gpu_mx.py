@@ -159,6 +159,37 @@ def test_gemm_block_shapes_sampled(fmt):
     assert m3.device_wait_timeouts() == 0
 
 
+# few tokens or few tiles and a long K: K over two, four and eight CTAs, at up to 16 tokens and
+# beyond, whole and ragged
+LONG_K = [(1, 129, 8192), (13, 4000, 3000), (7, 8200, 4160), (16, 8192, 8192), (3, 20000, 1000),
+          (17, 130, 6400), (100, 520, 8200), (129, 255, 4224), (130, 4100, 8200),
+          (257, 2000, 5000), (333, 1030, 2600)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", LONG_K)
+def test_gemm_long_k(fmt, M, N, K):
+    """Against fp64; the same bits from every run; other columns and rows of an output are
+    left; runs that overlap on two streams do not disturb one another."""
+    A, W = operands(M, N, K, fmt, M + N + K)
+    D = m3.gemm_mx(A, W)
+    check(D, A, W)
+    for ld, off in ((N + 8, 0), (N + 5, 3)):
+        big = torch.full((M + 1, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+        m3.gemm_mx(A, W, out=big[:M, off:off + N])
+        assert torch.equal(big[:M, off:off + N], D)
+        big[:M, off:off + N] = 7
+        assert torch.all(big == 7)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(m3.gemm_mx(A, W))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, D) for o in outs)
+    assert m3.device_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("M", [3, 200])
 def test_gemm_nan_blocks_stay_in_their_rows(fmt, M):
