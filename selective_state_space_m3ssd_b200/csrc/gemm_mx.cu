@@ -26,7 +26,10 @@
 //
 // What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
 // writes at HBM's 3.9 TB/s of them, 120 taken); with a long K shared memory, which feeds the
-// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).
+// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).  Not kept:
+// CTA pairs, 256 x 256 a pair, which bring W in once for both but leave no room in TMEM for a
+// second accumulator beside the scales: 8192^3 187 us against 197 in the same run, 32768 x
+// 6464 x 1024 134 against 121, 16384 x 1024 x 2048 with 8-bit A 40 against 39.
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
@@ -57,7 +60,7 @@ struct Cfg {
   // bytes the copies of a stage count on its barrier: W's 4-bit codes count as they are in
   // global memory, whether or not they are spread
   static constexpr uint32_t R_TX = R_BYTES;
-  static constexpr uint32_t C_TX = AF != mx::kFp4 ? C_BYTES / 2 : C_BYTES;
+  static constexpr uint32_t C_ROW_TX = AF != mx::kFp4 ? 64 : 128;
   static constexpr uint32_t SR_BYTES = H * ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
   static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
   static constexpr int NSTG = H == 1 ? 2 : 1;  // output blocks of an epilogue warp
@@ -73,7 +76,7 @@ struct Cfg {
   // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
   // E4M3 = 0, E2M1 = 5)
   static constexpr uint32_t FA = AF == mx::kFp4 ? 1 : 0, FW = AF == mx::kFp4 ? 1 : 5;
-  static constexpr uint32_t IDESC = tc5::idesc_mx(BM, BN, FA, FW);
+  static constexpr uint32_t IDESC = tc5::idesc_mx(BM, 0, FA, FW);  // the columns are ORed in
 };
 
 template <typename C>
@@ -95,6 +98,7 @@ struct Smem {
 
 struct MMaps {
   CUtensorMap r, c;  // codes of the rows and the columns operand, box 128 bytes x 128 H / BN rows
+  CUtensorMap c64;   // the columns operand in boxes of 64 rows
   CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 64 x 32, 128-byte swizzle (when vec)
 };
 
@@ -104,11 +108,24 @@ struct MArgs {
   __nv_bfloat16* D;
   const uint8_t* rs;  // scales of the rows and the columns operand
   const uint8_t* cs;
-  int mt, nt;         // tiles along the rows and the columns operand
+  int nt;             // tiles along the columns operand
+  int full, items;    // tiles taken whole; those and the parts of the others
+  int parts, pw;      // parts of a tile, columns of a part (a multiple of 64)
   int nkb;            // 128-column groups of K
   int rrb, crb;       // 128-row blocks of the rows and the columns operand
   bool vec;
 };
+
+// What a CTA takes: rows from 128 H mb, w columns from col0.
+struct Item {
+  int mb, col0, w;
+};
+template <int BN>
+__device__ __forceinline__ Item item_of(const MArgs& g, int t) {
+  if (t < g.full) return {t / g.nt, t % g.nt * BN, BN};
+  const int u = t - g.full, tile = g.full + u / g.parts, c = u % g.parts * g.pw;
+  return {tile / g.nt, tile % g.nt * BN + c, min(g.pw, BN - c)};
+}
 
 template <int AF, int H, int BN>
 __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
@@ -119,7 +136,7 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
   const uint32_t raw_addr = tc5::saddr(smem_raw);
   Smem<C>& sm = *reinterpret_cast<Smem<C>*>(smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int total = g.mt * g.nt, nk = (g.nkb + ATOMS - 1) / ATOMS;
+  const int nk = (g.nkb + ATOMS - 1) / ATOMS;
   volatile uint32_t* err = &sm.err;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -146,20 +163,25 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, armed = 0, last_par = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const int mb = t / g.nt, nb = t % g.nt;
-      const int rb0 = nb * BN / 128;  // the columns operand's first scale tile
+    for (int t = blockIdx.x; ok && t < g.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g, t);
+      const int mb = it.mb, rb0 = it.col0 / 128;  // the columns operand's first scale tile
+      const int nsb = max(0, min(NSB, g.crb - rb0)), nsr = min(H, g.rrb - mb * H);
       for (int kb = 0; kb < nk; ++kb) {
         ok = wait_all(&sm.empty[stage], phase ^ 1u, err);
         if (!ok) break;
         if (leader) {
           const int a0 = kb * ATOMS, na = min(ATOMS, g.nkb - a0);
-          const int nsb = min(NSB, g.crb - rb0), nsr = min(H, g.rrb - mb * H);
           uint64_t* const full = &sm.full[stage];
           tc5::mbar_arrive_expect_tx(
-              full, C::R_TX + C::C_TX + (uint32_t)((nsr + nsb) * na) * kTile);
+              full, C::R_TX + it.w * C::C_ROW_TX + (uint32_t)((nsr + nsb) * na) * kTile);
           tc5::tma_load_2d(tc5::saddr(sm.r[stage]), &tm.r, full, kb * 128, mb * (H * BM));
-          tc5::tma_load_2d(tc5::saddr(sm.c[stage]), &tm.c, full, kb * 128, nb * BN);
+          if (it.w == BN)
+            tc5::tma_load_2d(tc5::saddr(sm.c[stage]), &tm.c, full, kb * 128, it.col0);
+          else
+            for (int c = 0; c < it.w; c += 64)
+              tc5::tma_load_2d(tc5::saddr(sm.c[stage]) + c * 128, &tm.c64, full, kb * 128,
+                               it.col0 + c);
           for (int j = 0; j < nsr; ++j)
             tc5::bulk_load(tc5::saddr(sm.sr[stage]) + j * ATOMS * kTile,
                            g.rs + ((int64_t)(mb * H + j) * g.nkb + a0) * kTile, na * kTile, full);
@@ -185,12 +207,14 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < total; t += gridDim.x) {
+    for (int t = blockIdx.x; ok && t < g.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g, t);
+      const uint32_t shift = (uint32_t)(it.col0 % 128) / 32;  // inside the first scale tile
+      const uint32_t idesc = C::IDESC | (uint32_t)(it.w >> 3) << 17;
       ok = wait_all(&sm.tempty[acc], aphase ^ 1u, err);
       if (!ok) break;
       tc5::fence_after_sync();
       const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
-      const uint32_t shift = (uint32_t)((t % g.nt) * BN % 128) / 32;  // inside the first tile
       for (int kb = 0; kb < nk; ++kb) {
         ok = wait_all(&sm.full[stage], phase, err);
         if (!ok) break;
@@ -223,12 +247,12 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
               if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
                 if (k / 2 < na)
                   tc5::mma_mxf4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                                tc5::idesc_mx_sf(C::IDESC, 2 * (k & 1)),
+                                tc5::idesc_mx_sf(idesc, 2 * (k & 1)),
                                 sfr + 4 * (k / 2 * H + hh), sfc + 4 * NSB * (k / 2) + shift,
                                 kb > 0 || k > 0);
               } else {  // 32 values, one block
                 tc5::mma_mxf8f6f4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                                  tc5::idesc_mx_sf(C::IDESC, k), sfr + 4 * hh, sfc + shift,
+                                  tc5::idesc_mx_sf(idesc, k), sfr + 4 * hh, sfc + shift,
                                   kb > 0 || k > 0);
               }
             }
@@ -259,19 +283,19 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
     int acc = 0;
     uint32_t nst = 0, aphase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    for (int t = blockIdx.x; t < g.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g, t);
+      const int row0 = (it.mb * H + hh) * BM + 32 * q, col0 = it.col0;
       if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
         *err = 1;
         break;
       }
       tc5::fence_after_sync();
-      const int mb = t / g.nt, nb = t % g.nt;
-      const int row0 = (mb * H + hh) * BM + 32 * q, col0 = nb * BN;
       const uint32_t tbase =
           tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS + hh * BN);
       // the row into registers as bf16, then TMEM goes back: the stores below drain
       // while the next products run
-      const int nch = min(BN / 64, (g.N - col0 + 63) / 64);
+      const int nch = min(it.w / 64, (g.N - col0 + 63) / 64);
       uint32_t pk[BN / 64][32];
 #pragma unroll
       for (int c = 0; c < BN / 64; ++c) {
@@ -344,6 +368,30 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
   if (threadIdx.x == 0 && sm.err) atomicAdd(&g_gemm_mx_wait_timeouts, 1u);
 }
 
+// How bm x bn tiles go to the SMs: in whole rounds, and, from three rounds on, the tiles left
+// over in the narrowest parts that still make one round (20011 x 1024 x 2048, four rounds and
+// 36 tiles in four parts each: 25.4 against 27.5 us in 4 bits, 39.7 against 42.7 with 8-bit
+// A; with fewer rounds a smaller tile is better: 1000 x 2048 x 4096 8.3 against 10.0).
+struct Plan {
+  int64_t nt, rounds, full, items;
+  int pw;  // columns of a part, bn where nothing is split or left over
+};
+Plan plan(int64_t M, int64_t N, int64_t bm, int bn, int64_t sms) {
+  Plan p;
+  p.nt = (N + bn - 1) / bn;
+  const int64_t tiles = (M + bm - 1) / bm * p.nt, left = tiles % sms;
+  p.rounds = tiles / sms;
+  p.pw = bn;
+  for (int pw = 64; p.rounds > 2 && left && pw < bn && pw <= 128; pw += 64)
+    if (left * ((bn + pw - 1) / pw) <= sms) {
+      p.pw = pw;
+      break;
+    }
+  p.full = p.pw < bn ? tiles - left : tiles;
+  p.items = p.full + (tiles - p.full) * ((bn + p.pw - 1) / p.pw);
+  return p;
+}
+
 template <int AF, int H, int BN>
 cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   using C = Cfg<AF, H, BN>;
@@ -351,7 +399,8 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   MMaps tm;
   memset(&tm, 0, sizeof(tm));
   const bool ok = encode_codes(&tm.r, o.A, o.M, Kp, AF, false, H * BM) &&
-                  encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, BN);
+                  encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, BN) &&
+                  encode_codes(&tm.c64, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, 64);
   if (!ok) return cudaErrorInvalidValue;
   MArgs g{};
   g.M = (int)o.M;
@@ -360,10 +409,13 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   g.D = static_cast<__nv_bfloat16*>(o.D);
   g.rs = static_cast<const uint8_t*>(o.As);
   g.cs = static_cast<const uint8_t*>(o.Ws);
-  const int64_t mt = (o.M + H * BM - 1) / (H * BM), nt = (o.N + BN - 1) / BN;
-  if (mt * nt > INT32_MAX) return cudaErrorInvalidValue;
-  g.mt = (int)mt;
-  g.nt = (int)nt;
+  const Plan p = plan(o.M, o.N, H * BM, BN, sms);
+  if (p.items > INT32_MAX) return cudaErrorInvalidValue;
+  g.nt = (int)p.nt;
+  g.full = (int)p.full;
+  g.items = (int)p.items;
+  g.parts = (BN + p.pw - 1) / p.pw;
+  g.pw = p.pw;
   g.nkb = (int)(Kp / 128);
   g.rrb = (int)((o.M + 127) / 128);
   g.crb = (int)((o.N + 127) / 128);
@@ -391,9 +443,8 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t tiles = mt * nt;
   gemm_mx_kernel<AF, H, BN>
-      <<<(unsigned)(tiles < sms ? tiles : sms), C::THREADS, smem, s>>>(g, tm);
+      <<<(unsigned)(p.items < sms ? p.items : sms), C::THREADS, smem, s>>>(g, tm);
   return cudaGetLastError();
 }
 
@@ -408,9 +459,11 @@ cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int split = split_of(o.M, o.N, o.K, AF, sms);
   if (split > 0) return launch_split(AF, o, split, s);
-  auto cost = [&](int64_t bm, int64_t bn) {
-    const int64_t tiles = ((o.M + bm - 1) / bm) * ((o.N + bn - 1) / bn);
-    return ((tiles + sms - 1) / sms) * ((AF == mx::kFp4 ? 1 : 2) * bm + bn);
+  auto cost = [&](int64_t bm, int bn) {
+    const Plan p = plan(o.M, o.N, bm, bn, sms);
+    const int64_t rows = (AF == mx::kFp4 ? 1 : 2) * bm;
+    const bool left = p.full < p.items || p.items > p.rounds * sms;
+    return p.rounds * (rows + bn) + (left ? rows + p.pw : 0);
   };
   const int64_t c[4] = {cost(256, 192), cost(128, 256), cost(128, 192), cost(128, 128)};
   int best = 0;

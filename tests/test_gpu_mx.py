@@ -159,6 +159,21 @@ def test_gemm_block_shapes_sampled(fmt):
     assert m3.device_wait_timeouts() == 0
 
 
+# whole rounds of tiles and a rest in parts: 64 and 128 columns of 192 and of 256, aligned and
+# ragged
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", [(18992, 1032, 160), (19131, 963, 288), (13829, 1537, 96),
+                                   (19126, 578, 160), (20657, 577, 288), (20011, 1024, 96)])
+def test_gemm_parts_of_tiles(fmt, M, N, K):
+    A, W = operands(M, N, K, fmt, M + N + K)
+    big = torch.full((M + 1, N + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    m3.gemm_mx(A, W, out=big[:M, :N])
+    check(big[:M, :N], A, W)
+    assert torch.all(big[M:] == 7) and torch.all(big[:, N:] == 7)
+    assert torch.equal(m3.gemm_mx(A, W), big[:M, :N])
+    assert m3.device_wait_timeouts() == 0
+
+
 # few tokens or few tiles and a long K: K over two, four and eight CTAs, at up to 16 tokens and
 # beyond, whole and ragged
 LONG_K = [(1, 129, 8192), (13, 4000, 3000), (7, 8200, 4160), (16, 8192, 8192), (3, 20000, 1000),
