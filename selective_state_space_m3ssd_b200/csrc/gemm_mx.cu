@@ -26,10 +26,8 @@
 //
 // What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
 // writes at HBM's 3.9 TB/s of them, 120 taken); with a long K shared memory, which feeds the
-// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).  Not kept:
-// CTA pairs, 256 x 256 a pair, which bring W in once for both but leave no room in TMEM for a
-// second accumulator beside the scales: 8192^3 187 us against 197 in the same run, 32768 x
-// 6464 x 1024 134 against 121, 16384 x 1024 x 2048 with 8-bit A 40 against 39.
+// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).  Many
+// tiles of a long K go to pairs of CTAs (gemm_mx_pair.cu).
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
@@ -46,8 +44,6 @@ __device__ unsigned int g_gemm_mx_wait_timeouts;
 namespace {
 
 using namespace gemm_mx;
-
-constexpr uint32_t kStgBytes = 32 * 128;  // an output block: 32 rows x 64 bf16 columns
 
 // AF: A's format.  H: 128-row halves of a tile.  A stage is 128 bytes of K a row: 256 values
 // in 4 bits, 128 in 8.
@@ -108,24 +104,11 @@ struct MArgs {
   __nv_bfloat16* D;
   const uint8_t* rs;  // scales of the rows and the columns operand
   const uint8_t* cs;
-  int nt;             // tiles along the columns operand
-  int full, items;    // tiles taken whole; those and the parts of the others
-  int parts, pw;      // parts of a tile, columns of a part (a multiple of 64)
+  Tiles tiles;        // the items of the CTAs
   int nkb;            // 128-column groups of K
   int rrb, crb;       // 128-row blocks of the rows and the columns operand
   bool vec;
 };
-
-// What a CTA takes: rows from 128 H mb, w columns from col0.
-struct Item {
-  int mb, col0, w;
-};
-template <int BN>
-__device__ __forceinline__ Item item_of(const MArgs& g, int t) {
-  if (t < g.full) return {t / g.nt, t % g.nt * BN, BN};
-  const int u = t - g.full, tile = g.full + u / g.parts, c = u % g.parts * g.pw;
-  return {tile / g.nt, tile % g.nt * BN + c, min(g.pw, BN - c)};
-}
 
 template <int AF, int H, int BN>
 __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
@@ -163,8 +146,8 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, armed = 0, last_par = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < g.items; t += gridDim.x) {
-      const Item it = item_of<BN>(g, t);
+    for (int t = blockIdx.x; ok && t < g.tiles.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g.tiles, t);
       const int mb = it.mb, rb0 = it.col0 / 128;  // the columns operand's first scale tile
       const int nsb = max(0, min(NSB, g.crb - rb0)), nsr = min(H, g.rrb - mb * H);
       for (int kb = 0; kb < nk; ++kb) {
@@ -207,8 +190,8 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, aphase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < g.items; t += gridDim.x) {
-      const Item it = item_of<BN>(g, t);
+    for (int t = blockIdx.x; ok && t < g.tiles.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g.tiles, t);
       const uint32_t shift = (uint32_t)(it.col0 % 128) / 32;  // inside the first scale tile
       const uint32_t idesc = C::IDESC | (uint32_t)(it.w >> 3) << 17;
       ok = wait_all(&sm.tempty[acc], aphase ^ 1u, err);
@@ -283,8 +266,8 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
     int acc = 0;
     uint32_t nst = 0, aphase = 0;
-    for (int t = blockIdx.x; t < g.items; t += gridDim.x) {
-      const Item it = item_of<BN>(g, t);
+    for (int t = blockIdx.x; t < g.tiles.items; t += gridDim.x) {
+      const Item it = item_of<BN>(g.tiles, t);
       const int row0 = (it.mb * H + hh) * BM + 32 * q, col0 = it.col0;
       if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
         *err = 1;
@@ -297,62 +280,12 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
       // while the next products run
       const int nch = min(it.w / 64, (g.N - col0 + 63) / 64);
       uint32_t pk[BN / 64][32];
-#pragma unroll
-      for (int c = 0; c < BN / 64; ++c) {
-        if (c < nch) {
-          uint32_t v0[32], v1[32];
-          tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c), v0);
-          tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c + 32), v1);
-          tc5::wait_ld();
-          tc5::reg_after_ld(v0);
-          tc5::reg_after_ld(v1);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            pk[c][j] = pack2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
-            pk[c][16 + j] = pack2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
-          }
-        }
-      }
+      load_row<BN>(tbase, nch, pk);
       tc5::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
-#pragma unroll
-      for (int c = 0; c < BN / 64; ++c) {
-        if (c < nch) {
-          uint8_t* const blk = sm.stg[ew * C::NSTG + (int)(nst % C::NSTG)];
-          // the block's previous store has read it
-          if (g.vec && lane == 0) tc5::bulk_wait_group_read<C::NSTG - 1>();
-          __syncwarp();
-          uint4* const dst = reinterpret_cast<uint4*>(blk + lane * 128);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)  // the 128-byte swizzle: unit j of row r at j ^ (r % 8)
-            dst[j ^ (lane & 7)] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2],
-                                             pk[c][4 * j + 3]);
-          if (g.vec) {
-            tc5::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) {
-              tc5::tma_store_2d(&tm.d, tc5::saddr(blk), col0 + 64 * c, row0);
-              tc5::bulk_commit_group();
-            }
-          } else {  // row by row, consecutive lanes on consecutive columns
-            __syncwarp();
-            const int c0 = col0 + 64 * c + lane, rows = min(32, g.M - row0);
-            for (int r = 0; r < rows; ++r) {
-              const uint8_t* const src = blk + r * 128;
-              __nv_bfloat16* const out = g.D + (int64_t)(row0 + r) * g.ldd + c0;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int b = 2 * lane + 64 * i;  // byte of the row
-                if (c0 + 32 * i < g.N)
-                  out[32 * i] = *reinterpret_cast<const __nv_bfloat16*>(
-                      src + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
-              }
-            }
-          }
-          ++nst;
-        }
-      }
+      store_rows<BN, C::NSTG>(pk, nch, sm.stg[ew * C::NSTG], nst, &tm.d, g.D, g.ldd, g.M, g.N, g.vec,
+                              row0, col0);
       if (++acc == C::NACC) {
         acc = 0;
         aphase ^= 1u;
@@ -366,30 +299,6 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
   tc5::fence_after_sync();
   if (warp == 1) tc5::tmem_dealloc(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && sm.err) atomicAdd(&g_gemm_mx_wait_timeouts, 1u);
-}
-
-// How bm x bn tiles go to the SMs: in whole rounds, and, from three rounds on, the tiles left
-// over in the narrowest parts that still make one round (20011 x 1024 x 2048, four rounds and
-// 36 tiles in four parts each: 25.4 against 27.5 us in 4 bits, 39.7 against 42.7 with 8-bit
-// A; with fewer rounds a smaller tile is better: 1000 x 2048 x 4096 8.3 against 10.0).
-struct Plan {
-  int64_t nt, rounds, full, items;
-  int pw;  // columns of a part, bn where nothing is split or left over
-};
-Plan plan(int64_t M, int64_t N, int64_t bm, int bn, int64_t sms) {
-  Plan p;
-  p.nt = (N + bn - 1) / bn;
-  const int64_t tiles = (M + bm - 1) / bm * p.nt, left = tiles % sms;
-  p.rounds = tiles / sms;
-  p.pw = bn;
-  for (int pw = 64; p.rounds > 2 && left && pw < bn && pw <= 128; pw += 64)
-    if (left * ((bn + pw - 1) / pw) <= sms) {
-      p.pw = pw;
-      break;
-    }
-  p.full = p.pw < bn ? tiles - left : tiles;
-  p.items = p.full + (tiles - p.full) * ((bn + p.pw - 1) / p.pw);
-  return p;
 }
 
 template <int AF, int H, int BN>
@@ -409,29 +318,13 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   g.D = static_cast<__nv_bfloat16*>(o.D);
   g.rs = static_cast<const uint8_t*>(o.As);
   g.cs = static_cast<const uint8_t*>(o.Ws);
-  const Plan p = plan(o.M, o.N, H * BM, BN, sms);
+  const Plan p = plan(o.M, o.N, H * BM, BN, 64, sms);
   if (p.items > INT32_MAX) return cudaErrorInvalidValue;
-  g.nt = (int)p.nt;
-  g.full = (int)p.full;
-  g.items = (int)p.items;
-  g.parts = (BN + p.pw - 1) / p.pw;
-  g.pw = p.pw;
+  g.tiles = p.tiles(BN);
   g.nkb = (int)(Kp / 128);
   g.rrb = (int)((o.M + 127) / 128);
   g.crb = (int)((o.N + 127) / 128);
-  // a TMA store ends a row at a multiple of 16 bytes, so the columns must too
-  g.vec = o.N % 8 == 0 && o.ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 15) == 0;
-  if (g.vec) {
-    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-    const cuuint64_t dims[2] = {(cuuint64_t)o.N, (cuuint64_t)o.M};
-    const cuuint64_t strides[1] = {(cuuint64_t)o.ldd * 2};
-    const cuuint32_t box[2] = {64, 32};
-    const cuuint32_t estr[2] = {1, 1};
-    g.vec = fn && fn(&tm.d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.D, dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-                        CUDA_SUCCESS;
-  }
+  g.vec = encode_output(&tm.d, o);
   const size_t smem = sizeof(Smem<C>) + 1024;
   static_assert(sizeof(Smem<C>) + 1024 <= 232448, "one CTA's shared memory");
   static_assert(offsetof(Smem<C>, c) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&
@@ -460,15 +353,15 @@ cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int split = split_of(o.M, o.N, o.K, AF, sms);
   if (split > 0) return launch_split(AF, o, split, s);
   auto cost = [&](int64_t bm, int bn) {
-    const Plan p = plan(o.M, o.N, bm, bn, sms);
+    const Plan p = plan(o.M, o.N, bm, bn, 64, sms);
     const int64_t rows = (AF == mx::kFp4 ? 1 : 2) * bm;
-    const bool left = p.full < p.items || p.items > p.rounds * sms;
-    return p.rounds * (rows + bn) + (left ? rows + p.pw : 0);
+    return p.rounds * (rows + bn) + (p.left ? rows + p.pw : 0);
   };
   const int64_t c[4] = {cost(256, 192), cost(128, 256), cost(128, 192), cost(128, 128)};
   int best = 0;
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[best]) best = i;
+  if (pair_cost(o.M, o.N, o.K, AF, sms) < c[best]) return launch_pair(AF, o, sms, s);
   return best == 0   ? launch<AF, 2, 192>(o, sms, s)
          : best == 1 ? launch<AF, 1, 256>(o, sms, s)
          : best == 2 ? launch<AF, 1, 192>(o, sms, s)
@@ -487,12 +380,13 @@ cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const voi
 
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count) {
   const unsigned int zero = 0;
-  unsigned int split = 0;
+  unsigned int split = 0, pair = 0;
   cudaError_t e = cudaMemcpyFromSymbol(count, g_gemm_mx_wait_timeouts, sizeof(unsigned int));
   if (e == cudaSuccess)
     e = cudaMemcpyToSymbol(g_gemm_mx_wait_timeouts, &zero, sizeof(unsigned int));
   if (e == cudaSuccess) e = gemm_mx::read_and_clear_split_timeouts(&split);
-  if (e == cudaSuccess) *count += split;
+  if (e == cudaSuccess) e = gemm_mx::read_and_clear_pair_timeouts(&pair);
+  if (e == cudaSuccess) *count += split + pair;
   return e;
 }
 

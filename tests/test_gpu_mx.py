@@ -174,6 +174,27 @@ def test_gemm_parts_of_tiles(fmt, M, N, K):
     assert m3.device_wait_timeouts() == 0
 
 
+# many tiles and a K long enough for pairs of CTAs (with both types of A, or 8-bit A alone):
+# whole tiles, parts, columns and rows that end inside them
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", [(16384, 1024, 2048), (20011, 1024, 2048), (13000, 1537, 1500),
+                                   (4090, 4000, 4096), (4001, 4099, 4200), (19000, 1000, 2304)])
+def test_gemm_many_tiles(fmt, M, N, K):
+    A, W = operands(M, N, K, fmt, M + N + K)
+    big = torch.full((M + 1, N + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    m3.gemm_mx(A, W, out=big[:M, :N])
+    check(big[:M, :N], A, W)
+    assert torch.all(big[M:] == 7) and torch.all(big[:, N:] == 7)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(4):
+        with torch.cuda.stream(streams[i % 2]):
+            outs.append(m3.gemm_mx(A, W))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, big[:M, :N]) for o in outs)
+    assert m3.device_wait_timeouts() == 0
+
+
 # few tokens or few tiles and a long K: K over two, four and eight CTAs, at up to 16 tokens and
 # beyond, whole and ragged
 LONG_K = [(1, 129, 8192), (13, 4000, 3000), (7, 8200, 4160), (16, 8192, 8192), (3, 20000, 1000),
