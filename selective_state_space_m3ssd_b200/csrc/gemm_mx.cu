@@ -25,9 +25,13 @@
 // 1024 131 against 120).
 //
 // What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
-// writes at HBM's 3.9 TB/s of them, 120 taken); with a long K shared memory, which feeds the
-// products (107 bytes a cycle at 256 x 192 in 4 bits) while the stages come in (75).  Many
-// tiles of a long K go to pairs of CTAs (gemm_mx_pair.cu).
+// writes at HBM's 3.9 TB/s of them, 119 taken); with a long K what the copies bring in against
+// what the products read: the ring takes in 50 to 55 bytes a cycle and SM, 75 to 96 would keep
+// the products at their peak.  Measured and not kept: L2 prefetches of the stages behind the
+// ring (3 to 8 % slower); pairs of CTAs (256 x 256, W brought in once for both, but no second
+// accumulator fits beside the scales): with pairs 180 and 338 us at 8192^3 against 195 and 353,
+// 36.0 and 55.2 at 32768 x 1024 x 2048 against 34.4 and 56.4, 137 and 187 at 32768 x 6464 x 1024
+// against 119 and 191.
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.
@@ -45,6 +49,8 @@ namespace {
 
 using namespace gemm_mx;
 
+constexpr uint32_t kStgBytes = 32 * 128;  // an output block: 32 rows x 64 bf16 columns
+
 // AF: A's format.  H: 128-row halves of a tile.  A stage is 128 bytes of K a row: 256 values
 // in 4 bits, 128 in 8.
 template <int AF, int H, int BN>
@@ -59,8 +65,7 @@ struct Cfg {
   static constexpr uint32_t C_ROW_TX = AF != mx::kFp4 ? 64 : 128;
   static constexpr uint32_t SR_BYTES = H * ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
   static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
-  static constexpr int NSTG = H == 1 ? 2 : 1;  // output blocks of an epilogue warp
-  static constexpr int ROOM = 226 * 1024 - EPI_WARPS * NSTG * (int)kStgBytes - 1024;
+  static constexpr int ROOM = 226 * 1024 - EPI_WARPS * (int)kStgBytes - 1024;
   static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
   static constexpr int SF_COLS = ATOMS * 4 * (H + NSB);     // TMEM columns of a stage's scales
   static constexpr int ACC_COLS = H * BN;  // an accumulator, its halves side by side
@@ -69,6 +74,8 @@ struct Cfg {
   static constexpr int COLS = NACC * ACC_COLS + STAGES * SF_COLS;
   static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
+  static_assert(EPI_WARPS * (BN / 64) * (int)kStgBytes <= STAGES * (int)(R_BYTES + C_BYTES),
+                "the last item's staging");
   // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
   // E4M3 = 0, E2M1 = 5)
   static constexpr uint32_t FA = AF == mx::kFp4 ? 1 : 0, FW = AF == mx::kFp4 ? 1 : 5;
@@ -80,7 +87,7 @@ struct Smem {
   // every buffer a TMA copy reads or writes starts on a 1024-byte boundary
   uint8_t r[C::STAGES][C::R_BYTES];
   uint8_t c[C::STAGES][C::C_BYTES];
-  uint8_t stg[C::EPI_WARPS * C::NSTG][kStgBytes];
+  uint8_t stg[C::EPI_WARPS][kStgBytes];
   uint8_t sr[C::STAGES][C::SR_BYTES];
   uint8_t sc[C::STAGES][C::SC_BYTES];
   uint64_t full[C::STAGES];
@@ -98,6 +105,23 @@ struct MMaps {
   CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 64 x 32, 128-byte swizzle (when vec)
 };
 
+// What a CTA takes of D: rows of tile row mb, w columns from col0.  Tiles up to `full` whole,
+// then the parts of the others.
+struct Tiles {
+  int nt;           // tiles along N
+  int full, items;  // tiles taken whole; those and the parts of the others
+  int parts, pw;    // parts of a tile, columns of a part
+};
+struct Item {
+  int mb, col0, w;
+};
+template <int BN>
+__device__ __forceinline__ Item item_of(const Tiles& g, int t) {
+  if (t < g.full) return {t / g.nt, t % g.nt * BN, BN};
+  const int u = t - g.full, tile = g.full + u / g.parts, c = u % g.parts * g.pw;
+  return {tile / g.nt, tile % g.nt * BN + c, min(g.pw, BN - c)};
+}
+
 struct MArgs {
   int M, N;  // of D
   int64_t ldd;
@@ -109,6 +133,76 @@ struct MArgs {
   int rrb, crb;       // 128-row blocks of the rows and the columns operand
   bool vec;
 };
+
+// An epilogue warp's 32 rows of an accumulator, a thread a row, 64 nch columns from TMEM to
+// registers as bf16 pairs.
+template <int BN>
+__device__ __forceinline__ void load_row(uint32_t tbase, int nch, uint32_t (&pk)[BN / 64][32]) {
+#pragma unroll
+  for (int c = 0; c < BN / 64; ++c) {
+    if (c < nch) {
+      uint32_t v0[32], v1[32];
+      tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c), v0);
+      tc5::ld_32x32b_x32(tbase + (uint32_t)(64 * c + 32), v1);
+      tc5::wait_ld();
+      tc5::reg_after_ld(v0);
+      tc5::reg_after_ld(v1);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        pk[c][j] = pack2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
+        pk[c][16 + j] = pack2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
+      }
+    }
+  }
+}
+
+// Those rows to D from (row0, col0), block by block of 32 x 64 through swizzled staging: by TMA
+// (vec), or row by row.  The warp has one block for staging, so that the ring gets the memory (a
+// fourth stage of 128 x 256 is worth 9 %); the last item of a CTA finds the ring idle and
+// stages there without waiting (`fresh`: a block for each).
+template <int BN>
+__device__ __forceinline__ void store_rows(const uint32_t (&pk)[BN / 64][32], int nch, uint8_t* stg,
+                                           bool fresh, const CUtensorMap* tm_d, __nv_bfloat16* D,
+                                           int64_t ldd, int M, int N, bool vec, int row0,
+                                           int col0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < BN / 64; ++c) {
+    if (c < nch) {
+      uint8_t* const blk = fresh ? stg + c * kStgBytes : stg;
+      // the block's previous store has read it
+      if (vec && !fresh && lane == 0) tc5::bulk_wait_group_read<0>();
+      __syncwarp();
+      uint4* const dst = reinterpret_cast<uint4*>(blk + lane * 128);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)  // the 128-byte swizzle: unit j of row r at j ^ (r % 8)
+        dst[j ^ (lane & 7)] = make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2],
+                                         pk[c][4 * j + 3]);
+      if (vec) {
+        tc5::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          tc5::tma_store_2d(tm_d, tc5::saddr(blk), col0 + 64 * c, row0);
+          tc5::bulk_commit_group();
+        }
+      } else {  // row by row, consecutive lanes on consecutive columns
+        __syncwarp();
+        const int c0 = col0 + 64 * c + lane, rows = min(32, M - row0);
+        for (int r = 0; r < rows; ++r) {
+          const uint8_t* const src = blk + r * 128;
+          __nv_bfloat16* const out = D + (int64_t)(row0 + r) * ldd + c0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int b = 2 * lane + 64 * i;  // byte of the row
+            if (c0 + 32 * i < N)
+              out[32 * i] = *reinterpret_cast<const __nv_bfloat16*>(
+                  src + (((b >> 4) ^ (r & 7)) << 4) + (b & 15));
+          }
+        }
+      }
+    }
+  }
+}
 
 template <int AF, int H, int BN>
 __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
@@ -265,7 +359,7 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     // ---- epilogue: TMEM lane quarter q of half hh, one row of the rows operand a thread
     const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
     int acc = 0;
-    uint32_t nst = 0, aphase = 0;
+    uint32_t aphase = 0;
     for (int t = blockIdx.x; t < g.tiles.items; t += gridDim.x) {
       const Item it = item_of<BN>(g.tiles, t);
       const int row0 = (it.mb * H + hh) * BM + 32 * q, col0 = it.col0;
@@ -284,8 +378,9 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
       tc5::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
-      store_rows<BN, C::NSTG>(pk, nch, sm.stg[ew * C::NSTG], nst, &tm.d, g.D, g.ldd, g.M, g.N, g.vec,
-                              row0, col0);
+      const bool last = t + (int)gridDim.x >= g.tiles.items;
+      store_rows<BN>(pk, nch, last ? sm.r[0] + ew * (BN / 64) * kStgBytes : sm.stg[ew], last, &tm.d,
+                     g.D, g.ldd, g.M, g.N, g.vec, row0, col0);
       if (++acc == C::NACC) {
         acc = 0;
         aphase ^= 1u;
@@ -299,6 +394,50 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
   tc5::fence_after_sync();
   if (warp == 1) tc5::tmem_dealloc(tmem, C::TMEM_COLS);
   if (threadIdx.x == 0 && sm.err) atomicAdd(&g_gemm_mx_wait_timeouts, 1u);
+}
+
+// Where D's rows are multiples of 16 bytes (a TMA store ends a row at one): its map for the
+// stores of 32 x 64 blocks.
+bool encode_output(CUtensorMap* m, const Operands& o) {
+  if (o.N % 8 != 0 || o.ldd % 8 != 0 || (reinterpret_cast<uintptr_t>(o.D) & 15) != 0) return false;
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  const cuuint64_t dims[2] = {(cuuint64_t)o.N, (cuuint64_t)o.M};
+  const cuuint64_t strides[1] = {(cuuint64_t)o.ldd * 2};
+  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.D, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                   CUDA_SUCCESS;
+}
+
+// How bm x bn tiles go to the SMs: in whole rounds, and, from three rounds on, the tiles left
+// over in the narrowest parts that still make one round (20011 x 1024 x 2048 in 128 x 256
+// tiles, four rounds and 36 tiles in four parts each: 25.4 against 27.5 us in 4 bits, 39.7
+// against 42.7 with 8-bit A, before the ring's fourth stage; with fewer rounds a smaller tile
+// is better: 1000 x 2048 x 4096 8.3 against 10.0).
+struct Plan {
+  int64_t nt, rounds, left, full, items;
+  int pw;  // columns of a part, bn where nothing is split
+  Tiles tiles(int bn) const {
+    return {(int)nt, (int)full, (int)items, (bn + pw - 1) / pw, pw};
+  }
+};
+Plan plan(int64_t M, int64_t N, int64_t bm, int bn, int64_t sms) {
+  Plan p;
+  p.nt = (N + bn - 1) / bn;
+  const int64_t tiles = (M + bm - 1) / bm * p.nt;
+  p.rounds = tiles / sms;
+  p.left = tiles % sms;
+  p.pw = bn;
+  for (int pw = 64; p.rounds > 2 && p.left && pw < bn && pw <= 128; pw += 64)
+    if (p.left * ((bn + pw - 1) / pw) <= sms) {
+      p.pw = pw;
+      break;
+    }
+  p.full = p.pw < bn ? tiles - p.left : tiles;
+  p.items = p.full + (tiles - p.full) * ((bn + p.pw - 1) / p.pw);
+  return p;
 }
 
 template <int AF, int H, int BN>
@@ -318,7 +457,7 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   g.D = static_cast<__nv_bfloat16*>(o.D);
   g.rs = static_cast<const uint8_t*>(o.As);
   g.cs = static_cast<const uint8_t*>(o.Ws);
-  const Plan p = plan(o.M, o.N, H * BM, BN, 64, sms);
+  const Plan p = plan(o.M, o.N, H * BM, BN, sms);
   if (p.items > INT32_MAX) return cudaErrorInvalidValue;
   g.tiles = p.tiles(BN);
   g.nkb = (int)(Kp / 128);
@@ -341,27 +480,31 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// The tile.  The SMs share L2's bandwidth and a tile's time goes by the bytes its stages bring
-// in; of four tiles the one with the least bytes over the rounds that the tiles take on the
-// SMs.  On one B200, us with 4-bit A at 256 x 192, 128 x 256, 128 x 192 and 128 x 128:
-// 32768 x 6464 x 1024 120, 129, 128, 132; 8192 x 8192 x 8192 195, 215, 210, 233; 16384 x 1024
-// x 2048 28.2, 25.4, 28.1, 25.4; 1000 x 2048 x 4096 13.4, 10.3, 9.0, 8.5; 300 x 6464 x 1024
-// 8.2, 6.2, 6.0, 6.2.
+// The tile.  A round of 256 x 192, 128 x 256, 128 x 192 and 128 x 128 tiles takes about 150,
+// 100, 78 and 59 parts of the same time, whatever K and A's type (1.5, 1, 0.75 and 0.5 by their
+// products: small tiles bring in more bytes for each); of the four the one that needs the least
+// in its rounds and parts.  On one B200, us in 4 bits / with 8-bit A:
+//   32768 x 6464 x 1024  119 121 123 133    191 191 202 225
+//   20011 x 1024 x 2048  25.8 22.3 25.7 26.3  40.0 35.2 40.6 42.9
+//   8192 x 8192 x 8192   194 195 212 231    364 352 385 440
+//   4096 x 6464 x 1024   20.0 19.2 18.9 21.0  27.4 26.9 28.8 33.3
+//   3001 x 2000 x 1500   9.0 10.4 9.7 10.3  12.4 14.3 13.1 14.4
+//   1500 x 6464 x 1024   11.7 11.7 10.0 11.0  15.8 15.1 14.0 16.4
+//   1000 x 2048 x 4096   13.1 10.4 9.7 8.3  20.3 14.9 13.9 12.6
 template <int AF>
 cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int split = split_of(o.M, o.N, o.K, AF, sms);
   if (split > 0) return launch_split(AF, o, split, s);
-  auto cost = [&](int64_t bm, int bn) {
-    const Plan p = plan(o.M, o.N, bm, bn, 64, sms);
-    const int64_t rows = (AF == mx::kFp4 ? 1 : 2) * bm;
-    return p.rounds * (rows + bn) + (p.left ? rows + p.pw : 0);
+  auto cost = [&](int64_t bm, int bn, int64_t round) {
+    const Plan p = plan(o.M, o.N, bm, bn, sms);
+    return p.rounds * round + (p.left ? round * p.pw / bn : 0);
   };
-  const int64_t c[4] = {cost(256, 192), cost(128, 256), cost(128, 192), cost(128, 128)};
+  const int64_t c[4] = {cost(256, 192, 150), cost(128, 256, 100), cost(128, 192, 78),
+                        cost(128, 128, 59)};
   int best = 0;
   for (int i = 1; i < 4; ++i)
     if (c[i] < c[best]) best = i;
-  if (pair_cost(o.M, o.N, o.K, AF, sms) < c[best]) return launch_pair(AF, o, sms, s);
   return best == 0   ? launch<AF, 2, 192>(o, sms, s)
          : best == 1 ? launch<AF, 1, 256>(o, sms, s)
          : best == 2 ? launch<AF, 1, 192>(o, sms, s)
@@ -380,13 +523,12 @@ cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const voi
 
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count) {
   const unsigned int zero = 0;
-  unsigned int split = 0, pair = 0;
+  unsigned int split = 0;
   cudaError_t e = cudaMemcpyFromSymbol(count, g_gemm_mx_wait_timeouts, sizeof(unsigned int));
   if (e == cudaSuccess)
     e = cudaMemcpyToSymbol(g_gemm_mx_wait_timeouts, &zero, sizeof(unsigned int));
   if (e == cudaSuccess) e = gemm_mx::read_and_clear_split_timeouts(&split);
-  if (e == cudaSuccess) e = gemm_mx::read_and_clear_pair_timeouts(&pair);
-  if (e == cudaSuccess) *count += split + pair;
+  if (e == cudaSuccess) *count += split;
   return e;
 }
 

@@ -352,10 +352,10 @@ namespace gemm_mx {
 //   16 x 1024 x 8192     9.8  8.2  6.4  5.7  16.4 11.3  8.2  6.6
 //   16 x 8192 x 8192    11.6 10.9 10.4 13.5  17.5 13.0 11.5 15.3
 // and with gemm_mx.cu's tile, over 2, 4 and 8:
-//   128 x 6464 x 1024    5.2  6.5  9.3        6.2  7.2  9.4 17.1
-//   128 x 1024 x 8192   10.8  9.8  8.2  7.7  17.5 13.3  9.8  8.3
-//   128 x 4096 x 4096    7.7  8.2  7.9 11.4  11.0 10.3  9.2 11.8
-//   1024 x 1024 x 8192  11.4 10.8 12.3 20.9  18.6 14.8 15.0 24.1
+//   128 x 6464 x 1024    4.7  6.3  9.1        5.9  7.2  9.3 16.7
+//   128 x 1024 x 8192   10.3  9.3  8.2  7.3  16.9 12.9  9.8  8.2
+//   128 x 4096 x 4096    7.7  7.7  8.2 11.3  10.8  9.8  8.8 11.8
+//   1024 x 1024 x 8192  10.8 10.3 12.3 21.1  17.5 13.9 14.6 23.7
 int split_of(int64_t M, int64_t N, int64_t K, int a_fmt, int64_t sms) {
   const int64_t tiles = ((N + 127) / 128) * ((M + 127) / 128);
   const int64_t stage = a_fmt == mx::kFp4 ? 256 : 128, nk = (K + stage - 1) / stage;
