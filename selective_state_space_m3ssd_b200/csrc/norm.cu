@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
 template <typename T, typename R, bool DRES, int NV, int ACC>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[32];
+  cudaTriggerProgrammaticLaunchCompletion();  // norm_dw_kernel may be launched: it waits itself
   const int d = (int)a.d;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -263,12 +264,13 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
 
 // dw = sum of the partial rows, in a fixed order: a CTA takes eight columns, thread (c, p)
 // every 32nd partial row of column c, then the 32 sums.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int nparts,
-                                                      int64_t d, float* __restrict__ dw) {
+__global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, int nparts, int64_t d,
+                                                      float* dw) {
   __shared__ float red[32][8];
   const int c8 = threadIdx.x & 7, p0 = threadIdx.x >> 3;
   const int64_t c = (int64_t)blockIdx.x * 8 + c8;
   float s = 0.f;
+  cudaGridDependencySynchronize();  // launched before the backward's end: its sums are there
   if (c < d) {
 #pragma unroll 8
     for (int p = p0; p < nparts; p += 32) s += part[(int64_t)p * d + c];
@@ -393,9 +395,19 @@ cudaError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t s) {
                          : (a.res_bf16 ? bwd_t<float, __nv_bfloat16>(a, s)
                                        : bwd_t<float, float>(a, s));
   if (e != cudaSuccess) return e;
-  norm_dw_kernel<<<(unsigned)((a.d + 7) / 8), 256, 0, s>>>(a.part, (int)partial_rows(a.rows, a.d),
-                                                          a.d, a.dw);
-  return cudaGetLastError();
+  // its CTAs may take their places while the backward's last ones run
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.d + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, norm_dw_kernel, (const float*)a.part,
+                         (int)partial_rows(a.rows, a.d), (int64_t)a.d, a.dw);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace m3ssd
