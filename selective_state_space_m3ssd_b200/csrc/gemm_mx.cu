@@ -7,8 +7,8 @@
 // kind::mxf4 (A in 4 bits) or kind::mxf8f6f4 (A in 8 bits; TMA spreads the packed 4-bit
 // codes of W over 8-bit containers as it loads them) multiplies value times scale.
 //
-// A tile is 128 H rows of A by BN of W.  One persistent CTA per SM; warp 0 copies, warp 1
-// issues the scale copies and the products, four warps a half are the epilogue.  The
+// A tile is 128 rows of A by BN of W.  One persistent CTA per SM; warp 0 copies, warp 1
+// issues the scale copies and the products, four are the epilogue.  The
 // accumulators alternate where two fit beside the scales in TMEM; with one, the epilogue's
 // first step, the whole row into registers as bf16, is all the products wait for.  Every stage
 // of the ring has its own TMEM columns for its scales: they are free when the stage is (the
@@ -25,7 +25,7 @@
 // 1024 131 against 120).
 //
 // What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
-// writes at HBM's 3.9 TB/s of them, 119 taken); with a long K what the copies bring in against
+// writes at HBM's 3.9 TB/s of them, 120 taken); with a long K what the copies bring in against
 // what the products read: the ring takes in 50 to 55 bytes a cycle and SM, 75 to 96 would keep
 // the products at their peak.  Measured and not kept: L2 prefetches of the stages behind the
 // ring (3 to 8 % slower); pairs of CTAs (256 x 256, W brought in once for both, but no second
@@ -51,30 +51,27 @@ using namespace gemm_mx;
 
 constexpr uint32_t kStgBytes = 32 * 128;  // an output block: 32 rows x 64 bf16 columns
 
-// AF: A's format.  H: 128-row halves of a tile.  A stage is 128 bytes of K a row: 256 values
-// in 4 bits, 128 in 8.
-template <int AF, int H, int BN>
+// AF: A's format.  A stage is 128 bytes of K a row: 256 values in 4 bits, 128 in 8.
+template <int AF, int BN>
 struct Cfg {
   static constexpr int ATOMS = AF == mx::kFp4 ? 2 : 1;  // scale tiles along K a stage
   static constexpr int NSB = (BN + 127) / 128;          // scale tiles along the columns
-  static constexpr int EPI_WARPS = 4 * H, THREADS = 32 * (2 + EPI_WARPS);
-  static constexpr uint32_t R_BYTES = H * BM * 128, C_BYTES = BN * 128;
+  static constexpr int EPI_WARPS = 4, THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr uint32_t A_BYTES = BM * 128, W_BYTES = BN * 128;
   // bytes the copies of a stage count on its barrier: W's 4-bit codes count as they are in
   // global memory, whether or not they are spread
-  static constexpr uint32_t R_TX = R_BYTES;
-  static constexpr uint32_t C_ROW_TX = AF != mx::kFp4 ? 64 : 128;
-  static constexpr uint32_t SR_BYTES = H * ATOMS * kTile, SC_BYTES = NSB * ATOMS * kTile;
-  static constexpr int STAGE = R_BYTES + C_BYTES + SR_BYTES + SC_BYTES;
+  static constexpr uint32_t W_ROW_TX = AF != mx::kFp4 ? 64 : 128;
+  static constexpr uint32_t SA_BYTES = ATOMS * kTile, SW_BYTES = NSB * ATOMS * kTile;
+  static constexpr int STAGE = A_BYTES + W_BYTES + SA_BYTES + SW_BYTES;
   static constexpr int ROOM = 226 * 1024 - EPI_WARPS * (int)kStgBytes - 1024;
   static constexpr int STAGES = ROOM / STAGE < 8 ? ROOM / STAGE : 8;
-  static constexpr int SF_COLS = ATOMS * 4 * (H + NSB);     // TMEM columns of a stage's scales
-  static constexpr int ACC_COLS = H * BN;  // an accumulator, its halves side by side
+  static constexpr int SF_COLS = ATOMS * 4 * (1 + NSB);  // TMEM columns of a stage's scales
   // two accumulators, where they fit, alternate between the products and the epilogue
-  static constexpr int NACC = 2 * ACC_COLS + STAGES * SF_COLS <= 512 ? 2 : 1;
-  static constexpr int COLS = NACC * ACC_COLS + STAGES * SF_COLS;
+  static constexpr int NACC = 2 * BN + STAGES * SF_COLS <= 512 ? 2 : 1;
+  static constexpr int COLS = NACC * BN + STAGES * SF_COLS;
   static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
-  static_assert(EPI_WARPS * (BN / 64) * (int)kStgBytes <= STAGES * (int)(R_BYTES + C_BYTES),
+  static_assert(EPI_WARPS * (BN / 64) * (int)kStgBytes <= STAGES * (int)(A_BYTES + W_BYTES),
                 "the last item's staging");
   // operand formats of the instruction descriptor (kind::mxf4: E2M1 = 1; kind::mxf8f6f4:
   // E4M3 = 0, E2M1 = 5)
@@ -85,11 +82,11 @@ struct Cfg {
 template <typename C>
 struct Smem {
   // every buffer a TMA copy reads or writes starts on a 1024-byte boundary
-  uint8_t r[C::STAGES][C::R_BYTES];
-  uint8_t c[C::STAGES][C::C_BYTES];
+  uint8_t a[C::STAGES][C::A_BYTES];
+  uint8_t w[C::STAGES][C::W_BYTES];
   uint8_t stg[C::EPI_WARPS][kStgBytes];
-  uint8_t sr[C::STAGES][C::SR_BYTES];
-  uint8_t sc[C::STAGES][C::SC_BYTES];
+  uint8_t sa[C::STAGES][C::SA_BYTES];
+  uint8_t sw[C::STAGES][C::SW_BYTES];
   uint64_t full[C::STAGES];
   uint64_t empty[C::STAGES];
   uint64_t tfull[2];
@@ -100,8 +97,8 @@ struct Smem {
 };
 
 struct MMaps {
-  CUtensorMap r, c;  // codes of the rows and the columns operand, box 128 bytes x 128 H / BN rows
-  CUtensorMap c64;   // the columns operand in boxes of 64 rows
+  CUtensorMap a, w;  // codes, boxes of 128 bytes x 128 and BN rows
+  CUtensorMap w64;   // W's in boxes of 64 rows
   CUtensorMap d;     // bf16 (N, M) with row stride ldd, box 64 x 32, 128-byte swizzle (when vec)
 };
 
@@ -126,11 +123,10 @@ struct MArgs {
   int M, N;  // of D
   int64_t ldd;
   __nv_bfloat16* D;
-  const uint8_t* rs;  // scales of the rows and the columns operand
-  const uint8_t* cs;
-  Tiles tiles;        // the items of the CTAs
-  int nkb;            // 128-column groups of K
-  int rrb, crb;       // 128-row blocks of the rows and the columns operand
+  const uint8_t *sa, *sw;  // scales
+  Tiles tiles;             // the items of the CTAs
+  int nkb;                 // 128-column groups of K
+  int nb;                  // 128-row blocks of W
   bool vec;
 };
 
@@ -204,10 +200,10 @@ __device__ __forceinline__ void store_rows(const uint32_t (&pk)[BN / 64][32], in
   }
 }
 
-template <int AF, int H, int BN>
-__global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
+template <int AF, int BN>
+__global__ void __launch_bounds__(Cfg<AF, BN>::THREADS, 1)
     gemm_mx_kernel(MArgs g, const __grid_constant__ MMaps tm) {
-  using C = Cfg<AF, H, BN>;
+  using C = Cfg<AF, BN>;
   constexpr int STAGES = C::STAGES, ATOMS = C::ATOMS, NSB = C::NSB;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   const uint32_t raw_addr = tc5::saddr(smem_raw);
@@ -232,7 +228,7 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  const uint32_t tmem = sm.tmem, sf0 = tmem + C::NACC * C::ACC_COLS;
+  const uint32_t tmem = sm.tmem, sf0 = tmem + C::NACC * BN;
 
   if (warp == 0) {
     // ---- producer
@@ -242,8 +238,8 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     bool ok = true;
     for (int t = blockIdx.x; ok && t < g.tiles.items; t += gridDim.x) {
       const Item it = item_of<BN>(g.tiles, t);
-      const int mb = it.mb, rb0 = it.col0 / 128;  // the columns operand's first scale tile
-      const int nsb = max(0, min(NSB, g.crb - rb0)), nsr = min(H, g.rrb - mb * H);
+      const int mb = it.mb, rb0 = it.col0 / 128;  // W's first scale tile
+      const int nsb = max(0, min(NSB, g.nb - rb0));
       for (int kb = 0; kb < nk; ++kb) {
         ok = wait_all(&sm.empty[stage], phase ^ 1u, err);
         if (!ok) break;
@@ -251,20 +247,19 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
           const int a0 = kb * ATOMS, na = min(ATOMS, g.nkb - a0);
           uint64_t* const full = &sm.full[stage];
           tc5::mbar_arrive_expect_tx(
-              full, C::R_TX + it.w * C::C_ROW_TX + (uint32_t)((nsr + nsb) * na) * kTile);
-          tc5::tma_load_2d(tc5::saddr(sm.r[stage]), &tm.r, full, kb * 128, mb * (H * BM));
+              full, C::A_BYTES + it.w * C::W_ROW_TX + (uint32_t)((1 + nsb) * na) * kTile);
+          tc5::tma_load_2d(tc5::saddr(sm.a[stage]), &tm.a, full, kb * 128, mb * BM);
           if (it.w == BN)
-            tc5::tma_load_2d(tc5::saddr(sm.c[stage]), &tm.c, full, kb * 128, it.col0);
+            tc5::tma_load_2d(tc5::saddr(sm.w[stage]), &tm.w, full, kb * 128, it.col0);
           else
             for (int c = 0; c < it.w; c += 64)
-              tc5::tma_load_2d(tc5::saddr(sm.c[stage]) + c * 128, &tm.c64, full, kb * 128,
+              tc5::tma_load_2d(tc5::saddr(sm.w[stage]) + c * 128, &tm.w64, full, kb * 128,
                                it.col0 + c);
-          for (int j = 0; j < nsr; ++j)
-            tc5::bulk_load(tc5::saddr(sm.sr[stage]) + j * ATOMS * kTile,
-                           g.rs + ((int64_t)(mb * H + j) * g.nkb + a0) * kTile, na * kTile, full);
+          tc5::bulk_load(tc5::saddr(sm.sa[stage]), g.sa + ((int64_t)mb * g.nkb + a0) * kTile,
+                         na * kTile, full);
           for (int j = 0; j < nsb; ++j)
-            tc5::bulk_load(tc5::saddr(sm.sc[stage]) + j * ATOMS * kTile,
-                           g.cs + ((int64_t)(rb0 + j) * g.nkb + a0) * kTile, na * kTile, full);
+            tc5::bulk_load(tc5::saddr(sm.sw[stage]) + j * ATOMS * kTile,
+                           g.sw + ((int64_t)(rb0 + j) * g.nkb + a0) * kTile, na * kTile, full);
         }
         __syncwarp();
         armed |= 1u << stage;
@@ -291,47 +286,38 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
       ok = wait_all(&sm.tempty[acc], aphase ^ 1u, err);
       if (!ok) break;
       tc5::fence_after_sync();
-      const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+      const uint32_t d = tmem + (uint32_t)(acc * BN);
       for (int kb = 0; kb < nk; ++kb) {
         ok = wait_all(&sm.full[stage], phase, err);
         if (!ok) break;
         tc5::fence_after_sync();
         const int na = min(ATOMS, g.nkb - kb * ATOMS);
-        // the stage's columns: for each tile along K the halves' tiles, then the columns'
-        const uint32_t sfr = sf0 + (uint32_t)(stage * C::SF_COLS), sfc = sfr + ATOMS * H * 4;
-        const uint64_t dc = tc5::desc_sw128(tc5::saddr(sm.c[stage]), 16, 1024);
-        const uint64_t dr0 = tc5::desc_sw128(tc5::saddr(sm.r[stage]), 16, 1024);
-        const uint64_t dsr = tc5::desc_scales(tc5::saddr(sm.sr[stage]));
-        const uint64_t dsc = tc5::desc_scales(tc5::saddr(sm.sc[stage]));
+        // the stage's columns: A's tiles along K, then W's
+        const uint32_t sfa = sf0 + (uint32_t)(stage * C::SF_COLS), sfw = sfa + ATOMS * 4;
+        const uint64_t dw = tc5::desc_sw128(tc5::saddr(sm.w[stage]), 16, 1024);
+        const uint64_t da = tc5::desc_sw128(tc5::saddr(sm.a[stage]), 16, 1024);
+        const uint64_t dsa = tc5::desc_scales(tc5::saddr(sm.sa[stage]));
+        const uint64_t dsw = tc5::desc_scales(tc5::saddr(sm.sw[stage]));
         if (leader) {
 #pragma unroll
           for (int a = 0; a < ATOMS; ++a) {
             if (a < na) {
-#pragma unroll
-              for (int j = 0; j < H; ++j)
-                tc5::cp_scales(sfr + 4 * (a * H + j), dsr + (j * ATOMS + a) * (kTile / 16));
+              tc5::cp_scales(sfa + 4 * a, dsa + a * (kTile / 16));
 #pragma unroll
               for (int j = 0; j < NSB; ++j)
-                tc5::cp_scales(sfc + 4 * (a * NSB + j), dsc + (j * ATOMS + a) * (kTile / 16));
+                tc5::cp_scales(sfw + 4 * (a * NSB + j), dsw + (j * ATOMS + a) * (kTile / 16));
             }
           }
 #pragma unroll
-          for (int hh = 0; hh < H; ++hh) {
-            const uint64_t dr = dr0 + (uint64_t)(hh * BM * 128 / 16);
-            const uint32_t dh = d + (uint32_t)(hh * BN);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
-              if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
-                if (k / 2 < na)
-                  tc5::mma_mxf4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                                tc5::idesc_mx_sf(idesc, 2 * (k & 1)),
-                                sfr + 4 * (k / 2 * H + hh), sfc + 4 * NSB * (k / 2) + shift,
-                                kb > 0 || k > 0);
-              } else {  // 32 values, one block
-                tc5::mma_mxf8f6f4(dh, dr + (uint64_t)(2 * k), dc + (uint64_t)(2 * k),
-                                  tc5::idesc_mx_sf(idesc, k), sfr + 4 * hh, sfc + shift,
-                                  kb > 0 || k > 0);
-              }
+          for (int k = 0; k < 4; ++k) {  // +32 bytes a K step inside the swizzle atom
+            if (AF == mx::kFp4) {        // 64 values, two of a tile's four blocks
+              if (k / 2 < na)
+                tc5::mma_mxf4(d, da + (uint64_t)(2 * k), dw + (uint64_t)(2 * k),
+                              tc5::idesc_mx_sf(idesc, 2 * (k & 1)), sfa + 4 * (k / 2),
+                              sfw + 4 * NSB * (k / 2) + shift, kb > 0 || k > 0);
+            } else {  // 32 values, one block
+              tc5::mma_mxf8f6f4(d, da + (uint64_t)(2 * k), dw + (uint64_t)(2 * k),
+                                tc5::idesc_mx_sf(idesc, k), sfa, sfw + shift, kb > 0 || k > 0);
             }
           }
           tc5::commit(&sm.empty[stage]);
@@ -356,20 +342,20 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
     (void)tc5::mbar_wait(&sm.drain, 0, kWaitLimitNs);
     __syncwarp();
   } else {
-    // ---- epilogue: TMEM lane quarter q of half hh, one row of the rows operand a thread
-    const int q = warp & 3, ew = warp - 2, hh = ew >> 2;
+    // ---- epilogue: TMEM lane quarter q, one row a thread
+    const int q = warp & 3, ew = warp - 2;
     int acc = 0;
     uint32_t aphase = 0;
     for (int t = blockIdx.x; t < g.tiles.items; t += gridDim.x) {
       const Item it = item_of<BN>(g.tiles, t);
-      const int row0 = (it.mb * H + hh) * BM + 32 * q, col0 = it.col0;
+      const int row0 = it.mb * BM + 32 * q, col0 = it.col0;
       if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
         *err = 1;
         break;
       }
       tc5::fence_after_sync();
       const uint32_t tbase =
-          tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * C::ACC_COLS + hh * BN);
+          tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * BN);
       // the row into registers as bf16, then TMEM goes back: the stores below drain
       // while the next products run
       const int nch = min(it.w / 64, (g.N - col0 + 63) / 64);
@@ -379,7 +365,7 @@ __global__ void __launch_bounds__(Cfg<AF, H, BN>::THREADS, 1)
       __syncwarp();
       if (lane == 0) tc5::mbar_arrive(&sm.tempty[acc]);
       const bool last = t + (int)gridDim.x >= g.tiles.items;
-      store_rows<BN>(pk, nch, last ? sm.r[0] + ew * (BN / 64) * kStgBytes : sm.stg[ew], last, &tm.d,
+      store_rows<BN>(pk, nch, last ? sm.a[0] + ew * (BN / 64) * kStgBytes : sm.stg[ew], last, &tm.d,
                      g.D, g.ldd, g.M, g.N, g.vec, row0, col0);
       if (++acc == C::NACC) {
         acc = 0;
@@ -411,7 +397,7 @@ bool encode_output(CUtensorMap* m, const Operands& o) {
                    CUDA_SUCCESS;
 }
 
-// How bm x bn tiles go to the SMs: in whole rounds, and, from three rounds on, the tiles left
+// How 128 x bn tiles go to the SMs: in whole rounds, and, from three rounds on, the tiles left
 // over in the narrowest parts that still make one round (20011 x 1024 x 2048 in 128 x 256
 // tiles, four rounds and 36 tiles in four parts each: 25.4 against 27.5 us in 4 bits, 39.7
 // against 42.7 with 8-bit A, before the ring's fourth stage; with fewer rounds a smaller tile
@@ -423,10 +409,10 @@ struct Plan {
     return {(int)nt, (int)full, (int)items, (bn + pw - 1) / pw, pw};
   }
 };
-Plan plan(int64_t M, int64_t N, int64_t bm, int bn, int64_t sms) {
+Plan plan(int64_t M, int64_t N, int bn, int64_t sms) {
   Plan p;
   p.nt = (N + bn - 1) / bn;
-  const int64_t tiles = (M + bm - 1) / bm * p.nt;
+  const int64_t tiles = (M + BM - 1) / BM * p.nt;
   p.rounds = tiles / sms;
   p.left = tiles % sms;
   p.pw = bn;
@@ -440,75 +426,69 @@ Plan plan(int64_t M, int64_t N, int64_t bm, int bn, int64_t sms) {
   return p;
 }
 
-template <int AF, int H, int BN>
+template <int AF, int BN>
 cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
-  using C = Cfg<AF, H, BN>;
+  using C = Cfg<AF, BN>;
   const int64_t Kp = mx::pad128(o.K);
   MMaps tm;
   memset(&tm, 0, sizeof(tm));
-  const bool ok = encode_codes(&tm.r, o.A, o.M, Kp, AF, false, H * BM) &&
-                  encode_codes(&tm.c, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, BN) &&
-                  encode_codes(&tm.c64, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, 64);
+  const bool ok = encode_codes(&tm.a, o.A, o.M, Kp, AF, false, BM) &&
+                  encode_codes(&tm.w, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, BN) &&
+                  encode_codes(&tm.w64, o.W, o.N, Kp, mx::kFp4, AF != mx::kFp4, 64);
   if (!ok) return cudaErrorInvalidValue;
   MArgs g{};
   g.M = (int)o.M;
   g.N = (int)o.N;
   g.ldd = o.ldd;
   g.D = static_cast<__nv_bfloat16*>(o.D);
-  g.rs = static_cast<const uint8_t*>(o.As);
-  g.cs = static_cast<const uint8_t*>(o.Ws);
-  const Plan p = plan(o.M, o.N, H * BM, BN, sms);
+  g.sa = static_cast<const uint8_t*>(o.As);
+  g.sw = static_cast<const uint8_t*>(o.Ws);
+  const Plan p = plan(o.M, o.N, BN, sms);
   if (p.items > INT32_MAX) return cudaErrorInvalidValue;
   g.tiles = p.tiles(BN);
   g.nkb = (int)(Kp / 128);
-  g.rrb = (int)((o.M + 127) / 128);
-  g.crb = (int)((o.N + 127) / 128);
+  g.nb = (int)((o.N + 127) / 128);
   g.vec = encode_output(&tm.d, o);
   const size_t smem = sizeof(Smem<C>) + 1024;
   static_assert(sizeof(Smem<C>) + 1024 <= 232448, "one CTA's shared memory");
-  static_assert(offsetof(Smem<C>, c) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&
-                    offsetof(Smem<C>, sr) % 1024 == 0,
+  static_assert(offsetof(Smem<C>, w) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&
+                    offsetof(Smem<C>, sa) % 1024 == 0,
                 "TMA buffers on 1024-byte boundaries");
   static std::atomic<uint64_t> done;
   const cudaError_t e = once_per_device(done, [&]() {
-    return cudaFuncSetAttribute(gemm_mx_kernel<AF, H, BN>,
+    return cudaFuncSetAttribute(gemm_mx_kernel<AF, BN>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (e != cudaSuccess) return e;
-  gemm_mx_kernel<AF, H, BN>
+  gemm_mx_kernel<AF, BN>
       <<<(unsigned)(p.items < sms ? p.items : sms), C::THREADS, smem, s>>>(g, tm);
   return cudaGetLastError();
 }
 
-// The tile.  A round of 256 x 192, 128 x 256, 128 x 192 and 128 x 128 tiles takes about 150,
-// 100, 78 and 59 parts of the same time, whatever K and A's type (1.5, 1, 0.75 and 0.5 by their
-// products: small tiles bring in more bytes for each); of the four the one that needs the least
-// in its rounds and parts.  On one B200, us in 4 bits / with 8-bit A:
-//   32768 x 6464 x 1024  119 121 123 133    191 191 202 225
-//   20011 x 1024 x 2048  25.8 22.3 25.7 26.3  40.0 35.2 40.6 42.9
-//   8192 x 8192 x 8192   194 195 212 231    364 352 385 440
-//   4096 x 6464 x 1024   20.0 19.2 18.9 21.0  27.4 26.9 28.8 33.3
-//   3001 x 2000 x 1500   9.0 10.4 9.7 10.3  12.4 14.3 13.1 14.4
-//   1500 x 6464 x 1024   11.7 11.7 10.0 11.0  15.8 15.1 14.0 16.4
-//   1000 x 2048 x 4096   13.1 10.4 9.7 8.3  20.3 14.9 13.9 12.6
+// The tile.  A round of 128 x 256, 128 x 192 and 128 x 128 tiles takes about 100, 78 and 59
+// parts of the same time, whatever K and A's type (small tiles bring in more bytes for each
+// product); of the three the one that needs the least in its rounds and parts.  On one B200, us
+// in 4 bits / with 8-bit A:
+//   32768 x 6464 x 1024  121 123 133       191 202 225
+//   20011 x 1024 x 2048  22.3 25.7 26.3    35.2 40.6 42.9
+//   8192 x 8192 x 8192   195 212 231       352 385 440
+//   4096 x 6464 x 1024   19.2 18.9 21.0    26.9 28.8 33.3
+//   1500 x 6464 x 1024   11.7 10.0 11.0    15.1 14.0 16.4
+//   1000 x 2048 x 4096   10.4 9.7 8.3      14.9 13.9 12.6
+// (256 x 192 gained 1 to 5 % on a few shapes and lost 15 % on others.)
 template <int AF>
 cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int split = split_of(o.M, o.N, o.K, AF, sms);
   if (split > 0) return launch_split(AF, o, split, s);
-  auto cost = [&](int64_t bm, int bn, int64_t round) {
-    const Plan p = plan(o.M, o.N, bm, bn, sms);
+  auto cost = [&](int bn, int64_t round) {
+    const Plan p = plan(o.M, o.N, bn, sms);
     return p.rounds * round + (p.left ? round * p.pw / bn : 0);
   };
-  const int64_t c[4] = {cost(256, 192, 150), cost(128, 256, 100), cost(128, 192, 78),
-                        cost(128, 128, 59)};
-  int best = 0;
-  for (int i = 1; i < 4; ++i)
-    if (c[i] < c[best]) best = i;
-  return best == 0   ? launch<AF, 2, 192>(o, sms, s)
-         : best == 1 ? launch<AF, 1, 256>(o, sms, s)
-         : best == 2 ? launch<AF, 1, 192>(o, sms, s)
-                     : launch<AF, 1, 128>(o, sms, s);
+  const int64_t wide = cost(256, 100), mid = cost(192, 78), small = cost(128, 59);
+  return wide <= mid && wide <= small ? launch<AF, 256>(o, sms, s)
+         : mid <= small               ? launch<AF, 192>(o, sms, s)
+                                      : launch<AF, 128>(o, sms, s);
 }
 
 }  // namespace
