@@ -682,8 +682,9 @@ def _launch(name: str, dev, *args):
     device current (a stream, a workspace size and a launch all go by it)."""
     import torch
     f = getattr(_lib or load(), name)
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if torch._C._cuda_getDevice() == index:
         st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -695,8 +696,9 @@ def _launch(name: str, dev, *args):
 def _need_all(dev, *checks):
     """:func:`_need` for (tensor, name, dtype, shape) on the CUDA device ``dev``, in one
     loop: a decode step checks some twenty tensors."""
+    index = dev.index  # of a CUDA device; a CPU tensor's is -1
     for t, name, dtype, shape in checks:
-        if t is not None and (t.dtype != dtype or t.shape != shape or t.device != dev or
+        if t is not None and (t.dtype != dtype or t.shape != shape or t.get_device() != index or
                               not t.is_contiguous()):
             _need(t, name, dtype, shape, dev)
 
@@ -749,10 +751,11 @@ def _mx_of(t: MXTensor) -> Mx:
 def _mx_struct(t: MXTensor, name: str, device) -> Mx:
     """The C descriptor of a caller's tensor, its storage checked."""
     import torch
-    f, kp = _mx_format(t.fmt), _pad128(t.cols)
-    _need(t.codes, name + ".codes", torch.uint8, (t.rows, kp if f == MXFP8 else kp // 2), device)
-    _need(t.scales, name + ".scales", torch.uint8, (_pad128(t.rows) * (kp // 32),), device)
-    return _mx_of(t)
+    f, kp, u8 = _mx_format(t.fmt), _pad128(t.cols), torch.uint8
+    codes, scales = t.codes, t.scales
+    _need(codes, name + ".codes", u8, (t.rows, kp if f == MXFP8 else kp // 2), device)
+    _need(scales, name + ".scales", u8, (_pad128(t.rows) * (kp // 32),), device)
+    return Mx(f, 0, t.rows, t.cols, codes.data_ptr(), scales.data_ptr())
 
 
 def _rows_stride(x, name):
@@ -885,7 +888,7 @@ def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=No
     else:
         _need(dw, "dw", f32, (d,), dev)
     dims = NormDims(rows, d, _xdtype(dy), _xdtype(r), 0.0, 0)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         need = add_rmsnorm_bwd_workspace_size(dims)
     else:
         with torch.cuda.device(dev):
