@@ -466,9 +466,10 @@ m3ssd_status m3ssd_mx_dequant(const m3ssd_mx* in, int32_t x_dtype, void* x, int6
  * D (M x N, bf16, row stride ldd >= N) = A W^T of MX operands A (M x K, either format) and
  * W (N x K, M3SSD_MXFP4; else M3SSD_ERR_UNSUPPORTED), beside m3ssd_gemm_bf16 for the block's
  * projections with quantised weights.  Products of the held values, fp32 accumulation on
- * the tensor cores, each output rounded once to bf16.  D 2-byte aligned (tensor stores
- * when D is 16-byte aligned and N and ldd are multiples of 8).  No allocation, no
- * synchronisation.
+ * the tensor cores, each output rounded once to bf16.  The order of the sums over K goes by
+ * the shapes alone: the same call gives the same bits, one of other M or N may round an
+ * output otherwise.  D 2-byte aligned (tensor stores when D is 16-byte aligned and N and ldd
+ * are multiples of 8).  No allocation, no synchronisation.
  */
 m3ssd_status m3ssd_gemm_mx(const m3ssd_mx* A, const m3ssd_mx* W, void* D, int64_t ldd,
                            void* stream);

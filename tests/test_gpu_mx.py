@@ -227,6 +227,39 @@ def test_gemm_long_k(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M", [16, 100])
+def test_gemm_long_k_captured(fmt, M):
+    """Products with K over a cluster in two captured graphs, replayed on two streams on new
+    values; a NaN block stays in its row and column."""
+    x, w = values(M, 8192, 6).cuda(), m3.mx_quant(values(200, 8192, 7).cuda(), "mxfp4")
+    def run():
+        return m3.gemm_mx(m3.mx_quant(x, fmt), w)
+    run()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run()
+        graphs.append((g, out))
+    x.mul_(0.75)
+    x[2, 5000] = float("nan")
+    want = run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for (g, _), side in zip(graphs, streams):
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                g.replay()
+    torch.cuda.synchronize()
+    nan = torch.isnan(want)
+    assert nan[2].all() and int(nan.sum()) == 200
+    for _, out in graphs:
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert m3.device_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("M", [3, 200])
 def test_gemm_nan_blocks_stay_in_their_rows(fmt, M):
     A = values(M, 160, 1)
