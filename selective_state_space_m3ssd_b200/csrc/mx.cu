@@ -6,7 +6,7 @@
 // a block's largest magnitude is one shuffle, the four scale bytes of the group leave as one
 // 32-bit word, the tile layout's unit, and what a group costs (its place, scale and word)
 // is shared by sixteen values.  Rows that do not allow 32-byte accesses pass through shared
-// memory, element by element in the lanes' order on the global side.
+// memory, 32 consecutive elements an access on the global side, 16 bytes a lane on the other.
 // 32768 x 2048 bf16 to 4 bits and back on one B200: 60 us for both; HBM takes 3.9 TB/s of
 // writes alone (a fill), 6.5 of a copy, so the two cannot take less than 26 and 34.  Eight
 // values a lane, with a division a group and 16-byte loads, took 107.
@@ -20,7 +20,6 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kGroup = 8;   // lanes of a 128-column group
-constexpr int kUnroll = 2;  // groups a lane has in flight
 
 struct MxArgs {
   uint32_t rows, cols, nkb;  // nkb: 128-column groups a row
@@ -59,6 +58,7 @@ struct Raw16;
 template <>
 struct Raw16<__nv_bfloat16> {
   float w[8];  // two bf16 a word
+  __device__ float& word(int j) { return w[j]; }
   __device__ void load(const __nv_bfloat16* p) { mx::load8(reinterpret_cast<const float*>(p), w); }
   __device__ void clear() {
 #pragma unroll
@@ -72,10 +72,21 @@ struct Raw16<__nv_bfloat16> {
       v[2 * j + 1] = __uint_as_float(u & 0xffff0000u);
     }
   }
+  __device__ void put(const float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      w[j] = __uint_as_float(*reinterpret_cast<uint32_t*>(&h));
+    }
+  }
+  __device__ void store(__nv_bfloat16* p) const {
+    mx::store8(reinterpret_cast<float*>(p), w);
+  }
 };
 template <>
 struct Raw16<float> {
   float a[8], b[8];
+  __device__ float& word(int j) { return j < 8 ? a[j] : b[j - 8]; }
   __device__ void load(const float* p) {
     mx::load8(p, a);
     mx::load8(p + 8, b);
@@ -91,26 +102,18 @@ struct Raw16<float> {
       v[8 + j] = b[j];
     }
   }
+  __device__ void put(const float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      a[j] = v[j];
+      b[j] = v[8 + j];
+    }
+  }
+  __device__ void store(float* p) const {
+    mx::store8(p, a);
+    mx::store8(p + 8, b);
+  }
 };
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&v)[16]) {
-  float w[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-    w[j] = __uint_as_float(*reinterpret_cast<uint32_t*>(&h));
-  }
-  mx::store8(reinterpret_cast<float*>(p), w);
-}
-__device__ __forceinline__ void store16(float* p, const float (&v)[16]) {
-  float a[8], b[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    a[j] = v[j];
-    b[j] = v[8 + j];
-  }
-  mx::store8(p, a);
-  mx::store8(p + 8, b);
-}
 // The scale word of a group, counted in words.
 __device__ __forceinline__ uint32_t word_index(uint32_t row, uint32_t kb, uint32_t nkb) {
   return (((row >> 7) * nkb + kb) << 7) + ((row & 31) << 2) + ((row >> 5) & 3);
@@ -120,11 +123,49 @@ __device__ __forceinline__ uint32_t word_index(uint32_t row, uint32_t kb, uint32
 // a multiple of 16 (a lane's sixteen values are all there or all padding); kAny.
 enum Access { kFull, kVec, kAny };
 
+// Groups a lane has in flight, and the CTAs an SM is to hold.  Element by element a lane's loads
+// are many already and more CTAs serve better: 5300 x 6314 to 4 bits and back 31.9 and 28.0 us
+// from fp32 (six CTAs), 26.7 and 20.9 from bf16 (five), against 44.2, 28.5, 31.3 and 21.9 with two
+// groups a lane and what registers allow (three or four CTAs).
+template <int ACC>
+constexpr int kUnrollOf = ACC == kAny ? 1 : 2;
+template <typename T, int ACC>
+constexpr int kCtasOf = ACC != kAny ? 1 : sizeof(T) == 4 ? 6 : 5;
+
+// kAny: a warp's four groups of 128 elements in shared memory.  Element e is lane e / 16's, as
+// units of 16 bytes whose order goes round with the lane, so that neither the accesses of 32
+// consecutive elements nor the lanes' 16-byte accesses meet in a bank.
+template <typename T>
+struct Stage {
+  static constexpr uint32_t kUnit = 16 / sizeof(T), kUnits = 16 / kUnit;
+  T v[512];
+  static __device__ __forceinline__ uint32_t turn(uint32_t lane) {
+    return kUnits == 4 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+  }
+  __device__ __forceinline__ T& at(uint32_t e) {
+    const uint32_t b = e >> 4;
+    return v[b * 16 + ((e / kUnit % kUnits) ^ turn(b)) * kUnit + e % kUnit];
+  }
+  __device__ __forceinline__ float4& unit(uint32_t lane, uint32_t u) {
+    return *reinterpret_cast<float4*>(v + lane * 16 + (u ^ turn(lane)) * kUnit);
+  }
+};
+// Group g's row (null where there is none) and the columns it has from the group's first on;
+// row and kb are those of each lane's group.
+template <typename T>
+__device__ __forceinline__ T* group_row(T* x, int64_t ldx, uint32_t cols, uint32_t rows, int g,
+                                        uint32_t row, uint32_t kb, uint32_t& have) {
+  const uint32_t r = __shfl_sync(0xffffffffu, row, kGroup * g);
+  const uint32_t c = __shfl_sync(0xffffffffu, kb, kGroup * g) * 128;
+  have = r < rows ? cols - c : 0;
+  return x + ((int64_t)r * ldx + c);
+}
+
 template <int FMT, typename T, int ACC>
-__global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
-  // kAny: a warp's four groups as elements; a lane reads its sixteen at a stride of 17, which
-  // spreads over the banks
-  __shared__ T stage[ACC == kAny ? kWarps : 1][ACC == kAny ? 32 * 17 : 1];
+__global__ void __launch_bounds__(kThreads, kCtasOf<T, ACC>)
+    mx_quant_kernel(MxArgs a) {
+  constexpr int kUnroll = kUnrollOf<ACC>;
+  __shared__ __align__(16) Stage<T> stage[ACC == kAny ? kWarps : 1];
   const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
   const uint32_t step = gridDim.x * (kThreads / kGroup);
   Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
@@ -132,28 +173,20 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
   // a warp goes round together (its shuffles): by its first group
   for (uint32_t base = w.i - lane / kGroup; base < a.total; base += kUnroll * step) {
     Raw16<T> raw[kUnroll];
-    float any[ACC == kAny ? kUnroll : 1][16];
+    T any[ACC == kAny ? kUnroll : 1][16];
     uint32_t at[kUnroll];
     const uint32_t i0 = w.i;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if constexpr (ACC == kAny) {
-        // group e / 128 of the warp's four, column e % 128, lane by lane
-        T* const buf = stage[warp];
-        __syncwarp();
+      if constexpr (ACC == kAny) {  // 32 consecutive elements of a group an access
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t src = 8 * (j / 4);  // a lane of the group, for its row and place
-          const uint32_t row = __shfl_sync(0xffffffffu, w.row, src),
-                         kb = __shfl_sync(0xffffffffu, w.kb, src);
-          const uint32_t e = 32 * j + lane, col = kb * 128 + (e & 127);
-          T val = from_f32<T>(0.f);
-          if (row < a.rows && col < a.cols) val = x[(int64_t)row * a.ldx + col];
-          buf[(e >> 4) * 17 + (e & 15)] = val;
+        for (int g = 0; g < 4; ++g) {
+          uint32_t have;
+          const T* const p = group_row(x, a.ldx, a.cols, a.rows, g, w.row, w.kb, have) + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            any[u][4 * g + j] = lane + 32 * j < have ? p[32 * j] : from_f32<T>(0.f);
         }
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) any[u][j] = to_f32(buf[lane * 17 + j]);
       } else {
         const uint32_t c = w.kb * 128 + sub * 16;
         if (w.i < a.total && (ACC == kFull || c < a.cols))
@@ -164,16 +197,29 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
       at[u] = word_index(w.row, w.kb, a.nkb);
       w.next();
     }
+    if constexpr (ACC == kAny) {
+      Stage<T>& st = stage[warp];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) st.at(32 * j + lane) = any[u][j];
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < (int)Stage<T>::kUnits; ++n) {
+          const float4 f = st.unit(lane, n);
+          raw[u].word(4 * n) = f.x;
+          raw[u].word(4 * n + 1) = f.y;
+          raw[u].word(4 * n + 2) = f.z;
+          raw[u].word(4 * n + 3) = f.w;
+        }
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t i = i0 + u * step;
       float v[16];
-      if constexpr (ACC == kAny) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = any[u][j];
-      } else {
-        raw[u].get(v);
-      }
+      raw[u].get(v);
       uint4 c;
       const uint32_t word = mx::quant16<FMT>(v, c);
       if (i < a.total) {
@@ -192,8 +238,10 @@ __global__ void __launch_bounds__(kThreads) mx_quant_kernel(MxArgs a) {
 }
 
 template <int FMT, typename T, int ACC>
-__global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
-  __shared__ T stage[ACC == kAny ? kWarps : 1][ACC == kAny ? 32 * 17 : 1];
+__global__ void __launch_bounds__(kThreads, kCtasOf<T, ACC>)
+    mx_dequant_kernel(MxArgs a) {
+  constexpr int kUnroll = kUnrollOf<ACC>;
+  __shared__ __align__(16) Stage<T> stage[ACC == kAny ? kWarps : 1];
   const uint32_t lane = threadIdx.x & 31, sub = lane % kGroup, warp = threadIdx.x >> 5;
   const uint32_t step = gridDim.x * (kThreads / kGroup);
   Walk w((blockIdx.x * kThreads + threadIdx.x) / kGroup, step, a.nkb);
@@ -233,23 +281,30 @@ __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
         v[2 * j + 1] = f.y * s;
       }
       if constexpr (ACC == kAny) {
-        T* const buf = stage[warp];
+        Stage<T>& st = stage[warp];
+        Raw16<T> raw;
+        raw.put(v);
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = from_f32<T>(v[j]);
+        for (int n = 0; n < (int)Stage<T>::kUnits; ++n)
+          st.unit(lane, n) = make_float4(raw.word(4 * n), raw.word(4 * n + 1), raw.word(4 * n + 2),
+                                         raw.word(4 * n + 3));
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t src = 8 * (j / 4);
-          const uint32_t r = __shfl_sync(0xffffffffu, row[u], src),
-                         k = __shfl_sync(0xffffffffu, kb[u], src);
-          const uint32_t e = 32 * j + lane, col = k * 128 + (e & 127);
-          if (r < a.rows && col < a.cols) x[(int64_t)r * a.ldx + col] = buf[(e >> 4) * 17 + (e & 15)];
+        for (int g = 0; g < 4; ++g) {
+          uint32_t have;
+          T* const p = group_row(x, a.ldx, a.cols, a.rows, g, row[u], kb[u], have) + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (lane + 32 * j < have) p[32 * j] = st.at(32 * (4 * g + j) + lane);
         }
       } else {
         const uint32_t c = kb[u] * 128 + sub * 16;
-        if (row[u] < a.rows && (ACC == kFull || c < a.cols))
-          store16(x + ((int64_t)row[u] * a.ldx + c), v);
+        if (row[u] < a.rows && (ACC == kFull || c < a.cols)) {
+          Raw16<T> raw;
+          raw.put(v);
+          raw.store(x + ((int64_t)row[u] * a.ldx + c));
+        }
       }
     }
   }
@@ -257,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) mx_dequant_kernel(MxArgs a) {
 
 template <int FMT, typename T, int ACC>
 cudaError_t launch(const MxArgs& a, bool quant, cudaStream_t s) {
-  const uint64_t per = (uint64_t)(kThreads / kGroup) * kUnroll;  // groups a CTA takes at a time
+  const uint64_t per = (uint64_t)(kThreads / kGroup) * kUnrollOf<ACC>;  // groups a CTA takes at a time
   const uint64_t want = (a.total + per - 1) / per, most = (uint64_t)current_device_sms() * 16;
   const unsigned grid = (unsigned)(want < most || most == 0 ? want : most);
   if (quant)
