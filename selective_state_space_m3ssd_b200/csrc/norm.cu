@@ -41,9 +41,11 @@ __device__ __forceinline__ float row_sum(float v, float* red, int& flip) {
   return t;
 }
 
-// How a thread's values lie in a row: eight consecutive ones in one access, eight
-// consecutive ones one by one, or eight that are blockDim.x apart.
-enum Access { kVec, kTail, kStrided };
+// How a thread's values lie in a row: eight consecutive ones in one access; the same of rows
+// that start inside such an access (kShift: columns from 8 i - shift on, shift being the
+// row's first element modulo 8; the row's ends one by one); eight consecutive ones one by
+// one; or eight that are blockDim.x apart.
+enum Access { kVec, kShift, kTail, kStrided };
 
 // Eight values of a row as loaded.
 template <typename T>
@@ -84,37 +86,67 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Raw<__nv_bfloat
   r.u = *reinterpret_cast<const uint4*>(p);
 }
 
-// Group k of the thread's values of a row (zeros past its end), and back.
+// Group k of the thread's values of a row, and back.  With kShift the first and the last access
+// of a row bring in its neighbours' ends too (inside() drops them; elements that another
+// CTA may be writing, in place, are among them), the tensor's last one is element by element;
+// else there are zeros outside the row.
 template <int ACC, typename T>
-__device__ __forceinline__ void load_row(const T* row, int k, int d, Raw<T>& r) {
-  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x);
+__device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, bool last,
+                                         Raw<T>& r) {
+  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - (ACC == kStrided ? 0 : shift);
   float v[8];
-  if constexpr (ACC == kVec) {
+  if constexpr (ACC == kVec || ACC == kShift) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     pack(v, r);
-    if (c < d) load_vec(row + c, r);  // d is a multiple of 8
+    if (c < d && (ACC == kVec || !last || c + 8 <= d)) {
+      load_vec(row + c, r);  // with kVec d is a multiple of 8
+    } else if (ACC == kShift && c < d) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j >= 0 && c + j < d) v[j] = to_f32(row[c + j]);
+      pack(v, r);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = ACC == kTail ? c + j : (int)threadIdx.x + (8 * k + j) * (int)blockDim.x;
-      v[j] = i < d ? to_f32(row[i]) : 0.f;
+      v[j] = i >= 0 && i < d ? to_f32(row[i]) : 0.f;
     }
     pack(v, r);
   }
 }
+// Zeros in place of what lies outside the row.
+template <int ACC>
+__device__ __forceinline__ void inside(float (&v)[8], int k, int d, int shift) {
+  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - shift;
+  if (ACC == kShift && (c < 0 || c + 8 > d)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < 0 || c + j >= d) v[j] = 0.f;
+  }
+}
 template <int ACC, typename T>
-__device__ __forceinline__ void store_row(T* row, int k, int d, const float (&v)[8]) {
-  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x);
-  if constexpr (ACC == kVec) {
-    if (c < d) mx::store8(row + c, v);
-  } else {
+__device__ __forceinline__ void store_row(T* row, int k, int d, int shift, const float (&v)[8]) {
+  const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - (ACC == kStrided ? 0 : shift);
+  if (ACC == kVec ? c < d : ACC == kShift && c >= 0 && c + 8 <= d) {
+    mx::store8(row + c, v);
+  } else if constexpr (ACC != kVec) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = ACC == kTail ? c + j : (int)threadIdx.x + (8 * k + j) * (int)blockDim.x;
-      if (i < d) row[i] = from_f32<T>(v[j]);
+      const int i = ACC != kStrided ? c + j : (int)threadIdx.x + (8 * k + j) * (int)blockDim.x;
+      if (i >= 0 && i < d) row[i] = from_f32<T>(v[j]);
     }
   }
+}
+// The tensors of a walker's columns (w, dw): aligned to nothing.
+template <int ACC>
+constexpr int kColumns = ACC == kVec || ACC == kShift ? kTail : ACC;
+// kShift: the columns by which the walker's rows start inside an access.  Its rows are a
+// multiple of eight apart (grid_of), so all have this one.
+template <int ACC>
+__device__ __forceinline__ int shift_of(int64_t first_row, int64_t d) {
+  return ACC == kShift ? (int)((uint64_t)first_row * (uint64_t)d % 8) : 0;
 }
 // Whether a thread holds the next row's values while it finishes one: up to 16 values a
 // tensor; more would spill.
@@ -129,24 +161,27 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
   const int d = (int)a.d;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int shift = shift_of<ACC>(row, d);
   int flip = 0;
   float w[NV][8];
   Raw<T> xr[NV];
   Raw<R> rr[RES ? NV : 1];
   auto fetch = [&](int64_t i) {
+    const bool last = i + 1 == a.rows;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, xr[k]);
+    for (int k = 0; k < NV; ++k)
+      load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, shift, last, xr[k]);
     if (RES) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        load_row<ACC>(static_cast<const R*>(a.res) + i * d, k, d, rr[RES ? k : 0]);
+        load_row<ACC>(static_cast<const R*>(a.res) + i * d, k, d, shift, last, rr[RES ? k : 0]);
     }
   };
   if (ahead(NV) && row < a.rows) fetch(row);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     Raw<float> t;
-    load_row<ACC == kVec ? kTail : ACC>(a.w, k, d, t);
+    load_row<kColumns<ACC>>(a.w, k, d, shift, true, t);
     unpack(t, w[k]);
   }
   for (; row < a.rows; row += step) {
@@ -160,8 +195,9 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
         unpack(rr[RES ? k : 0], q);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = round_to<R>(v[k][j] + q[j]);
-        store_row<ACC>(static_cast<R*>(a.res_out) + row * d, k, d, v[k]);
+        store_row<ACC>(static_cast<R*>(a.res_out) + row * d, k, d, shift, v[k]);
       }
+      inside<ACC>(v[k], k, d, shift);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
     }
@@ -173,7 +209,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rstd * w[k][j];
       if (FMT < 0) {
-        store_row<ACC>(static_cast<T*>(a.y) + row * d, k, d, v[k]);
+        store_row<ACC>(static_cast<T*>(a.y) + row * d, k, d, shift, v[k]);
       } else {
         // columns past d (zero) fill the row's padding; past the padding nothing is stored
         const uint32_t c8 = threadIdx.x + k * blockDim.x, nkb = (uint32_t)(a.Kp >> 7);
@@ -202,6 +238,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
   const int d = (int)a.d;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const int64_t first = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int shift = shift_of<ACC>(first, d);
   int flip = 0;
   float w[NV][8], dw[NV][8];
   Raw<T> yr[NV];
@@ -209,11 +246,12 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
   Raw<float> ur[DRES ? NV : 1];
   float rs = 0.f;
   auto fetch = [&](int64_t i) {
+    const bool last = i + 1 == a.rows;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, yr[k]);
-      load_row<ACC>(static_cast<const R*>(a.r) + i * d, k, d, rr[k]);
-      if (DRES) load_row<ACC>(a.dres + i * d, k, d, ur[DRES ? k : 0]);
+      load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, shift, last, yr[k]);
+      load_row<ACC>(static_cast<const R*>(a.r) + i * d, k, d, shift, last, rr[k]);
+      if (DRES) load_row<ACC>(a.dres + i * d, k, d, shift, last, ur[DRES ? k : 0]);
     }
     rs = a.rstd[i];
   };
@@ -221,7 +259,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     Raw<float> t;
-    load_row<ACC == kVec ? kTail : ACC>(a.w, k, d, t);
+    load_row<kColumns<ACC>>(a.w, k, d, shift, true, t);
     unpack(t, w[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
@@ -236,6 +274,8 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
     for (int k = 0; k < NV; ++k) {
       unpack(yr[k], g[k]);
       unpack(rr[k], rh[k]);
+      inside<ACC>(g[k], k, d, shift);
+      inside<ACC>(rh[k], k, d, shift);
       if (DRES) unpack(ur[DRES ? k : 0], o[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -254,12 +294,12 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
         const float t = rstd * (g[k][j] - rh[k][j] * m);
         o[k][j] = DRES ? o[k][j] + t : t;
       }
-      store_row<ACC>(a.dr + row * d, k, d, o[k]);
+      store_row<ACC>(a.dr + row * d, k, d, shift, o[k]);
     }
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    store_row<ACC == kVec ? kTail : ACC>(a.part + first * d, k, d, dw[k]);
+    store_row<kColumns<ACC>>(a.part + first * d, k, d, shift, dw[k]);
 }
 
 // dw = sum of the partial rows, in a fixed order: a CTA takes eight columns, thread (c, p)
@@ -290,6 +330,7 @@ struct Shape {
   int threads, rows, nv;
 };
 Shape shape_of(int64_t width) {
+  if (width % 8 != 0) width += 7;  // kShift: a row may lie in one more access
   int64_t t = ((width + 7) / 8 + 31) / 32 * 32;
   if (t > kMaxThreads) t = kMaxThreads;
   const int64_t nv = (width + 8 * t - 1) / (8 * t);
@@ -302,21 +343,34 @@ Shape shape_of(int64_t width) {
 // residual) forward 71, 66, 63, 68 and 69 us at 512, 640, 768, 896 and 1024 threads, backward
 // 78, 76, 92, 85 and 84; the same order at widths of 256 to 2048.
 constexpr int kFwdThreads = 768, kBwdThreads = 640;
-unsigned grid_of(int64_t rows, const Shape& h, int threads, int least) {
+// Where d is no multiple of 8 the walkers' rows are a multiple of eight apart (kShift).
+unsigned grid_of(int64_t rows, int64_t d, const Shape& h, int threads, int least) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int cta = h.threads * h.rows, ctas = threads / cta > 1 ? threads / cta : 1;
   const int64_t most = sms * ctas, per = (int64_t)h.rows * least;
-  const int64_t want = (rows + per - 1) / per;
-  return (unsigned)(want < most ? want : most);
+  const int64_t want = (rows + per - 1) / per, unit = d % 8 == 0 ? 1 : 8;
+  // (more than `most` would wait for an SM: four CTAs too many doubled the time)
+  const int64_t up = (want + unit - 1) / unit * unit, down = most < unit ? unit : most / unit * unit;
+  return (unsigned)(up < down ? up : down);
+}
+
+constexpr int64_t kMaxWidth = (int64_t)kMaxThreads * 8 * 4;
+
+// aligned: the tensors' first elements are.
+Access access_of(bool aligned, int64_t d) {
+  return !aligned ? kStrided : d % 8 == 0 ? kVec : d + 7 <= kMaxWidth ? kShift : kStrided;
 }
 
 template <typename T, typename R, bool RES, int FMT, int NV>
-cudaError_t fwd_nv(const NormArgs& a, const Shape& h, bool vec, cudaStream_t s) {
+cudaError_t fwd_nv(const NormArgs& a, const Shape& h, Access acc, cudaStream_t s) {
   const dim3 block(h.threads, h.rows);
   // two CTAs where a row takes 512 threads: 69 us against 74 at 8192 x 4096
-  const unsigned grid = grid_of(a.rows, h, h.threads == kMaxThreads ? 2 * kMaxThreads : kFwdThreads, 1);
-  if (vec)
+  const unsigned grid =
+      grid_of(a.rows, a.d, h, h.threads == kMaxThreads ? 2 * kMaxThreads : kFwdThreads, 1);
+  if (acc == kVec)
     add_rmsnorm_kernel<T, R, RES, FMT, NV, kVec><<<grid, block, 0, s>>>(a);
+  else if (FMT < 0 && acc == kShift)
+    add_rmsnorm_kernel<T, R, RES, FMT, NV, FMT < 0 ? kShift : kTail><<<grid, block, 0, s>>>(a);
   else  // a microscaled output needs its blocks' values together
     add_rmsnorm_kernel<T, R, RES, FMT, NV, FMT < 0 ? kStrided : kTail><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
@@ -324,12 +378,14 @@ cudaError_t fwd_nv(const NormArgs& a, const Shape& h, bool vec, cudaStream_t s) 
 template <typename T, typename R, bool RES, int FMT>
 cudaError_t fwd_fmt(const NormArgs& a, cudaStream_t s) {
   const Shape h = shape_of(FMT < 0 ? a.d : a.Kp);
-  const bool vec = mx::aligned8<T>(a.x, a.d) &&
-                   (!RES || (mx::aligned8<R>(a.res, a.d) && mx::aligned8<R>(a.res_out, a.d))) &&
-                   (FMT >= 0 || mx::aligned8<T>(a.y, a.d));
-  return h.nv == 1   ? fwd_nv<T, R, RES, FMT, 1>(a, h, vec, s)
-         : h.nv == 2 ? fwd_nv<T, R, RES, FMT, 2>(a, h, vec, s)
-                     : fwd_nv<T, R, RES, FMT, 4>(a, h, vec, s);
+  const Access acc =
+      access_of(mx::aligned8<T>(a.x, 8) &&
+                    (!RES || (mx::aligned8<R>(a.res, 8) && mx::aligned8<R>(a.res_out, 8))) &&
+                    (FMT >= 0 || mx::aligned8<T>(a.y, 8)),
+                a.d);
+  return h.nv == 1   ? fwd_nv<T, R, RES, FMT, 1>(a, h, acc, s)
+         : h.nv == 2 ? fwd_nv<T, R, RES, FMT, 2>(a, h, acc, s)
+                     : fwd_nv<T, R, RES, FMT, 4>(a, h, acc, s);
 }
 template <typename T, typename R, bool RES>
 cudaError_t fwd_res(const NormArgs& a, cudaStream_t s) {
@@ -347,11 +403,13 @@ cudaError_t fwd_t(const NormArgs& a, cudaStream_t s) {
 constexpr int kLeastRows = 4;
 
 template <typename T, typename R, bool DRES, int NV>
-cudaError_t bwd_nv(const NormBwdArgs& a, const Shape& h, bool vec, cudaStream_t s) {
+cudaError_t bwd_nv(const NormBwdArgs& a, const Shape& h, Access acc, cudaStream_t s) {
   const dim3 block(h.threads, h.rows);
-  const unsigned grid = grid_of(a.rows, h, kBwdThreads, kLeastRows);
-  if (vec)
+  const unsigned grid = grid_of(a.rows, a.d, h, kBwdThreads, kLeastRows);
+  if (acc == kVec)
     add_rmsnorm_bwd_kernel<T, R, DRES, NV, kVec><<<grid, block, 0, s>>>(a);
+  else if (acc == kShift)
+    add_rmsnorm_bwd_kernel<T, R, DRES, NV, kShift><<<grid, block, 0, s>>>(a);
   else
     add_rmsnorm_bwd_kernel<T, R, DRES, NV, kStrided><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
@@ -359,25 +417,26 @@ cudaError_t bwd_nv(const NormBwdArgs& a, const Shape& h, bool vec, cudaStream_t 
 template <typename T, typename R>
 cudaError_t bwd_t(const NormBwdArgs& a, cudaStream_t s) {
   const Shape h = shape_of(a.d);
-  const bool vec = mx::aligned8<T>(a.dy, a.d) && mx::aligned8<R>(a.r, a.d) &&
-                   mx::aligned8<float>(a.dr, a.d) && mx::aligned8<float>(a.dres, a.d);
+  const Access acc = access_of(mx::aligned8<T>(a.dy, 8) && mx::aligned8<R>(a.r, 8) &&
+                                   mx::aligned8<float>(a.dr, 8) && mx::aligned8<float>(a.dres, 8),
+                               a.d);
   if (a.dres)
-    return h.nv == 1   ? bwd_nv<T, R, true, 1>(a, h, vec, s)
-           : h.nv == 2 ? bwd_nv<T, R, true, 2>(a, h, vec, s)
-                       : bwd_nv<T, R, true, 4>(a, h, vec, s);
-  return h.nv == 1   ? bwd_nv<T, R, false, 1>(a, h, vec, s)
-         : h.nv == 2 ? bwd_nv<T, R, false, 2>(a, h, vec, s)
-                     : bwd_nv<T, R, false, 4>(a, h, vec, s);
+    return h.nv == 1   ? bwd_nv<T, R, true, 1>(a, h, acc, s)
+           : h.nv == 2 ? bwd_nv<T, R, true, 2>(a, h, acc, s)
+                       : bwd_nv<T, R, true, 4>(a, h, acc, s);
+  return h.nv == 1   ? bwd_nv<T, R, false, 1>(a, h, acc, s)
+         : h.nv == 2 ? bwd_nv<T, R, false, 2>(a, h, acc, s)
+                     : bwd_nv<T, R, false, 4>(a, h, acc, s);
 }
 
 int64_t partial_rows(int64_t rows, int64_t d) {
   const Shape h = shape_of(d);
-  return (int64_t)grid_of(rows, h, kBwdThreads, kLeastRows) * h.rows;
+  return (int64_t)grid_of(rows, d, h, kBwdThreads, kLeastRows) * h.rows;
 }
 
 }  // namespace
 
-bool norm_width_ok(int64_t d) { return d <= (int64_t)kMaxThreads * 8 * 4; }
+bool norm_width_ok(int64_t d) { return d <= kMaxWidth; }
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;

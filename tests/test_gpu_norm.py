@@ -172,6 +172,47 @@ def test_unaligned_tensors_and_in_place():
     assert b[0] is up and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+# widths that are no multiple of eight, walkers of several rows: every offset of a row inside
+# an access, the widest rows there are
+@pytest.mark.parametrize("rows,d", [(5000, 33), (1301, 257), (2003, 1049), (700, 4103), (333, 9001),
+                                    (200, 16377), (200, 16383)])
+@pytest.mark.parametrize("dtype,res", [(BF16, F32), (BF16, BF16), (F32, F32), (F32, BF16)])
+def test_odd_widths(rows, d, dtype, res):
+    """Forward in place and backward against fp64, nothing written behind the tensors' ends, and
+    a NaN stays in its row."""
+    def guarded(t):
+        buf = torch.full((rows * d + 64,), 7.0, dtype=t.dtype, device="cuda")
+        buf[:rows * d] = t.reshape(-1).cuda()
+        return buf, buf[:rows * d].view(rows, d)
+    x, r, w = inputs(rows, d, dtype, res, 1)
+    wc, s = w.cuda(), summed(x, r)
+    (xb, xc), (rb, rc) = guarded(x), guarded(r)
+    y, out, rstd = m3.add_rmsnorm(xc, wc, residual=rc, residual_out=rc, y=xc, want_rstd=True)
+    assert torch.equal(out.cpu(), s)
+    ref, ref_rstd = ol.rmsnorm(np64(s), np64(w), 1e-6)
+    assert np.all(np.abs(np64(rstd) - ref_rstd) <= FP * ref_rstd)
+    tol = FP + (2.0 ** -8 if dtype == BF16 else 0)
+    assert np.all(np.abs(np64(y) - ref) <= tol * np.abs(ref) + 1e-38)
+    assert torch.all(xb[rows * d:] == 7) and torch.all(rb[rows * d:] == 7)
+    up = torch.randn(rows, d, generator=torch.Generator().manual_seed(4))
+    (ub, uc), dy = guarded(up), x.cuda()
+    dr, dw = m3.add_rmsnorm_bwd(dy, out, wc, rstd, dres=uc, dr=uc)
+    a = [np64(t) for t in (x, s, w, rstd)]
+    ref_dr, ref_dw = ol.rmsnorm_bwd(*a, np64(up))
+    gm, rh, sc = np.abs(a[0] * a[2]), np.abs(a[1]) * a[3][:, None], a[3][:, None]
+    mag = sc * (gm + rh * (gm * rh).mean(-1, keepdims=True)) + np.abs(np64(up))
+    assert np.all(np.abs(np64(dr) - ref_dr) <= 96 * 2.0 ** -24 * mag + 1e-38)
+    assert np.all(np.abs(np64(dw) - ref_dw) <=
+                  (rows + 32) * 2.0 ** -24 * (np.abs(a[0]) * rh).sum(0) + 1e-38)
+    assert torch.all(ub[rows * d:] == 7)
+    bad = rows // 2
+    dy[bad] = float("nan")
+    assert torch.isnan(m3.add_rmsnorm(dy, wc, residual=out)[0]).any(1).nonzero().flatten().tolist() \
+        == [bad]
+    dr, dw2 = m3.add_rmsnorm_bwd(dy, out, wc, rstd)
+    assert torch.isnan(dr).any(1).nonzero().flatten().tolist() == [bad] and torch.isnan(dw2).all()
+
+
 def test_nonfinite_and_zero_rows():
     x, _, w = inputs(4, 96, F32, None)
     x[0] = 0
