@@ -148,6 +148,51 @@ template <int ACC>
 __device__ __forceinline__ int shift_of(int64_t first_row, int64_t d) {
   return ACC == kShift ? (int)((uint64_t)first_row * (uint64_t)d % 8) : 0;
 }
+// A microscaled output's blocks start at the row's columns: from values of columns 8 i - shift
+// on to those of 8 i on.  A thread's last `shift` values come from the next one: by shuffles, and
+// past a warp's end from `edge`, which holds the first values of each warp and group (twice, so
+// that one barrier a call is enough).
+template <int NV>
+struct Edge {
+  float v[2][NV * 16][8];
+};
+template <int NV>
+__device__ __forceinline__ void realign(float (&v)[NV][8], int shift, Edge<NV>& edge, int& flip) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const bool shared = nw * NV > 1;
+  if (shared) {
+    flip ^= 1;
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) edge.v[flip][k * nw + warp][j] = v[k][j];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = v[k][j];
+      x[8 + j] = j < 7 ? __shfl_down_sync(0xffffffffu, v[k][j], 1) : 0.f;
+    }
+    if (lane == 31) {
+      const int next = k * nw + warp + 1;
+#pragma unroll
+      for (int j = 0; j < 7; ++j) x[8 + j] = next < NV * nw ? edge.v[flip][next][j] : 0.f;
+    }
+#pragma unroll
+    for (int b = 4; b > 0; b >>= 1) {  // by `shift`, a bit at a time
+#pragma unroll
+      for (int j = 0; j + b < 16; ++j)
+        if (shift & b) x[j] = x[j + b];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] = x[j];
+  }
+}
 // Whether a thread holds the next row's values while it finishes one: up to 16 values a
 // tensor; more would spill.
 constexpr bool ahead(int nv) { return nv <= 2; }
@@ -158,11 +203,14 @@ __device__ __forceinline__ float round_to(float v) { return to_f32(from_f32<T>(v
 template <typename T, typename R, bool RES, int FMT, int NV, int ACC>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
   __shared__ float red[32];
+  constexpr bool kRealign = FMT >= 0 && ACC == kShift;
+  __shared__ Edge<kRealign ? NV : 1> edge;
   const int d = (int)a.d;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int shift = shift_of<ACC>(row, d);
   int flip = 0;
+  [[maybe_unused]] int flip_edge = 0;
   float w[NV][8];
   Raw<T> xr[NV];
   Raw<R> rr[RES ? NV : 1];
@@ -208,6 +256,10 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rstd * w[k][j];
+    }
+    if constexpr (kRealign) realign<NV>(v, shift, edge, flip_edge);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
       if (FMT < 0) {
         store_row<ACC>(static_cast<T*>(a.y) + row * d, k, d, shift, v[k]);
       } else {
@@ -369,15 +421,17 @@ cudaError_t fwd_nv(const NormArgs& a, const Shape& h, Access acc, cudaStream_t s
       grid_of(a.rows, a.d, h, h.threads == kMaxThreads ? 2 * kMaxThreads : kFwdThreads, 1);
   if (acc == kVec)
     add_rmsnorm_kernel<T, R, RES, FMT, NV, kVec><<<grid, block, 0, s>>>(a);
-  else if (FMT < 0 && acc == kShift)
-    add_rmsnorm_kernel<T, R, RES, FMT, NV, FMT < 0 ? kShift : kTail><<<grid, block, 0, s>>>(a);
+  else if (acc == kShift)
+    add_rmsnorm_kernel<T, R, RES, FMT, NV, kShift><<<grid, block, 0, s>>>(a);
   else  // a microscaled output needs its blocks' values together
     add_rmsnorm_kernel<T, R, RES, FMT, NV, FMT < 0 ? kStrided : kTail><<<grid, block, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, typename R, bool RES, int FMT>
 cudaError_t fwd_fmt(const NormArgs& a, cudaStream_t s) {
-  const Shape h = shape_of(FMT < 0 ? a.d : a.Kp);
+  // a microscaled row is written to its padding's end
+  const int64_t held = a.d % 8 == 0 ? a.d : (a.d + 14) / 8 * 8;
+  const Shape h = shape_of(FMT < 0 ? a.d : a.Kp > held ? a.Kp : held);
   const Access acc =
       access_of(mx::aligned8<T>(a.x, 8) &&
                     (!RES || (mx::aligned8<R>(a.res, 8) && mx::aligned8<R>(a.res_out, 8))) &&

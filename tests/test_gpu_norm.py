@@ -91,6 +91,15 @@ def test_quantised_output(rows, d, fmt, dtype, res):
     assert not codes[:, (d + 1) // 2 if fmt == "mxfp4" else d:].any() or kp == d
 
 
+# every offset of a row inside an access; rows that end in the last access of their padding
+@pytest.mark.parametrize("rows,d", [(5000, 33), (1301, 257), (640, 1021), (900, 1049), (150, 4093),
+                                    (160, 8191), (150, 9001), (60, 16377), (60, 16383)])
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("dtype,res", [(BF16, BF16), (F32, F32), (F32, BF16)])
+def test_quantised_odd_widths(rows, d, fmt, dtype, res):
+    test_quantised_output(rows, d, fmt, dtype, res)
+
+
 @pytest.mark.parametrize("rows,d", SHAPES)
 @pytest.mark.parametrize("dtype,res", [(BF16, F32), (BF16, BF16), (F32, F32), (F32, BF16)])
 @pytest.mark.parametrize("dres", [False, True])
