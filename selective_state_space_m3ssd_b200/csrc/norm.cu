@@ -8,13 +8,15 @@
 //     dr = rstd (g - rhat mean(g rhat)) + dres,   dw = sum over rows of dy rhat.
 //
 // Streams: every tensor is read once and written once, so HBM bounds them.  A thread keeps
-// eight values (times NV) of a row in registers between the row's sum and its outputs.
-// Where rows are aligned they are consecutive (one access of 16 or 32 bytes; four lanes
-// share a block of 32 of a microscaled output); other rows of plain outputs go by single
-// elements, consecutive across the lanes.  The grid is persistent: a CTA walks rows,
-// fetching the next while it finishes one, with its columns of w, and in the backward its
-// columns of the dw sum, in registers.  The dw sums leave as one partial row a walker, which
-// a second kernel adds in a fixed order.
+// eight values (times NV) of a row in registers between the row's sum and its outputs, read
+// in one access of 16 or 32 bytes (four lanes share a block of 32 of a microscaled output).
+// Rows of a width that is no multiple of eight start inside an access: they are taken in the
+// accesses they lie in (kShift), a microscaled output's values moved to its blocks by shuffles.
+// 16000 x 1049 (bf16, fp32 residual) takes 43 us forward, 53 to 8 bits and 40 backward, 94, 71
+// and 65 element by element, which tensors that are not aligned themselves still are.  The
+// grid is persistent: a CTA walks rows, fetching the next while it finishes one, with its columns
+// of w, and in the backward its columns of the dw sum, in registers.  The dw sums leave as
+// one partial row a walker, which a second kernel adds in a fixed order.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -432,11 +434,15 @@ cudaError_t fwd_fmt(const NormArgs& a, cudaStream_t s) {
   // a microscaled row is written to its padding's end
   const int64_t held = a.d % 8 == 0 ? a.d : (a.d + 14) / 8 * 8;
   const Shape h = shape_of(FMT < 0 ? a.d : a.Kp > held ? a.Kp : held);
-  const Access acc =
-      access_of(mx::aligned8<T>(a.x, 8) &&
-                    (!RES || (mx::aligned8<R>(a.res, 8) && mx::aligned8<R>(a.res_out, 8))) &&
-                    (FMT >= 0 || mx::aligned8<T>(a.y, 8)),
-                a.d);
+  Access acc = access_of(mx::aligned8<T>(a.x, 8) &&
+                             (!RES || (mx::aligned8<R>(a.res, 8) && mx::aligned8<R>(a.res_out, 8))) &&
+                             (FMT >= 0 || mx::aligned8<T>(a.y, 8)),
+                         a.d);
+  // realigning to the blocks pays where a row is long: to 8 bits from bf16 with an fp32
+  // residual, 20000 x 513 38.5 us against 42.9 element by element, but from fp32 48.2 against
+  // 40.1; at 16000 x 1049 53 against 71 and 47 against 60; at 30000 x 275 40 against 37 and 47
+  // against 33
+  if (FMT >= 0 && acc == kShift && a.d < 768) acc = kStrided;
   return h.nv == 1   ? fwd_nv<T, R, RES, FMT, 1>(a, h, acc, s)
          : h.nv == 2 ? fwd_nv<T, R, RES, FMT, 2>(a, h, acc, s)
                      : fwd_nv<T, R, RES, FMT, 4>(a, h, acc, s);
