@@ -454,32 +454,71 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
   }
 }
 
-// Every other shape: one CTA a (b, h), a warp a row at a time, up to eight columns a lane.
-constexpr int kGenThreads = 256, kGenWarps = kGenThreads / 32;
-template <typename T>
-__global__ void __launch_bounds__(kGenThreads) step_q8_kernel(StepQ8Args a) {
+// Every other shape: one CTA a (b, h); `lanes` lanes (a power of two) share a row, eight columns
+// each.  VEC: rows of a multiple of eight columns, aligned: a lane's codes are one access.
+constexpr int kGenThreads = 128, kGenWarps = kGenThreads / 32, kGenUnroll = 4;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kGenThreads) step_q8_kernel(StepQ8Args a, int lanes) {
   extern __shared__ float smem[];
   const int N = (int)a.N, P = (int)a.P, NH = N / 2;
   const int64_t bh = blockIdx.x, b = bh / a.H, h = bh % a.H, rep = a.H / a.G, g = h / rep;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = 8 * (tid % lanes), r0 = tid / lanes, per = kGenThreads / lanes;
   float* bc = smem;            // N   gamma Bbar
   float* cc = bc + N;          // N   Cbar
   float* bp = cc + N;          // N   beta Bbar_prev
   float* ysum = bp + N;        // kGenWarps * P
+  uint2 q[kGenUnroll];
+  float sc[kGenUnroll];
+  auto fetch = [&](int base) {  // rows base, base + per, ...
+#pragma unroll
+    for (int u = 0; u < kGenUnroll; ++u) {
+      const int n = base + u * per;
+      q[u] = make_uint2(0u, 0u);
+      sc[u] = 0.f;
+      if (n < N) {
+        sc[u] = a.scale[bh * N + n];
+        const uint8_t* const p = a.ssm + (bh * N + n) * P + c;
+        if (VEC) {
+          if (c < P) q[u] = *reinterpret_cast<const uint2*>(p);
+        } else {
+          uint32_t w[2] = {0u, 0u};
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < P) w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+          q[u] = make_uint2(w[0], w[1]);
+        }
+      }
+    }
+  };
+  fetch(r0);
   const T* Bt = static_cast<const T*>(a.B_t) + (b * a.G + g) * N;
   const T* Ct = static_cast<const T*>(a.C_t) + (b * a.G + g) * N;
   const float* bprev = a.b_prev + (b * a.G + g) * N;
   const float alpha = expf(a.logdecay_t[bh]);
   const float be = a.beta_t ? a.beta_t[bh] : 0.f, ga = a.gamma_t[bh];
+  const T* xt = static_cast<const T*>(a.x_t) + bh * P;
+  float x[8], xp[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = xp[j] = 0.f;
+  if (VEC) {
+    if (c < P) {
+      mx::load8(xt + c, x);
+      mx::load8(a.x_prev + bh * P + c, xp);
+    }
+  } else {
+    mx::load8_tail(xt + c, P - c, x);
+    mx::load8_tail(a.x_prev + bh * P + c, P - c, xp);
+  }
   for (int i = tid; i < NH; i += kGenThreads) {
     const float ang = a.angle[bh * NH + i];
     const float ph = wrap_angle(ang + (a.theta_t ? a.theta_t[bh * NH + i] : 0.f));
-    float s, c, s0, c0;
-    sincosf(ph, &s, &c);
+    float s, c1, s0, c0;
+    sincosf(ph, &s, &c1);
     sincosf(ang, &s0, &c0);
     const float b0 = to_f32(Bt[2 * i]), b1 = to_f32(Bt[2 * i + 1]);
-    const float2 rb = rot2(c, s, b0, b1);
-    const float2 rc = rot2(c, s, to_f32(Ct[2 * i]), to_f32(Ct[2 * i + 1]));
+    const float2 rb = rot2(c1, s, b0, b1);
+    const float2 rc = rot2(c1, s, to_f32(Ct[2 * i]), to_f32(Ct[2 * i + 1]));
     const float2 rp = rot2(c0, s0, bprev[2 * i], bprev[2 * i + 1]);
     bc[2 * i] = ga * rb.x; bc[2 * i + 1] = ga * rb.y;
     cc[2 * i] = rc.x; cc[2 * i + 1] = rc.y;
@@ -490,52 +529,95 @@ __global__ void __launch_bounds__(kGenThreads) step_q8_kernel(StepQ8Args a) {
       a.b_prev_out[(b * a.G + g) * N + 2 * i + 1] = b1;
     }
   }
-  const T* xt = static_cast<const T*>(a.x_t) + bh * P;
-  float x[8], xp[8], acc[8];
+  uint64_t x2[4], xp2[4], acc[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int p = lane + 32 * j;
-    x[j] = p < P ? to_f32(xt[p]) : 0.f;
-    xp[j] = p < P ? a.x_prev[bh * P + p] : 0.f;
-    acc[j] = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    x2[j] = pack2(x[2 * j], x[2 * j + 1]);
+    xp2[j] = pack2(xp[2 * j], xp[2 * j + 1]);
+    acc[j] = pack2(0.f, 0.f);
   }
   __syncthreads();
-  for (int n = warp; n < N; n += kGenWarps) {
-    const uint8_t* S = a.ssm + (bh * N + n) * P;
-    uint8_t* So = a.ssm_out + (bh * N + n) * P;
-    const float as = alpha * a.scale[bh * N + n], f0 = bp[n], f1 = bc[n], f2 = cc[n];
-    float v[8], amax = 0.f;
+  // the CTA's threads go round together (the lanes of a row share shuffles)
+  for (int base = 0; base < N; base += kGenUnroll * per) {
+    uint2 now[kGenUnroll];
+    float ns[kGenUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int p = lane + 32 * j;
-      v[j] = 0.f;
-      if (p < P) {
-        v[j] = fmaf(f1, x[j], fmaf(f0, xp[j], as * mx::unpack2_e4m3(S[p]).x));
-        acc[j] = fmaf(f2, v[j], acc[j]);
+    for (int u = 0; u < kGenUnroll; ++u) {
+      now[u] = q[u];
+      ns[u] = sc[u];
+    }
+    if (base + kGenUnroll * per < N) fetch(base + kGenUnroll * per + r0);
+#pragma unroll
+    for (int u = 0; u < kGenUnroll; ++u) {
+      const int n = base + u * per + r0;
+      if (base + u * per >= N) break;
+      const bool have = n < N;
+      const float as = have ? alpha * ns[u] : 0.f, f0 = have ? bp[n] : 0.f, f1 = have ? bc[n] : 0.f,
+                  f2 = have ? cc[n] : 0.f;
+      const uint64_t as2 = pack2(as, as), f02 = pack2(f0, f0), f12 = pack2(f1, f1),
+                     f22 = pack2(f2, f2);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 e = mx::unpack2_e4m3((j < 2 ? now[u].x : now[u].y) >> (16 * (j & 1)));
+        const uint64_t w = fma2(f12, x2[j], fma2(f02, xp2[j], mul2(as2, pack2(e.x, e.y))));
+        if (have) acc[j] = fma2(f22, w, acc[j]);  // (x may be infinite)
+        const float2 f = unpack2(w);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
       }
-      amax = max_nan(amax, fabsf(v[j]));
-    }
+      if (!VEC) {  // columns past the row's end take no part (a NaN scale or factor)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float s, inv;
-    row_scale<false>(amax, s, inv);
+        for (int j = 0; j < 8; ++j)
+          if (c + j >= P) v[j] = 0.f;
+      } else if (c >= P) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int p = lane + 32 * j;
-      if (p < P) So[p] = (uint8_t)mx::pack2_e4m3(v[j] * inv, 0.f);
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
+      float amax = mx::amax8(v);
+      for (int o = 1; o < lanes; o <<= 1)
+        amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float s, inv;
+      row_scale<false>(amax, s, inv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= inv;
+      if (have) {
+        uint8_t* const out = a.ssm_out + (bh * N + n) * P + c;
+        if (VEC) {
+          if (c < P)
+            *reinterpret_cast<uint2*>(out) = make_uint2(mx::pack4_e4m3(v[0], v[1], v[2], v[3]),
+                                                        mx::pack4_e4m3(v[4], v[5], v[6], v[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < P) out[j] = (uint8_t)mx::pack2_e4m3(v[j], 0.f);
+        }
+        if (c == 0) a.scale_out[bh * N + n] = s;
+      }
     }
-    __syncwarp();  // every lane has read the row's scale
-    if (lane == 0) a.scale_out[bh * N + n] = s;
   }
+  float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (lane + 32 * j < P) ysum[warp * P + lane + 32 * j] = acc[j];
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack2(acc[j]);
+    y[2 * j] = f.x;
+    y[2 * j + 1] = f.y;
+  }
+  for (int o = lanes; o < 32; o <<= 1) {  // the warp's rows
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] += __shfl_xor_sync(0xffffffffu, y[j], o);
+  }
+  if (lane < lanes) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < P) ysum[warp * P + c + j] = y[j];
+  }
   __syncthreads();
   for (int p = tid; p < P; p += kGenThreads) {
     const float xv = to_f32(xt[p]);
-    float y = a.D ? a.D[h] * xv : 0.f;
-    for (int w = 0; w < kGenWarps; ++w) y += ysum[w * P + p];
-    static_cast<T*>(a.y_t)[bh * P + p] = from_f32<T>(y);
+    float t = a.D ? a.D[h] * xv : 0.f;
+    for (int w = 0; w < kGenWarps; ++w) t += ysum[w * P + p];
+    static_cast<T*>(a.y_t)[bh * P + p] = from_f32<T>(t);
     a.x_prev_out[bh * P + p] = xv;
   }
 }
@@ -570,7 +652,13 @@ cudaError_t launch_step_t(StepQ8Args a, cudaStream_t s) {
       step_q8_walk<T><<<(unsigned)(nbh < walkers ? nbh : walkers), kWalkThreads, 0, s>>>(a);
   } else {
     const size_t smem = sizeof(float) * (size_t)(3 * a.N + kGenWarps * a.P);
-    step_q8_kernel<T><<<(unsigned)nbh, kGenThreads, smem, s>>>(a);
+    int lanes = 1;
+    while (8 * lanes < a.P) lanes *= 2;  // P <= 256: at most 32
+    if (a.P % 8 == 0 && mx::aligned8<T>(a.x_t, a.P) && mx::aligned8<float>(a.x_prev, a.P) &&
+        (reinterpret_cast<uintptr_t>(a.ssm) | reinterpret_cast<uintptr_t>(a.ssm_out)) % 8 == 0)
+      step_q8_kernel<T, true><<<(unsigned)nbh, kGenThreads, smem, s>>>(a, lanes);
+    else
+      step_q8_kernel<T, false><<<(unsigned)nbh, kGenThreads, smem, s>>>(a, lanes);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !inplace) return e;
