@@ -456,6 +456,11 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
 
 // Every other shape: one CTA a (b, h); `lanes` lanes (a power of two) share a row, eight columns
 // each.  VEC: rows of a multiple of eight columns, aligned: a lane's codes are one access.
+// b256 H32 N64 P64 takes 40 us (13 for the bytes: a CTA's life is mostly its chain of angles,
+// rotations, rows and sum), b64 H32 N256 P64 30, b128 H32 N128 P75 bf16 93; with a warp a row, a
+// column of each 32 a lane, they took 136, 123 and 127.  Measured and not kept: odd rows in the
+// accesses they lie in (no faster, and the sums it needs cost the others 10 %), registers for
+// 8 or 10 CTAs an SM (spills; 10 to 40 % slower).
 constexpr int kGenThreads = 128, kGenWarps = kGenThreads / 32, kGenUnroll = 4;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kGenThreads) step_q8_kernel(StepQ8Args a, int lanes) {

@@ -108,6 +108,33 @@ def test_step(b, H, G, N, P, dtype):
         assert torch.equal(cd[k], out[k]), k
 
 
+# rows that start inside an access, of one column to the most; states in and out that lie alike
+# in an access and otherwise; the cache written over; whole rows of other widths
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,P", [(2, 1), (64, 7), (34, 17), (128, 75), (130, 121), (128, 125), (64, 249),
+                                 (62, 250), (64, 255), (64, 64), (256, 32), (100, 72), (64, 256)])
+@pytest.mark.parametrize("shift_in,shift_out", [(0, 0), (3, 3), (3, 6)])
+def test_rows_inside_an_access(N, P, dtype, shift_in, shift_out):
+    step, cache = make(3, 4, 2, N, P, dtype)
+    sd, cd = to_cuda(step), to_cuda(cache)
+    n = cd["ssm"].numel()
+    out = {k: torch.full_like(v, 77) for k, v in cd.items()}
+    bi = torch.full((n + 16,), 0x7F, dtype=torch.uint8, device="cuda")  # NaN codes around the state
+    bo = torch.full((n + 16,), 0x55, dtype=torch.uint8, device="cuda")
+    bi[shift_in:shift_in + n] = cd["ssm"].reshape(-1)
+    cd["ssm"] = bi[shift_in:shift_in + n].view(cd["ssm"].shape)
+    out["ssm"] = bo[shift_out:shift_out + n].view(out["ssm"].shape)
+    y = m3.step_q8(cd, *[sd[k] for k in ORDER], cache_out=out)
+    check(step, cache, y, out, dtype == "bf16")
+    assert torch.all(bo[:shift_out] == 0x55) and torch.all(bo[shift_out + n:] == 0x55)
+    if shift_in == shift_out:  # in place: the same bits
+        y2 = m3.step_q8(cd, *[sd[k] for k in ORDER])
+        assert torch.equal(y2, y)
+        for k in out:
+            assert torch.equal(cd[k], out[k]), k
+        assert torch.all(bi[:shift_in] == 0x7F) and torch.all(bi[shift_in + n:] == 0x7F)
+
+
 @pytest.mark.parametrize("b,H,N,P", [(3, 4, 128, 64), (30, 32, 128, 64), (2, 3, 10, 12)])
 @pytest.mark.parametrize("beta,theta,D", [(False, True, True), (True, False, True),
                                           (True, True, False), (False, False, False)])
