@@ -170,6 +170,28 @@ def test_state_round_trip(P, N):
     assert np.isnan(back.numpy()[~ok]).all()
 
 
+# every place a row can start at inside an access, in tensors that are aligned and not
+@pytest.mark.parametrize("P,N", [(1, 34), (7, 64), (17, 64), (75, 128), (121, 64), (130, 64),
+                                 (249, 62), (250, 64), (255, 64)])
+def test_odd_states(P, N):
+    test_state_round_trip(P, N)
+    h = state(3, 5, N, P, 12)
+    want_codes, want_scale = m3.quant_state(h.cuda())
+    want = m3.dequant_state(want_codes, want_scale)
+    n = h.numel()
+    for oh, oc in ((0, 0), (1, 0), (0, 3)):
+        hb = torch.full((n + 16,), float("nan"), device="cuda")
+        cb = torch.full((n + 16,), 0x55, dtype=torch.uint8, device="cuda")
+        hb[oh:oh + n] = h.reshape(-1).cuda()
+        hv, cv = hb[oh:oh + n].view(h.shape), cb[oc:oc + n].view(h.shape)
+        codes, scale = m3.quant_state(hv, codes=cv)
+        assert torch.equal(codes, want_codes) and torch.equal(scale, want_scale)
+        assert torch.all(cb[:oc] == 0x55) and torch.all(cb[oc + n:] == 0x55)
+        hb.fill_(7)
+        assert torch.equal(m3.dequant_state(cv, scale, ssm=hv), want)
+        assert torch.all(hb[:oh] == 7) and torch.all(hb[oh + n:] == 7)
+
+
 def test_nonfinite_state_rows():
     """A NaN or infinite input poisons the rows it reaches, reported by the check."""
     step, cache = make(2, 3, 1, 128, 64, "f32")
