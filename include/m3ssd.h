@@ -502,6 +502,12 @@ m3ssd_status m3ssd_add_rmsnorm_bwd(const m3ssd_norm_dims* dims, const void* dy, 
                                    float* dw, void* workspace, size_t workspace_bytes,
                                    void* stream);
 
+/* Whether the norm's kernels read columns `column` to `column` + 7 of `row` in one access, as
+ * they may where the columns lie inside an aligned tensor (`column` is negative where a row
+ * starts inside the access).  Host arithmetic only; for tests. */
+m3ssd_status m3ssd_test_norm_access(const m3ssd_norm_dims* dims, int64_t row, int32_t column,
+                                    int32_t* whole);
+
 /*
  * A decode cache whose state is held in 8 bits.  A row (b, h, n) of the state, P values, is
  * E4M3 codes with one fp32 scale: s = amax fp32(1 / 448), code = v (1 / s) rounded to nearest

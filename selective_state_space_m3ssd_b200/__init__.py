@@ -180,6 +180,8 @@ def load(path: str | None = None):
         lib.m3ssd_add_rmsnorm_bwd_workspace_size.restype = sz
         lib.m3ssd_add_rmsnorm_bwd.argtypes = [ndp] + [vp] * 8 + [sz, vp]
         lib.m3ssd_add_rmsnorm_bwd.restype = ctypes.c_int
+        lib.m3ssd_test_norm_access.argtypes = [ndp, i64, i32, i32p]
+        lib.m3ssd_test_norm_access.restype = ctypes.c_int
         for f in (lib.m3ssd_quant_state, lib.m3ssd_dequant_state):
             f.argtypes, f.restype = [ctypes.POINTER(Dims), vp, vp, vp, vp], ctypes.c_int
         lib.m3ssd_step_q8.argtypes = [ctypes.POINTER(Dims)] + [vp] * 8 + \

@@ -232,6 +232,8 @@ struct NormBwdArgs {
   float* part;
 };
 bool norm_width_ok(int64_t d);
+// Whether the kernels read columns c to c + 7 of `row` in one access (aligned tensors).
+bool norm_whole_access(int64_t rows, int64_t d, int64_t row, int c);
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t d);
 cudaError_t launch_add_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t s);

@@ -187,6 +187,16 @@ m3ssd_status m3ssd_add_rmsnorm_bwd(const m3ssd_norm_dims* dims, const void* dy, 
   return from_cuda(m3ssd::launch_add_rmsnorm_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
+m3ssd_status m3ssd_test_norm_access(const m3ssd_norm_dims* dims, int64_t row, int32_t column,
+                                    int32_t* whole) {
+  const m3ssd_status st = check_norm(dims);
+  if (st != M3SSD_OK) return st;
+  if (!whole || row < 0 || row >= dims->rows || column <= -8 || column >= dims->width)
+    return M3SSD_ERR_INVALID_ARG;
+  *whole = m3ssd::norm_whole_access(dims->rows, dims->width, row, column);
+  return M3SSD_OK;
+}
+
 m3ssd_status m3ssd_quant_state(const m3ssd_dims* dims, const float* ssm, void* codes, float* scale,
                                void* stream) {
   const m3ssd_status st = check_state_dims(dims);

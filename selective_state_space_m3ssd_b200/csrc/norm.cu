@@ -88,12 +88,17 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Raw<__nv_bfloat
   r.u = *reinterpret_cast<const uint4*>(p);
 }
 
+// kShift: whether the access of columns c to c + 7 of a row lies in the tensor, which has `left`
+// elements from the row's first on (a row of fewer than eight may have the tensor's end
+// rows behind it).
+__host__ __device__ __forceinline__ bool in_tensor(int c, int64_t left) { return c + 8 <= left; }
+
 // Group k of the thread's values of a row, and back.  With kShift the first and the last access
 // of a row bring in its neighbours' ends too (inside() drops them; elements that another
-// CTA may be writing, in place, are among them), the tensor's last one is element by element;
-// else there are zeros outside the row.
+// CTA may be writing, in place, are among them), those that would reach past the tensor's end
+// are element by element; else there are zeros outside the row.
 template <int ACC, typename T>
-__device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, bool last,
+__device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, int64_t left,
                                          Raw<T>& r) {
   const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - (ACC == kStrided ? 0 : shift);
   float v[8];
@@ -101,7 +106,7 @@ __device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     pack(v, r);
-    if (c < d && (ACC == kVec || !last || c + 8 <= d)) {
+    if (c < d && (ACC == kVec || in_tensor(c, left))) {
       load_vec(row + c, r);  // with kVec d is a multiple of 8
     } else if (ACC == kShift && c < d) {
 #pragma unroll
@@ -217,21 +222,21 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
   Raw<T> xr[NV];
   Raw<R> rr[RES ? NV : 1];
   auto fetch = [&](int64_t i) {
-    const bool last = i + 1 == a.rows;
+    const int64_t left = (a.rows - i) * d;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, shift, last, xr[k]);
+      load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, shift, left, xr[k]);
     if (RES) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        load_row<ACC>(static_cast<const R*>(a.res) + i * d, k, d, shift, last, rr[RES ? k : 0]);
+        load_row<ACC>(static_cast<const R*>(a.res) + i * d, k, d, shift, left, rr[RES ? k : 0]);
     }
   };
   if (ahead(NV) && row < a.rows) fetch(row);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     Raw<float> t;
-    load_row<kColumns<ACC>>(a.w, k, d, shift, true, t);
+    load_row<kColumns<ACC>>(a.w, k, d, shift, d, t);
     unpack(t, w[k]);
   }
   for (; row < a.rows; row += step) {
@@ -300,12 +305,12 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
   Raw<float> ur[DRES ? NV : 1];
   float rs = 0.f;
   auto fetch = [&](int64_t i) {
-    const bool last = i + 1 == a.rows;
+    const int64_t left = (a.rows - i) * d;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, shift, last, yr[k]);
-      load_row<ACC>(static_cast<const R*>(a.r) + i * d, k, d, shift, last, rr[k]);
-      if (DRES) load_row<ACC>(a.dres + i * d, k, d, shift, last, ur[DRES ? k : 0]);
+      load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, shift, left, yr[k]);
+      load_row<ACC>(static_cast<const R*>(a.r) + i * d, k, d, shift, left, rr[k]);
+      if (DRES) load_row<ACC>(a.dres + i * d, k, d, shift, left, ur[DRES ? k : 0]);
     }
     rs = a.rstd[i];
   };
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     Raw<float> t;
-    load_row<kColumns<ACC>>(a.w, k, d, shift, true, t);
+    load_row<kColumns<ACC>>(a.w, k, d, shift, d, t);
     unpack(t, w[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
@@ -495,6 +500,10 @@ int64_t partial_rows(int64_t rows, int64_t d) {
 }
 
 }  // namespace
+
+bool norm_whole_access(int64_t rows, int64_t d, int64_t row, int c) {
+  return access_of(true, d) != kStrided && in_tensor(c, (rows - row) * d);
+}
 
 bool norm_width_ok(int64_t d) { return d <= kMaxWidth; }
 
