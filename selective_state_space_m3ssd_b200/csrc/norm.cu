@@ -127,10 +127,10 @@ __device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, 
 template <int ACC>
 __device__ __forceinline__ void inside(float (&v)[8], int k, int d, int shift) {
   const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - shift;
-  if (ACC == kShift && (c < 0 || c + 8 > d)) {
+  if (c < 0 || c + 8 > d) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (c + j < 0 || c + j >= d) v[j] = 0.f;
+      if (ACC == kVec ? c >= d : c + j < 0 || c + j >= d) v[j] = 0.f;
   }
 }
 template <int ACC, typename T>
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
         for (int j = 0; j < 8; ++j) v[k][j] = round_to<R>(v[k][j] + q[j]);
         store_row<ACC>(static_cast<R*>(a.res_out) + row * d, k, d, shift, v[k]);
       }
-      inside<ACC>(v[k], k, d, shift);
+      if (ACC == kShift) inside<ACC>(v[k], k, d, shift);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
     }
@@ -263,6 +263,8 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[k][j] = v[k][j] * rstd * w[k][j];
+      // 0 rstd 0 outside the row is NaN where rstd is not finite
+      if (FMT >= 0 && !(rstd < INFINITY)) inside<ACC>(v[k], k, d, shift);
     }
     if constexpr (kRealign) realign<NV>(v, shift, edge, flip_edge);
 #pragma unroll
@@ -333,8 +335,10 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
     for (int k = 0; k < NV; ++k) {
       unpack(yr[k], g[k]);
       unpack(rr[k], rh[k]);
-      inside<ACC>(g[k], k, d, shift);
-      inside<ACC>(rh[k], k, d, shift);
+      if (ACC == kShift) {
+        inside<ACC>(g[k], k, d, shift);
+        inside<ACC>(rh[k], k, d, shift);
+      }
       if (DRES) unpack(ur[DRES ? k : 0], o[k]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

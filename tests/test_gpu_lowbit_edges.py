@@ -48,3 +48,30 @@ def test_what_follows_a_narrow_tensor_is_left_out_and_left(d):
                                dr=dr[:rows])
     assert torch.equal(dr[:rows], dr0) and torch.equal(dw, dw0)
     assert torch.isnan(dr[rows:]).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("d", [5, 96, 100, 300, 1000, 1049, 4097])
+@pytest.mark.parametrize("dtype,res", [(F32, None), (BF16, F32)])
+def test_quantised_rows_that_are_not_finite(d, fmt, dtype, res):
+    """Rows with a NaN, an infinity, or of zeros with eps 0 (rstd infinite): the bytes that
+    quantising their y gives, so byte 255 in every block with a column and 0 in the padding's."""
+    rows = 9
+    x, r, w = inputs(rows, d, dtype, res)
+    x[1, 0], x[4, d - 1], x[6] = float("nan"), float("inf"), 0
+    if r is not None:
+        r[6] = 0
+    xc, wc, rc = cu(x, w, r)
+    q = m3.add_rmsnorm(xc, wc, residual=rc, eps=0.0, fmt=fmt)[0]
+    y = m3.add_rmsnorm(xc, wc, residual=rc, eps=0.0)[0]
+    assert torch.isnan(y[[1, 6]]).all() and torch.isnan(y[4, d - 1])
+    u = m3.mx_quant(y, fmt)
+    bad = [1, 4, 6]
+    assert torch.equal(q.codes[[1, 6]], u.codes[[1, 6]])
+    blocks, kp = (d + 31) // 32, q.scales.numel() // 128 * 32
+    tiles = q.scales.view(-1, 32, 4, 4)[:, :, 0, :].permute(1, 0, 2).reshape(32, kp // 32)
+    other = u.scales.view(-1, 32, 4, 4)[:, :, 0, :].permute(1, 0, 2).reshape(32, kp // 32)
+    assert torch.equal(tiles[bad], other[bad])
+    assert torch.all(tiles[[1, 6], :blocks] == 255) and tiles[4, blocks - 1] == 255
+    assert torch.all(tiles[:, blocks:] == 0) and torch.all(tiles[rows:] == 0)
+    assert torch.all(q.codes[:, (d + 1) // 2 if fmt == "mxfp4" else d:] == 0)
