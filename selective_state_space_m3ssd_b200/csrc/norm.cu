@@ -90,15 +90,18 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, Raw<__nv_bfloat
 
 // kShift: whether the access of columns c to c + 7 of a row lies in the tensor, which has `left`
 // elements from the row's first on (a row of fewer than eight may have the tensor's end
-// rows behind it).
-__host__ __device__ __forceinline__ bool in_tensor(int c, int64_t left) { return c + 8 <= left; }
+// rows behind it), counted over eight rows at most: none of a row's accesses goes further.
+__host__ __device__ __forceinline__ bool in_tensor(int c, int left) { return c + 8 <= left; }
+__host__ __device__ __forceinline__ int left_of(int64_t rows, int64_t row, int d) {
+  return (int)(rows - row < 8 ? rows - row : 8) * d;
+}
 
 // Group k of the thread's values of a row, and back.  With kShift the first and the last access
 // of a row bring in its neighbours' ends too (inside() drops them; elements that another
 // CTA may be writing, in place, are among them), those that would reach past the tensor's end
 // are element by element; else there are zeros outside the row.
 template <int ACC, typename T>
-__device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, int64_t left,
+__device__ __forceinline__ void load_row(const T* row, int k, int d, int shift, int left,
                                          Raw<T>& r) {
   const int c = 8 * ((int)threadIdx.x + k * (int)blockDim.x) - (ACC == kStrided ? 0 : shift);
   float v[8];
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(NormArgs a) {
   Raw<T> xr[NV];
   Raw<R> rr[RES ? NV : 1];
   auto fetch = [&](int64_t i) {
-    const int64_t left = (a.rows - i) * d;
+    const int left = left_of(a.rows, i, d);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       load_row<ACC>(static_cast<const T*>(a.x) + i * d, k, d, shift, left, xr[k]);
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_bwd_kernel(NormBwdArg
   Raw<float> ur[DRES ? NV : 1];
   float rs = 0.f;
   auto fetch = [&](int64_t i) {
-    const int64_t left = (a.rows - i) * d;
+    const int left = left_of(a.rows, i, d);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       load_row<ACC>(static_cast<const T*>(a.dy) + i * d, k, d, shift, left, yr[k]);
@@ -506,7 +509,7 @@ int64_t partial_rows(int64_t rows, int64_t d) {
 }  // namespace
 
 bool norm_whole_access(int64_t rows, int64_t d, int64_t row, int c) {
-  return access_of(true, d) != kStrided && in_tensor(c, (rows - row) * d);
+  return access_of(true, d) != kStrided && in_tensor(c, left_of(rows, row, (int)d));
 }
 
 bool norm_width_ok(int64_t d) { return d <= kMaxWidth; }
