@@ -180,6 +180,8 @@ def load(path: str | None = None):
         lib.m3ssd_add_rmsnorm_bwd_workspace_size.restype = sz
         lib.m3ssd_add_rmsnorm_bwd.argtypes = [ndp] + [vp] * 8 + [sz, vp]
         lib.m3ssd_add_rmsnorm_bwd.restype = ctypes.c_int
+        lib.m3ssd_test_give_up_next_waits.argtypes = [ctypes.c_uint32]
+        lib.m3ssd_test_give_up_next_waits.restype = ctypes.c_int
         lib.m3ssd_test_norm_access.argtypes = [ndp, i64, i32, i32p]
         lib.m3ssd_test_norm_access.restype = ctypes.c_int
         for f in (lib.m3ssd_quant_state, lib.m3ssd_dequant_state):
@@ -274,6 +276,13 @@ def drop_next_gram_signal_for_tests():
     signal, so one of its bounded waits runs out (reported by
     device_wait_timeouts; that launch's outputs are undefined)."""
     _check(load().m3ssd_test_drop_next_gram_signal(), "m3ssd_test_drop_next_gram_signal")
+
+
+def give_up_next_waits_for_tests(lanes: int):
+    """Testing hook: in the next launch that has such waits (include/m3ssd.h), the lanes of
+    this mask in every warp that waits for a result give up at once (reported by
+    device_wait_timeouts; that launch's outputs are undefined)."""
+    _check(load().m3ssd_test_give_up_next_waits(int(lanes)), "m3ssd_test_give_up_next_waits")
 
 
 def fwd_split_plan(batch: int, seqlen: int, nheads: int, sms: int) -> tuple:

@@ -127,6 +127,7 @@ struct MArgs {
   Tiles tiles;             // the items of the CTAs
   int nkb;                 // 128-column groups of K
   int nb;                  // 128-row blocks of W
+  uint32_t give_up;        // lanes of the epilogue that do not wait (tests)
   bool vec;
 };
 
@@ -349,10 +350,7 @@ __global__ void __launch_bounds__(Cfg<AF, BN>::THREADS, 1)
     for (int t = blockIdx.x; t < g.tiles.items; t += gridDim.x) {
       const Item it = item_of<BN>(g.tiles, t);
       const int row0 = it.mb * BM + 32 * q, col0 = it.col0;
-      if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
-        *err = 1;
-        break;
-      }
+      if (!wait_all(&sm.tfull[acc], aphase, err, g.give_up)) break;
       tc5::fence_after_sync();
       const uint32_t tbase =
           tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * BN);
@@ -449,6 +447,7 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
   g.nkb = (int)(Kp / 128);
   g.nb = (int)((o.N + 127) / 128);
   g.vec = encode_output(&tm.d, o);
+  g.give_up = take_given_up_lanes();
   const size_t smem = sizeof(Smem<C>) + 1024;
   static_assert(sizeof(Smem<C>) + 1024 <= 232448, "one CTA's shared memory");
   static_assert(offsetof(Smem<C>, w) % 1024 == 0 && offsetof(Smem<C>, stg) % 1024 == 0 &&

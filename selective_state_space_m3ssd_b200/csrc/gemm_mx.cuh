@@ -33,9 +33,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// All lanes of a warp wait; a wait that runs out, for any of them, sets the CTA's error word.
-__device__ __forceinline__ bool wait_all(uint64_t* mbar, uint32_t parity, volatile uint32_t* err) {
-  if (__all_sync(0xffffffffu, tc5::mbar_wait(mbar, parity, kWaitLimitNs, err))) return true;
+// All lanes of a warp wait; a wait that runs out, for any of them, sets the CTA's error word, and
+// the warp goes on as one (what follows are instructions of whole warps).  The lanes of
+// `give_up` do not wait (a test's).
+__device__ __forceinline__ bool wait_all(uint64_t* mbar, uint32_t parity, volatile uint32_t* err,
+                                         uint32_t give_up = 0) {
+  const bool gave_up = give_up >> (threadIdx.x & 31) & 1u;
+  if (__all_sync(0xffffffffu, !gave_up && tc5::mbar_wait(mbar, parity, kWaitLimitNs, err)))
+    return true;
   *err = 1;
   return false;
 }

@@ -74,6 +74,7 @@ struct SArgs {
   int nt;                  // 128-column tiles of D
   int nkb;                 // 128-column groups of K
   int split;               // CTAs of a cluster
+  uint32_t give_up;        // lanes that do not wait for the products (tests)
   bool vec;                // four columns of D are one aligned store
 };
 
@@ -231,13 +232,15 @@ __global__ void __launch_bounds__(32 * Cfg<AF, BN, SWAP>::WARPS, 2)
     // every product issued has finished before the ring is written and TMEM released
     if (leader) tc5::commit(&sm.done);
     __syncwarp();
+    (void)tc5::mbar_wait(&sm.done, 0, kWaitLimitNs);
+    __syncwarp();
   } else {
     // ---- the partial tile, token by token: 16-byte unit u of a token's 128 sums at u ^ (token % 8)
-    if (!tc5::mbar_wait(&sm.done, 0, kWaitLimitNs)) *err = 1;
+    const bool ok = wait_all(&sm.done, 0, err, g.give_up);
     tc5::fence_after_sync();
     const int q = warp & 3, row = 32 * q + lane;  // of the tile's lanes
     const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16);
-    if (!*err) {
+    if (ok) {
       if constexpr (SWAP) {
         static_assert(!SWAP || BN == 16, "one load of TMEM");
         uint32_t v[16];
@@ -311,6 +314,7 @@ cudaError_t launch(const Operands& o, int split, cudaStream_t s) {
   g.nt = (int)nt;
   g.nkb = (int)(Kp / 128);
   g.split = split;
+  g.give_up = take_given_up_lanes();
   g.vec = o.N % 4 == 0 && o.ldd % 4 == 0 && (reinterpret_cast<uintptr_t>(o.D) & 7) == 0;
   const size_t smem = sizeof(Smem<C>) + 1024;
   static_assert(sizeof(Smem<C>) + 1024 <= 113 * 1024, "two CTAs on an SM");

@@ -249,6 +249,9 @@ cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const voi
                            const void* A_scales, const void* W, const void* W_scales, void* D,
                            int64_t ldd, cudaStream_t s);
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count);
+// The one-shot request of a test, handed to the launch that asks first: the lanes of the warps
+// that wait for a launch's results which give up their first waits at once (0: none).
+uint32_t take_given_up_lanes();
 
 // Decode step on a cache whose state is held as E4M3 codes with a scale a row
 // (csrc/step_q8.cu); every *_out may be the input it replaces.

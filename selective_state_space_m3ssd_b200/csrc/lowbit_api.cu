@@ -2,6 +2,7 @@
 // dispatch.  As in m3ssd_api.cu, nothing is allocated and nothing synchronises.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/m3ssd.h"
@@ -74,9 +75,20 @@ bool cache_aligned(const m3ssd_cache_q8* c) {
          aligned(c->b_prev, 4);
 }
 
+std::atomic<uint32_t> g_given_up_lanes{0};
+
 }  // namespace
 
+uint32_t m3ssd::take_given_up_lanes() {
+  return g_given_up_lanes.load(std::memory_order_relaxed) ? g_given_up_lanes.exchange(0) : 0;
+}
+
 extern "C" {
+
+m3ssd_status m3ssd_test_give_up_next_waits(uint32_t lanes) {
+  g_given_up_lanes.store(lanes);
+  return M3SSD_OK;
+}
 
 size_t m3ssd_mx_codes_size(int32_t format, int64_t rows, int64_t cols) {
   if (check_mx_size(format, rows, cols) != M3SSD_OK) return 0;

@@ -75,3 +75,26 @@ def test_quantised_rows_that_are_not_finite(d, fmt, dtype, res):
     assert torch.all(tiles[[1, 6], :blocks] == 255) and tiles[4, blocks - 1] == 255
     assert torch.all(tiles[:, blocks:] == 0) and torch.all(tiles[rows:] == 0)
     assert torch.all(q.codes[:, (d + 1) // 2 if fmt == "mxfp4" else d:] == 0)
+
+
+LANES = [1, 0x0000ffff, 0xaaaaaaaa, 0xffffffff]
+
+
+# one tile a CTA and several, whole and in parts; K in one CTA and over a cluster, tokens as the
+# narrow side and not
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", [(300, 520, 384), (20011, 1024, 256), (4096, 6464, 96),
+                                   (16, 8192, 256), (16, 1024, 8192), (100, 520, 8192)])
+def test_waits_that_some_lanes_give_up_end_the_product(fmt, M, N, K):
+    """The warps leave together, the launch is reported, and the next one is right."""
+    g = torch.Generator().manual_seed(M)
+    A = m3.mx_quant(torch.randn(M, K, generator=g).cuda(), fmt)
+    W = m3.mx_quant((torch.randn(N, K, generator=g) / K ** 0.5).cuda(), "mxfp4")
+    want = m3.gemm_mx(A, W)
+    assert m3.device_wait_timeouts() == 0
+    for lanes in LANES:
+        m3.give_up_next_waits_for_tests(lanes)
+        m3.gemm_mx(A, W)  # outputs undefined
+        assert m3.device_wait_timeouts() >= 1
+        assert torch.equal(m3.gemm_mx(A, W), want)
+        assert m3.device_wait_timeouts() == 0
