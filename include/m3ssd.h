@@ -570,10 +570,11 @@ m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count);
  */
 m3ssd_status m3ssd_test_set_wait_limit(uint64_t nanoseconds);
 m3ssd_status m3ssd_test_drop_next_gram_signal(void);
-/*   m3ssd_test_give_up_next_waits: in the next launch of m3ssd_gemm_mx, the lanes of this mask
- *     in every warp that waits for a result give up at once, as waits that run out do; the rest
- *     wait.  That launch is counted in m3ssd_device_wait_timeouts and leaves its outputs
- *     undefined; later launches are unaffected.  (Host state only; 0 takes it back.) */
+/*   m3ssd_test_give_up_next_waits: in the next launch of m3ssd_gemm_bf16 or m3ssd_gemm_mx,
+ *     the lanes of this mask in every warp that waits for a result give up at once, as waits
+ *     that run out do; the rest wait.  That launch is counted in m3ssd_device_wait_timeouts
+ *     and leaves its outputs undefined; later launches are unaffected.  (Host state only; 0
+ *     takes it back.) */
 m3ssd_status m3ssd_test_give_up_next_waits(uint32_t lanes);
 
 /* The result of the M3SSD_CHECK_FINITE checks enqueued since the last call:

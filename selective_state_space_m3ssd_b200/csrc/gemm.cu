@@ -109,6 +109,7 @@ struct GArgs {
   int64_t ldd;
   __nv_bfloat16* D;
   int mt, nt, nk;  // tiles along M and N, K slices
+  uint32_t give_up;  // lanes of the epilogue that do not wait (tests)
   bool vec;        // TMA stores (N % 8 == 0, ldd % 8 == 0 and D 16-byte aligned)
   bool nfast;      // tile t = (row block t / nt, column block t % nt), else (t % mt, t / mt)
 };
@@ -231,7 +232,10 @@ __global__ void __launch_bounds__(Cfg<H>::THREADS, 1)
     uint32_t nst = 0;  // blocks staged by this warp (alternating staging blocks)
     uint32_t aphase = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      if (!tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err)) {
+      // the warp leaves as one: what follows are loads of whole warps
+      const bool gave_up = g.give_up >> lane & 1u;
+      if (!__all_sync(0xffffffffu,
+                      !gave_up && tc5::mbar_wait(&sm.tfull[acc], aphase, kWaitLimitNs, err))) {
         *err = 1;
         break;
       }
@@ -388,6 +392,7 @@ cudaError_t launch_gemm_bf16(int64_t M, int64_t N, int64_t K, const void* A, con
   // a TMA store ends a row at a multiple of 16 bytes (it fills the rest with zeros), so N
   // must be a multiple of 8 too
   g.vec = N % 8 == 0 && ldd % 8 == 0 && (reinterpret_cast<uintptr_t>(D) & 15) == 0;
+  g.give_up = take_given_up_lanes();
   // the CTAs in flight share the panels of the smaller operand, which L2 keeps
   // while the larger one streams from DRAM once
   g.nfast = M > N;

@@ -98,3 +98,20 @@ def test_waits_that_some_lanes_give_up_end_the_product(fmt, M, N, K):
         assert m3.device_wait_timeouts() >= 1
         assert torch.equal(m3.gemm_mx(A, W), want)
         assert m3.device_wait_timeouts() == 0
+
+
+# one tile a CTA and several; the pairs of row blocks too; aligned outputs and not
+@pytest.mark.parametrize("M,N,K", [(300, 520, 72), (16384, 1024, 256), (37888, 256, 128),
+                                   (75000, 250, 64), (3000, 2001, 128)])
+def test_waits_that_some_lanes_give_up_end_the_bf16_product(M, N, K):
+    g = torch.Generator().manual_seed(M)
+    A = torch.randn(M, K, generator=g).bfloat16().cuda()
+    W = (torch.randn(N, K, generator=g) / K ** 0.5).bfloat16().cuda()
+    want = m3.gemm_bf16(A, W)
+    assert m3.device_wait_timeouts() == 0
+    for lanes in LANES:
+        m3.give_up_next_waits_for_tests(lanes)
+        m3.gemm_bf16(A, W)  # outputs undefined
+        assert m3.device_wait_timeouts() >= 1
+        assert torch.equal(m3.gemm_bf16(A, W), want)
+        assert m3.device_wait_timeouts() == 0
