@@ -548,9 +548,10 @@ m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float*
 
 /* Number of bounded device-side waits of the chunked forwards (SISO and
  * MIMO), the tensor-core backward, the GEMMs and the 8-bit step that ran out since
- * the last call (a forward's and a step's CTA then stops and leaves its
- * outputs unwritten; the backward's and the GEMMs' CTAs skip their remaining waits and
- * leave their outputs undefined); the count is then reset.  This call synchronises the current device
+ * the last call (a forward's CTA then stops and leaves its outputs unwritten, a step's those
+ * of the (b, h) it had not come to, so that with a cache_out of its own the step can be taken
+ * again while a cache written in place is undefined; the backward's and the GEMMs' CTAs skip
+ * their remaining waits and leave their outputs undefined); the count is then reset.  This call synchronises the current device
  * and must not be captured in a CUDA graph.  Returns M3SSD_ERR_INVALID_ARG for
  * a NULL pointer and M3SSD_ERR_CUDA if the device cannot be read. */
 m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count);
@@ -570,11 +571,12 @@ m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count);
  */
 m3ssd_status m3ssd_test_set_wait_limit(uint64_t nanoseconds);
 m3ssd_status m3ssd_test_drop_next_gram_signal(void);
-/*   m3ssd_test_give_up_next_waits: in the next launch of m3ssd_gemm_bf16 or m3ssd_gemm_mx,
- *     the lanes of this mask in every warp that waits for a result give up at once, as waits
- *     that run out do; the rest wait.  That launch is counted in m3ssd_device_wait_timeouts
- *     and leaves its outputs undefined; later launches are unaffected.  (Host state only; 0
- *     takes it back.) */
+/*   m3ssd_test_give_up_next_waits: in the next launch of m3ssd_gemm_bf16, m3ssd_gemm_mx or
+ *     m3ssd_step_q8 (N = 128, P = 64, 16-byte aligned, more than two (b, h) an SM), the lanes
+ *     of this mask in every warp that waits for copies or a result give up at once, as waits
+ *     that run out do; the rest wait.  That launch is counted in m3ssd_device_wait_timeouts,
+ *     its outputs as there; later launches are unaffected.  (Host state only; 0 takes it
+ *     back.) */
 m3ssd_status m3ssd_test_give_up_next_waits(uint32_t lanes);
 
 /* The result of the M3SSD_CHECK_FINITE checks enqueued since the last call:

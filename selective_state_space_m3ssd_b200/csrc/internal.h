@@ -277,6 +277,7 @@ struct StepQ8Args {
   float* x_prev_out;
   float* b_prev_out;
   void* y_t;
+  uint32_t give_up;      // lanes that do not wait for their copies (tests; the launch sets it)
 };
 cudaError_t launch_step_q8(const StepQ8Args& a, cudaStream_t s);
 cudaError_t read_and_clear_step_q8_wait_timeouts(unsigned int* count);

@@ -390,22 +390,20 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
     const float2 bp = cur.bp;
     const float alpha = expf(cur.ld), be = cur.be, ga = cur.ga;
     const StepStage<T>& d = stage[st];
-    const bool late = !tc5::mbar_wait(&full[st], (it >> 1) & 1u, kWaitLimitNs);
+    // the lanes of give_up do not wait (a test's); a warp is late where one of its lanes is
+    const bool late = __any_sync(0xffffffffu, (a.give_up >> lane & 1u) ||
+                                 !tc5::mbar_wait(&full[st], (it >> 1) & 1u, kWaitLimitNs));
+    float ph;
     {
       float sn, cs;
       const float ang = d.angle[t];
       sincos_reduced(ang, &sn, &cs);
       const float2 rp = rot2(cs, sn, bp.x, bp.y);
-      const float ph = wrap_angle(ang + (a.theta_t ? d.theta[t] : 0.f));
+      ph = wrap_angle(ang + (a.theta_t ? d.theta[t] : 0.f));
       sincos_reduced(ph, &sn, &cs);
       const float2 rb = rot2(cs, sn, b0, b1), rc = rot2(cs, sn, c0, c1);
       coef.set_all(2 * t, be * rp.x, ga * rb.x, rc.x, alpha * d.scale[2 * t]);
       coef.set_all(2 * t + 1, be * rp.y, ga * rb.y, rc.y, alpha * d.scale[2 * t + 1]);
-      if (!late) {
-        a.angle_out[bh * (kN / 2) + t] = ph;
-        if (a.b_prev_out && cur.first)
-          *reinterpret_cast<float2*>(a.b_prev_out + cur.at) = make_float2(b0, b1);
-      }
     }
     if (tc5::bar_or(1, kWalkThreads, late)) {  // the copies in flight land before the CTA ends
       if (t == 0) {
@@ -416,6 +414,10 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
       }
       return;
     }
+    // nothing of this (b, h) is written before no thread was late
+    a.angle_out[bh * (kN / 2) + t] = ph;
+    if (a.b_prev_out && cur.first)
+      *reinterpret_cast<float2*>(a.b_prev_out + cur.at) = make_float2(b0, b1);
     uint64_t x2[8], xp2[8], acc[8] = {};
     {
       float v[16];
@@ -651,10 +653,12 @@ cudaError_t launch_step_t(StepQ8Args a, cudaStream_t s) {
     const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
     const int64_t walkers = sms * kWalkCtas;
     // up to two CTAs of four warps an SM run at once; more (b, h) than that are walked
-    if (nbh <= 2 * sms)
+    if (nbh <= 2 * sms) {
       step_q8_one<T><<<(unsigned)nbh, 128, 0, s>>>(a);
-    else
+    } else {
+      a.give_up = take_given_up_lanes();
       step_q8_walk<T><<<(unsigned)(nbh < walkers ? nbh : walkers), kWalkThreads, 0, s>>>(a);
+    }
   } else {
     const size_t smem = sizeof(float) * (size_t)(3 * a.N + kGenWarps * a.P);
     int lanes = 1;

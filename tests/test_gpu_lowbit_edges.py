@@ -115,3 +115,36 @@ def test_waits_that_some_lanes_give_up_end_the_bf16_product(M, N, K):
         assert m3.device_wait_timeouts() >= 1
         assert torch.equal(m3.gemm_bf16(A, W), want)
         assert m3.device_wait_timeouts() == 0
+
+
+def step_inputs(b, H, P, N, G, dtype, seed=0):
+    """x_t, logdecay, beta, gamma, B, C, theta, D and a quantised cache."""
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    a = [n(b, H, P).to(dtype), -torch.rand(b, H, generator=g), n(b, H), n(b, H),
+         n(b, G, N).to(dtype), n(b, G, N).to(dtype), n(b, H, N // 2), n(H)]
+    cache = m3.quant_cache({"angle": n(b, H, N // 2).cuda(), "ssm": n(b, H, N, P).cuda(),
+                            "x_prev": n(b, H, P).cuda(), "b_prev": n(b, G, N).cuda()})
+    return [t.cuda() for t in a], cache
+
+
+# one round a CTA, and two
+@pytest.mark.parametrize("b,H,G", [(10, 32, 1), (40, 32, 4)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_step_whose_wait_some_lanes_give_up_writes_nothing(b, H, G, dtype):
+    a, cache = step_inputs(b, H, 64, 128, G, dtype)
+    want_cache = {k: torch.empty_like(v) for k, v in cache.items()}
+    want = m3.step_q8(cache, *a, cache_out=want_cache)
+    assert m3.device_wait_timeouts() == 0
+    for lanes in LANES:
+        out = {k: torch.full_like(v, 77) for k, v in cache.items()}
+        y = torch.full_like(a[0], 77)
+        m3.give_up_next_waits_for_tests(lanes)
+        m3.step_q8(cache, *a, cache_out=out, y_t=y)
+        assert m3.device_wait_timeouts() >= 1
+        for t in (y, *out.values()):
+            assert torch.all(t == 77)
+        m3.step_q8(cache, *a, cache_out=out, y_t=y)  # the same step again
+        assert m3.device_wait_timeouts() == 0
+        assert torch.equal(y, want)
+        assert all(torch.equal(out[k], want_cache[k]) for k in out)
