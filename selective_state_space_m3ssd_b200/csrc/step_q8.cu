@@ -74,9 +74,8 @@ template <bool EXACT>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   const float t = fmaf(amax, 1.f / 448.f, amax * 0.f);
   s = amax < kTiny ? 0.f : t;
-  const float u = fmaxf(t, 1.f / 448.f * kTiny);  // a row of zeros: finite, and codes of 0
-  inv = EXACT ? 1.f / u : rcp_approx(u);
-  if (EXACT && amax < kTiny) inv = 0.f;
+  const float u = fmaxf(t, 1.f / 448.f * kTiny);  // (a NaN row's codes are not read)
+  inv = amax < kTiny ? 0.f : EXACT ? 1.f / u : rcp_approx(u);
 }
 
 __device__ __forceinline__ void load16(const float* p, float (&v)[16]) {

@@ -148,3 +148,30 @@ def test_a_step_whose_wait_some_lanes_give_up_writes_nothing(b, H, G, dtype):
         assert m3.device_wait_timeouts() == 0
         assert torch.equal(y, want)
         assert all(torch.equal(out[k], want_cache[k]) for k in out)
+
+
+# both kernels of N = 128, P = 64, and the general one with whole accesses and without
+@pytest.mark.parametrize("b,H,P,N", [(2, 4, 64, 128), (10, 32, 64, 128), (3, 4, 64, 64),
+                                     (3, 4, 75, 32)])
+def test_a_step_holds_tiny_rows_as_quant_state_does(b, H, P, N):
+    """A state that decays below 2^-100 a row: scale 0 and codes 0 (or -0), as quant_state
+    writes the same values."""
+    a, _ = step_inputs(b, H, P, N, 1, F32)
+    g = torch.Generator().manual_seed(5)
+    ssm = torch.randn(b, H, N, P, generator=g).cuda()
+    up = torch.full((b, H, N, 1), 2.0 ** -99, device="cuda")
+    up[:, :, ::3], up[:, :, 1::3] = 2.0 ** -104, 2.0 ** -130
+    zero = torch.zeros(b, 1, N, device="cuda")
+    cache = m3.quant_cache({"angle": torch.zeros(b, H, N // 2, device="cuda"), "ssm": ssm,
+                            "x_prev": torch.zeros(b, H, P, device="cuda"), "b_prev": zero})
+    cache["scale"] *= up[..., 0]
+    held = m3.dequant_state(cache["ssm"], cache["scale"])
+    codes, scale = m3.quant_state(held)
+    m3.step_q8(cache, a[0], torch.zeros(b, H, device="cuda"), None, torch.zeros(b, H, device="cuda"),
+               zero, zero)
+    tiny = held.abs().amax(-1) < 2.0 ** -100
+    assert tiny[:, :, ::3].all() and tiny[:, :, 1::3].all() and not tiny.all()
+    assert torch.equal(cache["scale"] == 0, tiny) and torch.equal(scale == 0, tiny)
+    assert torch.all(cache["ssm"][tiny] & 127 == 0) and torch.all(codes[tiny] & 127 == 0)
+    assert torch.equal(m3.dequant_state(cache["ssm"], cache["scale"])[tiny],
+                       torch.zeros_like(held)[tiny])
