@@ -299,6 +299,18 @@ def make_dims(batch, seqlen, nheads, headdim, dstate, ngroups, x_dtype, chunk=0,
     return Dims(batch, seqlen, nheads, headdim, dstate, ngroups, chunk, x_dtype, flags, 0)
 
 
+def _workspace(workspace, need: int, device):
+    """A call's device scratch, allocated where the caller gave none: the tensor, its
+    address and its bytes.  A caller's is one contiguous run of memory on ``device``."""
+    if workspace is None and need:
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", device=device)
+    if workspace is None:
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def fwd_workspace_size(dims: Dims) -> int:
     return int(load().m3ssd_fwd_workspace_size(ctypes.byref(dims)))
 
@@ -349,13 +361,10 @@ def fwd(X, logdecay, beta, gamma, B, C, theta=None, D=None, h0=None, *, Y=None,
             *(None if cache_out is None else cache_out[k].data_ptr()
               for k in ("angle", "x_prev", "b_prev")))
     dims = make_dims(b, L, H, P, N, G, _xdtype(X), chunk, CHECK_FINITE if check_finite else 0)
-    ws_bytes = fwd_workspace_size(dims)
-    if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace, ws, ws_bytes = _workspace(workspace, fwd_workspace_size(dims), dev)
     st = load().m3ssd_fwd(ctypes.byref(dims), _ptr(X), _ptr(logdecay), _ptr(beta), _ptr(gamma),
                           _ptr(B), _ptr(C), _ptr(theta), _ptr(D), _ptr(h0), _ptr(Y), _ptr(hT),
-                          None if extra is None else ctypes.byref(extra), _ptr(workspace),
-                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                          None if extra is None else ctypes.byref(extra), ws, ws_bytes,
                           _stream_handle(dev))
     _check(st, "m3ssd_fwd")
     return Y, hT, cache_out
@@ -414,16 +423,12 @@ def bwd(X, logdecay, beta, gamma, B, C, theta=None, D=None, h0=None, *, dY, dhT=
     ``GRAD_NAMES``, each shaped like its input (allocated by torch unless
     ``grads`` supplies them).
     """
-    import torch
     dims, ptrs, extra, gs, grads = _bwd_args(X, logdecay, beta, gamma, B, C, theta, D, h0, dY,
                                              dhT, angle0, xprev0, bprev0, grads)
-    ws_bytes = bwd_workspace_size(dims)
-    if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=X.device)
+    workspace, ws, ws_bytes = _workspace(workspace, bwd_workspace_size(dims), X.device)
     st = load().m3ssd_bwd(ctypes.byref(dims), *ptrs,
                           None if extra is None else ctypes.byref(extra), _ptr(dY), _ptr(dhT),
-                          ctypes.byref(gs), _ptr(workspace),
-                          0 if workspace is None else workspace.numel() * workspace.element_size(),
+                          ctypes.byref(gs), ws, ws_bytes,
                           _stream_handle(X.device))
     _check(st, "m3ssd_bwd")
     return grads
@@ -642,13 +647,11 @@ def block_fwd(u, wts: dict, *, cache_in=None, cache_out=None, out=None, workspac
     _need(out, "out", torch.bfloat16, (b, L, dm), dev)
     ci = None if cache_in is None else _cache_struct(cache_in, b, H, P, N, G, dev, "cache_in")
     co = None if cache_out is None else _cache_struct(cache_out, b, H, P, N, G, dev, "cache_out")
-    need = block_workspace_size(dims)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace, ws, ws_bytes = _workspace(workspace, block_workspace_size(dims), dev)
     st = load().m3ssd_block_fwd(ctypes.byref(dims), ctypes.byref(w), _ptr(u), _ptr(out),
                                 None if ci is None else ctypes.byref(ci),
-                                None if co is None else ctypes.byref(co), _ptr(workspace),
-                                workspace.numel(), _stream_handle(dev))
+                                None if co is None else ctypes.byref(co), ws, ws_bytes,
+                                _stream_handle(dev))
     _check(st, "m3ssd_block_fwd")
     return out
 
@@ -678,12 +681,9 @@ def block_step(cache: dict, u_t, wts: dict, *, out_t=None, workspace=None):
     out_t = torch.empty_like(u_t) if out_t is None else out_t
     _need(out_t, "out_t", torch.bfloat16, (b, dm), dev)
     c = _cache_struct(cache, b, H, P, N, G, dev, "cache")
-    need = block_workspace_size(dims)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace, ws, ws_bytes = _workspace(workspace, block_workspace_size(dims), dev)
     st = load().m3ssd_block_step(ctypes.byref(dims), ctypes.byref(w), _ptr(u_t), _ptr(out_t),
-                                 ctypes.byref(c), _ptr(workspace), workspace.numel(),
-                                 _stream_handle(dev))
+                                 ctypes.byref(c), ws, ws_bytes, _stream_handle(dev))
     _check(st, "m3ssd_block_step")
     return out_t
 
@@ -904,11 +904,9 @@ def add_rmsnorm_bwd(dy, r, w, rstd, *, dres=None, dr=None, dw=None, workspace=No
     else:
         with torch.cuda.device(dev):
             need = add_rmsnorm_bwd_workspace_size(dims)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_add_rmsnorm_bwd", dev, ctypes.byref(dims), _addr(dy), _addr(r), _addr(w),
-            _addr(rstd), _addr(dres), _addr(dr), _addr(dw), _addr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size())
+            _addr(rstd), _addr(dres), _addr(dr), _addr(dw), ws, ws_bytes)
     return dr, dw
 
 

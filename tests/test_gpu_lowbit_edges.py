@@ -175,3 +175,26 @@ def test_a_step_holds_tiny_rows_as_quant_state_does(b, H, P, N):
     assert torch.all(cache["ssm"][tiny] & 127 == 0) and torch.all(codes[tiny] & 127 == 0)
     assert torch.equal(m3.dequant_state(cache["ssm"], cache["scale"])[tiny],
                        torch.zeros_like(held)[tiny])
+
+
+def test_a_workspace_elsewhere_is_refused():
+    """Host memory, and memory with holes: before any launch."""
+    dy, r, w = cu(*inputs(6, 40, F32, F32))
+    rstd = torch.ones(6, device="cuda")
+    need = m3.add_rmsnorm_bwd_workspace_size(m3.NormDims(6, 40, m3.F32, m3.F32, 0.0, 0))
+    want = m3.add_rmsnorm_bwd(dy, r, w, rstd)
+    for bad in (torch.empty(2 * need, dtype=torch.uint8),
+                torch.empty(4 * need, dtype=torch.uint8, device="cuda")[::2],
+                torch.empty(1, dtype=torch.uint8, device="cuda").expand(2 * need)):
+        with pytest.raises(ValueError, match="workspace must be"):
+            m3.add_rmsnorm_bwd(dy, r, w, rstd, workspace=bad)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    got = m3.add_rmsnorm_bwd(dy, r, w, rstd, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x = torch.randn(1, 70, 2, 64, device="cuda", dtype=BF16)
+    bc, f = torch.randn(1, 70, 1, 128, device="cuda", dtype=BF16), torch.randn(1, 70, 2, device="cuda")
+    for call in (lambda ws: m3.fwd(x, -f.abs(), f, f, bc, bc, workspace=ws),
+                 lambda ws: m3.bwd(x, -f.abs(), f, f, bc, bc, dY=x, workspace=ws)):
+        call(None)
+        with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+            call(torch.empty(1 << 24, dtype=torch.uint8))

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import selective_state_space_m3ssd_b200 as m3
 
@@ -37,3 +38,13 @@ def test_norm_access_arguments(lib):
         assert f(n, row, column, r) == m3.ERR_INVALID_ARG
     assert f(n, 0, 0, None) == m3.ERR_INVALID_ARG
     assert f(ctypes.byref(m3.NormDims(4, 0, 0, 0, 0, 0)), 0, 0, r) == m3.ERR_INVALID_ARG
+
+
+def test_a_workspace_is_memory_of_the_call_s_device():
+    dev = torch.device("cuda", 0)
+    assert m3._workspace(None, 0, dev) == (None, None, 0)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        m3._workspace(torch.empty(64, dtype=torch.uint8), 64, dev)
+    # the binding refuses before anything is launched
+    with pytest.raises(ValueError, match="workspace must be"):
+        m3._workspace(torch.empty(64, dtype=torch.uint8, device="meta"), 64, dev)
