@@ -511,9 +511,11 @@ m3ssd_status m3ssd_test_norm_access(const m3ssd_norm_dims* dims, int64_t row, in
 /*
  * A decode cache whose state is held in 8 bits.  A row (b, h, n) of the state, P values, is
  * E4M3 codes with one fp32 scale: s = amax fp32(1 / 448), code = v (1 / s) rounded to nearest
- * even, v ~ code s.  Rows with amax < 2^-100 are held as zeros (s = 0); a row with a NaN or an
- * infinity takes a NaN scale and reads back as NaN.  A held value is within 2^-4 of its
- * magnitude or 2^-10 s, whichever is larger.
+ * even, v ~ code s.  The reciprocal is correctly rounded in m3ssd_quant_state and within an ulp
+ * in m3ssd_step_q8, so that a value at a border between two codes may take either there.  Rows
+ * with amax < 2^-100 are held as zeros (s = 0, codes 0 or -0); a row with a NaN or an infinity
+ * takes a NaN scale and reads back as NaN.  A held value is within 2^-4 of its magnitude or
+ * 2^-10 s, whichever is larger, and 2^-23 of it for the reciprocal.
  */
 typedef struct {
   float* angle;      /* (b, H, N/2) */

@@ -69,7 +69,8 @@ __device__ __forceinline__ float rcp_approx(float v) {
 
 // A row's scale from its largest magnitude (NaN where that is not finite: amax 0), and its
 // reciprocal: the correctly rounded one (EXACT), or the hardware's, within an ulp, which moves
-// only values next to a rounding border.
+// only values next to a rounding border (rounded correctly the step takes 38.4 us against 35.4
+// at b256 H32, 53 against 46 at N64 P64).
 template <bool EXACT>
 __device__ __forceinline__ void row_scale(float amax, float& s, float& inv) {
   const float t = fmaf(amax, 1.f / 448.f, amax * 0.f);

@@ -7,6 +7,7 @@ import torch
 import selective_state_space_m3ssd_b200 as m3
 from oracle import lowbit as ol
 from tests import test_gpu_norm as norm
+from tests import test_gpu_step_q8 as step_q8
 from tests.test_gpu_norm import BF16, F32, FP, cu, inputs, np64, summed
 
 pytestmark = pytest.mark.gpu
@@ -198,3 +199,30 @@ def test_a_workspace_elsewhere_is_refused():
         call(None)
         with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
             call(torch.empty(1 << 24, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("b,H,P,N", [(2, 4, 64, 128), (12, 32, 64, 128), (3, 4, 64, 64),
+                                     (2, 3, 12, 10)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_angles_of_the_whole_range(b, H, P, N, dtype):
+    """Old angles and theta up to 1e5 with sums up to 1e5, all multiples of 2^-6: the fp32 sum
+    is exact, and so is x - k fp32(2 pi) or x - k fp32(pi / 2) (k below 2^16, multiples of
+    2^-21 or 2^-23 near or below pi).  The second term's rounding is 2^-23 at most and what two
+    terms leave of 2 pi or pi / 2 below 1e-9 for such k: within the 4 2^-23 that the step's
+    tolerances allow an angle."""
+    inp, cache = step_q8.make(b, H, 1, N, P, dtype)
+    g = torch.Generator().manual_seed(11)
+    at = lambda *s: torch.round((torch.rand(*s, generator=g) * 2 - 1) * 1e5 * 64) / 64  # noqa: E731
+    old, new = at(b, H, N // 2), at(b, H, N // 2)
+    theta = new - old
+    far = theta.abs() > 1e5
+    theta[far] = old[far].sign() * 0.25
+    old.view(-1)[:4] = torch.tensor([1e5, -1e5, 99999.0, 0.0])
+    theta.view(-1)[:4] = torch.tensor([-1e5, 1e5, 1.0, -99999.984375])
+    assert (old.double() + theta.double()).abs().max() <= 1e5 + 1
+    cache["angle"], inp["theta"] = old, theta
+    args = [None if inp[k] is None else inp[k].cuda() for k in step_q8.ORDER]
+    cd = step_q8.to_cuda(cache)
+    out = {k: torch.full_like(v, 77) for k, v in cd.items()}
+    y = m3.step_q8(cd, *args, cache_out=out)
+    step_q8.check(inp, cache, y, out, dtype == "bf16")
