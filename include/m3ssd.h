@@ -474,6 +474,13 @@ m3ssd_status m3ssd_mx_dequant(const m3ssd_mx* in, int32_t x_dtype, void* x, int6
 m3ssd_status m3ssd_gemm_mx(const m3ssd_mx* A, const m3ssd_mx* W, void* D, int64_t ldd,
                            void* stream);
 
+/* How m3ssd_gemm_mx takes such a product on a device with `sms` SMs: *split CTAs of a cluster
+ * share a tile's K, *tile tokens wide (0: no split; *tile columns of D), and the tiles left
+ * over after whole rounds go out in parts of *part columns (0: whole).  Host arithmetic only;
+ * for tests and tuning. */
+m3ssd_status m3ssd_test_gemm_mx_plan(int32_t a_format, int64_t M, int64_t N, int64_t K,
+                                     int32_t sms, int32_t* split, int32_t* tile, int32_t* part);
+
 /*
  * Forward of the residual addition and norm.  residual and residual_out are given together
  * or not at all; residual_out may be residual.  Exactly one of y (rows x width, x_dtype; may

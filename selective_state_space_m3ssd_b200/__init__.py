@@ -180,6 +180,8 @@ def load(path: str | None = None):
         lib.m3ssd_add_rmsnorm_bwd_workspace_size.restype = sz
         lib.m3ssd_add_rmsnorm_bwd.argtypes = [ndp] + [vp] * 8 + [sz, vp]
         lib.m3ssd_add_rmsnorm_bwd.restype = ctypes.c_int
+        lib.m3ssd_test_gemm_mx_plan.argtypes = [i32, i64, i64, i64, i32, i32p, i32p, i32p]
+        lib.m3ssd_test_gemm_mx_plan.restype = ctypes.c_int
         lib.m3ssd_test_give_up_next_waits.argtypes = [ctypes.c_uint32]
         lib.m3ssd_test_give_up_next_waits.restype = ctypes.c_int
         lib.m3ssd_test_norm_access.argtypes = [ndp, i64, i32, i32p]
@@ -825,6 +827,17 @@ def gemm_mx(A: MXTensor, W: MXTensor, *, out=None):
     a, w = _mx_struct(A, "A", out.device), _mx_struct(W, "W", out.device)
     _launch("m3ssd_gemm_mx", dev, ctypes.byref(a), ctypes.byref(w), _addr(out), ldd)
     return out
+
+
+def gemm_mx_plan(M: int, N: int, K: int, fmt: str, sms: int) -> tuple:
+    """(split, tile, part) of :func:`gemm_mx` with A (M, K) in ``fmt`` and W (N, K) on a device
+    with ``sms`` SMs: the CTAs that share a tile's K (0: none), the tile's tokens there, else
+    its columns, and the columns of the parts that the last tiles go out in (0: whole)."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    _check(load().m3ssd_test_gemm_mx_plan(_mx_format(fmt), int(M), int(N), int(K), int(sms),
+                                          *(ctypes.byref(v) for v in out)),
+           "m3ssd_test_gemm_mx_plan")
+    return tuple(v.value for v in out)
 
 
 # ---- the residual addition with the RMS norm -------------------------------------------

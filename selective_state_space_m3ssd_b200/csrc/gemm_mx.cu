@@ -475,19 +475,24 @@ cudaError_t launch(const Operands& o, int64_t sms, cudaStream_t s) {
 //   1500 x 6464 x 1024   11.7 10.0 11.0    15.1 14.0 16.4
 //   1000 x 2048 x 4096   10.4 9.7 8.3      14.9 13.9 12.6
 // (256 x 192 gained 1 to 5 % on a few shapes and lost 15 % on others.)
+int tile_of(int64_t M, int64_t N, int64_t sms) {
+  auto cost = [&](int bn, int64_t round) {
+    const Plan p = plan(M, N, bn, sms);
+    return p.rounds * round + (p.left ? round * p.pw / bn : 0);
+  };
+  const int64_t wide = cost(256, 100), mid = cost(192, 78), small = cost(128, 59);
+  return wide <= mid && wide <= small ? 256 : mid <= small ? 192 : 128;
+}
+
 template <int AF>
 cudaError_t launch_af(const Operands& o, cudaStream_t s) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int split = split_of(o.M, o.N, o.K, AF, sms);
   if (split > 0) return launch_split(AF, o, split, s);
-  auto cost = [&](int bn, int64_t round) {
-    const Plan p = plan(o.M, o.N, bn, sms);
-    return p.rounds * round + (p.left ? round * p.pw / bn : 0);
-  };
-  const int64_t wide = cost(256, 100), mid = cost(192, 78), small = cost(128, 59);
-  return wide <= mid && wide <= small ? launch<AF, 256>(o, sms, s)
-         : mid <= small               ? launch<AF, 192>(o, sms, s)
-                                      : launch<AF, 128>(o, sms, s);
+  const int bn = tile_of(o.M, o.N, sms);
+  return bn == 256   ? launch<AF, 256>(o, sms, s)
+         : bn == 192 ? launch<AF, 192>(o, sms, s)
+                     : launch<AF, 128>(o, sms, s);
 }
 
 }  // namespace
@@ -498,6 +503,14 @@ cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const voi
   if (M == 0 || N == 0) return cudaSuccess;
   const Operands o{M, N, K, A, A_scales, W, W_scales, D, ldd};
   return a_fmt == mx::kFp4 ? launch_af<mx::kFp4>(o, s) : launch_af<mx::kFp8>(o, s);
+}
+
+GemmMxPlan gemm_mx_plan(int a_fmt, int64_t M, int64_t N, int64_t K, int64_t sms) {
+  const int split = split_of(M, N, K, a_fmt, sms);
+  if (split > 0) return {split, M <= 16 ? 16 : 128, 0};
+  const int bn = tile_of(M, N, sms);
+  const Plan p = plan(M, N, bn, sms);
+  return {0, bn, p.full < p.items ? p.pw : 0};
 }
 
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count) {

@@ -248,6 +248,13 @@ cudaError_t launch_mx_dequant(int fmt, int64_t rows, int64_t cols, bool bf16, co
 cudaError_t launch_gemm_mx(int a_fmt, int64_t M, int64_t N, int64_t K, const void* A,
                            const void* A_scales, const void* W, const void* W_scales, void* D,
                            int64_t ldd, cudaStream_t s);
+// How such a product is taken on a device of `sms` SMs: K split over the CTAs of a cluster
+// (split > 0), or not; the tile's tokens there, else its columns; the columns of the parts that
+// the last tiles go out in (0: whole).
+struct GemmMxPlan {
+  int split, tile, part;
+};
+GemmMxPlan gemm_mx_plan(int a_fmt, int64_t M, int64_t N, int64_t K, int64_t sms);
 cudaError_t read_and_clear_gemm_mx_wait_timeouts(unsigned int* count);
 // The one-shot request of a test, handed to the launch that asks first: the lanes of the warps
 // that wait for a launch's results which give up their first waits at once (0: none).

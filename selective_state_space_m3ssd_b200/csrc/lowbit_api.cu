@@ -139,6 +139,19 @@ m3ssd_status m3ssd_gemm_mx(const m3ssd_mx* A, const m3ssd_mx* W, void* D, int64_
                                          static_cast<cudaStream_t>(stream)));
 }
 
+m3ssd_status m3ssd_test_gemm_mx_plan(int32_t a_format, int64_t M, int64_t N, int64_t K,
+                                     int32_t sms, int32_t* split, int32_t* tile, int32_t* part) {
+  m3ssd_status st = check_mx_size(a_format, M, K);
+  if (st == M3SSD_OK) st = check_mx_size(M3SSD_MXFP4, N, K);
+  if (st != M3SSD_OK) return st;
+  if (M < 1 || N < 1 || sms < 1 || !split || !tile || !part) return M3SSD_ERR_INVALID_ARG;
+  const m3ssd::GemmMxPlan p = m3ssd::gemm_mx_plan(a_format, M, N, K, sms);
+  *split = p.split;
+  *tile = p.tile;
+  *part = p.part;
+  return M3SSD_OK;
+}
+
 m3ssd_status m3ssd_add_rmsnorm(const m3ssd_norm_dims* dims, const void* x, const void* residual,
                                const float* w, void* y, const m3ssd_mx* y_mx, void* residual_out,
                                float* rstd, void* stream) {

@@ -6,6 +6,7 @@ import torch
 
 import selective_state_space_m3ssd_b200 as m3
 from oracle import lowbit as ol
+from tests import test_gpu_mx as mx
 from tests import test_gpu_norm as norm
 from tests import test_gpu_step_q8 as step_q8
 from tests.test_gpu_norm import BF16, F32, FP, cu, inputs, np64, summed
@@ -226,3 +227,15 @@ def test_angles_of_the_whole_range(b, H, P, N, dtype):
     out = {k: torch.full_like(v, 77) for k, v in cd.items()}
     y = m3.step_q8(cd, *args, cache_out=out)
     step_q8.check(inp, cache, y, out, dtype == "bf16")
+
+
+# what no other shape of the tests takes: the tiles left over in parts of 128 columns of 192, and
+# 4-bit A with K over four CTAs beyond 16 tokens
+PLANS = [(32006, 262, 38), (32006, 264, 200), (1785, 14959, 380), (269, 528, 4373),
+         (269, 529, 4400)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("M,N,K", PLANS)
+def test_gemm_plans(fmt, M, N, K):
+    mx.test_gemm_parts_of_tiles(fmt, M, N, K)
