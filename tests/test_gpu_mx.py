@@ -117,8 +117,8 @@ def check(D, A, W, rows=None):
 SHAPES = [(1, 8, 32), (1, 1, 1), (5, 24, 100), (16, 128, 128), (16, 300, 1024), (17, 129, 257),
           (33, 520, 384), (64, 200, 640), (65, 64, 96), (127, 255, 64), (128, 256, 512),
           (129, 257, 1032), (300, 520, 200), (1000, 808, 768),
-          # every tile the host chooses from, aligned and ragged: 128 x 192 (two), 128 x 256,
-          # 256 x 192 (128 x 128 above)
+          # every tile the host chooses from, aligned and ragged: 128 x 192 (two), 128 x 256 (two),
+          # 128 x 192 (two; 128 x 128 above)
           (300, 6464, 160), (299, 6463, 96), (4096, 1024, 160), (4001, 1001, 224),
           (3001, 2000, 160), (2000, 3001, 96)]
 
@@ -174,8 +174,8 @@ def test_gemm_parts_of_tiles(fmt, M, N, K):
     assert m3.device_wait_timeouts() == 0
 
 
-# many tiles and a K long enough for pairs of CTAs (with both types of A, or 8-bit A alone):
-# whole tiles, parts, columns and rows that end inside them
+# many tiles and a long K: whole tiles and parts of 64 and 128 columns, columns and rows that end
+# inside them
 @pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
 @pytest.mark.parametrize("M,N,K", [(16384, 1024, 2048), (20011, 1024, 2048), (13000, 1537, 1500),
                                    (4090, 4000, 4096), (4001, 4099, 4200), (19000, 1000, 2304)])
