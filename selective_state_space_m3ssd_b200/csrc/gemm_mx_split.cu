@@ -352,14 +352,14 @@ namespace gemm_mx {
 // tokens, which needs no detour through shared memory; a second CTA an SM 12.  (Clusters of
 // eight leave SMs of a GPC over and double up from about two thirds of the SMs on.)  On one
 // B200, us with 4-bit / 8-bit A, K over 1, 2, 4 and 8 CTAs:
-//   16 x 6464 x 1024     4.1  5.1  6.1        5.6  5.7  6.3  9.8
-//   16 x 1024 x 8192     9.8  8.2  6.4  5.7  16.4 11.3  8.2  6.6
-//   16 x 8192 x 8192    11.6 10.9 10.4 13.5  17.5 13.0 11.5 15.3
-// and with gemm_mx.cu's tile, over 2, 4 and 8:
-//   128 x 6464 x 1024    4.7  6.3  9.1        5.9  7.2  9.3 16.7
-//   128 x 1024 x 8192   10.3  9.3  8.2  7.3  16.9 12.9  9.8  8.2
-//   128 x 4096 x 4096    7.7  7.7  8.2 11.3  10.8  9.8  8.8 11.8
-//   1024 x 1024 x 8192  10.8 10.3 12.3 21.1  17.5 13.9 14.6 23.7
+//   16 x 6464 x 1024     3.8  4.4  5.6        5.0  5.3  5.7  9.0
+//   16 x 1024 x 8192     9.5  7.7  6.0  5.2  16.0 10.9  7.7  6.1
+//   16 x 8192 x 8192    11.5 11.1 10.6 13.6  17.6 13.1 11.5 15.4
+// (weights of more than L2 in turn), and with gemm_mx.cu's tile, over 2, 4 and 8:
+//   128 x 6464 x 1024    4.6  6.0  8.9        5.5  6.8  8.9 16.4
+//   128 x 1024 x 8192   10.1  9.1  7.8  7.0  16.9 12.8  9.5  8.0
+//   128 x 4096 x 4096    7.0  7.5  7.3 11.0  10.4  9.5  8.3 11.1
+//   1024 x 1024 x 8192  10.6 10.8 12.0 20.8  17.8 16.5 15.1 23.7
 int split_of(int64_t M, int64_t N, int64_t K, int a_fmt, int64_t sms) {
   const int64_t tiles = ((N + 127) / 128) * ((M + 127) / 128);
   const int64_t stage = a_fmt == mx::kFp4 ? 256 : 128, nk = (K + stage - 1) / stage;

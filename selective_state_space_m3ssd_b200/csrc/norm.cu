@@ -12,8 +12,9 @@
 // in one access of 16 or 32 bytes (four lanes share a block of 32 of a microscaled output).
 // Rows of a width that is no multiple of eight start inside an access: they are taken in the
 // accesses they lie in (kShift), a microscaled output's values moved to its blocks by shuffles.
-// 16000 x 1049 (bf16, fp32 residual) takes 43 us forward, 53 to 8 bits and 40 backward, 94, 71
-// and 65 element by element, which tensors that are not aligned themselves still are.  The
+// 16000 x 1049 (bf16, fp32 residual) takes 44 us forward, 53 to 8 bits and 40 backward (68 with
+// dres), 94, 71 and 65 element by element, which tensors that are not aligned themselves still
+// are.  The
 // grid is persistent: a CTA walks rows, fetching the next while it finishes one, with its columns
 // of w, and in the backward its columns of the dw sum, in registers.  The dw sums leave as
 // one partial row a walker, which a second kernel adds in a fixed order.

@@ -15,10 +15,11 @@
 // conversions two values at a time, multiply-adds two fp32 values at a time (f32x2), two
 // 16-byte shared-memory loads for a row's four factors, a sum of y whose exchanges are a
 // thirtieth of the work.  At b256 H32 N128 P64 on one B200: 35 us against 24 for the bytes at
-// the copy rate (the fp32 step takes 87); HBM runs at 47 % and the schedulers issue in 52 % of
-// the cycles (a two-wide operation takes two of them), four warps a scheduler.  Without the
-// decoding, the encoding or the maxima it took 1 to 2 us less, without its stores 4, with
-// 7 or 9 CTAs an SM 39 and 38 us: no one part bounds it.
+// the copy rate (4.5 TB/s, 0.68 of it; the fp32 step takes 87).  The schedulers issue in 56 % of
+// the cycles (a two-wide operation takes two of them), 3.6 warps a scheduler: what is left is
+// latency, part of it a round's own order (angles and rotations, a barrier, then the rows).
+// Without the decoding, the encoding or the maxima it took 1 to 2 us less, without its stores 4,
+// with 7 or 9 CTAs an SM 39 and 38 us.
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -458,9 +459,10 @@ __global__ void __launch_bounds__(kWalkThreads, kWalkCtas) step_q8_walk(StepQ8Ar
 
 // Every other shape: one CTA a (b, h); `lanes` lanes (a power of two) share a row, eight columns
 // each.  VEC: rows of a multiple of eight columns, aligned: a lane's codes are one access.
-// b256 H32 N64 P64 takes 40 us (13 for the bytes: a CTA's life is mostly its chain of angles,
-// rotations, rows and sum), b64 H32 N256 P64 30, b128 H32 N128 P75 bf16 93; with a warp a row, a
-// column of each 32 a lane, they took 136, 123 and 127.  Measured and not kept: odd rows in the
+// b256 H32 N64 P64 takes 46 us (13 for the bytes: a CTA's life is mostly its chain of angles,
+// rotations, rows and sum, with nothing in flight for the next one), b64 H32 N256 P64 32, b128
+// H32 N128 P75 bf16 110 (its codes go byte by byte); with a warp a row, a column of each 32 a
+// lane, 3.4, 4.1 and 1.4 times as long.  Measured and not kept: odd rows in the
 // accesses they lie in (no faster, and the sums it needs cost the others 10 %), registers for
 // 8 or 10 CTAs an SM (spills; 10 to 40 % slower).
 constexpr int kGenThreads = 128, kGenWarps = kGenThreads / 32, kGenUnroll = 4;
