@@ -560,9 +560,9 @@ m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float*
  * the last call (a forward's CTA then stops and leaves its outputs unwritten, a step's those
  * of the (b, h) it had not come to, so that with a cache_out of its own the step can be taken
  * again while a cache written in place is undefined; the backward's and the GEMMs' CTAs skip
- * their remaining waits and leave their outputs undefined); the count is then reset.  This call synchronises the current device
- * and must not be captured in a CUDA graph.  Returns M3SSD_ERR_INVALID_ARG for
- * a NULL pointer and M3SSD_ERR_CUDA if the device cannot be read. */
+ * their remaining waits and leave their outputs undefined); the count is then reset.  This
+ * call synchronises the current device and must not be captured in a CUDA graph.  Returns
+ * M3SSD_ERR_INVALID_ARG for a NULL pointer and M3SSD_ERR_CUDA if the device cannot be read. */
 m3ssd_status m3ssd_device_wait_timeouts(uint32_t* count);
 
 /*

@@ -24,15 +24,15 @@
 // stage was what bounded the products (8192^3 in 4 bits 241 us against 191, 32768 x 6464 x
 // 1024 131 against 120).
 //
-// What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for
-// writes at HBM's 3.9 TB/s of them, 120 taken at 1965 MHz; called for seconds, 1000 W hold the
-// SM clock near 1510 MHz and it takes 144, so what the SMs do is close behind); with a long K
-// what the copies bring in against what the products read: the ring takes in 50 to 55 bytes a
-// cycle and SM, 75 to 96 would keep the products at their peak.  Measured and not kept: L2 prefetches of the stages behind the
-// ring (3 to 8 % slower); pairs of CTAs (256 x 256, W brought in once for both; no second
-// accumulator of that width fits beside the scales, one of 192 columns would): with pairs 180 and 338 us at 8192^3 against 195 and 353,
-// 36.0 and 55.2 at 32768 x 1024 x 2048 against 34.4 and 56.4, 137 and 187 at 32768 x 6464 x 1024
-// against 119 and 191.
+// What bounds it on one B200: writing D where K is short (32768 x 6464 x 1024: 108 us for writes
+// at HBM's 3.9 TB/s of them, 120 taken at 1965 MHz; called for seconds, 1000 W hold the SM clock
+// near 1510 MHz and it takes 144, so what the SMs do is close behind); with a long K what the
+// copies bring in against what the products read: the ring takes in 50 to 55 bytes a cycle and SM,
+// 75 to 96 would keep the products at their peak. Measured and not kept: L2 prefetches of the
+// stages behind the ring (3 to 8 % slower); pairs of CTAs (256 x 256, W brought in once for both;
+// no second accumulator of that width fits beside the scales, one of 192 columns would): with
+// pairs 180 and 338 us at 8192^3 against 195 and 353, 36.0 and 55.2 at 32768 x 1024 x 2048 against
+// 34.4 and 56.4, 137 and 187 at 32768 x 6464 x 1024 against 119 and 191.
 //
 // Waits are bounded as in gemm.cu: one that runs out sets a shared flag that ends the
 // others, and the launch is counted in a device word the host query reads.

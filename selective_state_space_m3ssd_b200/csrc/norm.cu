@@ -7,17 +7,16 @@
 // computed.  With g = w dy and rhat = r rstd (means over the row's d values):
 //     dr = rstd (g - rhat mean(g rhat)) + dres,   dw = sum over rows of dy rhat.
 //
-// Streams: every tensor is read once and written once, so HBM bounds them.  A thread keeps
-// eight values (times NV) of a row in registers between the row's sum and its outputs, read
-// in one access of 16 or 32 bytes (four lanes share a block of 32 of a microscaled output).
-// Rows of a width that is no multiple of eight start inside an access: they are taken in the
-// accesses they lie in (kShift), a microscaled output's values moved to its blocks by shuffles.
-// 16000 x 1049 (bf16, fp32 residual) takes 44 us forward, 53 to 8 bits and 40 backward (68 with
-// dres), 94, 71 and 65 element by element, which tensors that are not aligned themselves still
-// are.  The
-// grid is persistent: a CTA walks rows, fetching the next while it finishes one, with its columns
-// of w, and in the backward its columns of the dw sum, in registers.  The dw sums leave as
-// one partial row a walker, which a second kernel adds in a fixed order.
+// Streams: every tensor is read once and written once, so HBM bounds them.  A thread keeps eight
+// values (times NV) of a row in registers between the row's sum and its outputs, read in one
+// access of 16 or 32 bytes (four lanes share a block of 32 of a microscaled output). Rows of a
+// width that is no multiple of eight start inside an access: they are taken in the accesses they
+// lie in (kShift), a microscaled output's values moved to its blocks by shuffles. 16000 x 1049
+// (bf16, fp32 residual) takes 44 us forward, 53 to 8 bits and 40 backward (68 with dres), 94, 71
+// and 65 element by element, which tensors that are not aligned themselves still are.  The grid
+// is persistent: a CTA walks rows, fetching the next while it finishes one, with its columns of
+// w, and in the backward its columns of the dw sum, in registers.  The dw sums leave as one
+// partial row a walker, which a second kernel adds in a fixed order.
 #include <cuda_runtime.h>
 
 #include "internal.h"
