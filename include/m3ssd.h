@@ -555,6 +555,92 @@ m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float*
                            const m3ssd_cache_q8* cache, const m3ssd_cache_q8* cache_out, void* y_t,
                            void* stream);
 
+/*
+ * The gated linear recurrence, one state a channel ("TorchMamba" README, "Functional cores",
+ * has the matrix-state recurrences; a layer that mixes tokens channel by channel runs this one
+ * beside them).  Over (b, L, width), per channel, with k = c softplus(rate):
+ *     rho = sigma(r + bias_r),  iota = sigma(i + bias_i),  a = exp(-k rho),
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) iota_t x_t,   y_t = h_t,
+ * computed in fp32 (1 - a_t^2 to fp32's relative precision however close a_t is to one, down
+ * to 1e-37; a gate below 2^-63 counts as that, an a_t below 2^-126 as zero), h held in fp32, y
+ * rounded once to x_dtype.
+ */
+typedef struct {
+  int64_t batch;      /* b >= 0 */
+  int64_t seqlen;     /* L >= 0 (ignored by m3ssd_glr_step) */
+  int64_t width;      /* channels, >= 1 */
+  int64_t ldx;        /* elements from a token's x to the next one's, >= width: x, r and i may */
+  int64_t ldr;        /*   be column ranges of one projection's rows; token t of sequence b is */
+  int64_t ldi;        /*   row b L + t (row b of the step) */
+  int32_t x_dtype;    /* m3ssd_dtype of x, r, i, y and dy */
+  float c;            /* > 0, finite */
+  uint32_t reserved;  /* must be 0 */
+} m3ssd_glr_dims;
+
+/*
+ * Forward.  rate, bias_r, bias_i (width) and h0, hT (b, width) are fp32; bias_r, bias_i and h0
+ * may be NULL (zero), hT may be NULL or h0.  y: dense (b, L, width).
+ *   reset (b, L) uint8, may be NULL: where it is not zero a sequence starts anew, a_t = 0
+ *     (whatever h_{t-1} was, NaN and infinity included), as between packed documents.
+ *   lengths (b) int32, may be NULL (L): the tokens of each sequence, taken between 0 and L.
+ *     Later rows of x, r, i and reset are not read, those of y are zero, hT is the state after
+ *     the last token (h0 where there is none).
+ * b times half the width, and every stride, up to 2^31 - 1 (else M3SSD_ERR_UNSUPPORTED).  y
+ * overlaps no input.  No allocation, no synchronisation; capture-safe.
+ */
+m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
+                           const float* rate, const float* bias_r, const float* bias_i,
+                           const float* h0, const uint8_t* reset, const int32_t* lengths, void* y,
+                           float* hT, void* stream);
+
+/* Gradients: dx, dr, di (b, L, width) in `dtype` (fp32, or bf16 where x_dtype is: each value
+ * rounded once), their rows `ld` elements apart, so that they may be column ranges of one
+ * projection's gradient; drate, dbias_r, dbias_i (width) and dh0 (b, width) fp32.  dbias_r,
+ * dbias_i and dh0 may be NULL. */
+typedef struct {
+  int64_t ld;         /* >= width */
+  int32_t dtype;      /* m3ssd_dtype */
+  uint32_t reserved;  /* must be 0 */
+  void* dx;
+  void* dr;
+  void* di;
+  float* drate;
+  float* dbias_r;
+  float* dbias_i;
+  float* dh0;
+} m3ssd_glr_grads;
+
+/* Bytes of device workspace m3ssd_glr_bwd needs on the current device; 0 for invalid dims. */
+size_t m3ssd_glr_bwd_workspace_size(const m3ssd_glr_dims* dims);
+
+/*
+ * Backward of m3ssd_glr_fwd: its inputs, its output y, dy (dense, x_dtype) and dhT (b, width,
+ * fp32, NULL = 0).  With g_t = dy_t + a_{t+1} g_{t+1} (dhT added at the last token), s =
+ * sqrt(1 - a^2):
+ *     dx = g s iota,  di = dx x (1 - iota),
+ *     E = g a (h_{t-1} - a iota x / s) log a,  dr = E (1 - rho),
+ *     drate = sum of E sigma(rate) / softplus(rate),  dbias_r, dbias_i = sums of dr and di,
+ *     dh0 = a_0 g_0
+ * (E = dr = 0 at a reset).  h_{t-1} is read as the stored y_{t-1}: in bf16 that is h rounded by
+ * 2^-9 of its value, a fifth of the forward's work saved (no second walk forward).  Rows at
+ * and past lengths[b] are zero.  Sums run in fp32 in a fixed order: the same call gives
+ * the same bits.  dh0 may be dhT; the other outputs overlap no input.  workspace: 256-byte
+ * aligned, not read afterwards.
+ */
+m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
+                           const float* rate, const float* bias_r, const float* bias_i,
+                           const float* h0, const uint8_t* reset, const int32_t* lengths,
+                           const void* y, const void* dy, const float* dhT,
+                           const m3ssd_glr_grads* grads, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* One token of each sequence: x_t, r_t, i_t (b, width, rows ldx, ldr, ldi apart), the state h
+ * (b, width) fp32 to h_out (NULL: in place; else h or no overlap), y_t dense. */
+m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const void* r_t,
+                            const void* i_t, const float* rate, const float* bias_r,
+                            const float* bias_i, const float* h, float* h_out, void* y_t,
+                            void* stream);
+
 /* Number of bounded device-side waits of the chunked forwards (SISO and
  * MIMO), the tensor-core backward, the GEMMs and the 8-bit step that ran out since
  * the last call (a forward's CTA then stops and leaves its outputs unwritten, a step's those

@@ -1,0 +1,76 @@
+"""fp64 oracle of the operators that a layer has around the scan: plain numpy, written
+from their definitions (include/m3ssd.h), sharing no code with the library.
+
+The gated linear recurrence walks token by token, forward and in reverse.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def sigmoid(v):
+    return np.where(v >= 0, 1 / (1 + np.exp(-np.abs(v))), np.exp(-np.abs(v)) / (1 + np.exp(-np.abs(v))))
+
+
+def softplus(v):
+    return np.maximum(v, 0) + np.log1p(np.exp(-np.abs(v)))
+
+
+def glr_gates(r, i, rate, bias_r=None, bias_i=None, c=8.0, reset=None):
+    """rho, iota, log a, a, s of every token; a = 0 and s = 1 at a reset."""
+    rho = sigmoid(r + (0 if bias_r is None else bias_r))
+    iota = sigmoid(i + (0 if bias_i is None else bias_i))
+    la = -c * softplus(rate) * rho
+    a, s = np.exp(la), np.sqrt(-np.expm1(2 * la))
+    if reset is not None:
+        cut = np.asarray(reset, bool)[..., None]
+        a, s = np.where(cut, 0.0, a), np.where(cut, 1.0, s)
+    return rho, iota, la, a, s
+
+
+def _lens(lengths, b, L):
+    return np.full(b, L) if lengths is None else np.clip(np.asarray(lengths), 0, L)
+
+
+def glr_fwd(x, r, i, rate, bias_r=None, bias_i=None, c=8.0, h0=None, reset=None, lengths=None):
+    """(y, hT) of x, r, i (b, L, D)."""
+    b, L, D = x.shape
+    _, iota, _, a, s = glr_gates(r, i, rate, bias_r, bias_i, c, reset)
+    h = np.zeros((b, D)) if h0 is None else np.array(h0, np.float64)
+    n, y = _lens(lengths, b, L), np.zeros((b, L, D))
+    for k in range(b):
+        for t in range(n[k]):
+            u = s[k, t] * iota[k, t] * x[k, t]
+            h[k] = u if reset is not None and reset[k, t] else a[k, t] * h[k] + u
+            y[k, t] = h[k]
+    return y, h
+
+
+def glr_bwd(x, r, i, rate, y, dy, bias_r=None, bias_i=None, c=8.0, h0=None, reset=None,
+            lengths=None, dhT=None):
+    """Gradients by the header's formulas, with h_{t-1} = y_{t-1}; also g (b, L, D)."""
+    b, L, D = x.shape
+    rho, iota, la, a, s = glr_gates(r, i, rate, bias_r, bias_i, c, reset)
+    back = np.zeros((b, D)) if dhT is None else np.array(dhT, np.float64)
+    n = _lens(lengths, b, L)
+    o = {k: np.zeros((b, L, D)) for k in ("dx", "dr", "di", "E", "g")}
+    for k in range(b):
+        for t in range(n[k] - 1, -1, -1):
+            prev = y[k, t - 1] if t > 0 else (0.0 if h0 is None else h0[k])
+            g = dy[k, t] + back[k]
+            cut = reset is not None and reset[k, t]
+            o["g"][k, t] = g
+            o["dx"][k, t] = g * s[k, t] * iota[k, t]
+            o["di"][k, t] = g * s[k, t] * x[k, t] * iota[k, t] * (1 - iota[k, t])
+            if not cut:
+                with np.errstate(divide="ignore", invalid="ignore"):
+                    slope = np.where(s[k, t] > 0, la[k, t] / s[k, t], 0.0)
+                E = g * (a[k, t] * la[k, t] * prev - a[k, t] ** 2 * slope * iota[k, t] * x[k, t])
+                o["E"][k, t] = E
+                o["dr"][k, t] = E * (1 - rho[k, t])
+            back[k] = 0.0 if cut else a[k, t] * g
+    # sigma / softplus is 1 - exp(rate) / 2 + ... far down
+    slope = np.where(rate < -40, 1.0, sigmoid(rate) / np.maximum(softplus(rate), 1e-300))
+    o["drate"] = o["E"].sum((0, 1)) * slope
+    o["dbias_r"], o["dbias_i"], o["dh0"] = o["dr"].sum((0, 1)), o["di"].sum((0, 1)), back
+    return o

@@ -84,6 +84,19 @@ class CacheQ8(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("angle", "ssm", "scale", "x_prev", "b_prev")]
 
 
+class GlrDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "width", "ldx", "ldr", "ldi")] + \
+        [("x_dtype", ctypes.c_int32), ("c", ctypes.c_float), ("reserved", ctypes.c_uint32)]
+
+
+GLR_GRAD_NAMES = ("dx", "dr", "di", "drate", "dbias_r", "dbias_i", "dh0")
+
+
+class GlrGrads(ctypes.Structure):
+    _fields_ = [("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_uint32)] + \
+        [(n, ctypes.c_void_p) for n in GLR_GRAD_NAMES]
+
+
 class BlockDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("batch", "seqlen", "d_model", "nheads", "headdim", "dstate", "ngroups")]
@@ -191,6 +204,15 @@ def load(path: str | None = None):
         lib.m3ssd_step_q8.argtypes = [ctypes.POINTER(Dims)] + [vp] * 8 + \
             [ctypes.POINTER(CacheQ8), ctypes.POINTER(CacheQ8), vp, vp]
         lib.m3ssd_step_q8.restype = ctypes.c_int
+        gdp = ctypes.POINTER(GlrDims)
+        lib.m3ssd_glr_fwd.argtypes = [gdp] + [vp] * 12
+        lib.m3ssd_glr_fwd.restype = ctypes.c_int
+        lib.m3ssd_glr_bwd_workspace_size.argtypes = [gdp]
+        lib.m3ssd_glr_bwd_workspace_size.restype = sz
+        lib.m3ssd_glr_bwd.argtypes = [gdp] + [vp] * 12 + [ctypes.POINTER(GlrGrads), vp, sz, vp]
+        lib.m3ssd_glr_bwd.restype = ctypes.c_int
+        lib.m3ssd_glr_step.argtypes = [gdp] + [vp] * 10
+        lib.m3ssd_glr_step.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -1019,6 +1041,152 @@ def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=Non
             _addr(gamma_t), _addr(B_t), _addr(C_t), _addr(theta_t), _addr(D), ctypes.byref(ci),
             None if co is None else ctypes.byref(co), _addr(y_t))
     return y_t
+
+
+# ---- the gated linear recurrence ---------------------------------------------------------
+
+def _tokens_stride(t, name, dtype, lead, width, index):
+    """A tensor (*lead, width) on CUDA device ``index`` whose tokens are rows of unit column
+    stride a fixed distance apart; returns that distance."""
+    if t.dtype != dtype or t.shape != (*lead, width):
+        _need_shape(t, name, dtype, (*lead, width))
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected a CUDA tensor on cuda:{index}")
+    if t.is_contiguous():
+        return width
+    stride, rows = t.stride(), 1
+    if width > 1 and stride[-1] != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = None  # from the innermost axis longer than one
+    for n, st in zip(reversed(lead), reversed(stride[:-1])):
+        if n > 1:
+            if ld is None:
+                ld = st // rows
+            if st != ld * rows or ld < width:
+                raise ValueError(f"{name}'s tokens must be a fixed distance apart")
+        rows *= n
+    return ld or width
+
+
+def _bytes_of(t):
+    """A mask as the bytes it is held in."""
+    import torch
+    return t.view(torch.uint8) if t is not None and t.dtype == torch.bool else t
+
+
+def _glr_dims(x, r, i, rate, bias_r, bias_i, c):
+    """Checks what the recurrence's calls share; its dims (seqlen 0 for a step)."""
+    import torch
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    f32, dev, index = torch.float32, x.device, x.get_device()
+    lead, D = x.shape[:-1], x.shape[-1]
+    xd = _xdtype(x)
+    ld = [_tokens_stride(t, n, x.dtype, lead, D, index) for t, n in ((x, "x"), (r, "r"), (i, "i"))]
+    if rate is None:
+        raise ValueError("rate is required")
+    _need_all(dev, (rate, "rate", f32, (D,)), (bias_r, "bias_r", f32, (D,)),
+              (bias_i, "bias_i", f32, (D,)))
+    return GlrDims(lead[0], lead[1] if len(lead) == 2 else 0, D, *ld, xd, float(c), 0)
+
+
+def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None, reset=None,
+            lengths=None, y=None, hT=None, want_hT: bool = True):
+    """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(i_t + bias_i) x_t
+    with a_t = exp(-c softplus(rate) sigma(r_t + bias_r)), through ``m3ssd_glr_fwd``.
+
+    x, r, i (b, L, D) bf16 or fp32, each a tensor of its own or a column range of a projection's
+    rows; rate, bias_r, bias_i (D) and h0 (b, D) fp32.  ``reset`` (b, L), bool or uint8: the
+    tokens at which a sequence starts anew.  ``lengths`` (b) int32: the tokens of each sequence
+    (y is zero behind them).  Returns ``(y, hT)``: y (b, L, D) in x's type, hT (b, D) fp32 the
+    state after the last token (may be given as ``h0``'s tensor), None unless ``want_hT``."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"x must have shape (b, L, D), got {tuple(x.shape)}")
+    dims = _glr_dims(x, r, i, rate, bias_r, bias_i, c)
+    b, L, D = x.shape
+    dev, f32 = x.device, torch.float32
+    reset = _bytes_of(reset)
+    if y is None:
+        y = torch.empty(b, L, D, dtype=x.dtype, device=dev)
+    if hT is None and want_hT:
+        hT = torch.empty(b, D, dtype=f32, device=dev)
+    _need_all(dev, (h0, "h0", f32, (b, D)), (reset, "reset", torch.uint8, (b, L)),
+              (lengths, "lengths", torch.int32, (b,)), (y, "y", x.dtype, (b, L, D)),
+              (hT, "hT", f32, (b, D)))
+    _launch("m3ssd_glr_fwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
+            _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y), _addr(hT))
+    return y, hT
+
+
+def glr_bwd_workspace_size(dims: GlrDims) -> int:
+    """Bytes on the current device."""
+    return int(load().m3ssd_glr_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def glr_bwd(x, r, i, rate, y, dy, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None,
+            reset=None, lengths=None, dhT=None, grad_dtype=None, grads=None, workspace=None):
+    """Backward of :func:`glr_fwd` through ``m3ssd_glr_bwd``: its inputs, its output ``y``, the
+    gradients ``dy`` (x's type) and ``dhT`` (fp32 or None).  Returns a dict of the gradients named
+    in ``GLR_GRAD_NAMES``: dx, dr, di in ``grad_dtype`` (fp32 unless given as x's type), the
+    others fp32.  ``grads`` may supply tensors, dx, dr and di as column ranges of one."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"x must have shape (b, L, D), got {tuple(x.shape)}")
+    dims = _glr_dims(x, r, i, rate, bias_r, bias_i, c)
+    b, L, D = x.shape
+    dev, f32 = x.device, torch.float32
+    grad_dtype = grad_dtype or f32
+    reset = _bytes_of(reset)
+    _need_all(dev, (h0, "h0", f32, (b, D)), (reset, "reset", torch.uint8, (b, L)),
+              (lengths, "lengths", torch.int32, (b,)), (dhT, "dhT", f32, (b, D)))
+    if y is None or dy is None:
+        raise ValueError("y and dy are required")
+    _need_all(dev, (y, "y", x.dtype, (b, L, D)), (dy, "dy", x.dtype, (b, L, D)))
+    grads = dict(grads or {})
+    for k in ("dx", "dr", "di"):
+        if grads.get(k) is None:
+            grads[k] = torch.empty(b, L, D, dtype=grad_dtype, device=dev)
+    for k, shape in (("drate", (D,)), ("dbias_r", (D,)), ("dbias_i", (D,)), ("dh0", (b, D))):
+        if grads.get(k) is None:
+            grads[k] = torch.empty(shape, dtype=f32, device=dev)
+        else:
+            _need(grads[k], k, f32, shape, dev)
+    lds = {_tokens_stride(grads[k], k, grad_dtype, (b, L), D, dev.index) for k in ("dx", "dr", "di")}
+    if len(lds) != 1 and b * L > 1:
+        raise ValueError("dx, dr and di must have their rows the same distance apart")
+    g = GlrGrads(max(lds), _xdtype(grads["dx"]), 0, *(grads[k].data_ptr() for k in GLR_GRAD_NAMES))
+    if torch._C._cuda_getDevice() == dev.index:
+        need = glr_bwd_workspace_size(dims)
+    else:
+        with torch.cuda.device(dev):
+            need = glr_bwd_workspace_size(dims)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
+    _launch("m3ssd_glr_bwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
+            _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y),
+            _addr(dy), _addr(dhT), ctypes.byref(g), ws, ws_bytes)
+    return {k: grads[k] for k in GLR_GRAD_NAMES}
+
+
+def glr_step(h, x_t, r_t, i_t, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h_out=None,
+             y_t=None):
+    """One token of :func:`glr_fwd` for each sequence through ``m3ssd_glr_step``: x_t, r_t, i_t
+    (b, D), the state ``h`` (b, D) fp32, written to ``h_out`` or in place.  Returns ``(y_t, h)``,
+    h being the tensor that holds the new state."""
+    import torch
+    if x_t.dim() != 2:
+        raise ValueError(f"x_t must have shape (b, D), got {tuple(x_t.shape)}")
+    dims = _glr_dims(x_t, r_t, i_t, rate, bias_r, bias_i, c)
+    b, D = x_t.shape
+    dev, f32 = x_t.device, torch.float32
+    if y_t is None:
+        y_t = torch.empty(b, D, dtype=x_t.dtype, device=dev)
+    h_out = h if h_out is None else h_out
+    _need_all(dev, (h, "h", f32, (b, D)), (h_out, "h_out", f32, (b, D)),
+              (y_t, "y_t", x_t.dtype, (b, D)))
+    _launch("m3ssd_glr_step", dev, ctypes.byref(dims), _addr(x_t), _addr(r_t), _addr(i_t),
+            _addr(rate), _addr(bias_r), _addr(bias_i), _addr(h), _addr(h_out), _addr(y_t))
+    return y_t, h_out
 
 
 class PreparedFwd:

@@ -293,6 +293,62 @@ cudaError_t launch_quant_state(int64_t rows, int64_t P, const float* h, void* co
                                cudaStream_t s);
 cudaError_t launch_dequant_state(int64_t rows, int64_t P, const void* codes, const float* scale,
                                  float* h, cudaStream_t s);
+// The gated linear recurrence (csrc/glr.cu) over b sequences of L tokens and D channels; x, r, i
+// with row strides in elements, y, hT and the state dense.
+struct GlrArgs {
+  int64_t b, L, D;
+  int64_t ldx, ldr, ldi;
+  bool bf16;  // type of x, r, i, y (and dy)
+  float c;
+  const void* x;
+  const void* r;
+  const void* i;
+  const float* rate;
+  const float* bias_r;      // nullable
+  const float* bias_i;      // nullable
+  const float* h0;          // nullable
+  const uint8_t* reset;     // nullable, (b, L)
+  const int32_t* lengths;   // nullable, (b)
+  void* y;                  // the backward reads it
+  float* hT;                // nullable
+};
+// Its backward; `part` holds glr_bwd_workspace_bytes.
+struct GlrBwdArgs {
+  GlrArgs f;
+  const void* dy;
+  const float* dhT;  // nullable
+  bool grad_bf16;
+  int64_t ldg;
+  void* dx;
+  void* dr;
+  void* di;
+  float* drate;
+  float* dbias_r;  // nullable
+  float* dbias_i;  // nullable
+  float* dh0;      // nullable
+  float* part;
+};
+// One step of b sequences; h_out may be h.
+struct GlrStepArgs {
+  int64_t b, D;
+  int64_t ldx, ldr, ldi;
+  bool bf16;
+  float c;
+  const void* x;
+  const void* r;
+  const void* i;
+  const float* rate;
+  const float* bias_r;
+  const float* bias_i;
+  const float* h;
+  float* h_out;
+  void* y;
+};
+cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s);
+size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D);
+cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s);
+cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s);
+
 // Decode step (two launches: the state/outputs, then b_prev <- B_t).
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 

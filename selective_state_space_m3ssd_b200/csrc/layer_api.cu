@@ -1,0 +1,152 @@
+// C-ABI entry points of the operators that a layer has around the scan: the gated linear
+// recurrence.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/m3ssd.h"
+#include "internal.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+m3ssd_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return M3SSD_OK;
+  (void)cudaGetLastError();
+  return M3SSD_ERR_CUDA;
+}
+
+bool dtype_ok(int32_t t) { return t == M3SSD_F32 || t == M3SSD_BF16; }
+uintptr_t dtype_size(int32_t t) { return t == M3SSD_BF16 ? 2 : 4; }
+
+bool all_aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
+
+m3ssd_status check_glr(const m3ssd_glr_dims* d, int64_t seqlen) {
+  if (!d || d->reserved != 0) return M3SSD_ERR_INVALID_ARG;
+  if (d->batch < 0 || seqlen < 0 || d->width < 1) return M3SSD_ERR_INVALID_ARG;
+  if (!dtype_ok(d->x_dtype)) return M3SSD_ERR_INVALID_ARG;
+  if (d->ldx < d->width || d->ldr < d->width || d->ldi < d->width) return M3SSD_ERR_INVALID_ARG;
+  if (!(d->c > 0.f) || !std::isfinite(d->c)) return M3SSD_ERR_INVALID_ARG;
+  // sequences x groups of channels are counted in 31 bits, strides of a tile in 32
+  const int64_t most = INT32_MAX;
+  if (d->width > most || seqlen > most || d->batch > most || d->ldx > most || d->ldr > most ||
+      d->ldi > most || d->batch * ((d->width + 1) / 2) > most)
+    return M3SSD_ERR_UNSUPPORTED;
+  return M3SSD_OK;
+}
+
+// The inputs that the forward and the backward share.
+bool glr_inputs_ok(const m3ssd_glr_dims* d, const void* x, const void* r, const void* i,
+                   const float* rate, const float* bias_r, const float* bias_i, const float* h0,
+                   const int32_t* lengths) {
+  const uintptr_t esz = dtype_size(d->x_dtype);
+  if (!rate || (d->batch > 0 && d->seqlen > 0 && (!x || !r || !i))) return false;
+  return aligned(x, esz) && aligned(r, esz) && aligned(i, esz) &&
+         all_aligned4({rate, bias_r, bias_i, h0, lengths});
+}
+
+m3ssd::GlrArgs glr_args(const m3ssd_glr_dims* d, const void* x, const void* r, const void* i,
+                        const float* rate, const float* bias_r, const float* bias_i,
+                        const float* h0, const uint8_t* reset, const int32_t* lengths) {
+  m3ssd::GlrArgs a{};
+  a.b = d->batch; a.L = d->seqlen; a.D = d->width;
+  a.ldx = d->ldx; a.ldr = d->ldr; a.ldi = d->ldi;
+  a.bf16 = d->x_dtype == M3SSD_BF16; a.c = d->c;
+  a.x = x; a.r = r; a.i = i; a.rate = rate; a.bias_r = bias_r; a.bias_i = bias_i;
+  a.h0 = h0; a.reset = reset; a.lengths = lengths;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
+                           const float* rate, const float* bias_r, const float* bias_i,
+                           const float* h0, const uint8_t* reset, const int32_t* lengths, void* y,
+                           float* hT, void* stream) {
+  const m3ssd_status st = check_glr(dims, dims ? dims->seqlen : 0);
+  if (st != M3SSD_OK) return st;
+  if (!glr_inputs_ok(dims, x, r, i, rate, bias_r, bias_i, h0, lengths)) return M3SSD_ERR_INVALID_ARG;
+  if ((dims->batch > 0 && dims->seqlen > 0 && !y) || !aligned(y, dtype_size(dims->x_dtype)) ||
+      !aligned(hT, 4))
+    return M3SSD_ERR_INVALID_ARG;
+  if (dims->batch == 0) return M3SSD_OK;
+  m3ssd::GlrArgs a = glr_args(dims, x, r, i, rate, bias_r, bias_i, h0, reset, lengths);
+  a.y = y;
+  a.hT = hT;
+  return from_cuda(m3ssd::launch_glr_fwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t m3ssd_glr_bwd_workspace_size(const m3ssd_glr_dims* dims) {
+  if (check_glr(dims, dims ? dims->seqlen : 0) != M3SSD_OK) return 0;
+  return m3ssd::glr_bwd_workspace_bytes(dims->batch, dims->seqlen, dims->width);
+}
+
+m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
+                           const float* rate, const float* bias_r, const float* bias_i,
+                           const float* h0, const uint8_t* reset, const int32_t* lengths,
+                           const void* y, const void* dy, const float* dhT,
+                           const m3ssd_glr_grads* grads, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const m3ssd_status st = check_glr(dims, dims ? dims->seqlen : 0);
+  if (st != M3SSD_OK) return st;
+  if (!grads || grads->reserved != 0 || !dtype_ok(grads->dtype)) return M3SSD_ERR_INVALID_ARG;
+  if (grads->dtype == M3SSD_BF16 && dims->x_dtype != M3SSD_BF16) return M3SSD_ERR_UNSUPPORTED;
+  if (grads->ld < dims->width) return M3SSD_ERR_INVALID_ARG;
+  if (grads->ld > INT32_MAX) return M3SSD_ERR_UNSUPPORTED;
+  if (!glr_inputs_ok(dims, x, r, i, rate, bias_r, bias_i, h0, lengths)) return M3SSD_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype_size(dims->x_dtype), gsz = dtype_size(grads->dtype);
+  if (dims->batch > 0 && dims->seqlen > 0 &&
+      (!y || !dy || !grads->dx || !grads->dr || !grads->di))
+    return M3SSD_ERR_INVALID_ARG;
+  if (!grads->drate || !aligned(y, esz) || !aligned(dy, esz) || !aligned(grads->dx, gsz) ||
+      !aligned(grads->dr, gsz) || !aligned(grads->di, gsz) ||
+      !all_aligned4({dhT, grads->drate, grads->dbias_r, grads->dbias_i, grads->dh0}))
+    return M3SSD_ERR_INVALID_ARG;
+  const size_t need = m3ssd::glr_bwd_workspace_bytes(dims->batch, dims->seqlen, dims->width);
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256))))
+    return M3SSD_ERR_WORKSPACE;
+  m3ssd::GlrBwdArgs a{};
+  a.f = glr_args(dims, x, r, i, rate, bias_r, bias_i, h0, reset, lengths);
+  a.f.y = const_cast<void*>(y);
+  a.dy = dy; a.dhT = dhT;
+  a.grad_bf16 = grads->dtype == M3SSD_BF16;
+  a.ldg = grads->ld;
+  a.dx = grads->dx; a.dr = grads->dr; a.di = grads->di;
+  a.drate = grads->drate; a.dbias_r = grads->dbias_r; a.dbias_i = grads->dbias_i;
+  a.dh0 = grads->dh0;
+  a.part = static_cast<float*>(workspace);
+  return from_cuda(m3ssd::launch_glr_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const void* r_t,
+                            const void* i_t, const float* rate, const float* bias_r,
+                            const float* bias_i, const float* h, float* h_out, void* y_t,
+                            void* stream) {
+  const m3ssd_status st = check_glr(dims, 0);
+  if (st != M3SSD_OK) return st;
+  const uintptr_t esz = dtype_size(dims->x_dtype);
+  float* const out = h_out ? h_out : const_cast<float*>(h);
+  if (!rate || (dims->batch > 0 && (!x_t || !r_t || !i_t || !h || !y_t)))
+    return M3SSD_ERR_INVALID_ARG;
+  if (!aligned(x_t, esz) || !aligned(r_t, esz) || !aligned(i_t, esz) || !aligned(y_t, esz) ||
+      !all_aligned4({rate, bias_r, bias_i, h, out}))
+    return M3SSD_ERR_INVALID_ARG;
+  m3ssd::GlrStepArgs a{};
+  a.b = dims->batch; a.D = dims->width;
+  a.ldx = dims->ldx; a.ldr = dims->ldr; a.ldi = dims->ldi;
+  a.bf16 = dims->x_dtype == M3SSD_BF16; a.c = dims->c;
+  a.x = x_t; a.r = r_t; a.i = i_t; a.rate = rate; a.bias_r = bias_r; a.bias_i = bias_i;
+  a.h = h; a.h_out = out; a.y = y_t;
+  return from_cuda(m3ssd::launch_glr_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,137 @@
+"""Host validation of the operators around the scan (no GPU: nothing here reaches a kernel)."""
+import ctypes
+
+import pytest
+import torch
+
+import selective_state_space_m3ssd_b200 as m3
+from selective_state_space_m3ssd_b200 import build as m3build
+
+P = ctypes.c_void_p
+A, ODD = P(0x10000), P(0x10001)  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    m3build.build()
+    return m3.load()
+
+
+def glr_dims(**kw):
+    d = dict(batch=2, seqlen=8, width=6, ldx=6, ldr=6, ldi=6, x_dtype=m3.F32, c=8.0, reserved=0)
+    d.update(kw)
+    return m3.GlrDims(*(d[n] for n, _ in m3.GlrDims._fields_))
+
+
+GLR_FWD = ("x", "r", "i", "rate", "bias_r", "bias_i", "h0", "reset", "lengths", "y", "hT")
+
+
+def glr_fwd(lib, dims, **kw):
+    a = {n: A for n in GLR_FWD}
+    a.update(kw)
+    return lib.m3ssd_glr_fwd(ctypes.byref(dims), *(a[n] for n in GLR_FWD), None)
+
+
+def glr_bwd(lib, dims, grads=None, ws=A, nbytes=1 << 20, **kw):
+    names = GLR_FWD[:9] + ("y", "dy", "dhT")
+    a = {n: A for n in names}
+    a.update(kw)
+    g = grads if grads is not None else m3.GlrGrads(6, m3.F32, 0, *[0x10000] * 7)
+    return lib.m3ssd_glr_bwd(ctypes.byref(dims), *(a[n] for n in names), ctypes.byref(g), ws, nbytes, None)
+
+
+def glr_step(lib, dims, **kw):
+    names = ("x", "r", "i", "rate", "bias_r", "bias_i", "h", "h_out", "y")
+    a = {n: A for n in names}
+    a.update(kw)
+    return lib.m3ssd_glr_step(ctypes.byref(dims), *(a[n] for n in names), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), m3.ERR_INVALID_ARG), (dict(width=0), m3.ERR_INVALID_ARG),
+    (dict(ldx=5), m3.ERR_INVALID_ARG), (dict(ldr=5), m3.ERR_INVALID_ARG),
+    (dict(ldi=0), m3.ERR_INVALID_ARG), (dict(x_dtype=5), m3.ERR_INVALID_ARG),
+    (dict(c=0.0), m3.ERR_INVALID_ARG), (dict(c=-1.0), m3.ERR_INVALID_ARG),
+    (dict(c=float("nan")), m3.ERR_INVALID_ARG), (dict(c=float("inf")), m3.ERR_INVALID_ARG),
+    (dict(reserved=1), m3.ERR_INVALID_ARG), (dict(ldx=1 << 31), m3.ERR_UNSUPPORTED),
+    (dict(batch=1 << 30, width=64, ldx=64, ldr=64, ldi=64), m3.ERR_UNSUPPORTED),
+    (dict(batch=1 << 40), m3.ERR_UNSUPPORTED),
+    (dict(width=1 << 32, ldx=1 << 32, ldr=1 << 32, ldi=1 << 32), m3.ERR_UNSUPPORTED)])
+def test_glr_rejects_bad_dims(lib, kw, status):
+    d = glr_dims(**kw)
+    assert glr_fwd(lib, d) == glr_bwd(lib, d) == glr_step(lib, d) == status
+    assert lib.m3ssd_glr_bwd_workspace_size(ctypes.byref(d)) == 0
+
+
+def test_glr_rejects_bad_lengths_and_null_dims(lib):
+    assert glr_fwd(lib, glr_dims(seqlen=-1)) == m3.ERR_INVALID_ARG
+    assert glr_fwd(lib, glr_dims(seqlen=1 << 31)) == m3.ERR_UNSUPPORTED
+    assert lib.m3ssd_glr_bwd_workspace_size(None) == 0
+
+
+def test_glr_rejects_null_and_misaligned_pointers(lib):
+    d = glr_dims()
+    for n in ("x", "r", "i", "rate", "y"):
+        assert glr_fwd(lib, d, **{n: None}) == m3.ERR_INVALID_ARG, n
+    for n in GLR_FWD:
+        if n != "reset":
+            assert glr_fwd(lib, d, **{n: ODD}) == m3.ERR_INVALID_ARG, n
+    for n in ("x", "r", "i", "rate", "h", "y"):
+        assert glr_step(lib, d, **{n: None}) == m3.ERR_INVALID_ARG, n
+        assert glr_step(lib, d, **{n: ODD}) == m3.ERR_INVALID_ARG, n
+    assert glr_step(lib, d, h_out=ODD) == m3.ERR_INVALID_ARG
+    for n in ("x", "r", "i", "rate", "y", "dy"):
+        assert glr_bwd(lib, d, **{n: None}) == m3.ERR_INVALID_ARG, n
+        assert glr_bwd(lib, d, **{n: ODD}) == m3.ERR_INVALID_ARG, n
+    assert glr_bwd(lib, d, dhT=ODD) == m3.ERR_INVALID_ARG
+    for j, n in enumerate(m3.GLR_GRAD_NAMES):
+        p = [0x10000] * 7
+        p[j] = 0x10001
+        assert glr_bwd(lib, d, m3.GlrGrads(6, m3.F32, 0, *p)) == m3.ERR_INVALID_ARG, n
+        if n in ("dx", "dr", "di", "drate"):
+            p[j] = None
+            assert glr_bwd(lib, d, m3.GlrGrads(6, m3.F32, 0, *p)) == m3.ERR_INVALID_ARG, n
+
+
+def test_glr_rejects_bad_gradients_and_workspaces(lib):
+    d, p = glr_dims(), [0x10000] * 7
+    assert glr_bwd(lib, d, m3.GlrGrads(5, m3.F32, 0, *p)) == m3.ERR_INVALID_ARG
+    assert glr_bwd(lib, d, m3.GlrGrads(1 << 31, m3.F32, 0, *p)) == m3.ERR_UNSUPPORTED
+    assert glr_bwd(lib, d, m3.GlrGrads(6, 9, 0, *p)) == m3.ERR_INVALID_ARG
+    assert glr_bwd(lib, d, m3.GlrGrads(6, m3.F32, 1, *p)) == m3.ERR_INVALID_ARG
+    assert glr_bwd(lib, d, m3.GlrGrads(6, m3.BF16, 0, *p)) == m3.ERR_UNSUPPORTED  # fp32 inputs
+    need = lib.m3ssd_glr_bwd_workspace_size(ctypes.byref(d))
+    assert need > 0
+    assert glr_bwd(lib, d, nbytes=need - 1) == m3.ERR_WORKSPACE
+    assert glr_bwd(lib, d, ws=None) == m3.ERR_WORKSPACE
+    assert glr_bwd(lib, d, ws=P(0x10080)) == m3.ERR_WORKSPACE
+
+
+def test_glr_without_sequences_is_a_no_op(lib):
+    d = glr_dims(batch=0)
+    none = {n: None for n in GLR_FWD if n != "rate"}
+    assert glr_fwd(lib, d, **none) == m3.OK
+    assert glr_step(lib, d, x=None, r=None, i=None, h=None, h_out=None, y=None) == m3.OK
+
+
+def test_glr_binding_refuses_on_the_host():
+    x, v = torch.zeros(2, 3, 8), torch.zeros(8)
+    for f, a in ((m3.glr_fwd, (x, x, x, v)), (m3.glr_bwd, (x, x, x, v, x, x)),
+                 (m3.glr_step, (x[:, 0], x[:, 0], x[:, 0], x[:, 0], v))):
+        with pytest.raises(ValueError):
+            f(*a)
+    with pytest.raises(ValueError):
+        m3.glr_fwd(x[0], x[0], x[0], v)
+
+
+def test_row_strides_of_token_tensors():
+    """The binding's rule for rows a fixed distance apart (device -1 is the host)."""
+    f = lambda t, lead, w: m3._tokens_stride(t, "t", t.dtype, lead, w, -1)  # noqa: E731
+    p = torch.zeros(3, 5, 40)
+    assert f(p[..., 8:16], (3, 5), 8) == 40 and f(p, (3, 5), 40) == 40
+    assert f(p[:1, :, 8:16], (1, 5), 8) == 40 and f(p[:, :1, 8:16], (3, 1), 8) == 200
+    assert f(p[:1, :1, 8:16], (1, 1), 8) == 8 and f(p[:, 0, 8:16], (3,), 8) == 200
+    for bad in (p[:, :4, 8:16], p[..., ::5], p[:, :, :1].expand(3, 5, 8), p[:, ::2, :8][:, :2],
+                torch.zeros(5, 3, 8).transpose(0, 1), torch.zeros(5, 8).expand(3, 5, 8)):
+        with pytest.raises(ValueError):
+            f(bad, tuple(bad.shape[:-1]), 8)
