@@ -585,8 +585,8 @@ typedef struct {
  *   lengths (b) int32, may be NULL (L): the tokens of each sequence, taken between 0 and L.
  *     Later rows of x, r, i and reset are not read, those of y are zero, hT is the state after
  *     the last token (h0 where there is none).
- * b times half the width, and every stride, up to 2^31 - 1 (else M3SSD_ERR_UNSUPPORTED).  y
- * overlaps no input.  No allocation, no synchronisation; capture-safe.
+ * width up to 2^25 - 1, L up to 2^30 - 1, b times half the width and every stride up to 2^31 - 1
+ * (else M3SSD_ERR_UNSUPPORTED).  y overlaps no input.  No allocation, no synchronisation; capture-safe.
  */
 m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
                            const float* rate, const float* bias_r, const float* bias_i,

@@ -88,31 +88,31 @@ __device__ __forceinline__ float2 gate_exp(float2 g, float2 nb) {
   return make_float2(ex2(min_nan(t.x, 63.f)), ex2(min_nan(t.y, 63.f)));
 }
 
-// a = 2^t and z = 1 - a^2 of t <= 0.  (2^f - 1) / f on [-1/2, 1/2] by the polynomial of degree
+// a = 2^t and nz = a^2 - 1 of t <= 0.  (2^f - 1) / f on [-1/2, 1/2] by the polynomial of degree
 // five with the least relative error (1.1e-8, found by an exchange algorithm).
-__device__ __forceinline__ void decay_of(float2 t, float2& a, float2& z) {
-  const float big = 12582912.f;  // 1.5 2^23: adding it rounds to whole numbers
+__device__ __forceinline__ void decay_of(float2 t, float2& a, float2& nz) {
+  // adding 1.5 2^23 rounds to whole numbers, 127 more leaves 2^n's exponent in the low bits
+  const float big = 12582912.f + 127.f;
   t = make_float2(max_nan(t.x, -127.f), max_nan(t.y, -127.f));  // 2^-127 is made as zero
   const float2 m = add2(t, splat(big));
-  const float2 f = add2(t, neg2(add2(m, splat(-big))));
+  const float2 f = add2(t, fma2(m, splat(-1.f), splat(big)));
   float2 p = fma2(f, splat(1.5403517521e-4f), splat(1.3390735724e-3f));
   p = fma2(f, p, splat(9.6182374772e-3f));
   p = fma2(f, p, splat(5.5503573998e-2f));
   p = fma2(f, p, splat(2.4022649811e-1f));
   p = fma2(f, p, splat(6.9314718793e-1f));
   const float2 q = mul2(f, p);
-  const float2 w = make_float2(__int_as_float((__float_as_int(m.x) << 23) + 0x3f800000),
-                               __int_as_float((__float_as_int(m.y) << 23) + 0x3f800000));
-  const float2 wq = mul2(w, q);  // exact: w is a power of two
-  a = add2(w, wq);
-  const float2 c = add2(add2(splat(1.f), neg2(w)), neg2(wq));  // 1 - a
-  z = fma2(c, a, c);
+  const float2 w = make_float2(__int_as_float(__float_as_int(m.x) << 23),
+                               __int_as_float(__float_as_int(m.y) << 23));
+  a = fma2(w, q, w);
+  const float2 nc = fma2(w, q, add2(w, splat(-1.f)));  // a - 1
+  nz = fma2(nc, a, nc);
 }
 
-// sqrt(z) and 1 / sqrt(z), z >= 0 (0 and a large number at z = 0).
-__device__ __forceinline__ void root_of(float2 z, float2& s, float2& inv) {
-  inv = make_float2(rsq(max_nan(z.x, 1e-37f)), rsq(max_nan(z.y, 1e-37f)));
-  s = mul2(z, inv);
+__device__ __forceinline__ float root(float v) {
+  float o;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+  return o;
 }
 
 // The forward's element: a and u = s iota x.  At a reset a = 0, so s = 1.
@@ -122,9 +122,9 @@ __device__ __forceinline__ void element(const Channel& ch, float2 x, float2 r, f
   const float2 di = add2(gate_exp(i, ch.nbi), splat(1.f));
   const float2 d = mul2(dr, di), R = make_float2(rcp(d.x), rcp(d.y));
   const float2 rho = mul2(di, R), iota = mul2(dr, R);
-  float2 z, s, inv;
-  decay_of(mul2(ch.k2, rho), a, z);
-  root_of(z, s, inv);
+  float2 nz;
+  decay_of(mul2(ch.k2, rho), a, nz);
+  float2 s = make_float2(root(-nz.x), root(-nz.y));
   if (reset) {
     a = splat(0.f);
     s = splat(1.f);
@@ -142,9 +142,11 @@ __device__ __forceinline__ float2 element_grad(const Channel& ch, float2 x, floa
   const float2 d = mul2(qr, qi), R = make_float2(rcp(d.x), rcp(d.y));
   const float2 rho = mul2(qi, R), iota = mul2(qr, R);
   const float2 t = mul2(ch.k2, rho);
-  float2 a, z, s, inv;
-  decay_of(t, a, z);
-  root_of(z, s, inv);
+  float2 a, nz;
+  decay_of(t, a, nz);
+  // 1 / s and s; 1e-37 changes no 1 - a^2 above 1e-29, and keeps both finite at zero
+  const float2 inv = make_float2(rsq(1e-37f - nz.x), rsq(1e-37f - nz.y));
+  float2 s = make_float2(-nz.x * inv.x, -nz.y * inv.y);
   if (reset) {
     a = splat(0.f);
     s = splat(1.f);

@@ -34,9 +34,10 @@ m3ssd_status check_glr(const m3ssd_glr_dims* d, int64_t seqlen) {
   if (!dtype_ok(d->x_dtype)) return M3SSD_ERR_INVALID_ARG;
   if (d->ldx < d->width || d->ldr < d->width || d->ldi < d->width) return M3SSD_ERR_INVALID_ARG;
   if (!(d->c > 0.f) || !std::isfinite(d->c)) return M3SSD_ERR_INVALID_ARG;
-  // sequences x groups of channels are counted in 31 bits, strides of a tile in 32
+  // tokens, a few rounds past the end too, sequences x channel pairs and the elements of a tile
+  // are counted in 31 bits
   const int64_t most = INT32_MAX;
-  if (d->width > most || seqlen > most || d->batch > most || d->ldx > most || d->ldr > most ||
+  if (d->width > most / 64 || seqlen > most / 2 || d->batch > most || d->ldx > most || d->ldr > most ||
       d->ldi > most || d->batch * ((d->width + 1) / 2) > most)
     return M3SSD_ERR_UNSUPPORTED;
   return M3SSD_OK;
