@@ -598,7 +598,7 @@ m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void
  * projection's gradient; drate, dbias_r, dbias_i (width) and dh0 (b, width) fp32.  dbias_r,
  * dbias_i and dh0 may be NULL. */
 typedef struct {
-  int64_t ld;         /* >= width */
+  int64_t ld;         /* width .. 2^25 - 1 */
   int32_t dtype;      /* m3ssd_dtype */
   uint32_t reserved;  /* must be 0 */
   void* dx;

@@ -133,13 +133,15 @@ struct Copier {
   static constexpr int rows = chunks < kLanes ? kLanes / chunks : 1;  // a warp's at once
   static constexpr int cols = chunks < kLanes ? 1 : chunks / kLanes;  // pieces of a row a lane
   static_assert(run % rows == 0, "a copy of the warp takes whole rows of its run");
+  const T* tensor; // where nothing is to be read
   const T* base;   // of the CTA's next tile: its first token, the group's first channel
   int64_t ld, off; // the lane's first piece from there
 
   __device__ __forceinline__ void init(const void* t, int64_t row, int64_t d0, int64_t ld_, int warp,
                                        int lane) {
     ld = ld_;
-    base = static_cast<const T*>(t) + row * ld + d0;
+    tensor = static_cast<const T*>(t);
+    base = tensor + row * ld + d0;
     off = (int64_t)(warp * run + row_of(lane)) * ld + col_of(lane);
   }
   static __device__ __forceinline__ int row_of(int lane) { return rows > 1 ? lane / chunks : 0; }
@@ -171,7 +173,7 @@ struct Copier {
         const int col = col_of(lane) + c * kLanes * per;
         const int n = r >= lo && r < hi ? min(max(left - col, 0), per) * (int)sizeof(T) : 0;
         T* const at = dst + r * kGroup + col;
-        const T* const from = n > 0 ? p + c * kLanes * per : base;
+        const T* const from = n > 0 ? p + c * kLanes * per : tensor;
         if constexpr (MODE == kCopy16)
           copy16(smem_addr(at), from, n);
         else if constexpr (MODE == kCopy4)
@@ -264,9 +266,11 @@ __device__ __forceinline__ float2 exchange(Maps& ex, int flip, const Map& mine, 
 #endif
 constexpr int kStages = KS;
 
-// Shared memory of a kernel whose stages hold `tensors` runs a warp.
+// Shared memory of `stages` stages of `tensors` runs a warp.
 template <typename T>
-constexpr int ring_bytes(int tensors) { return kStages * kWarps * tensors * kRun<T> * kGroup * (int)sizeof(T); }
+constexpr int ring_bytes(int tensors, int stages) {
+  return stages * kWarps * tensors * kRun<T> * kGroup * (int)sizeof(T);
+}
 
 template <typename T, int MODE, bool RESET, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * kLanes, KB) glr_fwd_kernel(GlrArgs a) {
@@ -385,48 +389,172 @@ __global__ void __launch_bounds__(kWarps * kLanes, KB) glr_fwd_kernel(GlrArgs a)
   }
 }
 
-// The same walk from the last token; the sums of a sequence go to a row of partial sums.
-template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads) glr_bwd_kernel(GlrBwdArgs a) {
-  const GlrArgs& f = a.f;
-  const int64_t pairs = (f.D + 1) / 2, id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (id >= f.b * pairs) return;
-  const int64_t b = id / pairs, d = id % pairs * 2;
-  const bool in1 = d + 1 < f.D;
+// The walk back: tiles from the last one, a tile's last run first.  With g_t = dy_t + back_t a
+// token maps back_t, what comes from later tokens, to back_{t-1} = a_t (back_t + dy_t).  A warp
+// first composes its run (the decays alone), and once back has reached it, walks the run again
+// with the whole gradient; recomputing the gates costs less than holding them would.
+template <typename T, typename G, int MODE, bool RESET, bool CLUSTER>
+__global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs args) {
+  constexpr int run = kRun<T>, tile = kWarps * run, kTensors = 5;
+  const GlrArgs& a = args.f;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ typename std::conditional<CLUSTER, Maps, Chain>::type ex;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, order = kWarps - 1 - warp;
+  const uint32_t rank = CLUSTER ? cluster_rank() : 0, ranks = CLUSTER ? cluster_size() : 1;
+  const int64_t groups = (a.D + kGroup - 1) / kGroup, item = blockIdx.x / ranks;
+  const int64_t b = item / groups, d0 = item % groups * kGroup, d = d0 + 2 * lane;
+  const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L;
+  const bool in0 = d < a.D, in1 = d + 1 < a.D;
+  const int len = a.lengths ? min(max(a.lengths[b], 0), L) : L;
+  const int step = (int)ranks * tile, rounds = (L + step - 1) / step;
+  int t0 = (rounds - 1) * step + (int)rank * tile;
+  const int64_t row = b * a.L + t0;
+  Copier<T, MODE> src[kTensors];
+  src[0].init(a.x, row, d0, a.ldx, warp, lane);
+  src[1].init(a.r, row, d0, a.ldr, warp, lane);
+  src[2].init(a.i, row, d0, a.ldi, warp, lane);
+  src[3].init(args.dy, row, d0, a.D, warp, lane);
+  src[4].init(a.y, row - 1, d0, a.D, warp, lane);  // h_{t-1}
+  const uint32_t ldg = (uint32_t)args.ldg, at = warp * run * ldg + 2 * lane;
+  G* out[3] = {static_cast<G*>(args.dx) + row * args.ldg + d0,
+               static_cast<G*>(args.dr) + row * args.ldg + d0,
+               static_cast<G*>(args.di) + row * args.ldg + d0};
+  const uint8_t* const reset = RESET ? a.reset + b * a.L : nullptr;
+  const bool whole = (a.D | ldg) % 2 == 0 &&
+                     (reinterpret_cast<uintptr_t>(args.dx) | reinterpret_cast<uintptr_t>(args.dr) |
+                      reinterpret_cast<uintptr_t>(args.di)) % (2 * sizeof(G)) == 0;
   Channel ch;
-  channel_of(f.rate, f.bias_r, f.bias_i, f.c, d, d + 1, f.D, ch);
-  const int64_t len = f.lengths ? min(max((int64_t)f.lengths[b], (int64_t)0), f.L) : f.L;
-  float2 back = a.dhT ? load2(a.dhT + b * f.D + d, in1) : splat(0.f);
-  float2 sr = splat(0.f), si = splat(0.f), se = splat(0.f);
-  const T* y = static_cast<const T*>(f.y) + b * f.L * f.D + d;
-  const T* dy = static_cast<const T*>(a.dy) + b * f.L * f.D + d;
-  for (int64_t t = f.L - 1; t >= 0; --t) {
-    const int64_t row = b * f.L + t;
-    float2 dx = splat(0.f), dr = dx, di = dx, E = dx;
-    if (t < len) {
-      const bool cut = f.reset && f.reset[row];
-      const float2 prev = t > 0     ? load2(y + (t - 1) * f.D, in1)
-                          : f.h0 ? load2(f.h0 + b * f.D + d, in1)
-                                 : splat(0.f);
-      const float2 g = add2(load2(dy + t * f.D, in1), back);
-      const float2 al = element_grad(ch, load2(static_cast<const T*>(f.x) + row * f.ldx + d, in1),
-                                     load2(static_cast<const T*>(f.r) + row * f.ldr + d, in1),
-                                     load2(static_cast<const T*>(f.i) + row * f.ldi + d, in1), cut,
-                                     prev, g, dx, dr, di, E);
-      back = cut ? splat(0.f) : mul2(al, g);
+  channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  float2 back = splat(0.f), h0 = splat(0.f);
+  if (args.dhT) {
+    if (in0) back.x = args.dhT[b * a.D + d];
+    if (in1) back.y = args.dhT[b * a.D + d + 1];
+  }
+  if (a.h0) {
+    if (in0) h0.x = a.h0[b * a.D + d];
+    if (in1) h0.y = a.h0[b * a.D + d + 1];
+  }
+  if constexpr (!CLUSTER) {
+    if (order == 0) ex.state[0][lane] = back;
+  }
+  float2 se = splat(0.f), sr = splat(0.f), si = splat(0.f);
+
+  T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
+  auto stage = [&](int k) { return ring + k * (kWarps * kTensors * run * kGroup); };
+  auto fetch = [&](int k, int t) {
+    const int hi = len - t - warp * run;
+    if (t >= 0 && hi > 0) {
+      const bool all = hi >= run && left == kGroup;
+      const int lo = t == 0 && warp == 0 ? 1 : 0;  // no h before the first token
+#pragma unroll
+      for (int j = 0; j < kTensors; ++j) {
+        if (all && (j < 4 || lo == 0))
+          src[j].copy_all(stage(k) + j * run * kGroup, lane);
+        else
+          src[j].copy_some(stage(k) + j * run * kGroup, j < 4 ? 0 : lo, hi, left, lane);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kTensors; ++j) src[j].base -= step * src[j].ld;
+    copies_end();
+  };
+  fetch(0, t0);
+  int k = 0;
+  [[maybe_unused]] int flip = 0;
+  for (int round = 0; round < rounds; ++round, t0 -= step) {
+    copies_wait<0>();
+    __syncwarp();
+    fetch(k ^ 1, t0 - step);
+    const T* const st = stage(k) + 2 * lane;
+    k ^= 1;
+    const int t = t0 + warp * run;
+    const bool full = t + run <= len;
+    const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    Map m = {splat(1.f), splat(0.f)};
+    auto compose = [&](int j) {
+      const bool cut = RESET && (cuts >> j & 1);
+      const float2 al = decay(ch, pair_of(st + (run + j) * kGroup), cut);
+      const float2 dy = pair_of(st + (3 * run + j) * kGroup);
+      m.A = cut ? splat(0.f) : mul2(al, m.A);
+      m.B = cut ? splat(0.f) : mul2(al, add2(m.B, dy));
+    };
+    if (full) {
+#pragma unroll
+      for (int j = run - 1; j >= 0; --j) compose(j);
+    } else {
+#pragma unroll
+      for (int j = run - 1; j >= 0; --j)
+        if (t + j < len) compose(j);
+    }
+    float2 g;  // what reaches the run from later tokens
+    if constexpr (CLUSTER)
+      g = exchange<RESET>(ex, flip, m, cuts != 0, order, ranks - 1 - rank, ranks, back, warp, lane);
+    else
+      g = pass_on(ex, m, cuts != 0, order, round == 0 && order == 0,
+                  round == rounds - 1 && order == kWarps - 1, lane);
+    flip ^= 1;
+    const float2 first = t == 0 ? h0 : splat(0.f);
+    auto finish = [&](int j, float2& dx, float2& dr, float2& di) {
+      const bool cut = RESET && (cuts >> j & 1);
+      g = add2(g, pair_of(st + (3 * run + j) * kGroup));
+      float2 prev = pair_of(st + (4 * run + j) * kGroup), E;
+      if (j == 0) prev = add2(prev, first);
+      const float2 al = element_grad(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
+                                     pair_of(st + (2 * run + j) * kGroup), cut, prev, g, dx, dr, di, E);
+      g = cut ? splat(0.f) : mul2(al, g);
+      se = add2(se, E);
       sr = add2(sr, dr);
       si = add2(si, di);
-      se = add2(se, E);
+    };
+    if (full && whole) {
+#pragma unroll
+      for (int j = run - 1; j >= 0; --j) {
+        float2 dx, dr, di;
+        finish(j, dx, dr, di);
+        put_pair(out[0] + (at + j * ldg), dx, true, in0, in1);
+        put_pair(out[1] + (at + j * ldg), dr, true, in0, in1);
+        put_pair(out[2] + (at + j * ldg), di, true, in0, in1);
+      }
+    } else {
+#pragma unroll
+      for (int j = run - 1; j >= 0; --j) {
+        float2 dx = splat(0.f), dr = dx, di = dx;
+        if (t + j < len) finish(j, dx, dr, di);
+        if (t + j < L) {
+          put_pair(out[0] + (at + j * ldg), dx, whole, in0, in1);
+          put_pair(out[1] + (at + j * ldg), dr, whole, in0, in1);
+          put_pair(out[2] + (at + j * ldg), di, whole, in0, in1);
+        }
+      }
     }
-    store2(static_cast<G*>(a.dx) + row * a.ldg + d, dx, in1);
-    store2(static_cast<G*>(a.dr) + row * a.ldg + d, dr, in1);
-    store2(static_cast<G*>(a.di) + row * a.ldg + d, di, in1);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) out[j] -= step * args.ldg;
   }
-  if (a.dh0) store2(a.dh0 + b * f.D + d, back, in1);
-  float* part = a.part + 3 * b * f.D + d;
-  store2(part, se, in1);
-  store2(part + f.D, sr, in1);
-  store2(part + 2 * f.D, si, in1);
+  if constexpr (CLUSTER) {
+    cluster_arrive();
+    cluster_wait();
+  }
+  // the CTA's sums, the warps' in order: a row of the workspace for each sequence and rank
+  copies_wait<0>();
+  __syncthreads();
+  if constexpr (!CLUSTER) back = ex.state[0][lane];
+  float2(*red)[3][kLanes] = reinterpret_cast<float2(*)[3][kLanes]>(smem);
+  red[warp][0][lane] = se;
+  red[warp][1][lane] = sr;
+  red[warp][2][lane] = si;
+  __syncthreads();
+  if (warp < 3) {
+    float2 s = splat(0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s = add2(s, red[w][warp][lane]);
+    float* const part = args.part + (3 * (b * ranks + rank) + warp) * a.D + d;
+    if (in0) part[0] = s.x;
+    if (in1) part[1] = s.y;
+  }
+  if (args.dh0 && rank == 0 && warp == 0) {
+    if (in0) args.dh0[b * a.D + d] = back.x;
+    if (in1) args.dh0[b * a.D + d + 1] = back.y;
+  }
 }
 
 // drate, dbias_r and dbias_i of a channel: its partial sums in a fixed order.
@@ -462,12 +590,6 @@ __global__ void __launch_bounds__(kThreads) glr_step_kernel(GlrStepArgs a) {
 }
 
 unsigned grid_for(int64_t n) { return (unsigned)((n + kThreads - 1) / kThreads); }
-
-template <typename T, typename G>
-cudaError_t bwd_t(const GlrBwdArgs& a, cudaStream_t s) {
-  glr_bwd_kernel<T, G><<<grid_for(a.f.b * ((a.f.D + 1) / 2)), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
 
 // The widest copies that rows at these addresses and strides allow.
 template <typename T>
@@ -510,8 +632,8 @@ cudaError_t fwd_m(const GlrArgs& a, cudaStream_t s) {
   const int64_t items = a.b * ((a.D + kGroup - 1) / kGroup);
   const int ranks = ranks_of(items, (a.L + kWarps * kRun<T> - 1) / (kWarps * kRun<T>));
   const unsigned grid = (unsigned)items;
-  return ranks > 1 ? launch(glr_fwd_kernel<T, MODE, RESET, true>, a, grid, ranks, ring_bytes<T>(3), s)
-                   : launch(glr_fwd_kernel<T, MODE, RESET, false>, a, grid, 1, ring_bytes<T>(3), s);
+  return ranks > 1 ? launch(glr_fwd_kernel<T, MODE, RESET, true>, a, grid, ranks, ring_bytes<T>(3, kStages), s)
+                   : launch(glr_fwd_kernel<T, MODE, RESET, false>, a, grid, 1, ring_bytes<T>(3, kStages), s);
 }
 template <typename T, int MODE>
 cudaError_t fwd_r(const GlrArgs& a, cudaStream_t s) {
@@ -528,14 +650,43 @@ cudaError_t fwd_t(const GlrArgs& a, cudaStream_t s) {
   }
 }
 
+int bwd_ranks(int64_t b, int64_t L, int64_t D, bool bf16) {
+  const int tile = kWarps * (bf16 ? kRun<__nv_bfloat16> : kRun<float>);
+  return ranks_of(b * ((D + kGroup - 1) / kGroup), (L + tile - 1) / tile);
+}
+
+template <typename T, typename G, int MODE, bool RESET>
+cudaError_t bwd_m(const GlrBwdArgs& a, cudaStream_t s) {
+  const GlrArgs& f = a.f;
+  const unsigned grid = (unsigned)(f.b * ((f.D + kGroup - 1) / kGroup));
+  const int ranks = bwd_ranks(f.b, f.L, f.D, f.bf16), smem = ring_bytes<T>(5, 2);
+  return ranks > 1 ? launch(glr_bwd_kernel<T, G, MODE, RESET, true>, a, grid, ranks, smem, s)
+                   : launch(glr_bwd_kernel<T, G, MODE, RESET, false>, a, grid, 1, smem, s);
+}
+template <typename T, typename G, int MODE>
+cudaError_t bwd_r(const GlrBwdArgs& a, cudaStream_t s) {
+  return a.f.reset ? bwd_m<T, G, MODE, true>(a, s) : bwd_m<T, G, MODE, false>(a, s);
+}
+template <typename T, typename G>
+cudaError_t bwd_t(const GlrBwdArgs& a, cudaStream_t s) {
+  const GlrArgs& f = a.f;
+  switch (copy_of<T>({f.x, f.r, f.i, f.y, a.dy}, {f.ldx, f.ldr, f.ldi, f.D})) {
+    case kCopy16: return bwd_r<T, G, kCopy16>(a, s);
+    case kCopy4: return bwd_r<T, G, kCopy4>(a, s);
+    default:
+      if constexpr (sizeof(T) == 2) return bwd_r<T, G, kCopyElem>(a, s);
+      return cudaErrorInvalidValue;  // fp32 rows start at whole words
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s) {
   return a.bf16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
 }
 
-size_t glr_bwd_workspace_bytes(int64_t b, int64_t, int64_t D) {
-  return (size_t)b * 3 * (size_t)D * sizeof(float);
+size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
+  return (size_t)b * bwd_ranks(b, L, D, bf16) * 3 * (size_t)D * sizeof(float);
 }
 
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s) {
@@ -546,8 +697,8 @@ cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s) {
                                         : bwd_t<__nv_bfloat16, float>(a, s);
     if (e != cudaSuccess) return e;
   }
-  glr_sum_kernel<<<grid_for(f.D), kThreads, 0, s>>>(a.part, f.b, f.D, f.rate, a.drate, a.dbias_r,
-                                                     a.dbias_i);
+  glr_sum_kernel<<<grid_for(f.D), kThreads, 0, s>>>(a.part, f.b * bwd_ranks(f.b, f.L, f.D, f.bf16), f.D,
+                                                     f.rate, a.drate, a.dbias_r, a.dbias_i);
   return cudaGetLastError();
 }
 

@@ -132,6 +132,14 @@ __device__ __forceinline__ void element(const Channel& ch, float2 x, float2 r, f
   u = mul2(mul2(s, iota), x);
 }
 
+// The decay alone, which is all that the walk of g needs.
+__device__ __forceinline__ float2 decay(const Channel& ch, float2 r, bool reset) {
+  const float2 q = add2(gate_exp(r, ch.nbr), splat(1.f));
+  float2 a, nz;
+  decay_of(mul2(ch.k2, make_float2(rcp(q.x), rcp(q.y))), a, nz);
+  return reset ? splat(0.f) : a;
+}
+
 // The backward's element, from g = dL/dh_t and h_{t-1} (prev): the gradients of x, i, r and
 // E = g dh/d(log a) log a, whose sum gives the rate's.  Returns a.
 __device__ __forceinline__ float2 element_grad(const Channel& ch, float2 x, float2 r, float2 i,

@@ -345,7 +345,7 @@ struct GlrStepArgs {
   void* y;
 };
 cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s);
-size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D);
+size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16);
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s);
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s);
 

@@ -88,7 +88,8 @@ m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void
 
 size_t m3ssd_glr_bwd_workspace_size(const m3ssd_glr_dims* dims) {
   if (check_glr(dims, dims ? dims->seqlen : 0) != M3SSD_OK) return 0;
-  return m3ssd::glr_bwd_workspace_bytes(dims->batch, dims->seqlen, dims->width);
+  return m3ssd::glr_bwd_workspace_bytes(dims->batch, dims->seqlen, dims->width,
+                                        dims->x_dtype == M3SSD_BF16);
 }
 
 m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
@@ -102,7 +103,7 @@ m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void
   if (!grads || grads->reserved != 0 || !dtype_ok(grads->dtype)) return M3SSD_ERR_INVALID_ARG;
   if (grads->dtype == M3SSD_BF16 && dims->x_dtype != M3SSD_BF16) return M3SSD_ERR_UNSUPPORTED;
   if (grads->ld < dims->width) return M3SSD_ERR_INVALID_ARG;
-  if (grads->ld > INT32_MAX) return M3SSD_ERR_UNSUPPORTED;
+  if (grads->ld > INT32_MAX / 64) return M3SSD_ERR_UNSUPPORTED;  // as the width
   if (!glr_inputs_ok(dims, x, r, i, rate, bias_r, bias_i, h0, lengths)) return M3SSD_ERR_INVALID_ARG;
   const uintptr_t esz = dtype_size(dims->x_dtype), gsz = dtype_size(grads->dtype);
   if (dims->batch > 0 && dims->seqlen > 0 &&
@@ -112,7 +113,7 @@ m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void
       !aligned(grads->dr, gsz) || !aligned(grads->di, gsz) ||
       !all_aligned4({dhT, grads->drate, grads->dbias_r, grads->dbias_i, grads->dh0}))
     return M3SSD_ERR_INVALID_ARG;
-  const size_t need = m3ssd::glr_bwd_workspace_bytes(dims->batch, dims->seqlen, dims->width);
+  const size_t need = m3ssd_glr_bwd_workspace_size(dims);
   if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256))))
     return M3SSD_ERR_WORKSPACE;
   m3ssd::GlrBwdArgs a{};

@@ -6,8 +6,11 @@ over, and the hardware exponential's 2^-22), so the gates by eta = (3 w + 16) e 
 products), log a by tau = eta + 16 e (softplus included), a by |log a| tau + 6 e, and
 sqrt(1 - a^2) by tau / 2 + 12 e, since |d log(1 - a^2)| <= 2 |d log a| / |log a| |log a| a^2 /
 (1 - a^2) <= tau.  So u = s iota x is off by (eta_r + eta_i + 40 e) |u|, and the state by what the
-recurrence makes of that: err_t = a err_{t-1} + a |h_{t-1}| (|log a| tau + 8 e) + ... + 2 e |h_t|, the
-8 covering one product more a token that a scan in pieces does.  Every bound is doubled.
+recurrence makes of that: err_t = a err_{t-1} + a M_{t-1} (|log a| tau + 8 e) + ... + 2 e M_t, the
+8 covering one product more a token that a scan in pieces does.  M_t = a M_{t-1} + |u_t| stands in
+for |h_t|: a scan in pieces adds A h and B of whole runs of tokens, whose roundings go by the size
+of those, and they may cancel (in the backward, |dy_t| + a_{t+1} M_{t+1} for |g_t|; at one token
+A h + B is a (back + dy) as a back + a dy).  Every bound is doubled.
 Where 1 - a^2 is below 1e-37, the kernels' root of it is off by up to sqrt(1e-37) = 3.2e-19 and
 (log a) / s, about s / 2 there, by no more: S0 = 4e-19 of iota x (or g iota x) is allowed for.
 An a that is no normal number counts as zero: A0 = 2^-126 of |h_{t-1}| (or g, g |log a| |h_{t-1}|).
@@ -70,14 +73,14 @@ def fwd_tolerance(h, y, hT):
                                     h.get("reset"))
     ru, ra, *_ = bounds(h)
     err, out = np.zeros_like(hT), np.zeros_like(y)
-    prev = np.zeros_like(hT) if h["h0"] is None else np.abs(h["h0"])
+    M = np.zeros_like(hT) if h["h0"] is None else np.abs(h["h0"])
     n = ly._lens(h.get("lengths"), *y.shape[:2])
     for t in range(y.shape[1]):
-        new = a[:, t] * err + prev * (a[:, t] * ra[:, t] + A0) + \
-            np.abs(iota * h["x"])[:, t] * (s[:, t] * ru[:, t] + S0) + \
-            2 * E * (np.abs(y[:, t]) + a[:, t] * prev)
+        u = np.abs(s * iota * h["x"])[:, t]
+        new = a[:, t] * err + M * (a[:, t] * ra[:, t] + A0) + u * ru[:, t] + \
+            np.abs(iota * h["x"])[:, t] * S0 + 2 * E * (u + 2 * a[:, t] * M)
         live = (t < n)[:, None]
-        err, prev = np.where(live, new, err), np.where(live, np.abs(y[:, t]), prev)
+        err, M = np.where(live, new, err), np.where(live, a[:, t] * M + u, M)
         out[:, t] = np.where(live, err, 0)
     return 2 * out, 2 * err
 
@@ -120,11 +123,13 @@ def check_bwd(d, y, got, grad_dtype):
     b, L, D = y.shape
     ru, ra, tau, er, ei = bounds(h)
     n = ly._lens(h.get("lengths"), b, L)
-    eg, nxt = np.zeros((b, L, D)), np.zeros((b, D))
+    eg, nxt, M = np.zeros((b, L, D)), np.zeros((b, D)), np.abs(h["dhT"])
     for t in range(L - 1, -1, -1):
         live = (t < n)[:, None]
-        eg[:, t] = np.where(live, nxt + 2 * E * np.abs(o["g"][:, t]), 0)
-        nxt = np.where(live, a[:, t] * eg[:, t] + np.abs(o["g"][:, t]) * (a[:, t] * ra[:, t] + A0), nxt)
+        Mg = np.where(live, M + np.abs(h["dy"][:, t]), 0)
+        eg[:, t] = np.where(live, nxt + 2 * E * Mg, 0)
+        nxt = np.where(live, a[:, t] * eg[:, t] + Mg * (a[:, t] * ra[:, t] + A0), nxt)
+        M = np.where(live, a[:, t] * Mg, M)
     first = np.zeros((b, 1, D)) if h["h0"] is None else h["h0"][:, None]
     prev = np.abs(np.concatenate((first, y[:, :-1]), 1))
     g, x = np.abs(o["g"]), np.abs(h["x"])
