@@ -577,6 +577,11 @@ typedef struct {
   uint32_t reserved;  /* must be 0 */
 } m3ssd_glr_dims;
 
+/* Bytes of device workspace m3ssd_glr_fwd needs on the current device: non-zero where few
+ * sequences are cut into parts, which goes by the sizes and the device's SM count.  0 for
+ * invalid dims. */
+size_t m3ssd_glr_fwd_workspace_size(const m3ssd_glr_dims* dims);
+
 /*
  * Forward.  rate, bias_r, bias_i (width) and h0, hT (b, width) are fp32; bias_r, bias_i and h0
  * may be NULL (zero), hT may be NULL or h0.  y: dense (b, L, width).
@@ -586,12 +591,13 @@ typedef struct {
  *     Later rows of x, r, i and reset are not read, those of y are zero, hT is the state after
  *     the last token (h0 where there is none).
  * width up to 2^25 - 1, L up to 2^30 - 1, b times half the width and every stride up to 2^31 - 1
- * (else M3SSD_ERR_UNSUPPORTED).  y overlaps no input.  No allocation, no synchronisation; capture-safe.
+ * (else M3SSD_ERR_UNSUPPORTED).  y overlaps no input.  workspace: 256-byte aligned, not read
+ * afterwards.  No allocation, no synchronisation; capture-safe.
  */
 m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
                            const float* rate, const float* bias_r, const float* bias_i,
                            const float* h0, const uint8_t* reset, const int32_t* lengths, void* y,
-                           float* hT, void* stream);
+                           float* hT, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients: dx, dr, di (b, L, width) in `dtype` (fp32, or bf16 where x_dtype is: each value
  * rounded once), their rows `ld` elements apart, so that they may be column ranges of one

@@ -205,7 +205,9 @@ def load(path: str | None = None):
             [ctypes.POINTER(CacheQ8), ctypes.POINTER(CacheQ8), vp, vp]
         lib.m3ssd_step_q8.restype = ctypes.c_int
         gdp = ctypes.POINTER(GlrDims)
-        lib.m3ssd_glr_fwd.argtypes = [gdp] + [vp] * 12
+        lib.m3ssd_glr_fwd.argtypes = [gdp] + [vp] * 12 + [sz, vp]
+        lib.m3ssd_glr_fwd_workspace_size.argtypes = [gdp]
+        lib.m3ssd_glr_fwd_workspace_size.restype = sz
         lib.m3ssd_glr_fwd.restype = ctypes.c_int
         lib.m3ssd_glr_bwd_workspace_size.argtypes = [gdp]
         lib.m3ssd_glr_bwd_workspace_size.restype = sz
@@ -728,6 +730,15 @@ def _launch(name: str, dev, *args):
         _check(st, name)
 
 
+def _on_device(dev, f, *args):
+    """f(*args) with the device current: a workspace's size goes by its SM count."""
+    import torch
+    if torch._C._cuda_getDevice() == dev.index:
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
 def _need_all(dev, *checks):
     """:func:`_need` for (tensor, name, dtype, shape) on the CUDA device ``dev``, in one
     loop: a decode step checks some twenty tensors."""
@@ -1091,7 +1102,7 @@ def _glr_dims(x, r, i, rate, bias_r, bias_i, c):
 
 
 def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None, reset=None,
-            lengths=None, y=None, hT=None, want_hT: bool = True):
+            lengths=None, y=None, hT=None, want_hT: bool = True, workspace=None):
     """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(i_t + bias_i) x_t
     with a_t = exp(-c softplus(rate) sigma(r_t + bias_r)), through ``m3ssd_glr_fwd``.
 
@@ -1114,9 +1125,17 @@ def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None,
     _need_all(dev, (h0, "h0", f32, (b, D)), (reset, "reset", torch.uint8, (b, L)),
               (lengths, "lengths", torch.int32, (b,)), (y, "y", x.dtype, (b, L, D)),
               (hT, "hT", f32, (b, D)))
+    need = _on_device(dev, glr_fwd_workspace_size, dims)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_glr_fwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
-            _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y), _addr(hT))
+            _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y), _addr(hT),
+            ws, ws_bytes)
     return y, hT
+
+
+def glr_fwd_workspace_size(dims: GlrDims) -> int:
+    """Bytes on the current device."""
+    return int(load().m3ssd_glr_fwd_workspace_size(ctypes.byref(dims)))
 
 
 def glr_bwd_workspace_size(dims: GlrDims) -> int:
@@ -1156,11 +1175,7 @@ def glr_bwd(x, r, i, rate, y, dy, *, bias_r=None, bias_i=None, c: float = 8.0, h
     if len(lds) != 1 and b * L > 1:
         raise ValueError("dx, dr and di must have their rows the same distance apart")
     g = GlrGrads(max(lds), _xdtype(grads["dx"]), 0, *(grads[k].data_ptr() for k in GLR_GRAD_NAMES))
-    if torch._C._cuda_getDevice() == dev.index:
-        need = glr_bwd_workspace_size(dims)
-    else:
-        with torch.cuda.device(dev):
-            need = glr_bwd_workspace_size(dims)
+    need = _on_device(dev, glr_bwd_workspace_size, dims)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_glr_bwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
             _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y),

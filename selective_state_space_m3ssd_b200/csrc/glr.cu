@@ -26,25 +26,22 @@ __device__ __forceinline__ void store2(T* p, float2 v, bool in1) {
   if (in1) p[1] = from_f32<T>(v.y);
 }
 
-// ---- the scan's pieces -------------------------------------------------------------------
+// ---- the walks' pieces -------------------------------------------------------------------
 //
 // A CTA of eight warps takes 64 channels of a sequence, two a lane, and walks the tokens in
-// tiles: a warp composes its kRun tokens into h -> A h + B, the warps' (A, B) meet in shared
-// memory, and every warp then finishes its tokens from the state that reaches it.  With few
-// (sequence, channels) a cluster's CTAs take consecutive tiles of one and hand each other
-// their tiles' (A, B) through shared memory.
+// tiles, one run of kRun tokens a warp: a warp composes its run into h -> A h + B, waits for
+// the state before it, hands the state after it to the next warp and finishes its tokens.
+// So the state's way through a tile is eight short hops, under which the other warps (and
+// another CTA) compute.  With too few (sequence, channels) to fill the device a sequence is cut
+// into parts instead, one a warp, of as many CTAs as there is room for: a first kernel composes
+// every part into its map, and in the walk each warp begins from what the maps before it
+// make of h0.  That reads the inputs twice, so it is for launches that would leave SMs idle.
 
-#ifndef KW
-#define KW 8
-#define KR 8
-#define KB 2
-#endif
-constexpr int kWarps = KW, kLanes = 32, kGroup = 64, kMaxCluster = 8;
+constexpr int kWarps = 8, kLanes = 32, kGroup = 64;
 
-// Tokens of a warp: 512 bytes of a row's channels either way, so that a stage of three tensors takes
-// 3 KB a warp.
+// Tokens of a run: 1 KB of a tensor either way.
 template <typename T>
-constexpr int kRun = sizeof(T) == 2 ? KR : 4;
+constexpr int kRun = sizeof(T) == 2 ? 8 : 4;
 
 // How rows are copied: in 16-byte pieces, 4-byte pieces, or element by element (bf16 rows that
 // start in the middle of a word).
@@ -73,36 +70,6 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// Stores to the same place of another CTA's shared memory.
-__device__ __forceinline__ void remote_store(uint32_t local, uint32_t rank, float4 v) {
-  uint32_t p;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y),
-               "f"(v.z), "f"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void remote_store(uint32_t local, uint32_t rank, uint32_t v) {
-  uint32_t p;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(local), "r"(rank));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory");
-}
-
 __device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
 __device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
   const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
@@ -134,15 +101,16 @@ struct Copier {
   static constexpr int cols = chunks < kLanes ? 1 : chunks / kLanes;  // pieces of a row a lane
   static_assert(run % rows == 0, "a copy of the warp takes whole rows of its run");
   const T* tensor; // where nothing is to be read
-  const T* base;   // of the CTA's next tile: its first token, the group's first channel
+  const T* base;   // a row and the group's first channel
   int64_t ld, off; // the lane's first piece from there
 
-  __device__ __forceinline__ void init(const void* t, int64_t row, int64_t d0, int64_t ld_, int warp,
+  // The warp's run begins `ahead` rows after `row`.
+  __device__ __forceinline__ void init(const void* t, int64_t row, int ahead, int64_t d0, int64_t ld_,
                                        int lane) {
     ld = ld_;
     tensor = static_cast<const T*>(t);
     base = tensor + row * ld + d0;
-    off = (int64_t)(warp * run + row_of(lane)) * ld + col_of(lane);
+    off = (ahead + row_of(lane)) * ld + col_of(lane);
   }
   static __device__ __forceinline__ int row_of(int lane) { return rows > 1 ? lane / chunks : 0; }
   static __device__ __forceinline__ int col_of(int lane) { return lane % chunks * per; }
@@ -192,26 +160,47 @@ __device__ __forceinline__ uint32_t resets_of(const uint8_t* reset, int t, int l
   return __ballot_sync(0xffffffffu, on);
 }
 
-// What a CTA's warps and a cluster's CTAs hand each other.
-struct Chain {  // the state before each warp's tokens
+// Where a warp walks: `rounds` runs of which the first begins at token t, `step` tokens apart;
+// all of a sequence's tiles with its CTA, or (SPLIT) one part of it alone.
+template <typename T, bool SPLIT>
+struct Way {
+  int64_t b, d0;
+  int first_row;  // the sequence's token that the CTA's (SPLIT: the warp's) first run counts from
+  int ahead;      // the warp's run from there
+  int step, rounds, part;
+
+  __device__ __forceinline__ Way(const GlrArgs& a, int warp) {
+    const int64_t groups = (a.D + kGroup - 1) / kGroup;
+    const uint32_t ctas = SPLIT ? (uint32_t)a.split : 1u;
+    const int64_t item = blockIdx.x / ctas;
+    b = item / groups;
+    d0 = item % groups * kGroup;
+    const int L = (int)a.L;
+    if constexpr (SPLIT) {
+      part = (int)(blockIdx.x % ctas) * kWarps + warp;
+      const int64_t at = (int64_t)part * a.part_len;
+      first_row = (int)min(at, (int64_t)L);
+      ahead = 0;
+      step = kRun<T>;
+      rounds = (min(L - first_row, a.part_len) + kRun<T> - 1) / kRun<T>;
+    } else {
+      part = 0;
+      first_row = 0;
+      ahead = warp * kRun<T>;
+      step = kWarps * kRun<T>;
+      rounds = (L + step - 1) / step;
+    }
+  }
+};
+
+// The state before each warp's run.
+struct Chain {
   float2 state[kWarps][kLanes];
 };
-struct Maps {  // the warps' and the CTAs' maps of two consecutive rounds
-  float4 warp[2][kWarps][kLanes];
-  float4 cta[2][kMaxCluster][kLanes];
-  uint32_t warp_cut[2][kWarps];
-  uint32_t cta_cut[2][kMaxCluster];
-};
-__device__ __forceinline__ float4 pack_map(const Map& m) {
-  return make_float4(m.A.x, m.A.y, m.B.x, m.B.y);
-}
-__device__ __forceinline__ Map unpack_map(float4 v) {
-  return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
-}
 
-// A CTA on its own: the state goes from warp to warp, in a circle, each waiting at the barrier of
-// its link (order + 1) only.  A warp's place is written anew after its state has come round to
-// the one before it, so after it was read.  Returns the state before the warp's tokens.
+// The state goes from warp to warp, in a circle, each waiting at the barrier of its link (order +
+// 1) only.  A warp's place is written anew after its state has come round to the one before it,
+// so after it was read.  Returns the state before the warp's run.
 __device__ __forceinline__ float2 pass_on(Chain& ch, const Map& mine, bool cut, int order, bool first,
                                           bool last, int lane) {
   if (!first) asm volatile("bar.sync %0, 64;" ::"r"(order + 1) : "memory");
@@ -222,49 +211,60 @@ __device__ __forceinline__ float2 pass_on(Chain& ch, const Map& mine, bool cut, 
   return in;
 }
 
-// A cluster: the warps' maps make the CTA's, the CTAs' the round's; two barriers a round.  The CTA
-// is number `rank_order` of `ranks` along the walk; `carry`, the state before the round, is
-// advanced past it.  Returns the state before the warp's tokens.
-template <bool RESET>
-__device__ __forceinline__ float2 exchange(Maps& ex, int flip, const Map& mine, bool cut, int order,
-                                           uint32_t rank_order, uint32_t ranks, float2& carry,
-                                           int warp, int lane) {
-  ex.warp[flip][order][lane] = pack_map(mine);
-  if (RESET && lane == 0) ex.warp_cut[flip][order] = cut;
-  __syncthreads();
-  Map all = {splat(1.f), splat(0.f)}, before = all;
-  bool all_cut = false, before_cut = false;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == order) {
-      before = all;
-      before_cut = all_cut;
-    }
-    const Map m = unpack_map(ex.warp[flip][w][lane]);
-    const bool c = RESET && ex.warp_cut[flip][w];
-    all.B = apply(m, all.B, c);
-    all.A = mul2(m.A, all.A);
-    all_cut |= c;
-  }
-  if (warp < (int)ranks) {  // warp q tells CTA q
-    remote_store(smem_addr(&ex.cta[flip][rank_order][lane]), (uint32_t)warp, pack_map(all));
-    if (RESET && lane == 0)
-      remote_store(smem_addr(&ex.cta_cut[flip][rank_order]), (uint32_t)warp, (uint32_t)all_cut);
-  }
-  cluster_arrive();
-  cluster_wait();
-  float2 in = carry;
-  for (uint32_t q = 0; q < ranks; ++q) {
-    if (q == rank_order) in = carry;
-    carry = apply(unpack_map(ex.cta[flip][q][lane]), carry, RESET && ex.cta_cut[flip][q]);
-  }
-  return apply(before, in, before_cut);
+// The workspace of a split: the parts' maps, each CTA's eight as one, which hold a reset, and the
+// state that the sequence starts from (a copy: the walk may write the new one in its place).
+struct SplitMaps {
+  float4* part;
+  float4* cta;
+  float2* start;
+  uint32_t* part_cut;
+  uint32_t* cta_cut;
+};
+__host__ __device__ __forceinline__ SplitMaps split_maps(void* p, int64_t items, int split) {
+  const int64_t n = items * split;
+  SplitMaps m;
+  m.part = static_cast<float4*>(p);
+  m.cta = m.part + n * kWarps * kLanes;
+  m.start = reinterpret_cast<float2*>(m.cta + n * kLanes);
+  m.part_cut = reinterpret_cast<uint32_t*>(m.start + items * kLanes);
+  m.cta_cut = m.part_cut + n * kWarps;
+  return m;
+}
+size_t split_bytes(int64_t items, int split) {
+  return split ? (size_t)(items * split) * (kWarps + 1) * (kLanes * sizeof(float4) + sizeof(uint32_t)) +
+                     (size_t)items * kLanes * sizeof(float2)
+               : 0;
+}
+__device__ __forceinline__ float4 pack_map(const Map& m) {
+  return make_float4(m.A.x, m.A.y, m.B.x, m.B.y);
+}
+__device__ __forceinline__ Map unpack_map(float4 v) {
+  return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
 
-#ifndef KS
-#define KS 3
-#endif
-constexpr int kStages = KS;
+// What the maps before a warp's part make of the start; BACK: before means later in the sequence.
+template <bool RESET, bool BACK>
+__device__ __forceinline__ float2 start_of(const GlrArgs& a, int warp, int lane) {
+  const int64_t items = gridDim.x / (uint32_t)a.split, cta0 = blockIdx.x / (uint32_t)a.split * a.split;
+  const SplitMaps m = split_maps(a.maps, items, a.split);
+  const int mine = (int)(blockIdx.x % (uint32_t)a.split);
+  float2 h = m.start[blockIdx.x / (uint32_t)a.split * kLanes + lane];
+  const int n = BACK ? a.split - 1 - mine : mine;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const int64_t c = cta0 + (BACK ? a.split - 1 - i : i);
+    h = apply(unpack_map(m.cta[c * kLanes + lane]), h, RESET && m.cta_cut[c]);
+  }
+  const int w = BACK ? kWarps - 1 - warp : warp;
+#pragma unroll
+  for (int i = 0; i < kWarps - 1; ++i) {
+    if (i < w) {
+      const int64_t p = (cta0 + mine) * kWarps + (BACK ? kWarps - 1 - i : i);
+      h = apply(unpack_map(m.part[p * kLanes + lane]), h, RESET && m.part_cut[p]);
+    }
+  }
+  return h;
+}
 
 // Shared memory of `stages` stages of `tensors` runs a warp.
 template <typename T>
@@ -272,44 +272,146 @@ constexpr int ring_bytes(int tensors, int stages) {
   return stages * kWarps * tensors * kRun<T> * kGroup * (int)sizeof(T);
 }
 
-template <typename T, int MODE, bool RESET, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * kLanes, KB) glr_fwd_kernel(GlrArgs a) {
-  constexpr int run = kRun<T>, tile = kWarps * run;
+constexpr int kStages = 3;
+
+// Channels d and d + 1 of a (b, D) state that may not be there.
+__device__ __forceinline__ float2 state_at(const float* state, int64_t b, int64_t d, int64_t D) {
+  float2 v = splat(0.f);
+  if (state && d < D) v.x = state[b * D + d];
+  if (state && d + 1 < D) v.y = state[b * D + d + 1];
+  return v;
+}
+
+// The map of every part of a split: of the forward (BACK: of the backward, from the end on).
+template <typename T, int MODE, bool RESET, bool BACK>
+__global__ void __launch_bounds__(kWarps * kLanes, 2)
+glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
+  constexpr int run = kRun<T>, kTensors = BACK ? 2 : 3;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ typename std::conditional<CLUSTER, Maps, Chain>::type ex;
+  __shared__ float4 maps[kWarps][kLanes];
+  __shared__ uint32_t cut_of[kWarps];
+  cudaTriggerProgrammaticLaunchCompletion();  // the walk may begin to load; it waits itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CLUSTER ? cluster_rank() : 0, ranks = CLUSTER ? cluster_size() : 1;
-  const int64_t groups = (a.D + kGroup - 1) / kGroup, item = blockIdx.x / ranks;
-  const int64_t b = item / groups, d0 = item % groups * kGroup, d = d0 + 2 * lane;
+  const Way<T, true> way(a, warp);
+  const int64_t d0 = way.d0, d = d0 + 2 * lane;
   const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L;
-  const bool in0 = d < a.D, in1 = d + 1 < a.D;
-  const int len = a.lengths ? min(max(a.lengths[b], 0), L) : L;
-  const int step = (int)ranks * tile;  // tokens of a round
-  int t0 = (int)rank * tile;           // the CTA's first one
-  const int64_t row = b * a.L + t0;
-  Copier<T, MODE> src[3];
-  src[0].init(a.x, row, d0, a.ldx, warp, lane);
-  src[1].init(a.r, row, d0, a.ldr, warp, lane);
-  src[2].init(a.i, row, d0, a.ldi, warp, lane);
-  T* y = static_cast<T*>(a.y) + row * a.D + d0;
-  const uint32_t D = (uint32_t)a.D, at = warp * run * D + 2 * lane;  // of the warp's first output
-  const uint8_t* const reset = RESET ? a.reset + b * a.L : nullptr;
-  const bool whole = a.D % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * sizeof(T)) == 0;
+  const int len = a.lengths ? min(max(a.lengths[way.b], 0), L) : L;
+  const int step = BACK ? -way.step : way.step;
+  int t = way.first_row + (BACK ? (way.rounds - 1) * way.step : 0);
+  const int64_t row = way.b * a.L + t;
+  Copier<T, MODE> src[kTensors];
+  src[0].init(a.r, row, 0, d0, a.ldr, lane);
+  src[1].init(BACK ? dy : a.x, row, 0, d0, BACK ? a.D : a.ldx, lane);
+  if constexpr (!BACK) src[kTensors - 1].init(a.i, row, 0, d0, a.ldi, lane);
+  const uint8_t* const reset = RESET ? a.reset + way.b * a.L : nullptr;
+  T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
+  auto stage = [&](int k) { return ring + k * (kWarps * kTensors * run * kGroup); };
+  auto fetch = [&](int k, int t, bool on) {
+    const int hi = on ? len - t : 0;
+    if (hi >= run && left == kGroup) {
+#pragma unroll
+      for (int j = 0; j < kTensors; ++j) src[j].copy_all(stage(k) + j * run * kGroup, lane);
+    } else if (hi > 0) {
+#pragma unroll
+      for (int j = 0; j < kTensors; ++j)
+        src[j].copy_some(stage(k) + j * run * kGroup, 0, hi, left, lane);
+    }
+#pragma unroll
+    for (int j = 0; j < kTensors; ++j) src[j].base += step * src[j].ld;
+    copies_end();
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) fetch(k, t + k * step, k < way.rounds);
   Channel ch;
   channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
-  float2 carry = splat(0.f);
-  if (a.h0) {
-    if (in0) carry.x = a.h0[b * a.D + d];
-    if (in1) carry.y = a.h0[b * a.D + d + 1];
+  Map m = {splat(1.f), splat(0.f)};
+  bool any = false;
+  int k = 0;
+  for (int round = 0; round < way.rounds; ++round, t += step) {
+    copies_wait<kStages - 2>();
+    __syncwarp();
+    fetch(k == 0 ? kStages - 1 : k - 1, t + (kStages - 1) * step, round + kStages - 1 < way.rounds);
+    const T* const st = stage(k) + 2 * lane;
+    k = k == kStages - 1 ? 0 : k + 1;
+    const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    any |= cuts != 0;
+    auto compose = [&](int j) {
+      const bool cut = RESET && (cuts >> j & 1);
+      const float2 r = pair_of(st + j * kGroup), v = pair_of(st + (run + j) * kGroup);
+      if constexpr (BACK) {
+        const float2 al = decay(ch, r, cut);
+        m.B = cut ? splat(0.f) : mul2(al, add2(m.B, v));
+        m.A = cut ? splat(0.f) : mul2(al, m.A);
+      } else {
+        Map e;
+        element(ch, v, r, pair_of(st + ((kTensors - 1) * run + j) * kGroup), cut, e.A, e.B);
+        m.B = apply(e, m.B, cut);
+        m.A = cut ? splat(0.f) : mul2(e.A, m.A);
+      }
+    };
+    if (t + run <= len) {
+#pragma unroll
+      for (int j = 0; j < run; ++j) compose(BACK ? run - 1 - j : j);
+    } else {
+#pragma unroll
+      for (int q = 0; q < run; ++q) {
+        const int j = BACK ? run - 1 - q : q;
+        if (t + j < len) compose(j);
+      }
+    }
   }
-  if constexpr (!CLUSTER) {
-    if (warp == 0) ex.state[0][lane] = carry;
+  maps[warp][lane] = pack_map(m);
+  if (lane == 0) cut_of[warp] = any;
+  const SplitMaps out = split_maps(a.maps, gridDim.x / (uint32_t)a.split, a.split);
+  const int64_t cta = blockIdx.x;
+  out.part[(cta * kWarps + warp) * kLanes + lane] = pack_map(m);
+  if (lane == 0) out.part_cut[cta * kWarps + warp] = any;
+  if (warp == 1 && blockIdx.x % (uint32_t)a.split == 0)
+    out.start[blockIdx.x / (uint32_t)a.split * kLanes + lane] = state_at(start, way.b, d, a.D);
+  __syncthreads();
+  if (warp == 0) {
+    Map all = {splat(1.f), splat(0.f)};
+    bool all_cut = false;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int w = BACK ? kWarps - 1 - i : i;
+      const Map one = unpack_map(maps[w][lane]);
+      const bool c = RESET && cut_of[w];
+      all.B = apply(one, all.B, c);
+      all.A = mul2(one.A, all.A);
+      all_cut |= c;
+    }
+    out.cta[cta * kLanes + lane] = pack_map(all);
+    if (lane == 0) out.cta_cut[cta] = all_cut;
   }
+}
+
+template <typename T, int MODE, bool RESET, bool SPLIT>
+__global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) {
+  constexpr int run = kRun<T>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ Chain chain;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Way<T, SPLIT> way(a, warp);
+  const int64_t b = way.b, d0 = way.d0, d = d0 + 2 * lane;
+  const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L, step = way.step;
+  const bool in0 = d < a.D, in1 = d + 1 < a.D;
+  const int len = a.lengths ? min(max(a.lengths[b], 0), L) : L;
+  const int64_t row = b * a.L + way.first_row;
+  Copier<T, MODE> src[3];
+  src[0].init(a.x, row, way.ahead, d0, a.ldx, lane);
+  src[1].init(a.r, row, way.ahead, d0, a.ldr, lane);
+  src[2].init(a.i, row, way.ahead, d0, a.ldi, lane);
+  T* y = static_cast<T*>(a.y) + row * a.D + d0;
+  const uint32_t D = (uint32_t)a.D, at = way.ahead * D + 2 * lane;  // of the warp's first output
+  const uint8_t* const reset = RESET ? a.reset + b * a.L : nullptr;
+  const bool whole = a.D % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * sizeof(T)) == 0;
+  if (!SPLIT && warp == 0) chain.state[0][lane] = state_at(a.h0, b, d, a.D);
 
   T* const ring = reinterpret_cast<T*>(smem) + warp * 3 * run * kGroup;
   auto stage = [&](int k) { return ring + k * (kWarps * 3 * run * kGroup); };
-  auto fetch = [&](int k, int t) {  // the tile whose first token is t
-    const int hi = len - t - warp * run;
+  auto fetch = [&](int k, int t, bool on) {  // the run whose first token is t
+    const int hi = on ? len - t : 0;
     if (hi >= run && left == kGroup) {
 #pragma unroll
       for (int j = 0; j < 3; ++j) src[j].copy_all(stage(k) + j * run * kGroup, lane);
@@ -321,71 +423,78 @@ __global__ void __launch_bounds__(kWarps * kLanes, KB) glr_fwd_kernel(GlrArgs a)
     for (int j = 0; j < 3; ++j) src[j].base += step * src[j].ld;
     copies_end();
   };
+  int t = way.first_row + way.ahead;
 #pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) fetch(k, t0 + k * step);
+  for (int k = 0; k < kStages - 1; ++k) fetch(k, t + k * step, k < way.rounds);
+  Channel ch;
+  channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  float2 h = splat(0.f);
+  if constexpr (SPLIT) {
+    cudaGridDependencySynchronize();  // the parts' maps are there
+    h = start_of<RESET, false>(a, warp, lane);
+  }
   int k = 0;
-  [[maybe_unused]] int flip = 0;
-  for (int done = 0; done < L; done += step, t0 += step) {
+  for (int round = 0; round < way.rounds; ++round, t += step) {
     copies_wait<kStages - 2>();
     __syncwarp();
-    fetch(k == 0 ? kStages - 1 : k - 1, t0 + (kStages - 1) * step);
+    fetch(k == 0 ? kStages - 1 : k - 1, t + (kStages - 1) * step, round + kStages - 1 < way.rounds);
     const T* const st = stage(k) + 2 * lane;
     k = k == kStages - 1 ? 0 : k + 1;
-    const int t = t0 + warp * run;
     const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    const bool full = t + run <= len;
+    // SPLIT: B is the state itself
     Map m[run];
-    if (t + run <= len) {
-#pragma unroll
-      for (int j = 0; j < run; ++j) {
-        const bool cut = RESET && (cuts >> j & 1);
-        Map e;
-        element(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
-                pair_of(st + (2 * run + j) * kGroup), cut, e.A, e.B);
+    auto compose = [&](int j, const Map& e) {
+      const bool cut = RESET && (cuts >> j & 1);
+      if constexpr (SPLIT) {
+        h = m[j].B = apply(e, h, cut);
+      } else {
         m[j].B = j ? apply(e, m[j - 1].B, cut) : e.B;
         m[j].A = !j ? e.A : cut ? splat(0.f) : mul2(e.A, m[j - 1].A);
       }
+    };
+    auto token = [&](int j) {
+      Map e;
+      element(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
+              pair_of(st + (2 * run + j) * kGroup), RESET && (cuts >> j & 1), e.A, e.B);
+      return e;
+    };
+    if (full) {
+#pragma unroll
+      for (int j = 0; j < run; ++j) compose(j, token(j));
     } else {  // the last tokens: past them the state stays
 #pragma unroll
-      for (int j = 0; j < run; ++j) {
-        const bool cut = RESET && (cuts >> j & 1);
-        Map e = {splat(1.f), splat(0.f)};
-        if (t + j < len)
-          element(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
-                  pair_of(st + (2 * run + j) * kGroup), cut, e.A, e.B);
-        m[j].B = j ? apply(e, m[j - 1].B, cut) : e.B;
-        m[j].A = !j ? e.A : cut ? splat(0.f) : mul2(e.A, m[j - 1].A);
-      }
+      for (int j = 0; j < run; ++j)
+        compose(j, t + j < len ? token(j) : Map{splat(1.f), splat(0.f)});
     }
     float2 in;
-    if constexpr (CLUSTER)
-      in = exchange<RESET>(ex, flip, m[run - 1], cuts != 0, warp, rank, ranks, carry, warp, lane);
-    else
-      in = pass_on(ex, m[run - 1], cuts != 0, warp, done == 0 && warp == 0,
-                   done + step >= L && warp == kWarps - 1, lane);
-    flip ^= 1;
-    if (t + run <= len && whole) {
+    if constexpr (!SPLIT)
+      in = pass_on(chain, m[run - 1], cuts != 0, warp, round == 0 && warp == 0,
+                   round == way.rounds - 1 && warp == kWarps - 1, lane);
+    auto state = [&](int j) {
+      if constexpr (SPLIT) return m[j].B;
+      return apply(m[j], in, RESET && (cuts & ((2u << j) - 1)));
+    };
+    if (full && whole) {
 #pragma unroll
-      for (int j = 0; j < run; ++j)
-        put_pair(y + (at + j * D), apply(m[j], in, RESET && (cuts & ((2u << j) - 1))), true, in0, in1);
+      for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j), true, in0, in1);
     } else {
 #pragma unroll
       for (int j = 0; j < run; ++j) {
-        const float2 h = apply(m[j], in, RESET && (cuts & ((2u << j) - 1)));
-        if (t + j < L) put_pair(y + (at + j * D), t + j < len ? h : splat(0.f), whole, in0, in1);
+        const float2 v = state(j);
+        if (t + j < L) put_pair(y + (at + j * D), t + j < len ? v : splat(0.f), whole, in0, in1);
       }
     }
     y += step * a.D;
   }
-  if constexpr (CLUSTER) {  // no CTA leaves while another may write to its shared memory
-    cluster_arrive();
-    cluster_wait();
-  } else {
+  bool mine = SPLIT ? way.rounds > 0 && way.first_row + a.part_len >= L : warp == 0;
+  if constexpr (!SPLIT) {
     __syncthreads();
-    carry = ex.state[0][lane];  // after the last warp's last tokens
+    h = chain.state[0][lane];  // after the last warp's last run
   }
-  if (a.hT && rank == 0 && warp == 0) {
-    if (in0) a.hT[b * a.D + d] = carry.x;
-    if (in1) a.hT[b * a.D + d + 1] = carry.y;
+  if (a.hT && mine) {
+    if (in0) a.hT[b * a.D + d] = h.x;
+    if (in1) a.hT[b * a.D + d + 1] = h.y;
   }
 }
 
@@ -393,29 +502,28 @@ __global__ void __launch_bounds__(kWarps * kLanes, KB) glr_fwd_kernel(GlrArgs a)
 // token maps back_t, what comes from later tokens, to back_{t-1} = a_t (back_t + dy_t).  A warp
 // first composes its run (the decays alone), and once back has reached it, walks the run again
 // with the whole gradient; recomputing the gates costs less than holding them would.
-template <typename T, typename G, int MODE, bool RESET, bool CLUSTER>
+template <typename T, typename G, int MODE, bool RESET, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs args) {
-  constexpr int run = kRun<T>, tile = kWarps * run, kTensors = 5;
+  constexpr int run = kRun<T>, kTensors = 5;
   const GlrArgs& a = args.f;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ typename std::conditional<CLUSTER, Maps, Chain>::type ex;
+  __shared__ Chain chain;
+  cudaTriggerProgrammaticLaunchCompletion();  // the sums' kernel waits itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, order = kWarps - 1 - warp;
-  const uint32_t rank = CLUSTER ? cluster_rank() : 0, ranks = CLUSTER ? cluster_size() : 1;
-  const int64_t groups = (a.D + kGroup - 1) / kGroup, item = blockIdx.x / ranks;
-  const int64_t b = item / groups, d0 = item % groups * kGroup, d = d0 + 2 * lane;
-  const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L;
+  const Way<T, SPLIT> way(a, warp);
+  const int64_t b = way.b, d0 = way.d0, d = d0 + 2 * lane;
+  const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L, step = way.step;
   const bool in0 = d < a.D, in1 = d + 1 < a.D;
   const int len = a.lengths ? min(max(a.lengths[b], 0), L) : L;
-  const int step = (int)ranks * tile, rounds = (L + step - 1) / step;
-  int t0 = (rounds - 1) * step + (int)rank * tile;
-  const int64_t row = b * a.L + t0;
+  const int t_base = way.first_row + (way.rounds - 1) * step;
+  const int64_t row = b * a.L + t_base;
   Copier<T, MODE> src[kTensors];
-  src[0].init(a.x, row, d0, a.ldx, warp, lane);
-  src[1].init(a.r, row, d0, a.ldr, warp, lane);
-  src[2].init(a.i, row, d0, a.ldi, warp, lane);
-  src[3].init(args.dy, row, d0, a.D, warp, lane);
-  src[4].init(a.y, row - 1, d0, a.D, warp, lane);  // h_{t-1}
-  const uint32_t ldg = (uint32_t)args.ldg, at = warp * run * ldg + 2 * lane;
+  src[0].init(a.x, row, way.ahead, d0, a.ldx, lane);
+  src[1].init(a.r, row, way.ahead, d0, a.ldr, lane);
+  src[2].init(a.i, row, way.ahead, d0, a.ldi, lane);
+  src[3].init(args.dy, row, way.ahead, d0, a.D, lane);
+  src[4].init(a.y, row - 1, way.ahead, d0, a.D, lane);  // h_{t-1}
+  const uint32_t ldg = (uint32_t)args.ldg, at = way.ahead * ldg + 2 * lane;
   G* out[3] = {static_cast<G*>(args.dx) + row * args.ldg + d0,
                static_cast<G*>(args.dr) + row * args.ldg + d0,
                static_cast<G*>(args.di) + row * args.ldg + d0};
@@ -423,29 +531,17 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
   const bool whole = (a.D | ldg) % 2 == 0 &&
                      (reinterpret_cast<uintptr_t>(args.dx) | reinterpret_cast<uintptr_t>(args.dr) |
                       reinterpret_cast<uintptr_t>(args.di)) % (2 * sizeof(G)) == 0;
-  Channel ch;
-  channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
-  float2 back = splat(0.f), h0 = splat(0.f);
-  if (args.dhT) {
-    if (in0) back.x = args.dhT[b * a.D + d];
-    if (in1) back.y = args.dhT[b * a.D + d + 1];
-  }
-  if (a.h0) {
-    if (in0) h0.x = a.h0[b * a.D + d];
-    if (in1) h0.y = a.h0[b * a.D + d + 1];
-  }
-  if constexpr (!CLUSTER) {
-    if (order == 0) ex.state[0][lane] = back;
-  }
+  const float2 h0 = state_at(a.h0, b, d, a.D);
+  if (!SPLIT && order == 0) chain.state[0][lane] = state_at(args.dhT, b, d, a.D);
   float2 se = splat(0.f), sr = splat(0.f), si = splat(0.f);
 
   T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
   auto stage = [&](int k) { return ring + k * (kWarps * kTensors * run * kGroup); };
-  auto fetch = [&](int k, int t) {
-    const int hi = len - t - warp * run;
-    if (t >= 0 && hi > 0) {
+  auto fetch = [&](int k, int t, bool on) {
+    const int hi = on ? len - t : 0;
+    if (hi > 0) {
       const bool all = hi >= run && left == kGroup;
-      const int lo = t == 0 && warp == 0 ? 1 : 0;  // no h before the first token
+      const int lo = t == 0 ? 1 : 0;  // no h before the first token
 #pragma unroll
       for (int j = 0; j < kTensors; ++j) {
         if (all && (j < 4 || lo == 0))
@@ -458,41 +554,43 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
     for (int j = 0; j < kTensors; ++j) src[j].base -= step * src[j].ld;
     copies_end();
   };
-  fetch(0, t0);
-  int k = 0;
-  [[maybe_unused]] int flip = 0;
-  for (int round = 0; round < rounds; ++round, t0 -= step) {
+  int t = t_base + way.ahead, k = 0;
+  fetch(0, t, way.rounds > 0);
+  Channel ch;
+  channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  float2 g = splat(0.f);  // what comes from later tokens
+  if constexpr (SPLIT) {
+    cudaGridDependencySynchronize();  // the parts' maps are there
+    g = start_of<RESET, true>(a, warp, lane);
+  }
+  for (int round = 0; round < way.rounds; ++round, t -= step) {
     copies_wait<0>();
     __syncwarp();
-    fetch(k ^ 1, t0 - step);
+    fetch(k ^ 1, t - step, round + 1 < way.rounds);
     const T* const st = stage(k) + 2 * lane;
     k ^= 1;
-    const int t = t0 + warp * run;
     const bool full = t + run <= len;
     const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
-    Map m = {splat(1.f), splat(0.f)};
-    auto compose = [&](int j) {
-      const bool cut = RESET && (cuts >> j & 1);
-      const float2 al = decay(ch, pair_of(st + (run + j) * kGroup), cut);
-      const float2 dy = pair_of(st + (3 * run + j) * kGroup);
-      m.A = cut ? splat(0.f) : mul2(al, m.A);
-      m.B = cut ? splat(0.f) : mul2(al, add2(m.B, dy));
-    };
-    if (full) {
+    if constexpr (!SPLIT) {
+      Map m = {splat(1.f), splat(0.f)};
+      auto compose = [&](int j) {
+        const bool cut = RESET && (cuts >> j & 1);
+        const float2 al = decay(ch, pair_of(st + (run + j) * kGroup), cut);
+        const float2 dy = pair_of(st + (3 * run + j) * kGroup);
+        m.A = cut ? splat(0.f) : mul2(al, m.A);
+        m.B = cut ? splat(0.f) : mul2(al, add2(m.B, dy));
+      };
+      if (full) {
 #pragma unroll
-      for (int j = run - 1; j >= 0; --j) compose(j);
-    } else {
+        for (int j = run - 1; j >= 0; --j) compose(j);
+      } else {
 #pragma unroll
-      for (int j = run - 1; j >= 0; --j)
-        if (t + j < len) compose(j);
+        for (int j = run - 1; j >= 0; --j)
+          if (t + j < len) compose(j);
+      }
+      g = pass_on(chain, m, cuts != 0, order, round == 0 && order == 0,
+                  round == way.rounds - 1 && order == kWarps - 1, lane);
     }
-    float2 g;  // what reaches the run from later tokens
-    if constexpr (CLUSTER)
-      g = exchange<RESET>(ex, flip, m, cuts != 0, order, ranks - 1 - rank, ranks, back, warp, lane);
-    else
-      g = pass_on(ex, m, cuts != 0, order, round == 0 && order == 0,
-                  round == rounds - 1 && order == kWarps - 1, lane);
-    flip ^= 1;
     const float2 first = t == 0 ? h0 : splat(0.f);
     auto finish = [&](int j, float2& dx, float2& dr, float2& di) {
       const bool cut = RESET && (cuts >> j & 1);
@@ -530,14 +628,10 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
 #pragma unroll
     for (int j = 0; j < 3; ++j) out[j] -= step * args.ldg;
   }
-  if constexpr (CLUSTER) {
-    cluster_arrive();
-    cluster_wait();
-  }
-  // the CTA's sums, the warps' in order: a row of the workspace for each sequence and rank
+  // the CTA's sums, the warps' in order, are a row of the workspace
   copies_wait<0>();
   __syncthreads();
-  if constexpr (!CLUSTER) back = ex.state[0][lane];
+  if constexpr (!SPLIT) g = chain.state[0][lane];
   float2(*red)[3][kLanes] = reinterpret_cast<float2(*)[3][kLanes]>(smem);
   red[warp][0][lane] = se;
   red[warp][1][lane] = sr;
@@ -547,13 +641,14 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
     float2 s = splat(0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) s = add2(s, red[w][warp][lane]);
-    float* const part = args.part + (3 * (b * ranks + rank) + warp) * a.D + d;
+    const int64_t slot = SPLIT ? b * a.split + blockIdx.x % (uint32_t)a.split : b;
+    float* const part = args.part + (3 * slot + warp) * a.D + d;
     if (in0) part[0] = s.x;
     if (in1) part[1] = s.y;
   }
-  if (args.dh0 && rank == 0 && warp == 0) {
-    if (in0) args.dh0[b * a.D + d] = back.x;
-    if (in1) args.dh0[b * a.D + d + 1] = back.y;
+  if (args.dh0 && way.part == 0 && warp == 0) {
+    if (in0) args.dh0[b * a.D + d] = g.x;
+    if (in1) args.dh0[b * a.D + d + 1] = g.y;
   }
 }
 
@@ -564,6 +659,7 @@ __global__ void __launch_bounds__(kThreads) glr_sum_kernel(const float* part, in
   const int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (d >= D) return;
   float s[3] = {0.f, 0.f, 0.f};
+  cudaGridDependencySynchronize();  // launched before the backward's end: its sums are there
   for (int64_t p = 0; p < parts; ++p)
 #pragma unroll
     for (int j = 0; j < 3; ++j) s[j] += part[(3 * p + j) * D + d];
@@ -600,40 +696,52 @@ Copy copy_of(std::initializer_list<const void*> ps, std::initializer_list<int64_
   return bits % 16 == 0 ? kCopy16 : bits % 4 == 0 ? kCopy4 : kCopyElem;
 }
 
-// CTAs along a sequence: as many (a power of two) as two an SM hold, each with two tiles or more.
-int ranks_of(int64_t items, int64_t tiles) {
+// How many CTAs share a sequence's tokens, a part a warp (0: one walks its tiles): as many as fill two
+// places an SM where the walks alone would leave half of them idle and there are tokens enough.
+int split_of(int64_t items, int64_t L, int run) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
-  int r = 1;
-  while (r < kMaxCluster && items * r * 2 <= sms * 2 && tiles >= 4 * r) r *= 2;
-  return r;
+  const int64_t room = items > 0 ? 2 * sms / items : 0, most = L / (2 * run * kWarps);
+  const int64_t n = room < most ? room : most;
+  return n >= 2 ? (int)n : 0;
 }
+// Tokens of a part, whole runs.
+int part_len_of(int64_t L, int split, int run) {
+  const int64_t parts = (int64_t)split * kWarps, n = (L + parts - 1) / parts;
+  return (int)((n + run - 1) / run * run);
+}
+int run_of(bool bf16) { return bf16 ? kRun<__nv_bfloat16> : kRun<float>; }
+int64_t items_of(int64_t b, int64_t D) { return b * ((D + kGroup - 1) / kGroup); }
 
-template <typename K, typename A>
-cudaError_t launch(K kernel, const A& args, unsigned grid, int ranks, int smem, cudaStream_t s) {
+// `early`: the kernel may begin before the one before it in the stream ends; it waits itself.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, bool early,
+                   cudaStream_t s, A... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid * (unsigned)ranks);
-  cfg.blockDim = dim3(kWarps * kLanes);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cfg.attrs = at;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, args);
+  cfg.numAttrs = early ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
+constexpr int kCta = kWarps * kLanes;
 
 template <typename T, int MODE, bool RESET>
 cudaError_t fwd_m(const GlrArgs& a, cudaStream_t s) {
-  const int64_t items = a.b * ((a.D + kGroup - 1) / kGroup);
-  const int ranks = ranks_of(items, (a.L + kWarps * kRun<T> - 1) / (kWarps * kRun<T>));
-  const unsigned grid = (unsigned)items;
-  return ranks > 1 ? launch(glr_fwd_kernel<T, MODE, RESET, true>, a, grid, ranks, ring_bytes<T>(3, kStages), s)
-                   : launch(glr_fwd_kernel<T, MODE, RESET, false>, a, grid, 1, ring_bytes<T>(3, kStages), s);
+  const int64_t items = items_of(a.b, a.D);
+  const int smem = ring_bytes<T>(3, kStages);
+  if (!a.split) return launch(glr_fwd_kernel<T, MODE, RESET, false>, items, kCta, smem, false, s, a);
+  const cudaError_t e = launch(glr_part_kernel<T, MODE, RESET, false>, items * a.split, kCta,
+                               smem, false, s, a, (const void*)nullptr, a.h0);
+  if (e != cudaSuccess) return e;
+  return launch(glr_fwd_kernel<T, MODE, RESET, true>, items * a.split, kCta, smem, true, s, a);
 }
 template <typename T, int MODE>
 cudaError_t fwd_r(const GlrArgs& a, cudaStream_t s) {
@@ -650,18 +758,16 @@ cudaError_t fwd_t(const GlrArgs& a, cudaStream_t s) {
   }
 }
 
-int bwd_ranks(int64_t b, int64_t L, int64_t D, bool bf16) {
-  const int tile = kWarps * (bf16 ? kRun<__nv_bfloat16> : kRun<float>);
-  return ranks_of(b * ((D + kGroup - 1) / kGroup), (L + tile - 1) / tile);
-}
-
 template <typename T, typename G, int MODE, bool RESET>
 cudaError_t bwd_m(const GlrBwdArgs& a, cudaStream_t s) {
   const GlrArgs& f = a.f;
-  const unsigned grid = (unsigned)(f.b * ((f.D + kGroup - 1) / kGroup));
-  const int ranks = bwd_ranks(f.b, f.L, f.D, f.bf16), smem = ring_bytes<T>(5, 2);
-  return ranks > 1 ? launch(glr_bwd_kernel<T, G, MODE, RESET, true>, a, grid, ranks, smem, s)
-                   : launch(glr_bwd_kernel<T, G, MODE, RESET, false>, a, grid, 1, smem, s);
+  const int64_t items = items_of(f.b, f.D);
+  const int smem = ring_bytes<T>(5, 2);
+  if (!f.split) return launch(glr_bwd_kernel<T, G, MODE, RESET, false>, items, kCta, smem, false, s, a);
+  const cudaError_t e = launch(glr_part_kernel<T, MODE, RESET, true>, items * f.split, kCta,
+                               ring_bytes<T>(2, kStages), false, s, f, a.dy, a.dhT);
+  if (e != cudaSuccess) return e;
+  return launch(glr_bwd_kernel<T, G, MODE, RESET, true>, items * f.split, kCta, smem, true, s, a);
 }
 template <typename T, typename G, int MODE>
 cudaError_t bwd_r(const GlrBwdArgs& a, cudaStream_t s) {
@@ -679,27 +785,48 @@ cudaError_t bwd_t(const GlrBwdArgs& a, cudaStream_t s) {
   }
 }
 
+void set_split(GlrArgs& a, void* maps) {
+  a.split = split_of(items_of(a.b, a.D), a.L, run_of(a.bf16));
+  a.part_len = a.split ? part_len_of(a.L, a.split, run_of(a.bf16)) : 0;
+  a.maps = maps;
+}
+// The backward's workspace: the split's maps, then the partial sums.
+size_t al256(size_t n) { return (n + 255) / 256 * 256; }
+
 }  // namespace
 
-cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s) {
+size_t glr_fwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
+  const int64_t items = items_of(b, D);
+  return split_bytes(items, split_of(items, L, run_of(bf16)));
+}
+
+cudaError_t launch_glr_fwd(const GlrArgs& args, void* workspace, cudaStream_t s) {
+  GlrArgs a = args;
+  set_split(a, workspace);
   return a.bf16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
 }
 
 size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
-  return (size_t)b * bwd_ranks(b, L, D, bf16) * 3 * (size_t)D * sizeof(float);
+  const int64_t items = items_of(b, D);
+  const int split = split_of(items, L, run_of(bf16));
+  return al256(split_bytes(items, split)) +
+         (size_t)b * (size_t)(split ? split : 1) * 3 * (size_t)D * sizeof(float);
 }
 
-cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s) {
-  const GlrArgs& f = a.f;
+cudaError_t launch_glr_bwd(const GlrBwdArgs& args, void* workspace, cudaStream_t s) {
+  GlrBwdArgs a = args;
+  GlrArgs& f = a.f;
+  set_split(f, workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                    al256(split_bytes(items_of(f.b, f.D), f.split)));
   if (f.b > 0) {
     const cudaError_t e = !f.bf16         ? bwd_t<float, float>(a, s)
                           : a.grad_bf16 ? bwd_t<__nv_bfloat16, __nv_bfloat16>(a, s)
                                         : bwd_t<__nv_bfloat16, float>(a, s);
     if (e != cudaSuccess) return e;
   }
-  glr_sum_kernel<<<grid_for(f.D), kThreads, 0, s>>>(a.part, f.b * bwd_ranks(f.b, f.L, f.D, f.bf16), f.D,
-                                                     f.rate, a.drate, a.dbias_r, a.dbias_i);
-  return cudaGetLastError();
+  return launch(glr_sum_kernel, grid_for(f.D), kThreads, 0, true, s, a.part,
+                f.b * (f.split ? f.split : 1), f.D, f.rate, a.drate, a.dbias_r, a.dbias_i);
 }
 
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s) {

@@ -311,8 +311,12 @@ struct GlrArgs {
   const int32_t* lengths;   // nullable, (b)
   void* y;                  // the backward reads it
   float* hT;                // nullable
+  // A sequence cut into parts (the launches set these): CTAs a sequence (0: it is not),
+  // tokens of a part, the parts' maps.
+  int split, part_len;
+  void* maps;
 };
-// Its backward; `part` holds glr_bwd_workspace_bytes.
+// Its backward.
 struct GlrBwdArgs {
   GlrArgs f;
   const void* dy;
@@ -326,7 +330,7 @@ struct GlrBwdArgs {
   float* dbias_r;  // nullable
   float* dbias_i;  // nullable
   float* dh0;      // nullable
-  float* part;
+  float* part;     // partial sums (the launch sets it)
 };
 // One step of b sequences; h_out may be h.
 struct GlrStepArgs {
@@ -344,9 +348,11 @@ struct GlrStepArgs {
   float* h_out;
   void* y;
 };
-cudaError_t launch_glr_fwd(const GlrArgs& a, cudaStream_t s);
+// Bytes of workspace, by the current device's SM count.
+size_t glr_fwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16);
+cudaError_t launch_glr_fwd(const GlrArgs& a, void* workspace, cudaStream_t s);
 size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16);
-cudaError_t launch_glr_bwd(const GlrBwdArgs& a, cudaStream_t s);
+cudaError_t launch_glr_bwd(const GlrBwdArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s);
 
 // Decode step (two launches: the state/outputs, then b_prev <- B_t).

@@ -69,21 +69,30 @@ m3ssd::GlrArgs glr_args(const m3ssd_glr_dims* d, const void* x, const void* r, c
 
 extern "C" {
 
+size_t m3ssd_glr_fwd_workspace_size(const m3ssd_glr_dims* dims) {
+  if (check_glr(dims, dims ? dims->seqlen : 0) != M3SSD_OK) return 0;
+  return m3ssd::glr_fwd_workspace_bytes(dims->batch, dims->seqlen, dims->width,
+                                        dims->x_dtype == M3SSD_BF16);
+}
+
 m3ssd_status m3ssd_glr_fwd(const m3ssd_glr_dims* dims, const void* x, const void* r, const void* i,
                            const float* rate, const float* bias_r, const float* bias_i,
                            const float* h0, const uint8_t* reset, const int32_t* lengths, void* y,
-                           float* hT, void* stream) {
+                           float* hT, void* workspace, size_t workspace_bytes, void* stream) {
   const m3ssd_status st = check_glr(dims, dims ? dims->seqlen : 0);
   if (st != M3SSD_OK) return st;
   if (!glr_inputs_ok(dims, x, r, i, rate, bias_r, bias_i, h0, lengths)) return M3SSD_ERR_INVALID_ARG;
   if ((dims->batch > 0 && dims->seqlen > 0 && !y) || !aligned(y, dtype_size(dims->x_dtype)) ||
       !aligned(hT, 4))
     return M3SSD_ERR_INVALID_ARG;
+  const size_t need = m3ssd_glr_fwd_workspace_size(dims);
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256))))
+    return M3SSD_ERR_WORKSPACE;
   if (dims->batch == 0) return M3SSD_OK;
   m3ssd::GlrArgs a = glr_args(dims, x, r, i, rate, bias_r, bias_i, h0, reset, lengths);
   a.y = y;
   a.hT = hT;
-  return from_cuda(m3ssd::launch_glr_fwd(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(m3ssd::launch_glr_fwd(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t m3ssd_glr_bwd_workspace_size(const m3ssd_glr_dims* dims) {
@@ -125,8 +134,7 @@ m3ssd_status m3ssd_glr_bwd(const m3ssd_glr_dims* dims, const void* x, const void
   a.dx = grads->dx; a.dr = grads->dr; a.di = grads->di;
   a.drate = grads->drate; a.dbias_r = grads->dbias_r; a.dbias_i = grads->dbias_i;
   a.dh0 = grads->dh0;
-  a.part = static_cast<float*>(workspace);
-  return from_cuda(m3ssd::launch_glr_bwd(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(m3ssd::launch_glr_bwd(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const void* r_t,

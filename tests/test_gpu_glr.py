@@ -157,7 +157,8 @@ def check_bwd(d, y, got, grad_dtype):
               grad_dtype if name in ("dx", "dr", "di") else torch.float32, name)
 
 
-# one token, ends around whole tiles, several tiles; widths around whole groups of channels
+# one token, ends around whole tiles, several tiles; widths around whole groups of channels; from
+# L = 256 on these few sequences are cut into parts
 SHAPES = [(1, 1, 1), (2, 1, 64), (1, 2, 2), (3, 7, 63), (2, 16, 65), (1, 63, 130), (2, 64, 128), (1, 65, 8),
           (2, 129, 72), (1, 300, 200), (5, 33, 4), (1, 1025, 40), (2, 517, 1)]
 
@@ -290,17 +291,19 @@ def test_a_projections_rows_are_read_in_place():
             assert (buf[..., :off] == 7).all() and (buf[..., off + 3 * D:] == 7).all()
 
 
-def test_state_in_place_and_continuation():
-    """hT may be h0's tensor, dh0 dhT's; two halves equal the whole."""
-    d = make(3, 210, 96, torch.float32, seed=13)
+@pytest.mark.parametrize("b,L,cut", [(3, 210, 100), (2, 3000, 1700)])
+def test_state_in_place_and_continuation(b, L, cut):
+    """hT may be h0's tensor, dh0 dhT's (also where few sequences are cut into parts); two pieces
+    equal the whole."""
+    d = make(b, L, 96, torch.float32, seed=13)
     c = gpu(d)
     y, hT = call(m3.glr_fwd, c)
     h = c["h0"].clone()
     half = lambda lo, hi: {k: (v[:, lo:hi].contiguous() if k in ("x", "r", "i") else v)  # noqa: E731
                            for k, v in dict(c, h0=h).items()}
-    y1, h1 = call(m3.glr_fwd, half(0, 100), hT=h)
+    y1, h1 = call(m3.glr_fwd, half(0, cut), hT=h)
     assert h1 is h
-    y2, _ = call(m3.glr_fwd, half(100, 210), hT=h)
+    y2, _ = call(m3.glr_fwd, half(cut, L), hT=h)
     hh = host(d)
     ref, refT = ly.glr_fwd(**{k: hh[k] for k in FWD if k in hh})
     ty, tT = fwd_tolerance(hh, ref, refT)

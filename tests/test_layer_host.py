@@ -26,10 +26,10 @@ def glr_dims(**kw):
 GLR_FWD = ("x", "r", "i", "rate", "bias_r", "bias_i", "h0", "reset", "lengths", "y", "hT")
 
 
-def glr_fwd(lib, dims, **kw):
+def glr_fwd(lib, dims, ws=A, nbytes=1 << 20, **kw):
     a = {n: A for n in GLR_FWD}
     a.update(kw)
-    return lib.m3ssd_glr_fwd(ctypes.byref(dims), *(a[n] for n in GLR_FWD), None)
+    return lib.m3ssd_glr_fwd(ctypes.byref(dims), *(a[n] for n in GLR_FWD), ws, nbytes, None)
 
 
 def glr_bwd(lib, dims, grads=None, ws=A, nbytes=1 << 20, **kw):
@@ -100,6 +100,12 @@ def test_glr_rejects_bad_gradients_and_workspaces(lib):
     assert glr_bwd(lib, d, m3.GlrGrads(6, 9, 0, *p)) == m3.ERR_INVALID_ARG
     assert glr_bwd(lib, d, m3.GlrGrads(6, m3.F32, 1, *p)) == m3.ERR_INVALID_ARG
     assert glr_bwd(lib, d, m3.GlrGrads(6, m3.BF16, 0, *p)) == m3.ERR_UNSUPPORTED  # fp32 inputs
+    long = glr_dims(batch=1, seqlen=4096)  # few sequences: cut into parts
+    need = lib.m3ssd_glr_fwd_workspace_size(ctypes.byref(long))
+    assert need > 0 and lib.m3ssd_glr_fwd_workspace_size(ctypes.byref(d)) == 0
+    assert glr_fwd(lib, long, nbytes=need - 1) == m3.ERR_WORKSPACE
+    assert glr_fwd(lib, long, ws=None) == m3.ERR_WORKSPACE
+    assert glr_fwd(lib, long, ws=P(0x10010)) == m3.ERR_WORKSPACE
     need = lib.m3ssd_glr_bwd_workspace_size(ctypes.byref(d))
     assert need > 0
     assert glr_bwd(lib, d, nbytes=need - 1) == m3.ERR_WORKSPACE
