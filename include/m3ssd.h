@@ -647,6 +647,71 @@ m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const v
                             const float* bias_i, const float* h, float* h_out, void* y_t,
                             void* stream);
 
+/*
+ * Queries and keys, the scan's C and B: the root-mean-square norm of every head with the
+ * rotation by position in the same pass ("VikramLex/mamba3-minimal" README, "Architecture": B, C:
+ * QK-norm, then RoPE).  Of every token (row) and head, over the head's `width` values:
+ *     rstd = 1 / sqrt(mean u^2 + eps),   v = u rstd w,
+ *     pair i (components 2i, 2i + 1) of the output = R(position freqs[i]) (pair i of v), i < pairs,
+ * the other components v, computed in fp32 (the angle's turns in fp64) and rounded once to
+ * x_dtype.  With its outputs as C and B, m3ssd_fwd and m3ssd_step run without theta.
+ */
+typedef struct {
+  int64_t rows;       /* tokens, >= 0 */
+  int64_t q_heads;    /* >= 1 */
+  int64_t k_heads;    /* >= 0 (0: queries alone) */
+  int64_t width;      /* 2 .. 256, even */
+  int64_t pairs;      /* rotated pairs, 0 .. width / 2 */
+  int64_t ldq;        /* elements from a token's queries to the next one's, >= q_heads width: */
+  int64_t ldk;        /*   q and k may be column ranges of a projection's rows; keys alike */
+  int32_t x_dtype;    /* m3ssd_dtype of q, k and the outputs */
+  float eps;          /* >= 0 */
+  uint32_t reserved;  /* must be 0 */
+} m3ssd_rotate_dims;
+
+/*
+ * Forward.  q (rows, q_heads, width), k (rows, k_heads, width); q_w, k_w (width) fp32, NULL = 1;
+ * positions (rows) int32, any sign; freqs (pairs) fp32, radians a position (both may be NULL where
+ * pairs is 0).  q_out, k_out: dense; they may be q and k where those are dense.  width up to 256,
+ * heads up to 65535, rows and strides up to 2^31 - 1 (else M3SSD_ERR_UNSUPPORTED).  No
+ * allocation, no synchronisation.
+ */
+m3ssd_status m3ssd_norm_rotate(const m3ssd_rotate_dims* dims, const void* q, const void* k,
+                               const float* q_w, const float* k_w, const int32_t* positions,
+                               const float* freqs, void* q_out, void* k_out, void* stream);
+
+/* Gradients: dq, dk in `dtype` (fp32, or bf16 where x_dtype is), their rows ldq and ldk elements
+ * apart; dq_w, dk_w (width) fp32, may be NULL. */
+typedef struct {
+  int64_t ldq;
+  int64_t ldk;
+  int32_t dtype;      /* m3ssd_dtype */
+  uint32_t reserved;  /* must be 0 */
+  void* dq;
+  void* dk;
+  float* dq_w;
+  float* dk_w;
+} m3ssd_rotate_grads;
+
+/* Bytes of device workspace m3ssd_norm_rotate_bwd needs on the current device (it depends on the
+ * SM count); 0 for invalid dims. */
+size_t m3ssd_norm_rotate_bwd_workspace_size(const m3ssd_rotate_dims* dims);
+
+/*
+ * Its backward, from the forward's inputs and the gradients dq_out, dk_out of its outputs (dense, in
+ * up_dtype: fp32 as m3ssd_bwd writes dC and dB, or bf16 where x_dtype is).  With dv = R(-position
+ * freqs[i]) d, g = w dv, uh = u rstd and means over the head:
+ *     du = rstd (g - uh mean(g uh)),   dw = sum over tokens and heads of dv uh.
+ * Sums run in a fixed order: the same call gives the same bits.  dq and dk overlap no input, but may
+ * be dq_out and dk_out where types and strides agree.  workspace: 256-byte aligned, not read
+ * afterwards.
+ */
+m3ssd_status m3ssd_norm_rotate_bwd(const m3ssd_rotate_dims* dims, const void* q, const void* k,
+                                   const float* q_w, const float* k_w, const int32_t* positions,
+                                   const float* freqs, int32_t up_dtype, const void* dq_out,
+                                   const void* dk_out, const m3ssd_rotate_grads* grads,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Number of bounded device-side waits of the chunked forwards (SISO and
  * MIMO), the tensor-core backward, the GEMMs and the 8-bit step that ran out since
  * the last call (a forward's CTA then stops and leaves its outputs unwritten, a step's those

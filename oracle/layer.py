@@ -1,7 +1,8 @@
 """fp64 oracle of the operators that a layer has around the scan: plain numpy, written
 from their definitions (include/m3ssd.h), sharing no code with the library.
 
-The gated linear recurrence walks token by token, forward and in reverse.
+The gated linear recurrence walks token by token, forward and in reverse.  The heads' norm with
+its rotation is written with complex pairs.
 """
 from __future__ import annotations
 
@@ -74,3 +75,36 @@ def glr_bwd(x, r, i, rate, y, dy, bias_r=None, bias_i=None, c=8.0, h0=None, rese
     o["drate"] = o["E"].sum((0, 1)) * slope
     o["dbias_r"], o["dbias_i"], o["dh0"] = o["dr"].sum((0, 1)), o["di"].sum((0, 1)), back
     return o
+
+
+def _turn(positions, freqs, N, sign):
+    """exp(i sign angle) of every (token, pair), 1 past the rotated ones; angles in long double."""
+    if positions is None:
+        return np.ones((1, 1, N // 2))
+    rows = len(positions)
+    ang = np.asarray(positions, np.longdouble)[:, None] * np.asarray(freqs, np.longdouble)[None]
+    whole = 2 * np.longdouble("3.14159265358979323846264338327950288")
+    ang = np.asarray(np.remainder(ang, whole), np.float64)
+    z = np.ones((rows, 1, N // 2), complex)
+    z[:, 0, :ang.shape[1]] = np.exp(1j * sign * ang)
+    return z
+
+
+def _turned(v, z):
+    p = v.reshape(*v.shape[:-1], -1, 2)
+    c = (p[..., 0] + 1j * p[..., 1]) * z
+    return np.stack((c.real, c.imag), -1).reshape(v.shape)
+
+
+def norm_rotate(u, w, positions, freqs, eps):
+    """u (rows, H, N) -> its normed, weighted and rotated heads."""
+    v = u / np.sqrt((u * u).mean(-1, keepdims=True) + eps) * (1.0 if w is None else w)
+    return _turned(v, _turn(positions, freqs, u.shape[-1], 1))
+
+
+def norm_rotate_bwd(u, w, d, positions, freqs, eps):
+    """(du, dw) from the gradient d of the output."""
+    rstd = 1 / np.sqrt((u * u).mean(-1, keepdims=True) + eps)
+    dv, uh = _turned(d, _turn(positions, freqs, u.shape[-1], -1)), u * rstd
+    g = dv * (1.0 if w is None else w)
+    return rstd * (g - uh * (g * uh).mean(-1, keepdims=True)), (dv * uh).sum((0, 1))

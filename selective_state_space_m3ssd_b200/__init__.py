@@ -97,6 +97,18 @@ class GlrGrads(ctypes.Structure):
         [(n, ctypes.c_void_p) for n in GLR_GRAD_NAMES]
 
 
+class RotateDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("rows", "q_heads", "k_heads", "width", "pairs", "ldq", "ldk")] + \
+        [("x_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_uint32)]
+
+
+class RotateGrads(ctypes.Structure):
+    _fields_ = [("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_uint32)] + \
+        [(n, ctypes.c_void_p) for n in ("dq", "dk", "dq_w", "dk_w")]
+
+
 class BlockDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("batch", "seqlen", "d_model", "nheads", "headdim", "dstate", "ngroups")]
@@ -215,6 +227,14 @@ def load(path: str | None = None):
         lib.m3ssd_glr_bwd.restype = ctypes.c_int
         lib.m3ssd_glr_step.argtypes = [gdp] + [vp] * 10
         lib.m3ssd_glr_step.restype = ctypes.c_int
+        rdp = ctypes.POINTER(RotateDims)
+        lib.m3ssd_norm_rotate.argtypes = [rdp] + [vp] * 9
+        lib.m3ssd_norm_rotate.restype = ctypes.c_int
+        lib.m3ssd_norm_rotate_bwd_workspace_size.argtypes = [rdp]
+        lib.m3ssd_norm_rotate_bwd_workspace_size.restype = sz
+        lib.m3ssd_norm_rotate_bwd.argtypes = [rdp] + [vp] * 6 + \
+            [i32, vp, vp, ctypes.POINTER(RotateGrads), vp, sz, vp]
+        lib.m3ssd_norm_rotate_bwd.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -1056,20 +1076,25 @@ def step_q8(cache: dict, x_t, logdecay_t, beta_t, gamma_t, B_t, C_t, theta_t=Non
 
 # ---- the gated linear recurrence ---------------------------------------------------------
 
-def _tokens_stride(t, name, dtype, lead, width, index):
-    """A tensor (*lead, width) on CUDA device ``index`` whose tokens are rows of unit column
-    stride a fixed distance apart; returns that distance."""
-    if t.dtype != dtype or t.shape != (*lead, width):
-        _need_shape(t, name, dtype, (*lead, width))
+def _tokens_stride(t, name, dtype, lead, inner, index):
+    """A tensor (*lead, *inner) on CUDA device ``index`` whose tokens (lead) are dense runs of
+    the inner axes a fixed distance apart; returns that distance in elements."""
+    if t.dtype != dtype or t.shape != (*lead, *inner):
+        _need_shape(t, name, dtype, (*lead, *inner))
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, expected a CUDA tensor on cuda:{index}")
+    width = 1
+    for n in inner:
+        width *= n
     if t.is_contiguous():
         return width
-    stride, rows = t.stride(), 1
-    if width > 1 and stride[-1] != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    ld = None  # from the innermost axis longer than one
-    for n, st in zip(reversed(lead), reversed(stride[:-1])):
+    stride, run = t.stride(), 1
+    for n, st in zip(reversed(inner), reversed(stride)):
+        if n > 1 and st != run:
+            raise ValueError(f"{name}'s tokens must be contiguous")
+        run *= n
+    ld, rows = None, 1  # from the innermost axis of tokens longer than one
+    for n, st in zip(reversed(lead), reversed(stride[:len(lead)])):
         if n > 1:
             if ld is None:
                 ld = st // rows
@@ -1093,7 +1118,7 @@ def _glr_dims(x, r, i, rate, bias_r, bias_i, c):
     f32, dev, index = torch.float32, x.device, x.get_device()
     lead, D = x.shape[:-1], x.shape[-1]
     xd = _xdtype(x)
-    ld = [_tokens_stride(t, n, x.dtype, lead, D, index) for t, n in ((x, "x"), (r, "r"), (i, "i"))]
+    ld = [_tokens_stride(t, n, x.dtype, lead, (D,), index) for t, n in ((x, "x"), (r, "r"), (i, "i"))]
     if rate is None:
         raise ValueError("rate is required")
     _need_all(dev, (rate, "rate", f32, (D,)), (bias_r, "bias_r", f32, (D,)),
@@ -1171,7 +1196,7 @@ def glr_bwd(x, r, i, rate, y, dy, *, bias_r=None, bias_i=None, c: float = 8.0, h
             grads[k] = torch.empty(shape, dtype=f32, device=dev)
         else:
             _need(grads[k], k, f32, shape, dev)
-    lds = {_tokens_stride(grads[k], k, grad_dtype, (b, L), D, dev.index) for k in ("dx", "dr", "di")}
+    lds = {_tokens_stride(grads[k], k, grad_dtype, (b, L), (D,), dev.index) for k in ("dx", "dr", "di")}
     if len(lds) != 1 and b * L > 1:
         raise ValueError("dx, dr and di must have their rows the same distance apart")
     g = GlrGrads(max(lds), _xdtype(grads["dx"]), 0, *(grads[k].data_ptr() for k in GLR_GRAD_NAMES))
@@ -1202,6 +1227,99 @@ def glr_step(h, x_t, r_t, i_t, rate, *, bias_r=None, bias_i=None, c: float = 8.0
     _launch("m3ssd_glr_step", dev, ctypes.byref(dims), _addr(x_t), _addr(r_t), _addr(i_t),
             _addr(rate), _addr(bias_r), _addr(bias_i), _addr(h), _addr(h_out), _addr(y_t))
     return y_t, h_out
+
+
+# ---- the norm of heads with their rotation -------------------------------------------------
+
+def _rotate_dims(q, k, q_w, k_w, positions, freqs, eps):
+    """Checks what the two calls share; their dims, and the tokens' axes."""
+    import torch
+    if q.dim() < 2 or (k is not None and k.dim() != q.dim()):
+        raise ValueError("q and k must have shapes (..., heads, width), with the same tokens")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    f32, dev, index = torch.float32, q.device, q.get_device()
+    lead, (Hq, N) = q.shape[:-2], q.shape[-2:]
+    xd = _xdtype(q)
+    ldq = _tokens_stride(q, "q", q.dtype, lead, (Hq, N), index)
+    Hk = 0 if k is None else k.shape[-2]
+    ldk = 0 if k is None else _tokens_stride(k, "k", q.dtype, lead, (Hk, N), index)
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs are given together")
+    R = 0 if freqs is None else freqs.shape[0]
+    rows = 1
+    for n in lead:
+        rows *= n
+    _need_all(dev, (q_w, "q_w", f32, (N,)), (k_w, "k_w", f32, (N,)),
+              (positions, "positions", torch.int32, lead), (freqs, "freqs", f32, (R,)))
+    return RotateDims(rows, Hq, Hk, N, R, ldq, ldk, xd, eps, 0), lead
+
+
+def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, eps: float = 1e-6,
+                q_out=None, k_out=None):
+    """The RMS norm of every head of q (..., Hq, N) and k (..., Hk, N), times q_w and k_w (N, fp32,
+    None = 1), and the rotation of pair i < len(freqs) by ``positions * freqs[i]``, in one pass
+    through ``m3ssd_norm_rotate``: the scan's C and B for :func:`fwd` and :func:`step` without
+    theta.  bf16 or fp32, each token's heads dense, tokens any fixed distance apart (a column
+    range of a projection); positions int32 of the leading shape, freqs fp32 radians.  Returns
+    ``(q_out, k_out)``, dense; they may be given as q and k to write in place."""
+    import torch
+    dims, lead = _rotate_dims(q, k, q_w, k_w, positions, freqs, eps)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    _need_all(dev, (q_out, "q_out", q.dtype, q.shape))
+    if k is not None:
+        _need_all(dev, (k_out, "k_out", k.dtype, k.shape))
+    _launch("m3ssd_norm_rotate", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
+            _addr(positions), _addr(freqs), _addr(q_out), None if k is None else _addr(k_out))
+    return q_out, None if k is None else k_out
+
+
+def norm_rotate_bwd_workspace_size(dims: RotateDims) -> int:
+    """Bytes on the current device."""
+    return int(load().m3ssd_norm_rotate_bwd_workspace_size(ctypes.byref(dims)))
+
+
+def norm_rotate_bwd(q, k, q_w, k_w, dq_out, dk_out, *, positions=None, freqs=None, eps: float = 1e-6,
+                    grad_dtype=None, grads=None, workspace=None):
+    """Backward of :func:`norm_rotate` through ``m3ssd_norm_rotate_bwd``: its inputs and the
+    gradients of its outputs, dense, fp32 (as :func:`bwd` returns dC and dB) or q's type.
+    Returns a dict with dq, dk in ``grad_dtype`` (fp32 unless given as q's type) and dq_w, dk_w
+    in fp32 (dk and dk_w None without k).  ``grads`` may supply tensors, dq and dk as column
+    ranges of a projection's gradient."""
+    import torch
+    dims, lead = _rotate_dims(q, k, q_w, k_w, positions, freqs, eps)
+    dev, f32, N = q.device, torch.float32, q.shape[-1]
+    grad_dtype = grad_dtype or f32
+    if dq_out is None or (dk_out is None) != (k is None):
+        raise ValueError("the gradients of all outputs are required")
+    _need_all(dev, (dq_out, "dq_out", dq_out.dtype, q.shape))
+    if k is not None:
+        _need_all(dev, (dk_out, "dk_out", dq_out.dtype, k.shape))
+    grads = dict(grads or {})
+    for n, t in (("dq", q), ("dk", k)):
+        if t is None:
+            grads[n] = grads[n + "_w"] = None
+            continue
+        if grads.get(n) is None:
+            grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=dev)
+        if grads.get(n + "_w") is None:
+            grads[n + "_w"] = torch.empty(N, dtype=f32, device=dev)
+        else:
+            _need(grads[n + "_w"], n + "_w", f32, (N,), dev)
+    ldq = _tokens_stride(grads["dq"], "dq", grad_dtype, lead, q.shape[-2:], dev.index)
+    ldk = 0 if k is None else _tokens_stride(grads["dk"], "dk", grad_dtype, lead, k.shape[-2:], dev.index)
+    g = RotateGrads(ldq, ldk, _xdtype(grads["dq"]), 0,
+                    *(_addr(grads[n]) for n in ("dq", "dk", "dq_w", "dk_w")))
+    need = _on_device(dev, norm_rotate_bwd_workspace_size, dims)
+    workspace, ws, ws_bytes = _workspace(workspace, need, dev)
+    _launch("m3ssd_norm_rotate_bwd", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
+            _addr(positions), _addr(freqs), _xdtype(dq_out), _addr(dq_out), _addr(dk_out),
+            ctypes.byref(g), ws, ws_bytes)
+    return {n: grads[n] for n in ("dq", "dk", "dq_w", "dk_w")}
 
 
 class PreparedFwd:

@@ -355,6 +355,39 @@ size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16);
 cudaError_t launch_glr_bwd(const GlrBwdArgs& a, void* workspace, cudaStream_t s);
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s);
 
+// The norm of every head of q (rows x Hq x N) and k (rows x Hk x N) with the rotation of the first R
+// pairs by position (csrc/rotate.cu); rows of q and k at strides in elements, outputs dense.
+struct RotateArgs {
+  int64_t rows, Hq, Hk, N, R;
+  int64_t ldq, ldk;
+  bool bf16;
+  float eps;
+  const void* q;
+  const void* k;               // nullable where Hk is 0
+  const float* q_w;            // nullable (ones)
+  const float* k_w;            // nullable (ones)
+  const int32_t* positions;    // (rows); nullable where R is 0
+  const float* freqs;          // (R); nullable where R is 0
+  void* q_out;
+  void* k_out;
+  int lanes, block, blocks;    // lanes of a head, heads of a warp's block, blocks a row (set at launch)
+};
+struct RotateBwdArgs {
+  RotateArgs f;
+  bool up_bf16, grad_bf16;
+  const void* dq_out;
+  const void* dk_out;
+  int64_t ldgq, ldgk;
+  void* dq;
+  void* dk;
+  float* dq_w;  // nullable
+  float* dk_w;  // nullable
+  float* part;  // norm_rotate_bwd_workspace_bytes
+};
+cudaError_t launch_norm_rotate(const RotateArgs& a, cudaStream_t s);
+size_t norm_rotate_bwd_workspace_bytes(const RotateArgs& a);
+cudaError_t launch_norm_rotate_bwd(const RotateBwdArgs& a, cudaStream_t s);
+
 // Decode step (two launches: the state/outputs, then b_prev <- B_t).
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 

@@ -1,5 +1,5 @@
 // C-ABI entry points of the operators that a layer has around the scan: the gated linear
-// recurrence.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
+// recurrence, and the norm of heads with their rotation.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -63,6 +63,35 @@ m3ssd::GlrArgs glr_args(const m3ssd_glr_dims* d, const void* x, const void* r, c
   a.x = x; a.r = r; a.i = i; a.rate = rate; a.bias_r = bias_r; a.bias_i = bias_i;
   a.h0 = h0; a.reset = reset; a.lengths = lengths;
   return a;
+}
+
+m3ssd_status check_rotate(const m3ssd_rotate_dims* d) {
+  if (!d || d->reserved != 0) return M3SSD_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->q_heads < 1 || d->k_heads < 0 || d->width < 2 || d->width % 2 != 0 ||
+      d->pairs < 0 || d->pairs > d->width / 2)
+    return M3SSD_ERR_INVALID_ARG;
+  if (!dtype_ok(d->x_dtype) || !(d->eps >= 0.f)) return M3SSD_ERR_INVALID_ARG;
+  const int64_t most = INT32_MAX;
+  if (d->width > 256 || d->q_heads > 65535 || d->k_heads > 65535 || d->rows > most || d->ldq > most ||
+      d->ldk > most)
+    return M3SSD_ERR_UNSUPPORTED;
+  if (d->ldq < d->q_heads * d->width || d->ldk < d->k_heads * d->width) return M3SSD_ERR_INVALID_ARG;
+  return M3SSD_OK;
+}
+
+// The inputs that the forward and the backward share, into `a`; false where one is wrong.
+bool rotate_inputs(const m3ssd_rotate_dims* d, const void* q, const void* k, const float* q_w,
+                   const float* k_w, const int32_t* positions, const float* freqs,
+                   m3ssd::RotateArgs& a) {
+  const uintptr_t esz = dtype_size(d->x_dtype);
+  if (d->rows > 0 && (!q || (d->k_heads > 0 && !k) || (d->pairs > 0 && !positions))) return false;
+  if (d->pairs > 0 && !freqs) return false;
+  if (!aligned(q, esz) || !aligned(k, esz) || !all_aligned4({q_w, k_w, positions, freqs})) return false;
+  a.rows = d->rows; a.Hq = d->q_heads; a.Hk = d->k_heads; a.N = d->width; a.R = d->pairs;
+  a.ldq = d->ldq; a.ldk = d->ldk;
+  a.bf16 = d->x_dtype == M3SSD_BF16; a.eps = d->eps;
+  a.q = q; a.k = k; a.q_w = q_w; a.k_w = k_w; a.positions = positions; a.freqs = freqs;
+  return true;
 }
 
 }  // namespace
@@ -157,6 +186,62 @@ m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const v
   a.x = x_t; a.r = r_t; a.i = i_t; a.rate = rate; a.bias_r = bias_r; a.bias_i = bias_i;
   a.h = h; a.h_out = out; a.y = y_t;
   return from_cuda(m3ssd::launch_glr_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+m3ssd_status m3ssd_norm_rotate(const m3ssd_rotate_dims* dims, const void* q, const void* k,
+                               const float* q_w, const float* k_w, const int32_t* positions,
+                               const float* freqs, void* q_out, void* k_out, void* stream) {
+  const m3ssd_status st = check_rotate(dims);
+  if (st != M3SSD_OK) return st;
+  m3ssd::RotateArgs a{};
+  if (!rotate_inputs(dims, q, k, q_w, k_w, positions, freqs, a)) return M3SSD_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype_size(dims->x_dtype);
+  if (!aligned(q_out, esz) || !aligned(k_out, esz)) return M3SSD_ERR_INVALID_ARG;
+  if (dims->rows == 0) return M3SSD_OK;
+  if (!q_out || (dims->k_heads > 0 && !k_out)) return M3SSD_ERR_INVALID_ARG;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  return from_cuda(m3ssd::launch_norm_rotate(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t m3ssd_norm_rotate_bwd_workspace_size(const m3ssd_rotate_dims* dims) {
+  if (check_rotate(dims) != M3SSD_OK) return 0;
+  m3ssd::RotateArgs a{};
+  a.rows = dims->rows; a.Hq = dims->q_heads; a.Hk = dims->k_heads; a.N = dims->width;
+  return m3ssd::norm_rotate_bwd_workspace_bytes(a);
+}
+
+m3ssd_status m3ssd_norm_rotate_bwd(const m3ssd_rotate_dims* dims, const void* q, const void* k,
+                                   const float* q_w, const float* k_w, const int32_t* positions,
+                                   const float* freqs, int32_t up_dtype, const void* dq_out,
+                                   const void* dk_out, const m3ssd_rotate_grads* grads,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const m3ssd_status st = check_rotate(dims);
+  if (st != M3SSD_OK) return st;
+  if (!grads || grads->reserved != 0 || !dtype_ok(grads->dtype) || !dtype_ok(up_dtype))
+    return M3SSD_ERR_INVALID_ARG;
+  if (dims->x_dtype == M3SSD_F32 && (grads->dtype != M3SSD_F32 || up_dtype != M3SSD_F32))
+    return M3SSD_ERR_UNSUPPORTED;
+  if (grads->ldq < dims->q_heads * dims->width || grads->ldk < dims->k_heads * dims->width)
+    return M3SSD_ERR_INVALID_ARG;
+  m3ssd::RotateBwdArgs a{};
+  if (!rotate_inputs(dims, q, k, q_w, k_w, positions, freqs, a.f)) return M3SSD_ERR_INVALID_ARG;
+  const uintptr_t usz = dtype_size(up_dtype), gsz = dtype_size(grads->dtype);
+  if (!aligned(dq_out, usz) || !aligned(dk_out, usz) || !aligned(grads->dq, gsz) ||
+      !aligned(grads->dk, gsz) || !all_aligned4({grads->dq_w, grads->dk_w}))
+    return M3SSD_ERR_INVALID_ARG;
+  if (dims->rows > 0 && (!dq_out || !grads->dq || (dims->k_heads > 0 && (!dk_out || !grads->dk))))
+    return M3SSD_ERR_INVALID_ARG;
+  const size_t need = m3ssd_norm_rotate_bwd_workspace_size(dims);
+  if (workspace_bytes < need || (need > 0 && (!workspace || !aligned(workspace, 256))))
+    return M3SSD_ERR_WORKSPACE;
+  a.up_bf16 = up_dtype == M3SSD_BF16;
+  a.grad_bf16 = grads->dtype == M3SSD_BF16;
+  a.dq_out = dq_out; a.dk_out = dk_out;
+  a.ldgq = grads->ldq; a.ldgk = grads->ldk;
+  a.dq = grads->dq; a.dk = grads->dk; a.dq_w = grads->dq_w; a.dk_w = grads->dk_w;
+  a.part = static_cast<float*>(workspace);
+  return from_cuda(m3ssd::launch_norm_rotate_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -132,12 +132,99 @@ def test_glr_binding_refuses_on_the_host():
 
 def test_row_strides_of_token_tensors():
     """The binding's rule for rows a fixed distance apart (device -1 is the host)."""
-    f = lambda t, lead, w: m3._tokens_stride(t, "t", t.dtype, lead, w, -1)  # noqa: E731
+    f = lambda t, lead, *w: m3._tokens_stride(t, "t", t.dtype, lead, w, -1)  # noqa: E731
     p = torch.zeros(3, 5, 40)
     assert f(p[..., 8:16], (3, 5), 8) == 40 and f(p, (3, 5), 40) == 40
     assert f(p[:1, :, 8:16], (1, 5), 8) == 40 and f(p[:, :1, 8:16], (3, 1), 8) == 200
     assert f(p[:1, :1, 8:16], (1, 1), 8) == 8 and f(p[:, 0, 8:16], (3,), 8) == 200
+    assert f(p[..., 8:20].unflatten(-1, (3, 4)), (3, 5), 3, 4) == 40
+    assert f(p[..., 8:20].unflatten(-1, (3, 4))[..., :1, :], (3, 5), 1, 4) == 40
+    with pytest.raises(ValueError):  # a token's heads apart
+        f(p[..., 8:20].unflatten(-1, (3, 4))[..., :2], (3, 5), 3, 2)
     for bad in (p[:, :4, 8:16], p[..., ::5], p[:, :, :1].expand(3, 5, 8), p[:, ::2, :8][:, :2],
                 torch.zeros(5, 3, 8).transpose(0, 1), torch.zeros(5, 8).expand(3, 5, 8)):
         with pytest.raises(ValueError):
             f(bad, tuple(bad.shape[:-1]), 8)
+
+
+def rot_dims(**kw):
+    d = dict(rows=4, q_heads=3, k_heads=2, width=8, pairs=4, ldq=24, ldk=16, x_dtype=m3.F32, eps=1e-6,
+             reserved=0)
+    d.update(kw)
+    return m3.RotateDims(*(d[n] for n, _ in m3.RotateDims._fields_))
+
+
+ROT_IN = ("q", "k", "q_w", "k_w", "positions", "freqs")
+
+
+def rot_fwd(lib, dims, **kw):
+    a = {n: A for n in ROT_IN + ("q_out", "k_out")}
+    a.update(kw)
+    return lib.m3ssd_norm_rotate(ctypes.byref(dims), *(a[n] for n in ROT_IN + ("q_out", "k_out")), None)
+
+
+def rot_bwd(lib, dims, grads=None, up=m3.F32, ws=A, nbytes=1 << 24, **kw):
+    a = {n: A for n in ROT_IN + ("dq_out", "dk_out")}
+    a.update(kw)
+    g = grads if grads is not None else m3.RotateGrads(24, 16, m3.F32, 0, *[0x10000] * 4)
+    return lib.m3ssd_norm_rotate_bwd(ctypes.byref(dims), *(a[n] for n in ROT_IN), up, a["dq_out"],
+                                     a["dk_out"], ctypes.byref(g), ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), m3.ERR_INVALID_ARG), (dict(q_heads=0), m3.ERR_INVALID_ARG),
+    (dict(k_heads=-1), m3.ERR_INVALID_ARG), (dict(width=7), m3.ERR_INVALID_ARG),
+    (dict(width=0), m3.ERR_INVALID_ARG), (dict(pairs=5), m3.ERR_INVALID_ARG),
+    (dict(pairs=-1), m3.ERR_INVALID_ARG), (dict(ldq=23), m3.ERR_INVALID_ARG),
+    (dict(ldk=15), m3.ERR_INVALID_ARG), (dict(x_dtype=2), m3.ERR_INVALID_ARG),
+    (dict(eps=-1.0), m3.ERR_INVALID_ARG), (dict(eps=float("nan")), m3.ERR_INVALID_ARG),
+    (dict(reserved=1), m3.ERR_INVALID_ARG), (dict(width=258, ldq=1000, ldk=1000), m3.ERR_UNSUPPORTED),
+    (dict(rows=1 << 31), m3.ERR_UNSUPPORTED), (dict(ldq=1 << 31), m3.ERR_UNSUPPORTED),
+    (dict(q_heads=65536, ldq=1 << 20), m3.ERR_UNSUPPORTED)])
+def test_rotate_rejects_bad_dims(lib, kw, status):
+    d = rot_dims(**kw)
+    assert rot_fwd(lib, d) == rot_bwd(lib, d) == status
+    assert lib.m3ssd_norm_rotate_bwd_workspace_size(ctypes.byref(d)) == 0
+
+
+def test_rotate_rejects_null_and_misaligned_pointers(lib):
+    d = rot_dims()
+    for n in ("q", "k", "positions", "freqs", "q_out", "k_out"):
+        assert rot_fwd(lib, d, **{n: None}) == m3.ERR_INVALID_ARG, n
+    for n in ROT_IN + ("q_out", "k_out"):
+        assert rot_fwd(lib, d, **{n: ODD}) == m3.ERR_INVALID_ARG, n
+    for n in ("q", "k", "positions", "freqs", "dq_out", "dk_out"):
+        assert rot_bwd(lib, d, **{n: None}) == m3.ERR_INVALID_ARG, n
+        assert rot_bwd(lib, d, **{n: ODD}) == m3.ERR_INVALID_ARG, n
+    p = [0x10000] * 4
+    for j in range(4):
+        bad = list(p)
+        bad[j] = 0x10002
+        assert rot_bwd(lib, d, m3.RotateGrads(24, 16, m3.F32, 0, *bad)) == m3.ERR_INVALID_ARG
+    for j in range(2):
+        bad = list(p)
+        bad[j] = None
+        assert rot_bwd(lib, d, m3.RotateGrads(24, 16, m3.F32, 0, *bad)) == m3.ERR_INVALID_ARG
+    assert rot_bwd(lib, d, m3.RotateGrads(23, 16, m3.F32, 0, *p)) == m3.ERR_INVALID_ARG
+    assert rot_bwd(lib, d, m3.RotateGrads(24, 15, m3.F32, 0, *p)) == m3.ERR_INVALID_ARG
+    assert rot_bwd(lib, d, m3.RotateGrads(24, 16, m3.BF16, 0, *p)) == m3.ERR_UNSUPPORTED
+    assert rot_bwd(lib, d, up=m3.BF16) == m3.ERR_UNSUPPORTED
+    assert rot_bwd(lib, d, up=9) == m3.ERR_INVALID_ARG
+    need = lib.m3ssd_norm_rotate_bwd_workspace_size(ctypes.byref(d))
+    assert need > 0 and rot_bwd(lib, d, nbytes=need - 1) == m3.ERR_WORKSPACE
+    assert rot_bwd(lib, d, ws=None) == rot_bwd(lib, d, ws=P(0x10040)) == m3.ERR_WORKSPACE
+
+
+def test_rotate_without_tokens_is_a_no_op(lib):
+    none = {n: None for n in ("q", "k", "positions", "q_out", "k_out")}
+    assert rot_fwd(lib, rot_dims(rows=0), **none) == m3.OK
+
+
+def test_rotate_binding_refuses_on_the_host():
+    q, w = torch.zeros(2, 3, 8), torch.zeros(8)
+    with pytest.raises(ValueError):
+        m3.norm_rotate(q, q, w, w)
+    with pytest.raises(ValueError):
+        m3.norm_rotate_bwd(q, q, w, w, q, q)
+    with pytest.raises(ValueError):
+        m3.norm_rotate(w)

@@ -83,3 +83,40 @@ def test_gates_at_their_ends():
         np.testing.assert_allclose(y, 2.0, atol=1e-12)
         o = ly.glr_bwd(x, x * r, x, np.array([rate - 0.0]), y, np.ones_like(y), h0=np.array([[2.0]]))
         assert np.isfinite(o["dr"]).all() and np.abs(o["dr"]).max() < 1e-12
+
+
+def test_rotation_is_a_matrix_and_keeps_the_norm():
+    """One pair, weight 1: the output has mean square 1 and is turned counter-clockwise."""
+    u = np.array([[[3.0, 4.0]]])
+    o = ly.norm_rotate(u, None, [2], [np.pi / 4], 0.0)
+    r = np.sqrt(12.5)
+    np.testing.assert_allclose(o[0, 0], [-4 / r, 3 / r], rtol=1e-12)
+    v = ly.norm_rotate(np.ones((1, 1, 4)), np.array([1.0, 2, 3, 4]), [5], [0.3], 0.0)[0, 0]
+    np.testing.assert_allclose(v, [np.cos(1.5) - 2 * np.sin(1.5), np.sin(1.5) + 2 * np.cos(1.5), 3, 4],
+                               rtol=1e-12)
+    np.testing.assert_allclose(ly.norm_rotate(np.ones((1, 1, 4)), None, None, None, 3.0), 0.5)
+
+
+def test_scores_depend_on_the_distance_alone():
+    g = np.random.default_rng(0)
+    q, k = g.standard_normal((2, 1, 1, 8))
+    f = 10000.0 ** (-np.arange(4) / 4)
+    dots = [np.sum(ly.norm_rotate(q, None, [p + 7], f, 0.0) * ly.norm_rotate(k, None, [p], f, 0.0))
+            for p in (0, 11, -30, 100000)]
+    np.testing.assert_allclose(dots, dots[0], rtol=1e-9)
+
+
+def test_norm_rotate_gradients_are_the_differences():
+    g = np.random.default_rng(1)
+    u, w, d = g.standard_normal((3, 2, 10)), g.standard_normal(10), g.standard_normal((3, 2, 10))
+    pos, f = [4, 0, -9], np.array([1.0, 0.25, 0.1])
+    du, dw = ly.norm_rotate_bwd(u, w, d, pos, f, 1e-3)
+    loss = lambda a, b: np.sum(d * ly.norm_rotate(a, b, pos, f, 1e-3))  # noqa: E731
+    for at in np.ndindex(u.shape):
+        e = np.zeros_like(u)
+        e[at] = 1e-5
+        assert abs((loss(u + e, w) - loss(u - e, w)) / 2e-5 - du[at]) < 1e-8
+    for j in range(10):
+        e = np.zeros(10)
+        e[j] = 1e-5
+        assert abs((loss(u, w + e) - loss(u, w - e)) / 2e-5 - dw[j]) < 1e-8
