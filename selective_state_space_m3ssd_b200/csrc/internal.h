@@ -370,7 +370,9 @@ struct RotateArgs {
   const float* freqs;          // (R); nullable where R is 0
   void* q_out;
   void* k_out;
-  int lanes, block, blocks;    // lanes of a head, heads of a warp's block, blocks a row (set at launch)
+  // Lanes of a head; slots (of 32 / lanes heads) of a token, the queries' first; slots of a warp's
+  // unit and units a token (the launch sets these).
+  int lanes, q_slots, slots, block, blocks;
 };
 struct RotateBwdArgs {
   RotateArgs f;

@@ -73,7 +73,7 @@ m3ssd_status check_rotate(const m3ssd_rotate_dims* d) {
   if (!dtype_ok(d->x_dtype) || !(d->eps >= 0.f)) return M3SSD_ERR_INVALID_ARG;
   const int64_t most = INT32_MAX;
   if (d->width > 256 || d->q_heads > 65535 || d->k_heads > 65535 || d->rows > most || d->ldq > most ||
-      d->ldk > most)
+      d->ldk > most || d->rows * (d->q_heads + d->k_heads) > most)
     return M3SSD_ERR_UNSUPPORTED;
   if (d->ldq < d->q_heads * d->width || d->ldk < d->k_heads * d->width) return M3SSD_ERR_INVALID_ARG;
   return M3SSD_OK;
