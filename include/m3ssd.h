@@ -712,6 +712,51 @@ m3ssd_status m3ssd_norm_rotate_bwd(const m3ssd_rotate_dims* dims, const void* q,
                                    const void* dk_out, const m3ssd_rotate_grads* grads,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Weights in 4 bits with a scale a group of columns, for the projections of a few decoding tokens
+ * with activations as they are (beside m3ssd_gemm_mx, whose operands are both in few bits):
+ *     W[n][k] = (code[n][k] - zero[k / group][n]) scale[k / group][n],   codes 0 .. 15.
+ *   codes:  K padded to a multiple of 128 and N to one of 16, in tiles of 16 rows x 128 columns,
+ *           1024 bytes each, row-block-major: byte 512 (r / 8) + 64 (r % 8) + 16 l + 4 j + m of row r
+ *           of the tile holds columns 32 j + 8 l + 2 m (low half) and the next one (high half), l, j
+ *           and m from 0 to 3.  16-byte aligned, m3ssd_w4_codes_size bytes.
+ *   scales: (ceil(cols / group), rows) bf16.
+ *   zeros:  (ceil(cols / group), rows) bytes 0 .. 15, or NULL: 8 everywhere.
+ */
+typedef struct {
+  int64_t rows;       /* N >= 0 */
+  int64_t cols;       /* K >= 1 */
+  int64_t group;      /* columns of a group: 32, 64, or a multiple of 128 */
+  uint64_t reserved;  /* must be 0 */
+  void* codes;
+  void* scales;
+  void* zeros;
+} m3ssd_w4;
+
+/* Bytes of the codes; 0 for invalid arguments. */
+size_t m3ssd_w4_codes_size(int64_t rows, int64_t cols);
+
+/*
+ * w (rows x cols, dtype, row stride ldw >= cols) to that form and back.  Without zeros a group's scale
+ * is bf16(max |w| / 7) and a code round(w / scale) + 8; with zeros the scale is bf16((hi - lo) / 15) of the
+ * group's range, zero included, the zero point round(-lo / scale) and a code round(w / scale) + it,
+ * all clamped to 0 .. 15, ties to even.  A group of zeros takes scale 0; one with a NaN or an
+ * infinity a NaN scale, and reads back as NaN.  Read back, (code - zero) scale is rounded once to dtype.
+ */
+m3ssd_status m3ssd_w4_quant(const m3ssd_w4* out, int32_t dtype, const void* w, int64_t ldw, void* stream);
+m3ssd_status m3ssd_w4_dequant(const m3ssd_w4* in, int32_t dtype, void* w, int64_t ldw, void* stream);
+
+/*
+ * out (tokens x rows, out_dtype, row stride ldd >= rows) = x (tokens x cols, x_dtype, row stride
+ * ldx >= cols) W^T for up to 16 tokens (else M3SSD_ERR_UNSUPPORTED: m3ssd_w4_dequant and
+ * m3ssd_gemm_bf16 take more).  Products of the held values, exact, fp32 sums over a group, each
+ * scaled in fp32, and rounded once to out_dtype.  The order of the sums goes by the sizes and the
+ * device's SM count: the same call gives the same bits.  No workspace, no allocation, no
+ * synchronisation; capture-safe.
+ */
+m3ssd_status m3ssd_gemv_w4(int64_t tokens, int32_t x_dtype, const void* x, int64_t ldx, const m3ssd_w4* W,
+                           int32_t out_dtype, void* out, int64_t ldd, void* stream);
+
 /* Number of bounded device-side waits of the chunked forwards (SISO and
  * MIMO), the tensor-core backward, the GEMMs and the 8-bit step that ran out since
  * the last call (a forward's CTA then stops and leaves its outputs unwritten, a step's those

@@ -2,7 +2,7 @@
 from their definitions (include/m3ssd.h), sharing no code with the library.
 
 The gated linear recurrence walks token by token, forward and in reverse.  The heads' norm with
-its rotation is written with complex pairs.
+its rotation is written with complex pairs.  4-bit weights are looked up byte by byte.
 """
 from __future__ import annotations
 
@@ -108,3 +108,46 @@ def norm_rotate_bwd(u, w, d, positions, freqs, eps):
     dv, uh = _turned(d, _turn(positions, freqs, u.shape[-1], -1)), u * rstd
     g = dv * (1.0 if w is None else w)
     return rstd * (g - uh * (g * uh).mean(-1, keepdims=True)), (dv * uh).sum((0, 1))
+
+
+def w4_codes(tiled, rows, cols):
+    """The codes (rows, cols) from the tiled bytes, one at a time by the header's formula."""
+    kb = (cols + 127) // 128
+    r, k = np.meshgrid(np.arange(rows), np.arange(cols), indexing="ij")
+    rr, c = r % 16, k % 128
+    j, l, m = c // 32, c % 32 // 8, c % 8 // 2
+    byte = (r // 16 * kb + k // 128) * 1024 + 512 * (rr // 8) + 64 * (rr % 8) + 16 * l + 4 * j + m
+    v = np.asarray(tiled)[byte]
+    return np.where(k % 2 == 0, v & 15, v >> 4)
+
+
+def w4_weights(codes, scales, zeros, group):
+    """Values of codes (rows, cols), scales and zeros (groups, rows; zeros may be None)."""
+    j = np.arange(codes.shape[1]) // group
+    z = 8.0 if zeros is None else np.asarray(zeros, np.float64)[j].T
+    return (codes - z) * np.asarray(scales, np.float64)[j].T
+
+
+def w4_quant(w, group, zeros, bf16):
+    """(codes, scales, zeros) of fp32 weights by the header's rules, in fp32 as it says; ``bf16``
+    rounds an fp32 array to bf16."""
+    w = np.asarray(w, np.float32)
+    rows, cols = w.shape
+    n = -(-cols // group)
+    codes = np.zeros((rows, cols), np.uint8)
+    scales, zs = np.zeros((n, rows), np.float32), np.zeros((n, rows), np.uint8)
+    f = np.float32
+    for j in range(n):
+        v = w[:, j * group:(j + 1) * group]
+        ok = np.isfinite(v).all(1)
+        v = np.where(ok[:, None], v, f(0))
+        lo, hi = np.minimum(v.min(1), f(0)), np.maximum(v.max(1), f(0))
+        s = f(2) * ((f(0.5) * hi - f(0.5) * lo) / f(15)) if zeros else np.maximum(hi, -lo) / f(7)
+        s = bf16(np.where(ok, s, f("nan")))
+        some = s > 0
+        d = np.where(some, s, f(1))
+        z = np.where(some, np.clip(np.rint(-lo / d), 0, 15), 0) if zeros else np.full(rows, 8.0)
+        q = np.where(some[:, None], np.rint(v / d[:, None]), 0) + z[:, None]
+        codes[:, j * group:(j + 1) * group] = np.clip(q, 0, 15).astype(np.uint8)
+        scales[j], zs[j] = s, z.astype(np.uint8)
+    return codes, scales, zs if zeros else None

@@ -9,8 +9,10 @@ other implementation behind these functions.
 
 Beside the scan, its step and its block: the residual addition and RMS norm
 (:func:`add_rmsnorm`), microscaled tensors and their product (:func:`mx_quant`,
-:func:`gemm_mx`) and the decode step on a cache held in 8 bits (:func:`quant_cache`,
-:func:`step_q8`).
+:func:`gemm_mx`), the decode step on a cache held in 8 bits (:func:`quant_cache`,
+:func:`step_q8`), the gated linear recurrence (:func:`glr_fwd`, :func:`glr_bwd`,
+:func:`glr_step`), the norm of heads with their rotation by position (:func:`norm_rotate`) and
+the product of a few tokens with 4-bit weights in groups (:func:`w4_quant`, :func:`gemv_w4`).
 """
 from __future__ import annotations
 
@@ -107,6 +109,12 @@ class RotateGrads(ctypes.Structure):
     _fields_ = [("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_uint32)] + \
         [(n, ctypes.c_void_p) for n in ("dq", "dk", "dq_w", "dk_w")]
+
+
+class W4(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("reserved", ctypes.c_uint64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
 class BlockDims(ctypes.Structure):
@@ -235,6 +243,13 @@ def load(path: str | None = None):
         lib.m3ssd_norm_rotate_bwd.argtypes = [rdp] + [vp] * 6 + \
             [i32, vp, vp, ctypes.POINTER(RotateGrads), vp, sz, vp]
         lib.m3ssd_norm_rotate_bwd.restype = ctypes.c_int
+        wp = ctypes.POINTER(W4)
+        lib.m3ssd_w4_codes_size.argtypes = [i64, i64]
+        lib.m3ssd_w4_codes_size.restype = sz
+        for f in (lib.m3ssd_w4_quant, lib.m3ssd_w4_dequant):
+            f.argtypes, f.restype = [wp, i32, vp, i64, vp], ctypes.c_int
+        lib.m3ssd_gemv_w4.argtypes = [i64, i32, vp, i64, wp, i32, vp, i64, vp]
+        lib.m3ssd_gemv_w4.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -1320,6 +1335,119 @@ def norm_rotate_bwd(q, k, q_w, k_w, dq_out, dk_out, *, positions=None, freqs=Non
             _addr(positions), _addr(freqs), _xdtype(dq_out), _addr(dq_out), _addr(dk_out),
             ctypes.byref(g), ws, ws_bytes)
     return {n: grads[n] for n in ("dq", "dk", "dq_w", "dk_w")}
+
+
+# ---- 4-bit weights with scales a group, and their product with a few tokens ----------------------
+
+class W4Tensor:
+    """Weights (``m3ssd_w4``): ``rows`` x ``cols`` codes of 4 bits in groups of ``group`` columns (32,
+    64 or a multiple of 128); ``codes`` flat uint8, tiled as laid out in ``include/m3ssd.h``,
+    ``scales`` (groups, rows) bf16, ``zeros`` (groups, rows) uint8 0 to 15 or None (8)."""
+
+    __slots__ = ("rows", "cols", "group", "codes", "scales", "zeros")
+
+    def __init__(self, rows: int, cols: int, group: int, codes, scales, zeros=None):
+        self.rows, self.cols, self.group = rows, cols, group
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, group: int = 128, zeros: bool = False, *, device):
+        """Unwritten storage for weights of this size."""
+        import torch
+        groups = _w4_groups(cols, group)
+        e = lambda dt, *s: torch.empty(*s, dtype=dt, device=device)  # noqa: E731
+        return cls(rows, cols, group, e(torch.uint8, _w4_codes(rows, cols)),
+                   e(torch.bfloat16, groups, rows), e(torch.uint8, groups, rows) if zeros else None)
+
+    @classmethod
+    def from_codes(cls, codes, scales, zeros=None, *, group: int = 128):
+        """Weights quantised elsewhere: ``codes`` (rows, cols) uint8 0 to 15, ``scales`` and ``zeros``
+        (rows, groups).  Laid out by torch, once."""
+        import torch
+        rows, cols = codes.shape
+        n = _w4_groups(cols, group)
+        _need_shape(codes, "codes", torch.uint8)
+        _need_shape(scales, "scales", None, (rows, n))
+        if zeros is not None:
+            _need_shape(zeros, "zeros", torch.uint8, (rows, n))
+        rp, kp = -(-rows // 16) * 16, _pad128(cols)
+        p = torch.zeros(rp, kp, dtype=torch.uint8, device=codes.device)
+        p[:rows, :cols] = codes
+        p = p[:, 0::2] | (p[:, 1::2] << 4)
+        tiled = p.view(rp // 16, 16, kp // 128, 4, 4, 4).permute(0, 2, 1, 4, 3, 5).reshape(-1)
+        return cls(rows, cols, group, tiled, scales.to(torch.bfloat16).t().contiguous(),
+                   None if zeros is None else zeros.t().contiguous())
+
+
+def _w4_groups(cols: int, group: int) -> int:
+    if group not in (32, 64) and (group < 128 or group % 128):
+        raise ValueError(f"a group must be 32, 64 or a multiple of 128 columns, got {group}")
+    return -(-cols // group)
+
+
+def _w4_codes(rows: int, cols: int) -> int:
+    return -(-rows // 16) * (_pad128(cols) // 128) * 1024
+
+
+def _w4_struct(w: W4Tensor, name: str, dev) -> W4:
+    import torch
+    groups = _w4_groups(w.cols, w.group)
+    _need_all(dev, (w.codes, name + ".codes", torch.uint8, (_w4_codes(w.rows, w.cols),)),
+              (w.scales, name + ".scales", torch.bfloat16, (groups, w.rows)),
+              (w.zeros, name + ".zeros", torch.uint8, (groups, w.rows)))
+    return W4(w.rows, w.cols, w.group, 0, w.codes.data_ptr(), w.scales.data_ptr(), _addr(w.zeros))
+
+
+def w4_quant(w, group: int = 128, *, zeros: bool = False, out: W4Tensor | None = None):
+    """Weights w (rows, cols), bf16 or fp32, rows contiguous (any row stride), in 4 bits through
+    ``m3ssd_w4_quant``: symmetric about code 8, or with a zero point a group."""
+    ldw = _rows_stride(w, "w")
+    rows, cols = w.shape
+    if out is None:
+        out = W4Tensor.empty(rows, cols, group, zeros, device=w.device)
+    elif not isinstance(out, W4Tensor) or \
+            (out.rows, out.cols, out.group, out.zeros is not None) != (rows, cols, group, zeros):
+        raise ValueError(f"out must be {rows} x {cols} in groups of {group}")
+    o = _w4_struct(out, "out", w.device)
+    _launch("m3ssd_w4_quant", w.device, ctypes.byref(o), _xdtype(w), _addr(w), ldw)
+    return out
+
+
+def w4_dequant(w: W4Tensor, dtype=None, *, out=None):
+    """The values of 4-bit weights (rows, cols) through ``m3ssd_w4_dequant``, in ``dtype`` (bf16
+    unless given) or into ``out`` (rows contiguous)."""
+    import torch
+    dev = w.codes.device
+    if out is None:
+        out, ldw = torch.empty(w.rows, w.cols, dtype=dtype or torch.bfloat16, device=dev), w.cols
+    else:
+        _need_shape(out, "out", dtype, (w.rows, w.cols))
+        ldw = _rows_stride(out, "out")
+    s = _w4_struct(w, "w", out.device)
+    _launch("m3ssd_w4_dequant", dev, ctypes.byref(s), _xdtype(out), _addr(out), ldw)
+    return out
+
+
+def gemv_w4(x, W: W4Tensor, *, out=None, out_dtype=None):
+    """x (tokens, cols) @ W (rows, cols)^T for up to 16 tokens, bf16 or fp32, through
+    ``m3ssd_gemv_w4`` -> out (tokens, rows) in ``out_dtype`` (x's type unless given); the rows of
+    x and out contiguous, any distance apart."""
+    import torch
+    dev = x.device
+    ldx = _rows_stride(x, "x")
+    if x.shape[1] != W.cols:
+        raise ValueError(f"x must have {W.cols} columns, got {tuple(x.shape)}")
+    if out is None:
+        out, ldd = torch.empty(x.shape[0], W.rows, dtype=out_dtype or x.dtype, device=dev), W.rows
+    else:
+        _need_shape(out, "out", out_dtype, (x.shape[0], W.rows))
+        ldd = _rows_stride(out, "out")
+        if out.device != dev:
+            raise ValueError(f"out is on {out.device}, expected {dev}")
+    w = _w4_struct(W, "W", dev)
+    _launch("m3ssd_gemv_w4", dev, x.shape[0], _xdtype(x), _addr(x), ldx, ctypes.byref(w), _xdtype(out),
+            _addr(out), ldd)
+    return out
 
 
 class PreparedFwd:

@@ -1,0 +1,398 @@
+// The product of a few tokens with 4-bit weights whose groups of columns have a bf16 scale (and a
+// zero point), and the weights into that form and back.
+//
+//     out[m][n] = sum over groups j of scale[j][n] (sum over the group's k of x[m][k] (code[n][k] - zero[j][n])).
+//
+// The codes are read once, and HBM bounds the product from about a million weights on; below, it is
+// latency.  A warp takes tiles of 16 rows by 128 columns, 1 KB of codes that its lanes read as two
+// 16-byte words each, in the order that a lane needs them as an operand of the (legacy) warp-wide
+// bf16 product of 16 x 16 weights by 16 x 8 tokens: the k order within a product is free as long as
+// both operands share it.  A code n becomes the bf16 number 128 + n by setting bits, less 128 + zero
+// exactly, so nothing is rounded before the products' fp32 sums; a group's sums are scaled in
+// fp32.  tcgen05 is not for this: its operands would have to go through shared or tensor memory, and
+// at 16 tokens the products are a tenth of the time the codes take to arrive.
+//
+// fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
+// A CTA's eight warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
+// order; the tokens lie there too, a piece of K at a time.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace m3ssd {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kTileRows = 16, kTileCols = 128, kTileBytes = 1024;
+constexpr int kRedRow = kTileRows + 1;
+
+// Tiles of codes in flight a warp.
+constexpr int kDeep = 2;
+
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// The pairs of codes (i, i + 4), i = 0 to 3, of a word of eight, less 128 + zero, as bf16 pairs.
+__device__ __forceinline__ void decode(uint32_t w, uint32_t offset, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t n = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;  // 128 + code
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&n),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&offset));
+    o[i] = *reinterpret_cast<const uint32_t*>(&d);
+  }
+}
+
+__device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight consecutive values of a token, from column k of K on (zeros past it), as the pairs (i, i + 4).
+__device__ __forceinline__ uint32_t two(uint32_t lo, uint32_t hi) { return lo >> 16 | (hi & 0xffff0000u); }
+__device__ __forceinline__ void load_tokens(const __nv_bfloat16* x, int64_t k, int64_t K, bool wide,
+                                            float (&v)[8]) {
+  if (wide && k + 8 <= K) {
+    const uint4 u = *reinterpret_cast<const uint4*>(x + k);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k + j < K ? to_f32(x[k + j]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load_tokens(const float* x, int64_t k, int64_t K, bool wide, float (&v)[8]) {
+  if (wide && k + 8 <= K) {
+    const float4 a = *reinterpret_cast<const float4*>(x + k), b = *reinterpret_cast<const float4*>(x + k + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k + j < K ? x[k + j] : 0.f;
+  }
+}
+// The leading bf16 part of each value (its high half), which is taken off it.  What is not finite has no
+// further parts.
+__device__ __forceinline__ uint4 part_of(float (&v)[8]) {
+  uint32_t h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] = __float_as_uint(v[j]) & 0xffff0000u;
+    if ((h[j] & 0x7f800000u) == 0x7f800000u) {
+      if (v[j] != v[j]) h[j] = 0x7fc00000u;  // a NaN whose high bits alone might read as infinity
+      v[j] = 0.f;
+    } else {
+      v[j] -= __uint_as_float(h[j]);
+    }
+  }
+  return make_uint4(two(h[0], h[4]), two(h[1], h[5]), two(h[2], h[6]), two(h[3], h[7]));
+}
+
+// NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero points given.
+template <int NT, int G, bool ZEROS>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) gemv_w4_kernel(GemvW4Args a) {
+  extern __shared__ __align__(16) char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int WK = a.wk, WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
+  const int64_t rb = (int64_t)blockIdx.x * WR + wr;
+  const bool live = rb < a.RB;
+  const int KB = (int)a.KB, per = a.per, chunk = per * WK;  // tiles: of K, of a warp and of a CTA a piece
+  const uint8_t* const codes = a.codes + (live ? rb : 0) * KB * kTileBytes + lane * 16;
+  const int64_t r0 = min(rb * kTileRows + g, a.N - 1), r1 = min(rb * kTileRows + g + 8, a.N - 1);
+  const int cols = a.cols, stride = chunk * kTileCols * 2 + 64;  // bytes of a column in shared memory
+
+  // Tile i of the warp's, in K's pieces one after the other.
+  auto tile_of = [&](int i) { return i / per * chunk + wk * per + i % per; };
+  struct Tile {
+    uint4 lo, hi;         // rows g and g + 8
+    uint32_t scale, zero; // of group t, row g in the low part
+  };
+  auto load = [&](int i, Tile& o) {
+    const int kb = tile_of(i);
+    if (!live || kb >= KB) return;
+    o.lo = load_codes(codes + (int64_t)kb * kTileBytes);
+    o.hi = load_codes(codes + (int64_t)kb * kTileBytes + 512);
+    if (t < G) {
+      const int64_t j = min(G == 1 ? kb / a.group_tiles : kb * G + t, a.groups - 1) * a.N;
+      o.scale = a.scales[j + r0] | (uint32_t)a.scales[j + r1] << 16;
+      if (ZEROS) o.zero = a.zeros[j + r0] | (uint32_t)a.zeros[j + r1] << 16;
+    }
+  };
+  Tile ring[kDeep];
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d) load(d, ring[d]);
+
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+
+  auto use = [&](const Tile& v, int at) {  // `at`: the tile's place in the piece
+    const char* const xs = smem + g * stride + at * kTileCols * 2 + t * 16;
+    const uint32_t lo[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w}, hi[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+    float sum[NT][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      constexpr int per_group = 4 / G;
+      const int from = (lane & ~3) | j / per_group;
+      uint32_t off0 = 0x43084308u, off1 = off0;  // 128 + 8
+      if (ZEROS) {
+        const uint32_t z = __shfl_sync(0xffffffffu, v.zero, from);
+        off0 = 0x43004300u | (z & 0xffu) * 0x10001u;
+        off1 = 0x43004300u | (z >> 16) * 0x10001u;
+      }
+      uint32_t p[4], q[4];
+      decode(lo[j], off0, p);
+      decode(hi[j], off1, q);
+      if (j % per_group == 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (8 * n + g < cols) b = *reinterpret_cast<const uint4*>(xs + 8 * n * stride + j * 64);
+        product(sum[n], p[0], q[0], p[1], q[1], b.x, b.y);
+        product(sum[n], p[2], q[2], p[3], q[3], b.z, b.w);
+      }
+      if (j % per_group == per_group - 1) {
+        const uint32_t s = __shfl_sync(0xffffffffu, v.scale, from);
+        const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xffff0000u);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          acc[n][0] = fmaf(s0, sum[n][0], acc[n][0]);
+          acc[n][1] = fmaf(s0, sum[n][1], acc[n][1]);
+          acc[n][2] = fmaf(s1, sum[n][2], acc[n][2]);
+          acc[n][3] = fmaf(s1, sum[n][3], acc[n][3]);
+        }
+      }
+    }
+  };
+  // The piece of the tokens from tile `first` on into shared memory.
+  auto stage = [&](int first) {
+    const int eighths = min(chunk, KB - first) * (kTileCols / 8);
+    for (int m = 0; m < (int)a.M; ++m) {
+      char* const xs = smem + m * a.parts * stride;
+#pragma unroll 4
+      for (int q = threadIdx.x; q < eighths; q += kThreads) {
+        const int64_t k = (int64_t)first * kTileCols + 8 * q;
+        float v[8];
+        if (a.x_bf16)
+          load_tokens(static_cast<const __nv_bfloat16*>(a.x) + m * a.ldx, k, a.K, a.wide, v);
+        else
+          load_tokens(static_cast<const float*>(a.x) + m * a.ldx, k, a.K, a.wide, v);
+        for (int p = 0; p < a.parts; ++p)
+          *reinterpret_cast<uint4*>(xs + p * stride + q * 16) = part_of(v);
+      }
+    }
+  };
+
+  const int total = (KB + chunk - 1) / chunk * per;
+  for (int i = 0, first = 0, at = 0; i < total; i += kDeep) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      if (i + d < total) {
+        if (at == 0) {  // a new piece
+          if (first > 0) __syncthreads();
+          stage(first);
+          __syncthreads();
+        }
+        if (live && first + wk * per + at < KB) use(ring[d], wk * per + at);
+        load(i + d + kDeep, ring[d]);
+        if (++at == per) {
+          at = 0;
+          first += chunk;
+        }
+      }
+    }
+  }
+
+  // the tile's sums: over the parts of K, and of a token
+  __syncthreads();
+  float* const red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int col = 8 * n + 2 * t + (e & 1), r = g + 8 * (e >> 1);
+      if (col < cols) red[(warp * cols + col) * kRedRow + r] = acc[n][e];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < WR * (int)a.M * kTileRows; i += kThreads) {
+    const int r = i % kTileRows, m = i / kTileRows % (int)a.M, w = i / kTileRows / (int)a.M;
+    const int64_t n = ((int64_t)blockIdx.x * WR + w) * kTileRows + r;
+    if (n >= a.N) continue;
+    float s = 0.f;
+    for (int p = 0; p < a.parts; ++p)
+      for (int k = 0; k < WK; ++k)
+        s += red[((w * WK + k) * cols + m * a.parts + p) * kRedRow + r];
+    if (a.out_bf16)
+      static_cast<__nv_bfloat16*>(a.out)[m * a.ldd + n] = __float2bfloat16_rn(s);
+    else
+      static_cast<float*>(a.out)[m * a.ldd + n] = s;
+  }
+}
+
+// Where column k of row r lies in the codes: the byte, and whether it is the high half.
+__device__ __forceinline__ int64_t code_byte(int64_t r, int64_t k, int64_t KB) {
+  const int rr = (int)(r % kTileRows), c = (int)(k % kTileCols);
+  return (r / kTileRows * KB + k / kTileCols) * kTileBytes + 512 * (rr / 8) + 64 * (rr % 8) +
+         16 * (c / 8 % 4) + 4 * (c / 32) + c % 8 / 2;
+}
+
+// A warp quantises a group of a row (rows of the last tile that are not there: codes of zero).  Lane l takes
+// pairs of columns, 64 columns a step.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) w4_quant_kernel(W4Args a, const T* w, int64_t ldw) {
+  const int64_t rows = (a.N + kTileRows - 1) / kTileRows * kTileRows, KB = (a.K + kTileCols - 1) / kTileCols;
+  const int64_t span = (KB * kTileCols + a.group - 1) / a.group;  // groups, the padding's too
+  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (id >= rows * span) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = id / span, j = id % span, k0 = j * a.group, k1 = min(k0 + a.group, KB * kTileCols);
+  const bool there = r < a.N;
+  float lo = 0.f, hi = 0.f;
+  bool finite = true;
+  for (int64_t k = k0 + lane; k < min(k1, a.K); k += 32) {
+    const float v = there ? to_f32(w[r * ldw + k]) : 0.f;
+    finite &= fabsf(v) < INFINITY;
+    lo = fminf(lo, v);
+    hi = fmaxf(hi, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  finite = __all_sync(0xffffffffu, finite);
+  // halves first: the range of the largest values overflows
+  const __nv_bfloat16 scale =
+      __float2bfloat16_rn(!finite    ? NAN
+                          : a.zeros ? 2.f * ((0.5f * hi - 0.5f * lo) / 15.f)
+                                    : fmaxf(hi, -lo) / 7.f);
+  const float s = to_f32(scale);
+  const bool some = s > 0.f;  // not of zeros, not NaN
+  const float zero = !a.zeros ? 8.f : some ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 0.f;
+  if (there && j < a.groups && lane == 0) {
+    a.scales[j * a.N + r] = __bfloat16_as_ushort(scale);
+    if (a.zeros) a.zeros[j * a.N + r] = (uint8_t)zero;
+  }
+  for (int64_t k = k0 + 2 * lane; k < k1; k += 64) {
+    uint32_t c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float v = there && some && k + e < a.K ? to_f32(w[r * ldw + k + e]) / s : 0.f;
+      c[e] = (uint32_t)fminf(fmaxf(rintf(v) + zero, 0.f), 15.f);
+    }
+    a.codes[code_byte(r, k, KB)] = (uint8_t)(c[0] | c[1] << 4);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) w4_dequant_kernel(W4Args a, T* w, int64_t ldw) {
+  const int64_t pairs = (a.K + 1) / 2, KB = (a.K + kTileCols - 1) / kTileCols;
+  for (int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x; id < a.N * pairs;
+       id += (int64_t)gridDim.x * kThreads) {
+    const int64_t r = id / pairs, k = id % pairs * 2, j = k / a.group;
+    const uint32_t c = a.codes[code_byte(r, k, KB)];
+    const float s = __uint_as_float((uint32_t)a.scales[j * a.N + r] << 16);
+    const float z = a.zeros ? (float)a.zeros[j * a.N + r] : 8.f;
+    w[r * ldw + k] = from_f32<T>(((float)(c & 15) - z) * s);
+    if (k + 1 < a.K) w[r * ldw + k + 1] = from_f32<T>(((float)(c >> 4) - z) * s);
+  }
+}
+
+// Columns in shared memory a CTA: few CTAs' worth of a whole K, or pieces of it.
+constexpr int kStageBytes = 36 * 1024, kWideStageBytes = 72 * 1024;
+
+template <int NT, int G, bool ZEROS>
+cudaError_t run(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(gemv_w4_kernel<NT, G, ZEROS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  gemv_w4_kernel<NT, G, ZEROS><<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+template <int NT, int G>
+cudaError_t run_z(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
+  return a.zeros ? run<NT, G, true>(a, grid, smem, s) : run<NT, G, false>(a, grid, smem, s);
+}
+template <int NT>
+cudaError_t run_g(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
+  return a.group == 32   ? run_z<NT, 4>(a, grid, smem, s)
+         : a.group == 64 ? run_z<NT, 2>(a, grid, smem, s)
+                         : run_z<NT, 1>(a, grid, smem, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
+  GemvW4Args a = args;
+  const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
+  a.parts = a.x_bf16 ? 1 : 3;
+  a.cols = (int)a.M * a.parts;
+  a.RB = (a.N + kTileRows - 1) / kTileRows;
+  a.KB = (a.K + kTileCols - 1) / kTileCols;
+  a.group_tiles = (int)(a.group / kTileCols);
+  a.wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % (a.x_bf16 ? 8 : 4) == 0;
+  // parts of K: as many as leave no more CTAs than an SM holds four of
+  a.wk = 1;
+  while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= 4 * sms) a.wk *= 2;
+  const int64_t all = (a.KB + a.wk - 1) / a.wk;  // tiles of a warp
+  const int64_t room = (a.cols <= 8 ? kStageBytes : kWideStageBytes) / a.cols - 64;
+  const int64_t most = room / (2 * kTileCols * a.wk);
+  a.per = (int)(all < most ? all : most < 1 ? 1 : most);
+  const int64_t wr = kWarps / a.wk;
+  const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
+  const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64);
+  const int sums = kWarps * a.cols * kRedRow * (int)sizeof(float), smem = held > sums ? held : sums;
+  const int nt = (a.cols + 7) / 8;
+  return nt == 1   ? run_g<1>(a, grid, smem, s)
+         : nt == 2 ? run_g<2>(a, grid, smem, s)
+         : nt <= 4 ? run_g<4>(a, grid, smem, s)
+                   : run_g<6>(a, grid, smem, s);
+}
+
+cudaError_t launch_w4_quant(const W4Args& a, bool bf16, const void* w, int64_t ldw, cudaStream_t s) {
+  const int64_t rows = (a.N + kTileRows - 1) / kTileRows * kTileRows;
+  const int64_t cols = (a.K + kTileCols - 1) / kTileCols * kTileCols, span = (cols + a.group - 1) / a.group;
+  const unsigned grid = (unsigned)((rows * span + kWarps - 1) / kWarps);
+  if (bf16)
+    w4_quant_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<const __nv_bfloat16*>(w), ldw);
+  else
+    w4_quant_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<const float*>(w), ldw);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_w4_dequant(const W4Args& a, bool bf16, void* w, int64_t ldw, cudaStream_t s) {
+  const int64_t n = a.N * ((a.K + 1) / 2), want = (n + kThreads - 1) / kThreads;
+  const unsigned grid = (unsigned)(want < 148 * 32 ? want : 148 * 32);
+  if (bf16)
+    w4_dequant_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<__nv_bfloat16*>(w), ldw);
+  else
+    w4_dequant_kernel<<<grid, kThreads, 0, s>>>(a, static_cast<float*>(w), ldw);
+  return cudaGetLastError();
+}
+
+}  // namespace m3ssd

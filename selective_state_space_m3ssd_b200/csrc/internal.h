@@ -390,6 +390,38 @@ cudaError_t launch_norm_rotate(const RotateArgs& a, cudaStream_t s);
 size_t norm_rotate_bwd_workspace_bytes(const RotateArgs& a);
 cudaError_t launch_norm_rotate_bwd(const RotateBwdArgs& a, cudaStream_t s);
 
+// 4-bit weights N x K in groups of columns (csrc/gemv_w4.cu): tiled codes, scales (bf16 bits) and zero points
+// (groups x N, nullable: 8), into that form and back.
+struct W4Args {
+  int64_t N, K, group;
+  int groups;
+  uint8_t* codes;
+  uint16_t* scales;
+  uint8_t* zeros;
+};
+cudaError_t launch_w4_quant(const W4Args& a, bool bf16, const void* w, int64_t ldw, cudaStream_t s);
+cudaError_t launch_w4_dequant(const W4Args& a, bool bf16, void* w, int64_t ldw, cudaStream_t s);
+// out (M x N) = x (M x K) W^T, M up to 16.
+struct GemvW4Args {
+  int64_t M, N, K, group;
+  int groups;
+  bool x_bf16, out_bf16;
+  const void* x;
+  int64_t ldx;
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+  void* out;
+  int64_t ldd;
+  // The launch sets these: bf16 columns a token and in all, tiles along N and K, tiles of a group,
+  // parts of K, tiles of a warp in a piece of K, whether tokens can be read 16 bytes at a time.
+  int parts, cols;
+  int64_t RB, KB;
+  int group_tiles, wk, per;
+  bool wide;
+};
+cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t s);
+
 // Decode step (two launches: the state/outputs, then b_prev <- B_t).
 cudaError_t launch_step(const StepArgs& a, cudaStream_t s);
 

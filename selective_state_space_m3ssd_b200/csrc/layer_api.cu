@@ -1,5 +1,5 @@
 // C-ABI entry points of the operators that a layer has around the scan: the gated linear
-// recurrence, and the norm of heads with their rotation.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
+// recurrence, the norm of heads with their rotation, and 4-bit weights with scales a group.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -92,6 +92,31 @@ bool rotate_inputs(const m3ssd_rotate_dims* d, const void* q, const void* k, con
   a.bf16 = d->x_dtype == M3SSD_BF16; a.eps = d->eps;
   a.q = q; a.k = k; a.q_w = q_w; a.k_w = k_w; a.positions = positions; a.freqs = freqs;
   return true;
+}
+
+m3ssd_status check_w4_size(int64_t rows, int64_t cols, int64_t group) {
+  if (rows < 0 || cols < 1 || group < 32) return M3SSD_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group % 128 != 0) return M3SSD_ERR_INVALID_ARG;
+  const int64_t most = INT32_MAX;  // rows, columns, and tiles of 16 x 128 are counted in 31 bits
+  if (rows > most - 15 || cols > most / 8 || group > most) return M3SSD_ERR_UNSUPPORTED;
+  if ((rows + 15) / 16 * ((cols + 127) / 128) > most / 8) return M3SSD_ERR_UNSUPPORTED;
+  return M3SSD_OK;
+}
+m3ssd_status check_w4(const m3ssd_w4* w) {
+  if (!w || w->reserved != 0) return M3SSD_ERR_INVALID_ARG;
+  const m3ssd_status st = check_w4_size(w->rows, w->cols, w->group);
+  if (st != M3SSD_OK) return st;
+  if (w->rows > 0 && (!w->codes || !w->scales)) return M3SSD_ERR_INVALID_ARG;
+  return aligned(w->codes, 16) && aligned(w->scales, 2) ? M3SSD_OK : M3SSD_ERR_INVALID_ARG;
+}
+m3ssd::W4Args w4_args(const m3ssd_w4* w) {
+  m3ssd::W4Args a{};
+  a.N = w->rows; a.K = w->cols; a.group = w->group;
+  a.groups = (int)((w->cols + w->group - 1) / w->group);
+  a.codes = static_cast<uint8_t*>(w->codes);
+  a.scales = static_cast<uint16_t*>(w->scales);
+  a.zeros = static_cast<uint8_t*>(w->zeros);
+  return a;
 }
 
 }  // namespace
@@ -242,6 +267,50 @@ m3ssd_status m3ssd_norm_rotate_bwd(const m3ssd_rotate_dims* dims, const void* q,
   a.dq = grads->dq; a.dk = grads->dk; a.dq_w = grads->dq_w; a.dk_w = grads->dk_w;
   a.part = static_cast<float*>(workspace);
   return from_cuda(m3ssd::launch_norm_rotate_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t m3ssd_w4_codes_size(int64_t rows, int64_t cols) {
+  if (check_w4_size(rows, cols, 32) != M3SSD_OK) return 0;
+  return (size_t)((rows + 15) / 16) * (size_t)((cols + 127) / 128) * 1024;
+}
+
+m3ssd_status m3ssd_w4_quant(const m3ssd_w4* out, int32_t dtype, const void* w, int64_t ldw, void* stream) {
+  const m3ssd_status st = check_w4(out);
+  if (st != M3SSD_OK) return st;
+  if (!dtype_ok(dtype) || ldw < out->cols) return M3SSD_ERR_INVALID_ARG;
+  if (out->rows == 0) return M3SSD_OK;
+  if (!w || !aligned(w, dtype_size(dtype))) return M3SSD_ERR_INVALID_ARG;
+  return from_cuda(m3ssd::launch_w4_quant(w4_args(out), dtype == M3SSD_BF16, w, ldw,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+m3ssd_status m3ssd_w4_dequant(const m3ssd_w4* in, int32_t dtype, void* w, int64_t ldw, void* stream) {
+  const m3ssd_status st = check_w4(in);
+  if (st != M3SSD_OK) return st;
+  if (!dtype_ok(dtype) || ldw < in->cols) return M3SSD_ERR_INVALID_ARG;
+  if (in->rows == 0) return M3SSD_OK;
+  if (!w || !aligned(w, dtype_size(dtype))) return M3SSD_ERR_INVALID_ARG;
+  return from_cuda(m3ssd::launch_w4_dequant(w4_args(in), dtype == M3SSD_BF16, w, ldw,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+m3ssd_status m3ssd_gemv_w4(int64_t tokens, int32_t x_dtype, const void* x, int64_t ldx, const m3ssd_w4* W,
+                           int32_t out_dtype, void* out, int64_t ldd, void* stream) {
+  const m3ssd_status st = check_w4(W);
+  if (st != M3SSD_OK) return st;
+  if (tokens < 0 || !dtype_ok(x_dtype) || !dtype_ok(out_dtype)) return M3SSD_ERR_INVALID_ARG;
+  if (tokens > 16) return M3SSD_ERR_UNSUPPORTED;
+  if (ldx < W->cols || ldd < W->rows) return M3SSD_ERR_INVALID_ARG;
+  if (tokens == 0 || W->rows == 0) return M3SSD_OK;
+  if (!x || !out || !aligned(x, dtype_size(x_dtype)) || !aligned(out, dtype_size(out_dtype)))
+    return M3SSD_ERR_INVALID_ARG;
+  const m3ssd::W4Args w = w4_args(W);
+  m3ssd::GemvW4Args a{};
+  a.M = tokens; a.N = w.N; a.K = w.K; a.group = w.group; a.groups = w.groups;
+  a.x_bf16 = x_dtype == M3SSD_BF16; a.out_bf16 = out_dtype == M3SSD_BF16;
+  a.x = x; a.ldx = ldx; a.codes = w.codes; a.scales = w.scales; a.zeros = w.zeros;
+  a.out = out; a.ldd = ldd;
+  return from_cuda(m3ssd::launch_gemv_w4(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

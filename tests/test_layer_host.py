@@ -228,3 +228,68 @@ def test_rotate_binding_refuses_on_the_host():
         m3.norm_rotate_bwd(q, q, w, w, q, q)
     with pytest.raises(ValueError):
         m3.norm_rotate(w)
+
+
+def w4(**kw):
+    d = dict(rows=4, cols=100, group=32, reserved=0, codes=0x10000, scales=0x10000, zeros=None)
+    d.update(kw)
+    return m3.W4(*(d[n] for n, _ in m3.W4._fields_))
+
+
+def gemv(lib, W, tokens=2, xd=m3.F32, x=A, ldx=100, od=m3.F32, out=A, ldd=4):
+    return lib.m3ssd_gemv_w4(tokens, xd, x, ldx, ctypes.byref(W), od, out, ldd, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), m3.ERR_INVALID_ARG), (dict(cols=0), m3.ERR_INVALID_ARG),
+    (dict(group=0), m3.ERR_INVALID_ARG), (dict(group=16), m3.ERR_INVALID_ARG),
+    (dict(group=96), m3.ERR_INVALID_ARG), (dict(group=160), m3.ERR_INVALID_ARG),
+    (dict(reserved=1), m3.ERR_INVALID_ARG), (dict(codes=None), m3.ERR_INVALID_ARG),
+    (dict(scales=None), m3.ERR_INVALID_ARG), (dict(codes=0x10008), m3.ERR_INVALID_ARG),
+    (dict(scales=0x10001), m3.ERR_INVALID_ARG), (dict(rows=1 << 31), m3.ERR_UNSUPPORTED),
+    (dict(cols=1 << 30), m3.ERR_UNSUPPORTED), (dict(rows=1 << 30, cols=1 << 14), m3.ERR_UNSUPPORTED)])
+def test_w4_rejects_bad_weights(lib, kw, status):
+    W = w4(**kw)
+    big = 1 << 31
+    assert gemv(lib, W, ldx=big, ldd=big) == status
+    assert lib.m3ssd_w4_quant(ctypes.byref(W), m3.F32, A, big, None) == status
+    assert lib.m3ssd_w4_dequant(ctypes.byref(W), m3.F32, A, big, None) == status
+
+
+def test_w4_rejects_bad_arguments(lib):
+    assert gemv(lib, w4(), tokens=-1) == m3.ERR_INVALID_ARG
+    assert gemv(lib, w4(), tokens=17) == m3.ERR_UNSUPPORTED
+    for kw in (dict(xd=5), dict(od=5), dict(ldx=99), dict(ldd=3), dict(x=None), dict(out=None), dict(x=ODD),
+               dict(out=ODD)):
+        assert gemv(lib, w4(), **kw) == m3.ERR_INVALID_ARG, kw
+    for f in (lib.m3ssd_w4_quant, lib.m3ssd_w4_dequant):
+        for dt, p, ld in ((5, A, 100), (m3.F32, None, 100), (m3.F32, ODD, 100), (m3.F32, A, 99)):
+            assert f(ctypes.byref(w4()), dt, p, ld, None) == m3.ERR_INVALID_ARG
+        assert f(None, m3.F32, A, 100, None) == m3.ERR_INVALID_ARG
+        assert f(ctypes.byref(w4(rows=0, codes=None, scales=None)), m3.F32, None, 100, None) == m3.OK
+    assert gemv(lib, w4(), tokens=0, x=None, out=None) == m3.OK
+    assert gemv(lib, w4(rows=0, codes=None, scales=None), x=None, out=None) == m3.OK
+    assert lib.m3ssd_w4_codes_size(17, 129) == 2 * 2 * 1024 and lib.m3ssd_w4_codes_size(1, 0) == 0
+
+
+def test_w4_binding_refuses_on_the_host():
+    W = m3.W4Tensor.empty(8, 64, 32, device="cpu")
+    for f in (lambda: m3.gemv_w4(torch.zeros(1, 64), W), lambda: m3.w4_quant(torch.zeros(8, 64)),
+              lambda: m3.w4_dequant(W), lambda: m3.W4Tensor.empty(8, 64, 48, device="cpu")):
+        with pytest.raises(ValueError):
+            f()
+
+
+@pytest.mark.parametrize("rows,cols,group", [(1, 1, 32), (16, 128, 128), (19, 333, 64), (40, 700, 256)])
+def test_w4_codes_from_elsewhere_are_laid_out(rows, cols, group):
+    from oracle import layer as ly
+    g = torch.Generator().manual_seed(1)
+    codes = torch.randint(0, 16, (rows, cols), generator=g, dtype=torch.uint8)
+    n = -(-cols // group)
+    scales, zeros = torch.rand(rows, n, generator=g), torch.randint(0, 16, (rows, n), dtype=torch.uint8)
+    W = m3.W4Tensor.from_codes(codes, scales, zeros, group=group)
+    assert (ly.w4_codes(W.codes.numpy(), rows, cols) == codes.numpy()).all()
+    assert torch.equal(W.scales, scales.bfloat16().t()) and torch.equal(W.zeros, zeros.t())
+    assert W.codes.numel() == m3._w4_codes(rows, cols)
+    with pytest.raises(ValueError):
+        m3.W4Tensor.from_codes(codes, scales[:, :-1], group=group)

@@ -120,3 +120,29 @@ def test_norm_rotate_gradients_are_the_differences():
         e = np.zeros(10)
         e[j] = 1e-5
         assert abs((loss(u, w + e) - loss(u, w - e)) / 2e-5 - dw[j]) < 1e-8
+
+
+def test_w4_layout_and_values():
+    """A byte at a time: row 9, column 128 + 32 * 2 + 8 * 3 + 5 of 17 rows x 300 columns."""
+    tiled = np.zeros(2 * 3 * 1024, np.uint8)
+    tiled[1024 + 512 + 64 * 1 + 16 * 3 + 4 * 2 + 2] = 0xb4
+    c = ly.w4_codes(tiled, 17, 300)
+    assert c[9, 128 + 64 + 24 + 5] == 11 and c[9, 128 + 64 + 24 + 4] == 4 and c.sum() == 15
+    w = ly.w4_weights(c, np.full((3, 17), 0.5), None, 128)
+    assert w[9, 221] == 1.5 and w[0, 0] == -4
+    w = ly.w4_weights(c, np.full((10, 17), 2.0), np.full((10, 17), 3), 32)
+    assert w[9, 220] == 2 and w[0, 0] == -6
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 128])
+def test_w4_quantisation_is_within_half_a_step(zeros, group):
+    """Scales rounded to bf16 (2^-9 up or down) let the ends clip by 15 * 2^-9 of a step."""
+    w = np.random.default_rng(0).standard_normal((5, 200)).astype(np.float32)
+    w[2, :128] = 0
+    bf = lambda a: (np.asarray(a, np.float32).view(np.uint32) + 0x7fff +  # noqa: E731
+                    (np.asarray(a, np.float32).view(np.uint32) >> 16 & 1) & 0xffff0000).view(np.float32)
+    c, s, z = ly.w4_quant(w, group, zeros, bf)
+    err = np.abs(ly.w4_weights(c, s, z, group) - w)
+    step = s.astype(np.float64)[np.arange(200) // group].T
+    assert (err <= step * (0.5 + 15 / 512)).all() and not err[2, :128].any()
