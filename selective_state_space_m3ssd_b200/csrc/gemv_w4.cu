@@ -31,7 +31,11 @@ constexpr int kTileRows = 16, kTileCols = 128, kTileBytes = 1024;
 constexpr int kRedRow = kTileRows + 1;
 
 // Tiles of codes in flight a warp.
-constexpr int kDeep = 2;
+#ifndef N1
+#define N1 4
+#define DP 1
+#endif
+constexpr int kDeep = DP;
 
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
   uint4 v;
@@ -41,44 +45,74 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t load_shared1(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 // The pairs of codes (i, i + 4), i = 0 to 3, of a word of eight, less 128 + zero, as bf16 pairs.
 __device__ __forceinline__ void decode(uint32_t w, uint32_t offset, uint32_t (&o)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t n = (w >> (4 * i) & 0x000f000fu) | 0x43004300u;  // 128 + code
+    uint32_t n;  // 128 + code: (w >> 4 i & 0x000f000f) | 0x43004300, the two in one operation
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(n) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
     const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&n),
                                      *reinterpret_cast<const __nv_bfloat162*>(&offset));
     o[i] = *reinterpret_cast<const uint32_t*>(&d);
   }
 }
 
+// d += a b, or d = a b where NEW.
+template <bool NEW>
 __device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (NEW)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Eight consecutive values of a token, from column k of K on (zeros past it), as the pairs (i, i + 4).
-__device__ __forceinline__ uint32_t two(uint32_t lo, uint32_t hi) { return lo >> 16 | (hi & 0xffff0000u); }
-__device__ __forceinline__ void load_tokens(const __nv_bfloat16* x, int64_t k, int64_t K, bool wide,
-                                            float (&v)[8]) {
+// Eight consecutive values of a token, from column k of K on (zeros past it), go to shared memory as
+// the pairs (i, i + 4).
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+__device__ __forceinline__ void stage_eight(const __nv_bfloat16* x, int64_t k, int64_t K, bool wide, char* to,
+                                            int) {
+  uint4 u;
   if (wide && k + 8 <= K) {
-    const uint4 u = *reinterpret_cast<const uint4*>(x + k);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    u = *reinterpret_cast<const uint4*>(x + k);
   } else {
+    const uint16_t* const p = reinterpret_cast<const uint16_t*>(x);
+    uint32_t h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k + j < K ? to_f32(x[k + j]) : 0.f;
+    for (int j = 0; j < 8; ++j) h[j] = k + j < K ? p[k + j] : 0;
+    u = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   }
+  *reinterpret_cast<uint4*>(to) = make_uint4(low_halves(u.x, u.z), high_halves(u.x, u.z),
+                                             low_halves(u.y, u.w), high_halves(u.y, u.w));
 }
-__device__ __forceinline__ void load_tokens(const float* x, int64_t k, int64_t K, bool wide, float (&v)[8]) {
+// fp32: three columns `stride` bytes apart, each value's leading bf16 part (its high half), that of the rest,
+// and the last, which leaves nothing.  What is not finite has no further parts.
+__device__ __forceinline__ void stage_eight(const float* x, int64_t k, int64_t K, bool wide, char* to,
+                                            int stride) {
+  float v[8];
   if (wide && k + 8 <= K) {
     const float4 a = *reinterpret_cast<const float4*>(x + k), b = *reinterpret_cast<const float4*>(x + k + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
@@ -87,57 +121,74 @@ __device__ __forceinline__ void load_tokens(const float* x, int64_t k, int64_t K
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = k + j < K ? x[k + j] : 0.f;
   }
-}
-// The leading bf16 part of each value (its high half), which is taken off it.  What is not finite has no
-// further parts.
-__device__ __forceinline__ uint4 part_of(float (&v)[8]) {
-  uint32_t h[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    h[j] = __float_as_uint(v[j]) & 0xffff0000u;
-    if ((h[j] & 0x7f800000u) == 0x7f800000u) {
-      if (v[j] != v[j]) h[j] = 0x7fc00000u;  // a NaN whose high bits alone might read as infinity
-      v[j] = 0.f;
-    } else {
-      v[j] -= __uint_as_float(h[j]);
+  for (int p = 0; p < 3; ++p) {
+    uint32_t h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[j] = __float_as_uint(v[j]) & 0xffff0000u;
+      if ((h[j] & 0x7f800000u) == 0x7f800000u) {
+        if (v[j] != v[j]) h[j] = 0x7fc00000u;  // a NaN whose high bits alone might read as infinity
+        v[j] = 0.f;
+      } else {
+        v[j] -= __uint_as_float(h[j]);
+      }
     }
+    *reinterpret_cast<uint4*>(to + p * stride) = make_uint4(high_halves(h[0], h[4]), high_halves(h[1], h[5]),
+                                                            high_halves(h[2], h[6]), high_halves(h[3], h[7]));
   }
-  return make_uint4(two(h[0], h[4]), two(h[1], h[5]), two(h[2], h[6]), two(h[3], h[7]));
+}
+template <typename X>
+__device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, int first, int eighths,
+                                             int stride, char* smem) {
+  const int all = (int)a.M * eighths;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    const int m = a.M == 1 ? 0 : (int)((uint32_t)i / (uint32_t)eighths), q = i - m * eighths;
+    stage_eight(x + m * a.ldx, (int64_t)first * kTileCols + 8 * q, a.K, a.wide,
+                smem + m * (sizeof(X) == 2 ? 1 : 3) * stride + q * 16, stride);
+  }
 }
 
 // NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero points given.
 template <int NT, int G, bool ZEROS>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) gemv_w4_kernel(GemvW4Args a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(GemvW4Args a) {
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int WK = a.wk, WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
   const int64_t rb = (int64_t)blockIdx.x * WR + wr;
   const bool live = rb < a.RB;
   const int KB = (int)a.KB, per = a.per, chunk = per * WK;  // tiles: of K, of a warp and of a CTA a piece
-  const uint8_t* const codes = a.codes + (live ? rb : 0) * KB * kTileBytes + lane * 16;
-  const int64_t r0 = min(rb * kTileRows + g, a.N - 1), r1 = min(rb * kTileRows + g + 8, a.N - 1);
   const int cols = a.cols, stride = chunk * kTileCols * 2 + 64;  // bytes of a column in shared memory
 
-  // Tile i of the warp's, in K's pieces one after the other.
-  auto tile_of = [&](int i) { return i / per * chunk + wk * per + i % per; };
+  const uint32_t smem_addr = (uint32_t)__cvta_generic_to_shared(smem);
+  // The rows' scales and zero points of a piece, after the tokens: a word for each group of a tile (for
+  // each tile, where groups are longer) and row of the CTA's, the scale above 128 + zero.
+  const int rows = kTileRows * WR, words_at = cols * stride;
+
+  // The warp's tiles in the order it takes them: `next` is read next, the piece's number `place`.
   struct Tile {
-    uint4 lo, hi;         // rows g and g + 8
-    uint32_t scale, zero; // of group t, row g in the low part
+    uint4 lo, hi;  // rows g and g + 8
   };
-  auto load = [&](int i, Tile& o) {
-    const int kb = tile_of(i);
-    if (!live || kb >= KB) return;
-    o.lo = load_codes(codes + (int64_t)kb * kTileBytes);
-    o.hi = load_codes(codes + (int64_t)kb * kTileBytes + 512);
-    if (t < G) {
-      const int64_t j = min(G == 1 ? kb / a.group_tiles : kb * G + t, a.groups - 1) * a.N;
-      o.scale = a.scales[j + r0] | (uint32_t)a.scales[j + r1] << 16;
-      if (ZEROS) o.zero = a.zeros[j + r0] | (uint32_t)a.zeros[j + r1] << 16;
+  int next = live ? wk * per : KB, place = 0;
+  const int skip = chunk - per;
+  const uint8_t* codes = a.codes + ((live ? rb : 0) * KB + wk * per) * kTileBytes + lane * 16;
+  auto load = [&](Tile& o) {
+    if (next < KB) {
+      o.lo = load_codes(codes);
+      o.hi = load_codes(codes + 512);
+    }
+    next += 1;
+    codes += kTileBytes;
+    if (++place == per) {
+      place = 0;
+      next += skip;
+      codes += (int64_t)skip * kTileBytes;
     }
   };
   Tile ring[kDeep];
 #pragma unroll
-  for (int d = 0; d < kDeep; ++d) load(d, ring[d]);
+  for (int d = 0; d < kDeep; ++d) load(ring[d]);
 
   float acc[NT][4];
 #pragma unroll
@@ -145,39 +196,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) gemv_w4_kernel(Gemv
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 
+  // Lanes of columns that are not there read the last one: what they make of it is dropped.
+  uint32_t xs[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    xs[n] = smem_addr + min(8 * n + g, cols - 1) * stride + t * 16;
+  const uint32_t words = smem_addr + words_at + (wr * kTileRows + g) * 4;
   auto use = [&](const Tile& v, int at) {  // `at`: the tile's place in the piece
-    const char* const xs = smem + g * stride + at * kTileCols * 2 + t * 16;
     const uint32_t lo[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w}, hi[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
     float sum[NT][4];
+    uint32_t w0 = 0, w1 = 0, off0 = 0x43084308u, off1 = off0;  // 128 + 8
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       constexpr int per_group = 4 / G;
-      const int from = (lane & ~3) | j / per_group;
-      uint32_t off0 = 0x43084308u, off1 = off0;  // 128 + 8
-      if (ZEROS) {
-        const uint32_t z = __shfl_sync(0xffffffffu, v.zero, from);
-        off0 = 0x43004300u | (z & 0xffu) * 0x10001u;
-        off1 = 0x43004300u | (z >> 16) * 0x10001u;
+      if (j % per_group == 0) {
+        const uint32_t from = words + (at * G + j / per_group) * rows * 4;
+        w0 = load_shared1(from);
+        w1 = load_shared1(from + 32);
+        if (ZEROS) {
+          off0 = __byte_perm(w0, w0, 0x1010);
+          off1 = __byte_perm(w1, w1, 0x1010);
+        }
       }
       uint32_t p[4], q[4];
       decode(lo[j], off0, p);
       decode(hi[j], off1, q);
-      if (j % per_group == 0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum[n][e] = 0.f;
-      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (8 * n + g < cols) b = *reinterpret_cast<const uint4*>(xs + 8 * n * stride + j * 64);
-        product(sum[n], p[0], q[0], p[1], q[1], b.x, b.y);
-        product(sum[n], p[2], q[2], p[3], q[3], b.z, b.w);
+        const uint4 b = load_shared(xs[n] + at * kTileCols * 2 + j * 64);
+        if (j % per_group == 0)
+          product<true>(sum[n], p[0], q[0], p[1], q[1], b.x, b.y);
+        else
+          product<false>(sum[n], p[0], q[0], p[1], q[1], b.x, b.y);
+        product<false>(sum[n], p[2], q[2], p[3], q[3], b.z, b.w);
       }
       if (j % per_group == per_group - 1) {
-        const uint32_t s = __shfl_sync(0xffffffffu, v.scale, from);
-        const float s0 = __uint_as_float(s << 16), s1 = __uint_as_float(s & 0xffff0000u);
+        const float s0 = __uint_as_float(w0 & 0xffff0000u), s1 = __uint_as_float(w1 & 0xffff0000u);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           acc[n][0] = fmaf(s0, sum[n][0], acc[n][0]);
@@ -188,22 +242,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) gemv_w4_kernel(Gemv
       }
     }
   };
-  // The piece of the tokens from tile `first` on into shared memory.
+  // The piece of the tokens and scales from tile `first` on into shared memory.
   auto stage = [&](int first) {
-    const int eighths = min(chunk, KB - first) * (kTileCols / 8);
-    for (int m = 0; m < (int)a.M; ++m) {
-      char* const xs = smem + m * a.parts * stride;
+    const int tiles = min(chunk, KB - first);
+    if (a.x_bf16)
+      stage_tokens(a, static_cast<const __nv_bfloat16*>(a.x), first, tiles * (kTileCols / 8), stride, smem);
+    else
+      stage_tokens(a, static_cast<const float*>(a.x), first, tiles * (kTileCols / 8), stride, smem);
+    const int shift = 31 - __clz(rows);
+    const int64_t row0 = (int64_t)blockIdx.x * rows;
+    uint32_t* const to = reinterpret_cast<uint32_t*>(smem + words_at);
 #pragma unroll 4
-      for (int q = threadIdx.x; q < eighths; q += kThreads) {
-        const int64_t k = (int64_t)first * kTileCols + 8 * q;
-        float v[8];
-        if (a.x_bf16)
-          load_tokens(static_cast<const __nv_bfloat16*>(a.x) + m * a.ldx, k, a.K, a.wide, v);
-        else
-          load_tokens(static_cast<const float*>(a.x) + m * a.ldx, k, a.K, a.wide, v);
-        for (int p = 0; p < a.parts; ++p)
-          *reinterpret_cast<uint4*>(xs + p * stride + q * 16) = part_of(v);
+    for (int i = threadIdx.x; i < tiles * G * rows; i += kThreads) {
+      const int e = i >> shift;
+      const int64_t n = row0 + (i & (rows - 1));
+      const int j = G > 1 ? first * G + e : a.group_tiles == 1 ? first + e : (first + e) / a.group_tiles;
+      uint32_t v = 0x4308u;
+      if (n < a.N && j < a.groups) {
+        v = (uint32_t)a.scales[j * a.N + n] << 16;
+        if (ZEROS) v |= 0x4300u + a.zeros[j * a.N + n];
       }
+      to[i] = v;
     }
   };
 
@@ -218,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) gemv_w4_kernel(Gemv
           __syncthreads();
         }
         if (live && first + wk * per + at < KB) use(ring[d], wk * per + at);
-        load(i + d + kDeep, ring[d]);
+        load(ring[d]);
         if (++at == per) {
           at = 0;
           first += chunk;
@@ -359,13 +418,16 @@ cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   // parts of K: as many as leave no more CTAs than an SM holds four of
   a.wk = 1;
   while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= 4 * sms) a.wk *= 2;
-  const int64_t all = (a.KB + a.wk - 1) / a.wk;  // tiles of a warp
-  const int64_t room = (a.cols <= 8 ? kStageBytes : kWideStageBytes) / a.cols - 64;
-  const int64_t most = room / (2 * kTileCols * a.wk);
-  a.per = (int)(all < most ? all : most < 1 ? 1 : most);
+  // Tiles of a warp in a piece: all, or a power of two such that the piece's tokens fit.
+  const int64_t all = (a.KB + a.wk - 1) / a.wk, room = a.cols <= 8 ? kStageBytes : kWideStageBytes;
+  a.per = 16;
+  while (a.per > 1 && a.cols * (a.per * a.wk * kTileCols * 2 + 64) > room) a.per /= 2;
+  if (a.per > all) a.per = (int)all;
   const int64_t wr = kWarps / a.wk;
   const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
-  const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64);
+  const int in_tile = a.group < kTileCols ? (int)(kTileCols / a.group) : 1;
+  const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64) +
+                   a.per * a.wk * in_tile * (int)wr * kTileRows * 4;
   const int sums = kWarps * a.cols * kRedRow * (int)sizeof(float), smem = held > sums ? held : sums;
   const int nt = (a.cols + 7) / 8;
   return nt == 1   ? run_g<1>(a, grid, smem, s)
