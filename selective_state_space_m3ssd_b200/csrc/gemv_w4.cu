@@ -30,19 +30,21 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kTileRows = 16, kTileCols = 128, kTileBytes = 1024;
 constexpr int kRedRow = kTileRows + 1;
 
-// Tiles of codes in flight a warp.
+// Tiles of codes in a warp's ring, copied ahead.
 #ifndef N1
 #define N1 4
-#define DP 1
+#define DP 3
+#define PM 8
 #endif
 constexpr int kDeep = DP;
 
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint4 load_shared(uint32_t addr) {
@@ -93,8 +95,7 @@ __device__ __forceinline__ void product(float (&d)[4], uint32_t a0, uint32_t a1,
 // the pairs (i, i + 4).
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
-__device__ __forceinline__ void stage_eight(const __nv_bfloat16* x, int64_t k, int64_t K, bool wide, char* to,
-                                            int) {
+__device__ __forceinline__ void stage_eight(const __nv_bfloat16* x, int k, int K, bool wide, char* to, int) {
   uint4 u;
   if (wide && k + 8 <= K) {
     u = *reinterpret_cast<const uint4*>(x + k);
@@ -110,8 +111,7 @@ __device__ __forceinline__ void stage_eight(const __nv_bfloat16* x, int64_t k, i
 }
 // fp32: three columns `stride` bytes apart, each value's leading bf16 part (its high half), that of the rest,
 // and the last, which leaves nothing.  What is not finite has no further parts.
-__device__ __forceinline__ void stage_eight(const float* x, int64_t k, int64_t K, bool wide, char* to,
-                                            int stride) {
+__device__ __forceinline__ void stage_eight(const float* x, int k, int K, bool wide, char* to, int stride) {
   float v[8];
   if (wide && k + 8 <= K) {
     const float4 a = *reinterpret_cast<const float4*>(x + k), b = *reinterpret_cast<const float4*>(x + k + 4);
@@ -138,20 +138,68 @@ __device__ __forceinline__ void stage_eight(const float* x, int64_t k, int64_t K
                                                             high_halves(h[2], h[6]), high_halves(h[3], h[7]));
   }
 }
+// The tokens' columns of `tiles` tiles from tile `first` on.  A piece's eights are a power of two but for the
+// last one's.
 template <typename X>
-__device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, int first, int eighths,
+__device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, int first, int tiles,
                                              int stride, char* smem) {
-  const int all = (int)a.M * eighths;
+  const int eighths = tiles * (kTileCols / 8), shift = 31 - __clz(eighths);
+  const int all = (int)a.M * eighths, k0 = first * kTileCols;
+  const bool even = (eighths & (eighths - 1)) == 0;
 #pragma unroll 4
   for (int i = threadIdx.x; i < all; i += kThreads) {
-    const int m = a.M == 1 ? 0 : (int)((uint32_t)i / (uint32_t)eighths), q = i - m * eighths;
-    stage_eight(x + m * a.ldx, (int64_t)first * kTileCols + 8 * q, a.K, a.wide,
+    const int m = even ? i >> shift : (int)((uint32_t)i / (uint32_t)eighths), q = i - m * eighths;
+    stage_eight(x + m * a.ldx, k0 + 8 * q, (int)a.K, a.wide,
                 smem + m * (sizeof(X) == 2 ? 1 : 3) * stride + q * 16, stride);
   }
 }
 
-// NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero points given.
-template <int NT, int G, bool ZEROS>
+// The words of scales and zero points of `count` groups from group `first` on (`repeat` words each: a long
+// group's, for each of its tiles from number `first` on) for `rows` rows from row0 on.
+template <bool ZEROS>
+__device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int count, int repeat,
+                                            int64_t row0, int rows, uint32_t* to) {
+  const int shift = 31 - __clz(rows) - 3;  // eights of rows
+  const bool wide = a.wide_scales && row0 + rows <= a.N;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < count << shift; i += kThreads) {
+    const int e = i >> shift, r = 8 * (i & ((1 << shift) - 1));
+    const int j = repeat == 1 ? first + e : (first + e) / repeat;
+    const int64_t at = j * a.N + row0 + r;
+    uint32_t s[4] = {0, 0, 0, 0}, z[2] = {0, 0};
+    if (j < a.groups) {
+      if (wide) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a.scales + at);
+        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+        if (ZEROS) {
+          const uint2 u = *reinterpret_cast<const uint2*>(a.zeros + at);
+          z[0] = u.x, z[1] = u.y;
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const bool in = row0 + r + h < a.N;
+          s[h / 2] |= in ? (uint32_t)a.scales[at + h] << (16 * (h & 1)) : 0u;
+          if (ZEROS) z[h / 4] |= in ? (uint32_t)a.zeros[at + h] << (8 * (h & 3)) : 0u;
+        }
+      }
+    }
+    uint32_t w[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      // the zero's byte under 0x43, with the scale above them
+      const uint32_t low = ZEROS ? __byte_perm(z[h / 4], 0x43u, 0x0040u | (h & 3)) : 0u;
+      w[h] = __byte_perm(low, s[h / 2], h & 1 ? 0x7610 : 0x5410);
+    }
+    uint4* const out = reinterpret_cast<uint4*>(to + e * rows + r);
+    out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// X: the tokens' type; NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero
+// points given.
+template <typename X, int NT, int G, bool ZEROS>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(GemvW4Args a) {
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -166,18 +214,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
   // each tile, where groups are longer) and row of the CTA's, the scale above 128 + zero.
   const int rows = kTileRows * WR, words_at = cols * stride;
 
-  // The warp's tiles in the order it takes them: `next` is read next, the piece's number `place`.
-  struct Tile {
-    uint4 lo, hi;  // rows g and g + 8
-  };
+  // The warp's tiles in the order it takes them: `next` is copied next, the piece's number `place`.
+  // A lane copies what it reads: 16 bytes of row g, and of row g + 8.
+  char* const ring = smem + words_at + a.per * WK * G * rows * 4 + (warp * kDeep * 2 * 32 + lane) * 16;
+  const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
   int next = live ? wk * per : KB, place = 0;
   const int skip = chunk - per;
   const uint8_t* codes = a.codes + ((live ? rb : 0) * KB + wk * per) * kTileBytes + lane * 16;
-  auto load = [&](Tile& o) {
+  auto copy = [&](int d) {
     if (next < KB) {
-      o.lo = load_codes(codes);
-      o.hi = load_codes(codes + 512);
+      copy_codes(ring_addr + d * kTileBytes, codes);
+      copy_codes(ring_addr + d * kTileBytes + 512, codes + 512);
     }
+    copies_end();
     next += 1;
     codes += kTileBytes;
     if (++place == per) {
@@ -186,9 +235,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
       codes += (int64_t)skip * kTileBytes;
     }
   };
-  Tile ring[kDeep];
 #pragma unroll
-  for (int d = 0; d < kDeep; ++d) load(ring[d]);
+  for (int d = 0; d < kDeep - 1; ++d) copy(d);
 
   float acc[NT][4];
 #pragma unroll
@@ -202,8 +250,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
   for (int n = 0; n < NT; ++n)
     xs[n] = smem_addr + min(8 * n + g, cols - 1) * stride + t * 16;
   const uint32_t words = smem_addr + words_at + (wr * kTileRows + g) * 4;
-  auto use = [&](const Tile& v, int at) {  // `at`: the tile's place in the piece
-    const uint32_t lo[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w}, hi[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+  auto use = [&](int d, int at) {  // the ring's tile d; `at`: the tile's place in the piece
+    const uint4 vlo = *reinterpret_cast<const uint4*>(ring + d * kTileBytes);
+    const uint4 vhi = *reinterpret_cast<const uint4*>(ring + d * kTileBytes + 512);
+    const uint32_t lo[4] = {vlo.x, vlo.y, vlo.z, vlo.w}, hi[4] = {vhi.x, vhi.y, vhi.z, vhi.w};
     float sum[NT][4];
     uint32_t w0 = 0, w1 = 0, off0 = 0x43084308u, off1 = off0;  // 128 + 8
 #pragma unroll
@@ -245,46 +295,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
   // The piece of the tokens and scales from tile `first` on into shared memory.
   auto stage = [&](int first) {
     const int tiles = min(chunk, KB - first);
-    if (a.x_bf16)
-      stage_tokens(a, static_cast<const __nv_bfloat16*>(a.x), first, tiles * (kTileCols / 8), stride, smem);
-    else
-      stage_tokens(a, static_cast<const float*>(a.x), first, tiles * (kTileCols / 8), stride, smem);
-    const int shift = 31 - __clz(rows);
-    const int64_t row0 = (int64_t)blockIdx.x * rows;
-    uint32_t* const to = reinterpret_cast<uint32_t*>(smem + words_at);
-#pragma unroll 4
-    for (int i = threadIdx.x; i < tiles * G * rows; i += kThreads) {
-      const int e = i >> shift;
-      const int64_t n = row0 + (i & (rows - 1));
-      const int j = G > 1 ? first * G + e : a.group_tiles == 1 ? first + e : (first + e) / a.group_tiles;
-      uint32_t v = 0x4308u;
-      if (n < a.N && j < a.groups) {
-        v = (uint32_t)a.scales[j * a.N + n] << 16;
-        if (ZEROS) v |= 0x4300u + a.zeros[j * a.N + n];
-      }
-      to[i] = v;
-    }
+    stage_tokens(a, static_cast<const X*>(a.x), first, tiles, stride, smem);
+    stage_words<ZEROS>(a, first * G, tiles * G, a.group_tiles, (int64_t)blockIdx.x * rows, rows,
+                       reinterpret_cast<uint32_t*>(smem + words_at));
   };
 
-  const int total = (KB + chunk - 1) / chunk * per;
-  for (int i = 0, first = 0, at = 0; i < total; i += kDeep) {
-#pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      if (i + d < total) {
-        if (at == 0) {  // a new piece
-          if (first > 0) __syncthreads();
-          stage(first);
-          __syncthreads();
-        }
-        if (live && first + wk * per + at < KB) use(ring[d], wk * per + at);
-        load(ring[d]);
-        if (++at == per) {
-          at = 0;
-          first += chunk;
-        }
-      }
+  int d = 0;  // the ring's tile that is used next; the one before it is free
+  for (int first = 0; first < KB; first += chunk) {
+    if (first > 0) __syncthreads();
+    stage(first);
+    __syncthreads();
+    const int mine = live ? KB - first - wk * per : 0;
+    for (int at = 0; at < per; ++at) {
+      copies_wait<kDeep - 2>();
+      copy(d == 0 ? kDeep - 1 : d - 1);
+      if (at < mine) use(d, wk * per + at);
+      d = d == kDeep - 1 ? 0 : d + 1;
     }
   }
+  copies_wait<0>();
 
   // the tile's sums: over the parts of K, and of a token
   __syncthreads();
@@ -385,23 +414,23 @@ __global__ void __launch_bounds__(kThreads) w4_dequant_kernel(W4Args a, T* w, in
 // Columns in shared memory a CTA: few CTAs' worth of a whole K, or pieces of it.
 constexpr int kStageBytes = 36 * 1024, kWideStageBytes = 72 * 1024;
 
-template <int NT, int G, bool ZEROS>
+template <typename X, int NT, int G, bool ZEROS>
 cudaError_t run(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(gemv_w4_kernel<NT, G, ZEROS>,
+  const cudaError_t e = cudaFuncSetAttribute(gemv_w4_kernel<X, NT, G, ZEROS>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  gemv_w4_kernel<NT, G, ZEROS><<<grid, kThreads, smem, s>>>(a);
+  gemv_w4_kernel<X, NT, G, ZEROS><<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
-template <int NT, int G>
-cudaError_t run_z(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
-  return a.zeros ? run<NT, G, true>(a, grid, smem, s) : run<NT, G, false>(a, grid, smem, s);
-}
-template <int NT>
+template <typename X, int NT>
 cudaError_t run_g(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
-  return a.group == 32   ? run_z<NT, 4>(a, grid, smem, s)
-         : a.group == 64 ? run_z<NT, 2>(a, grid, smem, s)
-                         : run_z<NT, 1>(a, grid, smem, s);
+  if (a.zeros)
+    return a.group == 32   ? run<X, NT, 4, true>(a, grid, smem, s)
+           : a.group == 64 ? run<X, NT, 2, true>(a, grid, smem, s)
+                           : run<X, NT, 1, true>(a, grid, smem, s);
+  return a.group == 32   ? run<X, NT, 4, false>(a, grid, smem, s)
+         : a.group == 64 ? run<X, NT, 2, false>(a, grid, smem, s)
+                         : run<X, NT, 1, false>(a, grid, smem, s);
 }
 
 }  // namespace
@@ -413,27 +442,31 @@ cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   a.cols = (int)a.M * a.parts;
   a.RB = (a.N + kTileRows - 1) / kTileRows;
   a.KB = (a.K + kTileCols - 1) / kTileCols;
-  a.group_tiles = (int)(a.group / kTileCols);
+  a.group_tiles = a.group < kTileCols ? 1 : (int)(a.group / kTileCols);
+  a.wide_scales = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
+                  reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
   a.wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % (a.x_bf16 ? 8 : 4) == 0;
   // parts of K: as many as leave no more CTAs than an SM holds four of
   a.wk = 1;
   while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= 4 * sms) a.wk *= 2;
   // Tiles of a warp in a piece: all, or a power of two such that the piece's tokens fit.
   const int64_t all = (a.KB + a.wk - 1) / a.wk, room = a.cols <= 8 ? kStageBytes : kWideStageBytes;
-  a.per = 16;
+  a.per = PM;
   while (a.per > 1 && a.cols * (a.per * a.wk * kTileCols * 2 + 64) > room) a.per /= 2;
   if (a.per > all) a.per = (int)all;
   const int64_t wr = kWarps / a.wk;
   const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
   const int in_tile = a.group < kTileCols ? (int)(kTileCols / a.group) : 1;
   const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64) +
-                   a.per * a.wk * in_tile * (int)wr * kTileRows * 4;
+                   a.per * a.wk * in_tile * (int)wr * kTileRows * 4 + kWarps * kDeep * kTileBytes;
   const int sums = kWarps * a.cols * kRedRow * (int)sizeof(float), smem = held > sums ? held : sums;
   const int nt = (a.cols + 7) / 8;
-  return nt == 1   ? run_g<1>(a, grid, smem, s)
-         : nt == 2 ? run_g<2>(a, grid, smem, s)
-         : nt <= 4 ? run_g<4>(a, grid, smem, s)
-                   : run_g<6>(a, grid, smem, s);
+  if (a.x_bf16)
+    return nt == 1 ? run_g<__nv_bfloat16, 1>(a, grid, smem, s) : run_g<__nv_bfloat16, 2>(a, grid, smem, s);
+  return nt == 1   ? run_g<float, 1>(a, grid, smem, s)
+         : nt == 2 ? run_g<float, 2>(a, grid, smem, s)
+         : nt <= 4 ? run_g<float, 4>(a, grid, smem, s)
+                   : run_g<float, 6>(a, grid, smem, s);
 }
 
 cudaError_t launch_w4_quant(const W4Args& a, bool bf16, const void* w, int64_t ldw, cudaStream_t s) {
