@@ -7,9 +7,10 @@
 // latency.  A warp takes tiles of 16 rows by 128 columns, 1 KB of codes that its lanes read as two
 // 16-byte words each, in the order that a lane needs them as an operand of the (legacy) warp-wide
 // bf16 product of 16 x 16 weights by 16 x 8 tokens: the k order within a product is free as long as
-// both operands share it.  A code n becomes the bf16 number 128 + n by setting bits, less 128 + zero
-// exactly, so nothing is rounded before the products' fp32 sums; a group's sums are scaled in
-// fp32.  tcgen05 is not for this: its operands would have to go through shared or tensor memory, and
+// both operands share it.  Codes masked out of a word are read as bf16 numbers as they are: bits 0 to 7
+// of one are linear, n 2^-133, through its subnormals and first binade, so one multiply-add makes
+// (n - zero) 2^-6 of it, exactly, wherever in those bits the code lies, and nothing is rounded
+// before the products' fp32 sums; a group's sums are scaled in fp32, and the 2^6 comes last.  tcgen05 is not for this: its operands would have to go through shared or tensor memory, and
 // at 16 tokens the products are a tenth of the time the codes take to arrive.
 //
 // fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
@@ -61,16 +62,20 @@ __device__ __forceinline__ uint32_t load_shared1(uint32_t addr) {
   return v;
 }
 
-// The pairs of codes (i, i + 4), i = 0 to 3, of a word of eight, less 128 + zero, as bf16 pairs.
+// The pairs of codes (i, i + 4), i = 0 to 3, of a word of eight, less the zero point, as bf16 pairs of
+// (code - zero) / 64; `offset` is -zero / 64 twice.
+__device__ __forceinline__ uint32_t scaled(uint32_t codes, uint32_t by, uint32_t offset) {
+  uint32_t o;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(codes), "r"(by), "r"(offset));
+  return o;
+}
+constexpr float kUnit = 64.f;
 __device__ __forceinline__ void decode(uint32_t w, uint32_t offset, uint32_t (&o)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t n;  // 128 + code: (w >> 4 i & 0x000f000f) | 0x43004300, the two in one operation
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(n) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&n),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&offset));
-    o[i] = *reinterpret_cast<const uint32_t*>(&d);
-  }
+  const uint32_t v = w >> 8, low = 0x7f007f00u, high = 0x7d007d00u;  // 2^127, 2^123
+  o[0] = scaled(w & 0x000f000fu, low, offset);
+  o[1] = scaled(w & 0x00f000f0u, high, offset);
+  o[2] = scaled(v & 0x000f000fu, low, offset);
+  o[3] = scaled(v & 0x00f000f0u, high, offset);
 }
 
 // d += a b, or d = a b where NEW.
@@ -138,33 +143,34 @@ __device__ __forceinline__ void stage_eight(const float* x, int k, int K, bool w
                                                             high_halves(h[2], h[6]), high_halves(h[3], h[7]));
   }
 }
-// The tokens' columns of `tiles` tiles from tile `first` on.  A piece's eights are a power of two but for the
-// last one's.
+// A piece of the tokens: for each part of K the columns of `per` (a power of two) tiles from the part's
+// tile number `first` on.
 template <typename X>
-__device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, int first, int tiles,
-                                             int stride, char* smem) {
-  const int eighths = tiles * (kTileCols / 8), shift = 31 - __clz(eighths);
-  const int all = (int)a.M * eighths, k0 = first * kTileCols;
-  const bool even = (eighths & (eighths - 1)) == 0;
+__device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, int first, int stride,
+                                             char* smem) {
+  const int in_part = 31 - __clz(a.per * (kTileCols / 8)), in_token = in_part + (31 - __clz(a.wk));
+  const int all = (int)a.M << in_token;
 #pragma unroll 4
   for (int i = threadIdx.x; i < all; i += kThreads) {
-    const int m = even ? i >> shift : (int)((uint32_t)i / (uint32_t)eighths), q = i - m * eighths;
-    stage_eight(x + m * a.ldx, k0 + 8 * q, (int)a.K, a.wide,
-                smem + m * (sizeof(X) == 2 ? 1 : 3) * stride + q * 16, stride);
+    const int m = i >> in_token, q = i & ((1 << in_token) - 1);
+    const int k = ((q >> in_part) * a.part + first) * kTileCols + 8 * (q & ((1 << in_part) - 1));
+    stage_eight(x + m * a.ldx, k, (int)a.K, a.wide, smem + m * (sizeof(X) == 2 ? 1 : 3) * stride + q * 16,
+                stride);
   }
 }
 
-// The words of scales and zero points of `count` groups from group `first` on (`repeat` words each: a long
-// group's, for each of its tiles from number `first` on) for `rows` rows from row0 on.
-template <bool ZEROS>
-__device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int count, int repeat,
-                                            int64_t row0, int rows, uint32_t* to) {
-  const int shift = 31 - __clz(rows) - 3;  // eights of rows
+// The words of scales and zero points of the same tiles, `G` a tile (a longer group's in each of its tiles), for
+// `rows` rows from row0 on: the scale above -zero / 64, both bf16.
+template <int G, bool ZEROS>
+__device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int64_t row0, int rows,
+                                            uint32_t* to) {
+  const int shift = 31 - __clz(rows) - 3, in_part = 31 - __clz(a.per);  // eights of rows; tiles
   const bool wide = a.wide_scales && row0 + rows <= a.N;
 #pragma unroll 2
-  for (int i = threadIdx.x; i < count << shift; i += kThreads) {
+  for (int i = threadIdx.x; i < (a.wk * a.per * G) << shift; i += kThreads) {
     const int e = i >> shift, r = 8 * (i & ((1 << shift) - 1));
-    const int j = repeat == 1 ? first + e : (first + e) / repeat;
+    const int place = e / G, tile = (place >> in_part) * a.part + first + (place & (a.per - 1));
+    const int j = G > 1 ? tile * G + e % G : a.group_tiles == 1 ? tile : tile / a.group_tiles;
     const int64_t at = j * a.N + row0 + r;
     uint32_t s[4] = {0, 0, 0, 0}, z[2] = {0, 0};
     if (j < a.groups) {
@@ -187,8 +193,9 @@ __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int 
     uint32_t w[8];
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      // the zero's byte under 0x43, with the scale above them
-      const uint32_t low = ZEROS ? __byte_perm(z[h / 4], 0x43u, 0x0040u | (h & 3)) : 0u;
+      // eight bits are exact in bf16: the high half of the fp32 number
+      const uint32_t low =
+          ZEROS ? __float_as_uint((float)(z[h / 4] >> (8 * (h & 3)) & 0xffu) * (-1.f / kUnit)) >> 16 : 0u;
       w[h] = __byte_perm(low, s[h / 2], h & 1 ? 0x7610 : 0x5410);
     }
     uint4* const out = reinterpret_cast<uint4*>(to + e * rows + r);
@@ -211,32 +218,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
 
   const uint32_t smem_addr = (uint32_t)__cvta_generic_to_shared(smem);
   // The rows' scales and zero points of a piece, after the tokens: a word for each group of a tile (for
-  // each tile, where groups are longer) and row of the CTA's, the scale above 128 + zero.
+  // each tile, where groups are longer) and row of the CTA's.
   const int rows = kTileRows * WR, words_at = cols * stride;
 
-  // The warp's tiles in the order it takes them: `next` is copied next, the piece's number `place`.
-  // A lane copies what it reads: 16 bytes of row g, and of row g + 8.
-  char* const ring = smem + words_at + a.per * WK * G * rows * 4 + (warp * kDeep * 2 * 32 + lane) * 16;
+  // The warp's tiles: `tiles` from number wk a.part of K on, `left` of them still to be copied.  A lane
+  // copies what it reads: 16 bytes of row g, and of row g + 8.
+  char* const ring = smem + words_at + chunk * G * rows * 4 + (warp * kDeep * 2 * 32 + lane) * 16;
   const uint32_t ring_addr = (uint32_t)__cvta_generic_to_shared(ring);
-  int next = live ? wk * per : KB, place = 0;
-  const int skip = chunk - per;
-  const uint8_t* codes = a.codes + ((live ? rb : 0) * KB + wk * per) * kTileBytes + lane * 16;
-  auto copy = [&](int d) {
-    if (next < KB) {
-      copy_codes(ring_addr + d * kTileBytes, codes);
-      copy_codes(ring_addr + d * kTileBytes + 512, codes + 512);
+  const int tiles = live ? max(min(KB - wk * a.part, a.part), 0) : 0;
+  int left = tiles;
+  const uint8_t* codes = a.codes + ((live ? rb : 0) * KB + wk * a.part) * kTileBytes + lane * 16;
+  auto copy = [&](int d) {  // d: bytes
+    if (left > 0) {
+      copy_codes(ring_addr + d, codes);
+      copy_codes(ring_addr + d + 512, codes + 512);
     }
     copies_end();
-    next += 1;
+    left -= 1;
     codes += kTileBytes;
-    if (++place == per) {
-      place = 0;
-      next += skip;
-      codes += (int64_t)skip * kTileBytes;
-    }
   };
 #pragma unroll
-  for (int d = 0; d < kDeep - 1; ++d) copy(d);
+  for (int d = 0; d < kDeep - 1; ++d) copy(d * kTileBytes);
 
   float acc[NT][4];
 #pragma unroll
@@ -250,12 +252,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
   for (int n = 0; n < NT; ++n)
     xs[n] = smem_addr + min(8 * n + g, cols - 1) * stride + t * 16;
   const uint32_t words = smem_addr + words_at + (wr * kTileRows + g) * 4;
-  auto use = [&](int d, int at) {  // the ring's tile d; `at`: the tile's place in the piece
-    const uint4 vlo = *reinterpret_cast<const uint4*>(ring + d * kTileBytes);
-    const uint4 vhi = *reinterpret_cast<const uint4*>(ring + d * kTileBytes + 512);
+  auto use = [&](int d, int at) {  // the ring's tile at byte d; `at`: the tile's place in the piece
+    const uint4 vlo = *reinterpret_cast<const uint4*>(ring + d);
+    const uint4 vhi = *reinterpret_cast<const uint4*>(ring + d + 512);
     const uint32_t lo[4] = {vlo.x, vlo.y, vlo.z, vlo.w}, hi[4] = {vhi.x, vhi.y, vhi.z, vhi.w};
     float sum[NT][4];
-    uint32_t w0 = 0, w1 = 0, off0 = 0x43084308u, off1 = off0;  // 128 + 8
+    uint32_t w0 = 0, w1 = 0, off0 = 0xbe00be00u, off1 = off0;  // -8 / 64
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       constexpr int per_group = 4 / G;
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
         product<false>(sum[n], p[2], q[2], p[3], q[3], b.z, b.w);
       }
       if (j % per_group == per_group - 1) {
-        const float s0 = __uint_as_float(w0 & 0xffff0000u), s1 = __uint_as_float(w1 & 0xffff0000u);
+        const float s0 = __uint_as_float(ZEROS ? w0 & 0xffff0000u : w0);
+        const float s1 = __uint_as_float(ZEROS ? w1 & 0xffff0000u : w1);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           acc[n][0] = fmaf(s0, sum[n][0], acc[n][0]);
@@ -292,25 +295,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
       }
     }
   };
-  // The piece of the tokens and scales from tile `first` on into shared memory.
-  auto stage = [&](int first) {
-    const int tiles = min(chunk, KB - first);
-    stage_tokens(a, static_cast<const X*>(a.x), first, tiles, stride, smem);
-    stage_words<ZEROS>(a, first * G, tiles * G, a.group_tiles, (int64_t)blockIdx.x * rows, rows,
-                       reinterpret_cast<uint32_t*>(smem + words_at));
-  };
-
   int d = 0;  // the ring's tile that is used next; the one before it is free
-  for (int first = 0; first < KB; first += chunk) {
+  for (int first = 0; first < a.part; first += per) {
     if (first > 0) __syncthreads();
-    stage(first);
+    stage_tokens(a, static_cast<const X*>(a.x), first, stride, smem);
+    stage_words<G, ZEROS>(a, first, (int64_t)blockIdx.x * rows, rows,
+                          reinterpret_cast<uint32_t*>(smem + words_at));
     __syncthreads();
-    const int mine = live ? KB - first - wk * per : 0;
-    for (int at = 0; at < per; ++at) {
+    const int n = min(tiles - first, per);
+    for (int at = 0; at < n; ++at) {
       copies_wait<kDeep - 2>();
-      copy(d == 0 ? kDeep - 1 : d - 1);
-      if (at < mine) use(d, wk * per + at);
-      d = d == kDeep - 1 ? 0 : d + 1;
+      copy(d == 0 ? (kDeep - 1) * kTileBytes : d - kTileBytes);
+      use(d, wk * per + at);
+      d = d == (kDeep - 1) * kTileBytes ? 0 : d + kTileBytes;
     }
   }
   copies_wait<0>();
@@ -335,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(Gem
     for (int p = 0; p < a.parts; ++p)
       for (int k = 0; k < WK; ++k)
         s += red[((w * WK + k) * cols + m * a.parts + p) * kRedRow + r];
+    s *= kUnit;
     if (a.out_bf16)
       static_cast<__nv_bfloat16*>(a.out)[m * a.ldd + n] = __float2bfloat16_rn(s);
     else
@@ -449,11 +447,11 @@ cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   // parts of K: as many as leave no more CTAs than an SM holds four of
   a.wk = 1;
   while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= 4 * sms) a.wk *= 2;
-  // Tiles of a warp in a piece: all, or a power of two such that the piece's tokens fit.
-  const int64_t all = (a.KB + a.wk - 1) / a.wk, room = a.cols <= 8 ? kStageBytes : kWideStageBytes;
-  a.per = PM;
-  while (a.per > 1 && a.cols * (a.per * a.wk * kTileCols * 2 + 64) > room) a.per /= 2;
-  if (a.per > all) a.per = (int)all;
+  // A part's tiles, and a power of two of them in a piece: all, as far as the piece's tokens fit.
+  a.part = (int)((a.KB + a.wk - 1) / a.wk);
+  const int64_t room = a.cols <= 8 ? kStageBytes : kWideStageBytes;
+  a.per = 1;
+  while (a.per < PM && a.per < a.part && a.cols * (2 * a.per * a.wk * kTileCols * 2 + 64) <= room) a.per *= 2;
   const int64_t wr = kWarps / a.wk;
   const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
   const int in_tile = a.group < kTileCols ? (int)(kTileCols / a.group) : 1;
