@@ -10,8 +10,9 @@
 // both operands share it.  Codes masked out of a word are read as bf16 numbers as they are: bits 0 to 7
 // of one are linear, n 2^-133, through its subnormals and first binade, so one multiply-add makes
 // (n - zero) 2^-6 of it, exactly, wherever in those bits the code lies, and nothing is rounded
-// before the products' fp32 sums; a group's sums are scaled in fp32, and the 2^6 comes last.  tcgen05 is not for this: its operands would have to go through shared or tensor memory, and
-// at 16 tokens the products are a tenth of the time the codes take to arrive.
+// before the products' fp32 sums; a group's sums are scaled in fp32, and the 2^6 comes last.  tcgen05
+// is not for this: its operands would have to go through shared or tensor memory, and the products
+// are a tenth of the time.
 //
 // fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
 // A CTA's eight warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
@@ -32,12 +33,7 @@ constexpr int kTileRows = 16, kTileCols = 128, kTileBytes = 1024;
 constexpr int kRedRow = kTileRows + 1;
 
 // Tiles of codes in a warp's ring, copied ahead.
-#ifndef N1
-#define N1 4
-#define DP 3
-#define PM 8
-#endif
-constexpr int kDeep = DP;
+constexpr int kDeep = 3;
 
 __device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src));
@@ -204,10 +200,14 @@ __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int6
   }
 }
 
+// CTAs an SM holds: 64 registers a thread for eight columns, 128 for 16, all there are for more.
+template <int NT>
+constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+
 // X: the tokens' type; NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero
 // points given.
 template <typename X, int NT, int G, bool ZEROS>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? N1 : 2) gemv_w4_kernel(GemvW4Args a) {
+__global__ void __launch_bounds__(kThreads, kCtas<NT>) gemv_w4_kernel(GemvW4Args a) {
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int WK = a.wk, WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
@@ -409,8 +409,8 @@ __global__ void __launch_bounds__(kThreads) w4_dequant_kernel(W4Args a, T* w, in
   }
 }
 
-// Columns in shared memory a CTA: few CTAs' worth of a whole K, or pieces of it.
-constexpr int kStageBytes = 36 * 1024, kWideStageBytes = 72 * 1024;
+// What the tokens' pieces may take of shared memory: four, two and one CTA an SM.
+constexpr int kStageBytes[3] = {36 * 1024, 72 * 1024, 150 * 1024};
 
 template <typename X, int NT, int G, bool ZEROS>
 cudaError_t run(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
@@ -444,21 +444,22 @@ cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   a.wide_scales = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
   a.wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % (a.x_bf16 ? 8 : 4) == 0;
-  // parts of K: as many as leave no more CTAs than an SM holds four of
+  // parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens)
+  const int nt = (a.cols + 7) / 8;
+  const int64_t ctas = sms * (nt == 1 ? kCtas<1> : nt == 2 ? kCtas<2> : kCtas<4>);
   a.wk = 1;
-  while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= 4 * sms) a.wk *= 2;
+  while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= ctas) a.wk *= 2;
   // A part's tiles, and a power of two of them in a piece: all, as far as the piece's tokens fit.
   a.part = (int)((a.KB + a.wk - 1) / a.wk);
-  const int64_t room = a.cols <= 8 ? kStageBytes : kWideStageBytes;
+  const int64_t room = kStageBytes[nt == 1 ? 0 : nt == 2 ? 1 : 2];
   a.per = 1;
-  while (a.per < PM && a.per < a.part && a.cols * (2 * a.per * a.wk * kTileCols * 2 + 64) <= room) a.per *= 2;
+  while (a.per < 8 && a.per < a.part && a.cols * (2 * a.per * a.wk * kTileCols * 2 + 64) <= room) a.per *= 2;
   const int64_t wr = kWarps / a.wk;
   const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
   const int in_tile = a.group < kTileCols ? (int)(kTileCols / a.group) : 1;
   const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64) +
                    a.per * a.wk * in_tile * (int)wr * kTileRows * 4 + kWarps * kDeep * kTileBytes;
   const int sums = kWarps * a.cols * kRedRow * (int)sizeof(float), smem = held > sums ? held : sums;
-  const int nt = (a.cols + 7) / 8;
   if (a.x_bf16)
     return nt == 1 ? run_g<__nv_bfloat16, 1>(a, grid, smem, s) : run_g<__nv_bfloat16, 2>(a, grid, smem, s);
   return nt == 1   ? run_g<float, 1>(a, grid, smem, s)
