@@ -363,12 +363,13 @@ def make_dims(batch, seqlen, nheads, headdim, dstate, ngroups, x_dtype, chunk=0,
 def _workspace(workspace, need: int, device):
     """A call's device scratch, allocated where the caller gave none: the tensor, its
     address and its bytes.  A caller's is one contiguous run of memory on ``device``."""
-    if workspace is None and need:
+    if workspace is None:
+        if not need:
+            return None, None, 0
         import torch
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     _need(workspace, "workspace", device=device)
-    if workspace is None:
-        return None, None, 0
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -1128,17 +1129,21 @@ def _bytes_of(t):
 def _glr_dims(x, r, i, rate, bias_r, bias_i, c):
     """Checks what the recurrence's calls share; its dims (seqlen 0 for a step)."""
     import torch
-    if not x.is_cuda:
+    shape, dt, index = x.shape, x.dtype, x.get_device()
+    if index < 0:
         raise ValueError("x must be a CUDA tensor")
-    f32, dev, index = torch.float32, x.device, x.get_device()
-    lead, D = x.shape[:-1], x.shape[-1]
-    xd = _xdtype(x)
-    ld = [_tokens_stride(t, n, x.dtype, lead, (D,), index) for t, n in ((x, "x"), (r, "r"), (i, "i"))]
     if rate is None:
         raise ValueError("rate is required")
-    _need_all(dev, (rate, "rate", f32, (D,)), (bias_r, "bias_r", f32, (D,)),
+    D, ld = shape[-1], []
+    for t, n in ((x, "x"), (r, "r"), (i, "i")):
+        if t.dtype == dt and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            ld.append(D)
+        else:
+            ld.append(_tokens_stride(t, n, dt, shape[:-1], (D,), index))
+    f32 = torch.float32
+    _need_all(x.device, (rate, "rate", f32, (D,)), (bias_r, "bias_r", f32, (D,)),
               (bias_i, "bias_i", f32, (D,)))
-    return GlrDims(lead[0], lead[1] if len(lead) == 2 else 0, D, *ld, xd, float(c), 0)
+    return GlrDims(shape[0], shape[1] if len(shape) == 3 else 0, D, ld[0], ld[1], ld[2], _xdtype(x), c, 0)
 
 
 def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None, reset=None,
@@ -1160,11 +1165,15 @@ def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None,
     reset = _bytes_of(reset)
     if y is None:
         y = torch.empty(b, L, D, dtype=x.dtype, device=dev)
-    if hT is None and want_hT:
+    else:
+        _need(y, "y", x.dtype, (b, L, D), dev)
+    if hT is not None:
+        _need(hT, "hT", f32, (b, D), dev)
+    elif want_hT:
         hT = torch.empty(b, D, dtype=f32, device=dev)
-    _need_all(dev, (h0, "h0", f32, (b, D)), (reset, "reset", torch.uint8, (b, L)),
-              (lengths, "lengths", torch.int32, (b,)), (y, "y", x.dtype, (b, L, D)),
-              (hT, "hT", f32, (b, D)))
+    if h0 is not None or reset is not None or lengths is not None:
+        _need_all(dev, (h0, "h0", f32, (b, D)), (reset, "reset", torch.uint8, (b, L)),
+                  (lengths, "lengths", torch.int32, (b,)))
     need = _on_device(dev, glr_fwd_workspace_size, dims)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_glr_fwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
@@ -1202,25 +1211,39 @@ def glr_bwd(x, r, i, rate, y, dy, *, bias_r=None, bias_i=None, c: float = 8.0, h
     if y is None or dy is None:
         raise ValueError("y and dy are required")
     _need_all(dev, (y, "y", x.dtype, (b, L, D)), (dy, "dy", x.dtype, (b, L, D)))
-    grads = dict(grads or {})
+    o = dict.fromkeys(GLR_GRAD_NAMES)
+    if grads:
+        for k in GLR_GRAD_NAMES:
+            o[k] = grads.get(k)
+        for k, shape in (("drate", (D,)), ("dbias_r", (D,)), ("dbias_i", (D,)), ("dh0", (b, D))):
+            if o[k] is not None:
+                _need(o[k], k, f32, shape, dev)
+    if o["dx"] is None and o["dr"] is None and o["di"] is None and b * L * D <= 1 << 18 and D % 8 == 0:
+        # one small allocation instead of three (a large one would live as long as any of them)
+        o["dx"], o["dr"], o["di"] = torch.empty(3, b, L, D, dtype=grad_dtype, device=dev).unbind(0)
     for k in ("dx", "dr", "di"):
-        if grads.get(k) is None:
-            grads[k] = torch.empty(b, L, D, dtype=grad_dtype, device=dev)
-    for k, shape in (("drate", (D,)), ("dbias_r", (D,)), ("dbias_i", (D,)), ("dh0", (b, D))):
-        if grads.get(k) is None:
-            grads[k] = torch.empty(shape, dtype=f32, device=dev)
-        else:
-            _need(grads[k], k, f32, shape, dev)
-    lds = {_tokens_stride(grads[k], k, grad_dtype, (b, L), (D,), dev.index) for k in ("dx", "dr", "di")}
-    if len(lds) != 1 and b * L > 1:
-        raise ValueError("dx, dr and di must have their rows the same distance apart")
-    g = GlrGrads(max(lds), _xdtype(grads["dx"]), 0, *(grads[k].data_ptr() for k in GLR_GRAD_NAMES))
+        if o[k] is None:
+            o[k] = torch.empty(b, L, D, dtype=grad_dtype, device=dev)
+    if o["drate"] is None and o["dbias_r"] is None and o["dbias_i"] is None:
+        o["drate"], o["dbias_r"], o["dbias_i"] = torch.empty(3, D, dtype=f32, device=dev).unbind(0)
+    for k in ("drate", "dbias_r", "dbias_i"):
+        if o[k] is None:
+            o[k] = torch.empty(D, dtype=f32, device=dev)
+    if o["dh0"] is None:
+        o["dh0"] = torch.empty(b, D, dtype=f32, device=dev)
+    ldg = D
+    if grads:
+        lds = {_tokens_stride(o[k], k, grad_dtype, (b, L), (D,), dev.index) for k in ("dx", "dr", "di")}
+        if len(lds) != 1 and b * L > 1:
+            raise ValueError("dx, dr and di must have their rows the same distance apart")
+        ldg = max(lds)
+    g = GlrGrads(ldg, _xdtype(o["dx"]), 0, *[t.data_ptr() for t in o.values()])
     need = _on_device(dev, glr_bwd_workspace_size, dims)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_glr_bwd", dev, ctypes.byref(dims), _addr(x), _addr(r), _addr(i), _addr(rate),
             _addr(bias_r), _addr(bias_i), _addr(h0), _addr(reset), _addr(lengths), _addr(y),
             _addr(dy), _addr(dhT), ctypes.byref(g), ws, ws_bytes)
-    return {k: grads[k] for k in GLR_GRAD_NAMES}
+    return o
 
 
 def glr_step(h, x_t, r_t, i_t, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h_out=None,
@@ -1236,9 +1259,15 @@ def glr_step(h, x_t, r_t, i_t, rate, *, bias_r=None, bias_i=None, c: float = 8.0
     dev, f32 = x_t.device, torch.float32
     if y_t is None:
         y_t = torch.empty(b, D, dtype=x_t.dtype, device=dev)
-    h_out = h if h_out is None else h_out
-    _need_all(dev, (h, "h", f32, (b, D)), (h_out, "h_out", f32, (b, D)),
-              (y_t, "y_t", x_t.dtype, (b, D)))
+    else:
+        _need(y_t, "y_t", x_t.dtype, (b, D), dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _need(h_out, "h_out", f32, (b, D), dev)
+    if h is None:
+        raise ValueError("h is required")
+    _need(h, "h", f32, (b, D), dev)
     _launch("m3ssd_glr_step", dev, ctypes.byref(dims), _addr(x_t), _addr(r_t), _addr(i_t),
             _addr(rate), _addr(bias_r), _addr(bias_i), _addr(h), _addr(h_out), _addr(y_t))
     return y_t, h_out
@@ -1251,23 +1280,23 @@ def _rotate_dims(q, k, q_w, k_w, positions, freqs, eps):
     import torch
     if q.dim() < 2 or (k is not None and k.dim() != q.dim()):
         raise ValueError("q and k must have shapes (..., heads, width), with the same tokens")
-    if not q.is_cuda:
+    dt, index = q.dtype, q.get_device()
+    if index < 0:
         raise ValueError("q must be a CUDA tensor")
-    f32, dev, index = torch.float32, q.device, q.get_device()
-    lead, (Hq, N) = q.shape[:-2], q.shape[-2:]
-    xd = _xdtype(q)
-    ldq = _tokens_stride(q, "q", q.dtype, lead, (Hq, N), index)
-    Hk = 0 if k is None else k.shape[-2]
-    ldk = 0 if k is None else _tokens_stride(k, "k", q.dtype, lead, (Hk, N), index)
+    f32, shape = torch.float32, q.shape
+    lead, Hq, N = shape[:-2], shape[-2], shape[-1]
+    ldq = Hq * N if q.is_contiguous() else _tokens_stride(q, "q", dt, lead, (Hq, N), index)
+    Hk = ldk = 0
+    if k is not None:
+        Hk = k.shape[-2]
+        ldk = _tokens_stride(k, "k", dt, lead, (Hk, N), index)
     if (positions is None) != (freqs is None):
         raise ValueError("positions and freqs are given together")
     R = 0 if freqs is None else freqs.shape[0]
-    rows = 1
-    for n in lead:
-        rows *= n
-    _need_all(dev, (q_w, "q_w", f32, (N,)), (k_w, "k_w", f32, (N,)),
+    rows = lead.numel()
+    _need_all(q.device, (q_w, "q_w", f32, (N,)), (k_w, "k_w", f32, (N,)),
               (positions, "positions", torch.int32, lead), (freqs, "freqs", f32, (R,)))
-    return RotateDims(rows, Hq, Hk, N, R, ldq, ldk, xd, eps, 0), lead
+    return RotateDims(rows, Hq, Hk, N, R, ldq, ldk, _xdtype(q), eps, 0), lead
 
 
 def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, eps: float = 1e-6,
@@ -1283,14 +1312,17 @@ def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, ep
     dev = q.device
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if k_out is None and k is not None:
+    else:
+        _need(q_out, "q_out", q.dtype, q.shape, dev)
+    if k is None:
+        k_out = None
+    elif k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    _need_all(dev, (q_out, "q_out", q.dtype, q.shape))
-    if k is not None:
-        _need_all(dev, (k_out, "k_out", k.dtype, k.shape))
+    else:
+        _need(k_out, "k_out", k.dtype, k.shape, dev)
     _launch("m3ssd_norm_rotate", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
-            _addr(positions), _addr(freqs), _addr(q_out), None if k is None else _addr(k_out))
-    return q_out, None if k is None else k_out
+            _addr(positions), _addr(freqs), _addr(q_out), _addr(k_out))
+    return q_out, k_out
 
 
 def norm_rotate_bwd_workspace_size(dims: RotateDims) -> int:
@@ -1314,27 +1346,36 @@ def norm_rotate_bwd(q, k, q_w, k_w, dq_out, dk_out, *, positions=None, freqs=Non
     _need_all(dev, (dq_out, "dq_out", dq_out.dtype, q.shape))
     if k is not None:
         _need_all(dev, (dk_out, "dk_out", dq_out.dtype, k.shape))
-    grads = dict(grads or {})
-    for n, t in (("dq", q), ("dk", k)):
-        if t is None:
-            grads[n] = grads[n + "_w"] = None
-            continue
-        if grads.get(n) is None:
-            grads[n] = torch.empty(t.shape, dtype=grad_dtype, device=dev)
-        if grads.get(n + "_w") is None:
-            grads[n + "_w"] = torch.empty(N, dtype=f32, device=dev)
+    grads = grads or {}
+    dq, dk, dq_w, dk_w = (grads.get(n) for n in ("dq", "dk", "dq_w", "dk_w"))
+    Hk = 0 if k is None else k.shape[-2]
+    ldq, ldk = q.shape[-2] * N, Hk * N
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=grad_dtype, device=dev)
+    else:
+        ldq = _tokens_stride(dq, "dq", grad_dtype, lead, q.shape[-2:], dev.index)
+    if dq_w is None and dk_w is None:
+        dq_w, dk_w = torch.empty(2, N, dtype=f32, device=dev).unbind(0)
+    elif dq_w is None:
+        dq_w = torch.empty(N, dtype=f32, device=dev)
+    _need(dq_w, "dq_w", f32, (N,), dev)
+    if k is None:
+        dk = dk_w = None
+    else:
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=grad_dtype, device=dev)
         else:
-            _need(grads[n + "_w"], n + "_w", f32, (N,), dev)
-    ldq = _tokens_stride(grads["dq"], "dq", grad_dtype, lead, q.shape[-2:], dev.index)
-    ldk = 0 if k is None else _tokens_stride(grads["dk"], "dk", grad_dtype, lead, k.shape[-2:], dev.index)
-    g = RotateGrads(ldq, ldk, _xdtype(grads["dq"]), 0,
-                    *(_addr(grads[n]) for n in ("dq", "dk", "dq_w", "dk_w")))
+            ldk = _tokens_stride(dk, "dk", grad_dtype, lead, k.shape[-2:], dev.index)
+        if dk_w is None:
+            dk_w = torch.empty(N, dtype=f32, device=dev)
+        _need(dk_w, "dk_w", f32, (N,), dev)
+    g = RotateGrads(ldq, ldk, _xdtype(dq), 0, _addr(dq), _addr(dk), _addr(dq_w), _addr(dk_w))
     need = _on_device(dev, norm_rotate_bwd_workspace_size, dims)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
     _launch("m3ssd_norm_rotate_bwd", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
             _addr(positions), _addr(freqs), _xdtype(dq_out), _addr(dq_out), _addr(dk_out),
             ctypes.byref(g), ws, ws_bytes)
-    return {n: grads[n] for n in ("dq", "dk", "dq_w", "dk_w")}
+    return {"dq": dq, "dk": dk, "dq_w": dq_w, "dk_w": dk_w}
 
 
 # ---- 4-bit weights with scales a group, and their product with a few tokens ----------------------

@@ -412,10 +412,13 @@ __global__ void __launch_bounds__(kThreads) w4_dequant_kernel(W4Args a, T* w, in
 // What the tokens' pieces may take of shared memory: four, two and one CTA an SM.
 constexpr int kStageBytes[3] = {36 * 1024, 72 * 1024, 150 * 1024};
 
+// The most that a launch asks for: the tokens' piece, the scales of its tiles and the ring.
+constexpr int kMostShared = 200 * 1024;
+
 template <typename X, int NT, int G, bool ZEROS>
 cudaError_t run(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(gemv_w4_kernel<X, NT, G, ZEROS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (smem > kMostShared) return cudaErrorInvalidValue;
+  const cudaError_t e = allow_shared<gemv_w4_kernel<X, NT, G, ZEROS>>(kMostShared);
   if (e != cudaSuccess) return e;
   gemv_w4_kernel<X, NT, G, ZEROS><<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();

@@ -713,10 +713,9 @@ int run_of(bool bf16) { return bf16 ? kRun<__nv_bfloat16> : kRun<float>; }
 int64_t items_of(int64_t b, int64_t D) { return b * ((D + kGroup - 1) / kGroup); }
 
 // `early`: the kernel may begin before the one before it in the stream ends; it waits itself.
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, bool early,
-                   cudaStream_t s, A... args) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto KERNEL, typename... A>
+cudaError_t launch(int64_t grid, int threads, int smem, bool early, cudaStream_t s, A... args) {
+  cudaError_t e = smem > 0 ? allow_shared<KERNEL>(smem) : cudaSuccess;
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -728,7 +727,7 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, bo
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = early ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  e = cudaLaunchKernelEx(&cfg, KERNEL, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 constexpr int kCta = kWarps * kLanes;
@@ -737,11 +736,11 @@ template <typename T, int MODE, bool RESET>
 cudaError_t fwd_m(const GlrArgs& a, cudaStream_t s) {
   const int64_t items = items_of(a.b, a.D);
   const int smem = ring_bytes<T>(3, kStages);
-  if (!a.split) return launch(glr_fwd_kernel<T, MODE, RESET, false>, items, kCta, smem, false, s, a);
-  const cudaError_t e = launch(glr_part_kernel<T, MODE, RESET, false>, items * a.split, kCta,
+  if (!a.split) return launch<glr_fwd_kernel<T, MODE, RESET, false>>(items, kCta, smem, false, s, a);
+  const cudaError_t e = launch<glr_part_kernel<T, MODE, RESET, false>>(items * a.split, kCta,
                                smem, false, s, a, (const void*)nullptr, a.h0);
   if (e != cudaSuccess) return e;
-  return launch(glr_fwd_kernel<T, MODE, RESET, true>, items * a.split, kCta, smem, true, s, a);
+  return launch<glr_fwd_kernel<T, MODE, RESET, true>>(items * a.split, kCta, smem, true, s, a);
 }
 template <typename T, int MODE>
 cudaError_t fwd_r(const GlrArgs& a, cudaStream_t s) {
@@ -763,11 +762,11 @@ cudaError_t bwd_m(const GlrBwdArgs& a, cudaStream_t s) {
   const GlrArgs& f = a.f;
   const int64_t items = items_of(f.b, f.D);
   const int smem = ring_bytes<T>(5, 2);
-  if (!f.split) return launch(glr_bwd_kernel<T, G, MODE, RESET, false>, items, kCta, smem, false, s, a);
-  const cudaError_t e = launch(glr_part_kernel<T, MODE, RESET, true>, items * f.split, kCta,
+  if (!f.split) return launch<glr_bwd_kernel<T, G, MODE, RESET, false>>(items, kCta, smem, false, s, a);
+  const cudaError_t e = launch<glr_part_kernel<T, MODE, RESET, true>>(items * f.split, kCta,
                                ring_bytes<T>(2, kStages), false, s, f, a.dy, a.dhT);
   if (e != cudaSuccess) return e;
-  return launch(glr_bwd_kernel<T, G, MODE, RESET, true>, items * f.split, kCta, smem, true, s, a);
+  return launch<glr_bwd_kernel<T, G, MODE, RESET, true>>(items * f.split, kCta, smem, true, s, a);
 }
 template <typename T, typename G, int MODE>
 cudaError_t bwd_r(const GlrBwdArgs& a, cudaStream_t s) {
@@ -825,8 +824,8 @@ cudaError_t launch_glr_bwd(const GlrBwdArgs& args, void* workspace, cudaStream_t
                                         : bwd_t<__nv_bfloat16, float>(a, s);
     if (e != cudaSuccess) return e;
   }
-  return launch(glr_sum_kernel, grid_for(f.D), kThreads, 0, true, s, a.part,
-                f.b * (f.split ? f.split : 1), f.D, f.rate, a.drate, a.dbias_r, a.dbias_i);
+  return launch<glr_sum_kernel>(grid_for(f.D), kThreads, 0, true, s, (const float*)a.part,
+                                (int64_t)(f.b * (f.split ? f.split : 1)), (int64_t)f.D, f.rate, a.drate, a.dbias_r, a.dbias_i);
 }
 
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s) {

@@ -560,12 +560,11 @@ Access access_of(int64_t N, std::initializer_list<Strided> ts) {
   return ok[0] ? kWide : ok[1] ? kQuads : ok[2] ? kPairs : kSingle;
 }
 
-template <typename A>
-cudaError_t launch(void (*kernel)(A), const A& a, unsigned grid, int smem, cudaStream_t s) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto KERNEL, typename A>
+cudaError_t launch(const A& a, unsigned grid, int smem, cudaStream_t s) {
+  const cudaError_t e = allow_shared<KERNEL>(smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, smem, s>>>(a);
+  KERNEL<<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -576,11 +575,11 @@ cudaError_t fwd_t(const RotateArgs& a, cudaStream_t s) {
   const unsigned grid = grid_of(a, kFwdCtas);
   switch (access_of(a.N, {{a.q, a.ldq, z}, {a.k, a.ldk, z}, {a.q_out, a.N, z}, {a.k_out, a.N, z}})) {
     case kWide:
-      if constexpr (sizeof(T) == 2) return launch(norm_rotate_kernel<T, kWide>, a, grid, smem, s);
+      if constexpr (sizeof(T) == 2) return launch<norm_rotate_kernel<T, kWide>>(a, grid, smem, s);
       return cudaErrorInvalidValue;  // not of fp32
-    case kQuads: return launch(norm_rotate_kernel<T, kQuads>, a, grid, smem, s);
-    case kPairs: return launch(norm_rotate_kernel<T, kPairs>, a, grid, smem, s);
-    default: return launch(norm_rotate_kernel<T, kSingle>, a, grid, smem, s);
+    case kQuads: return launch<norm_rotate_kernel<T, kQuads>>(a, grid, smem, s);
+    case kPairs: return launch<norm_rotate_kernel<T, kPairs>>(a, grid, smem, s);
+    default: return launch<norm_rotate_kernel<T, kSingle>>(a, grid, smem, s);
   }
 }
 template <typename T, typename U, typename G>
@@ -593,11 +592,11 @@ cudaError_t bwd_t(const RotateBwdArgs& a, unsigned grid, cudaStream_t s) {
                           {a.dq, a.ldgq, zg}, {a.dk, a.ldgk, zg}})) {
     case kWide:
       if constexpr (sizeof(T) + sizeof(U) + sizeof(G) == 6)
-        return launch(norm_rotate_bwd_kernel<T, U, G, kWide>, a, grid, smem, s);
+        return launch<norm_rotate_bwd_kernel<T, U, G, kWide>>(a, grid, smem, s);
       return cudaErrorInvalidValue;  // not where one is fp32
-    case kQuads: return launch(norm_rotate_bwd_kernel<T, U, G, kQuads>, a, grid, smem, s);
-    case kPairs: return launch(norm_rotate_bwd_kernel<T, U, G, kPairs>, a, grid, smem, s);
-    default: return launch(norm_rotate_bwd_kernel<T, U, G, kSingle>, a, grid, smem, s);
+    case kQuads: return launch<norm_rotate_bwd_kernel<T, U, G, kQuads>>(a, grid, smem, s);
+    case kPairs: return launch<norm_rotate_bwd_kernel<T, U, G, kPairs>>(a, grid, smem, s);
+    default: return launch<norm_rotate_bwd_kernel<T, U, G, kSingle>>(a, grid, smem, s);
   }
 }
 
