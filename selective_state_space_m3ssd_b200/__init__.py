@@ -1311,13 +1311,13 @@ def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, ep
     dims, lead = _rotate_dims(q, k, q_w, k_w, positions, freqs, eps)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = torch.empty(*q.shape, dtype=q.dtype, device=dev)
     else:
         _need(q_out, "q_out", q.dtype, q.shape, dev)
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        k_out = torch.empty(*k.shape, dtype=k.dtype, device=dev)
     else:
         _need(k_out, "k_out", k.dtype, k.shape, dev)
     _launch("m3ssd_norm_rotate", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
@@ -1351,24 +1351,24 @@ def norm_rotate_bwd(q, k, q_w, k_w, dq_out, dk_out, *, positions=None, freqs=Non
     Hk = 0 if k is None else k.shape[-2]
     ldq, ldk = q.shape[-2] * N, Hk * N
     if dq is None:
-        dq = torch.empty(q.shape, dtype=grad_dtype, device=dev)
+        dq = torch.empty(*q.shape, dtype=grad_dtype, device=dev)
     else:
         ldq = _tokens_stride(dq, "dq", grad_dtype, lead, q.shape[-2:], dev.index)
-    if dq_w is None and dk_w is None:
-        dq_w, dk_w = torch.empty(2, N, dtype=f32, device=dev).unbind(0)
-    elif dq_w is None:
+    if dq_w is None:
         dq_w = torch.empty(N, dtype=f32, device=dev)
-    _need(dq_w, "dq_w", f32, (N,), dev)
+    else:
+        _need(dq_w, "dq_w", f32, (N,), dev)
     if k is None:
         dk = dk_w = None
     else:
         if dk is None:
-            dk = torch.empty(k.shape, dtype=grad_dtype, device=dev)
+            dk = torch.empty(*k.shape, dtype=grad_dtype, device=dev)
         else:
             ldk = _tokens_stride(dk, "dk", grad_dtype, lead, k.shape[-2:], dev.index)
         if dk_w is None:
             dk_w = torch.empty(N, dtype=f32, device=dev)
-        _need(dk_w, "dk_w", f32, (N,), dev)
+        else:
+            _need(dk_w, "dk_w", f32, (N,), dev)
     g = RotateGrads(ldq, ldk, _xdtype(dq), 0, _addr(dq), _addr(dk), _addr(dq_w), _addr(dk_w))
     need = _on_device(dev, norm_rotate_bwd_workspace_size, dims)
     workspace, ws, ws_bytes = _workspace(workspace, need, dev)
