@@ -339,7 +339,8 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
       const bool cut = RESET && (cuts >> j & 1);
       const float2 r = pair_of(st + j * kGroup), v = pair_of(st + (run + j) * kGroup);
       if constexpr (BACK) {
-        const float2 al = decay(ch, r, cut);
+        float2 al, nz;
+        decay(ch, r, al, nz);
         m.B = cut ? splat(0.f) : mul2(al, add2(m.B, v));
         m.A = cut ? splat(0.f) : mul2(al, m.A);
       } else {
@@ -500,8 +501,8 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
 
 // The walk back: tiles from the last one, a tile's last run first.  With g_t = dy_t + back_t a
 // token maps back_t, what comes from later tokens, to back_{t-1} = a_t (back_t + dy_t).  A warp
-// first composes its run (the decays alone), and once back has reached it, walks the run again
-// with the whole gradient; recomputing the gates costs less than holding them would.
+// first composes its run (the decays alone, which it keeps in shared memory), and once back has
+// reached it, walks the run again with the whole gradient.
 template <typename T, typename G, int MODE, bool RESET, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs args) {
   constexpr int run = kRun<T>, kTensors = 5;
@@ -536,6 +537,8 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
   float2 se = splat(0.f), sr = splat(0.f), si = splat(0.f);
 
   T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
+  float4* const kept = reinterpret_cast<float4*>(smem + ring_bytes<T>(kTensors, 2)) +
+                       warp * (run - 1) * kLanes + lane;
   auto stage = [&](int k) { return ring + k * (kWarps * kTensors * run * kGroup); };
   auto fetch = [&](int k, int t, bool on) {
     const int hi = on ? len - t : 0;
@@ -571,11 +574,19 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
     k ^= 1;
     const bool full = t + run <= len;
     const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    float2 a0 = splat(0.f), nz0 = a0;
     if constexpr (!SPLIT) {
       Map m = {splat(1.f), splat(0.f)};
       auto compose = [&](int j) {
         const bool cut = RESET && (cuts >> j & 1);
-        const float2 al = decay(ch, pair_of(st + (run + j) * kGroup), cut);
+        float2 al, nz;
+        decay(ch, pair_of(st + (run + j) * kGroup), al, nz);
+        if (j == 0) {  // the first token's need no place
+          a0 = al;
+          nz0 = nz;
+        } else {
+          kept[(j - 1) * kLanes] = make_float4(al.x, al.y, nz.x, nz.y);
+        }
         const float2 dy = pair_of(st + (3 * run + j) * kGroup);
         m.A = cut ? splat(0.f) : mul2(al, m.A);
         m.B = cut ? splat(0.f) : mul2(al, add2(m.B, dy));
@@ -597,9 +608,14 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
       g = add2(g, pair_of(st + (3 * run + j) * kGroup));
       float2 prev = pair_of(st + (4 * run + j) * kGroup), E;
       if (j == 0) prev = add2(prev, first);
-      const float2 al = element_grad(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
-                                     pair_of(st + (2 * run + j) * kGroup), cut, prev, g, dx, dr, di, E);
-      g = cut ? splat(0.f) : mul2(al, g);
+      float2 al = a0, nz = nz0;
+      if (!SPLIT && j > 0) {
+        const float4 v = kept[(j - 1) * kLanes];
+        al = make_float2(v.x, v.y);
+        nz = make_float2(v.z, v.w);
+      }
+      element_grad<!SPLIT>(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
+                           pair_of(st + (2 * run + j) * kGroup), cut, prev, al, nz, g, dx, dr, di, E);
       se = add2(se, E);
       sr = add2(sr, dr);
       si = add2(si, di);
@@ -762,7 +778,10 @@ cudaError_t bwd_m(const GlrBwdArgs& a, cudaStream_t s) {
   const GlrArgs& f = a.f;
   const int64_t items = items_of(f.b, f.D);
   const int smem = ring_bytes<T>(5, 2);
-  if (!f.split) return launch<glr_bwd_kernel<T, G, MODE, RESET, false>>(items, kCta, smem, false, s, a);
+  // the decays of all but one token a run fit beside the ring twice an SM
+  const int kept = kWarps * (kRun<T> - 1) * kLanes * (int)sizeof(float4);
+  if (!f.split)
+    return launch<glr_bwd_kernel<T, G, MODE, RESET, false>>(items, kCta, smem + kept, false, s, a);
   const cudaError_t e = launch<glr_part_kernel<T, MODE, RESET, true>>(items * f.split, kCta,
                                ring_bytes<T>(2, kStages), false, s, f, a.dy, a.dhT);
   if (e != cudaSuccess) return e;

@@ -132,46 +132,44 @@ __device__ __forceinline__ void element(const Channel& ch, float2 x, float2 r, f
   u = mul2(mul2(s, iota), x);
 }
 
-// The decay alone, which is all that the walk of g needs.
-__device__ __forceinline__ float2 decay(const Channel& ch, float2 r, bool reset) {
-  const float2 q = add2(gate_exp(r, ch.nbr), splat(1.f));
-  float2 a, nz;
+// The decay alone, which is all that the walk of g needs, and a^2 - 1.  (A gate that is not clamped:
+// nothing multiplies its exponential.)
+__device__ __forceinline__ void decay(const Channel& ch, float2 r, float2& a, float2& nz) {
+  const float2 t = fma2(r, splat(-kLog2e), ch.nbr);
+  const float2 q = add2(make_float2(ex2(t.x), ex2(t.y)), splat(1.f));
   decay_of(mul2(ch.k2, make_float2(rcp(q.x), rcp(q.y))), a, nz);
-  return reset ? splat(0.f) : a;
 }
 
 // The backward's element, from g = dL/dh_t and h_{t-1} (prev): the gradients of x, i, r and
-// E = g dh/d(log a) log a, whose sum gives the rate's.  Returns a.
-__device__ __forceinline__ float2 element_grad(const Channel& ch, float2 x, float2 r, float2 i,
-                                               bool reset, float2 prev, float2 g, float2& dx,
-                                               float2& dr, float2& di, float2& E) {
+// E = g dh/d(log a) log a, whose sum gives the rate's.  KNOWN: a and a^2 - 1 are given, else
+// they are worked out.  g becomes a g, what goes on to h_{t-1}.
+template <bool KNOWN>
+__device__ __forceinline__ void element_grad(const Channel& ch, float2 x, float2 r, float2 i, bool reset,
+                                             float2 prev, float2 a, float2 nz, float2& g, float2& dx,
+                                             float2& dr, float2& di, float2& E) {
   const float2 er = gate_exp(r, ch.nbr), ei = gate_exp(i, ch.nbi);
   const float2 qr = add2(er, splat(1.f)), qi = add2(ei, splat(1.f));
   const float2 d = mul2(qr, qi), R = make_float2(rcp(d.x), rcp(d.y));
   const float2 rho = mul2(qi, R), iota = mul2(qr, R);
   const float2 t = mul2(ch.k2, rho);
-  float2 a, nz;
-  decay_of(t, a, nz);
+  if constexpr (!KNOWN) decay_of(t, a, nz);
   // 1 / s and s; 1e-37 changes no 1 - a^2 above 1e-29, and keeps both finite at zero
   const float2 inv = make_float2(rsq(1e-37f - nz.x), rsq(1e-37f - nz.y));
   float2 s = make_float2(-nz.x * inv.x, -nz.y * inv.y);
-  if (reset) {
-    a = splat(0.f);
-    s = splat(1.f);
-  }
+  if (reset) s = splat(1.f);
   const float2 v = mul2(iota, x);
   dx = mul2(mul2(g, s), iota);
   di = mul2(mul2(dx, x), mul2(ei, iota));
   if (reset) {
-    E = dr = splat(0.f);
+    E = dr = g = splat(0.f);
   } else {
-    const float2 la = mul2(t, splat(0.693147180559945309f));
+    g = mul2(g, a);
     // a (h_{t-1} - a v / s), times log a: (log a) / s stays finite as s goes to zero
+    const float2 la = mul2(t, splat(0.693147180559945309f));
     const float2 w = mul2(mul2(a, v), mul2(la, inv));
-    E = mul2(mul2(g, a), fma2(la, prev, neg2(w)));
+    E = mul2(g, fma2(la, prev, neg2(w)));
     dr = mul2(E, mul2(er, rho));
   }
-  return a;
 }
 
 }  // namespace glr
