@@ -242,19 +242,35 @@ __device__ __forceinline__ Map unpack_map(float4 v) {
   return {make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
 
-// What the maps before a warp's part make of the start; BACK: before means later in the sequence.
+// What the maps before a warp's part make of the start; BACK: before means later in the sequence.  The
+// CTAs' maps are composed by eight warps, an eighth of them each.
+struct Fold {
+  float4 map[kWarps][kLanes];
+  uint32_t cut[kWarps];
+};
 template <bool RESET, bool BACK>
-__device__ __forceinline__ float2 start_of(const GlrArgs& a, int warp, int lane) {
+__device__ __forceinline__ float2 start_of(const GlrArgs& a, Fold& fold, int warp, int lane) {
   const int64_t items = gridDim.x / (uint32_t)a.split, cta0 = blockIdx.x / (uint32_t)a.split * a.split;
   const SplitMaps m = split_maps(a.maps, items, a.split);
   const int mine = (int)(blockIdx.x % (uint32_t)a.split);
-  float2 h = m.start[blockIdx.x / (uint32_t)a.split * kLanes + lane];
-  const int n = BACK ? a.split - 1 - mine : mine;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
+  const int n = BACK ? a.split - 1 - mine : mine, eighth = (n + kWarps - 1) / kWarps;
+  Map all = {splat(1.f), splat(0.f)};
+  bool all_cut = false;
+#pragma unroll 2
+  for (int i = warp * eighth; i < min(warp * eighth + eighth, n); ++i) {
     const int64_t c = cta0 + (BACK ? a.split - 1 - i : i);
-    h = apply(unpack_map(m.cta[c * kLanes + lane]), h, RESET && m.cta_cut[c]);
+    const Map one = unpack_map(m.cta[c * kLanes + lane]);
+    const bool cut = RESET && m.cta_cut[c];
+    all.B = apply(one, all.B, cut);
+    all.A = mul2(one.A, all.A);
+    all_cut |= cut;
   }
+  fold.map[warp][lane] = pack_map(all);
+  if (RESET && lane == 0) fold.cut[warp] = all_cut;
+  __syncthreads();
+  float2 h = m.start[blockIdx.x / (uint32_t)a.split * kLanes + lane];
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) h = apply(unpack_map(fold.map[i][lane]), h, RESET && fold.cut[i]);
   const int w = BACK ? kWarps - 1 - warp : warp;
 #pragma unroll
   for (int i = 0; i < kWarps - 1; ++i) {
@@ -391,7 +407,7 @@ template <typename T, int MODE, bool RESET, bool SPLIT>
 __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) {
   constexpr int run = kRun<T>;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Chain chain;
+  __shared__ typename std::conditional<SPLIT, Fold, Chain>::type chain;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Way<T, SPLIT> way(a, warp);
   const int64_t b = way.b, d0 = way.d0, d = d0 + 2 * lane;
@@ -407,7 +423,9 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
   const uint32_t D = (uint32_t)a.D, at = way.ahead * D + 2 * lane;  // of the warp's first output
   const uint8_t* const reset = RESET ? a.reset + b * a.L : nullptr;
   const bool whole = a.D % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % (2 * sizeof(T)) == 0;
-  if (!SPLIT && warp == 0) chain.state[0][lane] = state_at(a.h0, b, d, a.D);
+  if constexpr (!SPLIT) {
+    if (warp == 0) chain.state[0][lane] = state_at(a.h0, b, d, a.D);
+  }
 
   T* const ring = reinterpret_cast<T*>(smem) + warp * 3 * run * kGroup;
   auto stage = [&](int k) { return ring + k * (kWarps * 3 * run * kGroup); };
@@ -432,7 +450,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
   float2 h = splat(0.f);
   if constexpr (SPLIT) {
     cudaGridDependencySynchronize();  // the parts' maps are there
-    h = start_of<RESET, false>(a, warp, lane);
+    h = start_of<RESET, false>(a, chain, warp, lane);
   }
   int k = 0;
   for (int round = 0; round < way.rounds; ++round, t += step) {
@@ -508,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
   constexpr int run = kRun<T>, kTensors = 5;
   const GlrArgs& a = args.f;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ Chain chain;
+  __shared__ typename std::conditional<SPLIT, Fold, Chain>::type chain;
   cudaTriggerProgrammaticLaunchCompletion();  // the sums' kernel waits itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, order = kWarps - 1 - warp;
   const Way<T, SPLIT> way(a, warp);
@@ -533,7 +551,9 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
                      (reinterpret_cast<uintptr_t>(args.dx) | reinterpret_cast<uintptr_t>(args.dr) |
                       reinterpret_cast<uintptr_t>(args.di)) % (2 * sizeof(G)) == 0;
   const float2 h0 = state_at(a.h0, b, d, a.D);
-  if (!SPLIT && order == 0) chain.state[0][lane] = state_at(args.dhT, b, d, a.D);
+  if constexpr (!SPLIT) {
+    if (order == 0) chain.state[0][lane] = state_at(args.dhT, b, d, a.D);
+  }
   float2 se = splat(0.f), sr = splat(0.f), si = splat(0.f);
 
   T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
@@ -564,7 +584,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
   float2 g = splat(0.f);  // what comes from later tokens
   if constexpr (SPLIT) {
     cudaGridDependencySynchronize();  // the parts' maps are there
-    g = start_of<RESET, true>(a, warp, lane);
+    g = start_of<RESET, true>(a, chain, warp, lane);
   }
   for (int round = 0; round < way.rounds; ++round, t -= step) {
     copies_wait<0>();
@@ -713,10 +733,19 @@ Copy copy_of(std::initializer_list<const void*> ps, std::initializer_list<int64_
 }
 
 // How many CTAs share a sequence's tokens, a part a warp (0: one walks its tiles): as many as fill two
-// places an SM where the walks alone would leave half of them idle and there are tokens enough.
-int split_of(int64_t items, int64_t L, int run) {
+// places an SM, but one an SM for a lone item.  The split pays for the maps with a second reading and a
+// second working out of the gates, so it has to have CTAs enough to gain by; measured split against
+// whole, us, bf16, 2048 channels (32 items a sequence, so 9, 4, 3 and 2 CTAs for 1, 2, 3 and 4
+// sequences):
+//   forward   1 x 256  7.9 / 6.0   1 x 512  8.0 / 9.8   1 x 2048  19 / 32   2 x 2048  31.1 / 31.7
+//             3 x 2048  40 / 32    4 x 2048  55 / 32
+//   backward  1 x 256 10.3 / 12.5  1 x 512 14.9 / 21.9  1 x 2048  25 / 73   2 x 2048  40 / 73
+//             3 x 2048  52 / 74    4 x 2048  70 / 74    4 x 2048 in fp32 115 / 99
+// A lone item of 32768 tokens in 148 or 256 CTAs: forward 13.0 / 14.3, backward 37.1 / 44.3.
+int split_of(bool back, int64_t items, int64_t L, int run) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
-  const int64_t room = items > 0 ? 2 * sms / items : 0, most = L / (2 * run * kWarps);
+  const int64_t room = items > 1 ? 2 * sms / items : items * sms, most = L / (2 * run * kWarps);
+  if (back ? room < 3 : room < 5 || L < 512) return 0;
   const int64_t n = room < most ? room : most;
   return n >= 2 ? (int)n : 0;
 }
@@ -803,8 +832,8 @@ cudaError_t bwd_t(const GlrBwdArgs& a, cudaStream_t s) {
   }
 }
 
-void set_split(GlrArgs& a, void* maps) {
-  a.split = split_of(items_of(a.b, a.D), a.L, run_of(a.bf16));
+void set_split(GlrArgs& a, bool back, void* maps) {
+  a.split = split_of(back, items_of(a.b, a.D), a.L, run_of(a.bf16));
   a.part_len = a.split ? part_len_of(a.L, a.split, run_of(a.bf16)) : 0;
   a.maps = maps;
 }
@@ -815,18 +844,18 @@ size_t al256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t glr_fwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
   const int64_t items = items_of(b, D);
-  return split_bytes(items, split_of(items, L, run_of(bf16)));
+  return split_bytes(items, split_of(false, items, L, run_of(bf16)));
 }
 
 cudaError_t launch_glr_fwd(const GlrArgs& args, void* workspace, cudaStream_t s) {
   GlrArgs a = args;
-  set_split(a, workspace);
+  set_split(a, false, workspace);
   return a.bf16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
 }
 
 size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
   const int64_t items = items_of(b, D);
-  const int split = split_of(items, L, run_of(bf16));
+  const int split = split_of(true, items, L, run_of(bf16));
   return al256(split_bytes(items, split)) +
          (size_t)b * (size_t)(split ? split : 1) * 3 * (size_t)D * sizeof(float);
 }
@@ -834,7 +863,7 @@ size_t glr_bwd_workspace_bytes(int64_t b, int64_t L, int64_t D, bool bf16) {
 cudaError_t launch_glr_bwd(const GlrBwdArgs& args, void* workspace, cudaStream_t s) {
   GlrBwdArgs a = args;
   GlrArgs& f = a.f;
-  set_split(f, workspace);
+  set_split(f, true, workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                     al256(split_bytes(items_of(f.b, f.D), f.split)));
   if (f.b > 0) {
@@ -844,7 +873,8 @@ cudaError_t launch_glr_bwd(const GlrBwdArgs& args, void* workspace, cudaStream_t
     if (e != cudaSuccess) return e;
   }
   return launch<glr_sum_kernel>(grid_for(f.D), kThreads, 0, true, s, (const float*)a.part,
-                                (int64_t)(f.b * (f.split ? f.split : 1)), (int64_t)f.D, f.rate, a.drate, a.dbias_r, a.dbias_i);
+                                (int64_t)(f.b * (f.split ? f.split : 1)), (int64_t)f.D, f.rate,
+                                a.drate, a.dbias_r, a.dbias_i);
 }
 
 cudaError_t launch_glr_step(const GlrStepArgs& a, cudaStream_t s) {

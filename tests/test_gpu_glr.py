@@ -186,6 +186,17 @@ def test_resets(dtype, rate):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("L", [512, 1100, 2311])
+def test_parts_of_a_long_sequence(L, dtype):
+    # both directions in parts: resets in some parts only, ends inside, between and before the parts
+    run_fwd(make(1, L, 70, dtype, seed=L, reset=0.002))
+    run_bwd(make(1, L, 70, dtype, seed=L, reset=0.002))
+    d = make(4, L, 33, dtype, seed=L + 1, reset=0.01, lengths=[0, L, 1, L // 2 + 3])
+    run_fwd(d)
+    run_bwd(d)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_lengths_of_padded_batches(dtype):
     d = make(7, 150, 66, dtype, seed=6, lengths=[0, 1, 64, 65, 150, 149, 8])
     for k in ("x", "r", "i", "dy"):  # what lies behind an end is not looked at
