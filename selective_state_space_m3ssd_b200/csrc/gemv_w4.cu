@@ -15,7 +15,7 @@
 // are a tenth of the time.
 //
 // fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
-// A CTA's eight warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
+// A CTA's warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
 // order; the tokens lie there too, a piece of K at a time.
 #include <cuda_runtime.h>
 
@@ -28,7 +28,7 @@
 namespace m3ssd {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 8, kThreads = kWarps * 32;  // of the kernels that lay weights out
 constexpr int kTileRows = 16, kTileCols = 128, kTileBytes = 1024;
 constexpr int kRedRow = kTileRows + 1;
 
@@ -147,7 +147,7 @@ __device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, in
   const int in_part = 31 - __clz(a.per * (kTileCols / 8)), in_token = in_part + (31 - __clz(a.wk));
   const int all = (int)a.M << in_token;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < all; i += kThreads) {
+  for (int i = threadIdx.x; i < all; i += blockDim.x) {
     const int m = i >> in_token, q = i & ((1 << in_token) - 1);
     const int k = ((q >> in_part) * a.part + first) * kTileCols + 8 * (q & ((1 << in_part) - 1));
     stage_eight(x + m * a.ldx, k, (int)a.K, a.wide, smem + m * (sizeof(X) == 2 ? 1 : 3) * stride + q * 16,
@@ -163,7 +163,7 @@ __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int6
   const int shift = 31 - __clz(rows) - 3, in_part = 31 - __clz(a.per);  // eights of rows; tiles
   const bool wide = a.wide_scales && row0 + rows <= a.N;
 #pragma unroll 2
-  for (int i = threadIdx.x; i < (a.wk * a.per * G) << shift; i += kThreads) {
+  for (int i = threadIdx.x; i < (a.wk * a.per * G) << shift; i += blockDim.x) {
     const int e = i >> shift, r = 8 * (i & ((1 << shift) - 1));
     const int place = e / G, tile = (place >> in_part) * a.part + first + (place & (a.per - 1));
     const int j = G > 1 ? tile * G + e % G : a.group_tiles == 1 ? tile : tile / a.group_tiles;
@@ -200,17 +200,17 @@ __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int6
   }
 }
 
-// CTAs an SM holds: 64 registers a thread for eight columns, 128 for 16, all there are for more.
+// Warps that an SM holds: 64 registers a thread for eight columns, 128 for 16, all there are for more.
 template <int NT>
-constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+constexpr int kSmWarps = NT == 1 ? 32 : NT == 2 ? 16 : 8;
 
-// X: the tokens' type; NT: eights of columns (tokens, or thirds of them); G: groups in a tile; ZEROS: zero
-// points given.
-template <typename X, int NT, int G, bool ZEROS>
-__global__ void __launch_bounds__(kThreads, kCtas<NT>) gemv_w4_kernel(GemvW4Args a) {
+// X: the tokens' type; NT: eights of columns (tokens, or thirds of them); W: warps of a CTA; G: groups in a
+// tile; ZEROS: zero points given.
+template <typename X, int NT, int W, int G, bool ZEROS>
+__global__ void __launch_bounds__(W * 32, kSmWarps<NT> / W) gemv_w4_kernel(GemvW4Args a) {
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int WK = a.wk, WR = kWarps / WK, wk = warp % WK, wr = warp / WK;
+  const int WK = a.wk, WR = W / WK, wk = warp % WK, wr = warp / WK;
   const int64_t rb = (int64_t)blockIdx.x * WR + wr;
   const bool live = rb < a.RB;
   const int KB = (int)a.KB, per = a.per, chunk = per * WK;  // tiles: of K, of a warp and of a CTA a piece
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<NT>) gemv_w4_kernel(GemvW4Args
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < WR * (int)a.M * kTileRows; i += kThreads) {
+  for (int i = threadIdx.x; i < WR * (int)a.M * kTileRows; i += W * 32) {
     const int r = i % kTileRows, m = i / kTileRows % (int)a.M, w = i / kTileRows / (int)a.M;
     const int64_t n = ((int64_t)blockIdx.x * WR + w) * kTileRows + r;
     if (n >= a.N) continue;
@@ -409,36 +409,63 @@ __global__ void __launch_bounds__(kThreads) w4_dequant_kernel(W4Args a, T* w, in
   }
 }
 
-// What the tokens' pieces may take of shared memory: four, two and one CTA an SM.
-constexpr int kStageBytes[3] = {36 * 1024, 72 * 1024, 150 * 1024};
+// What the tokens' pieces may take of an SM's shared memory, and the most that an SM's CTAs ask for: the
+// tokens' piece, the scales of its tiles and the ring.
+constexpr int kStageBytes = 144 * 1024, kMostShared = 200 * 1024;
 
-// The most that a launch asks for: the tokens' piece, the scales of its tiles and the ring.
-constexpr int kMostShared = 200 * 1024;
-
-template <typename X, int NT, int G, bool ZEROS>
-cudaError_t run(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
+template <typename X, int NT, int W, int G, bool ZEROS>
+cudaError_t run(GemvW4Args a, cudaStream_t s) {
+  constexpr int ctas = kSmWarps<NT> / W;
+  const int64_t places = (current_device_sms() > 0 ? current_device_sms() : 148) * ctas;
+  // parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens)
+  a.wk = 1;
+  while (a.wk < W && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + W - 1) / W <= places) a.wk *= 2;
+  // A part's tiles, and a power of two of them in a piece: all, as far as the piece's tokens fit.
+  a.part = (int)((a.KB + a.wk - 1) / a.wk);
+  a.per = 1;
+  const int64_t wr = W / a.wk;
+  auto tokens = [&](int per) { return a.cols * (per * a.wk * kTileCols * 2 + 64); };
+  auto held = [&](int per) {
+    return tokens(per) + per * a.wk * G * (int)wr * kTileRows * 4 + W * kDeep * kTileBytes;
+  };
+  while (a.per < 16 && a.per < a.part && tokens(2 * a.per) <= kStageBytes / ctas &&
+         held(2 * a.per) <= kMostShared / ctas)
+    a.per *= 2;
+  const int sums = W * a.cols * kRedRow * (int)sizeof(float);
+  const int smem = held(a.per) > sums ? held(a.per) : sums;
   if (smem > kMostShared) return cudaErrorInvalidValue;
-  const cudaError_t e = allow_shared<gemv_w4_kernel<X, NT, G, ZEROS>>(kMostShared);
+  const cudaError_t e = allow_shared<gemv_w4_kernel<X, NT, W, G, ZEROS>>(kMostShared);
   if (e != cudaSuccess) return e;
-  gemv_w4_kernel<X, NT, G, ZEROS><<<grid, kThreads, smem, s>>>(a);
+  gemv_w4_kernel<X, NT, W, G, ZEROS><<<(unsigned)((a.RB + wr - 1) / wr), W * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
-template <typename X, int NT>
-cudaError_t run_g(const GemvW4Args& a, unsigned grid, int smem, cudaStream_t s) {
+template <typename X, int NT, int W>
+cudaError_t run_g(const GemvW4Args& a, cudaStream_t s) {
   if (a.zeros)
-    return a.group == 32   ? run<X, NT, 4, true>(a, grid, smem, s)
-           : a.group == 64 ? run<X, NT, 2, true>(a, grid, smem, s)
-                           : run<X, NT, 1, true>(a, grid, smem, s);
-  return a.group == 32   ? run<X, NT, 4, false>(a, grid, smem, s)
-         : a.group == 64 ? run<X, NT, 2, false>(a, grid, smem, s)
-                         : run<X, NT, 1, false>(a, grid, smem, s);
+    return a.group == 32   ? run<X, NT, W, 4, true>(a, s)
+           : a.group == 64 ? run<X, NT, W, 2, true>(a, s)
+                           : run<X, NT, W, 1, true>(a, s);
+  return a.group == 32   ? run<X, NT, W, 4, false>(a, s)
+         : a.group == 64 ? run<X, NT, W, 2, false>(a, s)
+                         : run<X, NT, W, 1, false>(a, s);
+}
+// Every CTA stages all the tokens of its part of K.  Few tokens: CTAs of eight warps, which start and join
+// sooner; from 12 KB of them on one CTA an SM, which stages them once for all its warps.  Measured, us, eight
+// warps against one CTA: 1 x 2048 x 2048 3.0 / 4.1, 1 x 6464 x 1024 3.4 / 4.0, fp32 4.0 / 4.6, 3 x 20001 x
+// 1000 7.4 / 8.7; 1 x 8192 x 8192 (16 KB) 12.2 / 11.2, 5 x 6464 x 1024 fp32 6.2 / 5.7, 8 x 8192 x 8192
+// (groups of 32) 31 / 17, 16 x 8192 x 8192 42 / 29, 8 x 65536 x 4096 42 / 37.
+template <typename X, int NT>
+cudaError_t run_w(const GemvW4Args& a, cudaStream_t s) {
+  if constexpr (NT <= 2) {
+    if (a.cols * a.K * 2 >= 12 * 1024) return run_g<X, NT, kSmWarps<NT>>(a, s);
+  }
+  return run_g<X, NT, 8>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   GemvW4Args a = args;
-  const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   a.parts = a.x_bf16 ? 1 : 3;
   a.cols = (int)a.M * a.parts;
   a.RB = (a.N + kTileRows - 1) / kTileRows;
@@ -447,28 +474,12 @@ cudaError_t launch_gemv_w4(const GemvW4Args& args, cudaStream_t s) {
   a.wide_scales = a.N % 8 == 0 && reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 &&
                   reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0;
   a.wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % (a.x_bf16 ? 8 : 4) == 0;
-  // parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens)
   const int nt = (a.cols + 7) / 8;
-  const int64_t ctas = sms * (nt == 1 ? kCtas<1> : nt == 2 ? kCtas<2> : kCtas<4>);
-  a.wk = 1;
-  while (a.wk < kWarps && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + kWarps - 1) / kWarps <= ctas) a.wk *= 2;
-  // A part's tiles, and a power of two of them in a piece: all, as far as the piece's tokens fit.
-  a.part = (int)((a.KB + a.wk - 1) / a.wk);
-  const int64_t room = kStageBytes[nt == 1 ? 0 : nt == 2 ? 1 : 2];
-  a.per = 1;
-  while (a.per < 8 && a.per < a.part && a.cols * (2 * a.per * a.wk * kTileCols * 2 + 64) <= room) a.per *= 2;
-  const int64_t wr = kWarps / a.wk;
-  const unsigned grid = (unsigned)((a.RB + wr - 1) / wr);
-  const int in_tile = a.group < kTileCols ? (int)(kTileCols / a.group) : 1;
-  const int held = a.cols * (a.per * a.wk * kTileCols * 2 + 64) +
-                   a.per * a.wk * in_tile * (int)wr * kTileRows * 4 + kWarps * kDeep * kTileBytes;
-  const int sums = kWarps * a.cols * kRedRow * (int)sizeof(float), smem = held > sums ? held : sums;
-  if (a.x_bf16)
-    return nt == 1 ? run_g<__nv_bfloat16, 1>(a, grid, smem, s) : run_g<__nv_bfloat16, 2>(a, grid, smem, s);
-  return nt == 1   ? run_g<float, 1>(a, grid, smem, s)
-         : nt == 2 ? run_g<float, 2>(a, grid, smem, s)
-         : nt <= 4 ? run_g<float, 4>(a, grid, smem, s)
-                   : run_g<float, 6>(a, grid, smem, s);
+  if (a.x_bf16) return nt == 1 ? run_w<__nv_bfloat16, 1>(a, s) : run_w<__nv_bfloat16, 2>(a, s);
+  return nt == 1   ? run_w<float, 1>(a, s)
+         : nt == 2 ? run_w<float, 2>(a, s)
+         : nt <= 4 ? run_w<float, 4>(a, s)
+                   : run_w<float, 6>(a, s);
 }
 
 cudaError_t launch_w4_quant(const W4Args& a, bool bf16, const void* w, int64_t ldw, cudaStream_t s) {
