@@ -14,6 +14,11 @@
 // is not for this: its operands would have to go through shared or tensor memory, and the products
 // are a tenth of the time.
 //
+// Measured: 8 tokens x 65536 x 4096 in groups of 64 with zero points (146 MB) 34.3 us, 4.3 TB/s; one token
+// 30.3 us without zero points; 16 tokens 60 us (two products a word, half the warps: the tokens' operands
+// come from shared memory for every tile).  1 x 6464 x 1024 3.4 us: a launch, one read of codes after
+// another of tokens and scales, a join.
+//
 // fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
 // A CTA's warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
 // order; the tokens lie there too, a piece of K at a time.
@@ -211,8 +216,11 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<NT> / W) gemv_w4_kernel(GemvW
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int WK = a.wk, WR = W / WK, wk = warp % WK, wr = warp / WK;
-  const int64_t rb = (int64_t)blockIdx.x * WR + wr;
-  const bool live = rb < a.RB;
+  // The CTA's rows of tiles: `mine`, at most WR, from row0 / 16 on.
+  const int mine = (int)a.each + (blockIdx.x < a.more);
+  const int64_t row0 = (blockIdx.x * a.each + min((int64_t)blockIdx.x, a.more)) * kTileRows;
+  const int64_t rb = row0 / kTileRows + wr;
+  const bool live = wr < mine;
   const int KB = (int)a.KB, per = a.per, chunk = per * WK;  // tiles: of K, of a warp and of a CTA a piece
   const int cols = a.cols, stride = chunk * kTileCols * 2 + 64;  // bytes of a column in shared memory
 
@@ -299,7 +307,7 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<NT> / W) gemv_w4_kernel(GemvW
   for (int first = 0; first < a.part; first += per) {
     if (first > 0) __syncthreads();
     stage_tokens(a, static_cast<const X*>(a.x), first, stride, smem);
-    stage_words<G, ZEROS>(a, first, (int64_t)blockIdx.x * rows, rows,
+    stage_words<G, ZEROS>(a, first, row0, rows,
                           reinterpret_cast<uint32_t*>(smem + words_at));
     __syncthreads();
     const int n = min(tiles - first, per);
@@ -324,9 +332,9 @@ __global__ void __launch_bounds__(W * 32, kSmWarps<NT> / W) gemv_w4_kernel(GemvW
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < WR * (int)a.M * kTileRows; i += W * 32) {
+  for (int i = threadIdx.x; i < mine * (int)a.M * kTileRows; i += W * 32) {
     const int r = i % kTileRows, m = i / kTileRows % (int)a.M, w = i / kTileRows / (int)a.M;
-    const int64_t n = ((int64_t)blockIdx.x * WR + w) * kTileRows + r;
+    const int64_t n = row0 + w * kTileRows + r;
     if (n >= a.N) continue;
     float s = 0.f;
     for (int p = 0; p < a.parts; ++p)
@@ -416,7 +424,7 @@ constexpr int kStageBytes = 144 * 1024, kMostShared = 200 * 1024;
 template <typename X, int NT, int W, int G, bool ZEROS>
 cudaError_t run(GemvW4Args a, cudaStream_t s) {
   constexpr int ctas = kSmWarps<NT> / W;
-  const int64_t places = (current_device_sms() > 0 ? current_device_sms() : 148) * ctas;
+  const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148, places = sms * ctas;
   // parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens)
   a.wk = 1;
   while (a.wk < W && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + W - 1) / W <= places) a.wk *= 2;
@@ -436,7 +444,13 @@ cudaError_t run(GemvW4Args a, cudaStream_t s) {
   if (smem > kMostShared) return cudaErrorInvalidValue;
   const cudaError_t e = allow_shared<gemv_w4_kernel<X, NT, W, G, ZEROS>>(kMostShared);
   if (e != cudaSuccess) return e;
-  gemv_w4_kernel<X, NT, W, G, ZEROS><<<(unsigned)((a.RB + wr - 1) / wr), W * 32, smem, s>>>(a);
+  // As many CTAs for every SM, some of whose warps have no row, rather than SMs that have no CTA: 8 x 65536 x
+  // 4096 in 148 CTAs of 27 or 28 warps 34.3 us, in 128 of 32 36.6.
+  const int64_t need = (a.RB + wr - 1) / wr, even = (need + sms - 1) / sms * sms;
+  const int64_t grid = even < a.RB ? even : a.RB;
+  a.each = a.RB / grid;
+  a.more = a.RB % grid;
+  gemv_w4_kernel<X, NT, W, G, ZEROS><<<(unsigned)grid, W * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <typename X, int NT, int W>
@@ -451,9 +465,9 @@ cudaError_t run_g(const GemvW4Args& a, cudaStream_t s) {
 }
 // Every CTA stages all the tokens of its part of K.  Few tokens: CTAs of eight warps, which start and join
 // sooner; from 12 KB of them on one CTA an SM, which stages them once for all its warps.  Measured, us, eight
-// warps against one CTA: 1 x 2048 x 2048 3.0 / 4.1, 1 x 6464 x 1024 3.4 / 4.0, fp32 4.0 / 4.6, 3 x 20001 x
-// 1000 7.4 / 8.7; 1 x 8192 x 8192 (16 KB) 12.2 / 11.2, 5 x 6464 x 1024 fp32 6.2 / 5.7, 8 x 8192 x 8192
-// (groups of 32) 31 / 17, 16 x 8192 x 8192 42 / 29, 8 x 65536 x 4096 42 / 37.
+// warps against one CTA (tokens x rows x K): 1 x 2048 x 2048 3.0 / 4.1, 1 x 6464 x 1024 3.4 / 4.0, fp32
+// 4.0 / 4.6, 3 x 20001 x 1000 7.4 / 8.7; 1 x 8192 x 8192 (16 KB) 12.2 / 11.2, 5 x 6464 x 1024 fp32 6.2 / 5.7,
+// 8 x 8192 x 8192 (groups of 32) 31 / 17, 16 x 8192 x 8192 42 / 29, 8 x 65536 x 4096 42 / 37.
 template <typename X, int NT>
 cudaError_t run_w(const GemvW4Args& a, cudaStream_t s) {
   if constexpr (NT <= 2) {
