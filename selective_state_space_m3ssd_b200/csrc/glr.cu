@@ -738,14 +738,15 @@ Copy copy_of(std::initializer_list<const void*> ps, std::initializer_list<int64_
 // whole, us, bf16, 2048 channels (32 items a sequence, so 9, 4, 3 and 2 CTAs for 1, 2, 3 and 4
 // sequences):
 //   forward   1 x 256  7.9 / 6.0   1 x 512  8.0 / 9.8   1 x 2048  19 / 32   2 x 2048  31.1 / 31.7
-//             3 x 2048  40 / 32    4 x 2048  55 / 32
+//             3 x 2048  40 / 32    4 x 2048  55 / 32     2 x 32768 391 / 464, in fp32 600 / 533
 //   backward  1 x 256 10.3 / 12.5  1 x 512 14.9 / 21.9  1 x 2048  25 / 73   2 x 2048  40 / 73
 //             3 x 2048  52 / 74    4 x 2048  70 / 74    4 x 2048 in fp32 115 / 99
 // A lone item of 32768 tokens in 148 or 256 CTAs: forward 13.0 / 14.3, backward 37.1 / 44.3.
 int split_of(bool back, int64_t items, int64_t L, int run) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int64_t room = items > 1 ? 2 * sms / items : items * sms, most = L / (2 * run * kWarps);
-  if (back ? room < 3 : room < 5 || L < 512) return 0;
+  const int least = back ? 3 : run == kRun<__nv_bfloat16> && L >= 2048 ? 4 : 5;
+  if (room < least || (!back && L < 512)) return 0;
   const int64_t n = room < most ? room : most;
   return n >= 2 ? (int)n : 0;
 }
