@@ -1,7 +1,7 @@
 // The product of a few tokens with 4-bit weights whose groups of columns have a bf16 scale (and a
 // zero point), and the weights into that form and back.
 //
-//     out[m][n] = sum over groups j of scale[j][n] (sum over the group's k of x[m][k] (code[n][k] - zero[j][n])).
+//     out[m][n] = sum over groups j of scale[j][n] sum over j's k of x[m][k] (code[n][k] - zero[j][n]).
 //
 // The codes are read once, and HBM bounds the product from about a million weights on; below, it is
 // latency.  A warp takes tiles of 16 rows by 128 columns, 1 KB of codes that its lanes read as two
@@ -160,8 +160,8 @@ __device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, in
   }
 }
 
-// The words of scales and zero points of the same tiles, `G` a tile (a longer group's in each of its tiles), for
-// `rows` rows from row0 on: the scale above -zero / 64, both bf16.
+// The words of scales and zero points of the same tiles, `G` a tile (a longer group's in each of its
+// tiles), for `rows` rows from row0 on: the scale above -zero / 64, both bf16.
 template <int G, bool ZEROS>
 __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int64_t row0, int rows,
                                             uint32_t* to) {

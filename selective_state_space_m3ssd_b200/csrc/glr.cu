@@ -36,6 +36,12 @@ __device__ __forceinline__ void store2(T* p, float2 v, bool in1) {
 // into parts instead, one a warp, of as many CTAs as there is room for: a first kernel composes
 // every part into its map, and in the walk each warp begins from what the maps before it
 // make of h0.  That reads the inputs twice, so it is for launches that would leave SMs idle.
+//
+// Bytes: the forward reads x, r and i and writes y, the backward reads y and dy too and writes three
+// gradients.  Measured at 8 x 4096 tokens, 2048 channels, bf16: forward 106 us (0.77 of HBM's copy
+// rate), backward with bf16 gradients 220 (0.75).  The issue slots bound both: 66 and 130 warp
+// instructions for a token of two channels a lane, most of them the gates', in 256 CTAs, which are two
+// on 108 SMs and one on 40.  32 x 1024 tokens, 1024 CTAs: 98 and 203 us.
 
 constexpr int kWarps = 8, kLanes = 32, kGroup = 64;
 

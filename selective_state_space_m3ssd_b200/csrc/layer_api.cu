@@ -1,5 +1,6 @@
 // C-ABI entry points of the operators that a layer has around the scan: the gated linear
-// recurrence, the norm of heads with their rotation, and 4-bit weights with scales a group.  Host-side validation and dispatch; nothing is allocated, nothing synchronises.
+// recurrence, the norm of heads with their rotation, and 4-bit weights with scales a group.
+// Host-side validation and dispatch; nothing is allocated, nothing synchronises.
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -126,7 +126,8 @@ def test_padding_is_not_looked_at():
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("zeros", [False, True])
-@pytest.mark.parametrize("N,K,group", [(1, 1, 32), (16, 128, 128), (37, 333, 32), (50, 1000, 64), (9, 700, 256)])
+@pytest.mark.parametrize("N,K,group", [(1, 1, 32), (16, 128, 128), (37, 333, 32), (50, 1000, 64),
+                                       (9, 700, 256)])
 def test_quantisation_bit_for_bit(N, K, group, zeros, dt):
     g = torch.Generator().manual_seed(N)
     w = (torch.randn(N, K, generator=g) * torch.exp(torch.randn(N, 1, generator=g))).to(dt)

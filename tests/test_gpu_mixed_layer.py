@@ -30,7 +30,8 @@ def weights(seed=1):
     r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
     u = lambda *s: torch.rand(*s, generator=g)  # noqa: E731
     w = {"norm": 0.5 + u(DM), "W_in": r(WIDTH, DM) / DM ** 0.5, "W_out": r(DM, HP + R) / (HP + R) ** 0.5,
-         "Cw": (0.5 + u(N)) / N ** 0.5, "Bw": (0.5 + u(N)) / N ** 0.5, "dt_bias": -4 + 2 * u(H), "A": 1 + 15 * u(H), "D": r(H),
+         "Cw": (0.5 + u(N)) / N ** 0.5, "Bw": (0.5 + u(N)) / N ** 0.5, "dt_bias": -4 + 2 * u(H),
+         "A": 1 + 15 * u(H), "D": r(H),
          "rate": torch.log(torch.expm1(-torch.log(0.9 + 0.099 * u(R)))), "bias_r": r(R), "bias_i": r(R),
          "freqs": FREQS}
     w = {k: v.cuda() for k, v in w.items()}
