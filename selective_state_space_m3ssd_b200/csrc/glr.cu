@@ -159,12 +159,22 @@ struct Copier {
   }
 };
 
-// The resets among a warp's tokens from t on, a bit each (0 outside [0, len)).
-template <int RUN>
-__device__ __forceinline__ uint32_t resets_of(const uint8_t* reset, int t, int len, int lane) {
-  const bool on = lane < RUN && t + lane < len && reset[t + lane];
-  return __ballot_sync(0xffffffffu, on);
-}
+// The resets among a warp's tokens, a bit each (0 outside [0, len)), read a run ahead.
+template <int RUN, bool RESET>
+struct Resets {
+  uint32_t ahead = 0;  // a lane's of the run that is taken next
+  __device__ __forceinline__ void read(const uint8_t* reset, int t, int len, int lane) {
+    if constexpr (RESET)
+      ahead = lane < RUN && (uint32_t)(t + lane) < (uint32_t)len ? reset[t + lane] : 0;
+  }
+  // Those of the run, and the reading of the one from t on.
+  __device__ __forceinline__ uint32_t take(const uint8_t* reset, int t, int len, int lane) {
+    if constexpr (!RESET) return 0;
+    const uint32_t bits = __ballot_sync(0xffffffffu, ahead != 0);
+    read(reset, t, len, lane);
+    return bits;
+  }
+};
 
 // Where a warp walks: `rounds` runs of which the first begins at token t, `step` tokens apart;
 // all of a sequence's tiles with its CTA, or (SPLIT) one part of it alone.
@@ -346,6 +356,8 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
   for (int k = 0; k < kStages - 1; ++k) fetch(k, t + k * step, k < way.rounds);
   Channel ch;
   channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  Resets<run, RESET> resets;
+  resets.read(reset, t, len, lane);
   Map m = {splat(1.f), splat(0.f)};
   bool any = false;
   int k = 0;
@@ -355,9 +367,9 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
     fetch(k == 0 ? kStages - 1 : k - 1, t + (kStages - 1) * step, round + kStages - 1 < way.rounds);
     const T* const st = stage(k) + 2 * lane;
     k = k == kStages - 1 ? 0 : k + 1;
-    const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    const uint32_t cuts = resets.take(reset, t + step, len, lane);
     any |= cuts != 0;
-    auto compose = [&](int j) {
+    auto compose = [&](int j, uint32_t cuts) {
       const bool cut = RESET && (cuts >> j & 1);
       const float2 r = pair_of(st + j * kGroup), v = pair_of(st + (run + j) * kGroup);
       if constexpr (BACK) {
@@ -372,14 +384,14 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
         m.A = cut ? splat(0.f) : mul2(e.A, m.A);
       }
     };
-    if (t + run <= len) {
+    if (t + run <= len && cuts == 0) {  // most runs
 #pragma unroll
-      for (int j = 0; j < run; ++j) compose(BACK ? run - 1 - j : j);
+      for (int j = 0; j < run; ++j) compose(BACK ? run - 1 - j : j, 0);
     } else {
 #pragma unroll
       for (int q = 0; q < run; ++q) {
         const int j = BACK ? run - 1 - q : q;
-        if (t + j < len) compose(j);
+        if (t + j < len) compose(j, cuts);
       }
     }
   }
@@ -453,6 +465,8 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
   for (int k = 0; k < kStages - 1; ++k) fetch(k, t + k * step, k < way.rounds);
   Channel ch;
   channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  Resets<run, RESET> resets;
+  resets.read(reset, t, len, lane);
   float2 h = splat(0.f);
   if constexpr (SPLIT) {
     cudaGridDependencySynchronize();  // the parts' maps are there
@@ -465,11 +479,11 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
     fetch(k == 0 ? kStages - 1 : k - 1, t + (kStages - 1) * step, round + kStages - 1 < way.rounds);
     const T* const st = stage(k) + 2 * lane;
     k = k == kStages - 1 ? 0 : k + 1;
-    const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
-    const bool full = t + run <= len;
+    const uint32_t cuts = resets.take(reset, t + step, len, lane);
+    const bool full = t + run <= len && cuts == 0;  // most runs
     // SPLIT: B is the state itself
     Map m[run];
-    auto compose = [&](int j, const Map& e) {
+    auto compose = [&](int j, const Map& e, uint32_t cuts) {
       const bool cut = RESET && (cuts >> j & 1);
       if constexpr (SPLIT) {
         h = m[j].B = apply(e, h, cut);
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
         m[j].A = !j ? e.A : cut ? splat(0.f) : mul2(e.A, m[j - 1].A);
       }
     };
-    auto token = [&](int j) {
+    auto token = [&](int j, uint32_t cuts) {
       Map e;
       element(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
               pair_of(st + (2 * run + j) * kGroup), RESET && (cuts >> j & 1), e.A, e.B);
@@ -486,27 +500,27 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
     };
     if (full) {
 #pragma unroll
-      for (int j = 0; j < run; ++j) compose(j, token(j));
-    } else {  // the last tokens: past them the state stays
+      for (int j = 0; j < run; ++j) compose(j, token(j, 0), 0);
+    } else {  // past the last token the state stays
 #pragma unroll
       for (int j = 0; j < run; ++j)
-        compose(j, t + j < len ? token(j) : Map{splat(1.f), splat(0.f)});
+        compose(j, t + j < len ? token(j, cuts) : Map{splat(1.f), splat(0.f)}, cuts);
     }
     float2 in;
     if constexpr (!SPLIT)
       in = pass_on(chain, m[run - 1], cuts != 0, warp, round == 0 && warp == 0,
                    round == way.rounds - 1 && warp == kWarps - 1, lane);
-    auto state = [&](int j) {
+    auto state = [&](int j, uint32_t cuts) {
       if constexpr (SPLIT) return m[j].B;
       return apply(m[j], in, RESET && (cuts & ((2u << j) - 1)));
     };
     if (full && whole) {
 #pragma unroll
-      for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j), true, in0, in1);
+      for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j, 0), true, in0, in1);
     } else {
 #pragma unroll
       for (int j = 0; j < run; ++j) {
-        const float2 v = state(j);
+        const float2 v = state(j, cuts);
         if (t + j < L) put_pair(y + (at + j * D), t + j < len ? v : splat(0.f), whole, in0, in1);
       }
     }
@@ -587,6 +601,8 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
   fetch(0, t, way.rounds > 0);
   Channel ch;
   channel_of(a.rate, a.bias_r, a.bias_i, a.c, d, d + 1, a.D, ch);
+  Resets<run, RESET> resets;
+  resets.read(reset, t, len, lane);
   float2 g = splat(0.f);  // what comes from later tokens
   if constexpr (SPLIT) {
     cudaGridDependencySynchronize();  // the parts' maps are there
@@ -598,12 +614,12 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
     fetch(k ^ 1, t - step, round + 1 < way.rounds);
     const T* const st = stage(k) + 2 * lane;
     k ^= 1;
-    const bool full = t + run <= len;
-    const uint32_t cuts = RESET ? resets_of<run>(reset, t, len, lane) : 0;
+    const uint32_t cuts = resets.take(reset, t - step, len, lane);
+    const bool full = t + run <= len && cuts == 0;  // most runs
     float2 a0 = splat(0.f), nz0 = a0;
     if constexpr (!SPLIT) {
       Map m = {splat(1.f), splat(0.f)};
-      auto compose = [&](int j) {
+      auto compose = [&](int j, uint32_t cuts) {
         const bool cut = RESET && (cuts >> j & 1);
         float2 al, nz;
         decay(ch, pair_of(st + (run + j) * kGroup), al, nz);
@@ -619,17 +635,17 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
       };
       if (full) {
 #pragma unroll
-        for (int j = run - 1; j >= 0; --j) compose(j);
+        for (int j = run - 1; j >= 0; --j) compose(j, 0);
       } else {
 #pragma unroll
         for (int j = run - 1; j >= 0; --j)
-          if (t + j < len) compose(j);
+          if (t + j < len) compose(j, cuts);
       }
       g = pass_on(chain, m, cuts != 0, order, round == 0 && order == 0,
                   round == way.rounds - 1 && order == kWarps - 1, lane);
     }
     const float2 first = t == 0 ? h0 : splat(0.f);
-    auto finish = [&](int j, float2& dx, float2& dr, float2& di) {
+    auto finish = [&](int j, uint32_t cuts, float2& dx, float2& dr, float2& di) {
       const bool cut = RESET && (cuts >> j & 1);
       g = add2(g, pair_of(st + (3 * run + j) * kGroup));
       float2 prev = pair_of(st + (4 * run + j) * kGroup), E;
@@ -650,7 +666,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
 #pragma unroll
       for (int j = run - 1; j >= 0; --j) {
         float2 dx, dr, di;
-        finish(j, dx, dr, di);
+        finish(j, 0, dx, dr, di);
         put_pair(out[0] + (at + j * ldg), dx, true, in0, in1);
         put_pair(out[1] + (at + j * ldg), dr, true, in0, in1);
         put_pair(out[2] + (at + j * ldg), di, true, in0, in1);
@@ -659,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
 #pragma unroll
       for (int j = run - 1; j >= 0; --j) {
         float2 dx = splat(0.f), dr = dx, di = dx;
-        if (t + j < len) finish(j, dx, dr, di);
+        if (t + j < len) finish(j, cuts, dx, dr, di);
         if (t + j < L) {
           put_pair(out[0] + (at + j * ldg), dx, whole, in0, in1);
           put_pair(out[1] + (at + j * ldg), dr, whole, in0, in1);
