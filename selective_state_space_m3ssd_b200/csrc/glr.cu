@@ -177,7 +177,8 @@ struct Resets {
 };
 
 // Where a warp walks: `rounds` runs of which the first begins at token t, `step` tokens apart;
-// all of a sequence's tiles with its CTA, or (SPLIT) one part of it alone.
+// all of a sequence's tiles with its CTA, or (SPLIT) one part of it alone, or with others: `share`
+// warps, whole runs each, in order.
 template <typename T, bool SPLIT>
 struct Way {
   int64_t b, d0;
@@ -185,7 +186,7 @@ struct Way {
   int ahead;      // the warp's run from there
   int step, rounds, part;
 
-  __device__ __forceinline__ Way(const GlrArgs& a, int warp) {
+  __device__ __forceinline__ Way(const GlrArgs& a, int warp, int share = 1) {
     const int64_t groups = (a.D + kGroup - 1) / kGroup;
     const uint32_t ctas = SPLIT ? (uint32_t)a.split : 1u;
     const int64_t item = blockIdx.x / ctas;
@@ -193,12 +194,14 @@ struct Way {
     d0 = item % groups * kGroup;
     const int L = (int)a.L;
     if constexpr (SPLIT) {
-      part = (int)(blockIdx.x % ctas) * kWarps + warp;
-      const int64_t at = (int64_t)part * a.part_len;
-      first_row = (int)min(at, (int64_t)L);
+      part = (int)(blockIdx.x % ctas) * kWarps + warp / share;
+      const int len = (a.part_len / kRun<T> + share - 1) / share * kRun<T>;
+      const int64_t from = min((int64_t)part * a.part_len, (int64_t)L);
+      const int64_t end = min(from + a.part_len, (int64_t)L);
+      first_row = (int)min(from + warp % share * len, end);
       ahead = 0;
       step = kRun<T>;
-      rounds = (min(L - first_row, a.part_len) + kRun<T> - 1) / kRun<T>;
+      rounds = (min((int)end - first_row, len) + kRun<T> - 1) / kRun<T>;
     } else {
       part = 0;
       first_row = 0;
@@ -314,17 +317,23 @@ __device__ __forceinline__ float2 state_at(const float* state, int64_t b, int64_
   return v;
 }
 
-// The map of every part of a split: of the forward (BACK: of the backward, from the end on).
+// The map of every part of a split: of the forward (BACK: of the backward, from the end on).  kShare warps
+// make one: the backward's maps take half of the gates and fit in 64 registers, so that an SM holds 32
+// warps.  Measured, us, the backward with two against one: bf16 1 x 512 x 2048 12.0 / 14.7, 1 x 32768 x 64
+// 32.0 / 37.1, 2 x 32768 x 768 with resets 260 / 263; fp32 3 x 1777 x 513 40.8 / 35.0.
+template <typename T, bool BACK>
+constexpr int kShare = BACK && sizeof(T) == 2 ? 2 : 1;
+
 template <typename T, int MODE, bool RESET, bool BACK>
-__global__ void __launch_bounds__(kWarps * kLanes, 2)
+__global__ void __launch_bounds__(kShare<T, BACK> * kWarps * kLanes, 2)
 glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
-  constexpr int run = kRun<T>, kTensors = BACK ? 2 : 3;
+  constexpr int run = kRun<T>, kTensors = BACK ? 2 : 3, share = kShare<T, BACK>, warps = share * kWarps;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float4 maps[kWarps][kLanes];
-  __shared__ uint32_t cut_of[kWarps];
+  __shared__ float4 maps[warps][kLanes];
+  __shared__ uint32_t cut_of[warps];
   cudaTriggerProgrammaticLaunchCompletion();  // the walk may begin to load; it waits itself
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Way<T, true> way(a, warp);
+  const Way<T, true> way(a, warp, share);
   const int64_t d0 = way.d0, d = d0 + 2 * lane;
   const int left = (int)min(a.D - d0, (int64_t)kGroup), L = (int)a.L;
   const int len = a.lengths ? min(max(a.lengths[way.b], 0), L) : L;
@@ -337,7 +346,7 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
   if constexpr (!BACK) src[kTensors - 1].init(a.i, row, 0, d0, a.ldi, lane);
   const uint8_t* const reset = RESET ? a.reset + way.b * a.L : nullptr;
   T* const ring = reinterpret_cast<T*>(smem) + warp * kTensors * run * kGroup;
-  auto stage = [&](int k) { return ring + k * (kWarps * kTensors * run * kGroup); };
+  auto stage = [&](int k) { return ring + k * (warps * kTensors * run * kGroup); };
   auto fetch = [&](int k, int t, bool on) {
     const int hi = on ? len - t : 0;
     if (hi >= run && left == kGroup) {
@@ -399,25 +408,32 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
   if (lane == 0) cut_of[warp] = any;
   const SplitMaps out = split_maps(a.maps, gridDim.x / (uint32_t)a.split, a.split);
   const int64_t cta = blockIdx.x;
-  out.part[(cta * kWarps + warp) * kLanes + lane] = pack_map(m);
-  if (lane == 0) out.part_cut[cta * kWarps + warp] = any;
   if (warp == 1 && blockIdx.x % (uint32_t)a.split == 0)
     out.start[blockIdx.x / (uint32_t)a.split * kLanes + lane] = state_at(start, way.b, d, a.D);
   __syncthreads();
-  if (warp == 0) {
+  // the maps of n warps from w0 on, as one
+  auto composed = [&](int w0, int n, bool& all_cut) {
     Map all = {splat(1.f), splat(0.f)};
-    bool all_cut = false;
+    all_cut = false;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const int w = BACK ? kWarps - 1 - i : i;
+    for (int i = 0; i < n; ++i) {
+      const int w = w0 + (BACK ? n - 1 - i : i);
       const Map one = unpack_map(maps[w][lane]);
       const bool c = RESET && cut_of[w];
       all.B = apply(one, all.B, c);
       all.A = mul2(one.A, all.A);
       all_cut |= c;
     }
-    out.cta[cta * kLanes + lane] = pack_map(all);
-    if (lane == 0) out.cta_cut[cta] = all_cut;
+    return pack_map(all);
+  };
+  bool cut;
+  if (warp < kWarps) {
+    out.part[(cta * kWarps + warp) * kLanes + lane] = composed(share * warp, share, cut);
+    if (lane == 0) out.part_cut[cta * kWarps + warp] = cut;
+  }
+  if (warp == warps - 1) {
+    out.cta[cta * kLanes + lane] = composed(0, warps, cut);
+    if (lane == 0) out.cta_cut[cta] = cut;
   }
 }
 
@@ -761,9 +777,9 @@ Copy copy_of(std::initializer_list<const void*> ps, std::initializer_list<int64_
 // sequences):
 //   forward   1 x 256  7.9 / 6.0   1 x 512  8.0 / 9.8   1 x 2048  19 / 32   2 x 2048  31.1 / 31.7
 //             3 x 2048  40 / 32    4 x 2048  55 / 32     2 x 32768 391 / 464, in fp32 600 / 533
-//   backward  1 x 256 10.3 / 12.5  1 x 512 14.9 / 21.9  1 x 2048  25 / 73   2 x 2048  40 / 73
+//   backward  1 x 256 10.3 / 12.5  1 x 512 12.0 / 21.9  1 x 2048  25 / 73   2 x 2048  40 / 73
 //             3 x 2048  52 / 74    4 x 2048  70 / 74    4 x 2048 in fp32 115 / 99
-// A lone item of 32768 tokens in 148 or 256 CTAs: forward 13.0 / 14.3, backward 37.1 / 44.3.
+// A lone item of 32768 tokens in 148 or 256 CTAs: forward 13.0 / 14.3, backward 37.1 / 44.3 (32 since).
 int split_of(bool back, int64_t items, int64_t L, int run) {
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148;
   const int64_t room = items > 1 ? 2 * sms / items : items * sms, most = L / (2 * run * kWarps);
@@ -834,8 +850,9 @@ cudaError_t bwd_m(const GlrBwdArgs& a, cudaStream_t s) {
   const int kept = kWarps * (kRun<T> - 1) * kLanes * (int)sizeof(float4);
   if (!f.split)
     return launch<glr_bwd_kernel<T, G, MODE, RESET, false>>(items, kCta, smem + kept, false, s, a);
-  const cudaError_t e = launch<glr_part_kernel<T, MODE, RESET, true>>(items * f.split, kCta,
-                               ring_bytes<T>(2, kStages), false, s, f, a.dy, a.dhT);
+  const cudaError_t e = launch<glr_part_kernel<T, MODE, RESET, true>>(items * f.split,
+                               kShare<T, true> * kCta, kShare<T, true> * ring_bytes<T>(2, kStages), false,
+                               s, f, a.dy, a.dhT);
   if (e != cudaSuccess) return e;
   return launch<glr_bwd_kernel<T, G, MODE, RESET, true>>(items * f.split, kCta, smem, true, s, a);
 }
