@@ -15,7 +15,7 @@
 // are a tenth of the time.
 //
 // Measured: 8 tokens x 65536 x 4096 in groups of 64 with zero points (146 MB) 34.3 us, 4.3 TB/s; one token
-// 30.3 us without zero points; 16 tokens 60 us (two products a word, half the warps: the tokens' operands
+// 30.3 us without zero points; 16 tokens 58 us (two products a word, fewer warps: the tokens' operands
 // come from shared memory for every tile).  1 x 6464 x 1024 3.4 us: a launch, one read of codes after
 // another of tokens and scales, a join.
 //
@@ -165,11 +165,11 @@ __device__ __forceinline__ void stage_tokens(const GemvW4Args& a, const X* x, in
 template <int G, bool ZEROS>
 __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int64_t row0, int rows,
                                             uint32_t* to) {
-  const int shift = 31 - __clz(rows) - 3, in_part = 31 - __clz(a.per);  // eights of rows; tiles
+  const int eights = rows / 8, in_part = 31 - __clz(a.per);  // of rows; tiles
   const bool wide = a.wide_scales && row0 + rows <= a.N;
 #pragma unroll 2
-  for (int i = threadIdx.x; i < (a.wk * a.per * G) << shift; i += blockDim.x) {
-    const int e = i >> shift, r = 8 * (i & ((1 << shift) - 1));
+  for (int i = threadIdx.x; i < a.wk * a.per * G * eights; i += blockDim.x) {
+    const int e = __umulhi(i, a.over_eights), r = 8 * (i - e * eights);
     const int place = e / G, tile = (place >> in_part) * a.part + first + (place & (a.per - 1));
     const int j = G > 1 ? tile * G + e % G : a.group_tiles == 1 ? tile : tile / a.group_tiles;
     const int64_t at = j * a.N + row0 + r;
@@ -205,9 +205,10 @@ __device__ __forceinline__ void stage_words(const GemvW4Args& a, int first, int6
   }
 }
 
-// Warps that an SM holds: 64 registers a thread for eight columns, 128 for 16, all there are for more.
+// Warps that an SM holds, by the registers of the sums: 64 a thread for eight columns, 80 for 16, 128 for
+// more (with 8 warps of as many registers as they like 16 fp32 tokens x 16384 x 4096 took 61 us, so 42).
 template <int NT>
-constexpr int kSmWarps = NT == 1 ? 32 : NT == 2 ? 16 : 8;
+constexpr int kSmWarps = NT == 1 ? 32 : NT == 2 ? 24 : 16;
 
 // X: the tokens' type; NT: eights of columns (tokens, or thirds of them); W: warps of a CTA; G: groups in a
 // tile; ZEROS: zero points given.
@@ -425,22 +426,25 @@ template <typename X, int NT, int W, int G, bool ZEROS>
 cudaError_t run(GemvW4Args a, cudaStream_t s) {
   constexpr int ctas = kSmWarps<NT> / W;
   const int64_t sms = current_device_sms() > 0 ? current_device_sms() : 148, places = sms * ctas;
-  // parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens)
+  // Shared memory for pieces of `per` tiles of each of `wk` parts of K.
+  auto tokens = [&](int per, int wk) { return a.cols * (per * wk * kTileCols * 2 + 64); };
+  auto held = [&](int per, int wk) {
+    return tokens(per, wk) + per * wk * G * (W / wk) * kTileRows * 4 + W * kDeep * kTileBytes;
+  };
+  // Parts of K: as many as leave no more CTAs than all SMs hold at once (every one stages all tokens).
   a.wk = 1;
-  while (a.wk < W && 2 * a.wk <= a.KB && (a.RB * 2 * a.wk + W - 1) / W <= places) a.wk *= 2;
+  for (int wk = 2; W % wk == 0 && wk <= a.KB && (a.RB * wk + W - 1) / W <= places; wk *= 2)
+    if (held(1, wk) <= kMostShared / ctas) a.wk = wk;
   // A part's tiles, and a power of two of them in a piece: all, as far as the piece's tokens fit.
   a.part = (int)((a.KB + a.wk - 1) / a.wk);
   a.per = 1;
   const int64_t wr = W / a.wk;
-  auto tokens = [&](int per) { return a.cols * (per * a.wk * kTileCols * 2 + 64); };
-  auto held = [&](int per) {
-    return tokens(per) + per * a.wk * G * (int)wr * kTileRows * 4 + W * kDeep * kTileBytes;
-  };
-  while (a.per < 16 && a.per < a.part && tokens(2 * a.per) <= kStageBytes / ctas &&
-         held(2 * a.per) <= kMostShared / ctas)
+  a.over_eights = (uint32_t)(((int64_t(1) << 32) + 2 * wr - 1) / (2 * wr));
+  while (a.per < 16 && a.per < a.part && tokens(2 * a.per, a.wk) <= kStageBytes / ctas &&
+         held(2 * a.per, a.wk) <= kMostShared / ctas)
     a.per *= 2;
   const int sums = W * a.cols * kRedRow * (int)sizeof(float);
-  const int smem = held(a.per) > sums ? held(a.per) : sums;
+  const int smem = held(a.per, a.wk) > sums ? held(a.per, a.wk) : sums;
   if (smem > kMostShared) return cudaErrorInvalidValue;
   const cudaError_t e = allow_shared<gemv_w4_kernel<X, NT, W, G, ZEROS>>(kMostShared);
   if (e != cudaSuccess) return e;
@@ -470,10 +474,7 @@ cudaError_t run_g(const GemvW4Args& a, cudaStream_t s) {
 // 8 x 8192 x 8192 (groups of 32) 31 / 17, 16 x 8192 x 8192 42 / 29, 8 x 65536 x 4096 42 / 37.
 template <typename X, int NT>
 cudaError_t run_w(const GemvW4Args& a, cudaStream_t s) {
-  if constexpr (NT <= 2) {
-    if (a.cols * a.K * 2 >= 12 * 1024) return run_g<X, NT, kSmWarps<NT>>(a, s);
-  }
-  return run_g<X, NT, 8>(a, s);
+  return a.cols * a.K * 2 >= 12 * 1024 ? run_g<X, NT, kSmWarps<NT>>(a, s) : run_g<X, NT, 8>(a, s);
 }
 
 }  // namespace

@@ -432,11 +432,13 @@ struct GemvW4Args {
   int64_t ldd;
   // The launch sets these: bf16 columns a token and in all, tiles along N and K, tiles of a group,
   // parts of K, tiles of a part and of a part in a piece, rows of tiles of a CTA (and of the first `more`
-  // one more), whether tokens and scales can be read 16 bytes at a time.
+  // one more), 2^32 over the eights of rows of a CTA, whether tokens and scales can be read 16 bytes at a
+  // time.
   int parts, cols;
   int64_t RB, KB;
   int group_tiles, wk, part, per;
   int64_t each, more;
+  uint32_t over_eights;
   bool wide, wide_scales;
 };
 cudaError_t launch_gemv_w4(const GemvW4Args& a, cudaStream_t s);

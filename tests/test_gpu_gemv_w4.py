@@ -68,10 +68,12 @@ def test_every_number_of_tokens(M, dt):
     (1, 33, 9000, 32, True, BF), (1, 300, 8191, 128, False, BF), (2, 2500, 3100, 256, True, F32),
     (8, 7, 1024, 64, True, BF), (8, 300, 9000, 32, False, BF), (8, 40000, 1000, 64, True, BF),
     (9, 2500, 1111, 128, True, BF), (16, 300, 9000, 32, True, BF), (16, 40000, 640, 128, False, BF),
-    (5, 1234, 1030, 32, True, F32)])
+    (5, 1234, 1030, 32, True, F32), (8, 2500, 4100, 64, True, F32), (16, 2500, 4100, 32, False, F32),
+    (16, 7, 9000, 64, True, F32), (16, 3000, 100, 32, True, F32), (9, 333, 90, 32, False, F32),
+    (12, 3000, 300, 64, True, BF)])
 def test_many_bytes_of_tokens(M, N, K, group, zeros, dt):
     # from 12 KB of tokens on a CTA has all of an SM's warps: parts of K for all of them and for none,
-    # several pieces of the tokens and one
+    # several pieces of the tokens and one; and less than that of many columns
     W, w = weights(N, K, group, zeros, seed=N + K)
     x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(dt).cuda()
     check(m3.gemv_w4(x, W, out_dtype=F32), x, w, K)
