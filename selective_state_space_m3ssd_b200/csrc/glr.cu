@@ -397,11 +397,9 @@ glr_part_kernel(GlrArgs a, const void* dy, const float* start) {
 #pragma unroll
       for (int j = 0; j < run; ++j) compose(BACK ? run - 1 - j : j, 0);
     } else {
-#pragma unroll
-      for (int q = 0; q < run; ++q) {
-        const int j = BACK ? run - 1 - q : q;
-        if (t + j < len) compose(j, cuts);
-      }
+      const int n = min(len - t, run);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) compose(BACK ? n - 1 - j : j, cuts);
     }
   }
   maps[warp][lane] = pack_map(m);
@@ -496,47 +494,69 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_fwd_kernel(GlrArgs a) 
     const T* const st = stage(k) + 2 * lane;
     k = k == kStages - 1 ? 0 : k + 1;
     const uint32_t cuts = resets.take(reset, t + step, len, lane);
-    const bool full = t + run <= len && cuts == 0;  // most runs
-    // SPLIT: B is the state itself
-    Map m[run];
-    auto compose = [&](int j, const Map& e, uint32_t cuts) {
-      const bool cut = RESET && (cuts >> j & 1);
-      if constexpr (SPLIT) {
-        h = m[j].B = apply(e, h, cut);
-      } else {
-        m[j].B = j ? apply(e, m[j - 1].B, cut) : e.B;
-        m[j].A = !j ? e.A : cut ? splat(0.f) : mul2(e.A, m[j - 1].A);
-      }
-    };
-    auto token = [&](int j, uint32_t cuts) {
+    auto token = [&](int j, bool cut) {
       Map e;
       element(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
-              pair_of(st + (2 * run + j) * kGroup), RESET && (cuts >> j & 1), e.A, e.B);
+              pair_of(st + (2 * run + j) * kGroup), cut, e.A, e.B);
       return e;
     };
-    if (full) {
-#pragma unroll
-      for (int j = 0; j < run; ++j) compose(j, token(j, 0), 0);
-    } else {  // past the last token the state stays
-#pragma unroll
-      for (int j = 0; j < run; ++j)
-        compose(j, t + j < len ? token(j, cuts) : Map{splat(1.f), splat(0.f)}, cuts);
-    }
-    float2 in;
-    if constexpr (!SPLIT)
-      in = pass_on(chain, m[run - 1], cuts != 0, warp, round == 0 && warp == 0,
-                   round == way.rounds - 1 && warp == kWarps - 1, lane);
-    auto state = [&](int j, uint32_t cuts) {
-      if constexpr (SPLIT) return m[j].B;
-      return apply(m[j], in, RESET && (cuts & ((2u << j) - 1)));
+    auto pass = [&](const Map& m) {
+      if constexpr (SPLIT) return h;
+      else
+        return pass_on(chain, m, cuts != 0, warp, round == 0 && warp == 0,
+                       round == way.rounds - 1 && warp == kWarps - 1, lane);
     };
-    if (full && whole) {
-#pragma unroll
-      for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j, 0), true, in0, in1);
-    } else {
+    if (t + run <= len && cuts == 0) {  // most runs
+      Map m[run];  // SPLIT: B is the state itself
 #pragma unroll
       for (int j = 0; j < run; ++j) {
-        const float2 v = state(j, cuts);
+        const Map e = token(j, false);
+        if constexpr (SPLIT) {
+          h = m[j].B = apply(e, h, false);
+        } else {
+          m[j].B = j ? apply(e, m[j - 1].B, false) : e.B;
+          m[j].A = j ? mul2(e.A, m[j - 1].A) : e.A;
+        }
+      }
+      float2 in;
+      if constexpr (!SPLIT) in = pass(m[run - 1]);
+      auto state = [&](int j) {
+        if constexpr (SPLIT) return m[j].B;
+        return apply(m[j], in, false);
+      };
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j), true, in0, in1);
+      } else {
+#pragma unroll
+        for (int j = 0; j < run; ++j) put_pair(y + (at + j * D), state(j), false, in0, in1);
+      }
+    } else if (t >= len) {  // past the sequence's end the state stays
+      if constexpr (!SPLIT) pass({splat(1.f), splat(0.f)});
+#pragma unroll
+      for (int j = 0; j < run; ++j)
+        if (t + j < L) put_pair(y + (at + j * D), splat(0.f), whole, in0, in1);
+    } else {  // a reset or the end; selects, so that the gates overlap
+      Map m[run];
+#pragma unroll
+      for (int j = 0; j < run; ++j) {
+        const bool cut = RESET && (cuts >> j & 1), on = t + j < len;
+        Map e = token(j, cut);
+        e.A = on ? e.A : splat(1.f);
+        e.B = on ? e.B : splat(0.f);
+        if constexpr (SPLIT) {
+          h = m[j].B = apply(e, h, cut);
+        } else {
+          m[j].B = j ? apply(e, m[j - 1].B, cut) : e.B;
+          m[j].A = !j ? e.A : cut ? splat(0.f) : mul2(e.A, m[j - 1].A);
+        }
+      }
+      float2 in;
+      if constexpr (!SPLIT) in = pass(m[run - 1]);
+#pragma unroll
+      for (int j = 0; j < run; ++j) {
+        float2 v = m[j].B;
+        if constexpr (!SPLIT) v = apply(m[j], in, RESET && (cuts & ((2u << j) - 1)));
         if (t + j < L) put_pair(y + (at + j * D), t + j < len ? v : splat(0.f), whole, in0, in1);
       }
     }
@@ -631,72 +651,99 @@ __global__ void __launch_bounds__(kWarps * kLanes, 2) glr_bwd_kernel(GlrBwdArgs 
     const T* const st = stage(k) + 2 * lane;
     k ^= 1;
     const uint32_t cuts = resets.take(reset, t - step, len, lane);
-    const bool full = t + run <= len && cuts == 0;  // most runs
-    float2 a0 = splat(0.f), nz0 = a0;
-    if constexpr (!SPLIT) {
-      Map m = {splat(1.f), splat(0.f)};
-      auto compose = [&](int j, uint32_t cuts) {
-        const bool cut = RESET && (cuts >> j & 1);
-        float2 al, nz;
-        decay(ch, pair_of(st + (run + j) * kGroup), al, nz);
-        if (j == 0) {  // the first token's need no place
-          a0 = al;
-          nz0 = nz;
-        } else {
-          kept[(j - 1) * kLanes] = make_float4(al.x, al.y, nz.x, nz.y);
-        }
-        const float2 dy = pair_of(st + (3 * run + j) * kGroup);
-        m.A = cut ? splat(0.f) : mul2(al, m.A);
-        m.B = cut ? splat(0.f) : mul2(al, add2(m.B, dy));
-      };
-      if (full) {
-#pragma unroll
-        for (int j = run - 1; j >= 0; --j) compose(j, 0);
-      } else {
-#pragma unroll
-        for (int j = run - 1; j >= 0; --j)
-          if (t + j < len) compose(j, cuts);
-      }
-      g = pass_on(chain, m, cuts != 0, order, round == 0 && order == 0,
-                  round == way.rounds - 1 && order == kWarps - 1, lane);
-    }
     const float2 first = t == 0 ? h0 : splat(0.f);
-    auto finish = [&](int j, uint32_t cuts, float2& dx, float2& dr, float2& di) {
-      const bool cut = RESET && (cuts >> j & 1);
+    // g after token j is what goes on to j - 1; al and nz only where they are known
+    auto finish = [&](auto known, int j, bool cut, float2 al, float2 nz, float2& dx, float2& dr, float2& di) {
       g = add2(g, pair_of(st + (3 * run + j) * kGroup));
       float2 prev = pair_of(st + (4 * run + j) * kGroup), E;
       if (j == 0) prev = add2(prev, first);
-      float2 al = a0, nz = nz0;
-      if (!SPLIT && j > 0) {
-        const float4 v = kept[(j - 1) * kLanes];
-        al = make_float2(v.x, v.y);
-        nz = make_float2(v.z, v.w);
-      }
-      element_grad<!SPLIT>(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
-                           pair_of(st + (2 * run + j) * kGroup), cut, prev, al, nz, g, dx, dr, di, E);
+      element_grad<decltype(known)::value>(ch, pair_of(st + j * kGroup), pair_of(st + (run + j) * kGroup),
+                                           pair_of(st + (2 * run + j) * kGroup), cut, prev, al, nz, g, dx,
+                                           dr, di, E);
+      return E;
+    };
+    auto sum = [&](float2 E, float2 dr, float2 di) {
       se = add2(se, E);
       sr = add2(sr, dr);
       si = add2(si, di);
     };
-    if (full && whole) {
+    auto put = [&](int j, float2 dx, float2 dr, float2 di, bool whole) {
+      put_pair(out[0] + (at + j * ldg), dx, whole, in0, in1);
+      put_pair(out[1] + (at + j * ldg), dr, whole, in0, in1);
+      put_pair(out[2] + (at + j * ldg), di, whole, in0, in1);
+    };
+    auto pass = [&](const Map& m) {
+      if constexpr (SPLIT) return g;
+      else
+        return pass_on(chain, m, cuts != 0, order, round == 0 && order == 0,
+                       round == way.rounds - 1 && order == kWarps - 1, lane);
+    };
+    if (t + run <= len && cuts == 0) {  // most runs
+      float2 a0 = splat(0.f), nz0 = a0;
+      if constexpr (!SPLIT) {
+        Map m = {splat(1.f), splat(0.f)};
 #pragma unroll
-      for (int j = run - 1; j >= 0; --j) {
-        float2 dx, dr, di;
-        finish(j, 0, dx, dr, di);
-        put_pair(out[0] + (at + j * ldg), dx, true, in0, in1);
-        put_pair(out[1] + (at + j * ldg), dr, true, in0, in1);
-        put_pair(out[2] + (at + j * ldg), di, true, in0, in1);
-      }
-    } else {
-#pragma unroll
-      for (int j = run - 1; j >= 0; --j) {
-        float2 dx = splat(0.f), dr = dx, di = dx;
-        if (t + j < len) finish(j, cuts, dx, dr, di);
-        if (t + j < L) {
-          put_pair(out[0] + (at + j * ldg), dx, whole, in0, in1);
-          put_pair(out[1] + (at + j * ldg), dr, whole, in0, in1);
-          put_pair(out[2] + (at + j * ldg), di, whole, in0, in1);
+        for (int j = run - 1; j >= 0; --j) {
+          float2 al, nz;
+          decay(ch, pair_of(st + (run + j) * kGroup), al, nz);
+          if (j == 0) {  // the first token's need no place
+            a0 = al;
+            nz0 = nz;
+          } else {
+            kept[(j - 1) * kLanes] = make_float4(al.x, al.y, nz.x, nz.y);
+          }
+          m.A = mul2(al, m.A);
+          m.B = mul2(al, add2(m.B, pair_of(st + (3 * run + j) * kGroup)));
         }
+        g = pass(m);
+      }
+      auto all = [&](bool whole) {
+#pragma unroll
+        for (int j = run - 1; j >= 0; --j) {
+          float2 al = a0, nz = nz0, dx, dr, di;
+          if (!SPLIT && j > 0) {
+            const float4 v = kept[(j - 1) * kLanes];
+            al = make_float2(v.x, v.y);
+            nz = make_float2(v.z, v.w);
+          }
+          const float2 E = finish(std::bool_constant<!SPLIT>{}, j, false, al, nz, dx, dr, di);
+          sum(E, dr, di);
+          put(j, dx, dr, di, whole);
+        }
+      };
+      if (whole) all(true);
+      else all(false);
+    } else if (t >= len) {  // past the sequence's end
+      if constexpr (!SPLIT) g = pass({splat(1.f), splat(0.f)});
+#pragma unroll
+      for (int j = 0; j < run; ++j)
+        if (t + j < L) put(j, splat(0.f), splat(0.f), splat(0.f), whole);
+    } else {  // a reset or the end; selects, so that the gates overlap
+      if constexpr (!SPLIT) {
+        Map m = {splat(1.f), splat(0.f)};
+#pragma unroll
+        for (int j = run - 1; j >= 0; --j) {
+          const bool cut = RESET && (cuts >> j & 1), on = t + j < len;
+          float2 al, nz;
+          decay(ch, pair_of(st + (run + j) * kGroup), al, nz);
+          const float2 A = mul2(al, m.A), B = mul2(al, add2(m.B, pair_of(st + (3 * run + j) * kGroup)));
+          m.A = !on ? m.A : cut ? splat(0.f) : A;
+          m.B = !on ? m.B : cut ? splat(0.f) : B;
+        }
+        g = pass(m);
+      }
+#pragma unroll
+      for (int j = run - 1; j >= 0; --j) {
+        const bool on = t + j < len;
+        const float2 later = g, none = splat(0.f);
+        float2 dx, dr, di;
+        const float2 E = finish(std::false_type{}, j, RESET && (cuts >> j & 1), none, none, dx, dr, di);
+        g = on ? g : later;
+        dx = on ? dx : none;
+        dr = on ? dr : none;
+        di = on ? di : none;
+        sum(on ? E : none, dr, di);
+        if (t + j < L) put(j, dx, dr, di, whole);
       }
     }
 #pragma unroll
