@@ -673,8 +673,8 @@ typedef struct {
  * Forward.  q (rows, q_heads, width), k (rows, k_heads, width); q_w, k_w (width) fp32, NULL = 1;
  * positions (rows) int32, any sign; freqs (pairs) fp32, radians a position (both may be NULL where
  * pairs is 0).  q_out, k_out: dense; they may be q and k where those are dense.  width up to 256,
- * heads up to 65535, the heads of all rows and strides up to 2^31 - 1 (else M3SSD_ERR_UNSUPPORTED).  No
- * allocation, no synchronisation.
+ * heads up to 65535, strides up to 2^31 - 1, the heads of all rows up to 2^31 - 2^16 (else
+ * M3SSD_ERR_UNSUPPORTED).  No allocation, no synchronisation.
  */
 m3ssd_status m3ssd_norm_rotate(const m3ssd_rotate_dims* dims, const void* q, const void* k,
                                const float* q_w, const float* k_w, const int32_t* positions,

@@ -72,9 +72,10 @@ m3ssd_status check_rotate(const m3ssd_rotate_dims* d) {
       d->pairs < 0 || d->pairs > d->width / 2)
     return M3SSD_ERR_INVALID_ARG;
   if (!dtype_ok(d->x_dtype) || !(d->eps >= 0.f)) return M3SSD_ERR_INVALID_ARG;
-  const int64_t most = INT32_MAX;
+  // blocks of a token's heads are counted in 31 bits, up to a round of all warps past the last
+  const int64_t most = INT32_MAX, units = most - 65535;
   if (d->width > 256 || d->q_heads > 65535 || d->k_heads > 65535 || d->rows > most || d->ldq > most ||
-      d->ldk > most || d->rows * (d->q_heads + d->k_heads) > most)
+      d->ldk > most || d->rows * (d->q_heads + d->k_heads) > units)
     return M3SSD_ERR_UNSUPPORTED;
   if (d->ldq < d->q_heads * d->width || d->ldk < d->k_heads * d->width) return M3SSD_ERR_INVALID_ARG;
   return M3SSD_OK;

@@ -181,6 +181,8 @@ def rot_bwd(lib, dims, grads=None, up=m3.F32, ws=A, nbytes=1 << 24, **kw):
     (dict(reserved=1), m3.ERR_INVALID_ARG), (dict(width=258, ldq=1000, ldk=1000), m3.ERR_UNSUPPORTED),
     (dict(rows=1 << 31), m3.ERR_UNSUPPORTED), (dict(rows=(1 << 31) // 5 + 1), m3.ERR_UNSUPPORTED),
     (dict(ldq=1 << 31), m3.ERR_UNSUPPORTED),
+    (dict(rows=((1 << 31) - (1 << 16)) // 5 + 1), m3.ERR_UNSUPPORTED),
+    (dict(rows=(1 << 31) - 2, q_heads=1, k_heads=0), m3.ERR_UNSUPPORTED),
     (dict(q_heads=65536, ldq=1 << 20), m3.ERR_UNSUPPORTED)])
 def test_rotate_rejects_bad_dims(lib, kw, status):
     d = rot_dims(**kw)
