@@ -12,9 +12,9 @@
 // (n - zero) 2^-6 of it, exactly, wherever in those bits the code lies, and nothing is rounded
 // before the products' fp32 sums; a group's sums are scaled in fp32, and the 2^6 comes last.  tcgen05
 // is not for this: its operands would have to go through shared or tensor memory, and the products
-// are a tenth of the time.
+// keep the tensor pipe busy for a quarter of the time only.
 //
-// Measured: 8 tokens x 65536 x 4096 in groups of 64 with zero points (146 MB) 34.3 us, 4.3 TB/s; one token
+// Measured: 8 tokens x 65536 x 4096 in groups of 64 with zero points (149 MB) 34.6 us, 4.3 TB/s; one token
 // 30.3 us without zero points; 16 tokens 58 us (two products a word, fewer warps: the tokens' operands
 // come from shared memory for every tile).  1 x 6464 x 1024 3.4 us: a launch, one read of codes after
 // another of tokens and scales, a join.

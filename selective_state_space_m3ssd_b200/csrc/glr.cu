@@ -39,9 +39,9 @@ __device__ __forceinline__ void store2(T* p, float2 v, bool in1) {
 //
 // Bytes: the forward reads x, r and i and writes y, the backward reads y and dy too and writes three
 // gradients.  Measured at 8 x 4096 tokens, 2048 channels, bf16: forward 106 us (0.77 of HBM's copy
-// rate), backward with bf16 gradients 220 (0.75).  The issue slots bound both: 66 and 130 warp
+// rate), backward with bf16 gradients 216 (0.76).  The issue slots bound both: 66 and 131 warp
 // instructions for a token of two channels a lane, most of them the gates', in 256 CTAs, which are two
-// on 108 SMs and one on 40.  32 x 1024 tokens, 1024 CTAs: 98 and 203 us.
+// on 108 SMs and one on 40.  32 x 1024 tokens, 1024 CTAs: 97 and 199 us.
 
 constexpr int kWarps = 8, kLanes = 32, kGroup = 64;
 
