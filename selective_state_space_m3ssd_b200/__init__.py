@@ -1120,6 +1120,13 @@ def _tokens_stride(t, name, dtype, lead, inner, index):
     return ld or width
 
 
+def _dense_like(t):
+    """Unwritten dense memory of a tensor's shape and type (by its tensor, where it is dense, which
+    is the cheaper call)."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(*t.shape, dtype=t.dtype, device=t.device)
+
+
 def _bytes_of(t):
     """A mask as the bytes it is held in."""
     import torch
@@ -1164,7 +1171,7 @@ def glr_fwd(x, r, i, rate, *, bias_r=None, bias_i=None, c: float = 8.0, h0=None,
     dev, f32 = x.device, torch.float32
     reset = _bytes_of(reset)
     if y is None:
-        y = torch.empty(b, L, D, dtype=x.dtype, device=dev)
+        y = _dense_like(x)
     else:
         _need(y, "y", x.dtype, (b, L, D), dev)
     if hT is not None:
@@ -1258,7 +1265,7 @@ def glr_step(h, x_t, r_t, i_t, rate, *, bias_r=None, bias_i=None, c: float = 8.0
     b, D = x_t.shape
     dev, f32 = x_t.device, torch.float32
     if y_t is None:
-        y_t = torch.empty(b, D, dtype=x_t.dtype, device=dev)
+        y_t = _dense_like(x_t)
     else:
         _need(y_t, "y_t", x_t.dtype, (b, D), dev)
     if h_out is None:
@@ -1307,17 +1314,16 @@ def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, ep
     theta.  bf16 or fp32, each token's heads dense, tokens any fixed distance apart (a column
     range of a projection); positions int32 of the leading shape, freqs fp32 radians.  Returns
     ``(q_out, k_out)``, dense; they may be given as q and k to write in place."""
-    import torch
     dims, lead = _rotate_dims(q, k, q_w, k_w, positions, freqs, eps)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty(*q.shape, dtype=q.dtype, device=dev)
+        q_out = _dense_like(q)
     else:
         _need(q_out, "q_out", q.dtype, q.shape, dev)
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty(*k.shape, dtype=k.dtype, device=dev)
+        k_out = _dense_like(k)
     else:
         _need(k_out, "k_out", k.dtype, k.shape, dev)
     _launch("m3ssd_norm_rotate", dev, ctypes.byref(dims), _addr(q), _addr(k), _addr(q_w), _addr(k_w),
