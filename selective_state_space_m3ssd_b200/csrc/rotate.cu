@@ -242,9 +242,12 @@ struct Way {
       open(a);
     }
   }
-  // The position of the row after the unit's, read while the unit is done.
+  // The position of the next row that the warp takes, read while the unit's row is done.  A row of more
+  // blocks than there are warps gives a warp several units: those are passed over.
   __device__ __forceinline__ int next_position(const RotateArgs& a) const {
-    const int next = unit + (int)gridDim.x * kWarps;
+    const int warps = (int)gridDim.x * kWarps, end = (row + 1) * a.blocks;
+    int next = unit + warps;
+    if (next < end) next += ((end - 1 - next) / warps + 1) * warps;
     if (next >= total || a.R == 0) return 0;
     return a.positions[a.blocks == 1 ? next : (int)((uint32_t)next / (uint32_t)a.blocks)];
   }
