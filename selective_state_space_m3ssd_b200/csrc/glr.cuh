@@ -132,11 +132,10 @@ __device__ __forceinline__ void element(const Channel& ch, float2 x, float2 r, f
   u = mul2(mul2(s, iota), x);
 }
 
-// The decay alone, which is all that the walk of g needs, and a^2 - 1.  (A gate that is not clamped:
-// nothing multiplies its exponential.)
+// The decay alone, which is all that the walk of g needs, and a^2 - 1.  The gate is held as element()
+// and element_grad() hold it: the latter divides its own log a by the root of this a^2 - 1.
 __device__ __forceinline__ void decay(const Channel& ch, float2 r, float2& a, float2& nz) {
-  const float2 t = fma2(r, splat(-kLog2e), ch.nbr);
-  const float2 q = add2(make_float2(ex2(t.x), ex2(t.y)), splat(1.f));
+  const float2 q = add2(gate_exp(r, ch.nbr), splat(1.f));
   decay_of(mul2(ch.k2, make_float2(rcp(q.x), rcp(q.y))), a, nz);
 }
 
