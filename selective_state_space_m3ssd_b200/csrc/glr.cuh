@@ -73,7 +73,8 @@ __device__ __forceinline__ void channel_of(const float* rate, const float* bias_
   for (int j = 0; j < 2; ++j) {
     const int64_t d = j ? d1 : d0;
     const bool in = d < width;
-    k[j] = in ? -kLog2e * c * softplus(rate[d]) : 0.f;
+    // from 2^71 on no gate, 2^-63 or more, leaves any of the state: held there, (log a) times a = 0 is 0
+    k[j] = in ? max_nan(-kLog2e * c * softplus(rate[d]), -0x1p71f) : 0.f;
     br[j] = in && bias_r ? -kLog2e * bias_r[d] : 0.f;
     bi[j] = in && bias_i ? -kLog2e * bias_i[d] : 0.f;
   }

@@ -48,3 +48,31 @@ def test_closed_gates(b, L, D, kw, dtype):
     for grad in {torch.float32, dtype}:
         got = call(m3.glr_bwd, c, gy, c["dy"], dhT=c["dhT"], grad_dtype=grad)
         check_bwd(ref, np64(gy), got, grad)
+
+
+@pytest.mark.parametrize("b,L,kw", [(3, 70, {}), (1, 1100, {}), (3, 70, {"reset": 0.2})])
+def test_rates_that_leave_nothing_of_the_state(b, L, kw):
+    """Rates from where no gate leaves any of the state, a = 0, up to infinity: y is iota x, g is dy
+    (dhT joins at the last token), nothing of the gradient reaches r, the rate or h0."""
+    D = 64
+    d = make(b, L, D, torch.float32, seed=4, bias=False, **kw)
+    d["rate"] = torch.tensor([1e21, 1e25, 1e30, 1e37, 2.9e37, 1e38, 3e38, float("inf")]).repeat(D // 8)
+    d["r"][:, ::3] = -float("inf")
+    c = gpu(d)
+    y, hT = call(m3.glr_fwd, c)
+    h = host(d)
+    iota = ly.sigmoid(h["i"])
+    ry = iota * h["x"]
+    rel = 2 * (3 * abs(h["i"]) + 16 + 40 + 4) * 2.0 ** -24  # u's bound, and two products
+    check(y, ry, rel * abs(ry), torch.float32, "y")
+    assert torch.equal(hT, y[:, -1])
+    got = call(m3.glr_bwd, c, y, c["dy"], dhT=c["dhT"])
+    g = h["dy"].copy()
+    g[:, -1] += h["dhT"]
+    check(got["dx"], g * iota, rel * abs(g * iota), torch.float32, "dx")
+    di = g * ry * (1 - iota)
+    check(got["di"], di, 2 * rel * abs(di), torch.float32, "di")
+    for k in ("dr", "drate", "dbias_r", "dh0"):
+        assert (got[k] == 0).all(), k
+    y1, h1 = m3.glr_step(c["h0"].clone(), c["x"][:, 0], c["r"][:, 0], c["i"][:, 0], c["rate"])
+    assert torch.equal(y1, y[:, 0]) and torch.equal(h1, y1)
