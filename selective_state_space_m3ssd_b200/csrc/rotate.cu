@@ -189,8 +189,10 @@ __device__ __forceinline__ void load_weight(const float* w, const Place& pl, int
     o[p] = e >= N ? splat(0.f) : w ? make_float2(w[e], w[e + 1]) : splat(1.f);
   }
 }
-// Turns a position of a lane's pairs, and the cosines and sines of a position: for bf16 outputs by the
-// hardware's approximations on half a turn either side (2^-21), far below those outputs' steps.
+// Turns a position of a lane's pairs, and the cosines and sines of a position: for the forward's bf16 outputs
+// by the hardware's approximations on half a turn either side (2^-21), far below those outputs' steps.  Not in
+// the backward, whose dw is fp32 whatever the type of dq (with bf16 dq the approximations took 182.9 instead
+// of 185.6 us for 32768 tokens of 40 heads of 128, 37.8 instead of 41.0 for 1 + 1 heads).
 template <int ACC>
 __device__ __forceinline__ void load_freqs(const float* f, const Place& pl, int R, double (&o)[4]) {
 #pragma unroll
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rotate_bwd_kernel(Rot
   while (out.valid()) {
     if (at != out.row) {
       at = out.row;
-      if (a.R > 0) turn<sizeof(G) == 2>(pos, f, c, s);
+      if (a.R > 0) turn<false>(pos, f, c, s);
       pos = out.next_position(a);
     }
     if (out.keys)

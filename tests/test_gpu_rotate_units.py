@@ -50,3 +50,14 @@ def test_backward_of_many_tokens(rows, Hq, Hk, N, R, dtype, up, grad):
 def test_backward_of_many_slots():
     d = make(6000, 32, 8, 128, 40, BF, seed=6, up=BF)
     check_bwd(d, bwd(gpu(d), grad_dtype=BF), BF)
+
+
+@pytest.mark.parametrize("rows,Hq,Hk", [(1, 1, 1), (700, 3, 2)])
+def test_weights_gradients_do_not_depend_on_the_others_type(rows, Hq, Hk):
+    """dq_w and dk_w are fp32 whatever dq's type is: the same angles, and at ten values a head, which
+    either type moves in pairs, the same order of the sums, so the same bits."""
+    d = gpu(make(rows, Hq, Hk, 10, 5, BF, seed=8, up=BF))
+    a, b = bwd(d, grad_dtype=BF), bwd(d, grad_dtype=F32)
+    for n in ("dq_w", "dk_w"):
+        assert torch.equal(a[n], b[n])
+    assert torch.equal(a["dq"], b["dq"].to(BF)) and torch.equal(a["dk"], b["dk"].to(BF))
