@@ -1408,8 +1408,9 @@ class W4Tensor:
 
     @classmethod
     def from_codes(cls, codes, scales, zeros=None, *, group: int = 128):
-        """Weights quantised elsewhere: ``codes`` (rows, cols) uint8 0 to 15, ``scales`` and ``zeros``
-        (rows, groups).  Laid out by torch, once."""
+        """Weights quantised elsewhere: ``codes`` (rows, cols) and ``zeros`` (rows, groups) uint8 0 to
+        15, ``scales`` (rows, groups), rounded to bf16 (fp16 or fp32 ones move every weight by up to 2^-8 of
+        itself).  Laid out by torch, once; reads the largest code back, so it waits."""
         import torch
         rows, cols = codes.shape
         n = _w4_groups(cols, group)
@@ -1417,6 +1418,9 @@ class W4Tensor:
         _need_shape(scales, "scales", None, (rows, n))
         if zeros is not None:
             _need_shape(zeros, "zeros", torch.uint8, (rows, n))
+        for t, name in ((codes, "codes"), (zeros, "zeros")):
+            if t is not None and t.numel() and int(t.max()) > 15:
+                raise ValueError(f"{name} must be 0 to 15, got {int(t.max())}")
         rp, kp = -(-rows // 16) * 16, _pad128(cols)
         p = torch.zeros(rp, kp, dtype=torch.uint8, device=codes.device)
         p[:rows, :cols] = codes

@@ -296,3 +296,20 @@ def test_w4_codes_from_elsewhere_are_laid_out(rows, cols, group):
     assert W.codes.numel() == m3._w4_codes(rows, cols)
     with pytest.raises(ValueError):
         m3.W4Tensor.from_codes(codes, scales[:, :-1], group=group)
+
+
+def test_w4_codes_from_elsewhere_are_checked():
+    """A code above 15 would run into its neighbour's byte half, or lose bits."""
+    codes = torch.full((20, 200), 15, dtype=torch.uint8)
+    scales, zeros = torch.ones(20, 2), torch.full((20, 2), 15, dtype=torch.uint8)
+    m3.W4Tensor.from_codes(codes, scales, zeros)
+    for r, k in ((0, 0), (19, 199), (7, 33)):
+        bad = codes.clone()
+        bad[r, k] = 16
+        with pytest.raises(ValueError, match="codes must be 0 to 15, got 16"):
+            m3.W4Tensor.from_codes(bad, scales, zeros)
+    zeros[3, 1] = 255
+    with pytest.raises(ValueError, match="zeros must be 0 to 15, got 255"):
+        m3.W4Tensor.from_codes(codes, scales, zeros)
+    empty = m3.W4Tensor.from_codes(codes[:0], scales[:0])
+    assert empty.rows == 0 and empty.codes.numel() == 0
