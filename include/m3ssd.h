@@ -749,8 +749,9 @@ m3ssd_status m3ssd_w4_dequant(const m3ssd_w4* in, int32_t dtype, void* w, int64_
 /*
  * out (tokens x rows, out_dtype, row stride ldd >= rows) = x (tokens x cols, x_dtype, row stride
  * ldx >= cols) W^T for up to 16 tokens (else M3SSD_ERR_UNSUPPORTED: m3ssd_w4_dequant and
- * m3ssd_gemm_bf16 take more).  Products of the held values, exact, fp32 sums over a group, each
- * scaled in fp32, and rounded once to out_dtype.  The order of the sums goes by the sizes and the
+ * m3ssd_gemm_bf16 take more).  Products of the held values, exact (of an fp32 token below 2^-110 what is
+ * a multiple of 2^-133 counts, the rest is dropped), fp32 sums over a group, each scaled in fp32, and
+ * rounded once to out_dtype.  The order of the sums goes by the sizes and the
  * device's SM count: the same call gives the same bits.  No workspace, no allocation, no
  * synchronisation; capture-safe.
  */

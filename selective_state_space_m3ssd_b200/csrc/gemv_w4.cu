@@ -19,7 +19,8 @@
 // come from shared memory for every tile).  1 x 6464 x 1024 3.4 us: a launch, one read of codes after
 // another of tokens and scales, a join.
 //
-// fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact.
+// fp32 tokens are three bf16 columns each, their leading 8 bits, the next and the last: exact from 2^-110 on;
+// below, the last ones pass bf16's least number, 2^-133, and what is under it is dropped.
 // A CTA's warps are WR groups of rows by WK parts of K, joined in shared memory in a fixed
 // order; the tokens lie there too, a piece of K at a time.
 #include <cuda_runtime.h>
@@ -116,7 +117,8 @@ __device__ __forceinline__ void stage_eight(const __nv_bfloat16* x, int k, int K
                                              low_halves(u.y, u.w), high_halves(u.y, u.w));
 }
 // fp32: three columns `stride` bytes apart, each value's leading bf16 part (its high half), that of the rest,
-// and the last, which leaves nothing.  What is not finite has no further parts.
+// and the last, which leaves nothing (of a value below 2^-110 less than 2^-133).  What is not finite has no
+// further parts.
 __device__ __forceinline__ void stage_eight(const float* x, int k, int K, bool wide, char* to, int stride) {
   float v[8];
   if (wide && k + 8 <= K) {

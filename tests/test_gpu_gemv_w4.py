@@ -188,3 +188,26 @@ def test_refusals_and_empty_calls():
     assert m3.gemv_w4(torch.zeros(0, 64, device="cuda"), W).shape == (0, 20)
     V = m3.W4Tensor.empty(0, 64, 64, device="cuda")
     assert m3.gemv_w4(torch.zeros(3, 64, device="cuda"), V).shape == (3, 0)
+
+
+def test_small_fp32_tokens():
+    """A token's value counts whole from 2^-110 on, below to the multiple of 2^-133 under it: a row of
+    W with one column that is not zero leaves one product a part, three parts that add up with one
+    rounding of fp32 each (2^-24 of the sum), into multiples of 2^-149 (2^-6 of them before the last
+    product: half of 2^-143 each)."""
+    K, at = 200, 150
+    g = torch.Generator().manual_seed(5)
+    e = -torch.arange(90, 150).double()
+    x = (1 + torch.rand(60, generator=g, dtype=torch.float64)).mul(torch.exp2(e)).float()
+    want = torch.where(x.double() < 2.0 ** -110, torch.floor(x.double() * 2.0 ** 133) * 2.0 ** -133, x.double())
+    for code, value in ((15, 7.0), (9, 1.0), (0, -8.0)):
+        codes = torch.full((1, K), 8, dtype=torch.uint8)
+        codes[0, at] = code
+        W = m3.W4Tensor.from_codes(codes.cuda(), torch.ones(1, 2).cuda())
+        for lo in range(0, 60, 15):
+            t = torch.zeros(15, K)
+            t[:, at] = x[lo:lo + 15]
+            got = m3.gemv_w4(t.cuda(), W)[:, 0].cpu().double()
+            ref = value * want[lo:lo + 15]
+            assert (abs(got - ref) <= 3 * 2.0 ** -24 * abs(ref) + 3 * 2.0 ** -144).all(), (code, lo)
+            assert (got[(t[:, at] < 2.0 ** -133)] == 0).all()
