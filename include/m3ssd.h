@@ -562,8 +562,9 @@ m3ssd_status m3ssd_step_q8(const m3ssd_dims* dims, const void* x_t, const float*
  *     rho = sigma(r + bias_r),  iota = sigma(i + bias_i),  a = exp(-k rho),
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) iota_t x_t,   y_t = h_t,
  * computed in fp32 (1 - a_t^2 to fp32's relative precision however close a_t is to one, down
- * to 1e-37; a gate below 2^-63 counts as that, an a_t below 2^-126 as zero), h held in fp32, y
- * rounded once to x_dtype.
+ * to 1e-37, in the backward to 1e-29 and below that its root within 4e-19; a gate below 2^-63 counts
+ * as that, an a_t below 2^-126 as zero), h held in fp32, y rounded once to x_dtype.  A state that is
+ * infinite or NaN is one or the other until the next reset.
  */
 typedef struct {
   int64_t batch;      /* b >= 0 */
@@ -627,8 +628,8 @@ size_t m3ssd_glr_bwd_workspace_size(const m3ssd_glr_dims* dims);
  *     E = g a (h_{t-1} - a iota x / s) log a,  dr = E (1 - rho),
  *     drate = sum of E sigma(rate) / softplus(rate),  dbias_r, dbias_i = sums of dr and di,
  *     dh0 = a_0 g_0
- * (E = dr = 0 at a reset).  h_{t-1} is read as the stored y_{t-1}: in bf16 that is h rounded by
- * 2^-9 of its value, a fifth of the forward's work saved (no second walk forward).  Rows at
+ * (E = dr = 0 at a reset).  h_{t-1} is read as the stored y_{t-1}, which saves a second walk
+ * forward: in bf16 that is h rounded by up to 2^-8 of its value.  Rows at
  * and past lengths[b] are zero.  Sums run in fp32 in a fixed order: the same call gives
  * the same bits.  dh0 may be dhT; the other outputs overlap no input.  workspace: 256-byte
  * aligned, not read afterwards.
@@ -654,7 +655,8 @@ m3ssd_status m3ssd_glr_step(const m3ssd_glr_dims* dims, const void* x_t, const v
  *     rstd = 1 / sqrt(mean u^2 + eps),   v = u rstd w,
  *     pair i (components 2i, 2i + 1) of the output = R(position freqs[i]) (pair i of v), i < pairs,
  * the other components v, computed in fp32 (the angle's turns in fp64) and rounded once to
- * x_dtype.  With its outputs as C and B, m3ssd_fwd and m3ssd_step run without theta.
+ * x_dtype.  With its outputs as C and B, which have the same number of groups (q_heads = k_heads =
+ * ngroups), m3ssd_fwd and m3ssd_step run without theta.  Unlike heads are for attention beside the scan.
  */
 typedef struct {
   int64_t rows;       /* tokens, >= 0 */

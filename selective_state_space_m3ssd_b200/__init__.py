@@ -1310,8 +1310,8 @@ def norm_rotate(q, k=None, q_w=None, k_w=None, *, positions=None, freqs=None, ep
                 q_out=None, k_out=None):
     """The RMS norm of every head of q (..., Hq, N) and k (..., Hk, N), times q_w and k_w (N, fp32,
     None = 1), and the rotation of pair i < len(freqs) by ``positions * freqs[i]``, in one pass
-    through ``m3ssd_norm_rotate``: the scan's C and B for :func:`fwd` and :func:`step` without
-    theta.  bf16 or fp32, each token's heads dense, tokens any fixed distance apart (a column
+    through ``m3ssd_norm_rotate``: with Hq = Hk = G the scan's C and B for :func:`fwd` and
+    :func:`step` without theta.  bf16 or fp32, each token's heads dense, tokens any fixed distance apart (a column
     range of a projection); positions int32 of the leading shape, freqs fp32 radians.  Returns
     ``(q_out, k_out)``, dense; they may be given as q and k to write in place."""
     dims, lead = _rotate_dims(q, k, q_w, k_w, positions, freqs, eps)

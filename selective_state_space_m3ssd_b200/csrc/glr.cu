@@ -39,9 +39,10 @@ __device__ __forceinline__ void store2(T* p, float2 v, bool in1) {
 //
 // Bytes: the forward reads x, r and i and writes y, the backward reads y and dy too and writes three
 // gradients.  Measured at 8 x 4096 tokens, 2048 channels, bf16: forward 106 us (0.77 of HBM's copy
-// rate), backward with bf16 gradients 216 (0.76).  The issue slots bound both: 66 and 131 warp
-// instructions for a token of two channels a lane, most of them the gates', in 256 CTAs, which are two
-// on 108 SMs and one on 40.  32 x 1024 tokens, 1024 CTAs: 97 and 199 us.
+// rate), backward with bf16 gradients 216 (0.76).  Latency bounds both, with eight or 16 warps an SM (256 CTAs
+// are two on 108 SMs and one on 40): 66 and 133 warp instructions for a token of two channels a lane, most
+// of them the gates', fill 65 % of the issue slots of an SM that has a CTA, 55 % of all; the forward's
+// hardware approximations keep their pipe busy for 63 %.  32 x 1024 tokens, 1024 CTAs: 97 and 200 us.
 
 constexpr int kWarps = 8, kLanes = 32, kGroup = 64;
 
